@@ -10,9 +10,17 @@ Entry points (same names as the C ABI, without the ``gdr_`` prefix):
   recurrent_fwd       slot-indexed decode / verify (pool in place, ibuf)
   gating_fwd          g, beta from raw projections
   chunk_workspace_size
+  linrec_fwd          gated linear recurrence over packed sequences -> y, final_state
+  linrec_bwd          its gradients                       -> dx, dg, d_initial_state
+  linrec_step         the same over a slot-indexed state pool (decode / verify) -> y
+  rmsnorm_fwd         RMS norm with the residual's addition, in the input's type or
+                      e4m3 with scales                    -> y, residual_out, scales
+  rmsnorm_bwd         its gradients                       -> dx, dweight
+  linrec_workspace_size, rmsnorm_bwd_workspace_size
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -21,7 +29,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgdr.so")
 
-GDR_BF16, GDR_F32 = 0, 1
+GDR_BF16, GDR_F32, GDR_E4M3 = 0, 1, 2
 GDR_GATE_SCALAR, GDR_GATE_CHANNEL = 0, 1
 GDR_QK_L2NORM, GDR_NEG_EIGVAL, GDR_COMMIT, GDR_VALIDATE, GDR_CHANNEL_GATE = 0x1, 0x2, 0x4, 0x8, 0x10
 GDR_CHUNK_SCAN = 0x20
@@ -33,6 +41,8 @@ STATUS = {0: "GDR_OK", 1: "GDR_ERR_INVALID_ARG", 2: "GDR_ERR_UNSUPPORTED", 3: "G
 # every symbol include/gdr.h declares
 EXPORTED = ("gdr_chunk_workspace_size", "gdr_chunk_fwd", "gdr_chunk_fwd_noalloc", "gdr_recurrent_fwd",
             "gdr_recurrent_fwd_gated", "gdr_recurrent_fwd_norm", "gdr_gating_fwd",
+            "gdr_linrec_workspace_size", "gdr_linrec_fwd", "gdr_linrec_bwd", "gdr_linrec_step",
+            "gdr_rmsnorm_fwd", "gdr_rmsnorm_bwd_workspace_size", "gdr_rmsnorm_bwd",
             "gdr_last_error", "gdr_get_device_status", "gdr_selftest_bounded_wait", "gdr_profile_enable",
             "gdr_profile_read",
             "gdr_version")
@@ -71,6 +81,20 @@ def load(path: str | None = None):
     lib.gdr_recurrent_fwd_norm.restype = I
     lib.gdr_gating_fwd.argtypes = [P, P, P, P, I64, I, I, I, P, P, P]
     lib.gdr_gating_fwd.restype = I
+    lib.gdr_linrec_workspace_size.argtypes = [I, I64, I, I, I, ctypes.POINTER(SZ)]
+    lib.gdr_linrec_workspace_size.restype = I
+    lib.gdr_linrec_fwd.argtypes = [P, I64, P, I64, P, P, I, I64, I, I, I, I, P, I64, P, P, SZ, P]
+    lib.gdr_linrec_fwd.restype = I
+    lib.gdr_linrec_bwd.argtypes = [P, I64, P, I64, P, I64, P, P, P, I, I64, I, I, I, I, P, I64, P, I64, P, P, SZ, P]
+    lib.gdr_linrec_bwd.restype = I
+    lib.gdr_linrec_step.argtypes = [P, I64, P, I64, P, I, I, P, P, I, I64, I, I, I, I, P, I64, P, I, P]
+    lib.gdr_linrec_step.restype = I
+    lib.gdr_rmsnorm_fwd.argtypes = [P, I64, P, I64, P, I64, I, F, I, P, I64, P, I64, I, P, I, P]
+    lib.gdr_rmsnorm_fwd.restype = I
+    lib.gdr_rmsnorm_bwd_workspace_size.argtypes = [I64, I, ctypes.POINTER(SZ)]
+    lib.gdr_rmsnorm_bwd_workspace_size.restype = I
+    lib.gdr_rmsnorm_bwd.argtypes = [P, I64, P, I64, P, P, I64, I64, I, F, I, P, I64, P, P, SZ, P]
+    lib.gdr_rmsnorm_bwd.restype = I
     lib.gdr_last_error.argtypes = []
     lib.gdr_last_error.restype = ctypes.c_char_p
     lib.gdr_get_device_status.argtypes = [P, ctypes.POINTER(I)]
@@ -273,6 +297,246 @@ def gating_fwd(a, dt_bias, A_log, b, *, flags: int = 0, g=None, beta=None, strea
     _check(load().gdr_gating_fwd(_ptr(a), _ptr(dt_bias), _ptr(A_log), _ptr(b), T, Hv, _dtype_code(a),
                                  flags, _ptr(g), _ptr(beta), _stream(stream)))
     return g, beta
+
+
+# ---- gated linear recurrence and RMS norm -----------------------------------
+#
+# Rows are 2-D tensors whose last axis is dense; their row stride is free (a
+# column block of a wider matrix, an expanded row).  Everything runs on the
+# tensors' device; `stream` defaults to that device's current stream, and what
+# a call allocates belongs to the stream it runs on.
+
+
+def _need(t, shape, dtype, device, what):
+    """Address of a dense tensor of this shape, dtype and device."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}, not {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, shape, dtype, device, what):
+    """(address, row stride) of a [rows, D] tensor with a dense last axis."""
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}, not {t.device}")
+    row, col = t.stride()
+    rows, D = shape
+    if col != 1 and D > 1:
+        raise ValueError(f"{what} must be dense along its last axis")
+    return t.data_ptr(), row if rows > 1 else D
+
+
+def _device_of(t, what):
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D")
+    return t.device
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """Context in which to allocate and launch: the stream's, or the device's own current stream."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        return torch.cuda.stream(stream)
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _pool_of(size, device):
+    """(tensor, address, bytes) of a workspace; nothing for size 0."""
+    if size == 0:
+        return None, None, 0
+    t = torch.empty(size, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), size
+
+
+def _given(workspace, device):
+    if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a dense uint8 tensor on {device}")
+    return workspace, workspace.data_ptr(), workspace.numel()
+
+
+def linrec_workspace_size(N: int, T: int, D: int, *, dtype: int, gate_dtype: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().gdr_linrec_workspace_size(N, T, D, dtype, gate_dtype, ctypes.byref(out)))
+    return out.value
+
+
+def linrec_fwd(x, g, cu_seqlens, *, initial_state=None, flags: int = 0, y=None, final_state=None,
+               output_final_state: bool = True, workspace=None, stream=None):
+    """Gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t over packed
+    sequences.  x [T, D] bf16 or fp32; g [T, D] bf16 or fp32, <= 0; cu_seqlens
+    [N+1] int32; initial_state [N, D] fp32 or None.  Rows from cu_seqlens[N] on
+    are neither read nor written.  Returns (y, final_state or None)."""
+    dev = _device_of(x, "x")
+    T, D = shape = x.shape
+    N = cu_seqlens.numel() - 1
+    state = (N, D)
+    dt, gt = _dtype_code(x), _dtype_code(g)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty(T, D, dtype=x.dtype, device=dev)
+        if final_state is None and output_final_state:
+            final_state = torch.empty(N, D, dtype=torch.float32, device=dev)
+        ws, wp, wn = _pool_of(linrec_workspace_size(N, T, D, dtype=dt, gate_dtype=gt), dev) \
+            if workspace is None else _given(workspace, dev)
+        f32 = torch.float32
+        _check(load().gdr_linrec_fwd(
+            *_rows(x, shape, x.dtype, dev, "x"), *_rows(g, shape, g.dtype, dev, "g"),
+            _need(initial_state, state, f32, dev, "initial_state"),
+            _need(cu_seqlens, (N + 1,), torch.int32, dev, "cu_seqlens"), N, T, D, dt, gt, flags,
+            *_rows(y, shape, x.dtype, dev, "y"), _need(final_state, state, f32, dev, "final_state"), wp, wn,
+            torch.cuda.current_stream(dev).cuda_stream))
+    return y, final_state
+
+
+def linrec_bwd(dy, g, y, cu_seqlens, *, initial_state=None, d_final_state=None, flags: int = 0, dx=None, dg=None,
+               d_initial_state=None, output_d_initial_state: bool = True, workspace=None, stream=None):
+    """Gradients of linrec_fwd: dy [T, D] is the gradient of y, d_final_state
+    [N, D] fp32 (or None) that of the final state; g, y, initial_state are the
+    forward's.  Returns (dx, dg, d_initial_state or None)."""
+    dev = _device_of(dy, "dy")
+    T, D = shape = dy.shape
+    N = cu_seqlens.numel() - 1
+    state = (N, D)
+    dt, gt = _dtype_code(dy), _dtype_code(g)
+    with _on(dev, stream):
+        if dx is None:
+            dx = torch.empty(T, D, dtype=dy.dtype, device=dev)
+        if dg is None:
+            dg = torch.empty(T, D, dtype=g.dtype, device=dev)
+        if d_initial_state is None and output_d_initial_state:
+            d_initial_state = torch.empty(N, D, dtype=torch.float32, device=dev)
+        ws, wp, wn = _pool_of(linrec_workspace_size(N, T, D, dtype=dt, gate_dtype=gt), dev) \
+            if workspace is None else _given(workspace, dev)
+        f32 = torch.float32
+        _check(load().gdr_linrec_bwd(
+            *_rows(dy, shape, dy.dtype, dev, "dy"), *_rows(g, shape, g.dtype, dev, "g"),
+            *_rows(y, shape, dy.dtype, dev, "y"), _need(initial_state, state, f32, dev, "initial_state"),
+            _need(d_final_state, state, f32, dev, "d_final_state"),
+            _need(cu_seqlens, (N + 1,), torch.int32, dev, "cu_seqlens"), N, T, D, dt, gt, flags,
+            *_rows(dx, shape, dy.dtype, dev, "dx"), *_rows(dg, shape, g.dtype, dev, "dg"),
+            _need(d_initial_state, state, f32, dev, "d_initial_state"), wp, wn,
+            torch.cuda.current_stream(dev).cuda_stream))
+    return dx, dg, d_initial_state
+
+
+def linrec_step(x, g, state_pool, state_indices, cu_seqlens, *, flags: int = GDR_COMMIT, y=None,
+                intermediate_states=None, stream=None):
+    """The recurrence over a few tokens per sequence from state_pool [slots, D]
+    (fp32 or bf16) at state_indices [N] int32 (< 0: skipped).  The pool is
+    updated in place only with GDR_COMMIT; intermediate_states [rows >= N,
+    steps, D] (pool dtype) receives the state after every token.  Returns y."""
+    dev = _device_of(x, "x")
+    T, D = shape = x.shape
+    N = cu_seqlens.numel() - 1
+    steps, states = 0, None
+    slots = state_pool.shape[0]
+    if intermediate_states is not None:
+        if intermediate_states.dim() != 3 or intermediate_states.shape[0] < N:
+            raise ValueError("intermediate_states must be [rows >= N, steps, D]")
+        rows, steps = intermediate_states.shape[:2]
+        states = _need(intermediate_states, (rows, steps, D), state_pool.dtype, dev, "intermediate_states")
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty(T, D, dtype=x.dtype, device=dev)
+        _check(load().gdr_linrec_step(
+            *_rows(x, shape, x.dtype, dev, "x"), *_rows(g, shape, g.dtype, dev, "g"),
+            _need(state_pool, (slots, D), state_pool.dtype, dev, "state_pool"), _dtype_code(state_pool), slots,
+            _need(state_indices, (N,), torch.int32, dev, "state_indices"),
+            _need(cu_seqlens, (N + 1,), torch.int32, dev, "cu_seqlens"), N, T, D, _dtype_code(x), _dtype_code(g),
+            flags, *_rows(y, shape, x.dtype, dev, "y"), states, steps, torch.cuda.current_stream(dev).cuda_stream))
+    return y
+
+
+def rmsnorm_fwd(x, weight, *, residual=None, eps: float = 1e-6, y_dtype=None, scale_group: int = 0, y=None,
+                residual_out=None, scales=None, stream=None):
+    """s = x + residual (rounded to x's dtype; x without a residual), y = s /
+    sqrt(mean(s^2) + eps) * weight per row of x [M, D] (bf16 or fp32); weight
+    [D] fp32.  y_dtype None: y in x's dtype; torch.float8_e4m3fn: codes, with
+    one fp32 scale per scale_group (32, 64, 128; 0: the row) elements of a row.
+    residual_out may be residual (or x) itself.  Returns (y, residual_out or
+    None, scales or None)."""
+    dev = _device_of(x, "x")
+    M, D = shape = x.shape
+    if y_dtype is None:
+        y_dtype = x.dtype if y is None else y.dtype
+    dt = _dtype_code(x)
+    yt = GDR_E4M3 if y_dtype == torch.float8_e4m3fn else GDR_BF16 if y_dtype == torch.bfloat16 else \
+        GDR_F32 if y_dtype == torch.float32 else -1
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out without residual")
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty(M, D, dtype=y_dtype, device=dev)
+        sp = None
+        if yt == GDR_E4M3:
+            groups = -(-D // scale_group) if scale_group > 0 else 1
+            if scales is None:
+                scales = torch.empty(M, groups, dtype=torch.float32, device=dev)
+            sp = _need(scales, (M, groups), torch.float32, dev, "scales")
+        elif scales is not None:
+            raise ValueError("scales go with y_dtype torch.float8_e4m3fn only")
+        if residual is not None:
+            if residual_out is None:
+                residual_out = torch.empty(M, D, dtype=x.dtype, device=dev)
+            rp = _rows(residual, shape, x.dtype, dev, "residual")
+            op = _rows(residual_out, shape, x.dtype, dev, "residual_out")
+        else:
+            rp = op = (None, 0)
+        _check(load().gdr_rmsnorm_fwd(
+            *_rows(x, shape, x.dtype, dev, "x"), *rp, _need(weight, (D,), torch.float32, dev, "weight"), M, D, eps,
+            dt, *op, *_rows(y, shape, y_dtype, dev, "y"), yt, sp, scale_group,
+            torch.cuda.current_stream(dev).cuda_stream))
+    return y, residual_out, scales
+
+
+def rmsnorm_bwd_workspace_size(M: int, D: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().gdr_rmsnorm_bwd_workspace_size(M, D, ctypes.byref(out)))
+    return out.value
+
+
+def rmsnorm_bwd(dy, s, weight, *, eps: float = 1e-6, d_residual_out=None, dx=None, dweight=None,
+                output_dweight: bool = True, workspace=None, stream=None):
+    """Gradients of rmsnorm_fwd from dy [M, D]; s [M, D] is the forward's
+    residual_out (x without a residual), d_residual_out the gradient arriving
+    at s along the residual stream.  Returns (dx, dweight): dx is the gradient
+    of x and of residual alike, dweight [D] fp32."""
+    dev = _device_of(dy, "dy")
+    M, D = shape = dy.shape
+    with _on(dev, stream):
+        if dx is None:
+            dx = torch.empty(M, D, dtype=dy.dtype, device=dev)
+        if dweight is None and output_dweight:
+            dweight = torch.empty(D, dtype=torch.float32, device=dev)
+        ws = wp = None
+        wn = 0
+        if dweight is not None:
+            ws, wp, wn = _pool_of(rmsnorm_bwd_workspace_size(M, D), dev) if workspace is None \
+                else _given(workspace, dev)
+        rp = (None, 0) if d_residual_out is None else _rows(d_residual_out, shape, dy.dtype, dev, "d_residual_out")
+        _check(load().gdr_rmsnorm_bwd(
+            *_rows(dy, shape, dy.dtype, dev, "dy"), *_rows(s, shape, dy.dtype, dev, "s"),
+            _need(weight, (D,), torch.float32, dev, "weight"), *rp, M, D, eps, _dtype_code(dy),
+            *_rows(dx, shape, dy.dtype, dev, "dx"), _need(dweight, (D,), torch.float32, dev, "dweight"), wp, wn,
+            torch.cuda.current_stream(dev).cuda_stream))
+    return dx, dweight
 
 
 def device_status(stream=None) -> int:

@@ -39,19 +39,6 @@ int ok() {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// The kernels are built for sm_103a only.
-int check_device() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return fail(GDR_ERR_LAUNCH, "cudaGetDevice failed");
-    int major = 0, minor = 0;
-    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-    if (major != 10 || minor != 3)
-        return fail(GDR_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_103a only",
-                    dev, major, minor);
-    return GDR_OK;
-}
-
 int launch_status(cudaError_t e, const char* what) {
     if (e != cudaSuccess) return fail(GDR_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
     return ok();
@@ -130,6 +117,21 @@ int check_common(int N, int64_t T, int Hk, int Hv, int K, int V, int dtype) {
 }
 
 }  // namespace
+
+// The kernels are built for sm_103a only.
+int check_device() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return fail(GDR_ERR_LAUNCH, "cudaGetDevice failed");
+    int major = 0, minor = 0;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    if (major != 10 || minor != 3)
+        return fail(GDR_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_103a only",
+                    dev, major, minor);
+    return GDR_OK;
+}
+
+int set_ok() { return ok(); }
 
 int set_last_error(int code, const char* fmt, ...) {
     va_list ap;

@@ -122,6 +122,13 @@ cudaError_t launch_gating(const GatingArgs& a, cudaStream_t stream);
 // Record a formatted message for gdr_last_error() on this thread; returns code.
 int set_last_error(int code, const char* fmt, ...);
 
+// Clear the thread's last error; returns GDR_OK.
+int set_ok();
+
+// GDR_OK if the current device is one the kernels are built for (sm_103a),
+// else a status with its message set.
+int check_device();
+
 // Device error word (set by bounded device waits that give up).
 unsigned int* device_error_word();
 

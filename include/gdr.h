@@ -62,7 +62,11 @@ typedef enum gdr_status {
     GDR_ERR_VALIDATION = 6      /* GDR_VALIDATE found bad input content        */
 } gdr_status;
 
-typedef enum gdr_dtype { GDR_BF16 = 0, GDR_F32 = 1 } gdr_dtype;
+typedef enum gdr_dtype {
+    GDR_BF16 = 0,
+    GDR_F32 = 1,
+    GDR_E4M3 = 2 /* gdr_rmsnorm_fwd's y only: 8-bit codes with fp32 scales */
+} gdr_dtype;
 
 typedef enum gdr_gate_kind {
     GDR_GATE_SCALAR = 0,  /* g  [T, Hv]     one log-decay per token and value-head */
@@ -256,6 +260,169 @@ GDR_API int gdr_recurrent_fwd_gated(const void* q, const void* k, const void* v,
 GDR_API int gdr_gating_fwd(const void* a, const float* dt_bias, const float* A_log, const void* b,
                    int64_t T, int Hv, int dtype, int flags, float* g, void* beta,
                    gdr_stream_t stream);
+
+/*
+ * The gated linear recurrence: per channel c of sequence n, with the
+ * natural-log decay g <= 0 (-inf, a reset, is allowed),
+ *
+ *   h_t = exp(g_t) h_{t-1} + x_t,   h before the first token = initial_state[n]
+ *
+ * over the packed tokens cu_seqlens[n] .. cu_seqlens[n+1]-1.  The state is
+ * carried in fp32 whatever the tensors' types.
+ *
+ * Conventions of gdr_linrec_fwd, gdr_linrec_bwd and gdr_linrec_step, where
+ * they go beyond the library's:
+ *   - Token tensors are [T_total, D] with a row stride in elements of their
+ *     own (so they can be column blocks of a wider matrix): D or more for
+ *     tensors that are written, any stride >= 0 for those that are only read
+ *     (0: one row for every token).  They need their element's alignment only;
+ *     16-byte aligned rows (8 elements of the type) with D and the strides
+ *     multiples of 8 take the fast path.
+ *   - dtype (GDR_BF16 or GDR_F32) is that of x, y and their gradients,
+ *     gate_dtype (GDR_BF16 or GDR_F32) that of g and dg.  Prefill states are
+ *     fp32 [N, D], dense.
+ *   - cu_seqlens [N+1] int32 device, cu[0] = 0, non-decreasing; sequences may
+ *     be empty.  cu[N] may be less than T_total (a padded batch): rows from
+ *     cu[N] on are neither read nor written.  A cu_seqlens that breaks these
+ *     rules never causes an access outside the tensors, but what is written
+ *     is then unspecified; GDR_VALIDATE (the only flag of fwd and bwd) turns
+ *     it, and a gate that is NaN or > 0, into GDR_ERR_VALIDATION.
+ *   - A NaN or infinity stays within its sequence and channel.
+ *   - Results do not depend on scheduling: equal inputs give equal bits.
+ *
+ * gdr_linrec_workspace_size -- bytes of device workspace that gdr_linrec_fwd
+ * and gdr_linrec_bwd need (the same for both; may be 0).  Host only.
+ */
+GDR_API int gdr_linrec_workspace_size(int N, int64_t T_total, int D, int dtype, int gate_dtype,
+                                      size_t* bytes);
+
+/*
+ * gdr_linrec_fwd -- the recurrence over packed sequences (prefill, training
+ * forward).
+ *   x              [T_total, D] dtype, row stride x_stride
+ *   g              [T_total, D] gate_dtype, row stride g_stride
+ *   initial_state  [N, D] fp32, or NULL for zeros
+ *   y              [T_total, D] dtype, row stride y_stride (written): y_t = h_t
+ *   final_state    [N, D] fp32 (written: the last h, the initial state where
+ *                  a sequence is empty), or NULL
+ *   workspace      device scratch of gdr_linrec_workspace_size bytes, 256-byte
+ *                  aligned (NULL where that is 0); needs no initialisation.
+ *                  Calls whose work may overlap on the GPU need one each.
+ */
+GDR_API int gdr_linrec_fwd(const void* x, int64_t x_stride, const void* g, int64_t g_stride,
+                           const float* initial_state, const int32_t* cu_seqlens, int N,
+                           int64_t T_total, int D, int dtype, int gate_dtype, int flags, void* y,
+                           int64_t y_stride, float* final_state, void* workspace, size_t ws_bytes,
+                           gdr_stream_t stream);
+
+/*
+ * gdr_linrec_bwd -- gradients of gdr_linrec_fwd from the gradient dy of y and
+ * d_final_state [N, D] fp32 (NULL for zeros) of the final state.  With mu
+ * after a sequence's last token = d_final_state[n],
+ *
+ *   lam_t = dy_t + mu_{t+1},  mu_t = exp(g_t) lam_t
+ *   dx_t = lam_t,   dg_t = mu_t h_{t-1},   d_initial_state[n] = mu of the first token
+ *
+ * h_{t-1} is read from y, the forward's output as stored (initial_state, or 0,
+ * before the first token).
+ *   dx  [T_total, D] dtype, dg [T_total, D] gate_dtype (written)
+ *   d_initial_state [N, D] fp32 (written; d_final_state's row where a sequence
+ *                   is empty), or NULL
+ */
+GDR_API int gdr_linrec_bwd(const void* dy, int64_t dy_stride, const void* g, int64_t g_stride,
+                           const void* y, int64_t y_stride, const float* initial_state,
+                           const float* d_final_state, const int32_t* cu_seqlens, int N,
+                           int64_t T_total, int D, int dtype, int gate_dtype, int flags, void* dx,
+                           int64_t dx_stride, void* dg, int64_t dg_stride, float* d_initial_state,
+                           void* workspace, size_t ws_bytes, gdr_stream_t stream);
+
+/*
+ * gdr_linrec_step -- the recurrence over a few tokens of each sequence, from
+ * and to a slot-indexed state pool: decode and multi-step verify, with
+ * gdr_recurrent_fwd's rules.
+ *   state_pool     [num_slots, D] pool_dtype (GDR_F32 or GDR_BF16), dense; read,
+ *                  and written in place only with GDR_COMMIT
+ *   state_indices  [N] int32 device: the slot of each sequence; a value < 0 is
+ *                  padding (nothing of that sequence is read or written; nor is
+ *                  it for a value >= num_slots, an error that GDR_VALIDATE
+ *                  reports).  With GDR_COMMIT valid slots must be unique.
+ *   intermediate_states  [rows >= N, steps, D] pool dtype, dense, or NULL: row
+ *                  b, step t receives the state after token t of sequence b;
+ *                  steps >= L_b and padding rows are untouched.  L_b <= steps
+ *                  (checked under GDR_VALIDATE; later tokens' states are
+ *                  dropped otherwise).
+ * Flags: GDR_COMMIT, GDR_VALIDATE.
+ */
+GDR_API int gdr_linrec_step(const void* x, int64_t x_stride, const void* g, int64_t g_stride,
+                            void* state_pool, int pool_dtype, int num_slots,
+                            const int32_t* state_indices, const int32_t* cu_seqlens, int N,
+                            int64_t T_total, int D, int dtype, int gate_dtype, int flags, void* y,
+                            int64_t y_stride, void* intermediate_states, int steps,
+                            gdr_stream_t stream);
+
+/*
+ * gdr_rmsnorm_fwd -- root-mean-square norm of every row, with the residual's
+ * addition before it:
+ *
+ *   s = round(x + residual)  (x without a residual)
+ *   y = s / sqrt(mean(s^2) + eps) * weight
+ *
+ * The sum is rounded to dtype first, so that y is the norm of the residual
+ * stream as it is stored.
+ *   x, residual    [M, D] dtype (GDR_BF16 or GDR_F32), row strides in elements
+ *                  (any >= 0); residual may be NULL
+ *   weight         [D] fp32
+ *   residual_out   [M, D] dtype: s (written).  Given if and only if residual
+ *                  is.  It may be residual or x itself (the same pointer and
+ *                  stride): the addition is then in place.
+ *   y              [M, D] y_dtype (written): dtype, or GDR_E4M3 with scales
+ *   scales         [M, ceil(D / group)] fp32, dense (written), with GDR_E4M3
+ *                  only: for each group of scale_group consecutive elements of
+ *                  a row (32, 64 or 128; 0: the whole row), with a the larger of
+ *                  max |y| and 1e-12, scale = a / 448 and the stored code is
+ *                  y / scale rounded to the nearest e4m3 value, so that
+ *                  code * scale stands for y.  y is not rounded before.
+ * D up to GDR_RMSNORM_MAX_D.  Rows need their element's alignment only; rows
+ * of 8 aligned elements, with D and the strides multiples of 8, take the fast
+ * path.  Sums are fp32: a row whose sum of squares passes fp32's range
+ * (elements above about 1e19) gives 0 for its finite elements.
+ */
+#define GDR_RMSNORM_MAX_D 32768
+GDR_API int gdr_rmsnorm_fwd(const void* x, int64_t x_stride, const void* residual,
+                            int64_t residual_stride, const float* weight, int64_t M, int D,
+                            float eps, int dtype, void* residual_out, int64_t residual_out_stride,
+                            void* y, int64_t y_stride, int y_dtype, float* scales, int scale_group,
+                            gdr_stream_t stream);
+
+/* gdr_rmsnorm_bwd_workspace_size -- bytes of device workspace gdr_rmsnorm_bwd
+ * needs.  Host only. */
+GDR_API int gdr_rmsnorm_bwd_workspace_size(int64_t M, int D, size_t* bytes);
+
+/*
+ * gdr_rmsnorm_bwd -- gradients of gdr_rmsnorm_fwd from dy, the gradient of y
+ * (for GDR_E4M3: of the values its codes stand for, the rounding taken as the
+ * identity), and d_residual_out, the gradient that arrives at s along the
+ * residual stream (NULL for zeros).  With r = 1 / sqrt(mean(s^2) + eps) and
+ * z = weight * dy,
+ *
+ *   dx = r z - r^3 s mean(s z) + d_residual_out   (of x and of residual alike)
+ *   dweight = sum over rows of r dy s
+ *
+ *   dy, s, d_residual_out  [M, D] dtype, row strides in elements (any >= 0); s
+ *                          is the forward's residual_out (or x)
+ *   dx                     [M, D] dtype (written); may be dy or d_residual_out
+ *                          itself (the same pointer and stride)
+ *   dweight                [D] fp32 (written, not accumulated into), or NULL
+ *   workspace              gdr_rmsnorm_bwd_workspace_size bytes, 256-byte
+ *                          aligned; needs no initialisation; may be NULL with
+ *                          dweight NULL
+ * The rows are summed in a fixed order: equal inputs give equal bits.
+ */
+GDR_API int gdr_rmsnorm_bwd(const void* dy, int64_t dy_stride, const void* s, int64_t s_stride,
+                            const float* weight, const void* d_residual_out,
+                            int64_t d_residual_out_stride, int64_t M, int D, float eps, int dtype,
+                            void* dx, int64_t dx_stride, float* dweight, void* workspace,
+                            size_t ws_bytes, gdr_stream_t stream);
 
 /* Description of the last error on the calling thread ("" if none). */
 GDR_API const char* gdr_last_error(void);

@@ -15,6 +15,9 @@ Contents
   * ``gated_rmsnorm`` -- the optional output epilogue of decode (numpy, fp64):
                        rmsnorm(o) * w * sigmoid(gate) over each value row
                        (tokenspeed PR #834, fused gated-norm epilogue commit).
+  * ``linrec``, ``linrec_bwd`` -- the gated linear recurrence of packed
+                       sequences and its gradients (numpy, fp64).
+  * ``rmsnorm``, ``rmsnorm_bwd`` -- the row norm and its gradients (numpy, fp64).
 
 Recurrence per value-head (state S in R^{V x K}, V-major):
   S~ = exp(g_t) S_{t-1};  n_t = beta_t (v_t - S~ k_t);  S_t = S~ + n_t k_t^T;
@@ -235,3 +238,51 @@ def bruteforce(q, k, v, beta, *, g=None, gk=None, initial_state=None, scale):
             tail = tail @ Ps[s]
         closed = closed + beta[t] * np.outer(v[t], k[t]) @ tail
     return o, S, closed
+
+
+def linrec(x, g, cu_seqlens, *, initial_state=None):
+    """h_t = exp(g_t) h_{t-1} + x_t of each packed sequence, token by token.
+    Rows outside every sequence are NaN.  Returns (y [T, D], final [N, D])."""
+    x, g, cu = _f64(x), _f64(g), _cu64(cu_seqlens)
+    N, D = len(cu) - 1, x.shape[1]
+    y = np.full(x.shape, np.nan)
+    final = np.zeros((N, D)) if initial_state is None else _f64(initial_state).copy()
+    for n in range(N):
+        h = final[n]
+        for t in range(cu[n], cu[n + 1]):
+            h = np.exp(g[t]) * h + x[t]
+            y[t] = h
+        final[n] = h
+    return y, final
+
+
+def linrec_bwd(dy, g, y, cu_seqlens, *, initial_state=None, d_final_state=None):
+    """Gradients of ``linrec`` from dy and the final state's gradient, with
+    h_{t-1} taken from the given y.  Returns (dx, dg, d_initial_state)."""
+    dy, g, y, cu = _f64(dy), _f64(g), _f64(y), _cu64(cu_seqlens)
+    N, D = len(cu) - 1, dy.shape[1]
+    dx, dg = np.full(dy.shape, np.nan), np.full(dy.shape, np.nan)
+    first = np.zeros((N, D)) if d_final_state is None else _f64(d_final_state).copy()
+    h0 = np.zeros((N, D)) if initial_state is None else _f64(initial_state)
+    for n in range(N):
+        mu = first[n]
+        for t in range(cu[n + 1] - 1, cu[n] - 1, -1):
+            dx[t] = dy[t] + mu
+            mu = np.exp(g[t]) * dx[t]
+            dg[t] = mu * (y[t - 1] if t > cu[n] else h0[n])
+        first[n] = mu
+    return dx, dg, first
+
+
+def rmsnorm(s, weight, eps: float):
+    """s / sqrt(mean(s^2) + eps) * weight over the last axis."""
+    s = _f64(s)
+    return s / np.sqrt((s * s).mean(-1, keepdims=True) + eps) * _f64(weight)
+
+
+def rmsnorm_bwd(dy, s, weight, eps: float):
+    """Gradients (ds, dweight) of ``rmsnorm``."""
+    dy, s, w = _f64(dy), _f64(s), _f64(weight)
+    r = 1 / np.sqrt((s * s).mean(-1, keepdims=True) + eps)
+    z = w * dy
+    return r * z - r ** 3 * s * (s * z).mean(-1, keepdims=True), (r * dy * s).sum(0)
