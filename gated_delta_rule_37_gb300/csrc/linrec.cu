@@ -1,11 +1,40 @@
 // The gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t over packed
 // sequences: forward, backward and the slot-pool step, with their C entry
 // points (contract in include/gdr.h).
+//
+// The scan.  A token is the affine map h -> a h + b (a = exp(g), b = x), and
+// maps compose: (A, B) then (a, b) is (a A, a B + b).  The packed token axis is
+// cut into tiles of TT tokens by CC channels without regard to the sequences;
+// a token that starts a sequence takes its state from h0 instead of from its
+// left and cuts the composition there (a selection, not a product by 0, so that
+// nothing of one sequence, NaN included, reaches the next).  One pass over the
+// data: a tile is read once into registers, composed by runs of R tokens per
+// thread and across the threads, waits for the state that reaches its first
+// token, and is then evaluated from registers and written.
+//   Between tiles: a tile publishes its composition (A, B), and its outgoing
+// state once it knows its incoming one.  A tile looks back from its left
+// neighbour to the nearest published state and folds the compositions between
+// into it, always in token order and with the same fused multiply-adds, so that
+// the bits do not depend on which of the two it found.  Tiles are handed out by
+// a counter in token order, so that a tile only ever waits for tiles that are
+// already running; every wait has a limit.
+//   The backward is the same scan from the end: with mu_t = a_t (dy_t + mu_{t+1})
+// a token is the map mu -> a (mu + dy); dx = dy + mu_{t+1}, dg = mu_t h_{t-1}.
+//
+// Accuracy: a near 1 is applied thousands of times, so its error must have no
+// mean.  The hardware's exponential is about 0.3 * 2^-24 low on average just
+// below 0, which a memory of 4000 tokens turns into 6e-5 of the state; the
+// Taylor polynomial of degree 6 below 1/4, ending in a fused multiply-add with
+// 1, has a mean error below 0.001 * 2^-24.
+#include <cuda.h>
 #include <math.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "gdr.h"
 #include "launch.h"
+#include "tc.cuh"
 
 namespace gdr {
 namespace {
@@ -23,56 +52,701 @@ struct LinrecParams {
     int64_t ldx, ldg, ldh, ldo, lddg;
     int64_t T;
     int N, D;
+    int groups;          // channel groups of a tile row
+    int rows;            // tile rows of T tokens
+    unsigned int* head;  // workspace: [0] the tile counter, [1] set when a wait gave up
+    unsigned int* flags;  // [groups][rows]: 0, kComposed or kState
+    float* comp_a;       // [groups][rows][CC]: A, B of a tile, its outgoing state
+    float* comp_b;
+    float* state;
+    unsigned int* err;
 };
 
-// One thread per (sequence, channel), token after token.
-template <typename TX, typename TG, bool BWD>
-__global__ void linrec_serial_kernel(LinrecParams p) {
-    const int c = blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= p.D) return;
-    const TX* x = static_cast<const TX*>(p.x);
-    const TG* g = static_cast<const TG*>(p.g);
-    const TX* hs = static_cast<const TX*>(p.h);
-    TX* out = static_cast<TX*>(p.out);
-    TG* dg = static_cast<TG*>(p.dg);
-    for (int64_t n = blockIdx.y; n < p.N; n += gridDim.y) {
-        const int64_t lo = max((int64_t)p.cu[n], (int64_t)0), hi = min((int64_t)p.cu[n + 1], p.T);
-        float h = p.start ? p.start[n * p.D + c] : 0.f;
-        for (int64_t i = 0; i < hi - lo; ++i) {
-            const int64_t t = BWD ? hi - 1 - i : lo + i;
-            const float a = expf(to_f(g[t * p.ldg + c])), b = to_f(x[t * p.ldx + c]);
-            if (BWD) {
-                const float lam = b + h;
-                out[t * p.ldo + c] = from_f<TX>(lam);
-                h = a * lam;
-                const float before = t > lo ? to_f(hs[(t - 1) * p.ldh + c]) : p.h0 ? p.h0[n * p.D + c] : 0.f;
-                dg[t * p.lddg + c] = from_f<TG>(h * before);
-            } else {
-                h = fmaf(a, h, b);
-                out[t * p.ldo + c] = from_f<TX>(h);
-            }
+constexpr unsigned kComposed = 1, kState = 2;
+constexpr unsigned kScanError = 0x200;  // device error word: a tile's wait gave up
+
+// ---- exp(g) -------------------------------------------------------------------
+
+constexpr float kTaylor = 0.25f;  // |g| up to here: the polynomial
+
+__device__ __forceinline__ float taylor_exp(float g) {
+    float p = fmaf(g, 1.f / 720, 1.f / 120);
+    p = fmaf(g, p, 1.f / 24);
+    p = fmaf(g, p, 1.f / 6);
+    p = fmaf(g, p, 0.5f);
+    p = fmaf(g, p, 1.f);
+    return fmaf(g, p, 1.f);
+}
+
+__device__ __forceinline__ float decay(float g) { return fabsf(g) > kTaylor ? expf(g) : taylor_exp(g); }
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ void decay(float (&g)[1]) { g[0] = decay(g[0]); }
+
+__device__ __forceinline__ void decay(float (&g)[8]) {
+    float most = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(g[j]));
+    float a[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const float2 v = make_float2(g[j], g[j + 1]);
+        float2 p = __ffma2_rn(v, both(1.f / 720), both(1.f / 120));
+        p = __ffma2_rn(v, p, both(1.f / 24));
+        p = __ffma2_rn(v, p, both(1.f / 6));
+        p = __ffma2_rn(v, p, both(0.5f));
+        p = __ffma2_rn(v, p, both(1.f));
+        p = __ffma2_rn(v, p, both(1.f));
+        a[j] = p.x;
+        a[j + 1] = p.y;
+    }
+    if (most > kTaylor) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (fabsf(g[j]) > kTaylor) a[j] = expf(g[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] = a[j];
+}
+
+// ---- VEC consecutive elements, kept as they are stored -------------------------
+
+template <typename T, int VEC> struct Row;
+
+template <> struct Row<__nv_bfloat16, 8> {
+    uint4 v;
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
-        if (p.last) p.last[n * p.D + c] = h;
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(tc::pack_bf16(f[0], f[1]), tc::pack_bf16(f[2], f[3]),
+                                                  tc::pack_bf16(f[4], f[5]), tc::pack_bf16(f[6], f[7]));
+    }
+};
+template <> struct Row<float, 8> {
+    float4 a, b;
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void load(const float* p) {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+    static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+};
+template <typename T> struct Row<T, 1> {
+    T v;
+    __device__ __forceinline__ void zero() { v = from_f<T>(0.f); }
+    __device__ __forceinline__ void load(const T* p) { v = *p; }
+    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f(v); }
+    static __device__ __forceinline__ void store(T* p, const float (&f)[1]) { *p = from_f<T>(f[0]); }
+};
+
+// One token of the scan: h <- a h + b, or h <- a (h + b) from the end.
+template <bool BWD, int VEC>
+__device__ __forceinline__ void advance(float (&h)[VEC], const float (&a)[VEC], const float (&b)[VEC]) {
+    if (VEC == 1) {
+        h[0] = BWD ? a[0] * (h[0] + b[0]) : fmaf(a[0], h[0], b[0]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2) {
+            const float2 a2 = make_float2(a[j], a[j + 1]), b2 = make_float2(b[j], b[j + 1]);
+            float2 h2 = make_float2(h[j], h[j + 1]);
+            h2 = BWD ? __fmul2_rn(a2, __fadd2_rn(h2, b2)) : __ffma2_rn(a2, h2, b2);
+            h[j] = h2.x;
+            h[j + 1] = h2.y;
+        }
     }
 }
 
-template <typename TX, typename TG>
-cudaError_t launch_serial(const LinrecParams& p, bool bwd, cudaStream_t s) {
-    const dim3 grid((p.D + 127) / 128, p.N < 65535 ? p.N : 65535);
-    KernelTimer kt(bwd ? "linrec_bwd" : "linrec_fwd", s);
-    if (bwd)
-        linrec_serial_kernel<TX, TG, true><<<grid, 128, 0, s>>>(p);
-    else
-        linrec_serial_kernel<TX, TG, false><<<grid, 128, 0, s>>>(p);
-    return cudaGetLastError();
+// ---- the tile kernel --------------------------------------------------------------
+
+// WIDE: 8 channels per thread, 64 per tile, staged by TMA (aligned rows).
+// Otherwise one channel per thread, 32 per tile, read directly.
+template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
+    static constexpr int THREADS = 256, WARPS = THREADS / 32;
+    static constexpr int VEC = WIDE ? 8 : 1, LANES = WIDE ? 8 : 32, CC = VEC * LANES;
+    static constexpr int RUNS = WARPS * 32 / LANES;          // runs of R tokens
+    // A token takes 8 registers for its decays and 4 or 8 for each of b and h as
+    // stored; R of them is what fits beside the rest at two CTAs per SM.
+    static constexpr int R = !WIDE ? 16 : sizeof(TX) == 2 ? (BWD ? 4 : 5) : (BWD ? 3 : 4);
+    static constexpr int TT = RUNS * R;
+    static constexpr int PARTS = THREADS / CC, RUNS_PART = RUNS / PARTS;  // the fold over runs, in parts
+    // shared memory (bytes)
+    static constexpr int XS = 0, GS = XS + (WIDE ? TT * CC * (int)sizeof(TX) : 0);
+    static constexpr int HS = GS + (WIDE ? TT * CC * (int)sizeof(TG) : 0);
+    static constexpr int STAGE = HS + (WIDE && BWD ? TT * CC * (int)sizeof(TX) : 0);
+    static constexpr int CA = STAGE, CB = CA + RUNS * CC * 4, PA = CB + RUNS * CC * 4, PB = PA + PARTS * CC * 4;
+    static constexpr int CARRY = PB + PARTS * CC * 4, FIRST = CARRY + CC * 4, LAST = FIRST + 2 * TT * 4;
+    static constexpr int CUT = LAST + 2 * TT * 4, MISC = CUT + RUNS * 4, BYTES_SMEM = MISC + 64;
+    static_assert(RUNS % PARTS == 0 && STAGE % 128 == 0 && TT <= 256, "tile shape");
+    // the 16-byte halves of a thread's 8 channels are kept CC / 2 apart: its float4
+    // accesses then touch all banks in turn
+    static __device__ __forceinline__ int place(int lane, int j) {
+        return WIDE ? (j < 4 ? lane * 4 + j : CC / 2 + lane * 4 + j - 4) : lane;
+    }
+};
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c, int t, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        :: "r"(dst), "l"(map), "r"(c), "r"(t), "r"(mbar) : "memory");
 }
 
-cudaError_t launch_scan(const LinrecParams& p, int dtype, int gate_dtype, bool bwd, cudaStream_t s) {
+__device__ __forceinline__ unsigned load_acquire(const unsigned int* p) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_release(unsigned int* p, unsigned v) {
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" :: "l"(p), "r"(v) : "memory");
+}
+
+// The sequences that begin and end in the tile of tokens [t0, t0 + TT): by the
+// order of the scan, first[i] / last[i] is the sequence whose scan starts before
+// token i / ends after it, or -1.  One warp; returns whether there is any.
+template <int TT, bool BWD>
+__device__ bool find_boundaries(const int32_t* cu, int N, int t0, int* first, int* last, int lane) {
+    // smallest m in [0, N] with cu[m] >= t0 (N + 1 if none), 32 probes at a time
+    int lo = 0, n = N + 1;
+    while (n > 0) {
+        const int step = (n + 31) / 32;
+        const int m = lo + lane * step;  // the first element of this lane's piece
+        const unsigned less = __ballot_sync(0xffffffffu, m < lo + n && cu[min(m, N)] < t0);
+        if (!less) break;
+        const int k = 31 - __clz(less);  // the boundary lies in piece k, behind its first element
+        const int end = min(lo + (k + 1) * step, lo + n);
+        lo += k * step + 1;
+        n = end - lo;
+    }
+    int m = lo + lane, at = m <= N ? cu[m] : 0x7fffffff;
+    bool in = at >= t0 && at - t0 <= TT;
+    if (!__any_sync(0xffffffffu, in)) return false;
+    for (int i = lane; i < TT; i += 32) first[i] = last[i] = -1;
+    __syncwarp();
+    while (true) {
+        if (in) {
+            const int k = at - t0;  // between tokens k - 1 and k of the tile
+            if (k < TT && m < N && cu[m + 1] > at) (BWD ? last : first)[BWD ? TT - 1 - k : k] = m;
+            if (k > 0 && m > 0 && cu[m - 1] < at) (BWD ? first : last)[BWD ? TT - k : k - 1] = m - 1;
+        }
+        // sorted: once a lane is beyond the tile, so is everything after it
+        if (__any_sync(0xffffffffu, m >= N || (int64_t)at - t0 > TT)) break;
+        m += 32;
+        at = m <= N ? cu[m] : 0x7fffffff;
+        in = at >= t0 && at - t0 <= TT;
+    }
+    return true;
+}
+
+template <typename TX, typename TG, bool BWD, bool WIDE>
+__global__ void __launch_bounds__(256, 2)
+linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g,
+                   const __grid_constant__ CUtensorMap map_h, const __grid_constant__ LinrecParams p) {
+    using C = Tile<TX, TG, BWD, WIDE>;
+    constexpr int VEC = C::VEC, CC = C::CC, R = C::R, TT = C::TT;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    TX* xs = reinterpret_cast<TX*>(smem + C::XS);
+    TG* gs = reinterpret_cast<TG*>(smem + C::GS);
+    TX* hs = reinterpret_cast<TX*>(smem + C::HS);
+    float* ca = reinterpret_cast<float*>(smem + C::CA);
+    float* cb = reinterpret_cast<float*>(smem + C::CB);
+    float* pa = reinterpret_cast<float*>(smem + C::PA);
+    float* pb = reinterpret_cast<float*>(smem + C::PB);
+    float* carry_s = reinterpret_cast<float*>(smem + C::CARRY);
+    int* cut_s = reinterpret_cast<int*>(smem + C::CUT);
+    uint64_t* mbar_s = reinterpret_cast<uint64_t*>(smem + C::MISC);
+    int* misc = reinterpret_cast<int*>(smem + C::MISC + 16);  // next tile, abort, boundaries of either buffer
+    volatile int* abort_s = misc + 1;
+    const uint32_t mbar = tc::smem_u32(mbar_s);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int lc = lane % C::LANES, run = warp * (32 / C::LANES) + lane / C::LANES;
+    const int part = tid / CC, pos = tid % CC;
+    const bool many = p.rows > 1;
+
+    if (tid == 0) {
+        tc::mbar_init(mbar, 1);
+        tc::mbar_fence_init();
+        *abort_s = 0;
+    }
+    if (many) tc::grid_dep_wait();  // the workspace's head and flags have been cleared
+    const int valid = min((int64_t)max(p.cu[p.N], 0), p.T);
+    const int rows = (valid + TT - 1) / TT;  // tile rows that hold a sequence's token
+    const int64_t tiles = (int64_t)rows * p.groups;
+
+    // tiles are taken in the order of the scan, all channel groups of a row first
+    auto take = [&]() -> int64_t { return many ? (int64_t)atomicAdd(p.head, 1u) : tiles; };
+    auto token0 = [&](int64_t tile) -> int {
+        const int row = (int)(tile / p.groups);
+        return (BWD ? rows - 1 - row : row) * TT;
+    };
+    auto request = [&](int64_t tile) {  // one thread: the tile's rows into the stage
+        if (!WIDE) return;
+        const int c = (int)(tile % p.groups) * CC, t = token0(tile);
+        tc::mbar_arrive_tx(mbar, C::STAGE);
+        tma_load_2d(tc::smem_u32(xs), &map_x, c, t, mbar);
+        tma_load_2d(tc::smem_u32(gs), &map_g, c, t, mbar);
+        if (BWD) tma_load_2d(tc::smem_u32(hs), &map_h, c, t - 1, mbar);  // row t - 1 beside token t
+    };
+
+    if (tid == 0) {
+        const int64_t t = many ? take() : (int64_t)blockIdx.x;
+        misc[0] = t < tiles ? (int)t : -1;
+        if (t < tiles) request(t);
+    }
+    __syncthreads();
+    int tile = misc[0];
+    __syncthreads();
+    if (tile >= 0 && warp == C::WARPS - 1) {
+        const bool any = find_boundaries<TT, BWD>(p.cu, p.N, token0(tile), reinterpret_cast<int*>(smem + C::FIRST),
+                                                  reinterpret_cast<int*>(smem + C::LAST), lane);
+        if (lane == 0) misc[2] = any;
+    }
+
+    for (int it = 0; tile >= 0; ++it) {
+        const int buf = it & 1;
+        const int group = tile % p.groups, row = tile / p.groups, t0 = token0(tile), c0 = group * CC + lc * VEC;
+        const int* first = reinterpret_cast<int*>(smem + C::FIRST) + buf * TT;
+        const int* last = reinterpret_cast<int*>(smem + C::LAST) + buf * TT;
+        int64_t next = tiles;
+        if (tid == 0) next = take();
+        if (WIDE && !tc::mbar_wait(mbar, buf, abort_s)) {
+            *abort_s = 1;
+            atomicOr(p.err, kScanError);
+        }
+        __syncthreads();
+        const bool bounded = misc[2 + buf] != 0;  // sequences begin or end in the tile
+        const bool here = c0 < p.D;
+
+        // ---- into registers, and the composition of the thread's run
+        float a[R][VEC];
+        Row<TX, VEC> b[R], h[BWD ? R : 1];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int i = run * R + r, l = BWD ? TT - 1 - i : i, t = t0 + l;
+            const bool ok = here && t < valid;
+            b[r].zero();
+            if (BWD) h[r].zero();
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) a[r][j] = 0.f;  // gates first: exp(0) = 1 is the identity
+            if (ok) {
+                Row<TG, VEC> gr;
+                if (WIDE) {
+                    gr.load(gs + l * CC + lc * VEC);
+                    b[r].load(xs + l * CC + lc * VEC);
+                    if (BWD) h[r].load(hs + l * CC + lc * VEC);
+                } else {
+                    gr.load(static_cast<const TG*>(p.g) + t * p.ldg + c0);
+                    b[r].load(static_cast<const TX*>(p.x) + t * p.ldx + c0);
+                    if (BWD && t > 0) h[r].load(static_cast<const TX*>(p.h) + (t - 1) * p.ldh + c0);
+                }
+                gr.get(a[r]);
+            }
+        }
+        float A[VEC], B[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            A[j] = 1.f;
+            B[j] = 0.f;
+        }
+        auto start_state = [&](int n, float (&f)[VEC]) {
+            Row<float, VEC> s;
+            s.zero();
+            if (p.start && here) s.load(p.start + (int64_t)n * p.D + c0);
+            s.get(f);
+        };
+        int cut = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            decay(a[r]);
+            float f[VEC];
+            b[r].get(f);
+            if (bounded) {
+                const int n = first[run * R + r];
+                if (n >= 0) {
+                    start_state(n, B);
+                    cut = 1;
+                }
+            }
+            advance<BWD, VEC>(B, a[r], f);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) A[j] *= a[r][j];
+        }
+        if (WIDE) {
+            *reinterpret_cast<float4*>(ca + run * CC + C::place(lc, 0)) = make_float4(A[0], A[1 % VEC], A[2 % VEC], A[3 % VEC]);
+            *reinterpret_cast<float4*>(ca + run * CC + C::place(lc, 4)) = make_float4(A[4 % VEC], A[5 % VEC], A[6 % VEC], A[7 % VEC]);
+            *reinterpret_cast<float4*>(cb + run * CC + C::place(lc, 0)) = make_float4(B[0], B[1 % VEC], B[2 % VEC], B[3 % VEC]);
+            *reinterpret_cast<float4*>(cb + run * CC + C::place(lc, 4)) = make_float4(B[4 % VEC], B[5 % VEC], B[6 % VEC], B[7 % VEC]);
+        } else {
+            ca[run * CC + lc] = A[0];
+            cb[run * CC + lc] = B[0];
+        }
+        if (lc == 0) cut_s[run] = cut;
+        if (tid == 0) misc[0] = next < tiles ? (int)next : -1;
+        __syncthreads();
+        if (*abort_s) break;
+        const int ntile = misc[0];
+        if (tid == 0 && ntile >= 0) request(ntile);  // the stage has been read
+
+        // ---- the runs of each part, then the parts: the tile's composition
+        {
+            float fa = 1.f, fb = 0.f;
+#pragma unroll
+            for (int s = part * C::RUNS_PART; s < (part + 1) * C::RUNS_PART; ++s) {
+                const float ra = ca[s * CC + pos], rb = cb[s * CC + pos];
+                if (bounded && cut_s[s]) {
+                    fb = rb;
+                } else {
+                    fb = fmaf(ra, fb, rb);
+                    fa *= ra;
+                }
+            }
+            pa[part * CC + pos] = fa;
+            pb[part * CC + pos] = fb;
+        }
+        // whether a part is cut: read from cut_s by everyone alike
+        auto part_cut = [&](int q) {
+            int c = 0;
+            if (bounded)
+                for (int s = q * C::RUNS_PART; s < (q + 1) * C::RUNS_PART; ++s) c |= cut_s[s];
+            return c != 0;
+        };
+        if (warp == C::WARPS - 1 && ntile >= 0) {  // while the others fold: the next tile's sequences
+            const int nb = buf ^ 1;
+            const bool any = find_boundaries<TT, BWD>(p.cu, p.N, token0(ntile),
+                                                      reinterpret_cast<int*>(smem + C::FIRST) + nb * TT,
+                                                      reinterpret_cast<int*>(smem + C::LAST) + nb * TT, lane);
+            if (lane == 0) misc[2 + nb] = any;
+        }
+        __syncthreads();
+        if (many && tid < CC) {
+            float fa = 1.f, fb = 0.f;
+            bool cut_any = false;
+#pragma unroll
+            for (int q = 0; q < C::PARTS; ++q) {
+                const float ra = pa[q * CC + pos], rb = pb[q * CC + pos];
+                if (part_cut(q)) {
+                    fb = rb;
+                    cut_any = true;
+                } else {
+                    fb = fmaf(ra, fb, rb);
+                    fa *= ra;
+                }
+            }
+            const int64_t rec = (int64_t)group * p.rows + row;
+            unsigned int* flag = p.flags + rec;
+            const bool settled = cut_any || row == 0;  // the outgoing state does not depend on the incoming one
+            if (settled) {
+                __stcg(p.state + rec * CC + pos, fb);
+            } else {
+                __stcg(p.comp_a + rec * CC + pos, fa);
+                __stcg(p.comp_b + rec * CC + pos, fb);
+            }
+            tc::bar_sync(1, CC);
+            if (tid == 0) store_release(flag, settled ? kState : kComposed);
+            float carry = 0.f;
+            if (row > 0) {
+                if (warp == 0) {
+                    // nearest row to the left with a state, every row between composed
+                    int base = row - 1, found = -1;
+                    const uint64_t began = tc::globaltimer_ns();
+                    for (unsigned spin = 1;; ++spin) {
+                        const int k = base - lane;
+                        const unsigned f = k >= 0 ? load_acquire(flag - row + k) : kComposed;
+                        const unsigned state = __ballot_sync(0xffffffffu, f == kState);
+                        const unsigned none = __ballot_sync(0xffffffffu, f == 0);
+                        if (state && !(none & ((state & -state) - 1))) {
+                            found = base - (__ffs(state) - 1);
+                            break;
+                        }
+                        if (!state && !none) {  // all composed: further left (row 0 always has a state)
+                            base -= 32;
+                            continue;
+                        }
+                        if ((spin & 63) == 0 &&
+                            (load_acquire(p.head + 1) || tc::globaltimer_ns() - began > tc::kWaitLimitNs))
+                            break;
+                    }
+                    if (lane == 0) {
+                        misc[4] = found;
+                        if (found < 0) {
+                            *abort_s = 1;
+                            store_release(p.head + 1, 1u);
+                            atomicOr(p.err, kScanError);
+                        }
+                    }
+                }
+                tc::bar_sync(1, CC);
+                const int found = misc[4];
+                if (found >= 0) {
+                    int64_t k = rec - row + found;
+                    carry = __ldcg(p.state + k * CC + pos);
+#pragma unroll 4
+                    for (++k; k < rec; ++k)
+                        carry = fmaf(__ldcg(p.comp_a + k * CC + pos), carry, __ldcg(p.comp_b + k * CC + pos));
+                }
+                if (!settled) __stcg(p.state + rec * CC + pos, fmaf(fa, carry, fb));
+            }
+            carry_s[pos] = carry;
+        }
+        __syncthreads();
+        if (*abort_s) {
+            if (WIDE && tid == 0 && ntile >= 0) tc::mbar_wait_copies(mbar, buf ^ 1);
+            break;
+        }
+        if (many && tid == 0 && row > 0) {
+            const int64_t rec = (int64_t)group * p.rows + row;
+            store_release(p.flags + rec, kState);  // a tile that is cut has set it before
+        }
+
+        // ---- the state that reaches each run
+        {
+            float f = many ? carry_s[pos] : 0.f;
+            for (int q = 0; q < part; ++q) f = part_cut(q) ? pb[q * CC + pos] : fmaf(pa[q * CC + pos], f, pb[q * CC + pos]);
+#pragma unroll
+            for (int s = part * C::RUNS_PART; s < (part + 1) * C::RUNS_PART; ++s) {
+                const float ra = ca[s * CC + pos], rb = cb[s * CC + pos];
+                ca[s * CC + pos] = f;
+                f = bounded && cut_s[s] ? rb : fmaf(ra, f, rb);
+            }
+        }
+        __syncthreads();
+        if (here) {
+            float s[VEC];
+            if (WIDE) {
+                const float4 u = *reinterpret_cast<const float4*>(ca + run * CC + C::place(lc, 0));
+                const float4 v = *reinterpret_cast<const float4*>(ca + run * CC + C::place(lc, 4));
+                s[0] = u.x; s[1 % VEC] = u.y; s[2 % VEC] = u.z; s[3 % VEC] = u.w;
+                s[4 % VEC] = v.x; s[5 % VEC] = v.y; s[6 % VEC] = v.z; s[7 % VEC] = v.w;
+            } else {
+                s[0] = ca[run * CC + lc];
+            }
+            // ---- every token from its state
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int i = run * R + r, l = BWD ? TT - 1 - i : i;
+                const int64_t t = t0 + l;
+                if (t >= valid) continue;
+                int n_first = -1, n_last = -1;
+                if (bounded) {
+                    n_first = first[i];
+                    n_last = last[i];
+                    if (n_first >= 0) start_state(n_first, s);
+                }
+                float f[VEC];
+                b[r].get(f);
+                if (BWD) {
+                    float lam[VEC], before[VEC];
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) lam[j] = f[j] + s[j];
+                    Row<TX, VEC>::store(static_cast<TX*>(p.out) + t * p.ldo + c0, lam);
+                    advance<BWD, VEC>(s, a[r], f);
+                    h[r].get(before);
+                    if (n_last >= 0) {  // the sequence's first token: what came before it is h0
+                        Row<float, VEC> z;
+                        z.zero();
+                        if (p.h0) z.load(p.h0 + (int64_t)n_last * p.D + c0);
+                        z.get(before);
+                    }
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) before[j] *= s[j];
+                    Row<TG, VEC>::store(static_cast<TG*>(p.dg) + t * p.lddg + c0, before);
+                } else {
+                    advance<BWD, VEC>(s, a[r], f);
+                    Row<TX, VEC>::store(static_cast<TX*>(p.out) + t * p.ldo + c0, s);
+                }
+                if (n_last >= 0 && p.last) Row<float, VEC>::store(p.last + (int64_t)n_last * p.D + c0, s);
+            }
+        }
+        tile = ntile;
+    }
+
+    // sequences without a token pass their state on
+    if (p.last) {
+        for (int64_t n0 = (int64_t)blockIdx.x * C::THREADS + warp * 32; n0 < p.N; n0 += (int64_t)gridDim.x * C::THREADS) {
+            const int64_t n = n0 + lane;
+            unsigned empty = __ballot_sync(0xffffffffu, n < p.N && p.cu[min(n + 1, (int64_t)p.N)] <= p.cu[min(n, (int64_t)p.N)]);
+            while (empty) {
+                const int64_t m = n0 + __ffs(empty) - 1;
+                empty &= empty - 1;
+                for (int c = lane; c < p.D; c += 32) p.last[m * p.D + c] = p.start ? p.start[m * p.D + c] : 0.f;
+            }
+        }
+    }
+}
+
+// Clears the workspace's head and flags; the tile kernel behind it may start meanwhile.
+__global__ void linrec_clear_kernel(unsigned int* w, int64_t n) {
+    tc::grid_dep_launch();
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) w[i] = 0;
+}
+
+// ---- workspace and launch ------------------------------------------------------------
+
+constexpr int kHeadWords = 64;
+
+struct ScanLayout {
+    int groups, rows;
+    size_t off_a, off_b, off_state, total;  // bytes; 0 in all for a single row of tiles
+};
+
+ScanLayout scan_layout(int64_t T, int D, int TT, int CC) {
+    ScanLayout l{};
+    l.groups = (D + CC - 1) / CC;
+    l.rows = (int)((T + TT - 1) / TT);
+    if (l.rows <= 1) return l;
+    const size_t recs = (size_t)l.groups * l.rows, block = recs * CC * sizeof(float);
+    l.off_a = ((kHeadWords + recs) * sizeof(unsigned) + 255) / 256 * 256;
+    l.off_b = l.off_a + block;
+    l.off_state = l.off_b + block;
+    l.total = (l.off_state + block + 255) / 256 * 256;
+    return l;
+}
+
+template <typename TX, typename TG, bool WIDE>
+size_t scan_bytes(int64_t T, int D) {
+    using F = Tile<TX, TG, false, WIDE>;
+    using B = Tile<TX, TG, true, WIDE>;
+    const size_t f = scan_layout(T, D, F::TT, F::CC).total, b = scan_layout(T, D, B::TT, B::CC).total;
+    return f > b ? f : b;
+}
+
+template <typename TX, typename TG>
+size_t scan_bytes(int64_t T, int D) {
+    // whether rows are aligned is known only at the call
+    const size_t n = scan_bytes<TX, TG, false>(T, D), w = D % 8 ? 0 : scan_bytes<TX, TG, true>(T, D);
+    return n > w ? n : w;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static std::atomic<EncodeTiled> known{nullptr};
+    EncodeTiled f = known.load(std::memory_order_acquire);
+    if (f) return f;
+    void* entry = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &entry, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess || found != cudaDriverEntryPointSuccess)
+        return nullptr;
+    f = reinterpret_cast<EncodeTiled>(entry);
+    known.store(f, std::memory_order_release);
+    return f;
+}
+
+// The [T, D] rows at `p`, in boxes of `tokens` by `channels`.
+template <typename T>
+bool encode_rows(CUtensorMap* map, const void* p, int64_t ld, int64_t tokens_all, int D, int tokens, int channels) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)tokens_all}, strides[1] = {(cuuint64_t)ld * sizeof(T)};
+    const cuuint32_t box[2] = {(cuuint32_t)channels, (cuuint32_t)tokens}, steps[2] = {1, 1};
+    return f(map, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+             const_cast<void*>(p), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows that the wide tiles can read (TMA: 16-byte aligned rows, a stride that
+// is one) and write (16-byte vectors).
+template <typename T>
+bool wide_rows(const void* p, int64_t ld, int D) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0 && ld >= D &&
+           (uint64_t)ld * sizeof(T) < (1ull << 40);
+}
+
+int sm_count() {
+    static std::atomic<int> known{0};
+    int n = known.load(std::memory_order_relaxed);
+    if (n) return n;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+        return 1;
+    known.store(n, std::memory_order_relaxed);
+    return n;
+}
+
+template <typename TX, typename TG, bool BWD, bool WIDE>
+cudaError_t launch_tiles(LinrecParams p, void* ws, cudaStream_t s) {
+    using C = Tile<TX, TG, BWD, WIDE>;
+    auto kernel = linrec_tile_kernel<TX, TG, BWD, WIDE>;
+    static std::atomic<int> resident{0};  // CTAs per SM
+    int per_sm = resident.load(std::memory_order_relaxed);
+    if (!per_sm) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES_SMEM);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, C::THREADS, C::BYTES_SMEM);
+        if (e != cudaSuccess) return e;
+        if (per_sm < 1) return cudaErrorInvalidConfiguration;
+        resident.store(per_sm, std::memory_order_relaxed);
+    }
+    const ScanLayout l = scan_layout(p.T, p.D, C::TT, C::CC);
+    p.groups = l.groups;
+    p.rows = l.rows;
+    CUtensorMap mx{}, mg{}, mh{};
+    if (WIDE && !(encode_rows<TX>(&mx, p.x, p.ldx, p.T, p.D, C::TT, C::CC) &&
+                  encode_rows<TG>(&mg, p.g, p.ldg, p.T, p.D, C::TT, C::CC) &&
+                  (!BWD || encode_rows<TX>(&mh, p.h, p.ldh, p.T, p.D, C::TT, C::CC))))
+        return cudaErrorInvalidValue;
+    p.err = device_error_word();
+    if (!p.err) return cudaErrorInitializationError;
+    const int64_t tiles = (int64_t)l.groups * l.rows, slots = (int64_t)per_sm * sm_count();
+    if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+    if (l.rows <= 1) {
+        KernelTimer kt(BWD ? "linrec_bwd" : "linrec_fwd", s);
+        kernel<<<(unsigned)tiles, C::THREADS, C::BYTES_SMEM, s>>>(mx, mg, mh, p);
+        return cudaGetLastError();
+    }
+    char* w = static_cast<char*>(ws);
+    p.head = reinterpret_cast<unsigned int*>(w);
+    p.flags = p.head + kHeadWords;
+    p.comp_a = reinterpret_cast<float*>(w + l.off_a);
+    p.comp_b = reinterpret_cast<float*>(w + l.off_b);
+    p.state = reinterpret_cast<float*>(w + l.off_state);
+    {
+        KernelTimer kt("linrec_clear", s);
+        const int64_t words = kHeadWords + tiles, blocks = (words + 1023) / 1024;
+        linrec_clear_kernel<<<(unsigned)(blocks < 152 ? blocks : 152), 256, 0, s>>>(p.head, words);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    KernelTimer kt(BWD ? "linrec_bwd" : "linrec_fwd", s);
+    return launch_dependent(kernel, dim3((unsigned)(tiles < slots ? tiles : slots)), dim3(C::THREADS), C::BYTES_SMEM, s,
+                            mx, mg, mh, p);
+}
+
+template <typename TX, typename TG>
+cudaError_t launch_scan_t(const LinrecParams& p, bool bwd, void* ws, cudaStream_t s) {
+    const bool wide = p.D % 8 == 0 && wide_rows<TX>(p.x, p.ldx, p.D) && wide_rows<TG>(p.g, p.ldg, p.D) &&
+                      wide_rows<TX>(p.out, p.ldo, p.D) &&
+                      (!bwd || (wide_rows<TX>(p.h, p.ldh, p.D) && wide_rows<TG>(p.dg, p.lddg, p.D)));
+    if (bwd)
+        return wide ? launch_tiles<TX, TG, true, true>(p, ws, s) : launch_tiles<TX, TG, true, false>(p, ws, s);
+    return wide ? launch_tiles<TX, TG, false, true>(p, ws, s) : launch_tiles<TX, TG, false, false>(p, ws, s);
+}
+
+cudaError_t launch_scan(const LinrecParams& p, int dtype, int gate_dtype, bool bwd, void* ws, cudaStream_t s) {
     if (dtype == GDR_BF16)
-        return gate_dtype == GDR_BF16 ? launch_serial<__nv_bfloat16, __nv_bfloat16>(p, bwd, s)
-                                      : launch_serial<__nv_bfloat16, float>(p, bwd, s);
-    return gate_dtype == GDR_BF16 ? launch_serial<float, __nv_bfloat16>(p, bwd, s)
-                                  : launch_serial<float, float>(p, bwd, s);
+        return gate_dtype == GDR_BF16 ? launch_scan_t<__nv_bfloat16, __nv_bfloat16>(p, bwd, ws, s)
+                                      : launch_scan_t<__nv_bfloat16, float>(p, bwd, ws, s);
+    return gate_dtype == GDR_BF16 ? launch_scan_t<float, __nv_bfloat16>(p, bwd, ws, s)
+                                  : launch_scan_t<float, float>(p, bwd, ws, s);
 }
 
 // ---- the slot-pool step ------------------------------------------------------
@@ -105,7 +779,7 @@ __global__ void linrec_step_kernel(StepParams p) {
         TP* keep = p.states ? static_cast<TP*>(p.states) + n * p.steps * p.D + c : nullptr;
         float h = to_f(*cell);
         for (int64_t t = lo; t < hi; ++t) {
-            h = fmaf(expf(to_f(g[t * p.ldg + c])), h, to_f(x[t * p.ldx + c]));
+            h = fmaf(decay(to_f(g[t * p.ldg + c])), h, to_f(x[t * p.ldx + c]));
             y[t * p.ldy + c] = from_f<TX>(h);
             if (keep && t - lo < p.steps) keep[(t - lo) * p.D] = from_f<TP>(h);
         }
@@ -199,7 +873,8 @@ int check_sizes(int N, int64_t T, int D, int dtype, int gate_dtype) {
     if (dtype != GDR_BF16 && dtype != GDR_F32) return set_last_error(GDR_ERR_UNSUPPORTED, "dtype %d", dtype);
     if (gate_dtype != GDR_BF16 && gate_dtype != GDR_F32)
         return set_last_error(GDR_ERR_UNSUPPORTED, "gate_dtype %d", gate_dtype);
-    if (T > 0x7fffffffLL) return set_last_error(GDR_ERR_UNSUPPORTED, "T_total (%lld) above 2^31 - 1", (long long)T);
+    // token numbers are 32-bit in the kernels, a tile's beyond the last token included
+    if (T > 0x7fffff00LL) return set_last_error(GDR_ERR_UNSUPPORTED, "T_total (%lld) above 2^31 - 256", (long long)T);
     if (N > 0x7fffffff / 2) return set_last_error(GDR_ERR_UNSUPPORTED, "N too large");
     if (T > 0 && N == 0) return set_last_error(GDR_ERR_INVALID_ARG, "T_total > 0 with N == 0");
     return GDR_OK;
@@ -256,7 +931,12 @@ extern "C" {
 int gdr_linrec_workspace_size(int N, int64_t T_total, int D, int dtype, int gate_dtype, size_t* bytes) {
     if (!bytes) return set_last_error(GDR_ERR_INVALID_ARG, "bytes is NULL");
     if (int rc = check_sizes(N, T_total, D, dtype, gate_dtype)) return rc;
-    *bytes = 0;
+    if (dtype == GDR_BF16)
+        *bytes = gate_dtype == GDR_BF16 ? scan_bytes<__nv_bfloat16, __nv_bfloat16>(T_total, D)
+                                        : scan_bytes<__nv_bfloat16, float>(T_total, D);
+    else
+        *bytes = gate_dtype == GDR_BF16 ? scan_bytes<float, __nv_bfloat16>(T_total, D)
+                                        : scan_bytes<float, float>(T_total, D);
     return set_ok();
 }
 
@@ -282,7 +962,7 @@ int gdr_linrec_fwd(const void* x, int64_t x_stride, const void* g, int64_t g_str
     LinrecParams p{};
     p.x = x; p.g = g; p.out = y; p.start = initial_state; p.last = final_state; p.cu = cu_seqlens;
     p.ldx = x_stride; p.ldg = g_stride; p.ldo = y_stride; p.T = T_total; p.N = N; p.D = D;
-    return launched(launch_scan(p, dtype, gate_dtype, false, s), "gdr_linrec_fwd launch");
+    return launched(launch_scan(p, dtype, gate_dtype, false, workspace, s), "gdr_linrec_fwd launch");
 }
 
 int gdr_linrec_bwd(const void* dy, int64_t dy_stride, const void* g, int64_t g_stride, const void* y,
@@ -312,7 +992,7 @@ int gdr_linrec_bwd(const void* dy, int64_t dy_stride, const void* g, int64_t g_s
     p.x = dy; p.g = g; p.h = y; p.out = dx; p.dg = dg; p.h0 = initial_state; p.start = d_final_state;
     p.last = d_initial_state; p.cu = cu_seqlens; p.ldx = dy_stride; p.ldg = g_stride; p.ldh = y_stride;
     p.ldo = dx_stride; p.lddg = dg_stride; p.T = T_total; p.N = N; p.D = D;
-    return launched(launch_scan(p, dtype, gate_dtype, true, s), "gdr_linrec_bwd launch");
+    return launched(launch_scan(p, dtype, gate_dtype, true, workspace, s), "gdr_linrec_bwd launch");
 }
 
 int gdr_linrec_step(const void* x, int64_t x_stride, const void* g, int64_t g_stride, void* state_pool,
