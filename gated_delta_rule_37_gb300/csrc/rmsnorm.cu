@@ -4,14 +4,17 @@
 #include <cuda_fp8.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "gdr.h"
 #include "launch.h"
+#include "tc.cuh"
 
 namespace gdr {
 namespace {
 
-constexpr float kE4m3Max = 448.f;    // largest finite e4m3 value
+constexpr float kE4m3Max = 448.f;     // largest finite e4m3 value
 constexpr float kAmaxFloor = 1e-12f;  // a group of zeros gets a scale too
 
 struct NormParams {
@@ -23,73 +26,407 @@ struct NormParams {
     float* scales;
     int64_t ldx, ldr, lds, ldy, M;
     int D, group, groups;
+    int tpr;  // threads of a row, a power of two
     float eps;
 };
 
-__device__ __forceinline__ float block_sum(float v, float* shared) {
-    v = warp_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = threadIdx.x < (blockDim.x >> 5) ? shared[threadIdx.x] : 0.f;
-    if (threadIdx.x < 32) {
-        v = warp_sum(v);
-        if (threadIdx.x == 0) shared[32] = v;
+// ---- 8 consecutive elements, kept as they are stored, worked on in pairs ----------
+
+template <typename T> struct Cells;
+
+template <> struct Cells<__nv_bfloat16> {
+    uint32_t w[4];
+    __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
     }
-    __syncthreads();
-    return shared[32];
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ float2 get(int i) const {
+        return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+    __device__ __forceinline__ void set(int i, float2 f) { w[i] = tc::pack_bf16(f.x, f.y); }
+    // the rounded sum: a bf16 sum is the same rounded once or through fp32 (where fp32 has to
+    // round, the smaller term is below 2^-16 of the larger, and no midpoint is that near a bf16 value)
+    __device__ __forceinline__ void add(const Cells& o) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 r = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&o.w[i]));
+            w[i] = *reinterpret_cast<const uint32_t*>(&r);
+        }
+    }
+};
+template <> struct Cells<float> {
+    float2 w[4];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = make_float2(0.f, 0.f);
+    }
+    __device__ __forceinline__ void load(const float* p) {
+        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+        w[0] = make_float2(a.x, a.y); w[1] = make_float2(a.z, a.w);
+        w[2] = make_float2(b.x, b.y); w[3] = make_float2(b.z, b.w);
+    }
+    __device__ __forceinline__ void store(float* p) const {
+        reinterpret_cast<float4*>(p)[0] = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
+        reinterpret_cast<float4*>(p)[1] = make_float4(w[2].x, w[2].y, w[3].x, w[3].y);
+    }
+    __device__ __forceinline__ float2 get(int i) const { return w[i]; }
+    __device__ __forceinline__ void set(int i, float2 f) { w[i] = f; }
+    __device__ __forceinline__ void add(const Cells& o) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __fadd2_rn(w[i], o.w[i]);
+    }
+};
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ void store_codes(__nv_fp8_storage_t* p, const float2 (&f)[4]) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(f[2 * i], __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(f[2 * i + 1], __NV_SATFINITE, __NV_E4M3);
+        w[i] = lo | hi << 16;
+    }
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
 
-template <typename T, bool FP8>
-__global__ void rmsnorm_row_kernel(NormParams p) {
-    __shared__ float shared[33];
-    __shared__ int amax[GDR_RMSNORM_MAX_D / 32];
-    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
-        const T* x = static_cast<const T*>(p.x) + m * p.ldx;
-        const T* r = p.residual ? static_cast<const T*>(p.residual) + m * p.ldr : nullptr;
-        T* sum = p.residual ? static_cast<T*>(p.sum) + m * p.lds : nullptr;
-        const T* s = sum ? sum : x;
-        float ss = 0.f;
-        for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
-            float v = to_f(x[c]);
-            if (r) {
-                const T q = from_f<T>(v + to_f(r[c]));
-                sum[c] = q;
-                v = to_f(q);
-            }
-            ss += v * v;
+// A group's scale, and what its values are multiplied by: 1.5 ulp of amax / 448
+// and of its reciprocal, far below a code's half step.
+__device__ __forceinline__ float group_scale(float amax) {
+    return __fmul_rn(fmaxf(amax, kAmaxFloor), 1.f / kE4m3Max);
+}
+__device__ __forceinline__ float group_inverse(float scale) { return __fdividef(1.f, scale); }
+
+// Reductions over the tpr threads of a row: shuffles, and above a warp one
+// exchange of the warps' results behind a barrier of the row's threads.  `turn`
+// alternates from call to call (two buffers: one barrier each suffices).
+constexpr int kMaxThreads = 512;
+
+struct RowReduce {
+    float2 (*buf)[kMaxThreads / 32];
+    int tpr, slot, turn;
+
+    template <typename F>
+    __device__ __forceinline__ float2 all(float2 v, F op) {
+        for (int off = min(tpr, 32) >> 1; off >= 1; off >>= 1) {
+            const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, v.x, off), __shfl_xor_sync(0xffffffffu, v.y, off));
+            v = op(v, o);
         }
-        if (FP8)
-            for (int i = threadIdx.x; i < p.groups; i += blockDim.x) amax[i] = 0;
-        const float rstd = 1.f / sqrtf(block_sum(ss, shared) / p.D + p.eps);
-        if (!FP8) {
-            T* y = static_cast<T*>(p.y) + m * p.ldy;
-            for (int c = threadIdx.x; c < p.D; c += blockDim.x) y[c] = from_f<T>(to_f(s[c]) * rstd * p.w[c]);
-        } else {
-            for (int c = threadIdx.x; c < p.D; c += blockDim.x)
-                atomicMax(&amax[c / p.group], __float_as_int(fmaxf(fabsf(to_f(s[c]) * rstd * p.w[c]), kAmaxFloor)));
-            __syncthreads();
-            __nv_fp8_storage_t* y = static_cast<__nv_fp8_storage_t*>(p.y) + m * p.ldy;
-            for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
-                const float scale = __int_as_float(amax[c / p.group]) / kE4m3Max;
-                y[c] = __nv_cvt_float_to_fp8(to_f(s[c]) * rstd * p.w[c] / scale, __NV_SATFINITE, __NV_E4M3);
+        if (tpr > 32) {
+            const int warps = tpr >> 5, at = slot * warps;
+            if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x >> 5] = v;
+            tc::bar_sync(1 + slot, tpr);
+            v = buf[turn][at];
+            for (int i = 1; i < warps; ++i) v = op(v, buf[turn][at + i]);
+            turn ^= 1;
+        }
+        return v;
+    }
+    __device__ __forceinline__ float2 sum(float2 v) {
+        return all(v, [](float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); });
+    }
+    __device__ __forceinline__ float max(float v) {
+        return all(make_float2(v, 0.f), [](float2 a, float2 b) { return make_float2(fmaxf(a.x, b.x), 0.f); }).x;
+    }
+};
+
+// Forward on aligned rows.  A row belongs to tpr threads, CH pieces of 8 elements
+// each, and is held as stored from its one read to its output.  MODE: kSame for
+// the input's type, kRow for codes with one scale per row, else the group's
+// length: its 8-element pieces lie in neighbouring threads.
+constexpr int kSame = -1, kRow = 0;
+
+template <typename T, int CH, int MODE>
+__global__ void __launch_bounds__(kMaxThreads, 1) rmsnorm_fwd_kernel(NormParams p) {
+    __shared__ float2 exchange[2][kMaxThreads / 32];
+    const int tpr = p.tpr, slots = blockDim.x / tpr, slot = threadIdx.x / tpr, l = threadIdx.x % tpr;
+    RowReduce reduce{exchange, tpr, slot, 0};
+    const float mean = 1.f / p.D;
+    for (int64_t m0 = (int64_t)blockIdx.x * slots; m0 < p.M; m0 += (int64_t)gridDim.x * slots) {
+        const int64_t m = m0 + slot;
+        const int width = m < p.M ? p.D : 0;  // a missing row has no elements
+        const T* x = static_cast<const T*>(p.x) + m * p.ldx;
+        Cells<T> s[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = (c * tpr + l) * 8;
+            s[c].zero();
+            if (e < width) s[c].load(x + e);
+        }
+        if (p.residual) {
+            const T* res = static_cast<const T*>(p.residual) + m * p.ldr;
+            T* sum = static_cast<T*>(p.sum) + m * p.lds;
+            Cells<T> r[CH];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int e = (c * tpr + l) * 8;
+                r[c].zero();
+                if (e < width) r[c].load(res + e);
             }
-            for (int i = threadIdx.x; i < p.groups; i += blockDim.x)
-                p.scales[m * p.groups + i] = __int_as_float(amax[i]) / kE4m3Max;
-            __syncthreads();
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int e = (c * tpr + l) * 8;
+                s[c].add(r[c]);  // the stored sum is what the norm is taken of
+                if (e < width) s[c].store(sum + e);
+            }
+        }
+        float2 ss = both(0.f);
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = s[c].get(i);
+                ss = __ffma2_rn(f, f, ss);
+            }
+        const float rstd = 1.f / sqrtf(fmaf(reduce.sum(make_float2(ss.x + ss.y, 0.f)).x, mean, p.eps));
+
+        auto norm = [&](int c, float2 (&f)[4]) {
+            const int e = (c * tpr + l) * 8;
+            Cells<float> w;
+            w.zero();
+            if (e < p.D) w.load(p.w + e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(__fmul2_rn(s[c].get(i), both(rstd)), w.get(i));
+        };
+        auto largest = [](const float2 (&f)[4]) {
+            float a = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a = fmaxf(a, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
+            return a;
+        };
+        if (MODE == kSame) {
+            T* y = static_cast<T*>(p.y) + m * p.ldy;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int e = (c * tpr + l) * 8;
+                float2 f[4];
+                norm(c, f);
+                Cells<T> out;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) out.set(i, f[i]);
+                if (e < width) out.store(y + e);
+            }
+            continue;
+        }
+        __nv_fp8_storage_t* y = static_cast<__nv_fp8_storage_t*>(p.y) + m * p.ldy;
+        float* scales = p.scales + m * p.groups;
+        if (MODE == kRow) {
+            float most = 0.f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                float2 f[4];
+                norm(c, f);
+                most = fmaxf(most, largest(f));
+            }
+            const float scale = group_scale(reduce.max(most)), inv = group_inverse(scale);
+            if (l == 0 && width) *scales = scale;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int e = (c * tpr + l) * 8;
+                float2 f[4];
+                norm(c, f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(f[i], both(inv));
+                if (e < width) store_codes(y + e, f);
+            }
+        } else {
+            constexpr int SPAN = MODE > 0 ? MODE / 8 : 1;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int e = (c * tpr + l) * 8;
+                float2 f[4];
+                norm(c, f);
+                float most = largest(f);
+#pragma unroll
+                for (int off = SPAN / 2; off >= 1; off >>= 1)
+                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+                const float scale = group_scale(most), inv = group_inverse(scale);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(f[i], both(inv));
+                if (e < width) {
+                    store_codes(y + e, f);
+                    if (l % SPAN == 0) scales[e / (SPAN * 8)] = scale;
+                }
+            }
         }
     }
+}
+
+// Forward on any rows: one element at a time, CH per thread, neighbours in
+// neighbouring threads.
+template <typename T, int CH, bool FP8>
+__global__ void __launch_bounds__(kMaxThreads, 1) rmsnorm_fwd_any_kernel(NormParams p) {
+    __shared__ float2 exchange[2][kMaxThreads / 32];
+    __shared__ int amax_s[FP8 ? 1024 : 1];
+    const int tpr = p.tpr, slots = blockDim.x / tpr, slot = threadIdx.x / tpr, l = threadIdx.x % tpr;
+    RowReduce reduce{exchange, tpr, slot, 0};
+    const float mean = 1.f / p.D;
+    for (int64_t m0 = (int64_t)blockIdx.x * slots; m0 < p.M; m0 += (int64_t)gridDim.x * slots) {
+        const int64_t m = m0 + slot;
+        const int width = m < p.M ? p.D : 0;
+        const T* x = static_cast<const T*>(p.x) + m * p.ldx;
+        float s[CH], ss = 0.f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) s[c] = c * tpr + l < width ? to_f(x[c * tpr + l]) : 0.f;
+        if (p.residual) {
+            const T* res = static_cast<const T*>(p.residual) + m * p.ldr;
+            T* sum = static_cast<T*>(p.sum) + m * p.lds;
+            float r[CH];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) r[c] = c * tpr + l < width ? to_f(res[c * tpr + l]) : 0.f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const T q = from_f<T>(s[c] + r[c]);
+                s[c] = to_f(q);
+                if (c * tpr + l < width) sum[c * tpr + l] = q;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c) ss = fmaf(s[c], s[c], ss);
+        const float rstd = 1.f / sqrtf(fmaf(reduce.sum(make_float2(ss, 0.f)).x, mean, p.eps));
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            s[c] = c * tpr + l < p.D ? __fmul_rn(__fmul_rn(s[c], rstd), p.w[c * tpr + l]) : 0.f;
+        if (!FP8) {
+            T* y = static_cast<T*>(p.y) + m * p.ldy;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                if (c * tpr + l < width) y[c * tpr + l] = from_f<T>(s[c]);
+            continue;
+        }
+        __nv_fp8_storage_t* y = static_cast<__nv_fp8_storage_t*>(p.y) + m * p.ldy;
+        float* scales = p.scales + m * p.groups;
+        if (p.groups == 1) {
+            float most = 0.f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) most = fmaxf(most, fabsf(s[c]));
+            const float scale = group_scale(reduce.max(most)), inv = group_inverse(scale);
+            if (l == 0 && width) *scales = scale;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                if (c * tpr + l < width) y[c * tpr + l] = __nv_cvt_float_to_fp8(s[c] * inv, __NV_SATFINITE, __NV_E4M3);
+            continue;
+        }
+        // a group crosses warps: its largest magnitude in shared memory (the order of a maximum does not
+        // matter), a warp's 32 neighbours, which lie in one group, reduced before
+        int* amax = amax_s + slot * p.groups;
+        const int shift = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
+        auto meet = [&]() {
+            if (tpr <= 32)
+                __syncwarp();
+            else
+                tc::bar_sync(1 + slot, tpr);
+        };
+        for (int i = l; i < p.groups; i += tpr) amax[i] = 0;
+        meet();
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const unsigned most = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(s[c]), 0.f)));
+            if ((l & 31) == 0 && c * tpr + l < p.D) atomicMax(amax + ((c * tpr + l) >> shift), (int)most);
+        }
+        meet();
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = c * tpr + l;
+            if (e < width) {
+                const float scale = group_scale(__int_as_float(amax[e >> shift]));
+                y[e] = __nv_cvt_float_to_fp8(s[c] * group_inverse(scale), __NV_SATFINITE, __NV_E4M3);
+                if ((e & (p.group - 1)) == 0) scales[e >> shift] = scale;
+            }
+        }
+        meet();
+    }
+}
+
+int sm_count() {
+    static std::atomic<int> known{0};
+    int n = known.load(std::memory_order_relaxed);
+    if (n) return n;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+        return 1;
+    known.store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// Threads of a row that holds `pieces` pieces, ch of them per thread.
+int row_threads(int pieces, int ch, int least) {
+    int t = least;
+    while (t * ch < pieces && t < kMaxThreads) t *= 2;
+    return t;
+}
+
+struct Shape {
+    unsigned grid, block;
+};
+
+// CTAs of at least 256 threads, at most 32 per SM, which then walk the rows.
+Shape shape_of(const NormParams& p) {
+    const int block = p.tpr > 256 ? p.tpr : 256, slots = block / p.tpr;
+    const int64_t want = (p.M + slots - 1) / slots, most = (int64_t)sm_count() * 32;
+    return {(unsigned)(want < most ? want : most), (unsigned)block};
+}
+
+template <typename T, int CH>
+cudaError_t launch_fwd_ch(const NormParams& p, bool fp8, cudaStream_t s) {
+    const Shape h = shape_of(p);
+    KernelTimer kt("rmsnorm_fwd", s);
+    switch (!fp8 ? kSame : p.groups == 1 ? kRow : p.group) {
+        case kSame: rmsnorm_fwd_kernel<T, CH, kSame><<<h.grid, h.block, 0, s>>>(p); break;
+        case kRow: rmsnorm_fwd_kernel<T, CH, kRow><<<h.grid, h.block, 0, s>>>(p); break;
+        case 32: rmsnorm_fwd_kernel<T, CH, 32><<<h.grid, h.block, 0, s>>>(p); break;
+        case 64: rmsnorm_fwd_kernel<T, CH, 64><<<h.grid, h.block, 0, s>>>(p); break;
+        default: rmsnorm_fwd_kernel<T, CH, 128><<<h.grid, h.block, 0, s>>>(p); break;
+    }
+    return cudaGetLastError();
+}
+
+template <typename T, int CH>
+cudaError_t launch_fwd_any(const NormParams& p, bool fp8, cudaStream_t s) {
+    const Shape h = shape_of(p);
+    KernelTimer kt("rmsnorm_fwd", s);
+    if (fp8)
+        rmsnorm_fwd_any_kernel<T, CH, true><<<h.grid, h.block, 0, s>>>(p);
+    else
+        rmsnorm_fwd_any_kernel<T, CH, false><<<h.grid, h.block, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_fwd(const NormParams& p, bool fp8, cudaStream_t s) {
-    const unsigned grid = (unsigned)(p.M < 65535 ? p.M : 65535);
-    KernelTimer kt("rmsnorm_fwd", s);
-    if (fp8)
-        rmsnorm_row_kernel<T, true><<<grid, 256, 0, s>>>(p);
-    else
-        rmsnorm_row_kernel<T, false><<<grid, 256, 0, s>>>(p);
-    return cudaGetLastError();
+cudaError_t launch_fwd(NormParams p, bool fp8, bool wide, cudaStream_t s) {
+    // As many pieces per thread as registers hold, and fewer where there are too
+    // few rows to fill the GPU.
+    const int64_t full = (int64_t)sm_count() * 1024;
+    if (!wide) {
+        int ch = p.D > 32 * kMaxThreads ? 64 : p.D > 8 * kMaxThreads ? 32 : 8;
+        if (p.D <= 2 * kMaxThreads && (p.D <= 64 || p.M * row_threads(p.D, 8, 32) < full)) ch = 2;
+        p.tpr = row_threads(p.D, ch, 32);
+        switch (ch) {
+            case 2: return launch_fwd_any<T, 2>(p, fp8, s);
+            case 8: return launch_fwd_any<T, 8>(p, fp8, s);
+            case 32: return launch_fwd_any<T, 32>(p, fp8, s);
+            default: return launch_fwd_any<T, 64>(p, fp8, s);
+        }
+    }
+    const int pieces = p.D / 8;
+    int ch = 8;
+    while (ch > 1 && row_threads(pieces, ch / 2, 16) * (ch / 2) >= pieces &&
+           (row_threads(pieces, ch, 16) == row_threads(pieces, ch / 2, 16) ||
+            p.M * row_threads(pieces, ch, 16) < full))
+        ch /= 2;
+    p.tpr = row_threads(pieces, ch, 16);
+    switch (ch) {
+        case 1: return launch_fwd_ch<T, 1>(p, fp8, s);
+        case 2: return launch_fwd_ch<T, 2>(p, fp8, s);
+        case 4: return launch_fwd_ch<T, 4>(p, fp8, s);
+        default: return launch_fwd_ch<T, 8>(p, fp8, s);
+    }
 }
 
 // ---- backward ----------------------------------------------------------------
@@ -103,61 +440,236 @@ struct NormBwdParams {
     float* dw;
     float* partial;  // [parts, D]: dw summed over each CTA's rows
     int64_t lddy, lds, ldds, lddx, M;
-    int D, parts;
+    int D, parts, tpr;
     float eps;
 };
 
-constexpr int kMaxParts = 304;
+constexpr int kMaxParts = 608;  // CTAs of the backward: four per SM
 
 int norm_parts(int64_t M) { return (int)(M < kMaxParts ? M : kMaxParts); }
 
-template <typename T>
-__global__ void rmsnorm_bwd_kernel(NormBwdParams p) {
-    __shared__ float shared[33];
-    if (p.dw)
-        for (int c = threadIdx.x; c < p.D; c += blockDim.x) p.partial[(int64_t)blockIdx.x * p.D + c] = 0.f;
-    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
-        const T* dy = static_cast<const T*>(p.dy) + m * p.lddy;
-        const T* s = static_cast<const T*>(p.s) + m * p.lds;
-        const T* ds = p.ds ? static_cast<const T*>(p.ds) + m * p.ldds : nullptr;
-        T* dx = static_cast<T*>(p.dx) + m * p.lddx;
-        float ss = 0.f, sz = 0.f;
-        for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
-            const float v = to_f(s[c]);
-            ss += v * v;
-            sz += v * to_f(dy[c]) * p.w[c];
+// Rows are walked by the CTAs of one grid, so that a thread meets the same
+// columns in every row and sums dw in registers; one [D] part per CTA goes to
+// memory.
+template <typename T, int CH>
+__global__ void __launch_bounds__(kMaxThreads, 1) rmsnorm_bwd_kernel(NormBwdParams p) {
+    __shared__ float2 exchange[2][kMaxThreads / 32];
+    extern __shared__ float dw_s[];
+    const int tpr = p.tpr, slots = blockDim.x / tpr, slot = threadIdx.x / tpr, l = threadIdx.x % tpr;
+    RowReduce reduce{exchange, tpr, slot, 0};
+    const float mean = 1.f / p.D;
+    float2 dw[CH][4];
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dw[c][i] = both(0.f);
+    for (int64_t m0 = (int64_t)blockIdx.x * slots; m0 < p.M; m0 += (int64_t)gridDim.x * slots) {
+        const int64_t m = m0 + slot;
+        const int width = m < p.M ? p.D : 0;  // a missing row has no elements
+        const T* dy_row = static_cast<const T*>(p.dy) + m * p.lddy;
+        const T* s_row = static_cast<const T*>(p.s) + m * p.lds;
+        const T* ds_row = p.ds ? static_cast<const T*>(p.ds) + m * p.ldds : nullptr;
+        T* dx_row = static_cast<T*>(p.dx) + m * p.lddx;
+        Cells<T> dy[CH], s[CH], ds[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = (c * tpr + l) * 8;
+            dy[c].zero();
+            s[c].zero();
+            ds[c].zero();
+            if (e < width) {
+                dy[c].load(dy_row + e);
+                s[c].load(s_row + e);
+                if (ds_row) ds[c].load(ds_row + e);
+            }
         }
-        const float rstd = 1.f / sqrtf(block_sum(ss, shared) / p.D + p.eps);
-        const float proj = block_sum(sz, shared) * rstd * rstd / p.D;
-        for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
-            const float v = to_f(s[c]), d = to_f(dy[c]);
-            // one rounding each, written out: the same bits with and without dw
-            const float out = fmaf(rstd, fmaf(d, p.w[c], -__fmul_rn(v, proj)), ds ? to_f(ds[c]) : 0.f);
-            if (p.dw) p.partial[(int64_t)blockIdx.x * p.D + c] += rstd * d * v;
-            dx[c] = from_f<T>(out);
+        float2 square = both(0.f), dot = both(0.f);  // sums of s^2 and of s z
+        auto weight = [&](int c) {
+            const int e = (c * tpr + l) * 8;
+            Cells<float> w;
+            w.zero();
+            if (e < p.D) w.load(p.w + e);
+            return w;
+        };
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const Cells<float> w = weight(c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = s[c].get(i);
+                square = __ffma2_rn(v, v, square);
+                dot = __ffma2_rn(v, __fmul2_rn(dy[c].get(i), w.get(i)), dot);
+            }
         }
+        const float2 sums = reduce.sum(make_float2(square.x + square.y, dot.x + dot.y));
+        float rstd = 1.f / sqrtf(fmaf(sums.x, mean, p.eps));
+        if (!width) rstd = 0.f;  // with eps = 0 a missing row's would be infinite, and reach dw as NaN
+        const float proj = sums.y * mean * rstd * rstd;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = (c * tpr + l) * 8;
+            const Cells<float> w = weight(c);
+            Cells<T> out;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 d = dy[c].get(i), v = s[c].get(i);
+                const float2 t = __ffma2_rn(d, w.get(i), __fmul2_rn(v, both(-proj)));
+                out.set(i, __ffma2_rn(both(rstd), t, ds[c].get(i)));
+                dw[c][i] = __ffma2_rn(d, __fmul2_rn(v, both(rstd)), dw[c][i]);
+            }
+            if (e < width) out.store(dx_row + e);
+        }
+    }
+    if (!p.dw) return;
+    // the CTA's rows at once: slot after slot
+    float2* dw2 = reinterpret_cast<float2*>(dw_s);
+    for (int k = 0; k < slots; ++k) {
+        if (slot == k)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int e = (c * tpr + l) * 8;
+                if (k > 0)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dw[c][i] = __fadd2_rn(dw2[e / 2 + i], dw[c][i]);
+                if (k + 1 < slots) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dw2[e / 2 + i] = dw[c][i];
+                } else if (e < p.D) {
+                    Cells<float> out;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) out.set(i, dw[c][i]);
+                    out.store(p.partial + (int64_t)blockIdx.x * p.D + e);
+                }
+            }
+        __syncthreads();
     }
 }
 
-__global__ void rmsnorm_dw_kernel(const float* partial, int parts, int D, float* dw) {
-    const int c = blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= D) return;
-    float v = 0.f;
-    for (int i = 0; i < parts; ++i) v += partial[(int64_t)i * D + c];
-    dw[c] = v;
+// The same on any rows: one element at a time.
+template <typename T, int CH>
+__global__ void __launch_bounds__(kMaxThreads, 1) rmsnorm_bwd_any_kernel(NormBwdParams p) {
+    __shared__ float2 exchange[2][kMaxThreads / 32];
+    extern __shared__ float dw_s[];
+    const int tpr = p.tpr, slots = blockDim.x / tpr, slot = threadIdx.x / tpr, l = threadIdx.x % tpr;
+    RowReduce reduce{exchange, tpr, slot, 0};
+    const float mean = 1.f / p.D;
+    float dw[CH], w[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        dw[c] = 0.f;
+        w[c] = c * tpr + l < p.D ? p.w[c * tpr + l] : 0.f;
+    }
+    for (int64_t m0 = (int64_t)blockIdx.x * slots; m0 < p.M; m0 += (int64_t)gridDim.x * slots) {
+        const int64_t m = m0 + slot;
+        const int width = m < p.M ? p.D : 0;
+        const T* dy_row = static_cast<const T*>(p.dy) + m * p.lddy;
+        const T* s_row = static_cast<const T*>(p.s) + m * p.lds;
+        const T* ds_row = p.ds ? static_cast<const T*>(p.ds) + m * p.ldds : nullptr;
+        T* dx_row = static_cast<T*>(p.dx) + m * p.lddx;
+        T dy[CH], s[CH], ds[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = c * tpr + l;
+            dy[c] = e < width ? dy_row[e] : from_f<T>(0.f);
+            s[c] = e < width ? s_row[e] : from_f<T>(0.f);
+            ds[c] = e < width && ds_row ? ds_row[e] : from_f<T>(0.f);
+        }
+        float2 sums = both(0.f);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const float v = to_f(s[c]);
+            sums.x = fmaf(v, v, sums.x);
+            sums.y = fmaf(v, __fmul_rn(to_f(dy[c]), w[c]), sums.y);
+        }
+        sums = reduce.sum(sums);
+        float rstd = 1.f / sqrtf(fmaf(sums.x, mean, p.eps));
+        if (!width) rstd = 0.f;
+        const float proj = sums.y * mean * rstd * rstd;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = c * tpr + l;
+            const float d = to_f(dy[c]), v = to_f(s[c]);
+            const float o = fmaf(rstd, fmaf(d, w[c], __fmul_rn(v, -proj)), to_f(ds[c]));
+            dw[c] = fmaf(d, __fmul_rn(v, rstd), dw[c]);
+            if (e < width) dx_row[e] = from_f<T>(o);
+        }
+    }
+    if (!p.dw) return;
+    for (int k = 0; k < slots; ++k) {
+        if (slot == k)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int e = c * tpr + l;
+                if (k > 0) dw[c] = dw_s[e] + dw[c];
+                if (k + 1 < slots)
+                    dw_s[e] = dw[c];
+                else if (e < p.D)
+                    p.partial[(int64_t)blockIdx.x * p.D + e] = dw[c];
+            }
+        __syncthreads();
+    }
 }
 
-template <typename T>
-cudaError_t launch_bwd(const NormBwdParams& p, cudaStream_t s) {
+// The sum of the parts: 32 columns per CTA, 16 slices of the parts, in a fixed order.
+__global__ void rmsnorm_dw_kernel(const float* __restrict__ partial, int parts, int D, float* dw) {
+    __shared__ float slice[16][33];
+    tc::grid_dep_wait();
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), q = threadIdx.x >> 5;
+    float v = 0.f;
+    if (c < D) {
+#pragma unroll 8
+        for (int i = q; i < parts; i += 16) v += partial[(int64_t)i * D + c];
+    }
+    slice[q][threadIdx.x & 31] = v;
+    __syncthreads();
+    if (q == 0 && c < D) {
+        for (int i = 1; i < 16; ++i) v += slice[i][threadIdx.x];
+        dw[c] = v;
+    }
+}
+
+template <typename T, int CH, bool WIDE>
+cudaError_t launch_bwd_ch(NormBwdParams p, cudaStream_t s) {
+    const int block = p.tpr > 256 ? p.tpr : 256, slots = block / p.tpr;
+    const int64_t want = (p.M + slots - 1) / slots;
+    p.parts = norm_parts(want);
+    const size_t smem = slots > 1 ? (size_t)p.tpr * CH * (WIDE ? 8 : 1) * sizeof(float) : 0;
     {
         KernelTimer kt("rmsnorm_bwd", s);
-        rmsnorm_bwd_kernel<T><<<p.parts, 256, 0, s>>>(p);
+        if constexpr (WIDE)
+            rmsnorm_bwd_kernel<T, CH><<<p.parts, block, smem, s>>>(p);
+        else
+            rmsnorm_bwd_any_kernel<T, CH><<<p.parts, block, smem, s>>>(p);
     }
-    if (p.dw) {
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && p.dw) {
         KernelTimer kt("rmsnorm_dw", s);
-        rmsnorm_dw_kernel<<<(p.D + 127) / 128, 128, 0, s>>>(p.partial, p.parts, p.D, p.dw);
+        e = launch_dependent(rmsnorm_dw_kernel, dim3((p.D + 31) / 32), dim3(512), 0, s, p.partial, p.parts, p.D, p.dw);
     }
-    return cudaGetLastError();
+    return e;
+}
+
+template <typename T>
+cudaError_t launch_bwd(NormBwdParams p, bool wide, cudaStream_t s) {
+    if (!wide) {
+        const int ch = p.D <= 4 * kMaxThreads ? 4 : p.D <= 16 * kMaxThreads ? 16 : 64;
+        p.tpr = row_threads(p.D, ch, 32);
+        return ch == 4 ? launch_bwd_ch<T, 4, false>(p, s) : ch == 16 ? launch_bwd_ch<T, 16, false>(p, s)
+                                                                     : launch_bwd_ch<T, 64, false>(p, s);
+    }
+    const int pieces = p.D / 8, ch = pieces <= 16 ? 1 : pieces <= 2 * kMaxThreads ? 2 : pieces <= 4 * kMaxThreads ? 4 : 8;
+    p.tpr = row_threads(pieces, ch, 16);
+    switch (ch) {
+        case 1: return launch_bwd_ch<T, 1, true>(p, s);
+        case 2: return launch_bwd_ch<T, 2, true>(p, s);
+        case 4: return launch_bwd_ch<T, 4, true>(p, s);
+        default: return launch_bwd_ch<T, 8, true>(p, s);
+    }
+}
+
+// Rows of 8 aligned elements of `esize` bytes (16-byte vectors; codes: 8).
+bool wide_rows(const void* p, int64_t ld, int esize) {
+    return (reinterpret_cast<uintptr_t>(p) & (esize == 1 ? 7u : 15u)) == 0 && ld % 8 == 0;
 }
 
 // ---- argument checks -----------------------------------------------------------
@@ -230,7 +742,10 @@ int gdr_rmsnorm_fwd(const void* x, int64_t x_stride, const void* residual, int64
     p.groups = fp8 ? (D + p.group - 1) / p.group : 0;
     p.eps = eps;
     cudaStream_t s = (cudaStream_t)stream;
-    return launched(dtype == GDR_BF16 ? launch_fwd<__nv_bfloat16>(p, fp8, s) : launch_fwd<float>(p, fp8, s),
+    const bool wide = D % 8 == 0 && wide_rows(x, x_stride, esize) && wide_rows(y, y_stride, fp8 ? 1 : esize) &&
+                      (!residual || (wide_rows(residual, residual_stride, esize) &&
+                                     wide_rows(residual_out, residual_out_stride, esize)));
+    return launched(dtype == GDR_BF16 ? launch_fwd<__nv_bfloat16>(p, fp8, wide, s) : launch_fwd<float>(p, fp8, wide, s),
                     "gdr_rmsnorm_fwd launch");
 }
 
@@ -275,8 +790,11 @@ int gdr_rmsnorm_bwd(const void* dy, int64_t dy_stride, const void* s, int64_t s_
     p.dy = dy; p.s = s; p.w = weight; p.ds = d_residual_out; p.dx = dx; p.dw = dweight;
     p.partial = static_cast<float*>(workspace);
     p.lddy = dy_stride; p.lds = s_stride; p.ldds = d_residual_out_stride; p.lddx = dx_stride;
-    p.M = M; p.D = D; p.parts = norm_parts(M); p.eps = eps;
-    return launched(dtype == GDR_BF16 ? launch_bwd<__nv_bfloat16>(p, st) : launch_bwd<float>(p, st),
+    p.M = M; p.D = D; p.eps = eps;
+    const bool wide = D % 8 == 0 && wide_rows(dy, dy_stride, esize) && wide_rows(s, s_stride, esize) &&
+                      wide_rows(dx, dx_stride, esize) &&
+                      (!d_residual_out || wide_rows(d_residual_out, d_residual_out_stride, esize));
+    return launched(dtype == GDR_BF16 ? launch_bwd<__nv_bfloat16>(p, wide, st) : launch_bwd<float>(p, wide, st),
                     "gdr_rmsnorm_bwd launch");
 }
 
