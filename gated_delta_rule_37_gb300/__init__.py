@@ -20,8 +20,8 @@ Entry points (same names as the C ABI, without the ``gdr_`` prefix):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -304,19 +304,31 @@ def gating_fwd(a, dt_bias, A_log, b, *, flags: int = 0, g=None, beta=None, strea
 # Rows are 2-D tensors whose last axis is dense; their row stride is free (a
 # column block of a wider matrix, an expanded row).  Everything runs on the
 # tensors' device; `stream` defaults to that device's current stream, and what
-# a call allocates belongs to the stream it runs on.
+# a call allocates belongs to the stream it runs on.  What a call costs on the
+# host is the latency of a decode step: every tensor is checked once, and the
+# current stream is asked for its handle without making a Stream object.
+
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+_CODES = {torch.bfloat16: GDR_BF16, torch.float32: GDR_F32}
+
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _need(t, shape, dtype, device, what):
-    """Address of a dense tensor of this shape, dtype and device."""
-    if t is None:
-        return None
+def _refuse(t, shape, dtype, device, what):
     if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, not {t.device}")
+    raise ValueError(f"{what} must be on {device}, not {t.device}")
+
+
+def _dense(t, shape, dtype, device, what):
+    """Address of a dense tensor of this shape, dtype and device."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _refuse(t, shape, dtype, device, what)
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
@@ -324,17 +336,20 @@ def _need(t, shape, dtype, device, what):
 
 def _rows(t, shape, dtype, device, what):
     """(address, row stride) of a [rows, D] tensor with a dense last axis."""
-    if t.shape != shape:
-        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, not {t.device}")
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _refuse(t, shape, dtype, device, what)
     row, col = t.stride()
     rows, D = shape
     if col != 1 and D > 1:
         raise ValueError(f"{what} must be dense along its last axis")
     return t.data_ptr(), row if rows > 1 else D
+
+
+def _code(dtype):
+    c = _CODES.get(dtype)
+    if c is None:
+        raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
+    return c
 
 
 def _device_of(t, what):
@@ -345,32 +360,28 @@ def _device_of(t, what):
     return t.device
 
 
-_HERE = contextlib.nullcontext()
+def _elsewhere(device, stream):
+    """The context to enter first where a call does not run on the current
+    device's current stream; None where it does."""
+    if stream is None:
+        return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream)
 
 
-def _on(device, stream):
-    """Context in which to allocate and launch: the stream's, or the device's own current stream."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-        return torch.cuda.stream(stream)
-    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
-def _pool_of(size, device):
-    """(tensor, address, bytes) of a workspace; nothing for size 0."""
-    if size == 0:
-        return None, None, 0
-    t = torch.empty(size, dtype=torch.uint8, device=device)
-    return t, t.data_ptr(), size
-
-
-def _given(workspace, device):
-    if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+def _scratch(workspace, size, device):
+    """(tensor, address, bytes) of the given workspace, or of a new one of `size` bytes."""
+    if workspace is None:
+        if size == 0:
+            return None, None, 0
+        workspace = torch.empty(size, dtype=_U8, device=device)
+    elif workspace.device != device or workspace.dtype != _U8 or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a dense uint8 tensor on {device}")
     return workspace, workspace.data_ptr(), workspace.numel()
 
 
+@functools.lru_cache(maxsize=4096)
 def linrec_workspace_size(N: int, T: int, D: int, *, dtype: int, gate_dtype: int) -> int:
     out = ctypes.c_size_t(0)
     _check(load().gdr_linrec_workspace_size(N, T, D, dtype, gate_dtype, ctypes.byref(out)))
@@ -384,24 +395,31 @@ def linrec_fwd(x, g, cu_seqlens, *, initial_state=None, flags: int = 0, y=None, 
     [N+1] int32; initial_state [N, D] fp32 or None.  Rows from cu_seqlens[N] on
     are neither read nor written.  Returns (y, final_state or None)."""
     dev = _device_of(x, "x")
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return linrec_fwd(x, g, cu_seqlens, initial_state=initial_state, flags=flags, y=y, final_state=final_state,
+                              output_final_state=output_final_state, workspace=workspace)
     T, D = shape = x.shape
+    xt, gt = x.dtype, g.dtype
+    xc, gc = _code(xt), _code(gt)
     N = cu_seqlens.numel() - 1
     state = (N, D)
-    dt, gt = _dtype_code(x), _dtype_code(g)
-    with _on(dev, stream):
-        if y is None:
-            y = torch.empty(T, D, dtype=x.dtype, device=dev)
-        if final_state is None and output_final_state:
-            final_state = torch.empty(N, D, dtype=torch.float32, device=dev)
-        ws, wp, wn = _pool_of(linrec_workspace_size(N, T, D, dtype=dt, gate_dtype=gt), dev) \
-            if workspace is None else _given(workspace, dev)
-        f32 = torch.float32
-        _check(load().gdr_linrec_fwd(
-            *_rows(x, shape, x.dtype, dev, "x"), *_rows(g, shape, g.dtype, dev, "g"),
-            _need(initial_state, state, f32, dev, "initial_state"),
-            _need(cu_seqlens, (N + 1,), torch.int32, dev, "cu_seqlens"), N, T, D, dt, gt, flags,
-            *_rows(y, shape, x.dtype, dev, "y"), _need(final_state, state, f32, dev, "final_state"), wp, wn,
-            torch.cuda.current_stream(dev).cuda_stream))
+    xp, xs = _rows(x, shape, xt, dev, "x")
+    gp, gs = _rows(g, shape, gt, dev, "g")
+    hp = _dense(initial_state, state, _F32, dev, "initial_state")
+    cp = _dense(cu_seqlens, (N + 1,), _I32, dev, "cu_seqlens")
+    if y is None:
+        y = torch.empty(T, D, dtype=xt, device=dev)
+    yp, ys = _rows(y, shape, xt, dev, "y")
+    if final_state is None and output_final_state:
+        final_state = torch.empty(N, D, dtype=_F32, device=dev)
+    fp = _dense(final_state, state, _F32, dev, "final_state")
+    ws, wp, wn = _scratch(workspace, linrec_workspace_size(N, T, D, dtype=xc, gate_dtype=gc), dev)
+    code = (_lib or load()).gdr_linrec_fwd(xp, xs, gp, gs, hp, cp, N, T, D, xc, gc, flags, yp, ys, fp, wp, wn,
+                                           _current_handle(dev.index))
+    if code:
+        _check(code)
     return y, final_state
 
 
@@ -411,28 +429,37 @@ def linrec_bwd(dy, g, y, cu_seqlens, *, initial_state=None, d_final_state=None, 
     [N, D] fp32 (or None) that of the final state; g, y, initial_state are the
     forward's.  Returns (dx, dg, d_initial_state or None)."""
     dev = _device_of(dy, "dy")
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return linrec_bwd(dy, g, y, cu_seqlens, initial_state=initial_state, d_final_state=d_final_state,
+                              flags=flags, dx=dx, dg=dg, d_initial_state=d_initial_state,
+                              output_d_initial_state=output_d_initial_state, workspace=workspace)
     T, D = shape = dy.shape
+    xt, gt = dy.dtype, g.dtype
+    xc, gc = _code(xt), _code(gt)
     N = cu_seqlens.numel() - 1
     state = (N, D)
-    dt, gt = _dtype_code(dy), _dtype_code(g)
-    with _on(dev, stream):
-        if dx is None:
-            dx = torch.empty(T, D, dtype=dy.dtype, device=dev)
-        if dg is None:
-            dg = torch.empty(T, D, dtype=g.dtype, device=dev)
-        if d_initial_state is None and output_d_initial_state:
-            d_initial_state = torch.empty(N, D, dtype=torch.float32, device=dev)
-        ws, wp, wn = _pool_of(linrec_workspace_size(N, T, D, dtype=dt, gate_dtype=gt), dev) \
-            if workspace is None else _given(workspace, dev)
-        f32 = torch.float32
-        _check(load().gdr_linrec_bwd(
-            *_rows(dy, shape, dy.dtype, dev, "dy"), *_rows(g, shape, g.dtype, dev, "g"),
-            *_rows(y, shape, dy.dtype, dev, "y"), _need(initial_state, state, f32, dev, "initial_state"),
-            _need(d_final_state, state, f32, dev, "d_final_state"),
-            _need(cu_seqlens, (N + 1,), torch.int32, dev, "cu_seqlens"), N, T, D, dt, gt, flags,
-            *_rows(dx, shape, dy.dtype, dev, "dx"), *_rows(dg, shape, g.dtype, dev, "dg"),
-            _need(d_initial_state, state, f32, dev, "d_initial_state"), wp, wn,
-            torch.cuda.current_stream(dev).cuda_stream))
+    dp, ds = _rows(dy, shape, xt, dev, "dy")
+    gp, gs = _rows(g, shape, gt, dev, "g")
+    yp, ys = _rows(y, shape, xt, dev, "y")
+    hp = _dense(initial_state, state, _F32, dev, "initial_state")
+    fp = _dense(d_final_state, state, _F32, dev, "d_final_state")
+    cp = _dense(cu_seqlens, (N + 1,), _I32, dev, "cu_seqlens")
+    if dx is None:
+        dx = torch.empty(T, D, dtype=xt, device=dev)
+    if dg is None:
+        dg = torch.empty(T, D, dtype=gt, device=dev)
+    xp, xs = _rows(dx, shape, xt, dev, "dx")
+    ap, as_ = _rows(dg, shape, gt, dev, "dg")
+    if d_initial_state is None and output_d_initial_state:
+        d_initial_state = torch.empty(N, D, dtype=_F32, device=dev)
+    ip = _dense(d_initial_state, state, _F32, dev, "d_initial_state")
+    ws, wp, wn = _scratch(workspace, linrec_workspace_size(N, T, D, dtype=xc, gate_dtype=gc), dev)
+    code = (_lib or load()).gdr_linrec_bwd(dp, ds, gp, gs, yp, ys, hp, fp, cp, N, T, D, xc, gc, flags, xp, xs, ap, as_,
+                                           ip, wp, wn, _current_handle(dev.index))
+    if code:
+        _check(code)
     return dx, dg, d_initial_state
 
 
@@ -443,24 +470,33 @@ def linrec_step(x, g, state_pool, state_indices, cu_seqlens, *, flags: int = GDR
     updated in place only with GDR_COMMIT; intermediate_states [rows >= N,
     steps, D] (pool dtype) receives the state after every token.  Returns y."""
     dev = _device_of(x, "x")
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return linrec_step(x, g, state_pool, state_indices, cu_seqlens, flags=flags, y=y,
+                               intermediate_states=intermediate_states)
     T, D = shape = x.shape
+    xt, gt, pt = x.dtype, g.dtype, state_pool.dtype
     N = cu_seqlens.numel() - 1
-    steps, states = 0, None
     slots = state_pool.shape[0]
+    xp, xs = _rows(x, shape, xt, dev, "x")
+    gp, gs = _rows(g, shape, gt, dev, "g")
+    pp = _dense(state_pool, (slots, D), pt, dev, "state_pool")
+    ip = _dense(state_indices, (N,), _I32, dev, "state_indices")
+    cp = _dense(cu_seqlens, (N + 1,), _I32, dev, "cu_seqlens")
+    steps, bp = 0, None
     if intermediate_states is not None:
         if intermediate_states.dim() != 3 or intermediate_states.shape[0] < N:
             raise ValueError("intermediate_states must be [rows >= N, steps, D]")
         rows, steps = intermediate_states.shape[:2]
-        states = _need(intermediate_states, (rows, steps, D), state_pool.dtype, dev, "intermediate_states")
-    with _on(dev, stream):
-        if y is None:
-            y = torch.empty(T, D, dtype=x.dtype, device=dev)
-        _check(load().gdr_linrec_step(
-            *_rows(x, shape, x.dtype, dev, "x"), *_rows(g, shape, g.dtype, dev, "g"),
-            _need(state_pool, (slots, D), state_pool.dtype, dev, "state_pool"), _dtype_code(state_pool), slots,
-            _need(state_indices, (N,), torch.int32, dev, "state_indices"),
-            _need(cu_seqlens, (N + 1,), torch.int32, dev, "cu_seqlens"), N, T, D, _dtype_code(x), _dtype_code(g),
-            flags, *_rows(y, shape, x.dtype, dev, "y"), states, steps, torch.cuda.current_stream(dev).cuda_stream))
+        bp = _dense(intermediate_states, (rows, steps, D), pt, dev, "intermediate_states")
+    if y is None:
+        y = torch.empty(T, D, dtype=xt, device=dev)
+    yp, ys = _rows(y, shape, xt, dev, "y")
+    code = (_lib or load()).gdr_linrec_step(xp, xs, gp, gs, pp, _code(pt), slots, ip, cp, N, T, D, _code(xt), _code(gt),
+                                            flags, yp, ys, bp, steps, _current_handle(dev.index))
+    if code:
+        _check(code)
     return y
 
 
@@ -473,39 +509,48 @@ def rmsnorm_fwd(x, weight, *, residual=None, eps: float = 1e-6, y_dtype=None, sc
     residual_out may be residual (or x) itself.  Returns (y, residual_out or
     None, scales or None)."""
     dev = _device_of(x, "x")
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return rmsnorm_fwd(x, weight, residual=residual, eps=eps, y_dtype=y_dtype, scale_group=scale_group, y=y,
+                               residual_out=residual_out, scales=scales)
     M, D = shape = x.shape
+    xt = x.dtype
     if y_dtype is None:
-        y_dtype = x.dtype if y is None else y.dtype
-    dt = _dtype_code(x)
-    yt = GDR_E4M3 if y_dtype == torch.float8_e4m3fn else GDR_BF16 if y_dtype == torch.bfloat16 else \
-        GDR_F32 if y_dtype == torch.float32 else -1
-    if residual is None and residual_out is not None:
-        raise ValueError("residual_out without residual")
-    with _on(dev, stream):
-        if y is None:
-            y = torch.empty(M, D, dtype=y_dtype, device=dev)
-        sp = None
-        if yt == GDR_E4M3:
-            groups = -(-D // scale_group) if scale_group > 0 else 1
-            if scales is None:
-                scales = torch.empty(M, groups, dtype=torch.float32, device=dev)
-            sp = _need(scales, (M, groups), torch.float32, dev, "scales")
-        elif scales is not None:
+        y_dtype = xt if y is None else y.dtype
+    xp, xs = _rows(x, shape, xt, dev, "x")
+    wp = _dense(weight, (D,), _F32, dev, "weight")
+    sp = None
+    if y_dtype is torch.float8_e4m3fn:
+        yc = GDR_E4M3
+        groups = -(-D // scale_group) if scale_group > 0 else 1
+        if scales is None:
+            scales = torch.empty(M, groups, dtype=_F32, device=dev)
+        sp = _dense(scales, (M, groups), _F32, dev, "scales")
+    else:
+        yc = _CODES.get(y_dtype, -1)
+        if scales is not None:
             raise ValueError("scales go with y_dtype torch.float8_e4m3fn only")
-        if residual is not None:
-            if residual_out is None:
-                residual_out = torch.empty(M, D, dtype=x.dtype, device=dev)
-            rp = _rows(residual, shape, x.dtype, dev, "residual")
-            op = _rows(residual_out, shape, x.dtype, dev, "residual_out")
-        else:
-            rp = op = (None, 0)
-        _check(load().gdr_rmsnorm_fwd(
-            *_rows(x, shape, x.dtype, dev, "x"), *rp, _need(weight, (D,), torch.float32, dev, "weight"), M, D, eps,
-            dt, *op, *_rows(y, shape, y_dtype, dev, "y"), yt, sp, scale_group,
-            torch.cuda.current_stream(dev).cuda_stream))
+    if y is None:
+        y = torch.empty(M, D, dtype=y_dtype, device=dev)
+    yp, ys = _rows(y, shape, y_dtype, dev, "y")
+    if residual is not None:
+        rp, rs = _rows(residual, shape, xt, dev, "residual")
+        if residual_out is None:
+            residual_out = torch.empty(M, D, dtype=xt, device=dev)
+        op, os_ = _rows(residual_out, shape, xt, dev, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out without residual")
+    else:
+        rp, rs, op, os_ = None, 0, None, 0
+    code = (_lib or load()).gdr_rmsnorm_fwd(xp, xs, rp, rs, wp, M, D, eps, _code(xt), op, os_, yp, ys, yc, sp,
+                                            scale_group, _current_handle(dev.index))
+    if code:
+        _check(code)
     return y, residual_out, scales
 
 
+@functools.lru_cache(maxsize=4096)
 def rmsnorm_bwd_workspace_size(M: int, D: int) -> int:
     out = ctypes.c_size_t(0)
     _check(load().gdr_rmsnorm_bwd_workspace_size(M, D, ctypes.byref(out)))
@@ -519,23 +564,31 @@ def rmsnorm_bwd(dy, s, weight, *, eps: float = 1e-6, d_residual_out=None, dx=Non
     at s along the residual stream.  Returns (dx, dweight): dx is the gradient
     of x and of residual alike, dweight [D] fp32."""
     dev = _device_of(dy, "dy")
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return rmsnorm_bwd(dy, s, weight, eps=eps, d_residual_out=d_residual_out, dx=dx, dweight=dweight,
+                               output_dweight=output_dweight, workspace=workspace)
     M, D = shape = dy.shape
-    with _on(dev, stream):
-        if dx is None:
-            dx = torch.empty(M, D, dtype=dy.dtype, device=dev)
-        if dweight is None and output_dweight:
-            dweight = torch.empty(D, dtype=torch.float32, device=dev)
-        ws = wp = None
-        wn = 0
-        if dweight is not None:
-            ws, wp, wn = _pool_of(rmsnorm_bwd_workspace_size(M, D), dev) if workspace is None \
-                else _given(workspace, dev)
-        rp = (None, 0) if d_residual_out is None else _rows(d_residual_out, shape, dy.dtype, dev, "d_residual_out")
-        _check(load().gdr_rmsnorm_bwd(
-            *_rows(dy, shape, dy.dtype, dev, "dy"), *_rows(s, shape, dy.dtype, dev, "s"),
-            _need(weight, (D,), torch.float32, dev, "weight"), *rp, M, D, eps, _dtype_code(dy),
-            *_rows(dx, shape, dy.dtype, dev, "dx"), _need(dweight, (D,), torch.float32, dev, "dweight"), wp, wn,
-            torch.cuda.current_stream(dev).cuda_stream))
+    xt = dy.dtype
+    dp, ds = _rows(dy, shape, xt, dev, "dy")
+    sp, ss = _rows(s, shape, xt, dev, "s")
+    wp = _dense(weight, (D,), _F32, dev, "weight")
+    rp, rs = (None, 0) if d_residual_out is None else _rows(d_residual_out, shape, xt, dev, "d_residual_out")
+    if dx is None:
+        dx = torch.empty(M, D, dtype=xt, device=dev)
+    xp, xs = _rows(dx, shape, xt, dev, "dx")
+    ws = kp = gp = None
+    kn = 0
+    if dweight is None and output_dweight:
+        dweight = torch.empty(D, dtype=_F32, device=dev)
+    if dweight is not None:
+        gp = _dense(dweight, (D,), _F32, dev, "dweight")
+        ws, kp, kn = _scratch(workspace, rmsnorm_bwd_workspace_size(M, D), dev)
+    code = (_lib or load()).gdr_rmsnorm_bwd(dp, ds, sp, ss, wp, rp, rs, M, D, eps, _code(xt), xp, xs, gp, kp, kn,
+                                            _current_handle(dev.index))
+    if code:
+        _check(code)
     return dx, dweight
 
 

@@ -1,6 +1,7 @@
 // C ABI of libgdr.so: argument checks, workspace sizing, launch sequencing on
 // the caller's stream, error reporting.  The contract is documented in
 // include/gdr.h.
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -118,16 +119,19 @@ int check_common(int N, int64_t T, int Hk, int Hv, int K, int V, int dtype) {
 
 }  // namespace
 
-// The kernels are built for sm_103a only.
+// The kernels are built for sm_103a only.  A device found to be one is not asked again.
 int check_device() {
+    static std::atomic<bool> known[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(GDR_ERR_LAUNCH, "cudaGetDevice failed");
+    if (dev >= 0 && dev < 64 && known[dev].load(std::memory_order_relaxed)) return GDR_OK;
     int major = 0, minor = 0;
     cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
     cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
     if (major != 10 || minor != 3)
         return fail(GDR_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_103a only",
                     dev, major, minor);
+    if (dev >= 0 && dev < 64) known[dev].store(true, std::memory_order_relaxed);
     return GDR_OK;
 }
 

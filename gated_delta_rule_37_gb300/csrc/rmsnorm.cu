@@ -440,10 +440,13 @@ struct NormBwdParams {
     float* dw;
     float* partial;  // [parts, D]: dw summed over each CTA's rows
     int64_t lddy, lds, ldds, lddx, M;
-    int D, parts, tpr;
+    int D, parts, tpr, stages;
     float eps;
+    unsigned int* err;
 };
 
+constexpr unsigned kNormError = 0x400;  // device error word: a row's copies did not land
+constexpr int kMaxStages = 8;
 constexpr int kMaxParts = 608;  // CTAs of the backward: four per SM
 
 int norm_parts(int64_t M) { return (int)(M < kMaxParts ? M : kMaxParts); }
@@ -523,6 +526,124 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rmsnorm_bwd_kernel(NormBwdPara
     if (!p.dw) return;
     // the CTA's rows at once: slot after slot
     float2* dw2 = reinterpret_cast<float2*>(dw_s);
+    for (int k = 0; k < slots; ++k) {
+        if (slot == k)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int e = (c * tpr + l) * 8;
+                if (k > 0)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dw[c][i] = __fadd2_rn(dw2[e / 2 + i], dw[c][i]);
+                if (k + 1 < slots) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dw2[e / 2 + i] = dw[c][i];
+                } else if (e < p.D) {
+                    Cells<float> out;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) out.set(i, dw[c][i]);
+                    out.store(p.partial + (int64_t)blockIdx.x * p.D + e);
+                }
+            }
+        __syncthreads();
+    }
+}
+
+// The same for rows of 512 elements and more, whose rows (dy, s, d_residual) come
+// through a ring of `stages` rows in shared memory per row's threads (32 or more),
+// filled by bulk copies: the next rows are on their way while one is reduced.
+template <typename T, int CH, int MAX_THREADS, int MIN_CTAS>
+__global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) rmsnorm_bwd_ring_kernel(NormBwdParams p) {
+    __shared__ float2 exchange[2][kMaxThreads / 32];
+    __shared__ uint64_t full_s[kMaxThreads / 32][kMaxStages];
+    __shared__ int never;
+    extern __shared__ __align__(128) unsigned char ring[];
+    const int tpr = p.tpr, slots = blockDim.x / tpr, slot = threadIdx.x / tpr, l = threadIdx.x % tpr;
+    RowReduce reduce{exchange, tpr, slot, 0};
+    const float mean = 1.f / p.D;
+    const uint32_t row_bytes = p.D * (uint32_t)sizeof(T), rows = p.ds ? 3 : 2;
+    const uint32_t own = tc::smem_u32(ring) + slot * p.stages * rows * row_bytes;
+    const uint32_t full = tc::smem_u32(full_s[slot]);
+    const int64_t stride = (int64_t)gridDim.x * slots;
+    auto request = [&](int stage, int64_t m) {  // one thread of the row's
+        const uint32_t at = own + stage * rows * row_bytes, bar = full + stage * 8;
+        tc::mbar_arrive_tx(bar, rows * row_bytes);
+        tc::bulk_g2s(at, static_cast<const T*>(p.dy) + m * p.lddy, row_bytes, bar);
+        tc::bulk_g2s(at + row_bytes, static_cast<const T*>(p.s) + m * p.lds, row_bytes, bar);
+        if (p.ds) tc::bulk_g2s(at + 2 * row_bytes, static_cast<const T*>(p.ds) + m * p.ldds, row_bytes, bar);
+    };
+    const int64_t first = (int64_t)blockIdx.x * slots + slot;
+    if (l == 0) {
+        never = 0;
+        for (int k = 0; k < p.stages; ++k) tc::mbar_init(full + k * 8, 1);
+        tc::mbar_fence_init();
+        for (int k = 0; k < p.stages; ++k)
+            if (first + k * stride < p.M) request(k, first + k * stride);
+    }
+    float2 dw[CH][4];
+    Cells<float> w[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int e = (c * tpr + l) * 8;
+        w[c].zero();
+        if (e < p.D) w[c].load(p.w + e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dw[c][i] = both(0.f);
+    }
+    __syncthreads();
+    int stage = 0, parity = 0;
+    bool lost = false;
+    for (int64_t m = first; m < p.M; m += stride) {
+        if (!lost && !tc::mbar_wait(full + stage * 8, parity, &never)) {
+            lost = true;  // later waits are not begun: the rows run out without them
+            atomicOr(p.err, kNormError);
+        }
+        const unsigned char* at = ring + (own - tc::smem_u32(ring)) + stage * rows * row_bytes;
+        Cells<T> dy[CH], s[CH], ds[CH];
+        float2 square = both(0.f), dot = both(0.f);  // sums of s^2 and of s z
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = (c * tpr + l) * 8;
+            dy[c].zero();
+            s[c].zero();
+            ds[c].zero();
+            if (e < p.D) {
+                dy[c].load(reinterpret_cast<const T*>(at) + e);
+                s[c].load(reinterpret_cast<const T*>(at + row_bytes) + e);
+                if (p.ds) ds[c].load(reinterpret_cast<const T*>(at + 2 * row_bytes) + e);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = s[c].get(i);
+                square = __ffma2_rn(v, v, square);
+                dot = __ffma2_rn(v, __fmul2_rn(dy[c].get(i), w[c].get(i)), dot);
+            }
+        }
+        const float2 sums = reduce.sum(make_float2(square.x + square.y, dot.x + dot.y));
+        if (tpr == 32) __syncwarp();
+        if (l == 0 && m + p.stages * stride < p.M) request(stage, m + p.stages * stride);  // read by all
+        if (++stage == p.stages) {
+            stage = 0;
+            parity ^= 1;
+        }
+        const float rstd = 1.f / sqrtf(fmaf(sums.x, mean, p.eps)), proj = sums.y * mean * rstd * rstd;
+        T* dx_row = static_cast<T*>(p.dx) + m * p.lddx;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = (c * tpr + l) * 8;
+            Cells<T> out;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 d = dy[c].get(i), v = s[c].get(i);
+                const float2 t = __ffma2_rn(d, w[c].get(i), __fmul2_rn(v, both(-proj)));
+                out.set(i, __ffma2_rn(both(rstd), t, ds[c].get(i)));
+                dw[c][i] = __ffma2_rn(d, __fmul2_rn(v, both(rstd)), dw[c][i]);
+            }
+            if (e < p.D) out.store(dx_row + e);
+        }
+    }
+    if (!p.dw) return;
+    __syncthreads();  // the ring becomes the place of the sums
+    float2* dw2 = reinterpret_cast<float2*>(ring);
     for (int k = 0; k < slots; ++k) {
         if (slot == k)
 #pragma unroll
@@ -628,6 +749,11 @@ __global__ void rmsnorm_dw_kernel(const float* __restrict__ partial, int parts, 
     }
 }
 
+cudaError_t launch_dw(const NormBwdParams& p, cudaStream_t s) {
+    KernelTimer kt("rmsnorm_dw", s);
+    return launch_dependent(rmsnorm_dw_kernel, dim3((p.D + 31) / 32), dim3(512), 0, s, p.partial, p.parts, p.D, p.dw);
+}
+
 template <typename T, int CH, bool WIDE>
 cudaError_t launch_bwd_ch(NormBwdParams p, cudaStream_t s) {
     const int block = p.tpr > 256 ? p.tpr : 256, slots = block / p.tpr;
@@ -641,30 +767,61 @@ cudaError_t launch_bwd_ch(NormBwdParams p, cudaStream_t s) {
         else
             rmsnorm_bwd_any_kernel<T, CH><<<p.parts, block, smem, s>>>(p);
     }
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && p.dw) {
-        KernelTimer kt("rmsnorm_dw", s);
-        e = launch_dependent(rmsnorm_dw_kernel, dim3((p.D + 31) / 32), dim3(512), 0, s, p.partial, p.parts, p.D, p.dw);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess && p.dw ? launch_dw(p, s) : e;
+}
+
+// CTAS CTAs per SM; the ring takes their share of its 227 KB.
+template <typename T, int CH, int THREADS, int CTAS>
+cudaError_t launch_bwd_ring(NormBwdParams p, cudaStream_t s) {
+    auto kernel = rmsnorm_bwd_ring_kernel<T, CH, THREADS, CTAS>;
+    constexpr int kShare = 227 * 1024 / CTAS - 2048;
+    const int slots = THREADS / p.tpr, stage = slots * 3 * p.D * (int)sizeof(T);
+    p.stages = kShare / stage < kMaxStages ? kShare / stage : kMaxStages;
+    static std::atomic<bool> ready{false};
+    if (!ready.load(std::memory_order_relaxed)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShare);
+        if (e != cudaSuccess) return e;
+        ready.store(true, std::memory_order_relaxed);
     }
-    return e;
+    p.err = device_error_word();
+    if (!p.err) return cudaErrorInitializationError;
+    const int64_t want = (p.M + slots - 1) / slots, most = (int64_t)CTAS * sm_count();
+    p.parts = norm_parts(want < most ? want : most);
+    {
+        KernelTimer kt("rmsnorm_bwd", s);
+        kernel<<<p.parts, THREADS, p.stages * stage, s>>>(p);
+    }
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess && p.dw ? launch_dw(p, s) : e;
 }
 
 template <typename T>
 cudaError_t launch_bwd(NormBwdParams p, bool wide, cudaStream_t s) {
+    if (wide && p.D >= 512 && p.D * sizeof(T) <= 32768) {
+        const int pieces = p.D / 8;
+        if (pieces <= 512) {
+            p.tpr = row_threads(pieces, 2, 32);
+            return launch_bwd_ring<T, 2, 256, 2>(p, s);
+        }
+        if (pieces <= 1024) {
+            p.tpr = 512;
+            return launch_bwd_ring<T, 2, 512, 1>(p, s);
+        }
+        p.tpr = 512;
+        return launch_bwd_ring<T, 4, 512, 1>(p, s);
+    }
     if (!wide) {
         const int ch = p.D <= 4 * kMaxThreads ? 4 : p.D <= 16 * kMaxThreads ? 16 : 64;
         p.tpr = row_threads(p.D, ch, 32);
         return ch == 4 ? launch_bwd_ch<T, 4, false>(p, s) : ch == 16 ? launch_bwd_ch<T, 16, false>(p, s)
                                                                      : launch_bwd_ch<T, 64, false>(p, s);
     }
-    const int pieces = p.D / 8, ch = pieces <= 16 ? 1 : pieces <= 2 * kMaxThreads ? 2 : pieces <= 4 * kMaxThreads ? 4 : 8;
+    // narrow rows, and those of which the ring does not hold two
+    const int pieces = p.D / 8, ch = pieces <= 16 ? 1 : pieces <= 64 ? 2 : 8;
     p.tpr = row_threads(pieces, ch, 16);
-    switch (ch) {
-        case 1: return launch_bwd_ch<T, 1, true>(p, s);
-        case 2: return launch_bwd_ch<T, 2, true>(p, s);
-        case 4: return launch_bwd_ch<T, 4, true>(p, s);
-        default: return launch_bwd_ch<T, 8, true>(p, s);
-    }
+    return ch == 1 ? launch_bwd_ch<T, 1, true>(p, s) : ch == 2 ? launch_bwd_ch<T, 2, true>(p, s)
+                                                               : launch_bwd_ch<T, 8, true>(p, s);
 }
 
 // Rows of 8 aligned elements of `esize` bytes (16-byte vectors; codes: 8).
