@@ -15,9 +15,14 @@
 // state once it knows its incoming one.  A tile looks back from its left
 // neighbour to the nearest published state and folds the compositions between
 // into it, always in token order and with the same fused multiply-adds, so that
-// the bits do not depend on which of the two it found.  Tiles are handed out by
-// a counter in token order, so that a tile only ever waits for tiles that are
-// already running; every wait has a limit.
+// the bits do not depend on which of the two it found.  A published word says by
+// itself that it is there (the workspace is cleared to a NaN pattern that no
+// published value has), so that neither side needs a fence or a flag, and a tile
+// whose neighbour is done learns its state in one trip to L2.  (With a flag per
+// tile behind release and acquire, half of all cycles were waits at the barrier
+// behind the look-back.)  Tiles are handed out by a counter in token order, so
+// that a tile only ever waits for tiles that are already running; every wait has
+// a limit.
 //   The backward is the same scan from the end: with mu_t = a_t (dy_t + mu_{t+1})
 // a token is the map mu -> a (mu + dy); dx = dy + mu_{t+1}, dg = mu_t h_{t-1}.
 //
@@ -55,14 +60,12 @@ struct LinrecParams {
     int groups;          // channel groups of a tile row
     int rows;            // tile rows of T tokens
     unsigned int* head;  // workspace: [0] the tile counter, [1] set when a wait gave up
-    unsigned int* flags;  // [groups][rows]: 0, kComposed or kState
-    float* comp_a;       // [groups][rows][CC]: A, B of a tile, its outgoing state
-    float* comp_b;
-    float* state;
+    unsigned int* words;  // [groups][rows][3][CC]: a tile's outgoing state, A, B; kNothing until published
     unsigned int* err;
 };
 
-constexpr unsigned kComposed = 1, kState = 2;
+constexpr unsigned kNothing = 0xffffffffu;  // a NaN that arithmetic does not give
+constexpr int kHeadWords = 64;
 constexpr unsigned kScanError = 0x200;  // device error word: a tile's wait gave up
 
 // ---- exp(g) -------------------------------------------------------------------
@@ -163,11 +166,39 @@ __device__ __forceinline__ void advance(float (&h)[VEC], const float (&a)[VEC], 
     } else {
 #pragma unroll
         for (int j = 0; j < VEC; j += 2) {
-            const float2 a2 = make_float2(a[j], a[j + 1]), b2 = make_float2(b[j], b[j + 1]);
-            float2 h2 = make_float2(h[j], h[j + 1]);
+            const int k = (j + 1) % VEC;
+            const float2 a2 = make_float2(a[j], a[k]), b2 = make_float2(b[j], b[k]);
+            float2 h2 = make_float2(h[j], h[k]);
             h2 = BWD ? __fmul2_rn(a2, __fadd2_rn(h2, b2)) : __ffma2_rn(a2, h2, b2);
             h[j] = h2.x;
-            h[j + 1] = h2.y;
+            h[k] = h2.y;
+        }
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void add(float (&f)[VEC], const float (&s)[VEC]) {
+    if (VEC == 1) {
+        f[0] += s[0];
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2) {
+            const float2 v = __fadd2_rn(make_float2(f[j], f[(j + 1) % VEC]), make_float2(s[j], s[(j + 1) % VEC]));
+            f[j] = v.x;
+            f[(j + 1) % VEC] = v.y;
+        }
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void product(float (&o)[VEC], const float (&a)[VEC], const float (&b)[VEC]) {
+    if (VEC == 1) {
+        o[0] = a[0] * b[0];
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2) {
+            const float2 v = __fmul2_rn(make_float2(a[j], a[(j + 1) % VEC]), make_float2(b[j], b[(j + 1) % VEC]));
+            o[j] = v.x;
+            o[(j + 1) % VEC] = v.y;
         }
     }
 }
@@ -206,13 +237,107 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         :: "r"(dst), "l"(map), "r"(c), "r"(t), "r"(mbar) : "memory");
 }
 
-__device__ __forceinline__ unsigned load_acquire(const unsigned int* p) {
+__device__ __forceinline__ unsigned peek(const unsigned int* p) {
     unsigned v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void store_release(unsigned int* p, unsigned v) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" :: "l"(p), "r"(v) : "memory");
+__device__ __forceinline__ void publish(unsigned int* p, float f) {
+    unsigned v = __float_as_uint(f);
+    if (v == kNothing) v = 0x7fffffffu;  // some other NaN
+    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" :: "l"(p), "r"(v) : "memory");
+}
+
+// The state that reaches a tile of row `row` in one channel.  `w`: that channel's
+// words of row 0, rows `pitch` apart, fields `field` apart (state, A, B).  False
+// if a wait gave up.
+__device__ __forceinline__ bool look_back(const unsigned int* w, int row, int64_t pitch, int field, float& state,
+                                          const unsigned int* gave_up) {
+    constexpr int W = 4;
+    const uint64_t began = tc::globaltimer_ns();
+    unsigned spin = 0;
+    auto patience = [&]() {
+        return (++spin & 63) != 0 || (!peek(gave_up) && tc::globaltimer_ns() - began < tc::kWaitLimitNs);
+    };
+    // the nearest rows, all words at once
+    while (true) {
+        unsigned s[W], a[W], b[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const unsigned int* q = w + max(row - 1 - i, 0) * pitch;
+            s[i] = peek(q);
+            a[i] = peek(q + field);
+            b[i] = peek(q + 2 * field);
+        }
+        bool known = false, whole = true;
+        float h = 0.f;
+#pragma unroll
+        for (int i = W - 1; i >= 0; --i) {  // from the farthest: a state there starts anew, a map is applied
+            if (s[i] != kNothing) {
+                h = __uint_as_float(s[i]);
+                known = true;
+            } else if (a[i] != kNothing && b[i] != kNothing) {
+                h = fmaf(__uint_as_float(a[i]), h, __uint_as_float(b[i]));
+            } else {
+                known = whole = false;
+            }
+        }
+        if (known) {
+            state = h;
+            return true;
+        }
+        if (whole && row > W) break;
+        if (!patience()) return false;
+    }
+    // further: the nearest state, then forward over the maps
+    int k = row - 1 - W;
+    constexpr int V = 8;
+    while (true) {
+        unsigned s[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = peek(w + max(k - i, 0) * pitch);
+        int at = -1;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+            if (s[i] != kNothing) at = i;
+        if (at >= 0) {
+            k = max(k - at, 0);
+            state = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i == at) state = __uint_as_float(s[i]);
+            break;
+        }
+        if (k >= V)
+            k -= V;
+        else if (!patience())
+            return false;
+    }
+    for (++k; k < row;) {
+        unsigned s[V], a[V], b[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const unsigned int* q = w + min(k + i, row - 1) * pitch;
+            s[i] = peek(q);  // a tile that is cut publishes nothing else
+            a[i] = peek(q + field);
+            b[i] = peek(q + 2 * field);
+        }
+        bool ready = true;
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const bool map = a[i] != kNothing && b[i] != kNothing;
+            ready = ready && k + i < row && (s[i] != kNothing || map);
+            if (ready) {
+                state = s[i] != kNothing ? __uint_as_float(s[i])
+                                         : fmaf(__uint_as_float(a[i]), state, __uint_as_float(b[i]));
+                ++n;
+            }
+        }
+        k += n;
+        if (!n && !patience()) return false;
+    }
+    return true;
 }
 
 // The sequences that begin and end in the tile of tokens [t0, t0 + TT): by the
@@ -335,26 +460,37 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         // ---- into registers, and the composition of the thread's run
         float a[R][VEC];
         Row<TX, VEC> b[R], h[BWD ? R : 1];
+        const bool full = t0 + TT <= valid;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int i = run * R + r, l = BWD ? TT - 1 - i : i, t = t0 + l;
-            const bool ok = here && t < valid;
-            b[r].zero();
-            if (BWD) h[r].zero();
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) a[r][j] = 0.f;  // gates first: exp(0) = 1 is the identity
-            if (ok) {
+            const int i = run * R + r, l = BWD ? TT - 1 - i : i;
+            if (WIDE) {  // what lies outside the tensors has been filled with zeros
                 Row<TG, VEC> gr;
-                if (WIDE) {
-                    gr.load(gs + l * CC + lc * VEC);
-                    b[r].load(xs + l * CC + lc * VEC);
-                    if (BWD) h[r].load(hs + l * CC + lc * VEC);
-                } else {
-                    gr.load(static_cast<const TG*>(p.g) + t * p.ldg + c0);
+                gr.load(gs + l * CC + lc * VEC);
+                gr.get(a[r]);
+                b[r].load(xs + l * CC + lc * VEC);
+                if (BWD) h[r].load(hs + l * CC + lc * VEC);
+            } else {
+                const int t = t0 + l;
+                a[r][0] = 0.f;
+                b[r].zero();
+                if (BWD) h[r].zero();
+                if (here && t < valid) {
+                    a[r][0] = to_f(static_cast<const TG*>(p.g)[t * p.ldg + c0]);
                     b[r].load(static_cast<const TX*>(p.x) + t * p.ldx + c0);
                     if (BWD && t > 0) h[r].load(static_cast<const TX*>(p.h) + (t - 1) * p.ldh + c0);
                 }
-                gr.get(a[r]);
+            }
+        }
+        if (WIDE && !full) {  // rows behind the last sequence: the identity
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int i = run * R + r;
+                if (t0 + (BWD ? TT - 1 - i : i) >= valid) {
+                    b[r].zero();
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) a[r][j] = 0.f;  // exp(0) = 1
+                }
             }
         }
         float A[VEC], B[VEC];
@@ -383,8 +519,16 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 }
             }
             advance<BWD, VEC>(B, a[r], f);
+            if (VEC == 1) {
+                A[0] *= a[r][0];
+            } else {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) A[j] *= a[r][j];
+                for (int j = 0; j < VEC; j += 2) {
+                    const float2 m = __fmul2_rn(make_float2(A[j], A[(j + 1) % VEC]), make_float2(a[r][j], a[r][(j + 1) % VEC]));
+                    A[j] = m.x;
+                    A[(j + 1) % VEC] = m.y;
+                }
+            }
         }
         if (WIDE) {
             *reinterpret_cast<float4*>(ca + run * CC + C::place(lc, 0)) = make_float4(A[0], A[1 % VEC], A[2 % VEC], A[3 % VEC]);
@@ -447,59 +591,24 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                     fa *= ra;
                 }
             }
-            const int64_t rec = (int64_t)group * p.rows + row;
-            unsigned int* flag = p.flags + rec;
+            const int64_t pitch = 3 * CC;
+            unsigned int* words = p.words + (int64_t)group * p.rows * pitch + pos;
+            unsigned int* own = words + row * pitch;
             const bool settled = cut_any || row == 0;  // the outgoing state does not depend on the incoming one
             if (settled) {
-                __stcg(p.state + rec * CC + pos, fb);
+                publish(own, fb);
             } else {
-                __stcg(p.comp_a + rec * CC + pos, fa);
-                __stcg(p.comp_b + rec * CC + pos, fb);
+                publish(own + CC, fa);
+                publish(own + 2 * CC, fb);
             }
-            tc::bar_sync(1, CC);
-            if (tid == 0) store_release(flag, settled ? kState : kComposed);
             float carry = 0.f;
             if (row > 0) {
-                if (warp == 0) {
-                    // nearest row to the left with a state, every row between composed
-                    int base = row - 1, found = -1;
-                    const uint64_t began = tc::globaltimer_ns();
-                    for (unsigned spin = 1;; ++spin) {
-                        const int k = base - lane;
-                        const unsigned f = k >= 0 ? load_acquire(flag - row + k) : kComposed;
-                        const unsigned state = __ballot_sync(0xffffffffu, f == kState);
-                        const unsigned none = __ballot_sync(0xffffffffu, f == 0);
-                        if (state && !(none & ((state & -state) - 1))) {
-                            found = base - (__ffs(state) - 1);
-                            break;
-                        }
-                        if (!state && !none) {  // all composed: further left (row 0 always has a state)
-                            base -= 32;
-                            continue;
-                        }
-                        if ((spin & 63) == 0 &&
-                            (load_acquire(p.head + 1) || tc::globaltimer_ns() - began > tc::kWaitLimitNs))
-                            break;
-                    }
-                    if (lane == 0) {
-                        misc[4] = found;
-                        if (found < 0) {
-                            *abort_s = 1;
-                            store_release(p.head + 1, 1u);
-                            atomicOr(p.err, kScanError);
-                        }
-                    }
+                if (!look_back(words, row, pitch, CC, carry, p.head + 1)) {
+                    *abort_s = 1;
+                    p.head[1] = 1;
+                    atomicOr(p.err, kScanError);
                 }
-                tc::bar_sync(1, CC);
-                const int found = misc[4];
-                if (found >= 0) {
-                    int64_t k = rec - row + found;
-                    carry = __ldcg(p.state + k * CC + pos);
-#pragma unroll 4
-                    for (++k; k < rec; ++k)
-                        carry = fmaf(__ldcg(p.comp_a + k * CC + pos), carry, __ldcg(p.comp_b + k * CC + pos));
-                }
-                if (!settled) __stcg(p.state + rec * CC + pos, fmaf(fa, carry, fb));
+                if (!settled) publish(own, fmaf(fa, carry, fb));
             }
             carry_s[pos] = carry;
         }
@@ -508,11 +617,6 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             if (WIDE && tid == 0 && ntile >= 0) tc::mbar_wait_copies(mbar, buf ^ 1);
             break;
         }
-        if (many && tid == 0 && row > 0) {
-            const int64_t rec = (int64_t)group * p.rows + row;
-            store_release(p.flags + rec, kState);  // a tile that is cut has set it before
-        }
-
         // ---- the state that reaches each run
         {
             float f = many ? carry_s[pos] : 0.f;
@@ -536,25 +640,25 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 s[0] = ca[run * CC + lc];
             }
             // ---- every token from its state
+            const int64_t t_first = t0 + (BWD ? TT - 1 - run * R : run * R), dir = BWD ? -1 : 1;
+            TX* out = static_cast<TX*>(p.out) + t_first * p.ldo + c0;
+            TG* dg = BWD ? static_cast<TG*>(p.dg) + t_first * p.lddg + c0 : nullptr;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int i = run * R + r, l = BWD ? TT - 1 - i : i;
-                const int64_t t = t0 + l;
-                if (t >= valid) continue;
+            for (int r = 0; r < R; ++r, out += dir * p.ldo, dg += BWD ? -p.lddg : 0) {
+                if (!full && t_first + dir * r >= valid) continue;
                 int n_first = -1, n_last = -1;
                 if (bounded) {
-                    n_first = first[i];
-                    n_last = last[i];
+                    n_first = first[run * R + r];
+                    n_last = last[run * R + r];
                     if (n_first >= 0) start_state(n_first, s);
                 }
                 float f[VEC];
                 b[r].get(f);
                 if (BWD) {
-                    float lam[VEC], before[VEC];
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) lam[j] = f[j] + s[j];
-                    Row<TX, VEC>::store(static_cast<TX*>(p.out) + t * p.ldo + c0, lam);
-                    advance<BWD, VEC>(s, a[r], f);
+                    float before[VEC];
+                    add<VEC>(f, s);  // lam
+                    Row<TX, VEC>::store(out, f);
+                    product<VEC>(s, a[r], f);  // mu
                     h[r].get(before);
                     if (n_last >= 0) {  // the sequence's first token: what came before it is h0
                         Row<float, VEC> z;
@@ -562,12 +666,11 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                         if (p.h0) z.load(p.h0 + (int64_t)n_last * p.D + c0);
                         z.get(before);
                     }
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) before[j] *= s[j];
-                    Row<TG, VEC>::store(static_cast<TG*>(p.dg) + t * p.lddg + c0, before);
+                    product<VEC>(before, before, s);
+                    Row<TG, VEC>::store(dg, before);
                 } else {
                     advance<BWD, VEC>(s, a[r], f);
-                    Row<TX, VEC>::store(static_cast<TX*>(p.out) + t * p.ldo + c0, s);
+                    Row<TX, VEC>::store(out, s);
                 }
                 if (n_last >= 0 && p.last) Row<float, VEC>::store(p.last + (int64_t)n_last * p.D + c0, s);
             }
@@ -589,19 +692,20 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     }
 }
 
-// Clears the workspace's head and flags; the tile kernel behind it may start meanwhile.
-__global__ void linrec_clear_kernel(unsigned int* w, int64_t n) {
+// Clears the workspace; the tile kernel behind it may start meanwhile.
+__global__ void linrec_clear_kernel(uint4* w, int64_t n) {
     tc::grid_dep_launch();
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) w[i] = 0;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+        const unsigned v = i < kHeadWords / 4 ? 0u : kNothing;
+        w[i] = make_uint4(v, v, v, v);
+    }
 }
 
 // ---- workspace and launch ------------------------------------------------------------
 
-constexpr int kHeadWords = 64;
-
 struct ScanLayout {
     int groups, rows;
-    size_t off_a, off_b, off_state, total;  // bytes; 0 in all for a single row of tiles
+    size_t words, total;  // published words, bytes in all; 0 for a single row of tiles
 };
 
 ScanLayout scan_layout(int64_t T, int D, int TT, int CC) {
@@ -609,11 +713,8 @@ ScanLayout scan_layout(int64_t T, int D, int TT, int CC) {
     l.groups = (D + CC - 1) / CC;
     l.rows = (int)((T + TT - 1) / TT);
     if (l.rows <= 1) return l;
-    const size_t recs = (size_t)l.groups * l.rows, block = recs * CC * sizeof(float);
-    l.off_a = ((kHeadWords + recs) * sizeof(unsigned) + 255) / 256 * 256;
-    l.off_b = l.off_a + block;
-    l.off_state = l.off_b + block;
-    l.total = (l.off_state + block + 255) / 256 * 256;
+    l.words = (size_t)l.groups * l.rows * 3 * CC;
+    l.total = (kHeadWords + l.words) * sizeof(unsigned);
     return l;
 }
 
@@ -715,14 +816,12 @@ cudaError_t launch_tiles(LinrecParams p, void* ws, cudaStream_t s) {
     }
     char* w = static_cast<char*>(ws);
     p.head = reinterpret_cast<unsigned int*>(w);
-    p.flags = p.head + kHeadWords;
-    p.comp_a = reinterpret_cast<float*>(w + l.off_a);
-    p.comp_b = reinterpret_cast<float*>(w + l.off_b);
-    p.state = reinterpret_cast<float*>(w + l.off_state);
+    p.words = p.head + kHeadWords;
     {
         KernelTimer kt("linrec_clear", s);
-        const int64_t words = kHeadWords + tiles, blocks = (words + 1023) / 1024;
-        linrec_clear_kernel<<<(unsigned)(blocks < 152 ? blocks : 152), 256, 0, s>>>(p.head, words);
+        const int64_t quads = (int64_t)(l.total / 16), blocks = (quads + 511) / 512;
+        linrec_clear_kernel<<<(unsigned)(blocks < 608 ? blocks : 608), 256, 0, s>>>(
+            reinterpret_cast<uint4*>(p.head), quads);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
