@@ -35,6 +35,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "gdr.h"
@@ -85,32 +86,45 @@ __device__ __forceinline__ float decay(float g) { return fabsf(g) > kTaylor ? ex
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-__device__ __forceinline__ void decay(float (&g)[1]) { g[0] = decay(g[0]); }
-
-__device__ __forceinline__ void decay(float (&g)[8]) {
+// Of all R x VEC gates of a thread, in place.  Whether any is beyond the polynomial
+// is asked once, by the warp as a whole.
+template <int R, int VEC>
+__device__ __forceinline__ void decays(float (&g)[R][VEC]) {
     float most = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(g[j]));
-    float a[8];
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-        const float2 v = make_float2(g[j], g[j + 1]);
-        float2 p = __ffma2_rn(v, both(1.f / 720), both(1.f / 120));
-        p = __ffma2_rn(v, p, both(1.f / 24));
-        p = __ffma2_rn(v, p, both(1.f / 6));
-        p = __ffma2_rn(v, p, both(0.5f));
-        p = __ffma2_rn(v, p, both(1.f));
-        p = __ffma2_rn(v, p, both(1.f));
-        a[j] = p.x;
-        a[j + 1] = p.y;
-    }
-    if (most > kTaylor) {
+        for (int j = 0; j < VEC; ++j) most = fmaxf(most, fabsf(g[r][j]));
+    if (__any_sync(0xffffffffu, most > kTaylor)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (fabsf(g[j]) > kTaylor) a[j] = expf(g[j]);
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float far = expf(g[r][j]), near = taylor_exp(g[r][j]);
+                g[r][j] = fabsf(g[r][j]) > kTaylor ? far : near;
+            }
+        return;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = a[j];
+    for (int r = 0; r < R; ++r) {
+        if (VEC == 1) {
+            g[r][0] = taylor_exp(g[r][0]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; j += 2) {
+                const int k = (j + 1) % VEC;
+                const float2 v = make_float2(g[r][j], g[r][k]);
+                float2 p = __ffma2_rn(v, both(1.f / 720), both(1.f / 120));
+                p = __ffma2_rn(v, p, both(1.f / 24));
+                p = __ffma2_rn(v, p, both(1.f / 6));
+                p = __ffma2_rn(v, p, both(0.5f));
+                p = __ffma2_rn(v, p, both(1.f));
+                p = __ffma2_rn(v, p, both(1.f));
+                g[r][j] = p.x;
+                g[r][k] = p.y;
+            }
+        }
+    }
 }
 
 // ---- VEC consecutive elements, kept as they are stored -------------------------
@@ -208,7 +222,7 @@ __device__ __forceinline__ void product(float (&o)[VEC], const float (&a)[VEC], 
 // WIDE: 8 channels per thread, 64 per tile, staged by TMA (aligned rows).
 // Otherwise one channel per thread, 32 per tile, read directly.
 template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
-    static constexpr int THREADS = 256, WARPS = THREADS / 32;
+    static constexpr int THREADS = 256, CTAS = 2, WARPS = THREADS / 32;
     static constexpr int VEC = WIDE ? 8 : 1, LANES = WIDE ? 8 : 32, CC = VEC * LANES;
     static constexpr int RUNS = WARPS * 32 / LANES;          // runs of R tokens
     // A token takes 8 registers for its decays and 4 or 8 for each of b and h as
@@ -378,7 +392,7 @@ __device__ bool find_boundaries(const int32_t* cu, int N, int t0, int* first, in
 }
 
 template <typename TX, typename TG, bool BWD, bool WIDE>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(Tile<TX, TG, BWD, WIDE>::THREADS, Tile<TX, TG, BWD, WIDE>::CTAS)
 linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g,
                    const __grid_constant__ CUtensorMap map_h, const __grid_constant__ LinrecParams p) {
     using C = Tile<TX, TG, BWD, WIDE>;
@@ -493,6 +507,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 }
             }
         }
+        decays<R, VEC>(a);
         float A[VEC], B[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
@@ -506,30 +521,24 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             s.get(f);
         };
         int cut = 0;
+        // twice in the code: tiles in which a sequence begins or ends, and the others
+        auto compose = [&](auto cutting) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            decay(a[r]);
-            float f[VEC];
-            b[r].get(f);
-            if (bounded) {
-                const int n = first[run * R + r];
-                if (n >= 0) {
-                    start_state(n, B);
-                    cut = 1;
+            for (int r = 0; r < R; ++r) {
+                float f[VEC];
+                b[r].get(f);
+                if (decltype(cutting)::value) {
+                    const int n = first[run * R + r];
+                    if (n >= 0) {
+                        start_state(n, B);
+                        cut = 1;
+                    }
                 }
+                advance<BWD, VEC>(B, a[r], f);
+                product<VEC>(A, A, a[r]);
             }
-            advance<BWD, VEC>(B, a[r], f);
-            if (VEC == 1) {
-                A[0] *= a[r][0];
-            } else {
-#pragma unroll
-                for (int j = 0; j < VEC; j += 2) {
-                    const float2 m = __fmul2_rn(make_float2(A[j], A[(j + 1) % VEC]), make_float2(a[r][j], a[r][(j + 1) % VEC]));
-                    A[j] = m.x;
-                    A[(j + 1) % VEC] = m.y;
-                }
-            }
-        }
+        };
+        bounded ? compose(std::true_type()) : compose(std::false_type());
         if (WIDE) {
             *reinterpret_cast<float4*>(ca + run * CC + C::place(lc, 0)) = make_float4(A[0], A[1 % VEC], A[2 % VEC], A[3 % VEC]);
             *reinterpret_cast<float4*>(ca + run * CC + C::place(lc, 4)) = make_float4(A[4 % VEC], A[5 % VEC], A[6 % VEC], A[7 % VEC]);
@@ -547,12 +556,13 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         if (tid == 0 && ntile >= 0) request(ntile);  // the stage has been read
 
         // ---- the runs of each part, then the parts: the tile's composition
-        {
+        auto fold = [&](auto cutting) {
             float fa = 1.f, fb = 0.f;
 #pragma unroll
-            for (int s = part * C::RUNS_PART; s < (part + 1) * C::RUNS_PART; ++s) {
-                const float ra = ca[s * CC + pos], rb = cb[s * CC + pos];
-                if (bounded && cut_s[s]) {
+            for (int i = 0; i < C::RUNS_PART; ++i) {
+                const int at = part * C::RUNS_PART + i;
+                const float ra = ca[at * CC + pos], rb = cb[at * CC + pos];
+                if (decltype(cutting)::value && cut_s[at]) {
                     fb = rb;
                 } else {
                     fb = fmaf(ra, fb, rb);
@@ -561,12 +571,13 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             }
             pa[part * CC + pos] = fa;
             pb[part * CC + pos] = fb;
-        }
+        };
+        bounded ? fold(std::true_type()) : fold(std::false_type());
         // whether a part is cut: read from cut_s by everyone alike
         auto part_cut = [&](int q) {
             int c = 0;
             if (bounded)
-                for (int s = q * C::RUNS_PART; s < (q + 1) * C::RUNS_PART; ++s) c |= cut_s[s];
+                for (int i = q * C::RUNS_PART; i < (q + 1) * C::RUNS_PART; ++i) c |= cut_s[i];
             return c != 0;
         };
         if (warp == C::WARPS - 1 && ntile >= 0) {  // while the others fold: the next tile's sequences
@@ -618,16 +629,19 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             break;
         }
         // ---- the state that reaches each run
-        {
+        auto walk = [&](auto cutting) {
             float f = many ? carry_s[pos] : 0.f;
-            for (int q = 0; q < part; ++q) f = part_cut(q) ? pb[q * CC + pos] : fmaf(pa[q * CC + pos], f, pb[q * CC + pos]);
+            for (int q = 0; q < part; ++q)
+                f = decltype(cutting)::value && part_cut(q) ? pb[q * CC + pos] : fmaf(pa[q * CC + pos], f, pb[q * CC + pos]);
 #pragma unroll
-            for (int s = part * C::RUNS_PART; s < (part + 1) * C::RUNS_PART; ++s) {
-                const float ra = ca[s * CC + pos], rb = cb[s * CC + pos];
-                ca[s * CC + pos] = f;
-                f = bounded && cut_s[s] ? rb : fmaf(ra, f, rb);
+            for (int i = 0; i < C::RUNS_PART; ++i) {
+                const int at = part * C::RUNS_PART + i;
+                const float ra = ca[at * CC + pos], rb = cb[at * CC + pos];
+                ca[at * CC + pos] = f;
+                f = decltype(cutting)::value && cut_s[at] ? rb : fmaf(ra, f, rb);
             }
-        }
+        };
+        bounded ? walk(std::true_type()) : walk(std::false_type());
         __syncthreads();
         if (here) {
             float s[VEC];
@@ -643,37 +657,43 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             const int64_t t_first = t0 + (BWD ? TT - 1 - run * R : run * R), dir = BWD ? -1 : 1;
             TX* out = static_cast<TX*>(p.out) + t_first * p.ldo + c0;
             TG* dg = BWD ? static_cast<TG*>(p.dg) + t_first * p.lddg + c0 : nullptr;
+            auto evaluate = [&](auto cutting) {  // cutting: or rows behind the last sequence
 #pragma unroll
-            for (int r = 0; r < R; ++r, out += dir * p.ldo, dg += BWD ? -p.lddg : 0) {
-                if (!full && t_first + dir * r >= valid) continue;
-                int n_first = -1, n_last = -1;
-                if (bounded) {
-                    n_first = first[run * R + r];
-                    n_last = last[run * R + r];
-                    if (n_first >= 0) start_state(n_first, s);
-                }
-                float f[VEC];
-                b[r].get(f);
-                if (BWD) {
-                    float before[VEC];
-                    add<VEC>(f, s);  // lam
-                    Row<TX, VEC>::store(out, f);
-                    product<VEC>(s, a[r], f);  // mu
-                    h[r].get(before);
-                    if (n_last >= 0) {  // the sequence's first token: what came before it is h0
-                        Row<float, VEC> z;
-                        z.zero();
-                        if (p.h0) z.load(p.h0 + (int64_t)n_last * p.D + c0);
-                        z.get(before);
+                for (int r = 0; r < R; ++r, out += dir * p.ldo, dg += BWD ? -p.lddg : 0) {
+                    int n_last = -1;
+                    if (decltype(cutting)::value) {
+                        if (t_first + dir * r >= valid) continue;
+                        if (bounded) {
+                            const int n = first[run * R + r];
+                            n_last = last[run * R + r];
+                            if (n >= 0) start_state(n, s);
+                        }
                     }
-                    product<VEC>(before, before, s);
-                    Row<TG, VEC>::store(dg, before);
-                } else {
-                    advance<BWD, VEC>(s, a[r], f);
-                    Row<TX, VEC>::store(out, s);
+                    float f[VEC];
+                    b[r].get(f);
+                    if (BWD) {
+                        float before[VEC];
+                        add<VEC>(f, s);  // lam
+                        Row<TX, VEC>::store(out, f);
+                        product<VEC>(s, a[r], f);  // mu
+                        h[r].get(before);
+                        if (decltype(cutting)::value && n_last >= 0) {  // before the first token: h0
+                            Row<float, VEC> z;
+                            z.zero();
+                            if (p.h0) z.load(p.h0 + (int64_t)n_last * p.D + c0);
+                            z.get(before);
+                        }
+                        product<VEC>(before, before, s);
+                        Row<TG, VEC>::store(dg, before);
+                    } else {
+                        advance<BWD, VEC>(s, a[r], f);
+                        Row<TX, VEC>::store(out, s);
+                    }
+                    if (decltype(cutting)::value && n_last >= 0 && p.last)
+                        Row<float, VEC>::store(p.last + (int64_t)n_last * p.D + c0, s);
                 }
-                if (n_last >= 0 && p.last) Row<float, VEC>::store(p.last + (int64_t)n_last * p.D + c0, s);
-            }
+            };
+            bounded || !full ? evaluate(std::true_type()) : evaluate(std::false_type());
         }
         tile = ntile;
     }
