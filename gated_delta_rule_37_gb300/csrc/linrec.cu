@@ -29,8 +29,8 @@
 // Accuracy: a near 1 is applied thousands of times, so its error must have no
 // mean.  The hardware's exponential is about 0.3 * 2^-24 low on average just
 // below 0, which a memory of 4000 tokens turns into 6e-5 of the state; the
-// Taylor polynomial of degree 6 below 1/4, ending in a fused multiply-add with
-// 1, has a mean error below 0.001 * 2^-24.
+// Taylor polynomial, ending in a fused multiply-add with 1, has a mean error
+// below 0.001 * 2^-24 there.
 #include <cuda.h>
 #include <math.h>
 
@@ -60,6 +60,7 @@ struct LinrecParams {
     int N, D;
     int groups;          // channel groups of a tile row
     int rows;            // tile rows of T tokens
+    int clustered;       // one cluster of `rows` CTAs per channel group; else more than one row looks back
     unsigned int* head;  // workspace: [0] the tile counter, [1] set when a wait gave up
     unsigned int* words;  // [groups][rows][3][CC]: a tile's outgoing state, A, B; kNothing until published
     unsigned int* err;
@@ -71,7 +72,18 @@ constexpr unsigned kScanError = 0x200;  // device error word: a tile's wait gave
 
 // ---- exp(g) -------------------------------------------------------------------
 
-constexpr float kTaylor = 0.25f;  // |g| up to here: the polynomial
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+constexpr float kTaylor = 0.25f;  // |g| up to here: the polynomial of degree 6 (next term 1.2e-8)
+
+__device__ __forceinline__ float2 taylor_exp(float2 g) {
+    float2 p = __ffma2_rn(g, both(1.f / 720), both(1.f / 120));
+    p = __ffma2_rn(g, p, both(1.f / 24));
+    p = __ffma2_rn(g, p, both(1.f / 6));
+    p = __ffma2_rn(g, p, both(0.5f));
+    p = __ffma2_rn(g, p, both(1.f));
+    return __ffma2_rn(g, p, both(1.f));
+}
 
 __device__ __forceinline__ float taylor_exp(float g) {
     float p = fmaf(g, 1.f / 720, 1.f / 120);
@@ -82,48 +94,54 @@ __device__ __forceinline__ float taylor_exp(float g) {
     return fmaf(g, p, 1.f);
 }
 
-__device__ __forceinline__ float decay(float g) { return fabsf(g) > kTaylor ? expf(g) : taylor_exp(g); }
+// Any g: Cody and Waite's reduction ("Software Manual for the Elementary
+// Functions", 1980), g = n ln 2 + r with |r| <= ln 2 / 2 and ln 2 in two parts, the
+// polynomial of degree 7 in r (next term 5e-9), and 2^n put into the exponent.
+// Below -87.3 the result is not a normal number: 0.
+__device__ __forceinline__ float2 reduced_exp(float2 g) {
+    constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it leaves the nearest integer in the low bits
+    const float2 t = __ffma2_rn(g, both(1.44269504f), both(kRound));
+    const float2 n = __fadd2_rn(t, both(-kRound));
+    const float2 r = __ffma2_rn(n, both(1.90465e-9f), __ffma2_rn(n, both(-0.693147182f), g));
+    float2 p = __ffma2_rn(r, both(1.f / 5040), both(1.f / 720));
+    p = __ffma2_rn(r, p, both(1.f / 120));
+    p = __ffma2_rn(r, p, both(1.f / 24));
+    p = __ffma2_rn(r, p, both(1.f / 6));
+    p = __ffma2_rn(r, p, both(0.5f));
+    p = __ffma2_rn(r, p, both(1.f));
+    p = __ffma2_rn(r, p, both(1.f));
+    const float2 power = make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + 0x3f800000u),
+                                     __uint_as_float((__float_as_uint(t.y) << 23) + 0x3f800000u));
+    const float2 e = __fmul2_rn(p, power);  // NaN stays NaN
+    return make_float2(g.x < -87.3f ? 0.f : e.x, g.y < -87.3f ? 0.f : e.y);
+}
 
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+template <int N>
+__device__ __forceinline__ void exp_of(float (&g)[N], float2 (*f)(float2)) {
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+        const int k = j + 1 < N ? j + 1 : j;
+        const float2 e = f(make_float2(g[j], g[k]));
+        g[j] = e.x;
+        g[k] = e.y;
+    }
+}
 
-// Of all R x VEC gates of a thread, in place.  Whether any is beyond the polynomial
-// is asked once, by the warp as a whole.
-template <int R, int VEC>
-__device__ __forceinline__ void decays(float (&g)[R][VEC]) {
+// Of all N gates of a thread, in place.  Whether any is beyond the short
+// polynomial is asked once, by the warp as a whole.
+template <int N>
+__device__ __forceinline__ void decays(float (&g)[N]) {
     float most = 0.f;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) most = fmaxf(most, fabsf(g[r][j]));
+    for (int j = 0; j < N; ++j) most = fmaxf(most, fabsf(g[j]));
     if (__any_sync(0xffffffffu, most > kTaylor)) {
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float far = expf(g[r][j]), near = taylor_exp(g[r][j]);
-                g[r][j] = fabsf(g[r][j]) > kTaylor ? far : near;
-            }
-        return;
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (VEC == 1) {
-            g[r][0] = taylor_exp(g[r][0]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < VEC; j += 2) {
-                const int k = (j + 1) % VEC;
-                const float2 v = make_float2(g[r][j], g[r][k]);
-                float2 p = __ffma2_rn(v, both(1.f / 720), both(1.f / 120));
-                p = __ffma2_rn(v, p, both(1.f / 24));
-                p = __ffma2_rn(v, p, both(1.f / 6));
-                p = __ffma2_rn(v, p, both(0.5f));
-                p = __ffma2_rn(v, p, both(1.f));
-                p = __ffma2_rn(v, p, both(1.f));
-                g[r][j] = p.x;
-                g[r][k] = p.y;
-            }
+        for (int j = 0; j < N; ++j) {
+            const float far = expf(g[j]), near = taylor_exp(g[j]);
+            g[j] = fabsf(g[j]) > kTaylor ? far : near;
         }
+    } else {
+        exp_of(g, taylor_exp);
     }
 }
 
@@ -220,23 +238,27 @@ __device__ __forceinline__ void product(float (&o)[VEC], const float (&a)[VEC], 
 // ---- the tile kernel --------------------------------------------------------------
 
 // WIDE: 8 channels per thread, 64 per tile, staged by TMA (aligned rows).
-// Otherwise one channel per thread, 32 per tile, read directly.
+// Otherwise one channel per thread, 32 per tile, staged by 4-byte asynchronous
+// copies: fp32 rows are aligned to that, and a bf16 row's segment is copied from
+// the word that it begins in, one word more, and read from where it lies.
 template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
     static constexpr int THREADS = 256, CTAS = 2, WARPS = THREADS / 32;
     static constexpr int VEC = WIDE ? 8 : 1, LANES = WIDE ? 8 : 32, CC = VEC * LANES;
     static constexpr int RUNS = WARPS * 32 / LANES;          // runs of R tokens
-    // A token takes 8 registers for its decays and 4 or 8 for each of b and h as
-    // stored; R of them is what fits beside the rest at two CTAs per SM.
-    static constexpr int R = !WIDE ? 16 : sizeof(TX) == 2 ? (BWD ? 4 : 5) : (BWD ? 3 : 4);
+    // A token takes a register per channel for its decay and one (8 bf16 channels: a
+    // half) for each of b and h; R of them is what fits beside the rest.
+    static constexpr int R = !WIDE ? (BWD ? 16 : 24) : sizeof(TX) == 2 ? (BWD ? 4 : 5) : (BWD ? 3 : 4);
     static constexpr int TT = RUNS * R;
     static constexpr int PARTS = THREADS / CC, RUNS_PART = RUNS / PARTS;  // the fold over runs, in parts
+    // bytes of a token in the stage, a row of x / h and one of g
+    static constexpr int PITCH_X = WIDE ? CC * (int)sizeof(TX) : sizeof(TX) == 4 ? CC * 4 : CC * 2 + 8;
+    static constexpr int PITCH_G = WIDE ? CC * (int)sizeof(TG) : sizeof(TG) == 4 ? CC * 4 : CC * 2 + 8;
     // shared memory (bytes)
-    static constexpr int XS = 0, GS = XS + (WIDE ? TT * CC * (int)sizeof(TX) : 0);
-    static constexpr int HS = GS + (WIDE ? TT * CC * (int)sizeof(TG) : 0);
-    static constexpr int STAGE = HS + (WIDE && BWD ? TT * CC * (int)sizeof(TX) : 0);
+    static constexpr int XS = 0, GS = XS + TT * PITCH_X, HS = GS + TT * PITCH_G, STAGE = HS + (BWD ? TT * PITCH_X : 0);
     static constexpr int CA = STAGE, CB = CA + RUNS * CC * 4, PA = CB + RUNS * CC * 4, PB = PA + PARTS * CC * 4;
-    static constexpr int CARRY = PB + PARTS * CC * 4, FIRST = CARRY + CC * 4, LAST = FIRST + 2 * TT * 4;
-    static constexpr int CUT = LAST + 2 * TT * 4, MISC = CUT + RUNS * 4, BYTES_SMEM = MISC + 64;
+    static constexpr int TA = PB + PARTS * CC * 4, TB = TA + CC * 4, CARRY = TB + CC * 4;
+    static constexpr int FIRST = CARRY + CC * 4, LAST = FIRST + 2 * TT * 4, CUT = LAST + 2 * TT * 4;
+    static constexpr int MISC = CUT + RUNS * 4, BYTES_SMEM = MISC + 64;
     static_assert(RUNS % PARTS == 0 && STAGE % 128 == 0 && TT <= 256, "tile shape");
     // the 16-byte halves of a thread's 8 channels are kept CC / 2 apart: its float4
     // accesses then touch all banks in turn
@@ -249,6 +271,55 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
         :: "r"(dst), "l"(map), "r"(c), "r"(t), "r"(mbar) : "memory");
+}
+
+// One row's segment of n <= 32 channels at `from` into a stage row, by one warp.
+// The first and last rows of a bf16 tensor may have words that reach outside it:
+// those are copied element by element.
+template <typename T>
+__device__ __forceinline__ void copy_segment(uint32_t dst, const T* from, int n, bool edge, const T* base, const T* end,
+                                             int lane) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(from);
+    if (sizeof(T) == 4) {
+        if (lane < n)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + lane * 4), "l"(at + lane * 4) : "memory");
+        return;
+    }
+    const uintptr_t word = (at & ~uintptr_t(3)) + 4 * lane;
+    if (word >= at + 2 * n) return;
+    if (!edge || (word >= reinterpret_cast<uintptr_t>(base) && word + 4 <= reinterpret_cast<uintptr_t>(end))) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + 4 * lane), "l"(word) : "memory");
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; k += 2)
+            if (word + k >= at && word + k < at + 2 * n)
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + 4 * lane + k),
+                             "h"(*reinterpret_cast<const unsigned short*>(word + k)) : "memory");
+    }
+}
+// The rows [t0, t0 + TT) below `rows` of a [T, D] tensor into the stage, a warp
+// per row; `back` rows further up in the tensor.
+template <typename T, int TT, int WARPS, int PITCH>
+__device__ __forceinline__ void copy_rows(uint32_t stage, const void* tensor, int64_t ld, int64_t T_all, int D, int t0,
+                                          int rows, int back, int c, int warp, int lane) {
+    const T* base = static_cast<const T*>(tensor);
+    const T* end = base + (T_all - 1) * ld + D;
+    const int n = min(32, D - c), last = (int)T_all - 1 + back;
+    const T* from = base + (int64_t)(t0 + warp - back) * ld + c;
+    stage += warp * PITCH;
+    for (int t = t0 + warp; t < min(t0 + TT, rows); t += WARPS, from += WARPS * ld, stage += WARPS * PITCH)
+        if (t >= back) copy_segment(stage, from, n, t == back || t == last || ld == 0, base, end, lane);
+}
+
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float cluster_read(const void* own, unsigned rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(own)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ unsigned peek(const unsigned int* p) {
@@ -415,7 +486,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int lc = lane % C::LANES, run = warp * (32 / C::LANES) + lane / C::LANES;
     const int part = tid / CC, pos = tid % CC;
-    const bool many = p.rows > 1;
+    const bool many = p.rows > 1 && !p.clustered;
 
     if (tid == 0) {
         tc::mbar_init(mbar, 1);
@@ -429,27 +500,42 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
 
     // tiles are taken in the order of the scan, all channel groups of a row first
     auto take = [&]() -> int64_t { return many ? (int64_t)atomicAdd(p.head, 1u) : tiles; };
-    auto token0 = [&](int64_t tile) -> int {
-        const int row = (int)(tile / p.groups);
+    auto token0 = [&](int tile) -> int {
+        const int row = tile / p.groups;
         return (BWD ? rows - 1 - row : row) * TT;
     };
-    auto request = [&](int64_t tile) {  // one thread: the tile's rows into the stage
-        if (!WIDE) return;
-        const int c = (int)(tile % p.groups) * CC, t = token0(tile);
-        tc::mbar_arrive_tx(mbar, C::STAGE);
-        tma_load_2d(tc::smem_u32(xs), &map_x, c, t, mbar);
-        tma_load_2d(tc::smem_u32(gs), &map_g, c, t, mbar);
-        if (BWD) tma_load_2d(tc::smem_u32(hs), &map_h, c, t - 1, mbar);  // row t - 1 beside token t
+    auto request = [&](int tile) {  // the tile's rows into the stage; all threads call it
+        if (WIDE && tid != 0) return;
+        const int c = tile % p.groups * CC, t0 = token0(tile);
+        if (WIDE) {
+            tc::mbar_arrive_tx(mbar, C::STAGE);
+            tma_load_2d(tc::smem_u32(smem + C::XS), &map_x, c, t0, mbar);
+            tma_load_2d(tc::smem_u32(smem + C::GS), &map_g, c, t0, mbar);
+            if (BWD) tma_load_2d(tc::smem_u32(smem + C::HS), &map_h, c, t0 - 1, mbar);  // row t - 1 beside token t
+            return;
+        }
+        copy_rows<TX, TT, C::WARPS, C::PITCH_X>(tc::smem_u32(smem + C::XS), p.x, p.ldx, p.T, p.D, t0, valid, 0, c, warp, lane);
+        copy_rows<TG, TT, C::WARPS, C::PITCH_G>(tc::smem_u32(smem + C::GS), p.g, p.ldg, p.T, p.D, t0, valid, 0, c, warp, lane);
+        if (BWD)
+            copy_rows<TX, TT, C::WARPS, C::PITCH_X>(tc::smem_u32(smem + C::HS), p.h, p.ldh, p.T, p.D, t0, valid, 1, c, warp,
+                                                    lane);
+    };
+    // bf16 rows staged by words: the half word that row t's segment begins in
+    auto half = [&](const void* tensor, int64_t ld, int c, int t, int size) {
+        return size == 4 ? 0 : (int)((reinterpret_cast<uintptr_t>(tensor) >> 1) + c + ((int)ld & t)) & 1;
     };
 
+    bool met = false;  // this CTA has been at its cluster's first meeting
     if (tid == 0) {
-        const int64_t t = many ? take() : (int64_t)blockIdx.x;
+        int64_t t = blockIdx.x;  // one tile of each CTA: a row of the cluster, or a group of the only row
+        if (many) t = take();
+        if (p.clustered) t = (int)(blockIdx.x % p.rows) < rows ? (int64_t)(blockIdx.x % p.rows) * p.groups + blockIdx.x / p.rows : tiles;
         misc[0] = t < tiles ? (int)t : -1;
-        if (t < tiles) request(t);
     }
     __syncthreads();
     int tile = misc[0];
     __syncthreads();
+    if (tile >= 0) request(tile);
     if (tile >= 0 && warp == C::WARPS - 1) {
         const bool any = find_boundaries<TT, BWD>(p.cu, p.N, token0(tile), reinterpret_cast<int*>(smem + C::FIRST),
                                                   reinterpret_cast<int*>(smem + C::LAST), lane);
@@ -458,12 +544,15 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
 
     for (int it = 0; tile >= 0; ++it) {
         const int buf = it & 1;
-        const int group = tile % p.groups, row = tile / p.groups, t0 = token0(tile), c0 = group * CC + lc * VEC;
+        const int row = tile / p.groups, group = tile - row * p.groups, t0 = (BWD ? rows - 1 - row : row) * TT;
+        const int c0 = group * CC + lc * VEC;
         const int* first = reinterpret_cast<int*>(smem + C::FIRST) + buf * TT;
         const int* last = reinterpret_cast<int*>(smem + C::LAST) + buf * TT;
         int64_t next = tiles;
         if (tid == 0) next = take();
-        if (WIDE && !tc::mbar_wait(mbar, buf, abort_s)) {
+        if (!WIDE) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        } else if (!tc::mbar_wait(mbar, buf, abort_s)) {
             *abort_s = 1;
             atomicOr(p.err, kScanError);
         }
@@ -485,29 +574,32 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 b[r].load(xs + l * CC + lc * VEC);
                 if (BWD) h[r].load(hs + l * CC + lc * VEC);
             } else {
-                const int t = t0 + l;
-                a[r][0] = 0.f;
-                b[r].zero();
-                if (BWD) h[r].zero();
-                if (here && t < valid) {
-                    a[r][0] = to_f(static_cast<const TG*>(p.g)[t * p.ldg + c0]);
-                    b[r].load(static_cast<const TX*>(p.x) + t * p.ldx + c0);
-                    if (BWD && t > 0) h[r].load(static_cast<const TX*>(p.h) + (t - 1) * p.ldh + c0);
-                }
+                const int c = group * CC, t = t0 + l;
+                a[r][0] = to_f(*(reinterpret_cast<const TG*>(smem + C::GS + l * C::PITCH_G) +
+                                 half(p.g, p.ldg, c, t, sizeof(TG)) + lane));
+                b[r].load(reinterpret_cast<const TX*>(smem + C::XS + l * C::PITCH_X) + half(p.x, p.ldx, c, t, sizeof(TX)) + lane);
+                if (BWD)
+                    h[r].load(reinterpret_cast<const TX*>(smem + C::HS + l * C::PITCH_X) +
+                              half(p.h, p.ldh, c, t - 1, sizeof(TX)) + lane);
             }
         }
-        if (WIDE && !full) {  // rows behind the last sequence: the identity
+        if (BWD && !WIDE && t0 == 0) {  // there is no row before the first
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (run * R + r == TT - 1) h[r].zero();
+        }
+        if (!full || (!WIDE && !here)) {  // rows behind the last sequence, channels that are none: the identity
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int i = run * R + r;
-                if (t0 + (BWD ? TT - 1 - i : i) >= valid) {
+                if (!here || t0 + (BWD ? TT - 1 - i : i) >= valid) {
                     b[r].zero();
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) a[r][j] = 0.f;  // exp(0) = 1
                 }
             }
         }
-        decays<R, VEC>(a);
+        decays(reinterpret_cast<float (&)[R * VEC]>(a));
         float A[VEC], B[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
@@ -553,7 +645,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         __syncthreads();
         if (*abort_s) break;
         const int ntile = misc[0];
-        if (tid == 0 && ntile >= 0) request(ntile);  // the stage has been read
+        if (ntile >= 0) request(ntile);  // the stage has been read
 
         // ---- the runs of each part, then the parts: the tile's composition
         auto fold = [&](auto cutting) {
@@ -588,9 +680,9 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             if (lane == 0) misc[2 + nb] = any;
         }
         __syncthreads();
-        if (many && tid < CC) {
-            float fa = 1.f, fb = 0.f;
-            bool cut_any = false;
+        float fa = 1.f, fb = 0.f;  // of the tile, in the threads of the first part
+        bool cut_any = false;
+        if (p.rows > 1 && tid < CC) {
 #pragma unroll
             for (int q = 0; q < C::PARTS; ++q) {
                 const float ra = pa[q * CC + pos], rb = pb[q * CC + pos];
@@ -602,6 +694,26 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                     fa *= ra;
                 }
             }
+        }
+        if (p.clustered) {  // the compositions of the cluster's tiles are read from their CTAs
+            float* ta = reinterpret_cast<float*>(smem + C::TA);
+            float* tb = reinterpret_cast<float*>(smem + C::TB);
+            if (tid < CC) {
+                ta[pos] = fa;
+                tb[pos] = fb;
+            }
+            if (tid == 0) misc[4] = cut_any;
+            cluster_meet();
+            met = true;
+            if (tid < CC) {
+                float carry = 0.f;
+                for (int k = 0; k < row; ++k) {
+                    const float ra = cluster_read(ta + pos, k), rb = cluster_read(tb + pos, k);
+                    carry = __float_as_int(cluster_read(misc + 4, k)) || k == 0 ? rb : fmaf(ra, carry, rb);
+                }
+                carry_s[pos] = carry;
+            }
+        } else if (many && tid < CC) {
             const int64_t pitch = 3 * CC;
             unsigned int* words = p.words + (int64_t)group * p.rows * pitch + pos;
             unsigned int* own = words + row * pitch;
@@ -630,7 +742,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         }
         // ---- the state that reaches each run
         auto walk = [&](auto cutting) {
-            float f = many ? carry_s[pos] : 0.f;
+            float f = p.rows > 1 ? carry_s[pos] : 0.f;
             for (int q = 0; q < part; ++q)
                 f = decltype(cutting)::value && part_cut(q) ? pb[q * CC + pos] : fmaf(pa[q * CC + pos], f, pb[q * CC + pos]);
 #pragma unroll
@@ -698,6 +810,11 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         tile = ntile;
     }
 
+    if (p.clustered) {
+        if (!met) cluster_meet();
+        cluster_meet();  // nobody's shared memory goes before all have read
+    }
+
     // sequences without a token pass their state on
     if (p.last) {
         for (int64_t n0 = (int64_t)blockIdx.x * C::THREADS + warp * 32; n0 < p.N; n0 += (int64_t)gridDim.x * C::THREADS) {
@@ -723,8 +840,13 @@ __global__ void linrec_clear_kernel(uint4* w, int64_t n) {
 
 // ---- workspace and launch ------------------------------------------------------------
 
+// Up to 8 tile rows whose tiles all fit on the GPU at once: clusters, one launch
+// and no workspace (512 tokens by 1024 channels).
+constexpr int kMaxCluster = 8, kMaxClusterTiles = 304;
+
 struct ScanLayout {
     int groups, rows;
+    bool clustered;
     size_t words, total;  // published words, bytes in all; 0 for a single row of tiles
 };
 
@@ -732,7 +854,8 @@ ScanLayout scan_layout(int64_t T, int D, int TT, int CC) {
     ScanLayout l{};
     l.groups = (D + CC - 1) / CC;
     l.rows = (int)((T + TT - 1) / TT);
-    if (l.rows <= 1) return l;
+    l.clustered = l.rows > 1 && l.rows <= kMaxCluster && (int64_t)l.groups * l.rows <= kMaxClusterTiles;
+    if (l.rows <= 1 || l.clustered) return l;
     l.words = (size_t)l.groups * l.rows * 3 * CC;
     l.total = (kHeadWords + l.words) * sizeof(unsigned);
     return l;
@@ -820,6 +943,7 @@ cudaError_t launch_tiles(LinrecParams p, void* ws, cudaStream_t s) {
     const ScanLayout l = scan_layout(p.T, p.D, C::TT, C::CC);
     p.groups = l.groups;
     p.rows = l.rows;
+    p.clustered = l.clustered;
     CUtensorMap mx{}, mg{}, mh{};
     if (WIDE && !(encode_rows<TX>(&mx, p.x, p.ldx, p.T, p.D, C::TT, C::CC) &&
                   encode_rows<TG>(&mg, p.g, p.ldg, p.T, p.D, C::TT, C::CC) &&
@@ -833,6 +957,21 @@ cudaError_t launch_tiles(LinrecParams p, void* ws, cudaStream_t s) {
         KernelTimer kt(BWD ? "linrec_bwd" : "linrec_fwd", s);
         kernel<<<(unsigned)tiles, C::THREADS, C::BYTES_SMEM, s>>>(mx, mg, mh, p);
         return cudaGetLastError();
+    }
+    if (l.clustered) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)tiles);
+        cfg.blockDim = dim3(C::THREADS);
+        cfg.dynamicSmemBytes = C::BYTES_SMEM;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)l.rows;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        KernelTimer kt(BWD ? "linrec_bwd" : "linrec_fwd", s);
+        return cudaLaunchKernelEx(&cfg, kernel, mx, mg, mh, p);
     }
     char* w = static_cast<char*>(ws);
     p.head = reinterpret_cast<unsigned int*>(w);
@@ -882,36 +1021,90 @@ struct StepParams {
     int N, D, num_slots, steps, commit;
 };
 
-template <typename TX, typename TG, typename TP>
-__global__ void linrec_step_kernel(StepParams p) {
-    const int c = blockIdx.x * blockDim.x + threadIdx.x;
+// VEC elements in one access (two for 8 fp32).
+template <typename T, int VEC> struct alignas(sizeof(T) * VEC < 16 ? sizeof(T) * VEC : 16) Pack {
+    T v[VEC];
+};
+
+// A thread owns VEC channels of a sequence and walks its tokens, those of the
+// next TOKENS steps loaded at once.  Bound by latency at decode sizes (the slot
+// and the sequence's place, then the rows), by memory at large ones.
+template <typename TX, typename TG, typename TP, int VEC>
+__global__ void __launch_bounds__(128) linrec_step_kernel(StepParams p) {
+    constexpr int TOKENS = VEC >= 8 ? 2 : 4;
+    const int c = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
     if (c >= p.D) return;
-    const TX* x = static_cast<const TX*>(p.x);
-    const TG* g = static_cast<const TG*>(p.g);
-    TX* y = static_cast<TX*>(p.y);
     for (int64_t n = blockIdx.y; n < p.N; n += gridDim.y) {
         const int slot = p.idx[n];
-        if (slot < 0 || slot >= p.num_slots) continue;
         const int64_t lo = max((int64_t)p.cu[n], (int64_t)0), hi = min((int64_t)p.cu[n + 1], p.T);
-        if (hi <= lo) continue;
-        TP* cell = static_cast<TP*>(p.pool) + (int64_t)slot * p.D + c;
-        TP* keep = p.states ? static_cast<TP*>(p.states) + n * p.steps * p.D + c : nullptr;
-        float h = to_f(*cell);
-        for (int64_t t = lo; t < hi; ++t) {
-            h = fmaf(decay(to_f(g[t * p.ldg + c])), h, to_f(x[t * p.ldx + c]));
-            y[t * p.ldy + c] = from_f<TX>(h);
-            if (keep && t - lo < p.steps) keep[(t - lo) * p.D] = from_f<TP>(h);
+        if (slot < 0 || slot >= p.num_slots || hi <= lo) continue;
+        Pack<TP, VEC>* cell = reinterpret_cast<Pack<TP, VEC>*>(static_cast<TP*>(p.pool) + (int64_t)slot * p.D + c);
+        const Pack<TP, VEC> before = *cell;
+        const TX* x = static_cast<const TX*>(p.x) + lo * p.ldx + c;
+        const TG* g = static_cast<const TG*>(p.g) + lo * p.ldg + c;
+        TX* y = static_cast<TX*>(p.y) + lo * p.ldy + c;
+        const int len = (int)(hi - lo), kept = p.states ? min(len, p.steps) : 0;
+        TP* keep = kept ? static_cast<TP*>(p.states) + n * p.steps * p.D + c : nullptr;
+        float h[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) h[j] = to_f(before.v[j]);
+        for (int t0 = 0; t0 < len; t0 += TOKENS) {
+            Pack<TX, VEC> xs[TOKENS];
+            Pack<TG, VEC> gs[TOKENS];
+#pragma unroll
+            for (int i = 0; i < TOKENS; ++i)
+                if (t0 + i < len) {
+                    xs[i] = *reinterpret_cast<const Pack<TX, VEC>*>(x + (t0 + i) * p.ldx);
+                    gs[i] = *reinterpret_cast<const Pack<TG, VEC>*>(g + (t0 + i) * p.ldg);
+                }
+#pragma unroll
+            for (int i = 0; i < TOKENS; ++i)
+                if (t0 + i < len) {
+                    Pack<TX, VEC> out;
+                    float a[VEC];
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) a[j] = to_f(gs[i].v[j]);
+                    exp_of(a, reduced_exp);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        h[j] = fmaf(a[j], h[j], to_f(xs[i].v[j]));
+                        out.v[j] = from_f<TX>(h[j]);
+                    }
+                    *reinterpret_cast<Pack<TX, VEC>*>(y + (t0 + i) * p.ldy) = out;
+                    if (t0 + i < kept) {
+                        Pack<TP, VEC> state;
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) state.v[j] = from_f<TP>(h[j]);
+                        *reinterpret_cast<Pack<TP, VEC>*>(keep + (int64_t)(t0 + i) * p.D) = state;
+                    }
+                }
         }
-        if (p.commit) *cell = from_f<TP>(h);
+        if (p.commit) {
+            Pack<TP, VEC> state;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) state.v[j] = from_f<TP>(h[j]);
+            *cell = state;
+        }
     }
+}
+
+template <typename TX, typename TG, typename TP, int VEC>
+cudaError_t launch_step_v(const StepParams& p, cudaStream_t s) {
+    const dim3 grid((p.D + 128 * VEC - 1) / (128 * VEC), p.N < 65535 ? p.N : 65535);
+    KernelTimer kt("linrec_step", s);
+    linrec_step_kernel<TX, TG, TP, VEC><<<grid, 128, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename TX, typename TG, typename TP>
 cudaError_t launch_step_t(const StepParams& p, cudaStream_t s) {
-    const dim3 grid((p.D + 127) / 128, p.N < 65535 ? p.N : 65535);
-    KernelTimer kt("linrec_step", s);
-    linrec_step_kernel<TX, TG, TP><<<grid, 128, 0, s>>>(p);
-    return cudaGetLastError();
+    if (p.D % 8 || !wide_rows<TX>(p.x, p.ldx, p.D) || !wide_rows<TG>(p.g, p.ldg, p.D) ||
+        !wide_rows<TX>(p.y, p.ldy, p.D))
+        return launch_step_v<TX, TG, TP, 1>(p, s);
+    // 8 channels per thread where that still gives every SM's schedulers work
+    const int64_t channels = (int64_t)p.N * p.D, full = (int64_t)sm_count() * 768;
+    return channels >= full * 8 ? launch_step_v<TX, TG, TP, 8>(p, s)
+         : channels >= full * 4 ? launch_step_v<TX, TG, TP, 4>(p, s) : launch_step_v<TX, TG, TP, 2>(p, s);
 }
 
 template <typename TX, typename TG>
