@@ -314,6 +314,8 @@ _CODES = {torch.bfloat16: GDR_BF16, torch.float32: GDR_F32}
 _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
 
 def _refuse(t, shape, dtype, device, what):
     if t.shape != shape:
@@ -345,6 +347,16 @@ def _rows(t, shape, dtype, device, what):
     return t.data_ptr(), row if rows > 1 else D
 
 
+def _like(t, shape, dtype, device):
+    """(tensor, address, row stride) of a new dense [rows, D] tensor; `t` has its shape."""
+    if t.dtype is dtype:
+        new = torch.empty_like(t)  # costs less than empty(); laid out as t where that is dense
+        if new.is_contiguous():
+            return new, new.data_ptr(), shape[1]
+    new = torch.empty(shape, dtype=dtype, device=device)
+    return new, new.data_ptr(), shape[1]
+
+
 def _code(dtype):
     c = _CODES.get(dtype)
     if c is None:
@@ -364,7 +376,7 @@ def _elsewhere(device, stream):
     """The context to enter first where a call does not run on the current
     device's current stream; None where it does."""
     if stream is None:
-        return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        return None if _current_device() == device.index else torch.cuda.device(device)
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
     return torch.cuda.stream(stream)
@@ -410,11 +422,14 @@ def linrec_fwd(x, g, cu_seqlens, *, initial_state=None, flags: int = 0, y=None, 
     hp = _dense(initial_state, state, _F32, dev, "initial_state")
     cp = _dense(cu_seqlens, (N + 1,), _I32, dev, "cu_seqlens")
     if y is None:
-        y = torch.empty(T, D, dtype=xt, device=dev)
-    yp, ys = _rows(y, shape, xt, dev, "y")
-    if final_state is None and output_final_state:
-        final_state = torch.empty(N, D, dtype=_F32, device=dev)
-    fp = _dense(final_state, state, _F32, dev, "final_state")
+        y, yp, ys = _like(x, shape, xt, dev)
+    else:
+        yp, ys = _rows(y, shape, xt, dev, "y")
+    if final_state is not None or not output_final_state:
+        fp = _dense(final_state, state, _F32, dev, "final_state")
+    else:
+        final_state = torch.empty(N, D, dtype=_F32, device=dev) if hp is None else torch.empty_like(initial_state)
+        fp = final_state.data_ptr()
     ws, wp, wn = _scratch(workspace, linrec_workspace_size(N, T, D, dtype=xc, gate_dtype=gc), dev)
     code = (_lib or load()).gdr_linrec_fwd(xp, xs, gp, gs, hp, cp, N, T, D, xc, gc, flags, yp, ys, fp, wp, wn,
                                            _current_handle(dev.index))
@@ -447,14 +462,18 @@ def linrec_bwd(dy, g, y, cu_seqlens, *, initial_state=None, d_final_state=None, 
     fp = _dense(d_final_state, state, _F32, dev, "d_final_state")
     cp = _dense(cu_seqlens, (N + 1,), _I32, dev, "cu_seqlens")
     if dx is None:
-        dx = torch.empty(T, D, dtype=xt, device=dev)
+        dx, xp, xs = _like(dy, shape, xt, dev)
+    else:
+        xp, xs = _rows(dx, shape, xt, dev, "dx")
     if dg is None:
-        dg = torch.empty(T, D, dtype=gt, device=dev)
-    xp, xs = _rows(dx, shape, xt, dev, "dx")
-    ap, as_ = _rows(dg, shape, gt, dev, "dg")
-    if d_initial_state is None and output_d_initial_state:
-        d_initial_state = torch.empty(N, D, dtype=_F32, device=dev)
-    ip = _dense(d_initial_state, state, _F32, dev, "d_initial_state")
+        dg, ap, as_ = _like(g, shape, gt, dev)
+    else:
+        ap, as_ = _rows(dg, shape, gt, dev, "dg")
+    if d_initial_state is not None or not output_d_initial_state:
+        ip = _dense(d_initial_state, state, _F32, dev, "d_initial_state")
+    else:
+        d_initial_state = torch.empty(N, D, dtype=_F32, device=dev) if hp is None else torch.empty_like(initial_state)
+        ip = d_initial_state.data_ptr()
     ws, wp, wn = _scratch(workspace, linrec_workspace_size(N, T, D, dtype=xc, gate_dtype=gc), dev)
     code = (_lib or load()).gdr_linrec_bwd(dp, ds, gp, gs, yp, ys, hp, fp, cp, N, T, D, xc, gc, flags, xp, xs, ap, as_,
                                            ip, wp, wn, _current_handle(dev.index))
@@ -491,8 +510,9 @@ def linrec_step(x, g, state_pool, state_indices, cu_seqlens, *, flags: int = GDR
         rows, steps = intermediate_states.shape[:2]
         bp = _dense(intermediate_states, (rows, steps, D), pt, dev, "intermediate_states")
     if y is None:
-        y = torch.empty(T, D, dtype=xt, device=dev)
-    yp, ys = _rows(y, shape, xt, dev, "y")
+        y, yp, ys = _like(x, shape, xt, dev)
+    else:
+        yp, ys = _rows(y, shape, xt, dev, "y")
     code = (_lib or load()).gdr_linrec_step(xp, xs, gp, gs, pp, _code(pt), slots, ip, cp, N, T, D, _code(xt), _code(gt),
                                             flags, yp, ys, bp, steps, _current_handle(dev.index))
     if code:
@@ -526,19 +546,23 @@ def rmsnorm_fwd(x, weight, *, residual=None, eps: float = 1e-6, y_dtype=None, sc
         groups = -(-D // scale_group) if scale_group > 0 else 1
         if scales is None:
             scales = torch.empty(M, groups, dtype=_F32, device=dev)
-        sp = _dense(scales, (M, groups), _F32, dev, "scales")
+            sp = scales.data_ptr()
+        else:
+            sp = _dense(scales, (M, groups), _F32, dev, "scales")
     else:
         yc = _CODES.get(y_dtype, -1)
         if scales is not None:
             raise ValueError("scales go with y_dtype torch.float8_e4m3fn only")
     if y is None:
-        y = torch.empty(M, D, dtype=y_dtype, device=dev)
-    yp, ys = _rows(y, shape, y_dtype, dev, "y")
+        y, yp, ys = _like(x, shape, y_dtype, dev)
+    else:
+        yp, ys = _rows(y, shape, y_dtype, dev, "y")
     if residual is not None:
         rp, rs = _rows(residual, shape, xt, dev, "residual")
         if residual_out is None:
-            residual_out = torch.empty(M, D, dtype=xt, device=dev)
-        op, os_ = _rows(residual_out, shape, xt, dev, "residual_out")
+            residual_out, op, os_ = _like(x, shape, xt, dev)
+        else:
+            op, os_ = _rows(residual_out, shape, xt, dev, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out without residual")
     else:
@@ -576,12 +600,13 @@ def rmsnorm_bwd(dy, s, weight, *, eps: float = 1e-6, d_residual_out=None, dx=Non
     wp = _dense(weight, (D,), _F32, dev, "weight")
     rp, rs = (None, 0) if d_residual_out is None else _rows(d_residual_out, shape, xt, dev, "d_residual_out")
     if dx is None:
-        dx = torch.empty(M, D, dtype=xt, device=dev)
-    xp, xs = _rows(dx, shape, xt, dev, "dx")
+        dx, xp, xs = _like(dy, shape, xt, dev)
+    else:
+        xp, xs = _rows(dx, shape, xt, dev, "dx")
     ws = kp = gp = None
     kn = 0
     if dweight is None and output_dweight:
-        dweight = torch.empty(D, dtype=_F32, device=dev)
+        dweight = torch.empty_like(weight)
     if dweight is not None:
         gp = _dense(dweight, (D,), _F32, dev, "dweight")
         ws, kp, kn = _scratch(workspace, rmsnorm_bwd_workspace_size(M, D), dev)
