@@ -333,20 +333,13 @@ __device__ __forceinline__ void publish(unsigned int* p, float f) {
     asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" :: "l"(p), "r"(v) : "memory");
 }
 
-// The state that reaches a tile of row `row` in one channel.  `w`: that channel's
-// words of row 0, rows `pitch` apart, fields `field` apart (state, A, B).  False
-// if a wait gave up.
-__device__ __forceinline__ bool look_back(const unsigned int* w, int row, int64_t pitch, int field, float& state,
-                                          const unsigned int* gave_up) {
-    constexpr int W = 4;
-    const uint64_t began = tc::globaltimer_ns();
-    unsigned spin = 0;
-    auto patience = [&]() {
-        return (++spin & 63) != 0 || (!peek(gave_up) && tc::globaltimer_ns() - began < tc::kWaitLimitNs);
-    };
-    // the nearest rows, all words at once
-    while (true) {
-        unsigned s[W], a[W], b[W];
+// The words of the rows left of `row` in one channel, nearest first.  `w`: that
+// channel's words of row 0, rows `pitch` apart, fields `field` apart (state, A, B).
+struct Neighbours {
+    static constexpr int W = 2;
+    unsigned s[W], a[W], b[W];
+
+    __device__ __forceinline__ void peek_at(const unsigned int* w, int row, int64_t pitch, int field) {
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             const unsigned int* q = w + max(row - 1 - i, 0) * pitch;
@@ -354,8 +347,13 @@ __device__ __forceinline__ bool look_back(const unsigned int* w, int row, int64_
             a[i] = peek(q + field);
             b[i] = peek(q + 2 * field);
         }
-        bool known = false, whole = true;
+    }
+    // Whether a state is among them with every map behind it; `whole`: every row is
+    // at least composed.
+    __device__ __forceinline__ bool reach(float& state, bool& whole) const {
+        bool known = false;
         float h = 0.f;
+        whole = true;
 #pragma unroll
         for (int i = W - 1; i >= 0; --i) {  // from the farthest: a state there starts anew, a map is applied
             if (s[i] != kNothing) {
@@ -367,15 +365,30 @@ __device__ __forceinline__ bool look_back(const unsigned int* w, int row, int64_
                 known = whole = false;
             }
         }
-        if (known) {
-            state = h;
-            return true;
-        }
-        if (whole && row > W) break;
+        state = h;
+        return known;
+    }
+};
+
+// The state that reaches a tile of row `row` in one channel, waited for.  False if
+// a wait gave up.
+__device__ __forceinline__ bool look_back(const unsigned int* w, int row, int64_t pitch, int field, float& state,
+                                          const unsigned int* gave_up) {
+    const uint64_t began = tc::globaltimer_ns();
+    unsigned spin = 0;
+    auto patience = [&]() {
+        return (++spin & 63) != 0 || (!peek(gave_up) && tc::globaltimer_ns() - began < tc::kWaitLimitNs);
+    };
+    while (true) {
+        Neighbours near;
+        bool whole;
+        near.peek_at(w, row, pitch, field);
+        if (near.reach(state, whole)) return true;
+        if (whole && row > Neighbours::W) break;
         if (!patience()) return false;
     }
     // further: the nearest state, then forward over the maps
-    int k = row - 1 - W;
+    int k = row - 1 - Neighbours::W;
     constexpr int V = 8;
     while (true) {
         unsigned s[V];
@@ -499,7 +512,6 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     const int64_t tiles = (int64_t)rows * p.groups;
 
     // tiles are taken in the order of the scan, all channel groups of a row first
-    auto take = [&]() -> int64_t { return many ? (int64_t)atomicAdd(p.head, 1u) : tiles; };
     auto token0 = [&](int tile) -> int {
         const int row = tile / p.groups;
         return (BWD ? rows - 1 - row : row) * TT;
@@ -528,7 +540,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     bool met = false;  // this CTA has been at its cluster's first meeting
     if (tid == 0) {
         int64_t t = blockIdx.x;  // one tile of each CTA: a row of the cluster, or a group of the only row
-        if (many) t = take();
+        if (many) t = atomicAdd(p.head, 1u);
         if (p.clustered) t = (int)(blockIdx.x % p.rows) < rows ? (int64_t)(blockIdx.x % p.rows) * p.groups + blockIdx.x / p.rows : tiles;
         misc[0] = t < tiles ? (int)t : -1;
     }
@@ -548,8 +560,8 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         const int c0 = group * CC + lc * VEC;
         const int* first = reinterpret_cast<int*>(smem + C::FIRST) + buf * TT;
         const int* last = reinterpret_cast<int*>(smem + C::LAST) + buf * TT;
-        int64_t next = tiles;
-        if (tid == 0) next = take();
+        unsigned next = 0xffffffffu;  // looked at after the composition: the counter's answer takes its time
+        if (many && tid == 0) next = atomicAdd(p.head, 1u);
         if (!WIDE) {
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (!tc::mbar_wait(mbar, buf, abort_s)) {
@@ -641,11 +653,18 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             cb[run * CC + lc] = B[0];
         }
         if (lc == 0) cut_s[run] = cut;
-        if (tid == 0) misc[0] = next < tiles ? (int)next : -1;
+        if (tid == 0) misc[0] = (int64_t)next < tiles ? (int)next : -1;
         __syncthreads();
         if (*abort_s) break;
         const int ntile = misc[0];
         if (ntile >= 0) request(ntile);  // the stage has been read
+
+        // The left neighbours' words are asked for before the fold, and looked at behind it.
+        constexpr int64_t pitch = 3 * CC;
+        unsigned int* words = p.words + (int64_t)group * p.rows * pitch + pos;
+        Neighbours near;
+        const bool looks = many && tid < CC && row > 0;
+        if (looks) near.peek_at(words, row, pitch, CC);
 
         // ---- the runs of each part, then the parts: the tile's composition
         auto fold = [&](auto cutting) {
@@ -672,14 +691,14 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 for (int i = q * C::RUNS_PART; i < (q + 1) * C::RUNS_PART; ++i) c |= cut_s[i];
             return c != 0;
         };
-        if (warp == C::WARPS - 1 && ntile >= 0) {  // while the others fold: the next tile's sequences
+        __syncthreads();
+        if (warp == C::WARPS - 1 && ntile >= 0) {  // while others look back: the next tile's sequences
             const int nb = buf ^ 1;
             const bool any = find_boundaries<TT, BWD>(p.cu, p.N, token0(ntile),
                                                       reinterpret_cast<int*>(smem + C::FIRST) + nb * TT,
                                                       reinterpret_cast<int*>(smem + C::LAST) + nb * TT, lane);
             if (lane == 0) misc[2 + nb] = any;
         }
-        __syncthreads();
         float fa = 1.f, fb = 0.f;  // of the tile, in the threads of the first part
         bool cut_any = false;
         if (p.rows > 1 && tid < CC) {
@@ -714,19 +733,18 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 carry_s[pos] = carry;
             }
         } else if (many && tid < CC) {
-            const int64_t pitch = 3 * CC;
-            unsigned int* words = p.words + (int64_t)group * p.rows * pitch + pos;
             unsigned int* own = words + row * pitch;
             const bool settled = cut_any || row == 0;  // the outgoing state does not depend on the incoming one
+            float carry = 0.f;
+            bool whole, known = looks && near.reach(carry, whole);
             if (settled) {
                 publish(own, fb);
-            } else {
+            } else if (!known) {
                 publish(own + CC, fa);
                 publish(own + 2 * CC, fb);
             }
-            float carry = 0.f;
-            if (row > 0) {
-                if (!look_back(words, row, pitch, CC, carry, p.head + 1)) {
+            if (looks) {
+                if (!known && !look_back(words, row, pitch, CC, carry, p.head + 1)) {
                     *abort_s = 1;
                     p.head[1] = 1;
                     atomicOr(p.err, kScanError);
