@@ -145,14 +145,25 @@ __device__ __forceinline__ void decays(float (&g)[N]) {
     }
 }
 
-// ---- VEC consecutive elements, kept as they are stored -------------------------
+// ---- a thread's VEC elements of a row, kept as they are stored ---------------------
+//
+// Eight elements are either neighbours, or (APART) two runs of four, APART elements
+// from one another: a warp's 16-byte accesses to fp32 rows in shared memory then
+// touch all banks in turn, and its stores whole sectors.
 
-template <typename T, int VEC> struct Row;
+template <typename T, int VEC, int APART> struct Row;
 
-template <> struct Row<__nv_bfloat16, 8> {
+template <int APART> struct Row<__nv_bfloat16, 8, APART> {
     uint4 v;
     __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        if (APART) {
+            const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + APART);
+            v = make_uint4(a.x, a.y, b.x, b.y);
+        } else {
+            v = *reinterpret_cast<const uint4*>(p);
+        }
+    }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -161,33 +172,46 @@ template <> struct Row<__nv_bfloat16, 8> {
             f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(tc::pack_bf16(f[0], f[1]), tc::pack_bf16(f[2], f[3]),
-                                                  tc::pack_bf16(f[4], f[5]), tc::pack_bf16(f[6], f[7]));
+    // `both`: whether the second run lies inside the tensor
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8], bool both) {
+        const uint2 a = make_uint2(tc::pack_bf16(f[0], f[1]), tc::pack_bf16(f[2], f[3]));
+        const uint2 b = make_uint2(tc::pack_bf16(f[4], f[5]), tc::pack_bf16(f[6], f[7]));
+        if (APART) {
+            *reinterpret_cast<uint2*>(p) = a;
+            if (both) *reinterpret_cast<uint2*>(p + APART) = b;
+        } else {
+            *reinterpret_cast<uint4*>(p) = make_uint4(a.x, a.y, b.x, b.y);
+        }
     }
 };
-template <> struct Row<float, 8> {
+template <int APART> struct Row<float, 8, APART> {
+    static constexpr int STEP = APART ? APART : 4;
     float4 a, b;
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void load(const float* p) {
-        a = reinterpret_cast<const float4*>(p)[0];
-        b = reinterpret_cast<const float4*>(p)[1];
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + STEP);
+    }
+    __device__ __forceinline__ void load(const float* p, bool both) {
+        a = *reinterpret_cast<const float4*>(p);
+        if (both) b = *reinterpret_cast<const float4*>(p + STEP);
     }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
         f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
     }
-    static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    static __device__ __forceinline__ void store(float* p, const float (&f)[8], bool both) {
+        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+        if (both) *reinterpret_cast<float4*>(p + STEP) = make_float4(f[4], f[5], f[6], f[7]);
     }
 };
-template <typename T> struct Row<T, 1> {
+template <typename T, int APART> struct Row<T, 1, APART> {
     T v;
     __device__ __forceinline__ void zero() { v = from_f<T>(0.f); }
     __device__ __forceinline__ void load(const T* p) { v = *p; }
+    __device__ __forceinline__ void load(const T* p, bool) { v = *p; }
     __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f(v); }
-    static __device__ __forceinline__ void store(T* p, const float (&f)[1]) { *p = from_f<T>(f[0]); }
+    static __device__ __forceinline__ void store(T* p, const float (&f)[1], bool) { *p = from_f<T>(f[0]); }
 };
 
 // One token of the scan: h <- a h + b, or h <- a (h + b) from the end.
@@ -260,8 +284,10 @@ template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
     static constexpr int FIRST = CARRY + CC * 4, LAST = FIRST + 2 * TT * 4, CUT = LAST + 2 * TT * 4;
     static constexpr int MISC = CUT + RUNS * 4, BYTES_SMEM = MISC + 64;
     static_assert(RUNS % PARTS == 0 && STAGE % 128 == 0 && TT <= 256, "tile shape");
-    // the 16-byte halves of a thread's 8 channels are kept CC / 2 apart: its float4
-    // accesses then touch all banks in turn
+    // fp32 rows: a thread's channels are 4 lane .. + 3 and CC / 2 further; else 8 lane .. + 7
+    static constexpr int APART = WIDE && (sizeof(TX) == 4 || sizeof(TG) == 4) ? CC / 2 : 0;
+    static __device__ __forceinline__ int channel(int lane) { return APART ? lane * 4 : lane * VEC; }
+    // where channel j of a thread lies in the arrays of compositions: apart in any case
     static __device__ __forceinline__ int place(int lane, int j) {
         return WIDE ? (j < 4 ? lane * 4 + j : CC / 2 + lane * 4 + j - 4) : lane;
     }
@@ -480,7 +506,7 @@ __global__ void __launch_bounds__(Tile<TX, TG, BWD, WIDE>::THREADS, Tile<TX, TG,
 linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g,
                    const __grid_constant__ CUtensorMap map_h, const __grid_constant__ LinrecParams p) {
     using C = Tile<TX, TG, BWD, WIDE>;
-    constexpr int VEC = C::VEC, CC = C::CC, R = C::R, TT = C::TT;
+    constexpr int VEC = C::VEC, CC = C::CC, R = C::R, TT = C::TT, APART = C::APART;
     extern __shared__ __align__(1024) unsigned char smem[];
     TX* xs = reinterpret_cast<TX*>(smem + C::XS);
     TG* gs = reinterpret_cast<TG*>(smem + C::GS);
@@ -557,11 +583,12 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     for (int it = 0; tile >= 0; ++it) {
         const int buf = it & 1;
         const int row = tile / p.groups, group = tile - row * p.groups, t0 = (BWD ? rows - 1 - row : row) * TT;
-        const int c0 = group * CC + lc * VEC;
+        const int lane_c = C::channel(lc), c0 = group * CC + lane_c;
         const int* first = reinterpret_cast<int*>(smem + C::FIRST) + buf * TT;
         const int* last = reinterpret_cast<int*>(smem + C::LAST) + buf * TT;
         unsigned next = 0xffffffffu;  // looked at after the composition: the counter's answer takes its time
-        if (many && tid == 0) next = atomicAdd(p.head, 1u);
+        if (many && tid == 0)
+            asm volatile("atom.relaxed.gpu.global.add.u32 %0, [%1], 1;" : "=r"(next) : "l"(p.head) : "memory");
         if (!WIDE) {
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (!tc::mbar_wait(mbar, buf, abort_s)) {
@@ -570,21 +597,21 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         }
         __syncthreads();
         const bool bounded = misc[2 + buf] != 0;  // sequences begin or end in the tile
-        const bool here = c0 < p.D;
+        const bool here = c0 < p.D, both = !APART || c0 + APART < p.D;  // the thread's channels are the tensors'
 
         // ---- into registers, and the composition of the thread's run
         float a[R][VEC];
-        Row<TX, VEC> b[R], h[BWD ? R : 1];
+        Row<TX, VEC, APART> b[R], h[BWD ? R : 1];
         const bool full = t0 + TT <= valid;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int i = run * R + r, l = BWD ? TT - 1 - i : i;
             if (WIDE) {  // what lies outside the tensors has been filled with zeros
-                Row<TG, VEC> gr;
-                gr.load(gs + l * CC + lc * VEC);
+                Row<TG, VEC, APART> gr;
+                gr.load(gs + l * CC + lane_c);
                 gr.get(a[r]);
-                b[r].load(xs + l * CC + lc * VEC);
-                if (BWD) h[r].load(hs + l * CC + lc * VEC);
+                b[r].load(xs + l * CC + lane_c);
+                if (BWD) h[r].load(hs + l * CC + lane_c);
             } else {
                 const int c = group * CC, t = t0 + l;
                 a[r][0] = to_f(*(reinterpret_cast<const TG*>(smem + C::GS + l * C::PITCH_G) +
@@ -619,9 +646,9 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             B[j] = 0.f;
         }
         auto start_state = [&](int n, float (&f)[VEC]) {
-            Row<float, VEC> s;
+            Row<float, VEC, APART> s;
             s.zero();
-            if (p.start && here) s.load(p.start + (int64_t)n * p.D + c0);
+            if (p.start && here) s.load(p.start + (int64_t)n * p.D + c0, both);
             s.get(f);
         };
         int cut = 0;
@@ -804,23 +831,23 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                     if (BWD) {
                         float before[VEC];
                         add<VEC>(f, s);  // lam
-                        Row<TX, VEC>::store(out, f);
+                        Row<TX, VEC, APART>::store(out, f, both);
                         product<VEC>(s, a[r], f);  // mu
                         h[r].get(before);
                         if (decltype(cutting)::value && n_last >= 0) {  // before the first token: h0
-                            Row<float, VEC> z;
+                            Row<float, VEC, APART> z;
                             z.zero();
-                            if (p.h0) z.load(p.h0 + (int64_t)n_last * p.D + c0);
+                            if (p.h0) z.load(p.h0 + (int64_t)n_last * p.D + c0, both);
                             z.get(before);
                         }
                         product<VEC>(before, before, s);
-                        Row<TG, VEC>::store(dg, before);
+                        Row<TG, VEC, APART>::store(dg, before, both);
                     } else {
                         advance<BWD, VEC>(s, a[r], f);
-                        Row<TX, VEC>::store(out, s);
+                        Row<TX, VEC, APART>::store(out, s, both);
                     }
                     if (decltype(cutting)::value && n_last >= 0 && p.last)
-                        Row<float, VEC>::store(p.last + (int64_t)n_last * p.D + c0, s);
+                        Row<float, VEC, APART>::store(p.last + (int64_t)n_last * p.D + c0, s, both);
                 }
             };
             bounded || !full ? evaluate(std::true_type()) : evaluate(std::false_type());
