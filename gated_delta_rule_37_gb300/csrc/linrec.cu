@@ -145,23 +145,30 @@ __device__ __forceinline__ void decays(float (&g)[N]) {
     }
 }
 
-// ---- a thread's VEC elements of a row, kept as they are stored ---------------------
+// ---- a thread's 8 elements of a row, kept as they are stored -----------------------
 //
-// Eight elements are either neighbours, or (APART) two runs of four, APART elements
-// from one another: a warp's 16-byte accesses to fp32 rows in shared memory then
-// touch all banks in turn, and its stores whole sectors.
+// kNext: neighbours, one 16-byte access of bf16.  kHalves: two runs of four, 32
+// elements from one another: a warp's 16-byte accesses to fp32 rows in shared memory
+// then touch all banks in turn, and its stores whole sectors.  kEvery8: every eighth
+// element, for rows of any alignment.  `n` counts those that lie inside the tensor.
 
-template <typename T, int VEC, int APART> struct Row;
+enum Layout { kNext, kHalves, kEvery8 };
+constexpr int kHalf = 32;
 
-template <int APART> struct Row<__nv_bfloat16, 8, APART> {
+template <typename T, Layout L> struct Row;
+
+template <Layout L> struct Row<__nv_bfloat16, L> {
     uint4 v;
     __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-        if (APART) {
-            const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + APART);
+        if (L == kNext) {
+            v = *reinterpret_cast<const uint4*>(p);
+        } else if (L == kHalves) {
+            const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + kHalf);
             v = make_uint4(a.x, a.y, b.x, b.y);
         } else {
-            v = *reinterpret_cast<const uint4*>(p);
+            const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
+            v = make_uint4(u[0] | u[8] << 16, u[16] | u[24] << 16, u[32] | u[40] << 16, u[48] | u[56] << 16);
         }
     }
     __device__ __forceinline__ void get(float (&f)[8]) const {
@@ -172,125 +179,116 @@ template <int APART> struct Row<__nv_bfloat16, 8, APART> {
             f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
-    // `both`: whether the second run lies inside the tensor
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8], bool both) {
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8], int n) {
         const uint2 a = make_uint2(tc::pack_bf16(f[0], f[1]), tc::pack_bf16(f[2], f[3]));
         const uint2 b = make_uint2(tc::pack_bf16(f[4], f[5]), tc::pack_bf16(f[6], f[7]));
-        if (APART) {
-            *reinterpret_cast<uint2*>(p) = a;
-            if (both) *reinterpret_cast<uint2*>(p + APART) = b;
-        } else {
+        if (L == kNext) {
             *reinterpret_cast<uint4*>(p) = make_uint4(a.x, a.y, b.x, b.y);
+        } else if (L == kHalves) {
+            *reinterpret_cast<uint2*>(p) = a;
+            if (n > 4) *reinterpret_cast<uint2*>(p + kHalf) = b;
+        } else {
+            const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+            unsigned short* u = reinterpret_cast<unsigned short*>(p);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) u[8 * j] = (unsigned short)(w[j / 2] >> (16 * (j & 1)));
         }
     }
 };
-template <int APART> struct Row<float, 8, APART> {
-    static constexpr int STEP = APART ? APART : 4;
-    float4 a, b;
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void load(const float* p) {
-        a = *reinterpret_cast<const float4*>(p);
-        b = *reinterpret_cast<const float4*>(p + STEP);
+template <Layout L> struct Row<float, L> {
+    float v[8];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
     }
-    __device__ __forceinline__ void load(const float* p, bool both) {
-        a = *reinterpret_cast<const float4*>(p);
-        if (both) b = *reinterpret_cast<const float4*>(p + STEP);
+    __device__ __forceinline__ void load(const float* p, int n = 8) {
+        if (L == kEvery8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) v[j] = p[8 * j];
+        } else {
+            const float4 a = *reinterpret_cast<const float4*>(p);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            if (n > 4) {
+                const float4 b = *reinterpret_cast<const float4*>(p + (L == kHalves ? kHalf : 4));
+                v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+            }
+        }
     }
     __device__ __forceinline__ void get(float (&f)[8]) const {
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = v[j];
     }
-    static __device__ __forceinline__ void store(float* p, const float (&f)[8], bool both) {
-        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-        if (both) *reinterpret_cast<float4*>(p + STEP) = make_float4(f[4], f[5], f[6], f[7]);
+    static __device__ __forceinline__ void store(float* p, const float (&f)[8], int n) {
+        if (L == kEvery8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) p[8 * j] = f[j];
+        } else {
+            *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+            if (n > 4) *reinterpret_cast<float4*>(p + (L == kHalves ? kHalf : 4)) = make_float4(f[4], f[5], f[6], f[7]);
+        }
     }
 };
-template <typename T, int APART> struct Row<T, 1, APART> {
-    T v;
-    __device__ __forceinline__ void zero() { v = from_f<T>(0.f); }
-    __device__ __forceinline__ void load(const T* p) { v = *p; }
-    __device__ __forceinline__ void load(const T* p, bool) { v = *p; }
-    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f(v); }
-    static __device__ __forceinline__ void store(T* p, const float (&f)[1], bool) { *p = from_f<T>(f[0]); }
-};
+
+__device__ __forceinline__ float2 pair(const float (&f)[8], int i) { return make_float2(f[2 * i], f[2 * i + 1]); }
+__device__ __forceinline__ void put(float (&f)[8], int i, float2 v) {
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+}
 
 // One token of the scan: h <- a h + b, or h <- a (h + b) from the end.
-template <bool BWD, int VEC>
-__device__ __forceinline__ void advance(float (&h)[VEC], const float (&a)[VEC], const float (&b)[VEC]) {
-    if (VEC == 1) {
-        h[0] = BWD ? a[0] * (h[0] + b[0]) : fmaf(a[0], h[0], b[0]);
-    } else {
+template <bool BWD>
+__device__ __forceinline__ void advance(float (&h)[8], const float (&a)[8], const float (&b)[8]) {
 #pragma unroll
-        for (int j = 0; j < VEC; j += 2) {
-            const int k = (j + 1) % VEC;
-            const float2 a2 = make_float2(a[j], a[k]), b2 = make_float2(b[j], b[k]);
-            float2 h2 = make_float2(h[j], h[k]);
-            h2 = BWD ? __fmul2_rn(a2, __fadd2_rn(h2, b2)) : __ffma2_rn(a2, h2, b2);
-            h[j] = h2.x;
-            h[k] = h2.y;
-        }
-    }
+    for (int i = 0; i < 4; ++i)
+        put(h, i, BWD ? __fmul2_rn(pair(a, i), __fadd2_rn(pair(h, i), pair(b, i)))
+                      : __ffma2_rn(pair(a, i), pair(h, i), pair(b, i)));
 }
-
-template <int VEC>
-__device__ __forceinline__ void add(float (&f)[VEC], const float (&s)[VEC]) {
-    if (VEC == 1) {
-        f[0] += s[0];
-    } else {
+__device__ __forceinline__ void add(float (&f)[8], const float (&s)[8]) {
 #pragma unroll
-        for (int j = 0; j < VEC; j += 2) {
-            const float2 v = __fadd2_rn(make_float2(f[j], f[(j + 1) % VEC]), make_float2(s[j], s[(j + 1) % VEC]));
-            f[j] = v.x;
-            f[(j + 1) % VEC] = v.y;
-        }
-    }
+    for (int i = 0; i < 4; ++i) put(f, i, __fadd2_rn(pair(f, i), pair(s, i)));
 }
-template <int VEC>
-__device__ __forceinline__ void product(float (&o)[VEC], const float (&a)[VEC], const float (&b)[VEC]) {
-    if (VEC == 1) {
-        o[0] = a[0] * b[0];
-    } else {
+__device__ __forceinline__ void product(float (&o)[8], const float (&a)[8], const float (&b)[8]) {
 #pragma unroll
-        for (int j = 0; j < VEC; j += 2) {
-            const float2 v = __fmul2_rn(make_float2(a[j], a[(j + 1) % VEC]), make_float2(b[j], b[(j + 1) % VEC]));
-            o[j] = v.x;
-            o[(j + 1) % VEC] = v.y;
-        }
-    }
+    for (int i = 0; i < 4; ++i) put(o, i, __fmul2_rn(pair(a, i), pair(b, i)));
 }
 
 // ---- the tile kernel --------------------------------------------------------------
 
-// WIDE: 8 channels per thread, 64 per tile, staged by TMA (aligned rows).
-// Otherwise one channel per thread, 32 per tile, staged by 4-byte asynchronous
-// copies: fp32 rows are aligned to that, and a bf16 row's segment is copied from
-// the word that it begins in, one word more, and read from where it lies.
+// 64 channels per tile, 8 per thread.  WIDE: aligned rows, staged by TMA.  Otherwise
+// rows are staged by 16-byte asynchronous copies of the aligned blocks around each
+// row's segment, and read from where it lies in them.
 template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
     static constexpr int THREADS = 256, CTAS = 2, WARPS = THREADS / 32;
-    static constexpr int VEC = WIDE ? 8 : 1, LANES = WIDE ? 8 : 32, CC = VEC * LANES;
-    static constexpr int RUNS = WARPS * 32 / LANES;          // runs of R tokens
-    // A token takes a register per channel for its decay and one (8 bf16 channels: a
-    // half) for each of b and h; R of them is what fits beside the rest.
-    static constexpr int R = !WIDE ? (BWD ? 16 : 24) : sizeof(TX) == 2 ? (BWD ? 4 : 5) : (BWD ? 3 : 4);
+    static constexpr int LANES = 8, CC = 64, RUNS = THREADS / LANES;  // runs of R tokens
+    // A token takes 8 registers for its decays and 4 or 8 for each of b and h as
+    // stored; R of them is what fits beside the rest at two CTAs per SM.
+    static constexpr int R = sizeof(TX) == 2 ? (BWD ? 4 : 5) : (BWD ? 3 : 4);
     static constexpr int TT = RUNS * R;
     static constexpr int PARTS = THREADS / CC, RUNS_PART = RUNS / PARTS;  // the fold over runs, in parts
+    static constexpr Layout LAYOUT = !WIDE ? kEvery8 : sizeof(TX) == 4 || sizeof(TG) == 4 ? kHalves : kNext;
     // bytes of a token in the stage, a row of x / h and one of g
-    static constexpr int PITCH_X = WIDE ? CC * (int)sizeof(TX) : sizeof(TX) == 4 ? CC * 4 : CC * 2 + 8;
-    static constexpr int PITCH_G = WIDE ? CC * (int)sizeof(TG) : sizeof(TG) == 4 ? CC * 4 : CC * 2 + 8;
+    static constexpr int PITCH_X = CC * (int)sizeof(TX) + (WIDE ? 0 : 16), PITCH_G = CC * (int)sizeof(TG) + (WIDE ? 0 : 16);
     // shared memory (bytes)
     static constexpr int XS = 0, GS = XS + TT * PITCH_X, HS = GS + TT * PITCH_G, STAGE = HS + (BWD ? TT * PITCH_X : 0);
     static constexpr int CA = STAGE, CB = CA + RUNS * CC * 4, PA = CB + RUNS * CC * 4, PB = PA + PARTS * CC * 4;
     static constexpr int TA = PB + PARTS * CC * 4, TB = TA + CC * 4, CARRY = TB + CC * 4;
     static constexpr int FIRST = CARRY + CC * 4, LAST = FIRST + 2 * TT * 4, CUT = LAST + 2 * TT * 4;
     static constexpr int MISC = CUT + RUNS * 4, BYTES_SMEM = MISC + 64;
-    static_assert(RUNS % PARTS == 0 && STAGE % 128 == 0 && TT <= 256, "tile shape");
-    // fp32 rows: a thread's channels are 4 lane .. + 3 and CC / 2 further; else 8 lane .. + 7
-    static constexpr int APART = WIDE && (sizeof(TX) == 4 || sizeof(TG) == 4) ? CC / 2 : 0;
-    static __device__ __forceinline__ int channel(int lane) { return APART ? lane * 4 : lane * VEC; }
-    // where channel j of a thread lies in the arrays of compositions: apart in any case
-    static __device__ __forceinline__ int place(int lane, int j) {
-        return WIDE ? (j < 4 ? lane * 4 + j : CC / 2 + lane * 4 + j - 4) : lane;
+    static_assert(RUNS % PARTS == 0 && STAGE % 128 == 0 && TT <= 256 && CC == 2 * kHalf && CC == 8 * LANES, "tile shape");
+    // the first of a lane's channels
+    static __device__ __forceinline__ int channel(int lane) {
+        return LAYOUT == kNext ? lane * 8 : LAYOUT == kHalves ? lane * 4 : lane;
     }
+    // how many of its channels lie below D, from its first one
+    static __device__ __forceinline__ int inside(int c, int D) {
+        return LAYOUT == kNext ? (c < D ? 8 : 0) : LAYOUT == kHalves ? (c < D ? 4 : 0) + (c + kHalf < D ? 4 : 0)
+                                                                     : min(max((D - c + 7) / 8, 0), 8);
+    }
+    // where a lane's channels lie in the arrays of compositions: two runs of four
+    static __device__ __forceinline__ int place(int lane, int half) { return lane * 4 + half * kHalf; }
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c, int t, uint32_t mbar) {
@@ -299,42 +297,42 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         :: "r"(dst), "l"(map), "r"(c), "r"(t), "r"(mbar) : "memory");
 }
 
-// One row's segment of n <= 32 channels at `from` into a stage row, by one warp.
-// The first and last rows of a bf16 tensor may have words that reach outside it:
-// those are copied element by element.
-template <typename T>
-__device__ __forceinline__ void copy_segment(uint32_t dst, const T* from, int n, bool edge, const T* base, const T* end,
-                                             int lane) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(from);
-    if (sizeof(T) == 4) {
-        if (lane < n)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + lane * 4), "l"(at + lane * 4) : "memory");
+// The segments [c, c + 64) of the rows [t0, t0 + TT) below `rows`, `back` rows further
+// up in the tensor, into the stage.  A warp takes every WARPS-th row: these lie a
+// multiple of 16 bytes from one another whatever the stride, so that its lanes'
+// 16-byte blocks keep their places.  Blocks that reach outside the tensor (near its
+// ends only) are copied element by element.
+template <typename T, int TT, int WARPS, int PITCH>
+__device__ __forceinline__ void copy_rows(unsigned char* stage, const void* tensor, int64_t ld, int64_t T_all, int D,
+                                          int t0, int rows, int back, int c, int warp, int lane) {
+    constexpr int ES = (int)sizeof(T), AT_ONCE = ES == 4 ? 1 : 2;  // rows that a warp's lanes cover
+    static_assert(WARPS * ES % 16 == 0, "rows of a warp are 16-byte blocks apart");
+    const int sub = lane / (32 / AT_ONCE), ln = lane % (32 / AT_ONCE), bytes = min(64, D - c) * ES;
+    const uintptr_t base = reinterpret_cast<uintptr_t>(tensor), end = base + ((T_all - 1) * ld + D) * ES;
+    int l = warp + sub * WARPS;
+    uintptr_t at = base + ((t0 + l - back) * ld + c) * ES;  // the row's segment
+    const int shift = (int)(at & 15);
+    if (16 * ln >= shift + bytes) return;
+    const int most = min(TT, rows - t0);
+    const int64_t step = (int64_t)AT_ONCE * WARPS * ld * ES;
+    uint32_t dst = tc::smem_u32(stage) + l * PITCH + 16 * ln;
+    uintptr_t block = at - shift + 16 * ln;
+    if (ld > 0 && t0 >= 32 && t0 + TT + 32 <= T_all) {
+#pragma unroll 4
+        for (; l < most; l += AT_ONCE * WARPS, block += step, dst += AT_ONCE * WARPS * PITCH)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(block) : "memory");
         return;
     }
-    const uintptr_t word = (at & ~uintptr_t(3)) + 4 * lane;
-    if (word >= at + 2 * n) return;
-    if (!edge || (word >= reinterpret_cast<uintptr_t>(base) && word + 4 <= reinterpret_cast<uintptr_t>(end))) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + 4 * lane), "l"(word) : "memory");
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; k += 2)
-            if (word + k >= at && word + k < at + 2 * n)
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + 4 * lane + k),
-                             "h"(*reinterpret_cast<const unsigned short*>(word + k)) : "memory");
+    for (; l < most; l += AT_ONCE * WARPS, at += step, block += step, dst += AT_ONCE * WARPS * PITCH) {
+        if (t0 + l < back) continue;
+        if (block >= base && block + 16 <= end) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(block) : "memory");
+        } else {
+            for (int k = 0; k < 16; k += ES)
+                if (block + k >= at && block + k < at + bytes)
+                    *reinterpret_cast<T*>(stage + l * PITCH + 16 * ln + k) = *reinterpret_cast<const T*>(block + k);
+        }
     }
-}
-// The rows [t0, t0 + TT) below `rows` of a [T, D] tensor into the stage, a warp
-// per row; `back` rows further up in the tensor.
-template <typename T, int TT, int WARPS, int PITCH>
-__device__ __forceinline__ void copy_rows(uint32_t stage, const void* tensor, int64_t ld, int64_t T_all, int D, int t0,
-                                          int rows, int back, int c, int warp, int lane) {
-    const T* base = static_cast<const T*>(tensor);
-    const T* end = base + (T_all - 1) * ld + D;
-    const int n = min(32, D - c), last = (int)T_all - 1 + back;
-    const T* from = base + (int64_t)(t0 + warp - back) * ld + c;
-    stage += warp * PITCH;
-    for (int t = t0 + warp; t < min(t0 + TT, rows); t += WARPS, from += WARPS * ld, stage += WARPS * PITCH)
-        if (t >= back) copy_segment(stage, from, n, t == back || t == last || ld == 0, base, end, lane);
 }
 
 __device__ __forceinline__ void cluster_meet() {
@@ -506,11 +504,9 @@ __global__ void __launch_bounds__(Tile<TX, TG, BWD, WIDE>::THREADS, Tile<TX, TG,
 linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g,
                    const __grid_constant__ CUtensorMap map_h, const __grid_constant__ LinrecParams p) {
     using C = Tile<TX, TG, BWD, WIDE>;
-    constexpr int VEC = C::VEC, CC = C::CC, R = C::R, TT = C::TT, APART = C::APART;
+    constexpr int CC = C::CC, R = C::R, TT = C::TT;
+    constexpr Layout L = C::LAYOUT;
     extern __shared__ __align__(1024) unsigned char smem[];
-    TX* xs = reinterpret_cast<TX*>(smem + C::XS);
-    TG* gs = reinterpret_cast<TG*>(smem + C::GS);
-    TX* hs = reinterpret_cast<TX*>(smem + C::HS);
     float* ca = reinterpret_cast<float*>(smem + C::CA);
     float* cb = reinterpret_cast<float*>(smem + C::CB);
     float* pa = reinterpret_cast<float*>(smem + C::PA);
@@ -552,15 +548,13 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             if (BWD) tma_load_2d(tc::smem_u32(smem + C::HS), &map_h, c, t0 - 1, mbar);  // row t - 1 beside token t
             return;
         }
-        copy_rows<TX, TT, C::WARPS, C::PITCH_X>(tc::smem_u32(smem + C::XS), p.x, p.ldx, p.T, p.D, t0, valid, 0, c, warp, lane);
-        copy_rows<TG, TT, C::WARPS, C::PITCH_G>(tc::smem_u32(smem + C::GS), p.g, p.ldg, p.T, p.D, t0, valid, 0, c, warp, lane);
-        if (BWD)
-            copy_rows<TX, TT, C::WARPS, C::PITCH_X>(tc::smem_u32(smem + C::HS), p.h, p.ldh, p.T, p.D, t0, valid, 1, c, warp,
-                                                    lane);
+        copy_rows<TX, TT, C::WARPS, C::PITCH_X>(smem + C::XS, p.x, p.ldx, p.T, p.D, t0, valid, 0, c, warp, lane);
+        copy_rows<TG, TT, C::WARPS, C::PITCH_G>(smem + C::GS, p.g, p.ldg, p.T, p.D, t0, valid, 0, c, warp, lane);
+        if (BWD) copy_rows<TX, TT, C::WARPS, C::PITCH_X>(smem + C::HS, p.h, p.ldh, p.T, p.D, t0, valid, 1, c, warp, lane);
     };
-    // bf16 rows staged by words: the half word that row t's segment begins in
-    auto half = [&](const void* tensor, int64_t ld, int c, int t, int size) {
-        return size == 4 ? 0 : (int)((reinterpret_cast<uintptr_t>(tensor) >> 1) + c + ((int)ld & t)) & 1;
+    // where row t's segment from channel c on begins in its blocks
+    auto shift = [&](const void* tensor, int64_t ld, int c, int t, int size) {
+        return WIDE ? 0 : (int)(reinterpret_cast<uintptr_t>(tensor) + c * size + (t & 15) * ((int)ld & 15) * size) & 15;
     };
 
     bool met = false;  // this CTA has been at its cluster's first meeting
@@ -583,7 +577,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     for (int it = 0; tile >= 0; ++it) {
         const int buf = it & 1;
         const int row = tile / p.groups, group = tile - row * p.groups, t0 = (BWD ? rows - 1 - row : row) * TT;
-        const int lane_c = C::channel(lc), c0 = group * CC + lane_c;
+        const int lane_c = C::channel(lc), c0 = group * CC + lane_c, inside = C::inside(c0, p.D);
         const int* first = reinterpret_cast<int*>(smem + C::FIRST) + buf * TT;
         const int* last = reinterpret_cast<int*>(smem + C::LAST) + buf * TT;
         unsigned next = 0xffffffffu;  // looked at after the composition: the counter's answer takes its time
@@ -597,58 +591,58 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         }
         __syncthreads();
         const bool bounded = misc[2 + buf] != 0;  // sequences begin or end in the tile
-        const bool here = c0 < p.D, both = !APART || c0 + APART < p.D;  // the thread's channels are the tensors'
 
         // ---- into registers, and the composition of the thread's run
-        float a[R][VEC];
-        Row<TX, VEC, APART> b[R], h[BWD ? R : 1];
+        float a[R][8];
+        Row<TX, L> b[R], h[BWD ? R : 1];
         const bool full = t0 + TT <= valid;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int i = run * R + r, l = BWD ? TT - 1 - i : i;
-            if (WIDE) {  // what lies outside the tensors has been filled with zeros
-                Row<TG, VEC, APART> gr;
-                gr.load(gs + l * CC + lane_c);
-                gr.get(a[r]);
-                b[r].load(xs + l * CC + lane_c);
-                if (BWD) h[r].load(hs + l * CC + lane_c);
-            } else {
-                const int c = group * CC, t = t0 + l;
-                a[r][0] = to_f(*(reinterpret_cast<const TG*>(smem + C::GS + l * C::PITCH_G) +
-                                 half(p.g, p.ldg, c, t, sizeof(TG)) + lane));
-                b[r].load(reinterpret_cast<const TX*>(smem + C::XS + l * C::PITCH_X) + half(p.x, p.ldx, c, t, sizeof(TX)) + lane);
-                if (BWD)
-                    h[r].load(reinterpret_cast<const TX*>(smem + C::HS + l * C::PITCH_X) +
-                              half(p.h, p.ldh, c, t - 1, sizeof(TX)) + lane);
+        for (int r = 0; r < R; ++r) {  // TMA has filled with zeros what lies outside the tensors
+            const int i = run * R + r, l = BWD ? TT - 1 - i : i, t = t0 + l, c = group * CC;
+            Row<TG, L> gr;
+            gr.load(reinterpret_cast<const TG*>(smem + C::GS + l * C::PITCH_G + shift(p.g, p.ldg, c, t, sizeof(TG))) + lane_c);
+            gr.get(a[r]);
+            b[r].load(reinterpret_cast<const TX*>(smem + C::XS + l * C::PITCH_X + shift(p.x, p.ldx, c, t, sizeof(TX))) + lane_c);
+            if (BWD)
+                h[r].load(reinterpret_cast<const TX*>(smem + C::HS + l * C::PITCH_X + shift(p.h, p.ldh, c, t - 1, sizeof(TX))) +
+                          lane_c);
+        }
+        if (!WIDE) {  // nothing was staged for channels that are none, and there is no row before the first
+            if (inside < 8) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j >= inside) a[r][j] = 0.f;
+            }
+            if (BWD && t0 == 0) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    if (run * R + r == TT - 1) h[r].zero();
             }
         }
-        if (BWD && !WIDE && t0 == 0) {  // there is no row before the first
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (run * R + r == TT - 1) h[r].zero();
-        }
-        if (!full || (!WIDE && !here)) {  // rows behind the last sequence, channels that are none: the identity
+        if (!full) {  // rows behind the last sequence: the identity
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int i = run * R + r;
-                if (!here || t0 + (BWD ? TT - 1 - i : i) >= valid) {
+                if (t0 + (BWD ? TT - 1 - i : i) >= valid) {
                     b[r].zero();
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) a[r][j] = 0.f;  // exp(0) = 1
+                    for (int j = 0; j < 8; ++j) a[r][j] = 0.f;  // exp(0) = 1
                 }
             }
         }
-        decays(reinterpret_cast<float (&)[R * VEC]>(a));
-        float A[VEC], B[VEC];
+        decays(reinterpret_cast<float (&)[R * 8]>(a));
+        float A[8], B[8];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
+        for (int j = 0; j < 8; ++j) {
             A[j] = 1.f;
             B[j] = 0.f;
         }
-        auto start_state = [&](int n, float (&f)[VEC]) {
-            Row<float, VEC, APART> s;
+        auto start_state = [&](int n, float (&f)[8]) {
+            Row<float, L> s;
             s.zero();
-            if (p.start && here) s.load(p.start + (int64_t)n * p.D + c0, both);
+            if (p.start && inside) s.load(p.start + (int64_t)n * p.D + c0, inside);
             s.get(f);
         };
         int cut = 0;
@@ -656,7 +650,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         auto compose = [&](auto cutting) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                float f[VEC];
+                float f[8];
                 b[r].get(f);
                 if (decltype(cutting)::value) {
                     const int n = first[run * R + r];
@@ -665,19 +659,16 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                         cut = 1;
                     }
                 }
-                advance<BWD, VEC>(B, a[r], f);
-                product<VEC>(A, A, a[r]);
+                advance<BWD>(B, a[r], f);
+                product(A, A, a[r]);
             }
         };
         bounded ? compose(std::true_type()) : compose(std::false_type());
-        if (WIDE) {
-            *reinterpret_cast<float4*>(ca + run * CC + C::place(lc, 0)) = make_float4(A[0], A[1 % VEC], A[2 % VEC], A[3 % VEC]);
-            *reinterpret_cast<float4*>(ca + run * CC + C::place(lc, 4)) = make_float4(A[4 % VEC], A[5 % VEC], A[6 % VEC], A[7 % VEC]);
-            *reinterpret_cast<float4*>(cb + run * CC + C::place(lc, 0)) = make_float4(B[0], B[1 % VEC], B[2 % VEC], B[3 % VEC]);
-            *reinterpret_cast<float4*>(cb + run * CC + C::place(lc, 4)) = make_float4(B[4 % VEC], B[5 % VEC], B[6 % VEC], B[7 % VEC]);
-        } else {
-            ca[run * CC + lc] = A[0];
-            cb[run * CC + lc] = B[0];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int at = run * CC + C::place(lc, k);
+            *reinterpret_cast<float4*>(ca + at) = make_float4(A[4 * k], A[4 * k + 1], A[4 * k + 2], A[4 * k + 3]);
+            *reinterpret_cast<float4*>(cb + at) = make_float4(B[4 * k], B[4 * k + 1], B[4 * k + 2], B[4 * k + 3]);
         }
         if (lc == 0) cut_s[run] = cut;
         if (tid == 0) misc[0] = (int64_t)next < tiles ? (int)next : -1;
@@ -800,15 +791,12 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         };
         bounded ? walk(std::true_type()) : walk(std::false_type());
         __syncthreads();
-        if (here) {
-            float s[VEC];
-            if (WIDE) {
-                const float4 u = *reinterpret_cast<const float4*>(ca + run * CC + C::place(lc, 0));
-                const float4 v = *reinterpret_cast<const float4*>(ca + run * CC + C::place(lc, 4));
-                s[0] = u.x; s[1 % VEC] = u.y; s[2 % VEC] = u.z; s[3 % VEC] = u.w;
-                s[4 % VEC] = v.x; s[5 % VEC] = v.y; s[6 % VEC] = v.z; s[7 % VEC] = v.w;
-            } else {
-                s[0] = ca[run * CC + lc];
+        if (inside) {
+            float s[8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float4 u = *reinterpret_cast<const float4*>(ca + run * CC + C::place(lc, k));
+                s[4 * k] = u.x; s[4 * k + 1] = u.y; s[4 * k + 2] = u.z; s[4 * k + 3] = u.w;
             }
             // ---- every token from its state
             const int64_t t_first = t0 + (BWD ? TT - 1 - run * R : run * R), dir = BWD ? -1 : 1;
@@ -826,28 +814,28 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                             if (n >= 0) start_state(n, s);
                         }
                     }
-                    float f[VEC];
+                    float f[8];
                     b[r].get(f);
                     if (BWD) {
-                        float before[VEC];
-                        add<VEC>(f, s);  // lam
-                        Row<TX, VEC, APART>::store(out, f, both);
-                        product<VEC>(s, a[r], f);  // mu
+                        float before[8];
+                        add(f, s);  // lam
+                        Row<TX, L>::store(out, f, inside);
+                        product(s, a[r], f);  // mu
                         h[r].get(before);
                         if (decltype(cutting)::value && n_last >= 0) {  // before the first token: h0
-                            Row<float, VEC, APART> z;
+                            Row<float, L> z;
                             z.zero();
-                            if (p.h0) z.load(p.h0 + (int64_t)n_last * p.D + c0, both);
+                            if (p.h0) z.load(p.h0 + (int64_t)n_last * p.D + c0, inside);
                             z.get(before);
                         }
-                        product<VEC>(before, before, s);
-                        Row<TG, VEC, APART>::store(dg, before, both);
+                        product(before, before, s);
+                        Row<TG, L>::store(dg, before, inside);
                     } else {
-                        advance<BWD, VEC>(s, a[r], f);
-                        Row<TX, VEC, APART>::store(out, s, both);
+                        advance<BWD>(s, a[r], f);
+                        Row<TX, L>::store(out, s, inside);
                     }
                     if (decltype(cutting)::value && n_last >= 0 && p.last)
-                        Row<float, VEC, APART>::store(p.last + (int64_t)n_last * p.D + c0, s, both);
+                        Row<float, L>::store(p.last + (int64_t)n_last * p.D + c0, s, inside);
                 }
             };
             bounded || !full ? evaluate(std::true_type()) : evaluate(std::false_type());
