@@ -131,10 +131,10 @@ __device__ __forceinline__ void exp_of(float (&g)[N], float2 (*f)(float2)) {
 // polynomial is asked once, by the warp as a whole.
 template <int N>
 __device__ __forceinline__ void decays(float (&g)[N]) {
-    float most = 0.f;
+    float most[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < N; ++j) most = fmaxf(most, fabsf(g[j]));
-    if (__any_sync(0xffffffffu, most > kTaylor)) {
+    for (int j = 0; j < N; ++j) most[j % 4] = fmaxf(most[j % 4], fabsf(g[j]));
+    if (__any_sync(0xffffffffu, fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) > kTaylor)) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const float far = expf(g[j]), near = taylor_exp(g[j]);
@@ -262,10 +262,11 @@ __device__ __forceinline__ void product(float (&o)[8], const float (&a)[8], cons
 // row's segment, and read from where it lies in them.
 template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
     static constexpr int THREADS = 256, CTAS = 2, WARPS = THREADS / 32;
+    static constexpr int COPIERS = WARPS - 2;  // warps that issue bulk copies, while the others look back
     static constexpr int LANES = 8, CC = 64, RUNS = THREADS / LANES;  // runs of R tokens
     // A token takes 8 registers for its decays and 4 or 8 for each of b and h as
     // stored; R of them is what fits beside the rest at two CTAs per SM.
-    static constexpr int R = sizeof(TX) == 2 ? (BWD ? 4 : 5) : (BWD ? 3 : 4);
+    static constexpr int R = sizeof(TX) == 2 ? (BWD ? (WIDE ? 5 : 4) : WIDE ? 7 : 6) : (BWD ? 3 : 5);
     static constexpr int TT = RUNS * R;
     static constexpr int PARTS = THREADS / CC, RUNS_PART = RUNS / PARTS;  // the fold over runs, in parts
     static constexpr Layout LAYOUT = !WIDE ? kEvery8 : sizeof(TX) == 4 || sizeof(TG) == 4 ? kHalves : kNext;
@@ -278,6 +279,7 @@ template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
     static constexpr int FIRST = CARRY + CC * 4, LAST = FIRST + 2 * TT * 4, CUT = LAST + 2 * TT * 4;
     static constexpr int MISC = CUT + RUNS * 4, BYTES_SMEM = MISC + 64;
     static_assert(RUNS % PARTS == 0 && STAGE % 128 == 0 && TT <= 256 && CC == 2 * kHalf && CC == 8 * LANES, "tile shape");
+    static_assert(CTAS * (BYTES_SMEM + 1024) <= 228 * 1024, "shared memory of the CTAs of an SM");
     // the first of a lane's channels
     static __device__ __forceinline__ int channel(int lane) {
         return LAYOUT == kNext ? lane * 8 : LAYOUT == kHalves ? lane * 4 : lane;
@@ -297,42 +299,32 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         :: "r"(dst), "l"(map), "r"(c), "r"(t), "r"(mbar) : "memory");
 }
 
-// The segments [c, c + 64) of the rows [t0, t0 + TT) below `rows`, `back` rows further
-// up in the tensor, into the stage.  A warp takes every WARPS-th row: these lie a
-// multiple of 16 bytes from one another whatever the stride, so that its lanes'
-// 16-byte blocks keep their places.  Blocks that reach outside the tensor (near its
-// ends only) are copied element by element.
-template <typename T, int TT, int WARPS, int PITCH>
-__device__ __forceinline__ void copy_rows(unsigned char* stage, const void* tensor, int64_t ld, int64_t T_all, int D,
-                                          int t0, int rows, int back, int c, int warp, int lane) {
-    constexpr int ES = (int)sizeof(T), AT_ONCE = ES == 4 ? 1 : 2;  // rows that a warp's lanes cover
-    static_assert(WARPS * ES % 16 == 0, "rows of a warp are 16-byte blocks apart");
-    const int sub = lane / (32 / AT_ONCE), ln = lane % (32 / AT_ONCE), bytes = min(64, D - c) * ES;
+// The segment [c, c + 64) of one row of a tensor into its stage row: the 16-byte
+// blocks around it by one bulk copy, and what of them lies outside the tensor (in
+// rows near its ends) left out, the elements there copied one by one.
+template <typename T>
+__device__ __forceinline__ void copy_segment(unsigned char* dst, const void* tensor, int64_t ld, int64_t T_all, int D,
+                                             int64_t row, int c, uint32_t mbar) {
+    constexpr int ES = (int)sizeof(T);
     const uintptr_t base = reinterpret_cast<uintptr_t>(tensor), end = base + ((T_all - 1) * ld + D) * ES;
-    int l = warp + sub * WARPS;
-    uintptr_t at = base + ((t0 + l - back) * ld + c) * ES;  // the row's segment
-    const int shift = (int)(at & 15);
-    if (16 * ln >= shift + bytes) return;
-    const int most = min(TT, rows - t0);
-    const int64_t step = (int64_t)AT_ONCE * WARPS * ld * ES;
-    uint32_t dst = tc::smem_u32(stage) + l * PITCH + 16 * ln;
-    uintptr_t block = at - shift + 16 * ln;
-    if (ld > 0 && t0 >= 32 && t0 + TT + 32 <= T_all) {
-#pragma unroll 4
-        for (; l < most; l += AT_ONCE * WARPS, block += step, dst += AT_ONCE * WARPS * PITCH)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(block) : "memory");
-        return;
+    const uintptr_t at = base + (row * ld + c) * ES, stop = at + min(64, D - c) * ES;
+    const uintptr_t first = at & ~uintptr_t(15);  // where dst begins
+    uintptr_t lo = first, hi = (stop + 15) & ~uintptr_t(15);
+    if (lo < base) lo = (base + 15) & ~uintptr_t(15);
+    if (hi > end) hi = end & ~uintptr_t(15);
+    if (hi > lo) {
+        const uint32_t bytes = (uint32_t)(hi - lo);
+        asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(mbar), "r"(bytes) : "memory");
+        tc::bulk_g2s(tc::smem_u32(dst) + (uint32_t)(lo - first), reinterpret_cast<const void*>(lo), bytes, mbar);
+    } else {
+        lo = hi = stop;
     }
-    for (; l < most; l += AT_ONCE * WARPS, at += step, block += step, dst += AT_ONCE * WARPS * PITCH) {
-        if (t0 + l < back) continue;
-        if (block >= base && block + 16 <= end) {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(block) : "memory");
+    for (uintptr_t e = at; e < stop; e += ES)
+        if (e < lo || e >= hi) {
+            *reinterpret_cast<T*>(dst + (e - first)) = *reinterpret_cast<const T*>(e);
         } else {
-            for (int k = 0; k < 16; k += ES)
-                if (block + k >= at && block + k < at + bytes)
-                    *reinterpret_cast<T*>(stage + l * PITCH + 16 * ln + k) = *reinterpret_cast<const T*>(block + k);
+            e = hi - ES;
         }
-    }
 }
 
 __device__ __forceinline__ void cluster_meet() {
@@ -524,11 +516,10 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     const bool many = p.rows > 1 && !p.clustered;
 
     if (tid == 0) {
-        tc::mbar_init(mbar, 1);
+        tc::mbar_init(mbar, WIDE ? 1 : 32 * C::COPIERS);
         tc::mbar_fence_init();
         *abort_s = 0;
     }
-    if (many) tc::grid_dep_wait();  // the workspace's head and flags have been cleared
     const int valid = min((int64_t)max(p.cu[p.N], 0), p.T);
     const int rows = (valid + TT - 1) / TT;  // tile rows that hold a sequence's token
     const int64_t tiles = (int64_t)rows * p.groups;
@@ -538,24 +529,29 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         const int row = tile / p.groups;
         return (BWD ? rows - 1 - row : row) * TT;
     };
-    auto request = [&](int tile) {  // the tile's rows into the stage; all threads call it
-        if (WIDE && tid != 0) return;
+    auto request = [&](int tile) {  // the tile's rows into the stage; one thread, or if not WIDE the copiers
         const int c = tile % p.groups * CC, t0 = token0(tile);
-        if (WIDE) {
+        if constexpr (WIDE) {
             tc::mbar_arrive_tx(mbar, C::STAGE);
             tma_load_2d(tc::smem_u32(smem + C::XS), &map_x, c, t0, mbar);
             tma_load_2d(tc::smem_u32(smem + C::GS), &map_g, c, t0, mbar);
             if (BWD) tma_load_2d(tc::smem_u32(smem + C::HS), &map_h, c, t0 - 1, mbar);  // row t - 1 beside token t
-            return;
+        } else {
+            for (int l = warp - 2 + C::COPIERS * lane; l < min(TT, valid - t0); l += 32 * C::COPIERS) {
+                const int64_t t = t0 + l;
+                copy_segment<TX>(smem + C::XS + l * C::PITCH_X, p.x, p.ldx, p.T, p.D, t, c, mbar);
+                copy_segment<TG>(smem + C::GS + l * C::PITCH_G, p.g, p.ldg, p.T, p.D, t, c, mbar);
+                if (BWD && t > 0) copy_segment<TX>(smem + C::HS + l * C::PITCH_X, p.h, p.ldh, p.T, p.D, t - 1, c, mbar);
+            }
+            tc::mbar_arrive(mbar);
         }
-        copy_rows<TX, TT, C::WARPS, C::PITCH_X>(smem + C::XS, p.x, p.ldx, p.T, p.D, t0, valid, 0, c, warp, lane);
-        copy_rows<TG, TT, C::WARPS, C::PITCH_G>(smem + C::GS, p.g, p.ldg, p.T, p.D, t0, valid, 0, c, warp, lane);
-        if (BWD) copy_rows<TX, TT, C::WARPS, C::PITCH_X>(smem + C::HS, p.h, p.ldh, p.T, p.D, t0, valid, 1, c, warp, lane);
     };
     // where row t's segment from channel c on begins in its blocks
     auto shift = [&](const void* tensor, int64_t ld, int c, int t, int size) {
         return WIDE ? 0 : (int)(reinterpret_cast<uintptr_t>(tensor) + c * size + (t & 15) * ((int)ld & 15) * size) & 15;
     };
+
+    if (many) tc::grid_dep_wait();  // the workspace has been cleared
 
     bool met = false;  // this CTA has been at its cluster's first meeting
     if (tid == 0) {
@@ -567,7 +563,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     __syncthreads();
     int tile = misc[0];
     __syncthreads();
-    if (tile >= 0) request(tile);
+    if (tile >= 0 && (WIDE ? tid == 0 : warp >= 2)) request(tile);
     if (tile >= 0 && warp == C::WARPS - 1) {
         const bool any = find_boundaries<TT, BWD>(p.cu, p.N, token0(tile), reinterpret_cast<int*>(smem + C::FIRST),
                                                   reinterpret_cast<int*>(smem + C::LAST), lane);
@@ -583,9 +579,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         unsigned next = 0xffffffffu;  // looked at after the composition: the counter's answer takes its time
         if (many && tid == 0)
             asm volatile("atom.relaxed.gpu.global.add.u32 %0, [%1], 1;" : "=r"(next) : "l"(p.head) : "memory");
-        if (!WIDE) {
-            asm volatile("cp.async.wait_all;" ::: "memory");
-        } else if (!tc::mbar_wait(mbar, buf, abort_s)) {
+        if (!tc::mbar_wait(mbar, buf, abort_s)) {
             *abort_s = 1;
             atomicOr(p.err, kScanError);
         }
@@ -675,7 +669,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         __syncthreads();
         if (*abort_s) break;
         const int ntile = misc[0];
-        if (ntile >= 0) request(ntile);  // the stage has been read
+        if (WIDE && tid == 0 && ntile >= 0) request(ntile);  // the stage has been read
 
         // The left neighbours' words are asked for before the fold, and looked at behind it.
         constexpr int64_t pitch = 3 * CC;
@@ -717,6 +711,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                                                       reinterpret_cast<int*>(smem + C::LAST) + nb * TT, lane);
             if (lane == 0) misc[2 + nb] = any;
         }
+        if (!WIDE && warp >= 2 && ntile >= 0) request(ntile);  // and its rows, in many small copies
         float fa = 1.f, fb = 0.f;  // of the tile, in the threads of the first part
         bool cut_any = false;
         if (p.rows > 1 && tid < CC) {
@@ -773,7 +768,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         }
         __syncthreads();
         if (*abort_s) {
-            if (WIDE && tid == 0 && ntile >= 0) tc::mbar_wait_copies(mbar, buf ^ 1);
+            if (tid == 0 && ntile >= 0) tc::mbar_wait_copies(mbar, buf ^ 1);
             break;
         }
         // ---- the state that reaches each run

@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rmsnorm_fwd_kernel(NormParams 
 // Forward on any rows: one element at a time, CH per thread, neighbours in
 // neighbouring threads.
 template <typename T, int CH, bool FP8>
-__global__ void __launch_bounds__(kMaxThreads, 1) rmsnorm_fwd_any_kernel(NormParams p) {
+__global__ void __launch_bounds__(kMaxThreads, CH <= 8 ? 2 : 1) rmsnorm_fwd_any_kernel(NormParams p) {
     __shared__ float2 exchange[2][kMaxThreads / 32];
     __shared__ int amax_s[FP8 ? 1024 : 1];
     const int tpr = p.tpr, slots = blockDim.x / tpr, slot = threadIdx.x / tpr, l = threadIdx.x % tpr;
@@ -455,7 +455,7 @@ int norm_parts(int64_t M) { return (int)(M < kMaxParts ? M : kMaxParts); }
 // columns in every row and sums dw in registers; one [D] part per CTA goes to
 // memory.
 template <typename T, int CH>
-__global__ void __launch_bounds__(kMaxThreads, 1) rmsnorm_bwd_kernel(NormBwdParams p) {
+__global__ void __launch_bounds__(kMaxThreads, CH <= 2 ? 2 : 1) rmsnorm_bwd_kernel(NormBwdParams p) {
     __shared__ float2 exchange[2][kMaxThreads / 32];
     extern __shared__ float dw_s[];
     const int tpr = p.tpr, slots = blockDim.x / tpr, slot = threadIdx.x / tpr, l = threadIdx.x % tpr;
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) rmsnorm_bwd_ring_kernel
 
 // The same on any rows: one element at a time.
 template <typename T, int CH>
-__global__ void __launch_bounds__(kMaxThreads, 1) rmsnorm_bwd_any_kernel(NormBwdParams p) {
+__global__ void __launch_bounds__(kMaxThreads, CH <= 8 ? 2 : 1) rmsnorm_bwd_any_kernel(NormBwdParams p) {
     __shared__ float2 exchange[2][kMaxThreads / 32];
     extern __shared__ float dw_s[];
     const int tpr = p.tpr, slots = blockDim.x / tpr, slot = threadIdx.x / tpr, l = threadIdx.x % tpr;
