@@ -266,7 +266,7 @@ template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
     static constexpr int LANES = 8, CC = 64, RUNS = THREADS / LANES;  // runs of R tokens
     // A token takes 8 registers for its decays and 4 or 8 for each of b and h as
     // stored; R of them is what fits beside the rest at two CTAs per SM.
-    static constexpr int R = sizeof(TX) == 2 ? (BWD ? (WIDE ? 5 : 4) : WIDE ? 7 : 6) : (BWD ? 3 : 5);
+    static constexpr int R = sizeof(TX) == 2 ? (BWD ? (WIDE ? 5 : 4) : WIDE && sizeof(TG) == 2 ? 7 : 6) : (BWD ? 3 : 5);
     static constexpr int TT = RUNS * R;
     static constexpr int PARTS = THREADS / CC, RUNS_PART = RUNS / PARTS;  // the fold over runs, in parts
     static constexpr Layout LAYOUT = !WIDE ? kEvery8 : sizeof(TX) == 4 || sizeof(TG) == 4 ? kHalves : kNext;
@@ -626,13 +626,15 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 }
             }
         }
-        decays(reinterpret_cast<float (&)[R * 8]>(a));
+        // The run's decay is the exponential of its gates' sum: the product of its
+        // tokens' decays would carry the rounding of each, and 32 runs do so after it.
         float A[8], B[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            A[j] = 1.f;
-            B[j] = 0.f;
-        }
+        for (int j = 0; j < 8; ++j) A[j] = B[j] = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) add(A, a[r]);
+        decays(A);
+        decays(reinterpret_cast<float (&)[R * 8]>(a));
         auto start_state = [&](int n, float (&f)[8]) {
             Row<float, L> s;
             s.zero();
@@ -654,7 +656,6 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                     }
                 }
                 advance<BWD>(B, a[r], f);
-                product(A, A, a[r]);
             }
         };
         bounded ? compose(std::true_type()) : compose(std::false_type());

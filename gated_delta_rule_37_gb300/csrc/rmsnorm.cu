@@ -749,7 +749,13 @@ __global__ void rmsnorm_dw_kernel(const float* __restrict__ partial, int parts, 
     }
 }
 
+// A single part is written as dw itself.
+void place_parts(NormBwdParams& p) {
+    if (p.parts == 1) p.partial = p.dw;
+}
+
 cudaError_t launch_dw(const NormBwdParams& p, cudaStream_t s) {
+    if (p.parts == 1) return cudaSuccess;
     KernelTimer kt("rmsnorm_dw", s);
     return launch_dependent(rmsnorm_dw_kernel, dim3((p.D + 31) / 32), dim3(512), 0, s, p.partial, p.parts, p.D, p.dw);
 }
@@ -759,6 +765,7 @@ cudaError_t launch_bwd_ch(NormBwdParams p, cudaStream_t s) {
     const int block = p.tpr > 256 ? p.tpr : 256, slots = block / p.tpr;
     const int64_t want = (p.M + slots - 1) / slots;
     p.parts = norm_parts(want);
+    place_parts(p);
     const size_t smem = slots > 1 ? (size_t)p.tpr * CH * (WIDE ? 8 : 1) * sizeof(float) : 0;
     {
         KernelTimer kt("rmsnorm_bwd", s);
@@ -788,6 +795,7 @@ cudaError_t launch_bwd_ring(NormBwdParams p, cudaStream_t s) {
     if (!p.err) return cudaErrorInitializationError;
     const int64_t want = (p.M + slots - 1) / slots, most = (int64_t)CTAS * sm_count();
     p.parts = norm_parts(want < most ? want : most);
+    place_parts(p);
     {
         KernelTimer kt("rmsnorm_bwd", s);
         kernel<<<p.parts, THREADS, p.stages * stage, s>>>(p);
