@@ -137,6 +137,32 @@ int check_device() {
 
 int set_ok() { return ok(); }
 
+int launch_result(cudaError_t e, const char* what) { return launch_status(e, what); }
+
+int check_rows(const char* name, const void* p, int64_t stride, int64_t least, unsigned esize) {
+    if (!p) return fail(GDR_ERR_INVALID_ARG, "null pointer argument (%s)", name);
+    if (reinterpret_cast<uintptr_t>(p) & (esize - 1))
+        return fail(GDR_ERR_INVALID_ARG, "%s not aligned to its element", name);
+    if (stride < least) return fail(GDR_ERR_INVALID_ARG, "%s: row stride %lld too small", name, (long long)stride);
+    return GDR_OK;
+}
+
+int check_aligned16(const char* name, const void* p) {
+    return aligned16(p) ? GDR_OK : fail(GDR_ERR_INVALID_ARG, "%s not 16-byte aligned", name);
+}
+
+int sm_count() {
+    static std::atomic<int> known{0};
+    int n = known.load(std::memory_order_relaxed);
+    if (n) return n;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+        return 1;
+    known.store(n, std::memory_order_relaxed);
+    return n;
+}
+
 int set_last_error(int code, const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);

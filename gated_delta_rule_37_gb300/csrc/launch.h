@@ -129,6 +129,19 @@ int set_ok();
 // else a status with its message set.
 int check_device();
 
+// The status of a launch, with its message set.
+int launch_result(cudaError_t e, const char* what);
+
+// A tensor of rows: present, aligned to its element of `esize` bytes, its row
+// stride (elements) at least `least`.  GDR_OK or a status with its message set.
+int check_rows(const char* name, const void* p, int64_t stride, int64_t least, unsigned esize);
+
+// GDR_OK if `p` (NULL included) is 16-byte aligned, else a status with its message set.
+int check_aligned16(const char* name, const void* p);
+
+// Multiprocessors of the GPU.
+int sm_count();
+
 // Device error word (set by bounded device waits that give up).
 unsigned int* device_error_word();
 

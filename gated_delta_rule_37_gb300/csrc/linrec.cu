@@ -328,7 +328,7 @@ __device__ __forceinline__ void copy_segment(unsigned char* dst, const void* ten
 }
 
 __device__ __forceinline__ void cluster_meet() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ float cluster_read(const void* own, unsigned rank) {
     uint32_t at;
@@ -944,31 +944,20 @@ bool wide_rows(const void* p, int64_t ld, int D) {
            (uint64_t)ld * sizeof(T) < (1ull << 40);
 }
 
-int sm_count() {
-    static std::atomic<int> known{0};
-    int n = known.load(std::memory_order_relaxed);
-    if (n) return n;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-        return 1;
-    known.store(n, std::memory_order_relaxed);
-    return n;
-}
-
 template <typename TX, typename TG, bool BWD, bool WIDE>
 cudaError_t launch_tiles(LinrecParams p, void* ws, cudaStream_t s) {
     using C = Tile<TX, TG, BWD, WIDE>;
     auto kernel = linrec_tile_kernel<TX, TG, BWD, WIDE>;
+    // at every call: the attribute belongs to the context
+    cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES_SMEM);
     static std::atomic<int> resident{0};  // CTAs per SM
     int per_sm = resident.load(std::memory_order_relaxed);
-    if (!per_sm) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES_SMEM);
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, C::THREADS, C::BYTES_SMEM);
-        if (e != cudaSuccess) return e;
-        if (per_sm < 1) return cudaErrorInvalidConfiguration;
-        resident.store(per_sm, std::memory_order_relaxed);
+    if (set == cudaSuccess && !per_sm) {
+        set = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, C::THREADS, C::BYTES_SMEM);
+        if (set == cudaSuccess && per_sm < 1) set = cudaErrorInvalidConfiguration;
+        if (set == cudaSuccess) resident.store(per_sm, std::memory_order_relaxed);
     }
+    if (set != cudaSuccess) return set;
     const ScanLayout l = scan_layout(p.T, p.D, C::TT, C::CC);
     p.groups = l.groups;
     p.rows = l.rows;
@@ -1217,23 +1206,18 @@ int check_sizes(int N, int64_t T, int D, int dtype, int gate_dtype) {
     // token numbers are 32-bit in the kernels, a tile's beyond the last token included
     if (T > 0x7fffff00LL) return set_last_error(GDR_ERR_UNSUPPORTED, "T_total (%lld) above 2^31 - 256", (long long)T);
     if (N > 0x7fffffff / 2) return set_last_error(GDR_ERR_UNSUPPORTED, "N too large");
+    if (D > 1 << 24) return set_last_error(GDR_ERR_UNSUPPORTED, "D (%d) above 2^24", D);
     if (T > 0 && N == 0) return set_last_error(GDR_ERR_INVALID_ARG, "T_total > 0 with N == 0");
     return GDR_OK;
 }
 
-// A token tensor: present, aligned to its element, its stride in range.
-int check_rows(const char* name, const void* p, int64_t stride, int D, int dtype, bool written) {
-    if (!p) return set_last_error(GDR_ERR_INVALID_ARG, "null pointer argument (%s)", name);
-    if (reinterpret_cast<uintptr_t>(p) & (dtype == GDR_BF16 ? 1u : 3u))
-        return set_last_error(GDR_ERR_INVALID_ARG, "%s not aligned to its element", name);
-    if (stride < (written ? D : 0))
-        return set_last_error(GDR_ERR_INVALID_ARG, "%s: row stride %lld too small", name, (long long)stride);
-    return GDR_OK;
-}
+unsigned element(int dtype) { return dtype == GDR_BF16 ? 2 : 4; }
 
-int check_state(const char* name, const void* p) {
-    if (reinterpret_cast<uintptr_t>(p) & 15u)
-        return set_last_error(GDR_ERR_INVALID_ARG, "%s not 16-byte aligned", name);
+// cu_seqlens and state_indices.
+int check_ints(const char* name, const void* p) {
+    if (!p) return set_last_error(GDR_ERR_INVALID_ARG, "null pointer argument (%s)", name);
+    if (reinterpret_cast<uintptr_t>(p) & 3u)
+        return set_last_error(GDR_ERR_INVALID_ARG, "%s not 4-byte aligned", name);
     return GDR_OK;
 }
 
@@ -1248,17 +1232,12 @@ int check_workspace(int N, int64_t T, int D, int dtype, int gate_dtype, const vo
     return GDR_OK;
 }
 
-int launched(cudaError_t e, const char* what) {
-    if (e != cudaSuccess) return set_last_error(GDR_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
-    return set_ok();
-}
-
 // No tokens at all: every sequence's last state is its first.
 int pass_states(const float* start, float* last, int N, int D, cudaStream_t s) {
     if (N == 0 || !last) return set_ok();
     if (int rc = check_device()) return rc;
     const size_t bytes = sizeof(float) * (size_t)N * D;
-    return launched(start ? cudaMemcpyAsync(last, start, bytes, cudaMemcpyDeviceToDevice, s)
+    return launch_result(start ? cudaMemcpyAsync(last, start, bytes, cudaMemcpyDeviceToDevice, s)
                           : cudaMemsetAsync(last, 0, bytes, s), "empty recurrence");
 }
 
@@ -1288,14 +1267,14 @@ int gdr_linrec_fwd(const void* x, int64_t x_stride, const void* g, int64_t g_str
     if (int rc = check_sizes(N, T_total, D, dtype, gate_dtype)) return rc;
     if (flags & ~GDR_VALIDATE)
         return set_last_error(GDR_ERR_INVALID_ARG, "unsupported flags 0x%x for gdr_linrec_fwd", flags);
-    if (int rc = check_state("initial_state", initial_state)) return rc;
-    if (int rc = check_state("final_state", final_state)) return rc;
+    if (int rc = check_aligned16("initial_state", initial_state)) return rc;
+    if (int rc = check_aligned16("final_state", final_state)) return rc;
     cudaStream_t s = (cudaStream_t)stream;
     if (T_total == 0) return pass_states(initial_state, final_state, N, D, s);
-    if (int rc = check_rows("x", x, x_stride, D, dtype, false)) return rc;
-    if (int rc = check_rows("g", g, g_stride, D, gate_dtype, false)) return rc;
-    if (int rc = check_rows("y", y, y_stride, D, dtype, true)) return rc;
-    if (!cu_seqlens) return set_last_error(GDR_ERR_INVALID_ARG, "null pointer argument (cu_seqlens)");
+    if (int rc = check_rows("x", x, x_stride, 0, element(dtype))) return rc;
+    if (int rc = check_rows("g", g, g_stride, 0, element(gate_dtype))) return rc;
+    if (int rc = check_rows("y", y, y_stride, D, element(dtype))) return rc;
+    if (int rc = check_ints("cu_seqlens", cu_seqlens)) return rc;
     if (int rc = check_workspace(N, T_total, D, dtype, gate_dtype, workspace, ws_bytes)) return rc;
     if (int rc = check_device()) return rc;
     if (flags & GDR_VALIDATE)
@@ -1303,7 +1282,7 @@ int gdr_linrec_fwd(const void* x, int64_t x_stride, const void* g, int64_t g_str
     LinrecParams p{};
     p.x = x; p.g = g; p.out = y; p.start = initial_state; p.last = final_state; p.cu = cu_seqlens;
     p.ldx = x_stride; p.ldg = g_stride; p.ldo = y_stride; p.T = T_total; p.N = N; p.D = D;
-    return launched(launch_scan(p, dtype, gate_dtype, false, workspace, s), "gdr_linrec_fwd launch");
+    return launch_result(launch_scan(p, dtype, gate_dtype, false, workspace, s), "gdr_linrec_fwd launch");
 }
 
 int gdr_linrec_bwd(const void* dy, int64_t dy_stride, const void* g, int64_t g_stride, const void* y,
@@ -1314,17 +1293,17 @@ int gdr_linrec_bwd(const void* dy, int64_t dy_stride, const void* g, int64_t g_s
     if (int rc = check_sizes(N, T_total, D, dtype, gate_dtype)) return rc;
     if (flags & ~GDR_VALIDATE)
         return set_last_error(GDR_ERR_INVALID_ARG, "unsupported flags 0x%x for gdr_linrec_bwd", flags);
-    if (int rc = check_state("initial_state", initial_state)) return rc;
-    if (int rc = check_state("d_final_state", d_final_state)) return rc;
-    if (int rc = check_state("d_initial_state", d_initial_state)) return rc;
+    if (int rc = check_aligned16("initial_state", initial_state)) return rc;
+    if (int rc = check_aligned16("d_final_state", d_final_state)) return rc;
+    if (int rc = check_aligned16("d_initial_state", d_initial_state)) return rc;
     cudaStream_t s = (cudaStream_t)stream;
     if (T_total == 0) return pass_states(d_final_state, d_initial_state, N, D, s);
-    if (int rc = check_rows("dy", dy, dy_stride, D, dtype, false)) return rc;
-    if (int rc = check_rows("g", g, g_stride, D, gate_dtype, false)) return rc;
-    if (int rc = check_rows("y", y, y_stride, D, dtype, false)) return rc;
-    if (int rc = check_rows("dx", dx, dx_stride, D, dtype, true)) return rc;
-    if (int rc = check_rows("dg", dg, dg_stride, D, gate_dtype, true)) return rc;
-    if (!cu_seqlens) return set_last_error(GDR_ERR_INVALID_ARG, "null pointer argument (cu_seqlens)");
+    if (int rc = check_rows("dy", dy, dy_stride, 0, element(dtype))) return rc;
+    if (int rc = check_rows("g", g, g_stride, 0, element(gate_dtype))) return rc;
+    if (int rc = check_rows("y", y, y_stride, 0, element(dtype))) return rc;
+    if (int rc = check_rows("dx", dx, dx_stride, D, element(dtype))) return rc;
+    if (int rc = check_rows("dg", dg, dg_stride, D, element(gate_dtype))) return rc;
+    if (int rc = check_ints("cu_seqlens", cu_seqlens)) return rc;
     if (int rc = check_workspace(N, T_total, D, dtype, gate_dtype, workspace, ws_bytes)) return rc;
     if (int rc = check_device()) return rc;
     if (flags & GDR_VALIDATE)
@@ -1333,7 +1312,7 @@ int gdr_linrec_bwd(const void* dy, int64_t dy_stride, const void* g, int64_t g_s
     p.x = dy; p.g = g; p.h = y; p.out = dx; p.dg = dg; p.h0 = initial_state; p.start = d_final_state;
     p.last = d_initial_state; p.cu = cu_seqlens; p.ldx = dy_stride; p.ldg = g_stride; p.ldh = y_stride;
     p.ldo = dx_stride; p.lddg = dg_stride; p.T = T_total; p.N = N; p.D = D;
-    return launched(launch_scan(p, dtype, gate_dtype, true, workspace, s), "gdr_linrec_bwd launch");
+    return launch_result(launch_scan(p, dtype, gate_dtype, true, workspace, s), "gdr_linrec_bwd launch");
 }
 
 int gdr_linrec_step(const void* x, int64_t x_stride, const void* g, int64_t g_stride, void* state_pool,
@@ -1349,13 +1328,14 @@ int gdr_linrec_step(const void* x, int64_t x_stride, const void* g, int64_t g_st
     if (num_slots <= 0) return set_last_error(GDR_ERR_INVALID_ARG, "num_slots must be positive");
     if (intermediate_states && steps <= 0)
         return set_last_error(GDR_ERR_INVALID_ARG, "steps must be positive with intermediate_states");
-    if (!state_pool || !state_indices || !cu_seqlens)
-        return set_last_error(GDR_ERR_INVALID_ARG, "null pointer argument");
-    if (int rc = check_state("state_pool", state_pool)) return rc;
-    if (int rc = check_state("intermediate_states", intermediate_states)) return rc;
-    if (int rc = check_rows("x", x, x_stride, D, dtype, false)) return rc;
-    if (int rc = check_rows("g", g, g_stride, D, gate_dtype, false)) return rc;
-    if (int rc = check_rows("y", y, y_stride, D, dtype, true)) return rc;
+    if (!state_pool) return set_last_error(GDR_ERR_INVALID_ARG, "null pointer argument (state_pool)");
+    if (int rc = check_ints("state_indices", state_indices)) return rc;
+    if (int rc = check_ints("cu_seqlens", cu_seqlens)) return rc;
+    if (int rc = check_aligned16("state_pool", state_pool)) return rc;
+    if (int rc = check_aligned16("intermediate_states", intermediate_states)) return rc;
+    if (int rc = check_rows("x", x, x_stride, 0, element(dtype))) return rc;
+    if (int rc = check_rows("g", g, g_stride, 0, element(gate_dtype))) return rc;
+    if (int rc = check_rows("y", y, y_stride, D, element(dtype))) return rc;
     if (int rc = check_device()) return rc;
     cudaStream_t s = (cudaStream_t)stream;
     if (flags & GDR_VALIDATE)
@@ -1366,7 +1346,7 @@ int gdr_linrec_step(const void* x, int64_t x_stride, const void* g, int64_t g_st
     p.x = x; p.g = g; p.pool = state_pool; p.idx = state_indices; p.cu = cu_seqlens; p.y = y;
     p.states = intermediate_states; p.ldx = x_stride; p.ldg = g_stride; p.ldy = y_stride; p.T = T_total; p.N = N;
     p.D = D; p.num_slots = num_slots; p.steps = intermediate_states ? steps : 0; p.commit = (flags & GDR_COMMIT) ? 1 : 0;
-    return launched(launch_step(p, dtype, gate_dtype, pool_dtype, s), "gdr_linrec_step launch");
+    return launch_result(launch_step(p, dtype, gate_dtype, pool_dtype, s), "gdr_linrec_step launch");
 }
 
 }  // extern "C"

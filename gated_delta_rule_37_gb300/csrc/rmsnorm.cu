@@ -4,8 +4,6 @@
 #include <cuda_fp8.h>
 #include <math.h>
 
-#include <atomic>
-
 #include "common.cuh"
 #include "gdr.h"
 #include "launch.h"
@@ -341,18 +339,6 @@ __global__ void __launch_bounds__(kMaxThreads, CH <= 8 ? 2 : 1) rmsnorm_fwd_any_
         }
         meet();
     }
-}
-
-int sm_count() {
-    static std::atomic<int> known{0};
-    int n = known.load(std::memory_order_relaxed);
-    if (n) return n;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-        return 1;
-    known.store(n, std::memory_order_relaxed);
-    return n;
 }
 
 // Threads of a row that holds `pieces` pieces, ch of them per thread.
@@ -785,12 +771,9 @@ cudaError_t launch_bwd_ring(NormBwdParams p, cudaStream_t s) {
     constexpr int kShare = 227 * 1024 / CTAS - 2048;
     const int slots = THREADS / p.tpr, stage = slots * 3 * p.D * (int)sizeof(T);
     p.stages = kShare / stage < kMaxStages ? kShare / stage : kMaxStages;
-    static std::atomic<bool> ready{false};
-    if (!ready.load(std::memory_order_relaxed)) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShare);
-        if (e != cudaSuccess) return e;
-        ready.store(true, std::memory_order_relaxed);
-    }
+    // at every call: the attribute belongs to the context
+    const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShare);
+    if (set != cudaSuccess) return set;
     p.err = device_error_word();
     if (!p.err) return cudaErrorInitializationError;
     const int64_t want = (p.M + slots - 1) / slots, most = (int64_t)CTAS * sm_count();
@@ -847,25 +830,16 @@ int check_sizes(int64_t M, int D, float eps, int dtype) {
     return GDR_OK;
 }
 
-int check_rows(const char* name, const void* p, int64_t stride, int64_t least, unsigned esize) {
-    if (!p) return set_last_error(GDR_ERR_INVALID_ARG, "null pointer argument (%s)", name);
-    if (reinterpret_cast<uintptr_t>(p) & (esize - 1))
-        return set_last_error(GDR_ERR_INVALID_ARG, "%s not aligned to its element", name);
-    if (stride < least)
-        return set_last_error(GDR_ERR_INVALID_ARG, "%s: row stride %lld too small", name, (long long)stride);
-    return GDR_OK;
-}
-
 int check_floats(const char* name, const void* p) {
     if (!p) return set_last_error(GDR_ERR_INVALID_ARG, "null pointer argument (%s)", name);
-    if (reinterpret_cast<uintptr_t>(p) & 15u)
-        return set_last_error(GDR_ERR_INVALID_ARG, "%s not 16-byte aligned", name);
-    return GDR_OK;
+    return check_aligned16(name, p);
 }
 
-int launched(cudaError_t e, const char* what) {
-    if (e != cudaSuccess) return set_last_error(GDR_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
-    return set_ok();
+// One tensor on another: the same pointer and stride, or neither.
+int check_in_place(const char* name, const void* p, int64_t ld, const char* other, const void* q, int64_t ldq, int64_t M) {
+    if (p == q && ld != ldq && M > 1)
+        return set_last_error(GDR_ERR_INVALID_ARG, "%s is %s with another row stride", name, other);
+    return GDR_OK;
 }
 
 }  // namespace
@@ -894,6 +868,9 @@ int gdr_rmsnorm_fwd(const void* x, int64_t x_stride, const void* residual, int64
     if (residual) {
         if (int rc = check_rows("residual", residual, residual_stride, 0, esize)) return rc;
         if (int rc = check_rows("residual_out", residual_out, residual_out_stride, D, esize)) return rc;
+        if (int rc = check_in_place("residual_out", residual_out, residual_out_stride, "residual", residual, residual_stride, M))
+            return rc;
+        if (int rc = check_in_place("residual_out", residual_out, residual_out_stride, "x", x, x_stride, M)) return rc;
     }
     if (int rc = check_rows("y", y, y_stride, D, fp8 ? 1 : esize)) return rc;
     if (int rc = check_floats("weight", weight)) return rc;
@@ -910,7 +887,7 @@ int gdr_rmsnorm_fwd(const void* x, int64_t x_stride, const void* residual, int64
     const bool wide = D % 8 == 0 && wide_rows(x, x_stride, esize) && wide_rows(y, y_stride, fp8 ? 1 : esize) &&
                       (!residual || (wide_rows(residual, residual_stride, esize) &&
                                      wide_rows(residual_out, residual_out_stride, esize)));
-    return launched(dtype == GDR_BF16 ? launch_fwd<__nv_bfloat16>(p, fp8, wide, s) : launch_fwd<float>(p, fp8, wide, s),
+    return launch_result(dtype == GDR_BF16 ? launch_fwd<__nv_bfloat16>(p, fp8, wide, s) : launch_fwd<float>(p, fp8, wide, s),
                     "gdr_rmsnorm_fwd launch");
 }
 
@@ -932,7 +909,7 @@ int gdr_rmsnorm_bwd(const void* dy, int64_t dy_stride, const void* s, int64_t s_
     if (M == 0) {
         if (!dweight) return set_ok();
         if (int rc = check_device()) return rc;
-        return launched(cudaMemsetAsync(dweight, 0, sizeof(float) * (size_t)D, st), "gdr_rmsnorm_bwd launch");
+        return launch_result(cudaMemsetAsync(dweight, 0, sizeof(float) * (size_t)D, st), "gdr_rmsnorm_bwd launch");
     }
     const unsigned esize = dtype == GDR_BF16 ? 2 : 4;
     if (int rc = check_rows("dy", dy, dy_stride, 0, esize)) return rc;
@@ -940,6 +917,8 @@ int gdr_rmsnorm_bwd(const void* dy, int64_t dy_stride, const void* s, int64_t s_
     if (d_residual_out)
         if (int rc = check_rows("d_residual_out", d_residual_out, d_residual_out_stride, 0, esize)) return rc;
     if (int rc = check_rows("dx", dx, dx_stride, D, esize)) return rc;
+    if (int rc = check_in_place("dx", dx, dx_stride, "dy", dy, dy_stride, M)) return rc;
+    if (int rc = check_in_place("dx", dx, dx_stride, "d_residual_out", d_residual_out, d_residual_out_stride, M)) return rc;
     if (int rc = check_floats("weight", weight)) return rc;
     if (dweight) {
         size_t need = 0;
@@ -959,7 +938,7 @@ int gdr_rmsnorm_bwd(const void* dy, int64_t dy_stride, const void* s, int64_t s_
     const bool wide = D % 8 == 0 && wide_rows(dy, dy_stride, esize) && wide_rows(s, s_stride, esize) &&
                       wide_rows(dx, dx_stride, esize) &&
                       (!d_residual_out || wide_rows(d_residual_out, d_residual_out_stride, esize));
-    return launched(dtype == GDR_BF16 ? launch_bwd<__nv_bfloat16>(p, wide, st) : launch_bwd<float>(p, wide, st),
+    return launch_result(dtype == GDR_BF16 ? launch_bwd<__nv_bfloat16>(p, wide, st) : launch_bwd<float>(p, wide, st),
                     "gdr_rmsnorm_bwd launch");
 }
 

@@ -289,6 +289,11 @@ GDR_API int gdr_gating_fwd(const void* a, const float* dt_bias, const float* A_l
  *     it, and a gate that is NaN or > 0, into GDR_ERR_VALIDATION.
  *   - A NaN or infinity stays within its sequence and channel.
  *   - Results do not depend on scheduling: equal inputs give equal bits.
+ *   - A tile of a long call waits for the state that reaches it from the tiles
+ *     before it, which are running by then.  Every wait is bounded (one second):
+ *     one that gives up is reported by gdr_get_device_status, and what the call
+ *     has not written by then stays unwritten.
+ *   - D up to 2^24, T_total up to 2^31 - 256.
  *
  * gdr_linrec_workspace_size -- bytes of device workspace that gdr_linrec_fwd
  * and gdr_linrec_bwd need (the same for both; may be 0).  Host only.

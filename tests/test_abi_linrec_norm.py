@@ -32,7 +32,8 @@ def _fwd(lib, **kw):
     (dict(x=P(17)), INVALID),                              # bf16 at an odd address
     (dict(g=P(34)), INVALID),                              # fp32 off its 4 bytes
     (dict(ldx=-64), INVALID), (dict(ldy=63), INVALID),
-    (dict(h0=P(20)), INVALID), (dict(hT=P(20)), INVALID),
+    (dict(h0=P(20)), INVALID), (dict(hT=P(20)), INVALID), (dict(cu=P(50)), INVALID),
+    (dict(D=(1 << 24) + 1, ldx=1 << 25, ldg=1 << 25, ldy=1 << 25), UNSUPPORTED),
     (dict(D=0), INVALID), (dict(N=-1), INVALID), (dict(T=-1), INVALID), (dict(N=0), INVALID),
     (dict(dtype=E4M3), UNSUPPORTED), (dict(gate=7), UNSUPPORTED), (dict(T=1 << 31), UNSUPPORTED),
     (dict(flags=gdr.GDR_COMMIT), INVALID), (dict(flags=0x40), INVALID),
@@ -93,7 +94,7 @@ def _step(lib, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(x=None), INVALID), (dict(pool=None), INVALID), (dict(idx=None), INVALID), (dict(cu=None), INVALID),
     (dict(y=None), INVALID), (dict(pool=P(50)), INVALID), (dict(ib=P(112)), INVALID),
-    (dict(ib=P(113), steps=2), INVALID), (dict(slots=0), INVALID), (dict(pt=2), UNSUPPORTED),
+    (dict(ib=P(113), steps=2), INVALID), (dict(idx=P(66)), INVALID), (dict(slots=0), INVALID), (dict(pt=2), UNSUPPORTED),
     (dict(flags=gdr.GDR_QK_L2NORM), INVALID), (dict(ldy=1), INVALID), (dict(D=-1), INVALID),
 ])
 def test_linrec_step_rejects_before_launch(lib, kw, code):

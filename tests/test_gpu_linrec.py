@@ -188,6 +188,38 @@ def test_long_memory(types):
     check_bwd(c, *run_bwd(c))
 
 
+@pytest.mark.parametrize("types", [(BF, BF), (F, F)], ids=["bf16", "f32"])
+def test_long_unaligned_rows(types):
+    """The same with rows of every alignment."""
+    c = make(22, [4000, 1, 4199], 65, *types, g_lo=-0.02, pad=1)
+    check_fwd(c, *run_fwd(c))
+    check_bwd(c, *run_bwd(c))
+
+
+@pytest.mark.parametrize("lens,pad", [([100], 900), ([5, 0, 300], 4000), ([3000], 3000), ([0, 0], 700), ([0], 9000)])
+@pytest.mark.parametrize("D", [64, 65])
+def test_padded_batches(D, lens, pad):
+    """Whole tiles behind the last sequence, in calls of every size."""
+    c = make(23, lens, D, BF, F, pad=pad)
+    check_fwd(c, *run_fwd(c))
+    check_bwd(c, *run_bwd(c))
+
+
+@pytest.mark.parametrize("T,D", [(400, 64), (1500, 72), (3000, 200), (3000, 65)])
+def test_workspace_is_kept_to(T, D):
+    """The stated size is enough, and nothing around it is written."""
+    c = make(24, [T], D, BF, F)
+    n = gdr.linrec_workspace_size(1, T, D, dtype=gdr.GDR_BF16, gate_dtype=gdr.GDR_F32)
+    ws = Guarded((n,), torch.uint8, DEV, fill_bytes=torch.full((n,), 0x3C, dtype=torch.uint8))
+    y, hT = run_fwd(c, workspace=ws.view)
+    assert ws.guards_intact()
+    check_fwd(c, y, hT)
+    if n:
+        with pytest.raises(gdr.GdrError, match="workspace"):
+            run_fwd(c, workspace=ws.view[:n - 1])
+    assert gdr.device_status() == 0
+
+
 def test_many_sequences():
     """More sequences than a grid axis holds, most of them one token or none."""
     c = make(12, [(i * 5) % 3 for i in range(70000)], 8, BF, F)
@@ -328,6 +360,28 @@ def test_streams():
     for runs in got:
         for y, hT in runs:
             assert bits_equal(y, want[0]) and bits_equal(hT, want[1])
+
+
+def test_calls_that_share_the_gpu():
+    """Calls of several times the GPU's size at once, on streams and workspaces
+    of their own: tiles wait only for tiles that are running, so all end, with
+    the bits of a call alone."""
+    c = make(25, [9000, 11000], 1024, BF, BF)
+    x, g, y, cu, h0, df = (c[k].to(DEV) for k in ("x", "g", "y", "cu", "h0", "df"))
+    want = gdr.linrec_fwd(x, g, cu, initial_state=h0) + \
+        gdr.linrec_bwd(x, g, y, cu, initial_state=h0, d_final_state=df)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for s in streams:
+            got.append(gdr.linrec_fwd(x, g, cu, initial_state=h0, stream=s) +
+                       gdr.linrec_bwd(x, g, y, cu, initial_state=h0, d_final_state=df, stream=s))
+    torch.cuda.synchronize()
+    for run in got:
+        for a, b in zip(run, want):
+            assert torch.equal(a, b)
+    assert gdr.device_status() == 0
 
 
 def test_empty_calls():

@@ -182,6 +182,29 @@ def test_in_place(dtype):
             assert bits_equal(dx2, dx) and bits_equal(dw2, dw)
 
 
+@pytest.mark.parametrize("M,D", [(3000, 1024), (2000, 4096), (1, 4096), (700, 512)])
+def test_in_place_with_rows_on_their_way(M, D):
+    """dx written over dy while later rows are being fetched; rows more than a
+    CTA's, and fewer than it can hold."""
+    c = make(45, M, D, BF)
+    x, w, dy, ds = (c[k].to(DEV) for k in ("x", "w", "dy", "ds"))
+    dx, dw = gdr.rmsnorm_bwd(dy, x, w, eps=EPS, d_residual_out=ds)
+    for into in (0, 1):
+        ops = [dy.clone(), ds.clone()]
+        dx2, dw2 = gdr.rmsnorm_bwd(ops[0], x, w, eps=EPS, d_residual_out=ops[1], dx=ops[into])
+        assert bits_equal(dx2, dx) and bits_equal(dw2, dw)
+
+
+def test_in_place_with_another_stride_is_refused():
+    wide = torch.randn(6, 32, device=DEV)
+    x, w = torch.randn(6, 8, device=DEV), torch.ones(8, device=DEV)
+    flat = wide.view(-1)[:48].view(6, 8)                   # the same address, rows 8 apart instead of 32
+    with pytest.raises(gdr.GdrError, match="stride"):
+        gdr.rmsnorm_fwd(x, w, residual=wide[:, :8], residual_out=flat)
+    with pytest.raises(gdr.GdrError, match="stride"):
+        gdr.rmsnorm_bwd(wide[:, :8], x, w, dx=flat)
+
+
 def test_strides_and_alignment():
     for off, width, D in ((0, 256, 128), (128, 256, 128), (3, 200, 128), (1, 140, 131)):
         c = make(50 + off, 90, D, BF)
