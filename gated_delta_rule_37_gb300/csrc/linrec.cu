@@ -30,7 +30,26 @@
 // mean.  The hardware's exponential is about 0.3 * 2^-24 low on average just
 // below 0, which a memory of 4000 tokens turns into 6e-5 of the state; the
 // Taylor polynomial, ending in a fused multiply-add with 1, has a mean error
-// below 0.001 * 2^-24 there.
+// below 0.001 * 2^-24 there.  A run's decay is the exponential of its gates' sum:
+// the product of its tokens' rounded decays left 1.0e-6 at that memory, the sum
+// 3.5e-7 (fp32 states against 64 bits).
+//
+// What bounds it.  Less than two flops per byte: memory.  The floor of a call is
+// its rows' bytes at the copy rate (6.69 TB/s measured); one GB300, device times:
+//   forward  32768 x 4096  bf16, fp32 gates   180 us   89 %    (bf16 gates 152 us, 79 %;
+//                          fp32, 16384 rows   128 us   94 %)
+//   backward 32768 x 4096  bf16, bf16 gates   226 us   89 %    (fp32 gates 286 us, 98 %;
+//                          fp32, 16384 rows   207 us   97 %)
+//   backward 7001 x 1001   fp32, odd rows      48 us   44 %
+//   forward  6113 x 2048   bf16, 4 sequences   30 us   49 %
+// Long calls of narrow types are held by the chain of one tile's steps (composition,
+// fold, look-back, evaluation: about 8,500 cycles at two CTAs per SM, of which the
+// look-back is a quarter), which longer tiles spread over more tokens: R went from
+// 4 and 5 to the most that registers hold, 240 -> 224 us and 189 -> 181 us.  Three
+// and four smaller CTAs per SM (233 and 287 us forward), a larger window of the
+// look-back (4 instead of 2 rows: 195 -> 203 us) and the look-back as a function
+// of its own (173 -> 213 us) cost more in registers than they hid.  Short calls are
+// bound by their first tile's latency, odd rows by their scalar stores.
 #include <cuda.h>
 #include <math.h>
 
@@ -258,14 +277,17 @@ __device__ __forceinline__ void product(float (&o)[8], const float (&a)[8], cons
 // ---- the tile kernel --------------------------------------------------------------
 
 // 64 channels per tile, 8 per thread.  WIDE: aligned rows, staged by TMA.  Otherwise
-// rows are staged by 16-byte asynchronous copies of the aligned blocks around each
-// row's segment, and read from where it lies in them.
+// each row's segment is staged by a bulk copy of the 16-byte blocks around it, and
+// read from where it lies in them: about 60 cycles to issue, so six warps issue them
+// while two look back (one warp for all took 17,600 cycles of a tile; 4-byte
+// asynchronous copies by all warps before the fold took 3,200 to 10,700).
 template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
     static constexpr int THREADS = 256, CTAS = 2, WARPS = THREADS / 32;
     static constexpr int COPIERS = WARPS - 2;  // warps that issue bulk copies, while the others look back
     static constexpr int LANES = 8, CC = 64, RUNS = THREADS / LANES;  // runs of R tokens
     // A token takes 8 registers for its decays and 4 or 8 for each of b and h as
-    // stored; R of them is what fits beside the rest at two CTAs per SM.
+    // stored; R is the most that fits beside the rest in 128 registers (one more
+    // spills, 181 -> 220 us forward) and in shared memory at two CTAs per SM.
     static constexpr int R = sizeof(TX) == 2 ? (BWD ? (WIDE ? 5 : 4) : WIDE && sizeof(TG) == 2 ? 7 : 6) : (BWD ? 3 : 5);
     static constexpr int TT = RUNS * R;
     static constexpr int PARTS = THREADS / CC, RUNS_PART = RUNS / PARTS;  // the fold over runs, in parts
@@ -869,8 +891,10 @@ __global__ void linrec_clear_kernel(uint4* w, int64_t n) {
 
 // ---- workspace and launch ------------------------------------------------------------
 
-// Up to 8 tile rows whose tiles all fit on the GPU at once: clusters, one launch
-// and no workspace (512 tokens by 1024 channels).
+// Up to 8 tile rows whose tiles all fit on the GPU at once are a cluster per channel
+// group: one launch, no workspace.  On the device about the same (1200 tokens by 1024
+// channels 7.5 us, with the look-back 8.1 us); for the host one launch and one
+// allocation less (16 instead of 22 us a call).
 constexpr int kMaxCluster = 8, kMaxClusterTiles = 304;
 
 struct ScanLayout {
@@ -1046,7 +1070,10 @@ template <typename T, int VEC> struct alignas(sizeof(T) * VEC < 16 ? sizeof(T) *
 
 // A thread owns VEC channels of a sequence and walks its tokens, those of the
 // next TOKENS steps loaded at once.  Bound by latency at decode sizes (the slot
-// and the sequence's place, then the rows), by memory at large ones.
+// and the sequence's place, then the rows), by memory at large ones: 4 x 2048
+// channels 1.7 us, 256 x 4096 3.6 us (62 % of the copy rate, all of it in L2),
+// 64 x 1..12 tokens x 4096 with every state kept 6.4 us (37 %).  All 12 tokens
+// loaded at once instead of 4 was slower (9.7 us: a larger program than its run).
 template <typename TX, typename TG, typename TP, int VEC>
 __global__ void __launch_bounds__(128) linrec_step_kernel(StepParams p) {
     constexpr int TOKENS = VEC >= 8 ? 2 : 4;
@@ -1119,7 +1146,9 @@ cudaError_t launch_step_t(const StepParams& p, cudaStream_t s) {
     if (p.D % 8 || !wide_rows<TX>(p.x, p.ldx, p.D) || !wide_rows<TG>(p.g, p.ldg, p.D) ||
         !wide_rows<TX>(p.y, p.ldy, p.D))
         return launch_step_v<TX, TG, TP, 1>(p, s);
-    // 8 channels per thread where that still gives every SM's schedulers work
+    // 8 channels per thread where that still gives every SM's schedulers work (the
+    // decode batch of 256: 3.8 us, with 4 channels 4.9, with 2 6.6), fewer otherwise
+    // (the verify batch of 64: with 2 channels 6.4 us, with 4 7.5, with 8 11.4)
     const int64_t channels = (int64_t)p.N * p.D, full = (int64_t)sm_count() * 768;
     return channels >= full * 8 ? launch_step_v<TX, TG, TP, 8>(p, s)
          : channels >= full * 4 ? launch_step_v<TX, TG, TP, 4>(p, s) : launch_step_v<TX, TG, TP, 2>(p, s);
