@@ -357,28 +357,22 @@ def _like(t, shape, dtype, device):
     return new, new.data_ptr(), shape[1]
 
 
-def _code(dtype):
-    c = _CODES.get(dtype)
-    if c is None:
-        raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
-    return c
+def _not_a_code(*dtypes):
+    bad = next(d for d in dtypes if d not in _CODES)
+    raise TypeError(f"unsupported dtype {bad} (bf16 or fp32)")
 
 
-def _device_of(t, what):
+def _elsewhere(t, what, stream):
+    """The context to enter first where a call does not run on the current
+    device's current stream; refuses tensors that no call takes."""
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
     if t.dim() != 2:
         raise ValueError(f"{what} must be 2-D")
-    return t.device
-
-
-def _elsewhere(device, stream):
-    """The context to enter first where a call does not run on the current
-    device's current stream; None where it does."""
     if stream is None:
-        return None if _current_device() == device.index else torch.cuda.device(device)
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        return torch.cuda.device(t.device)
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {t.device}")
     return torch.cuda.stream(stream)
 
 
@@ -394,10 +388,14 @@ def _scratch(workspace, size, device):
 
 
 @functools.lru_cache(maxsize=4096)
-def linrec_workspace_size(N: int, T: int, D: int, *, dtype: int, gate_dtype: int) -> int:
+def _linrec_bytes(N, T, D, dtype, gate_dtype):
     out = ctypes.c_size_t(0)
     _check(load().gdr_linrec_workspace_size(N, T, D, dtype, gate_dtype, ctypes.byref(out)))
     return out.value
+
+
+def linrec_workspace_size(N: int, T: int, D: int, *, dtype: int, gate_dtype: int) -> int:
+    return _linrec_bytes(N, T, D, dtype, gate_dtype)
 
 
 def linrec_fwd(x, g, cu_seqlens, *, initial_state=None, flags: int = 0, y=None, final_state=None,
@@ -406,15 +404,15 @@ def linrec_fwd(x, g, cu_seqlens, *, initial_state=None, flags: int = 0, y=None, 
     sequences.  x [T, D] bf16 or fp32; g [T, D] bf16 or fp32, <= 0; cu_seqlens
     [N+1] int32; initial_state [N, D] fp32 or None.  Rows from cu_seqlens[N] on
     are neither read nor written.  Returns (y, final_state or None)."""
-    dev = _device_of(x, "x")
-    elsewhere = _elsewhere(dev, stream)
-    if elsewhere is not None:
-        with elsewhere:
+    if stream is not None or not x.is_cuda or x.get_device() != _current_device() or x.dim() != 2:
+        with _elsewhere(x, "x", stream):
             return linrec_fwd(x, g, cu_seqlens, initial_state=initial_state, flags=flags, y=y, final_state=final_state,
                               output_final_state=output_final_state, workspace=workspace)
-    T, D = shape = x.shape
-    xt, gt = x.dtype, g.dtype
-    xc, gc = _code(xt), _code(gt)
+    dev, shape, xt, gt = x.device, x.shape, x.dtype, g.dtype
+    T, D = shape
+    xc, gc = _CODES.get(xt), _CODES.get(gt)
+    if xc is None or gc is None:
+        _not_a_code(xt, gt)
     N = cu_seqlens.numel() - 1
     state = (N, D)
     xp, xs = _rows(x, shape, xt, dev, "x")
@@ -430,7 +428,7 @@ def linrec_fwd(x, g, cu_seqlens, *, initial_state=None, flags: int = 0, y=None, 
     else:
         final_state = torch.empty(N, D, dtype=_F32, device=dev) if hp is None else torch.empty_like(initial_state)
         fp = final_state.data_ptr()
-    ws, wp, wn = _scratch(workspace, linrec_workspace_size(N, T, D, dtype=xc, gate_dtype=gc), dev)
+    ws, wp, wn = _scratch(workspace, _linrec_bytes(N, T, D, xc, gc), dev)
     code = (_lib or load()).gdr_linrec_fwd(xp, xs, gp, gs, hp, cp, N, T, D, xc, gc, flags, yp, ys, fp, wp, wn,
                                            _current_handle(dev.index))
     if code:
@@ -443,16 +441,16 @@ def linrec_bwd(dy, g, y, cu_seqlens, *, initial_state=None, d_final_state=None, 
     """Gradients of linrec_fwd: dy [T, D] is the gradient of y, d_final_state
     [N, D] fp32 (or None) that of the final state; g, y, initial_state are the
     forward's.  Returns (dx, dg, d_initial_state or None)."""
-    dev = _device_of(dy, "dy")
-    elsewhere = _elsewhere(dev, stream)
-    if elsewhere is not None:
-        with elsewhere:
+    if stream is not None or not dy.is_cuda or dy.get_device() != _current_device() or dy.dim() != 2:
+        with _elsewhere(dy, "dy", stream):
             return linrec_bwd(dy, g, y, cu_seqlens, initial_state=initial_state, d_final_state=d_final_state,
                               flags=flags, dx=dx, dg=dg, d_initial_state=d_initial_state,
                               output_d_initial_state=output_d_initial_state, workspace=workspace)
-    T, D = shape = dy.shape
-    xt, gt = dy.dtype, g.dtype
-    xc, gc = _code(xt), _code(gt)
+    dev, shape, xt, gt = dy.device, dy.shape, dy.dtype, g.dtype
+    T, D = shape
+    xc, gc = _CODES.get(xt), _CODES.get(gt)
+    if xc is None or gc is None:
+        _not_a_code(xt, gt)
     N = cu_seqlens.numel() - 1
     state = (N, D)
     dp, ds = _rows(dy, shape, xt, dev, "dy")
@@ -474,7 +472,7 @@ def linrec_bwd(dy, g, y, cu_seqlens, *, initial_state=None, d_final_state=None, 
     else:
         d_initial_state = torch.empty(N, D, dtype=_F32, device=dev) if hp is None else torch.empty_like(initial_state)
         ip = d_initial_state.data_ptr()
-    ws, wp, wn = _scratch(workspace, linrec_workspace_size(N, T, D, dtype=xc, gate_dtype=gc), dev)
+    ws, wp, wn = _scratch(workspace, _linrec_bytes(N, T, D, xc, gc), dev)
     code = (_lib or load()).gdr_linrec_bwd(dp, ds, gp, gs, yp, ys, hp, fp, cp, N, T, D, xc, gc, flags, xp, xs, ap, as_,
                                            ip, wp, wn, _current_handle(dev.index))
     if code:
@@ -488,14 +486,15 @@ def linrec_step(x, g, state_pool, state_indices, cu_seqlens, *, flags: int = GDR
     (fp32 or bf16) at state_indices [N] int32 (< 0: skipped).  The pool is
     updated in place only with GDR_COMMIT; intermediate_states [rows >= N,
     steps, D] (pool dtype) receives the state after every token.  Returns y."""
-    dev = _device_of(x, "x")
-    elsewhere = _elsewhere(dev, stream)
-    if elsewhere is not None:
-        with elsewhere:
+    if stream is not None or not x.is_cuda or x.get_device() != _current_device() or x.dim() != 2:
+        with _elsewhere(x, "x", stream):
             return linrec_step(x, g, state_pool, state_indices, cu_seqlens, flags=flags, y=y,
                                intermediate_states=intermediate_states)
-    T, D = shape = x.shape
-    xt, gt, pt = x.dtype, g.dtype, state_pool.dtype
+    dev, shape, xt, gt, pt = x.device, x.shape, x.dtype, g.dtype, state_pool.dtype
+    T, D = shape
+    xc, gc, pc = _CODES.get(xt), _CODES.get(gt), _CODES.get(pt)
+    if xc is None or gc is None or pc is None:
+        _not_a_code(xt, gt, pt)
     N = cu_seqlens.numel() - 1
     slots = state_pool.shape[0]
     xp, xs = _rows(x, shape, xt, dev, "x")
@@ -513,8 +512,8 @@ def linrec_step(x, g, state_pool, state_indices, cu_seqlens, *, flags: int = GDR
         y, yp, ys = _like(x, shape, xt, dev)
     else:
         yp, ys = _rows(y, shape, xt, dev, "y")
-    code = (_lib or load()).gdr_linrec_step(xp, xs, gp, gs, pp, _code(pt), slots, ip, cp, N, T, D, _code(xt), _code(gt),
-                                            flags, yp, ys, bp, steps, _current_handle(dev.index))
+    code = (_lib or load()).gdr_linrec_step(xp, xs, gp, gs, pp, pc, slots, ip, cp, N, T, D, xc, gc, flags, yp, ys, bp,
+                                            steps, _current_handle(dev.index))
     if code:
         _check(code)
     return y
@@ -528,14 +527,15 @@ def rmsnorm_fwd(x, weight, *, residual=None, eps: float = 1e-6, y_dtype=None, sc
     one fp32 scale per scale_group (32, 64, 128; 0: the row) elements of a row.
     residual_out may be residual (or x) itself.  Returns (y, residual_out or
     None, scales or None)."""
-    dev = _device_of(x, "x")
-    elsewhere = _elsewhere(dev, stream)
-    if elsewhere is not None:
-        with elsewhere:
+    if stream is not None or not x.is_cuda or x.get_device() != _current_device() or x.dim() != 2:
+        with _elsewhere(x, "x", stream):
             return rmsnorm_fwd(x, weight, residual=residual, eps=eps, y_dtype=y_dtype, scale_group=scale_group, y=y,
                                residual_out=residual_out, scales=scales)
-    M, D = shape = x.shape
-    xt = x.dtype
+    dev, shape, xt = x.device, x.shape, x.dtype
+    M, D = shape
+    xc = _CODES.get(xt)
+    if xc is None:
+        _not_a_code(xt)
     if y_dtype is None:
         y_dtype = xt if y is None else y.dtype
     xp, xs = _rows(x, shape, xt, dev, "x")
@@ -567,8 +567,8 @@ def rmsnorm_fwd(x, weight, *, residual=None, eps: float = 1e-6, y_dtype=None, sc
         raise ValueError("residual_out without residual")
     else:
         rp, rs, op, os_ = None, 0, None, 0
-    code = (_lib or load()).gdr_rmsnorm_fwd(xp, xs, rp, rs, wp, M, D, eps, _code(xt), op, os_, yp, ys, yc, sp,
-                                            scale_group, _current_handle(dev.index))
+    code = (_lib or load()).gdr_rmsnorm_fwd(xp, xs, rp, rs, wp, M, D, eps, xc, op, os_, yp, ys, yc, sp, scale_group,
+                                            _current_handle(dev.index))
     if code:
         _check(code)
     return y, residual_out, scales
@@ -587,14 +587,15 @@ def rmsnorm_bwd(dy, s, weight, *, eps: float = 1e-6, d_residual_out=None, dx=Non
     residual_out (x without a residual), d_residual_out the gradient arriving
     at s along the residual stream.  Returns (dx, dweight): dx is the gradient
     of x and of residual alike, dweight [D] fp32."""
-    dev = _device_of(dy, "dy")
-    elsewhere = _elsewhere(dev, stream)
-    if elsewhere is not None:
-        with elsewhere:
+    if stream is not None or not dy.is_cuda or dy.get_device() != _current_device() or dy.dim() != 2:
+        with _elsewhere(dy, "dy", stream):
             return rmsnorm_bwd(dy, s, weight, eps=eps, d_residual_out=d_residual_out, dx=dx, dweight=dweight,
                                output_dweight=output_dweight, workspace=workspace)
-    M, D = shape = dy.shape
-    xt = dy.dtype
+    dev, shape, xt = dy.device, dy.shape, dy.dtype
+    M, D = shape
+    xc = _CODES.get(xt)
+    if xc is None:
+        _not_a_code(xt)
     dp, ds = _rows(dy, shape, xt, dev, "dy")
     sp, ss = _rows(s, shape, xt, dev, "s")
     wp = _dense(weight, (D,), _F32, dev, "weight")
@@ -610,7 +611,7 @@ def rmsnorm_bwd(dy, s, weight, *, eps: float = 1e-6, d_residual_out=None, dx=Non
     if dweight is not None:
         gp = _dense(dweight, (D,), _F32, dev, "dweight")
         ws, kp, kn = _scratch(workspace, rmsnorm_bwd_workspace_size(M, D), dev)
-    code = (_lib or load()).gdr_rmsnorm_bwd(dp, ds, sp, ss, wp, rp, rs, M, D, eps, _code(xt), xp, xs, gp, kp, kn,
+    code = (_lib or load()).gdr_rmsnorm_bwd(dp, ds, sp, ss, wp, rp, rs, M, D, eps, xc, xp, xs, gp, kp, kn,
                                             _current_handle(dev.index))
     if code:
         _check(code)
