@@ -36,16 +36,16 @@
 //
 // What bounds it.  Less than two flops per byte: memory.  The floor of a call is
 // its rows' bytes at the copy rate (6.69 TB/s measured); one GB300, device times:
-//   forward  32768 x 4096  bf16, fp32 gates   180 us   89 %    (bf16 gates 152 us, 79 %;
-//                          fp32, 16384 rows   128 us   94 %)
-//   backward 32768 x 4096  bf16, bf16 gates   226 us   89 %    (fp32 gates 286 us, 98 %;
+//   forward  32768 x 4096  bf16, fp32 gates   172 us   93 %    (bf16 gates 151 us, 80 %;
+//                          fp32, 16384 rows   127 us   95 %)
+//   backward 32768 x 4096  bf16, bf16 gates   226 us   89 %    (fp32 gates 283 us, 99 %;
 //                          fp32, 16384 rows   207 us   97 %)
 //   backward 7001 x 1001   fp32, odd rows      48 us   44 %
-//   forward  6113 x 2048   bf16, 4 sequences   30 us   49 %
+//   forward  6113 x 2048   bf16, 4 sequences   29 us   52 %
 // Long calls of narrow types are held by the chain of one tile's steps (composition,
 // fold, look-back, evaluation: about 8,500 cycles at two CTAs per SM, of which the
 // look-back is a quarter), which longer tiles spread over more tokens: R went from
-// 4 and 5 to the most that registers hold, 240 -> 224 us and 189 -> 181 us.  Three
+// 4 and 5 to the most that registers hold, 240 -> 226 us and 189 -> 172 us.  Three
 // and four smaller CTAs per SM (233 and 287 us forward), a larger window of the
 // look-back (4 instead of 2 rows: 195 -> 203 us) and the look-back as a function
 // of its own (173 -> 213 us) cost more in registers than they hid.  Short calls are
@@ -287,8 +287,9 @@ template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
     static constexpr int LANES = 8, CC = 64, RUNS = THREADS / LANES;  // runs of R tokens
     // A token takes 8 registers for its decays and 4 or 8 for each of b and h as
     // stored; R is the most that fits beside the rest in 128 registers (one more
-    // spills, 181 -> 220 us forward) and in shared memory at two CTAs per SM.
-    static constexpr int R = sizeof(TX) == 2 ? (BWD ? (WIDE ? 5 : 4) : WIDE && sizeof(TG) == 2 ? 7 : 6) : (BWD ? 3 : 5);
+    // spills: forward 151 -> 157 us with bf16 gates, backward 226 -> 235 us) and in
+    // shared memory at two CTAs per SM.
+    static constexpr int R = sizeof(TX) == 2 ? (BWD ? (WIDE ? 5 : 4) : WIDE ? 7 : 6) : (BWD ? 3 : 5);
     static constexpr int TT = RUNS * R;
     static constexpr int PARTS = THREADS / CC, RUNS_PART = RUNS / PARTS;  // the fold over runs, in parts
     static constexpr Layout LAYOUT = !WIDE ? kEvery8 : sizeof(TX) == 4 || sizeof(TG) == 4 ? kHalves : kNext;
@@ -608,55 +609,64 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         __syncthreads();
         const bool bounded = misc[2 + buf] != 0;  // sequences begin or end in the tile
 
-        // ---- into registers, and the composition of the thread's run
-        float a[R][8];
-        Row<TX, L> b[R], h[BWD ? R : 1];
+        // ---- into registers, and the composition of the thread's run.  The gates
+        // first and their exponentials, then the rest: the most registers at a time are
+        // those held to the tile's end anyway.  TMA has filled with zeros what lies
+        // outside the tensors; what was not staged (channels that are none, the row
+        // before the first) and rows behind the last sequence become the identity here.
         const bool full = t0 + TT <= valid;
+        auto local = [&](int r) { return BWD ? TT - 1 - (run * R + r) : run * R + r; };  // the run's token r in the tile
+        float a[R][8], A[8];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {  // TMA has filled with zeros what lies outside the tensors
-            const int i = run * R + r, l = BWD ? TT - 1 - i : i, t = t0 + l, c = group * CC;
+        for (int r = 0; r < R; ++r) {
+            const int l = local(r);
             Row<TG, L> gr;
-            gr.load(reinterpret_cast<const TG*>(smem + C::GS + l * C::PITCH_G + shift(p.g, p.ldg, c, t, sizeof(TG))) + lane_c);
+            gr.load(reinterpret_cast<const TG*>(smem + C::GS + l * C::PITCH_G +
+                                                shift(p.g, p.ldg, group * CC, t0 + l, sizeof(TG))) + lane_c);
             gr.get(a[r]);
-            b[r].load(reinterpret_cast<const TX*>(smem + C::XS + l * C::PITCH_X + shift(p.x, p.ldx, c, t, sizeof(TX))) + lane_c);
-            if (BWD)
-                h[r].load(reinterpret_cast<const TX*>(smem + C::HS + l * C::PITCH_X + shift(p.h, p.ldh, c, t - 1, sizeof(TX))) +
-                          lane_c);
         }
-        if (!WIDE) {  // nothing was staged for channels that are none, and there is no row before the first
-            if (inside < 8) {
+        if (!full || (!WIDE && inside < 8)) {
 #pragma unroll
-                for (int r = 0; r < R; ++r)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j >= inside) a[r][j] = 0.f;
-            }
-            if (BWD && t0 == 0) {
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    if (run * R + r == TT - 1) h[r].zero();
-            }
-        }
-        if (!full) {  // rows behind the last sequence: the identity
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int i = run * R + r;
-                if (t0 + (BWD ? TT - 1 - i : i) >= valid) {
-                    b[r].zero();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) a[r][j] = 0.f;  // exp(0) = 1
-                }
-            }
+                for (int j = 0; j < 8; ++j)
+                    if (t0 + local(r) >= valid || (!WIDE && j >= inside)) a[r][j] = 0.f;  // exp(0) = 1
         }
         // The run's decay is the exponential of its gates' sum: the product of its
         // tokens' decays would carry the rounding of each, and 32 runs do so after it.
-        float A[8], B[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) A[j] = B[j] = 0.f;
+        for (int j = 0; j < 8; ++j) A[j] = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) add(A, a[r]);
         decays(A);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<float4*>(ca + run * CC + C::place(lc, k)) =
+                make_float4(A[4 * k], A[4 * k + 1], A[4 * k + 2], A[4 * k + 3]);
         decays(reinterpret_cast<float (&)[R * 8]>(a));
+        Row<TX, L> b[R], h[BWD ? R : 1];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int l = local(r);
+            b[r].load(reinterpret_cast<const TX*>(smem + C::XS + l * C::PITCH_X +
+                                                  shift(p.x, p.ldx, group * CC, t0 + l, sizeof(TX))) + lane_c);
+            if (BWD)
+                h[r].load(reinterpret_cast<const TX*>(smem + C::HS + l * C::PITCH_X +
+                                                      shift(p.h, p.ldh, group * CC, t0 + l - 1, sizeof(TX))) + lane_c);
+        }
+        if (!full) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (t0 + local(r) >= valid) b[r].zero();
+        }
+        if (BWD && !WIDE && t0 == 0) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (local(r) == 0) h[r].zero();
+        }
+        float B[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) B[j] = 0.f;
         auto start_state = [&](int n, float (&f)[8]) {
             Row<float, L> s;
             s.zero();
@@ -682,11 +692,9 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         };
         bounded ? compose(std::true_type()) : compose(std::false_type());
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int at = run * CC + C::place(lc, k);
-            *reinterpret_cast<float4*>(ca + at) = make_float4(A[4 * k], A[4 * k + 1], A[4 * k + 2], A[4 * k + 3]);
-            *reinterpret_cast<float4*>(cb + at) = make_float4(B[4 * k], B[4 * k + 1], B[4 * k + 2], B[4 * k + 3]);
-        }
+        for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<float4*>(cb + run * CC + C::place(lc, k)) =
+                make_float4(B[4 * k], B[4 * k + 1], B[4 * k + 2], B[4 * k + 3]);
         if (lc == 0) cut_s[run] = cut;
         if (tid == 0) misc[0] = (int64_t)next < tiles ? (int)next : -1;
         __syncthreads();
