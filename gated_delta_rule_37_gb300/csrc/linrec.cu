@@ -166,24 +166,24 @@ __device__ __forceinline__ void decays(float (&g)[N]) {
 
 // ---- a thread's 8 elements of a row, kept as they are stored -----------------------
 //
-// kNext: neighbours, one 16-byte access of bf16.  kHalves: two runs of four, 32
+// kNext: neighbours, one 16-byte access of bf16.  kHalves: two runs of four, `d`
 // elements from one another: a warp's 16-byte accesses to fp32 rows in shared memory
 // then touch all banks in turn, and its stores whole sectors.  kEvery8: every eighth
-// element, for rows of any alignment.  `n` counts those that lie inside the tensor.
+// element, for rows of any alignment.  `n` says which lie inside the tensor: all or
+// none (kNext), bit 0 and bit 1 for the runs (kHalves), how many (kEvery8).
 
 enum Layout { kNext, kHalves, kEvery8 };
-constexpr int kHalf = 32;
 
 template <typename T, Layout L> struct Row;
 
 template <Layout L> struct Row<__nv_bfloat16, L> {
     uint4 v;
     __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, int d) {
         if (L == kNext) {
             v = *reinterpret_cast<const uint4*>(p);
         } else if (L == kHalves) {
-            const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + kHalf);
+            const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + d);
             v = make_uint4(a.x, a.y, b.x, b.y);
         } else {
             const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
@@ -198,14 +198,14 @@ template <Layout L> struct Row<__nv_bfloat16, L> {
             f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8], int n) {
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8], int n, int d) {
         const uint2 a = make_uint2(tc::pack_bf16(f[0], f[1]), tc::pack_bf16(f[2], f[3]));
         const uint2 b = make_uint2(tc::pack_bf16(f[4], f[5]), tc::pack_bf16(f[6], f[7]));
         if (L == kNext) {
             *reinterpret_cast<uint4*>(p) = make_uint4(a.x, a.y, b.x, b.y);
         } else if (L == kHalves) {
-            *reinterpret_cast<uint2*>(p) = a;
-            if (n > 4) *reinterpret_cast<uint2*>(p + kHalf) = b;
+            if (n & 1) *reinterpret_cast<uint2*>(p) = a;
+            if (n & 2) *reinterpret_cast<uint2*>(p + d) = b;
         } else {
             const uint32_t w[4] = {a.x, a.y, b.x, b.y};
             unsigned short* u = reinterpret_cast<unsigned short*>(p);
@@ -221,32 +221,35 @@ template <Layout L> struct Row<float, L> {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.f;
     }
-    __device__ __forceinline__ void load(const float* p, int n = 8) {
+    __device__ __forceinline__ void load(const float* p, int d, int n) {
         if (L == kEvery8) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (j < n) v[j] = p[8 * j];
         } else {
-            const float4 a = *reinterpret_cast<const float4*>(p);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            if (n > 4) {
-                const float4 b = *reinterpret_cast<const float4*>(p + (L == kHalves ? kHalf : 4));
+            if (n & 1) {
+                const float4 a = *reinterpret_cast<const float4*>(p);
+                v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            }
+            if (n & 2) {
+                const float4 b = *reinterpret_cast<const float4*>(p + (L == kHalves ? d : 4));
                 v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
             }
         }
     }
+    __device__ __forceinline__ void load(const float* p, int d) { load(p, d, L == kEvery8 ? 8 : 3); }
     __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = v[j];
     }
-    static __device__ __forceinline__ void store(float* p, const float (&f)[8], int n) {
+    static __device__ __forceinline__ void store(float* p, const float (&f)[8], int n, int d) {
         if (L == kEvery8) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (j < n) p[8 * j] = f[j];
         } else {
-            *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-            if (n > 4) *reinterpret_cast<float4*>(p + (L == kHalves ? kHalf : 4)) = make_float4(f[4], f[5], f[6], f[7]);
+            if (n & 1) *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+            if (n & 2) *reinterpret_cast<float4*>(p + (L == kHalves ? d : 4)) = make_float4(f[4], f[5], f[6], f[7]);
         }
     }
 };
@@ -276,15 +279,15 @@ __device__ __forceinline__ void product(float (&o)[8], const float (&a)[8], cons
 
 // ---- the tile kernel --------------------------------------------------------------
 
-// 64 channels per tile, 8 per thread.  WIDE: aligned rows, staged by TMA.  Otherwise
-// each row's segment is staged by a bulk copy of the 16-byte blocks around it, and
+// 8 channels per thread.  WIDE: 32 channels per tile, aligned rows, staged by TMA.  Otherwise
+// 64, and each row's segment is staged by a bulk copy of the 16-byte blocks around it, and
 // read from where it lies in them: about 60 cycles to issue, so six warps issue them
 // while two look back (one warp for all took 17,600 cycles of a tile; 4-byte
 // asynchronous copies by all warps before the fold took 3,200 to 10,700).
 template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
     static constexpr int THREADS = 256, CTAS = 2, WARPS = THREADS / 32;
     static constexpr int COPIERS = WARPS - 2;  // warps that issue bulk copies, while the others look back
-    static constexpr int LANES = 8, CC = 64, RUNS = THREADS / LANES;  // runs of R tokens
+    static constexpr int LANES = WIDE ? 4 : 8, CC = 8 * LANES, RUNS = THREADS / LANES;  // runs of R tokens
     // A token takes 8 registers for its decays and 4 or 8 for each of b and h as
     // stored; R is the most that fits beside the rest in 128 registers (one more
     // spills: forward 151 -> 157 us with bf16 gates, backward 226 -> 235 us) and in
@@ -301,19 +304,25 @@ template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
     static constexpr int TA = PB + PARTS * CC * 4, TB = TA + CC * 4, CARRY = TB + CC * 4;
     static constexpr int FIRST = CARRY + CC * 4, LAST = FIRST + 2 * TT * 4, CUT = LAST + 2 * TT * 4;
     static constexpr int MISC = CUT + RUNS * 4, BYTES_SMEM = MISC + 64;
-    static_assert(RUNS % PARTS == 0 && STAGE % 128 == 0 && TT <= 256 && CC == 2 * kHalf && CC == 8 * LANES, "tile shape");
+    static constexpr int BOX = TT > 256 ? TT / 2 : TT;  // tokens of a TMA copy
+    static_assert(RUNS % PARTS == 0 && STAGE % 128 == 0 && TT % BOX == 0 && BOX <= 256 && BOX * CC * 2 % 128 == 0, "tile shape");
     static_assert(CTAS * (BYTES_SMEM + 1024) <= 228 * 1024, "shared memory of the CTAs of an SM");
-    // the first of a lane's channels
-    static __device__ __forceinline__ int channel(int lane) {
-        return LAYOUT == kNext ? lane * 8 : LAYOUT == kHalves ? lane * 4 : lane;
+    // A lane's first channel, and how far its second run of four is (kHalves: runs of
+    // odd number begin with the second half, so that the two runs that share a
+    // quarter of a warp's access take different banks).
+    static __device__ __forceinline__ int channel(int lane, int run) {
+        return LAYOUT == kNext ? lane * 8 : LAYOUT == kHalves ? lane * 4 + (run & 1) * (CC / 2) : lane;
     }
-    // how many of its channels lie below D, from its first one
-    static __device__ __forceinline__ int inside(int c, int D) {
-        return LAYOUT == kNext ? (c < D ? 8 : 0) : LAYOUT == kHalves ? (c < D ? 4 : 0) + (c + kHalf < D ? 4 : 0)
+    static __device__ __forceinline__ int apart(int run) { return LAYOUT == kHalves && (run & 1) ? -CC / 2 : CC / 2; }
+    // Which of its channels lie below D, from its first one.
+    static __device__ __forceinline__ int inside(int c, int d, int D) {
+        return LAYOUT == kNext ? (c < D ? 3 : 0) : LAYOUT == kHalves ? (c < D ? 1 : 0) + (c + d < D ? 2 : 0)
                                                                      : min(max((D - c + 7) / 8, 0), 8);
     }
-    // where a lane's channels lie in the arrays of compositions: two runs of four
-    static __device__ __forceinline__ int place(int lane, int half) { return lane * 4 + half * kHalf; }
+    // Where its channels lie in the arrays of compositions: two runs of four.
+    static __device__ __forceinline__ int place(int lane, int run, int k) {
+        return lane * 4 + (LAYOUT == kHalves ? k ^ (run & 1) : k) * (CC / 2);
+    }
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c, int t, uint32_t mbar) {
@@ -535,6 +544,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int lc = lane % C::LANES, run = warp * (32 / C::LANES) + lane / C::LANES;
+    const int lane_c = C::channel(lc, run), apart = C::apart(run);
     const int part = tid / CC, pos = tid % CC;
     const bool many = p.rows > 1 && !p.clustered;
 
@@ -556,9 +566,12 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         const int c = tile % p.groups * CC, t0 = token0(tile);
         if constexpr (WIDE) {
             tc::mbar_arrive_tx(mbar, C::STAGE);
-            tma_load_2d(tc::smem_u32(smem + C::XS), &map_x, c, t0, mbar);
-            tma_load_2d(tc::smem_u32(smem + C::GS), &map_g, c, t0, mbar);
-            if (BWD) tma_load_2d(tc::smem_u32(smem + C::HS), &map_h, c, t0 - 1, mbar);  // row t - 1 beside token t
+            for (int l = 0; l < TT; l += C::BOX) {
+                tma_load_2d(tc::smem_u32(smem + C::XS + l * C::PITCH_X), &map_x, c, t0 + l, mbar);
+                tma_load_2d(tc::smem_u32(smem + C::GS + l * C::PITCH_G), &map_g, c, t0 + l, mbar);
+                if (BWD)  // row t - 1 beside token t
+                    tma_load_2d(tc::smem_u32(smem + C::HS + l * C::PITCH_X), &map_h, c, t0 + l - 1, mbar);
+            }
         } else {
             for (int l = warp - 2 + C::COPIERS * lane; l < min(TT, valid - t0); l += 32 * C::COPIERS) {
                 const int64_t t = t0 + l;
@@ -596,7 +609,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     for (int it = 0; tile >= 0; ++it) {
         const int buf = it & 1;
         const int row = tile / p.groups, group = tile - row * p.groups, t0 = (BWD ? rows - 1 - row : row) * TT;
-        const int lane_c = C::channel(lc), c0 = group * CC + lane_c, inside = C::inside(c0, p.D);
+        const int c0 = group * CC + lane_c, inside = C::inside(c0, apart, p.D);
         const int* first = reinterpret_cast<int*>(smem + C::FIRST) + buf * TT;
         const int* last = reinterpret_cast<int*>(smem + C::LAST) + buf * TT;
         unsigned next = 0xffffffffu;  // looked at after the composition: the counter's answer takes its time
@@ -622,7 +635,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             const int l = local(r);
             Row<TG, L> gr;
             gr.load(reinterpret_cast<const TG*>(smem + C::GS + l * C::PITCH_G +
-                                                shift(p.g, p.ldg, group * CC, t0 + l, sizeof(TG))) + lane_c);
+                                                shift(p.g, p.ldg, group * CC, t0 + l, sizeof(TG))) + lane_c, apart);
             gr.get(a[r]);
         }
         if (!full || (!WIDE && inside < 8)) {
@@ -641,7 +654,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         decays(A);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<float4*>(ca + run * CC + C::place(lc, k)) =
+            *reinterpret_cast<float4*>(ca + run * CC + C::place(lc, run, k)) =
                 make_float4(A[4 * k], A[4 * k + 1], A[4 * k + 2], A[4 * k + 3]);
         decays(reinterpret_cast<float (&)[R * 8]>(a));
         Row<TX, L> b[R], h[BWD ? R : 1];
@@ -649,10 +662,10 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         for (int r = 0; r < R; ++r) {
             const int l = local(r);
             b[r].load(reinterpret_cast<const TX*>(smem + C::XS + l * C::PITCH_X +
-                                                  shift(p.x, p.ldx, group * CC, t0 + l, sizeof(TX))) + lane_c);
+                                                  shift(p.x, p.ldx, group * CC, t0 + l, sizeof(TX))) + lane_c, apart);
             if (BWD)
                 h[r].load(reinterpret_cast<const TX*>(smem + C::HS + l * C::PITCH_X +
-                                                      shift(p.h, p.ldh, group * CC, t0 + l - 1, sizeof(TX))) + lane_c);
+                                                      shift(p.h, p.ldh, group * CC, t0 + l - 1, sizeof(TX))) + lane_c, apart);
         }
         if (!full) {
 #pragma unroll
@@ -670,7 +683,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         auto start_state = [&](int n, float (&f)[8]) {
             Row<float, L> s;
             s.zero();
-            if (p.start && inside) s.load(p.start + (int64_t)n * p.D + c0, inside);
+            if (p.start && inside) s.load(p.start + (int64_t)n * p.D + c0, apart, inside);
             s.get(f);
         };
         int cut = 0;
@@ -693,7 +706,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         bounded ? compose(std::true_type()) : compose(std::false_type());
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<float4*>(cb + run * CC + C::place(lc, k)) =
+            *reinterpret_cast<float4*>(cb + run * CC + C::place(lc, run, k)) =
                 make_float4(B[4 * k], B[4 * k + 1], B[4 * k + 2], B[4 * k + 3]);
         if (lc == 0) cut_s[run] = cut;
         if (tid == 0) misc[0] = (int64_t)next < tiles ? (int)next : -1;
@@ -821,7 +834,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             float s[8];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float4 u = *reinterpret_cast<const float4*>(ca + run * CC + C::place(lc, k));
+                const float4 u = *reinterpret_cast<const float4*>(ca + run * CC + C::place(lc, run, k));
                 s[4 * k] = u.x; s[4 * k + 1] = u.y; s[4 * k + 2] = u.z; s[4 * k + 3] = u.w;
             }
             // ---- every token from its state
@@ -845,23 +858,23 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                     if (BWD) {
                         float before[8];
                         add(f, s);  // lam
-                        Row<TX, L>::store(out, f, inside);
+                        Row<TX, L>::store(out, f, inside, apart);
                         product(s, a[r], f);  // mu
                         h[r].get(before);
                         if (decltype(cutting)::value && n_last >= 0) {  // before the first token: h0
                             Row<float, L> z;
                             z.zero();
-                            if (p.h0) z.load(p.h0 + (int64_t)n_last * p.D + c0, inside);
+                            if (p.h0) z.load(p.h0 + (int64_t)n_last * p.D + c0, apart, inside);
                             z.get(before);
                         }
                         product(before, before, s);
-                        Row<TG, L>::store(dg, before, inside);
+                        Row<TG, L>::store(dg, before, inside, apart);
                     } else {
                         advance<BWD>(s, a[r], f);
-                        Row<TX, L>::store(out, s, inside);
+                        Row<TX, L>::store(out, s, inside, apart);
                     }
                     if (decltype(cutting)::value && n_last >= 0 && p.last)
-                        Row<float, L>::store(p.last + (int64_t)n_last * p.D + c0, s, inside);
+                        Row<float, L>::store(p.last + (int64_t)n_last * p.D + c0, s, inside, apart);
                 }
             };
             bounded || !full ? evaluate(std::true_type()) : evaluate(std::false_type());
@@ -995,9 +1008,9 @@ cudaError_t launch_tiles(LinrecParams p, void* ws, cudaStream_t s) {
     p.rows = l.rows;
     p.clustered = l.clustered;
     CUtensorMap mx{}, mg{}, mh{};
-    if (WIDE && !(encode_rows<TX>(&mx, p.x, p.ldx, p.T, p.D, C::TT, C::CC) &&
-                  encode_rows<TG>(&mg, p.g, p.ldg, p.T, p.D, C::TT, C::CC) &&
-                  (!BWD || encode_rows<TX>(&mh, p.h, p.ldh, p.T, p.D, C::TT, C::CC))))
+    if (WIDE && !(encode_rows<TX>(&mx, p.x, p.ldx, p.T, p.D, C::BOX, C::CC) &&
+                  encode_rows<TG>(&mg, p.g, p.ldg, p.T, p.D, C::BOX, C::CC) &&
+                  (!BWD || encode_rows<TX>(&mh, p.h, p.ldh, p.T, p.D, C::BOX, C::CC))))
         return cudaErrorInvalidValue;
     p.err = device_error_word();
     if (!p.err) return cudaErrorInitializationError;
