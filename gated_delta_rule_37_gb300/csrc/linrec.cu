@@ -85,6 +85,7 @@ struct LinrecParams {
     unsigned int* err;
 };
 
+constexpr int kMaxTileTokens = 512;         // a tile's at most: token numbers are 32-bit, a tile's last one included
 constexpr unsigned kNothing = 0xffffffffu;  // a NaN that arithmetic does not give
 constexpr int kHeadWords = 64;
 constexpr unsigned kScanError = 0x200;  // device error word: a tile's wait gave up
@@ -305,6 +306,7 @@ template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
     static constexpr int FIRST = CARRY + CC * 4, LAST = FIRST + 2 * TT * 4, CUT = LAST + 2 * TT * 4;
     static constexpr int MISC = CUT + RUNS * 4, BYTES_SMEM = MISC + 64;
     static constexpr int BOX = TT > 256 ? TT / 2 : TT;  // tokens of a TMA copy
+    static_assert(TT <= kMaxTileTokens, "T_total's limit");
     static_assert(RUNS % PARTS == 0 && STAGE % 128 == 0 && TT % BOX == 0 && BOX <= 256 && BOX * CC * 2 % 128 == 0, "tile shape");
     static_assert(CTAS * (BYTES_SMEM + 1024) <= 228 * 1024, "shared memory of the CTAs of an SM");
     // A lane's first channel, and how far its second run of four is (kHalves: runs of
@@ -1253,8 +1255,8 @@ int check_sizes(int N, int64_t T, int D, int dtype, int gate_dtype) {
     if (dtype != GDR_BF16 && dtype != GDR_F32) return set_last_error(GDR_ERR_UNSUPPORTED, "dtype %d", dtype);
     if (gate_dtype != GDR_BF16 && gate_dtype != GDR_F32)
         return set_last_error(GDR_ERR_UNSUPPORTED, "gate_dtype %d", gate_dtype);
-    // token numbers are 32-bit in the kernels, a tile's beyond the last token included
-    if (T > 0x7fffff00LL) return set_last_error(GDR_ERR_UNSUPPORTED, "T_total (%lld) above 2^31 - 256", (long long)T);
+    if (T > 0x7fffffffLL - kMaxTileTokens + 1)
+        return set_last_error(GDR_ERR_UNSUPPORTED, "T_total (%lld) above 2^31 - 512", (long long)T);
     if (N > 0x7fffffff / 2) return set_last_error(GDR_ERR_UNSUPPORTED, "N too large");
     if (D > 1 << 24) return set_last_error(GDR_ERR_UNSUPPORTED, "D (%d) above 2^24", D);
     if (T > 0 && N == 0) return set_last_error(GDR_ERR_INVALID_ARG, "T_total > 0 with N == 0");
@@ -1268,6 +1270,13 @@ int check_ints(const char* name, const void* p) {
     if (!p) return set_last_error(GDR_ERR_INVALID_ARG, "null pointer argument (%s)", name);
     if (reinterpret_cast<uintptr_t>(p) & 3u)
         return set_last_error(GDR_ERR_INVALID_ARG, "%s not 4-byte aligned", name);
+    return GDR_OK;
+}
+
+// A sequence's last state may be written while another tile has yet to read its first.
+int check_apart(const char* name, const float* written, const float* read) {
+    if (written && written == read)
+        return set_last_error(GDR_ERR_INVALID_ARG, "%s must not be a state that the call reads", name);
     return GDR_OK;
 }
 
@@ -1319,6 +1328,7 @@ int gdr_linrec_fwd(const void* x, int64_t x_stride, const void* g, int64_t g_str
         return set_last_error(GDR_ERR_INVALID_ARG, "unsupported flags 0x%x for gdr_linrec_fwd", flags);
     if (int rc = check_aligned16("initial_state", initial_state)) return rc;
     if (int rc = check_aligned16("final_state", final_state)) return rc;
+    if (int rc = check_apart("final_state", final_state, initial_state)) return rc;
     cudaStream_t s = (cudaStream_t)stream;
     if (T_total == 0) return pass_states(initial_state, final_state, N, D, s);
     if (int rc = check_rows("x", x, x_stride, 0, element(dtype))) return rc;
@@ -1346,6 +1356,8 @@ int gdr_linrec_bwd(const void* dy, int64_t dy_stride, const void* g, int64_t g_s
     if (int rc = check_aligned16("initial_state", initial_state)) return rc;
     if (int rc = check_aligned16("d_final_state", d_final_state)) return rc;
     if (int rc = check_aligned16("d_initial_state", d_initial_state)) return rc;
+    if (int rc = check_apart("d_initial_state", d_initial_state, initial_state)) return rc;
+    if (int rc = check_apart("d_initial_state", d_initial_state, d_final_state)) return rc;
     cudaStream_t s = (cudaStream_t)stream;
     if (T_total == 0) return pass_states(d_final_state, d_initial_state, N, D, s);
     if (int rc = check_rows("dy", dy, dy_stride, 0, element(dtype))) return rc;

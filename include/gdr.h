@@ -280,7 +280,7 @@ GDR_API int gdr_gating_fwd(const void* a, const float* dt_bias, const float* A_l
  *     multiples of 8 take the fast path.
  *   - dtype (GDR_BF16 or GDR_F32) is that of x, y and their gradients,
  *     gate_dtype (GDR_BF16 or GDR_F32) that of g and dg.  Prefill states are
- *     fp32 [N, D], dense.
+ *     fp32 [N, D], dense; the one that is written is not one that is read.
  *   - cu_seqlens [N+1] int32 device, cu[0] = 0, non-decreasing; sequences may
  *     be empty.  cu[N] may be less than T_total (a padded batch): rows from
  *     cu[N] on are neither read nor written.  A cu_seqlens that breaks these
@@ -293,7 +293,7 @@ GDR_API int gdr_gating_fwd(const void* a, const float* dt_bias, const float* A_l
  *     before it, which are running by then.  Every wait is bounded (one second):
  *     one that gives up is reported by gdr_get_device_status, and what the call
  *     has not written by then stays unwritten.
- *   - D up to 2^24, T_total up to 2^31 - 256.
+ *   - D up to 2^24, T_total up to 2^31 - 512.
  *
  * gdr_linrec_workspace_size -- bytes of device workspace that gdr_linrec_fwd
  * and gdr_linrec_bwd need (the same for both; may be 0).  Host only.

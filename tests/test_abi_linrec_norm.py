@@ -36,7 +36,9 @@ def _fwd(lib, **kw):
     (dict(D=(1 << 24) + 1, ldx=1 << 25, ldg=1 << 25, ldy=1 << 25), UNSUPPORTED),
     (dict(D=0), INVALID), (dict(N=-1), INVALID), (dict(T=-1), INVALID), (dict(N=0), INVALID),
     (dict(dtype=E4M3), UNSUPPORTED), (dict(gate=7), UNSUPPORTED), (dict(T=1 << 31), UNSUPPORTED),
+    (dict(T=(1 << 31) - 511), UNSUPPORTED), (dict(T=(1 << 31) - 512, wn=16), WORKSPACE),
     (dict(flags=gdr.GDR_COMMIT), INVALID), (dict(flags=0x40), INVALID),
+    (dict(h0=P(512), hT=P(512)), INVALID), (dict(h0=P(512), hT=P(512), T=0), INVALID),   # the state in place
 ])
 def test_linrec_fwd_rejects_before_launch(lib, kw, code):
     assert _fwd(lib, **kw) == code
@@ -76,6 +78,7 @@ def _bwd(lib, **kw):
     (dict(dg=None), INVALID), (dict(cu=None), INVALID), (dict(y=P(49)), INVALID), (dict(dg=P(98)), INVALID),
     (dict(ldx=8), INVALID), (dict(lddg=8), INVALID), (dict(df=P(8)), INVALID), (dict(d0=P(8)), INVALID),
     (dict(h0=P(8)), INVALID), (dict(dtype=2), UNSUPPORTED), (dict(flags=4), INVALID), (dict(N=0), INVALID),
+    (dict(df=P(512), d0=P(512)), INVALID), (dict(h0=P(512), d0=P(512)), INVALID),        # the state in place
 ])
 def test_linrec_bwd_rejects_before_launch(lib, kw, code):
     assert _bwd(lib, **kw) == code

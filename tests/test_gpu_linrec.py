@@ -169,6 +169,45 @@ def test_fwd_and_bwd(lens, D, types):
     check_bwd(c, *run_bwd(c))
 
 
+@pytest.mark.parametrize("types", TYPES, ids=lambda t: "-".join(str(d)[6:] for d in t))
+@pytest.mark.parametrize("D", [72, 65])
+@pytest.mark.parametrize("lens", [[192, 192, 320, 448, 1], [448], [320, 0, 320, 0], [191, 1, 193, 447, 1, 449, 319, 321],
+                                  [192 * 35], [64, 1, 64 * 105 - 1]],
+                         ids=["ends of tiles", "one", "two", "around", "whole tiles", "a token before"])
+def test_sequences_that_end_with_tiles(lens, D, types):
+    """Tiles are 96 to 448 tokens, by type and direction: sequences that end
+    with them, just before and just behind, in calls of one row of tiles, of a
+    few and of many."""
+    c = make(26 + len(lens), lens, D, *types)
+    check_fwd(c, *run_fwd(c))
+    check_bwd(c, *run_bwd(c))
+
+
+@pytest.mark.parametrize("D", [2080, 2081])
+def test_offsets_beyond_32_bits(D):
+    """Rows whose elements' numbers pass 2^31 (and bytes 2^32): the last
+    sequence of a long batch, against 64 bits."""
+    T, n = (1 << 20) + 5, 700
+    assert (T - n) * D > 1 << 31
+    big = {}
+    for k in ("x", "y"):
+        big[k] = torch.zeros(T, D, dtype=BF, device=DEV)
+    big["g"] = torch.full((T, D), -1.0, dtype=BF, device=DEV)
+    c = make(31, [n], D, BF, BF)
+    for k, v in big.items():
+        v[T - n:] = c[k].to(DEV)
+    cu = torch.tensor([0, T - n, T], dtype=torch.int32, device=DEV)
+    h0 = torch.cat([torch.zeros(1, D), c["h0"]]).to(DEV)
+    df = torch.cat([torch.zeros(1, D), c["df"]]).to(DEV)
+    y, hT = gdr.linrec_fwd(big["x"], big["g"], cu, initial_state=h0)
+    check_fwd(c, y[T - n:].cpu(), hT[1:].cpu())
+    assert not y[:T - n].any() and not hT[0].any()
+    del y
+    dx, dg, d0 = gdr.linrec_bwd(big["x"], big["g"], big["y"], cu, initial_state=h0, d_final_state=df)
+    check_bwd(c, dx[T - n:].cpu(), dg[T - n:].cpu(), d0[1:].cpu())
+    assert not dx[:T - n].any() and not dg[:T - n].any() and not d0[0].any()
+
+
 def test_without_states():
     c = make(3, [40, 0, 300], 72, BF, F)
     check_fwd(c, *run_fwd(c, h0=False), h0=False)

@@ -145,6 +145,33 @@ def test_bwd(M, D, dtype):
         assert none is None and bits_equal(only, dx.view)
 
 
+@pytest.mark.parametrize("D", [2080, 2081])
+def test_offsets_beyond_32_bits(D):
+    """Rows whose elements' numbers pass 2^31: the last ones against 64 bits."""
+    M, n = (1 << 20) + 5, 50
+    assert (M - n) * D > 1 << 31
+    c = make(41, n, D, BF)
+    big = {}
+    for k in ("x", "r", "dy", "ds"):
+        big[k] = torch.zeros(M, D, dtype=BF, device=DEV)
+        big[k][M - n:] = c[k].to(DEV)
+    w = c["w"].to(DEV)
+    for y_dtype, group in ((BF, 0), (E4, 32)):
+        y, ro, sc = gdr.rmsnorm_fwd(big["x"], w, residual=big["r"], eps=EPS, y_dtype=y_dtype, scale_group=group)
+        check_fwd(c, y[M - n:].cpu(), ro[M - n:].cpu(), sc[M - n:].cpu() if group else None, residual=True, group=group)
+        assert not ro[:M - n].any() and not (y[:M - n].view(torch.int8) & 0x7f).any()
+        del y, ro, sc
+    s, dy = f64(c["x"]), f64(c["dy"])
+    rs, rw = oracle.rmsnorm_bwd(dy, s, f64(c["w"]), EPS)
+    r = 1 / np.sqrt((s * s).mean(1, keepdims=True) + EPS)
+    terms = r * np.abs(f64(c["w"]) * dy) + r ** 3 * np.abs(s) * np.abs(s * f64(c["w"]) * dy).mean(1, keepdims=True)
+    dx, dw = gdr.rmsnorm_bwd(big["dy"], big["x"], w, eps=EPS, d_residual_out=big["ds"])
+    want = rs + f64(c["ds"])
+    check(dx[M - n:].cpu(), want, 160 * U * terms + (U + half_step(BF)) * np.abs(want), "dx")
+    check(dw.cpu(), rw, 400 * U * np.abs(r * dy * s).sum(0), "dweight")
+    assert not dx[:M - n].any()
+
+
 @pytest.mark.parametrize("D", [64, 1001, 4096])
 def test_gradient_against_differences(D):
     """The kernel's gradient against differences of the kernel's own forward, in fp32."""
