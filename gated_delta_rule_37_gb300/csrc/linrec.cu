@@ -36,20 +36,24 @@
 //
 // What bounds it.  Less than two flops per byte: memory.  The floor of a call is
 // its rows' bytes at the copy rate (6.69 TB/s measured); one GB300, device times:
-//   forward  32768 x 4096  bf16, fp32 gates   172 us   93 %    (bf16 gates 151 us, 80 %;
-//                          fp32, 16384 rows   127 us   95 %)
-//   backward 32768 x 4096  bf16, bf16 gates   226 us   89 %    (fp32 gates 283 us, 99 %;
-//                          fp32, 16384 rows   207 us   97 %)
-//   backward 7001 x 1001   fp32, odd rows      48 us   44 %
-//   forward  6113 x 2048   bf16, 4 sequences   29 us   52 %
+//   forward  32768 x 4096  bf16, fp32 gates   167 us   96 %    (bf16 gates 148 us, 81 %;
+//                          fp32, 16384 rows   123 us   98 %)
+//   backward 32768 x 4096  bf16, bf16 gates   214 us   94 %    (fp32 gates 275 us, 102 %;
+//                          fp32, 16384 rows   200 us  100 %)
+//   backward 7001 x 1001   fp32, odd rows      47 us   45 %    (50000 rows 233 us, 64 %)
+//   forward  6113 x 2048   bf16, 4 sequences   30 us   50 %
 // Long calls of narrow types are held by the chain of one tile's steps (composition,
-// fold, look-back, evaluation: about 8,500 cycles at two CTAs per SM, of which the
-// look-back is a quarter), which longer tiles spread over more tokens: R went from
-// 4 and 5 to the most that registers hold, 240 -> 226 us and 189 -> 172 us.  Three
-// and four smaller CTAs per SM (233 and 287 us forward), a larger window of the
-// look-back (4 instead of 2 rows: 195 -> 203 us) and the look-back as a function
-// of its own (173 -> 213 us) cost more in registers than they hid.  Short calls are
-// bound by their first tile's latency, odd rows by their scalar stores.
+// fold, look-back, evaluation: about 10,500 cycles at two CTAs per SM, of which the
+// look-back is a seventh), which longer tiles spread over more tokens: R is the most
+// that registers hold, and tiles are narrow, which also leaves fewer tiles of one
+// channel group in flight to look back over (64 channels by half the tokens: 172 and
+// 226 us forward and backward; 16 channels by twice: 238 and 277).  Three and four
+// smaller CTAs per SM (233 and 287 us forward), a larger window of the look-back (4
+// instead of 2 rows: 195 -> 203 us; 16 rows a trip farther back instead of 8: 167 ->
+// 172 us) and the look-back as a function of its own (173 -> 213 us) cost more in
+// registers than they hid.  Short calls are bound by their first tile's latency and,
+// like narrow ones, by the look-back over the tiles in flight; odd rows by
+// element-wise copies and stores.
 #include <cuda.h>
 #include <math.h>
 
@@ -291,7 +295,7 @@ template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
     static constexpr int LANES = WIDE ? 4 : 8, CC = 8 * LANES, RUNS = THREADS / LANES;  // runs of R tokens
     // A token takes 8 registers for its decays and 4 or 8 for each of b and h as
     // stored; R is the most that fits beside the rest in 128 registers (one more
-    // spills: forward 151 -> 157 us with bf16 gates, backward 226 -> 235 us) and in
+    // spilled: forward 151 -> 157 us with bf16 gates, backward 226 -> 235 us) and in
     // shared memory at two CTAs per SM.
     static constexpr int R = sizeof(TX) == 2 ? (BWD ? (WIDE ? 5 : 4) : WIDE ? 7 : 6) : (BWD ? 3 : 5);
     static constexpr int TT = RUNS * R;
@@ -915,8 +919,8 @@ __global__ void linrec_clear_kernel(uint4* w, int64_t n) {
 // ---- workspace and launch ------------------------------------------------------------
 
 // Up to 8 tile rows whose tiles all fit on the GPU at once are a cluster per channel
-// group: one launch, no workspace.  On the device about the same (1200 tokens by 1024
-// channels 7.5 us, with the look-back 8.1 us); for the host one launch and one
+// group: one launch, no workspace.  On the device a little faster (1200 tokens by 1024
+// channels 8.0 us, with the look-back 8.7 us); for the host one launch and one
 // allocation less (16 instead of 22 us a call).
 constexpr int kMaxCluster = 8, kMaxClusterTiles = 304;
 
