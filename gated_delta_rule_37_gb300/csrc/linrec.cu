@@ -40,7 +40,7 @@
 //                          fp32, 16384 rows   123 us   98 %)
 //   backward 32768 x 4096  bf16, bf16 gates   214 us   94 %    (fp32 gates 275 us, 102 %;
 //                          fp32, 16384 rows   200 us  100 %)
-//   backward 7001 x 1001   fp32, odd rows      47 us   45 %    (50000 rows 233 us, 64 %)
+//   backward 7001 x 1001   fp32, odd rows      43 us   49 %    (50000 rows 195 us, 77 %)
 //   forward  6113 x 2048   bf16, 4 sequences   30 us   50 %
 // Long calls of narrow types are held by the chain of one tile's steps (composition,
 // fold, look-back, evaluation: about 10,500 cycles at two CTAs per SM, of which the
@@ -169,15 +169,16 @@ __device__ __forceinline__ void decays(float (&g)[N]) {
     }
 }
 
-// ---- a thread's 8 elements of a row, kept as they are stored -----------------------
+// ---- a thread's elements of a row, kept as they are stored -------------------------
 //
-// kNext: neighbours, one 16-byte access of bf16.  kHalves: two runs of four, `d`
+// kNext: 8 neighbours, one 16-byte access of bf16.  kHalves: two runs of four, `d`
 // elements from one another: a warp's 16-byte accesses to fp32 rows in shared memory
-// then touch all banks in turn, and its stores whole sectors.  kEvery8: every eighth
-// element, for rows of any alignment.  `n` says which lie inside the tensor: all or
-// none (kNext), bit 0 and bit 1 for the runs (kHalves), how many (kEvery8).
+// then touch all banks in turn, and its stores whole sectors.  kApart: two elements 32
+// apart, for rows of any alignment: a warp's accesses are 32 neighbours.  `n` says
+// which lie inside the tensor: all or none (kNext), bit 0 and bit 1 for the runs
+// (kHalves), how many (kApart).
 
-enum Layout { kNext, kHalves, kEvery8 };
+enum Layout { kNext, kHalves, kApart };
 
 template <typename T, Layout L> struct Row;
 
@@ -187,12 +188,9 @@ template <Layout L> struct Row<__nv_bfloat16, L> {
     __device__ __forceinline__ void load(const __nv_bfloat16* p, int d) {
         if (L == kNext) {
             v = *reinterpret_cast<const uint4*>(p);
-        } else if (L == kHalves) {
+        } else {
             const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + d);
             v = make_uint4(a.x, a.y, b.x, b.y);
-        } else {
-            const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
-            v = make_uint4(u[0] | u[8] << 16, u[16] | u[24] << 16, u[32] | u[40] << 16, u[48] | u[56] << 16);
         }
     }
     __device__ __forceinline__ void get(float (&f)[8]) const {
@@ -208,16 +206,26 @@ template <Layout L> struct Row<__nv_bfloat16, L> {
         const uint2 b = make_uint2(tc::pack_bf16(f[4], f[5]), tc::pack_bf16(f[6], f[7]));
         if (L == kNext) {
             *reinterpret_cast<uint4*>(p) = make_uint4(a.x, a.y, b.x, b.y);
-        } else if (L == kHalves) {
+        } else {
             if (n & 1) *reinterpret_cast<uint2*>(p) = a;
             if (n & 2) *reinterpret_cast<uint2*>(p + d) = b;
-        } else {
-            const uint32_t w[4] = {a.x, a.y, b.x, b.y};
-            unsigned short* u = reinterpret_cast<unsigned short*>(p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) u[8 * j] = (unsigned short)(w[j / 2] >> (16 * (j & 1)));
         }
+    }
+};
+template <> struct Row<__nv_bfloat16, kApart> {
+    uint32_t v;
+    __device__ __forceinline__ void zero() { v = 0; }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, int) {
+        const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
+        v = u[0] | u[32] << 16;
+    }
+    __device__ __forceinline__ void get(float (&f)[2]) const {
+        f[0] = __uint_as_float(v << 16);
+        f[1] = __uint_as_float(v & 0xffff0000u);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[2], int n, int) {
+        if (n > 0) p[0] = __float2bfloat16_rn(f[0]);
+        if (n > 1) p[32] = __float2bfloat16_rn(f[1]);
     }
 };
 template <Layout L> struct Row<float, L> {
@@ -226,81 +234,90 @@ template <Layout L> struct Row<float, L> {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.f;
     }
-    __device__ __forceinline__ void load(const float* p, int d, int n) {
-        if (L == kEvery8) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) v[j] = p[8 * j];
-        } else {
-            if (n & 1) {
-                const float4 a = *reinterpret_cast<const float4*>(p);
-                v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            }
-            if (n & 2) {
-                const float4 b = *reinterpret_cast<const float4*>(p + (L == kHalves ? d : 4));
-                v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-            }
+    __device__ __forceinline__ void load(const float* p, int d, int n = 3) {
+        if (n & 1) {
+            const float4 a = *reinterpret_cast<const float4*>(p);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        }
+        if (n & 2) {
+            const float4 b = *reinterpret_cast<const float4*>(p + (L == kHalves ? d : 4));
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         }
     }
-    __device__ __forceinline__ void load(const float* p, int d) { load(p, d, L == kEvery8 ? 8 : 3); }
     __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = v[j];
     }
     static __device__ __forceinline__ void store(float* p, const float (&f)[8], int n, int d) {
-        if (L == kEvery8) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) p[8 * j] = f[j];
-        } else {
-            if (n & 1) *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-            if (n & 2) *reinterpret_cast<float4*>(p + (L == kHalves ? d : 4)) = make_float4(f[4], f[5], f[6], f[7]);
-        }
+        if (n & 1) *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+        if (n & 2) *reinterpret_cast<float4*>(p + (L == kHalves ? d : 4)) = make_float4(f[4], f[5], f[6], f[7]);
+    }
+};
+template <> struct Row<float, kApart> {
+    float v[2];
+    __device__ __forceinline__ void zero() { v[0] = v[1] = 0.f; }
+    __device__ __forceinline__ void load(const float* p, int, int n = 2) {
+        if (n > 0) v[0] = p[0];
+        if (n > 1) v[1] = p[32];
+    }
+    __device__ __forceinline__ void get(float (&f)[2]) const {
+        f[0] = v[0];
+        f[1] = v[1];
+    }
+    static __device__ __forceinline__ void store(float* p, const float (&f)[2], int n, int) {
+        if (n > 0) p[0] = f[0];
+        if (n > 1) p[32] = f[1];
     }
 };
 
-__device__ __forceinline__ float2 pair(const float (&f)[8], int i) { return make_float2(f[2 * i], f[2 * i + 1]); }
-__device__ __forceinline__ void put(float (&f)[8], int i, float2 v) {
+template <int N> __device__ __forceinline__ float2 pair(const float (&f)[N], int i) {
+    return make_float2(f[2 * i], f[2 * i + 1]);
+}
+template <int N> __device__ __forceinline__ void put(float (&f)[N], int i, float2 v) {
     f[2 * i] = v.x;
     f[2 * i + 1] = v.y;
 }
 
 // One token of the scan: h <- a h + b, or h <- a (h + b) from the end.
-template <bool BWD>
-__device__ __forceinline__ void advance(float (&h)[8], const float (&a)[8], const float (&b)[8]) {
+template <bool BWD, int N>
+__device__ __forceinline__ void advance(float (&h)[N], const float (&a)[N], const float (&b)[N]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < N / 2; ++i)
         put(h, i, BWD ? __fmul2_rn(pair(a, i), __fadd2_rn(pair(h, i), pair(b, i)))
                       : __ffma2_rn(pair(a, i), pair(h, i), pair(b, i)));
 }
-__device__ __forceinline__ void add(float (&f)[8], const float (&s)[8]) {
+template <int N> __device__ __forceinline__ void add(float (&f)[N], const float (&s)[N]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) put(f, i, __fadd2_rn(pair(f, i), pair(s, i)));
+    for (int i = 0; i < N / 2; ++i) put(f, i, __fadd2_rn(pair(f, i), pair(s, i)));
 }
-__device__ __forceinline__ void product(float (&o)[8], const float (&a)[8], const float (&b)[8]) {
+template <int N> __device__ __forceinline__ void product(float (&o)[N], const float (&a)[N], const float (&b)[N]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) put(o, i, __fmul2_rn(pair(a, i), pair(b, i)));
+    for (int i = 0; i < N / 2; ++i) put(o, i, __fmul2_rn(pair(a, i), pair(b, i)));
 }
 
 // ---- the tile kernel --------------------------------------------------------------
 
-// 8 channels per thread.  WIDE: 32 channels per tile, aligned rows, staged by TMA.  Otherwise
-// 64, and each row's segment is staged by a bulk copy of the 16-byte blocks around it, and
-// read from where it lies in them: about 60 cycles to issue, so six warps issue them
-// while two look back (one warp for all took 17,600 cycles of a tile; 4-byte
-// asynchronous copies by all warps before the fold took 3,200 to 10,700).
+// WIDE: 32 channels per tile, 8 per thread, aligned rows, staged by TMA.  Otherwise 64
+// channels, 2 per thread and a run of tokens per warp, so that the element-wise accesses
+// of a warp are neighbours (with 8 per thread: backward 7001 x 1001 fp32 47 -> 43 us,
+// 50000 x 1001 bf16 forward 125 -> 104, backward 215 -> 157).  Each row's segment is
+// staged by a bulk copy of the 16-byte blocks around it, and read from where it lies in
+// them: about 110 cycles of a warp each to issue, so six warps issue them while two look
+// back (one warp for all took 17,600 cycles of a tile; 4-byte asynchronous copies by all
+// warps before the fold took 3,200 to 10,700).
 template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
     static constexpr int THREADS = 256, CTAS = 2, WARPS = THREADS / 32;
     static constexpr int COPIERS = WARPS - 2;  // warps that issue bulk copies, while the others look back
-    static constexpr int LANES = WIDE ? 4 : 8, CC = 8 * LANES, RUNS = THREADS / LANES;  // runs of R tokens
-    // A token takes 8 registers for its decays and 4 or 8 for each of b and h as
-    // stored; R is the most that fits beside the rest in 128 registers (one more
-    // spilled: forward 151 -> 157 us with bf16 gates, backward 226 -> 235 us) and in
-    // shared memory at two CTAs per SM.
-    static constexpr int R = sizeof(TX) == 2 ? (BWD ? (WIDE ? 5 : 4) : WIDE ? 7 : 6) : (BWD ? 3 : 5);
+    static constexpr int E = WIDE ? 8 : 2, LANES = WIDE ? 4 : 32, CC = E * LANES, RUNS = THREADS / LANES;  // runs of R tokens
+    // Of 8 channels a token takes 8 registers for its decays and 4 or 8 for each of b
+    // and h as stored; R is the most that fits beside the rest in 128 registers (one
+    // more spilled: forward 151 -> 157 us with bf16 gates, backward 226 -> 235 us) and
+    // in shared memory at two CTAs per SM.  Four times as many at 2 channels, where two
+    // more fit but gain nothing.
+    static constexpr int R = sizeof(TX) == 2 ? (BWD ? (WIDE ? 5 : 16) : WIDE ? 7 : 24) : (BWD ? (WIDE ? 3 : 12) : WIDE ? 5 : 20);
     static constexpr int TT = RUNS * R;
     static constexpr int PARTS = THREADS / CC, RUNS_PART = RUNS / PARTS;  // the fold over runs, in parts
-    static constexpr Layout LAYOUT = !WIDE ? kEvery8 : sizeof(TX) == 4 || sizeof(TG) == 4 ? kHalves : kNext;
+    static constexpr Layout LAYOUT = !WIDE ? kApart : sizeof(TX) == 4 || sizeof(TG) == 4 ? kHalves : kNext;
     // bytes of a token in the stage, a row of x / h and one of g
     static constexpr int PITCH_X = CC * (int)sizeof(TX) + (WIDE ? 0 : 16), PITCH_G = CC * (int)sizeof(TG) + (WIDE ? 0 : 16);
     // shared memory (bytes)
@@ -323,11 +340,33 @@ template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
     // Which of its channels lie below D, from its first one.
     static __device__ __forceinline__ int inside(int c, int d, int D) {
         return LAYOUT == kNext ? (c < D ? 3 : 0) : LAYOUT == kHalves ? (c < D ? 1 : 0) + (c + d < D ? 2 : 0)
-                                                                     : min(max((D - c + 7) / 8, 0), 8);
+                                                                     : (c < D ? 1 : 0) + (c + 32 < D ? 1 : 0);
     }
-    // Where its channels lie in the arrays of compositions: two runs of four.
-    static __device__ __forceinline__ int place(int lane, int run, int k) {
-        return lane * 4 + (LAYOUT == kHalves ? k ^ (run & 1) : k) * (CC / 2);
+    // A run's values of a lane's channels in the arrays of compositions.
+    static __device__ __forceinline__ float* place(float* c, int lane, int run, int k) {
+        return c + run * CC + (WIDE ? lane * 4 + (LAYOUT == kHalves ? k ^ (run & 1) : k) * (CC / 2) : lane + k * 32);
+    }
+    static __device__ __forceinline__ void put_run(float* c, int lane, int run, const float (&f)[E]) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float* q = place(c, lane, run, k);
+            if constexpr (WIDE)
+                *reinterpret_cast<float4*>(q) = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+            else
+                *q = f[k];
+        }
+    }
+    static __device__ __forceinline__ void get_run(float* c, int lane, int run, float (&f)[E]) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float* q = place(c, lane, run, k);
+            if constexpr (WIDE) {
+                const float4 u = *reinterpret_cast<const float4*>(q);
+                f[4 * k] = u.x; f[4 * k + 1] = u.y; f[4 * k + 2] = u.z; f[4 * k + 3] = u.w;
+            } else {
+                f[k] = *q;
+            }
+        }
     }
 };
 
@@ -534,7 +573,7 @@ __global__ void __launch_bounds__(Tile<TX, TG, BWD, WIDE>::THREADS, Tile<TX, TG,
 linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g,
                    const __grid_constant__ CUtensorMap map_h, const __grid_constant__ LinrecParams p) {
     using C = Tile<TX, TG, BWD, WIDE>;
-    constexpr int CC = C::CC, R = C::R, TT = C::TT;
+    constexpr int CC = C::CC, E = C::E, R = C::R, TT = C::TT;
     constexpr Layout L = C::LAYOUT;
     extern __shared__ __align__(1024) unsigned char smem[];
     float* ca = reinterpret_cast<float*>(smem + C::CA);
@@ -635,7 +674,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         // before the first) and rows behind the last sequence become the identity here.
         const bool full = t0 + TT <= valid;
         auto local = [&](int r) { return BWD ? TT - 1 - (run * R + r) : run * R + r; };  // the run's token r in the tile
-        float a[R][8], A[8];
+        float a[R][E], A[E];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int l = local(r);
@@ -644,25 +683,22 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                                                 shift(p.g, p.ldg, group * CC, t0 + l, sizeof(TG))) + lane_c, apart);
             gr.get(a[r]);
         }
-        if (!full || (!WIDE && inside < 8)) {
+        if (!full || (!WIDE && inside < E)) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < E; ++j)
                     if (t0 + local(r) >= valid || (!WIDE && j >= inside)) a[r][j] = 0.f;  // exp(0) = 1
         }
         // The run's decay is the exponential of its gates' sum: the product of its
-        // tokens' decays would carry the rounding of each, and 32 runs do so after it.
+        // tokens' decays would carry the rounding of each, as the runs' do after it.
 #pragma unroll
-        for (int j = 0; j < 8; ++j) A[j] = 0.f;
+        for (int j = 0; j < E; ++j) A[j] = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) add(A, a[r]);
         decays(A);
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<float4*>(ca + run * CC + C::place(lc, run, k)) =
-                make_float4(A[4 * k], A[4 * k + 1], A[4 * k + 2], A[4 * k + 3]);
-        decays(reinterpret_cast<float (&)[R * 8]>(a));
+        C::put_run(ca, lc, run, A);
+        decays(reinterpret_cast<float (&)[R * E]>(a));
         Row<TX, L> b[R], h[BWD ? R : 1];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -683,10 +719,10 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             for (int r = 0; r < R; ++r)
                 if (local(r) == 0) h[r].zero();
         }
-        float B[8];
+        float B[E];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) B[j] = 0.f;
-        auto start_state = [&](int n, float (&f)[8]) {
+        for (int j = 0; j < E; ++j) B[j] = 0.f;
+        auto start_state = [&](int n, float (&f)[E]) {
             Row<float, L> s;
             s.zero();
             if (p.start && inside) s.load(p.start + (int64_t)n * p.D + c0, apart, inside);
@@ -697,7 +733,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         auto compose = [&](auto cutting) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                float f[8];
+                float f[E];
                 b[r].get(f);
                 if (decltype(cutting)::value) {
                     const int n = first[run * R + r];
@@ -706,14 +742,11 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                         cut = 1;
                     }
                 }
-                advance<BWD>(B, a[r], f);
+                advance<BWD, E>(B, a[r], f);
             }
         };
         bounded ? compose(std::true_type()) : compose(std::false_type());
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<float4*>(cb + run * CC + C::place(lc, run, k)) =
-                make_float4(B[4 * k], B[4 * k + 1], B[4 * k + 2], B[4 * k + 3]);
+        C::put_run(cb, lc, run, B);
         if (lc == 0) cut_s[run] = cut;
         if (tid == 0) misc[0] = (int64_t)next < tiles ? (int)next : -1;
         __syncthreads();
@@ -837,12 +870,8 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         bounded ? walk(std::true_type()) : walk(std::false_type());
         __syncthreads();
         if (inside) {
-            float s[8];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float4 u = *reinterpret_cast<const float4*>(ca + run * CC + C::place(lc, run, k));
-                s[4 * k] = u.x; s[4 * k + 1] = u.y; s[4 * k + 2] = u.z; s[4 * k + 3] = u.w;
-            }
+            float s[E];
+            C::get_run(ca, lc, run, s);
             // ---- every token from its state
             const int64_t t_first = t0 + (BWD ? TT - 1 - run * R : run * R), dir = BWD ? -1 : 1;
             TX* out = static_cast<TX*>(p.out) + t_first * p.ldo + c0;
@@ -859,10 +888,10 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                             if (n >= 0) start_state(n, s);
                         }
                     }
-                    float f[8];
+                    float f[E];
                     b[r].get(f);
                     if (BWD) {
-                        float before[8];
+                        float before[E];
                         add(f, s);  // lam
                         Row<TX, L>::store(out, f, inside, apart);
                         product(s, a[r], f);  // mu
@@ -876,7 +905,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                         product(before, before, s);
                         Row<TG, L>::store(dg, before, inside, apart);
                     } else {
-                        advance<BWD>(s, a[r], f);
+                        advance<BWD, E>(s, a[r], f);
                         Row<TX, L>::store(out, s, inside, apart);
                     }
                     if (decltype(cutting)::value && n_last >= 0 && p.last)
