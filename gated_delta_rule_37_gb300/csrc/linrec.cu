@@ -40,7 +40,7 @@
 //                          fp32, 16384 rows   123 us   98 %)
 //   backward 32768 x 4096  bf16, bf16 gates   214 us   94 %    (fp32 gates 275 us, 102 %;
 //                          fp32, 16384 rows   200 us  100 %)
-//   backward 7001 x 1001   fp32, odd rows      43 us   49 %    (50000 rows 195 us, 77 %)
+//   backward 7001 x 1001   fp32, odd rows      42 us   49 %    (50000 rows 193 us, 78 %)
 //   forward  6113 x 2048   bf16, 4 sequences   30 us   50 %
 // Long calls of narrow types are held by the chain of one tile's steps (composition,
 // fold, look-back, evaluation: about 10,500 cycles at two CTAs per SM, of which the
@@ -316,7 +316,10 @@ template <typename TX, typename TG, bool BWD, bool WIDE> struct Tile {
     // more fit but gain nothing.
     static constexpr int R = sizeof(TX) == 2 ? (BWD ? (WIDE ? 5 : 16) : WIDE ? 7 : 24) : (BWD ? (WIDE ? 3 : 12) : WIDE ? 5 : 20);
     static constexpr int TT = RUNS * R;
-    static constexpr int PARTS = THREADS / CC, RUNS_PART = RUNS / PARTS;  // the fold over runs, in parts
+    // The fold over runs, in parts.  The 8 runs of the tiles that are not WIDE are one part,
+    // folded by the two warps that look back while the others already copy (all warps in
+    // four parts, then the copies: 7001 x 1001 backward 43.1 us, so 42.5).
+    static constexpr int PARTS = WIDE ? THREADS / CC : 1, RUNS_PART = RUNS / PARTS;
     static constexpr Layout LAYOUT = !WIDE ? kApart : sizeof(TX) == 4 || sizeof(TG) == 4 ? kHalves : kNext;
     // bytes of a token in the stage, a row of x / h and one of g
     static constexpr int PITCH_X = CC * (int)sizeof(TX) + (WIDE ? 0 : 16), PITCH_G = CC * (int)sizeof(TG) + (WIDE ? 0 : 16);
@@ -778,7 +781,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             pa[part * CC + pos] = fa;
             pb[part * CC + pos] = fb;
         };
-        bounded ? fold(std::true_type()) : fold(std::false_type());
+        if (part < C::PARTS) bounded ? fold(std::true_type()) : fold(std::false_type());
         // whether a part is cut: read from cut_s by everyone alike
         auto part_cut = [&](int q) {
             int c = 0;
@@ -786,7 +789,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 for (int i = q * C::RUNS_PART; i < (q + 1) * C::RUNS_PART; ++i) c |= cut_s[i];
             return c != 0;
         };
-        __syncthreads();
+        if (C::PARTS > 1) __syncthreads();
         if (warp == C::WARPS - 1 && ntile >= 0) {  // while others look back: the next tile's sequences
             const int nb = buf ^ 1;
             const bool any = find_boundaries<TT, BWD>(p.cu, p.N, token0(ntile),
@@ -867,7 +870,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 f = decltype(cutting)::value && cut_s[at] ? rb : fmaf(ra, f, rb);
             }
         };
-        bounded ? walk(std::true_type()) : walk(std::false_type());
+        if (part < C::PARTS) bounded ? walk(std::true_type()) : walk(std::false_type());
         __syncthreads();
         if (inside) {
             float s[E];
