@@ -621,6 +621,9 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                     tma_load_2d(tc::smem_u32(smem + C::HS + l * C::PITCH_X), &map_h, c, t0 + l - 1, mbar);
             }
         } else {
+            // What earlier tiles had copied into the stage element by element, and all have
+            // read behind a barrier, before the bulk copies that may write the same bytes.
+            tc::fence_proxy_async();
             for (int l = warp - 2 + C::COPIERS * lane; l < min(TT, valid - t0); l += 32 * C::COPIERS) {
                 const int64_t t = t0 + l;
                 copy_segment<TX>(smem + C::XS + l * C::PITCH_X, p.x, p.ldx, p.T, p.D, t, c, mbar);

@@ -1,0 +1,40 @@
+"""Paths of the gated linear recurrence that depend on the call's size: stages
+used again by later tiles; against the fp64 oracle, with the bounds of
+tests/test_gpu_linrec.py."""
+import pytest
+import torch
+
+import gated_delta_rule_37_gb300 as gdr
+from tests.test_gpu_linrec import DEV, TYPES, check_bwd, check_fwd, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    gdr.load()
+
+
+def shifted(t):
+    """A copy whose first element lies one element behind a 16-byte boundary."""
+    flat = torch.empty(t.numel() + 8, dtype=t.dtype, device=DEV)
+    out = flat[1:1 + t.numel()].view(t.shape)
+    out.copy_(t)
+    assert out.data_ptr() % 16
+    return out
+
+
+@pytest.mark.parametrize("types", TYPES, ids=lambda t: "-".join(str(d)[6:] for d in t))
+def test_unaligned_rows_through_a_stage_used_again(types):
+    """Rows at the ends of unaligned tensors go into the stage element by
+    element, and later tiles of the same CTA by bulk copies over them: more
+    tiles than CTAs (three groups of channels by 200 rows of tiles and more)."""
+    c = make(61, [15000, 1, 24999], 129, *types, g_lo=-0.5)
+    x, g, y = (shifted(c[k].to(DEV)) for k in ("x", "g", "y"))
+    cu, h0, df = (c[k].to(DEV) for k in ("cu", "h0", "df"))
+    out, hT = gdr.linrec_fwd(x, g, cu, initial_state=h0)
+    check_fwd(c, out.cpu(), hT.cpu())
+    check_bwd(c, *(t.cpu() for t in gdr.linrec_bwd(x, g, y, cu, initial_state=h0, d_final_state=df)))
+    assert gdr.device_status() == 0
