@@ -6,7 +6,7 @@
 // arithmetic is kept short (packed fp32 pairs, the scale group a compile-time
 // length, no division per element: e4m3 at 32768 x 4096 went 212 -> 149 us on
 // that alone).  One GB300, device times, of the copy rate (6.69 TB/s measured):
-//   forward  32768 x 4096  bf16 + residual, e4m3 by 128   149 us   95 %
+//   forward  32768 x 4096  bf16 + residual, e4m3 by 128   153 us   92 %
 //            16384 x 4096  bf16 + residual, bf16           84 us   95 %
 //             8192 x 8192  bf16 + residual, e4m3 by row    90 us   78 %
 //             3001 x 1001  fp32, e4m3 by row, odd rows     11 us   20 % (in L2)
@@ -105,12 +105,32 @@ __device__ __forceinline__ void store_codes(__nv_fp8_storage_t* p, const float2 
     *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
 
-// A group's scale, and what its values are multiplied by: 1.5 ulp of amax / 448
-// and of its reciprocal, far below a code's half step.
-__device__ __forceinline__ float group_scale(float amax) {
-    return __fmul_rn(fmaxf(amax, kAmaxFloor), 1.f / kE4m3Max);
-}
-__device__ __forceinline__ float group_inverse(float scale) { return __fdividef(1.f, scale); }
+// A group's scale, amax / 448, and its values' quotients by it: products with the
+// reciprocal, each corrected by its exact remainder (P. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990), which finds a
+// quotient that fp32 holds to the last bit whatever the reciprocal's own rounding.  So a
+// value half-way between two codes is seen to be half-way; by the product alone about
+// half of those went to the wrong code.  (At 32768 x 4096 by the product alone 149 us, by division 163,
+// so 153.)
+// Where the scale is infinite there is no remainder: finite values give 0.
+struct Scale {
+    float scale, inverse, minus;
+    __device__ __forceinline__ explicit Scale(float amax) {
+        const float a = fmaxf(amax, kAmaxFloor), q = __fmul_rn(a, 1.f / kE4m3Max);
+        const bool finite = a < INFINITY;
+        scale = finite ? fmaf(fmaf(q, -kE4m3Max, a), 1.f / kE4m3Max, q) : a;
+        inverse = __fdividef(1.f, scale);
+        minus = finite ? -scale : 0.f;
+    }
+    __device__ __forceinline__ float2 operator()(float2 f) const {
+        const float2 q = __fmul2_rn(f, both(inverse));
+        return __ffma2_rn(__ffma2_rn(q, both(minus), f), both(inverse), q);
+    }
+    __device__ __forceinline__ float operator()(float f) const {
+        const float q = __fmul_rn(f, inverse);
+        return fmaf(fmaf(q, minus, f), inverse, q);
+    }
+};
 
 // Reductions over the tpr threads of a row: shuffles, and above a warp one
 // exchange of the warps' results behind a barrier of the row's threads.  `turn`
@@ -234,15 +254,15 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rmsnorm_fwd_kernel(NormParams 
                 norm(c, f);
                 most = fmaxf(most, largest(f));
             }
-            const float scale = group_scale(reduce.max(most)), inv = group_inverse(scale);
-            if (l == 0 && width) *scales = scale;
+            const Scale by(reduce.max(most));
+            if (l == 0 && width) *scales = by.scale;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 const int e = (c * tpr + l) * 8;
                 float2 f[4];
                 norm(c, f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(f[i], both(inv));
+                for (int i = 0; i < 4; ++i) f[i] = by(f[i]);
                 if (e < width) store_codes(y + e, f);
             }
         } else {
@@ -256,12 +276,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rmsnorm_fwd_kernel(NormParams 
 #pragma unroll
                 for (int off = SPAN / 2; off >= 1; off >>= 1)
                     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-                const float scale = group_scale(most), inv = group_inverse(scale);
+                const Scale by(most);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(f[i], both(inv));
+                for (int i = 0; i < 4; ++i) f[i] = by(f[i]);
                 if (e < width) {
                     store_codes(y + e, f);
-                    if (l % SPAN == 0) scales[e / (SPAN * 8)] = scale;
+                    if (l % SPAN == 0) scales[e / (SPAN * 8)] = by.scale;
                 }
             }
         }
@@ -317,11 +337,11 @@ __global__ void __launch_bounds__(kMaxThreads, CH <= 8 ? 2 : 1) rmsnorm_fwd_any_
             float most = 0.f;
 #pragma unroll
             for (int c = 0; c < CH; ++c) most = fmaxf(most, fabsf(s[c]));
-            const float scale = group_scale(reduce.max(most)), inv = group_inverse(scale);
-            if (l == 0 && width) *scales = scale;
+            const Scale by(reduce.max(most));
+            if (l == 0 && width) *scales = by.scale;
 #pragma unroll
             for (int c = 0; c < CH; ++c)
-                if (c * tpr + l < width) y[c * tpr + l] = __nv_cvt_float_to_fp8(s[c] * inv, __NV_SATFINITE, __NV_E4M3);
+                if (c * tpr + l < width) y[c * tpr + l] = __nv_cvt_float_to_fp8(by(s[c]), __NV_SATFINITE, __NV_E4M3);
             continue;
         }
         // a group crosses warps: its largest magnitude in shared memory (the order of a maximum does not
@@ -346,9 +366,9 @@ __global__ void __launch_bounds__(kMaxThreads, CH <= 8 ? 2 : 1) rmsnorm_fwd_any_
         for (int c = 0; c < CH; ++c) {
             const int e = c * tpr + l;
             if (e < width) {
-                const float scale = group_scale(__int_as_float(amax[e >> shift]));
-                y[e] = __nv_cvt_float_to_fp8(s[c] * group_inverse(scale), __NV_SATFINITE, __NV_E4M3);
-                if ((e & (p.group - 1)) == 0) scales[e >> shift] = scale;
+                const Scale by(__int_as_float(amax[e >> shift]));
+                y[e] = __nv_cvt_float_to_fp8(by(s[c]), __NV_SATFINITE, __NV_E4M3);
+                if ((e & (p.group - 1)) == 0) scales[e >> shift] = by.scale;
             }
         }
         meet();

@@ -385,8 +385,9 @@ GDR_API int gdr_linrec_step(const void* x, int64_t x_stride, const void* g, int6
  *                  only: for each group of scale_group consecutive elements of
  *                  a row (32, 64 or 128; 0: the whole row), with a the larger of
  *                  max |y| and 1e-12, scale = a / 448 and the stored code is
- *                  y / scale rounded to the nearest e4m3 value, so that
- *                  code * scale stands for y.  y is not rounded before.
+ *                  y / scale (both quotients rounded to fp32) rounded to the
+ *                  nearest e4m3 value, half-way to the even code, so that
+ *                  code * scale stands for y.  y is fp32, not rounded before.
  * D up to GDR_RMSNORM_MAX_D.  Rows need their element's alignment only; rows
  * of 8 aligned elements, with D and the strides multiples of 8, take the fast
  * path.  Sums are fp32: a row whose sum of squares passes fp32's range
