@@ -110,13 +110,13 @@ __device__ __forceinline__ void store_codes(__nv_fp8_storage_t* p, const float2 
 // elementary functions on the IBM RISC System/6000 processor", 1990), which finds a
 // quotient that fp32 holds to the last bit whatever the reciprocal's own rounding.  So a
 // value half-way between two codes is seen to be half-way; by the product alone about
-// half of those went to the wrong code.  (At 32768 x 4096 by the product alone 149 us, by division 163,
-// so 153.)
-// Where the scale is infinite there is no remainder: finite values give 0.
+// half of those went to the wrong code.  (At 32768 x 4096 by the product alone 149 us,
+// by division 163, so 153.)  Where the scale is infinite there is no remainder: finite
+// values give 0.  Where it is NaN, so is every code.
 struct Scale {
     float scale, inverse, minus;
     __device__ __forceinline__ explicit Scale(float amax) {
-        const float a = fmaxf(amax, kAmaxFloor), q = __fmul_rn(a, 1.f / kE4m3Max);
+        const float a = amax < kAmaxFloor ? kAmaxFloor : amax, q = __fmul_rn(a, 1.f / kE4m3Max);
         const bool finite = a < INFINITY;
         scale = finite ? fmaf(fmaf(q, -kE4m3Max, a), 1.f / kE4m3Max, q) : a;
         inverse = __fdividef(1.f, scale);
@@ -131,6 +131,13 @@ struct Scale {
         return fmaf(fmaf(q, minus, f), inverse, q);
     }
 };
+
+// The larger of two, NaN if either is: a NaN reaches its group's scale.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
 
 // Reductions over the tpr threads of a row: shuffles, and above a warp one
 // exchange of the warps' results behind a barrier of the row's threads.  `turn`
@@ -161,7 +168,7 @@ struct RowReduce {
         return all(v, [](float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); });
     }
     __device__ __forceinline__ float max(float v) {
-        return all(make_float2(v, 0.f), [](float2 a, float2 b) { return make_float2(fmaxf(a.x, b.x), 0.f); }).x;
+        return all(make_float2(v, 0.f), [](float2 a, float2 b) { return make_float2(max_nan(a.x, b.x), 0.f); }).x;
     }
 };
 
@@ -227,7 +234,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rmsnorm_fwd_kernel(NormParams 
         auto largest = [](const float2 (&f)[4]) {
             float a = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a = fmaxf(a, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
+            for (int i = 0; i < 4; ++i) a = max_nan(a, max_nan(fabsf(f[i].x), fabsf(f[i].y)));
             return a;
         };
         if (MODE == kSame) {
@@ -252,7 +259,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rmsnorm_fwd_kernel(NormParams 
             for (int c = 0; c < CH; ++c) {
                 float2 f[4];
                 norm(c, f);
-                most = fmaxf(most, largest(f));
+                most = max_nan(most, largest(f));
             }
             const Scale by(reduce.max(most));
             if (l == 0 && width) *scales = by.scale;
@@ -275,7 +282,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rmsnorm_fwd_kernel(NormParams 
                 float most = largest(f);
 #pragma unroll
                 for (int off = SPAN / 2; off >= 1; off >>= 1)
-                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+                    most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, off));
                 const Scale by(most);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f[i] = by(f[i]);
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__(kMaxThreads, CH <= 8 ? 2 : 1) rmsnorm_fwd_any_
         if (p.groups == 1) {
             float most = 0.f;
 #pragma unroll
-            for (int c = 0; c < CH; ++c) most = fmaxf(most, fabsf(s[c]));
+            for (int c = 0; c < CH; ++c) most = max_nan(most, fabsf(s[c]));
             const Scale by(reduce.max(most));
             if (l == 0 && width) *scales = by.scale;
 #pragma unroll
@@ -345,7 +352,8 @@ __global__ void __launch_bounds__(kMaxThreads, CH <= 8 ? 2 : 1) rmsnorm_fwd_any_
             continue;
         }
         // a group crosses warps: its largest magnitude in shared memory (the order of a maximum does not
-        // matter), a warp's 32 neighbours, which lie in one group, reduced before
+        // matter), a warp's 32 neighbours, which lie in one group, reduced before; the bits of magnitudes
+        // are ordered as they are, NaN above all numbers
         int* amax = amax_s + slot * p.groups;
         const int shift = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
         auto meet = [&]() {
@@ -358,7 +366,7 @@ __global__ void __launch_bounds__(kMaxThreads, CH <= 8 ? 2 : 1) rmsnorm_fwd_any_
         meet();
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const unsigned most = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(s[c]), 0.f)));
+            const unsigned most = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(s[c])));
             if ((l & 31) == 0 && c * tpr + l < p.D) atomicMax(amax + ((c * tpr + l) >> shift), (int)most);
         }
         meet();

@@ -388,6 +388,9 @@ GDR_API int gdr_linrec_step(const void* x, int64_t x_stride, const void* g, int6
  *                  y / scale (both quotients rounded to fp32) rounded to the
  *                  nearest e4m3 value, half-way to the even code, so that
  *                  code * scale stands for y.  y is fp32, not rounded before.
+ *                  A NaN in a group makes its scale and all its codes NaN; an
+ *                  infinity makes the scale infinite, its own code NaN and the
+ *                  group's finite values' 0.
  * D up to GDR_RMSNORM_MAX_D.  Rows need their element's alignment only; rows
  * of 8 aligned elements, with D and the strides multiples of 8, take the fast
  * path.  Sums are fp32: a row whose sum of squares passes fp32's range

@@ -54,3 +54,33 @@ def test_values_half_way_between_codes(D, group, dtype, aligned):
     assert bits_equal(scales, s.float().view(1, -1).expand(7, -1))
     want = (sign * m.flatten().float()).to(E4)
     assert bits_equal(q.cpu().view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("aligned", [True, False], ids=["aligned", "unaligned"])
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("D", [256, 2048, 16384])
+def test_a_bad_value_in_a_group(D, group, dtype, aligned):
+    """A NaN among a group's values makes its scale and its codes NaN, an
+    infinity its scale infinite, its own code NaN and the others 0; the other
+    groups are as they were."""
+    r = torch.Generator().manual_seed(D + group)
+    span = group or D
+    w = torch.randn(D, generator=r)
+    _, x = signs(5, D, dtype, aligned, r)
+    call = lambda w: [t.cpu() for t in gdr.rmsnorm_fwd(x, w.to(DEV), eps=0.0, y_dtype=E4, scale_group=group)[::2]]  # noqa: E731
+    q0, s0 = call(w)
+    for value in (float("nan"), float("inf"), -float("inf")):
+        bad = w.clone()
+        bad[D - 3] = value                                 # in the last group
+        q, s = call(bad)
+        hit = torch.arange(D) >= D - span
+        assert bits_equal(q.view(torch.uint8)[:, ~hit], q0.view(torch.uint8)[:, ~hit])
+        assert bits_equal(s[:, :-1], s0[:, :-1])
+        own = q.float()[:, hit]
+        if value != value:
+            assert torch.isnan(s[:, -1]).all() and torch.isnan(own).all()
+        else:
+            assert (s[:, -1] == float("inf")).all() and torch.isnan(own[:, span - 3]).all()
+            own[:, span - 3] = 0
+            assert (own == 0).all()
