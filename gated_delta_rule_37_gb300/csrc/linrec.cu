@@ -84,6 +84,7 @@ struct LinrecParams {
     int groups;          // channel groups of a tile row
     int rows;            // tile rows of T tokens
     int clustered;       // one cluster of `rows` CTAs per channel group; else more than one row looks back
+    int lost;            // LOSE only: the tile row whose copies are not to complete
     unsigned int* head;  // workspace: [0] the tile counter, [1] set when a wait gave up
     unsigned int* words;  // [groups][rows][3][CC]: a tile's outgoing state, A, B; kNothing until published
     unsigned int* err;
@@ -379,6 +380,10 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         :: "r"(dst), "l"(map), "r"(c), "r"(t), "r"(mbar) : "memory");
 }
 
+__device__ __forceinline__ void expect_bytes(uint32_t mbar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(mbar), "r"(bytes) : "memory");
+}
+
 // The segment [c, c + 64) of one row of a tensor into its stage row: the 16-byte
 // blocks around it by one bulk copy, and what of them lies outside the tensor (in
 // rows near its ends) left out, the elements there copied one by one.
@@ -394,7 +399,7 @@ __device__ __forceinline__ void copy_segment(unsigned char* dst, const void* ten
     if (hi > end) hi = end & ~uintptr_t(15);
     if (hi > lo) {
         const uint32_t bytes = (uint32_t)(hi - lo);
-        asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(mbar), "r"(bytes) : "memory");
+        expect_bytes(mbar, bytes);
         tc::bulk_g2s(tc::smem_u32(dst) + (uint32_t)(lo - first), reinterpret_cast<const void*>(lo), bytes, mbar);
     } else {
         lo = hi = stop;
@@ -571,7 +576,9 @@ __device__ bool find_boundaries(const int32_t* cu, int N, int t0, int* first, in
     return true;
 }
 
-template <typename TX, typename TG, bool BWD, bool WIDE>
+// LOSE: tiles of row p.lost wait for 16 bytes that nobody copies, for the test of the
+// way out.
+template <typename TX, typename TG, bool BWD, bool WIDE, bool LOSE>
 __global__ void __launch_bounds__(Tile<TX, TG, BWD, WIDE>::THREADS, Tile<TX, TG, BWD, WIDE>::CTAS)
 linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g,
                    const __grid_constant__ CUtensorMap map_h, const __grid_constant__ LinrecParams p) {
@@ -586,8 +593,12 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     float* carry_s = reinterpret_cast<float*>(smem + C::CARRY);
     int* cut_s = reinterpret_cast<int*>(smem + C::CUT);
     uint64_t* mbar_s = reinterpret_cast<uint64_t*>(smem + C::MISC);
-    int* misc = reinterpret_cast<int*>(smem + C::MISC + 16);  // next tile, abort, boundaries of either buffer
-    volatile int* abort_s = misc + 1;
+    // next tile, copies lost, boundaries of either buffer, cut, state lost
+    int* misc = reinterpret_cast<int*>(smem + C::MISC + 16);
+    // Either is set in front of one barrier and looked at behind it, and not set in
+    // between, so that all threads of the CTA leave at the same place.
+    volatile int* abort_s = misc + 1;  // the tile's copies did not land
+    volatile int* stop_s = misc + 5;   // the state that reaches the tile did not arrive
     const uint32_t mbar = tc::smem_u32(mbar_s);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -599,7 +610,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     if (tid == 0) {
         tc::mbar_init(mbar, WIDE ? 1 : 32 * C::COPIERS);
         tc::mbar_fence_init();
-        *abort_s = 0;
+        *abort_s = *stop_s = 0;
     }
     const int valid = min((int64_t)max(p.cu[p.N], 0), p.T);
     const int rows = (valid + TT - 1) / TT;  // tile rows that hold a sequence's token
@@ -613,7 +624,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     auto request = [&](int tile) {  // the tile's rows into the stage; one thread, or if not WIDE the copiers
         const int c = tile % p.groups * CC, t0 = token0(tile);
         if constexpr (WIDE) {
-            tc::mbar_arrive_tx(mbar, C::STAGE);
+            tc::mbar_arrive_tx(mbar, C::STAGE + (LOSE && tile / p.groups == p.lost ? 16 : 0));
             for (int l = 0; l < TT; l += C::BOX) {
                 tma_load_2d(tc::smem_u32(smem + C::XS + l * C::PITCH_X), &map_x, c, t0 + l, mbar);
                 tma_load_2d(tc::smem_u32(smem + C::GS + l * C::PITCH_G), &map_g, c, t0 + l, mbar);
@@ -630,6 +641,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 copy_segment<TG>(smem + C::GS + l * C::PITCH_G, p.g, p.ldg, p.T, p.D, t, c, mbar);
                 if (BWD && t > 0) copy_segment<TX>(smem + C::HS + l * C::PITCH_X, p.h, p.ldh, p.T, p.D, t - 1, c, mbar);
             }
+            if (LOSE && warp == 2 && lane == 0 && tile / p.groups == p.lost) expect_bytes(mbar, 16);
             tc::mbar_arrive(mbar);
         }
     };
@@ -668,6 +680,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             asm volatile("atom.relaxed.gpu.global.add.u32 %0, [%1], 1;" : "=r"(next) : "l"(p.head) : "memory");
         if (!tc::mbar_wait(mbar, buf, abort_s)) {
             *abort_s = 1;
+            if (many) p.head[1] = 1;
             atomicOr(p.err, kScanError);
         }
         __syncthreads();
@@ -847,7 +860,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             }
             if (looks) {
                 if (!known && !look_back(words, row, pitch, CC, carry, p.head + 1)) {
-                    *abort_s = 1;
+                    *stop_s = 1;
                     p.head[1] = 1;
                     atomicOr(p.err, kScanError);
                 }
@@ -856,7 +869,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             carry_s[pos] = carry;
         }
         __syncthreads();
-        if (*abort_s) {
+        if (*stop_s) {
             if (tid == 0 && ntile >= 0) tc::mbar_wait_copies(mbar, buf ^ 1);
             break;
         }
@@ -1030,10 +1043,10 @@ bool wide_rows(const void* p, int64_t ld, int D) {
            (uint64_t)ld * sizeof(T) < (1ull << 40);
 }
 
-template <typename TX, typename TG, bool BWD, bool WIDE>
+template <typename TX, typename TG, bool BWD, bool WIDE, bool LOSE = false>
 cudaError_t launch_tiles(LinrecParams p, void* ws, cudaStream_t s) {
     using C = Tile<TX, TG, BWD, WIDE>;
-    auto kernel = linrec_tile_kernel<TX, TG, BWD, WIDE>;
+    auto kernel = linrec_tile_kernel<TX, TG, BWD, WIDE, LOSE>;
     // at every call: the attribute belongs to the context
     cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES_SMEM);
     static std::atomic<int> resident{0};  // CTAs per SM
@@ -1101,6 +1114,14 @@ cudaError_t launch_scan_t(const LinrecParams& p, bool bwd, void* ws, cudaStream_
     if (bwd)
         return wide ? launch_tiles<TX, TG, true, true>(p, ws, s) : launch_tiles<TX, TG, true, false>(p, ws, s);
     return wide ? launch_tiles<TX, TG, false, true>(p, ws, s) : launch_tiles<TX, TG, false, false>(p, ws, s);
+}
+
+// The forward on fp32 with the copies of tile row p.lost made to run out.
+cudaError_t launch_scan_losing(const LinrecParams& p, void* ws, cudaStream_t s) {
+    const bool wide = p.D % 8 == 0 && wide_rows<float>(p.x, p.ldx, p.D) && wide_rows<float>(p.g, p.ldg, p.D) &&
+                      wide_rows<float>(p.out, p.ldo, p.D);
+    return wide ? launch_tiles<float, float, false, true, true>(p, ws, s)
+                : launch_tiles<float, float, false, false, true>(p, ws, s);
 }
 
 cudaError_t launch_scan(const LinrecParams& p, int dtype, int gate_dtype, bool bwd, void* ws, cudaStream_t s) {
@@ -1382,6 +1403,24 @@ int gdr_linrec_fwd(const void* x, int64_t x_stride, const void* g, int64_t g_str
     p.x = x; p.g = g; p.out = y; p.start = initial_state; p.last = final_state; p.cu = cu_seqlens;
     p.ldx = x_stride; p.ldg = g_stride; p.ldo = y_stride; p.T = T_total; p.N = N; p.D = D;
     return launch_result(launch_scan(p, dtype, gate_dtype, false, workspace, s), "gdr_linrec_fwd launch");
+}
+
+int gdr_selftest_linrec_lost_copy(const float* x, const float* g, const int32_t* cu_seqlens, int N, int64_t T_total,
+                                  int D, int lost_row, float* y, float* final_state, void* workspace, size_t ws_bytes,
+                                  gdr_stream_t stream) {
+    if (int rc = check_sizes(N, T_total, D, GDR_F32, GDR_F32)) return rc;
+    if (T_total == 0) return set_ok();
+    if (int rc = check_rows("x", x, D, 0, 4)) return rc;
+    if (int rc = check_rows("g", g, D, 0, 4)) return rc;
+    if (int rc = check_rows("y", y, D, D, 4)) return rc;
+    if (int rc = check_aligned16("final_state", final_state)) return rc;
+    if (int rc = check_ints("cu_seqlens", cu_seqlens)) return rc;
+    if (int rc = check_workspace(N, T_total, D, GDR_F32, GDR_F32, workspace, ws_bytes)) return rc;
+    if (int rc = check_device()) return rc;
+    LinrecParams p{};
+    p.x = x; p.g = g; p.out = y; p.last = final_state; p.cu = cu_seqlens;
+    p.ldx = p.ldg = p.ldo = D; p.T = T_total; p.N = N; p.D = D; p.lost = lost_row;
+    return launch_result(launch_scan_losing(p, workspace, (cudaStream_t)stream), "gdr_selftest_linrec_lost_copy launch");
 }
 
 int gdr_linrec_bwd(const void* dy, int64_t dy_stride, const void* g, int64_t g_stride, const void* y,

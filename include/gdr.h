@@ -456,6 +456,18 @@ GDR_API int gdr_get_device_status(gdr_stream_t stream, int* word);
 GDR_API int gdr_selftest_bounded_wait(gdr_stream_t stream);
 
 /*
+ * gdr_selftest_linrec_lost_copy -- the same for gdr_linrec_fwd's way out: the
+ * recurrence over dense fp32 tensors, from zero states, in which the tiles of
+ * row `lost_row` (counted along the tokens, 160 or 320 a row) wait for bytes
+ * that nothing copies.  After a second or two bit 0x200 of the device error
+ * word is set; y and final_state hold the recurrence's values or are unwritten.
+ */
+GDR_API int gdr_selftest_linrec_lost_copy(const float* x, const float* g, const int32_t* cu_seqlens,
+                                          int N, int64_t T_total, int D, int lost_row, float* y,
+                                          float* final_state, void* workspace, size_t ws_bytes,
+                                          gdr_stream_t stream);
+
+/*
  * Kernel timing for diagnostics (no counterpart on the pages; measurement
  * support).  gdr_profile_enable(1): from then on every kernel the library
  * launches is bracketed by two CUDA events on its stream (not capturable:
