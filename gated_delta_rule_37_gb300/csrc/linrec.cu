@@ -680,7 +680,6 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             asm volatile("atom.relaxed.gpu.global.add.u32 %0, [%1], 1;" : "=r"(next) : "l"(p.head) : "memory");
         if (!tc::mbar_wait(mbar, buf, abort_s)) {
             *abort_s = 1;
-            if (many) p.head[1] = 1;
             atomicOr(p.err, kScanError);
         }
         __syncthreads();
@@ -769,7 +768,10 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         if (lc == 0) cut_s[run] = cut;
         if (tid == 0) misc[0] = (int64_t)next < tiles ? (int)next : -1;
         __syncthreads();
-        if (*abort_s) break;
+        if (*abort_s) {
+            if (tid == 0) tc::mbar_wait_copies(mbar, buf);  // none may land after the CTA
+            break;
+        }
         const int ntile = misc[0];
         if (WIDE && tid == 0 && ntile >= 0) request(ntile);  // the stage has been read
 
