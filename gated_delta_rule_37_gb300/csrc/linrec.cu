@@ -844,6 +844,7 @@ linrec_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             if (tid < CC) {
                 float carry = 0.f;
                 for (int k = 0; k < row; ++k) {
+                    if (__float_as_int(cluster_read(misc + 1, k))) *stop_s = 1;  // that tile was not composed
                     const float ra = cluster_read(ta + pos, k), rb = cluster_read(tb + pos, k);
                     carry = __float_as_int(cluster_read(misc + 4, k)) || k == 0 ? rb : fmaf(ra, carry, rb);
                 }

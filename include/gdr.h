@@ -459,7 +459,7 @@ GDR_API int gdr_selftest_bounded_wait(gdr_stream_t stream);
  * gdr_selftest_linrec_lost_copy -- the same for gdr_linrec_fwd's way out: the
  * recurrence over dense fp32 tensors, from zero states, in which the tiles of
  * row `lost_row` (counted along the tokens, 160 or 320 a row) wait for bytes
- * that nothing copies.  After a second or two bit 0x200 of the device error
+ * that nothing copies.  After two or three seconds bit 0x200 of the device error
  * word is set; y and final_state hold the recurrence's values or are unwritten.
  */
 GDR_API int gdr_selftest_linrec_lost_copy(const float* x, const float* g, const int32_t* cu_seqlens,

@@ -34,9 +34,9 @@ def status():
     return w.value
 
 
-# one row of tiles; rows that look back, few and many of them
-@pytest.mark.parametrize("T,D,lost", [(100, 64, 0), (100, 65, 0), (4000, 64, 2), (4000, 65, 0), (60000, 72, 100),
-                                      (40000, 129, 30)])
+# one row of tiles; a cluster of rows; rows that look back, few and many of them
+@pytest.mark.parametrize("T,D,lost", [(100, 64, 0), (100, 65, 0), (900, 64, 0), (900, 64, 1), (1100, 65, 3),
+                                      (900, 65, 5), (4000, 64, 2), (4000, 65, 0), (60000, 72, 100), (40000, 129, 30)])
 def test_scan(T, D, lost):
     r = torch.Generator().manual_seed(T + D)
     x, g = torch.randn(T, D, generator=r).to(DEV), (-torch.rand(T, D, generator=r)).to(DEV)
