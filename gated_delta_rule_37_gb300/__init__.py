@@ -44,9 +44,7 @@ EXPORTED = ("gdr_chunk_workspace_size", "gdr_chunk_fwd", "gdr_chunk_fwd_noalloc"
             "gdr_linrec_workspace_size", "gdr_linrec_fwd", "gdr_linrec_bwd", "gdr_linrec_step",
             "gdr_rmsnorm_fwd", "gdr_rmsnorm_bwd_workspace_size", "gdr_rmsnorm_bwd",
             "gdr_last_error", "gdr_get_device_status", "gdr_selftest_bounded_wait", "gdr_selftest_linrec_lost_copy",
-            "gdr_profile_enable",
-            "gdr_profile_read",
-            "gdr_version")
+            "gdr_selftest_rmsnorm_lost_copy", "gdr_profile_enable", "gdr_profile_read", "gdr_version")
 
 _lib = None
 
@@ -104,6 +102,8 @@ def load(path: str | None = None):
     lib.gdr_selftest_bounded_wait.restype = I
     lib.gdr_selftest_linrec_lost_copy.argtypes = [P, P, P, I, I64, I, I, P, P, P, SZ, P]
     lib.gdr_selftest_linrec_lost_copy.restype = I
+    lib.gdr_selftest_rmsnorm_lost_copy.argtypes = [P, P, P, I64, I, I64, P, P, P, SZ, P]
+    lib.gdr_selftest_rmsnorm_lost_copy.restype = I
     lib.gdr_profile_enable.argtypes = [I]
     lib.gdr_profile_enable.restype = I
     lib.gdr_profile_read.argtypes = [I, ctypes.c_char_p, SZ, ctypes.POINTER(ctypes.c_double),

@@ -471,6 +471,7 @@ struct NormBwdParams {
     int D, parts, tpr, stages;
     float eps;
     unsigned int* err;
+    int64_t lost;  // LOSE only: the row whose copies are not to complete
 };
 
 constexpr unsigned kNormError = 0x400;  // device error word: a row's copies did not land
@@ -579,12 +580,15 @@ __global__ void __launch_bounds__(kMaxThreads, CH <= 2 ? 2 : 1) rmsnorm_bwd_kern
 // The same for rows of 512 elements and more, whose rows (dy, s, d_residual) come
 // through a ring of `stages` rows in shared memory per row's threads (32 or more),
 // filled by bulk copies: the next rows are on their way while one is reduced
-// (16384 x 4096 bf16: 110 us from registers, 90 us through the ring).
-template <typename T, int CH, int MAX_THREADS, int MIN_CTAS>
+// (16384 x 4096 bf16: 110 us from registers, 90 us through the ring).  A row whose
+// copies do not land ends its threads' rows: that row and the later ones stay
+// unwritten, and the CTA's part of dw is NaN.  LOSE: row p.lost waits for 16 bytes that
+// nobody copies, for the test of that.
+template <typename T, int CH, int MAX_THREADS, int MIN_CTAS, bool LOSE>
 __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) rmsnorm_bwd_ring_kernel(NormBwdParams p) {
     __shared__ float2 exchange[2][kMaxThreads / 32];
     __shared__ uint64_t full_s[kMaxThreads / 32][kMaxStages];
-    __shared__ int never;
+    __shared__ int never, lost_s[kMaxThreads / 32];  // per row's threads: the step that lost its copies
     extern __shared__ __align__(128) unsigned char ring[];
     const int tpr = p.tpr, slots = blockDim.x / tpr, slot = threadIdx.x / tpr, l = threadIdx.x % tpr;
     RowReduce reduce{exchange, tpr, slot, 0};
@@ -595,7 +599,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) rmsnorm_bwd_ring_kernel
     const int64_t stride = (int64_t)gridDim.x * slots;
     auto request = [&](int stage, int64_t m) {  // one thread of the row's
         const uint32_t at = own + stage * rows * row_bytes, bar = full + stage * 8;
-        tc::mbar_arrive_tx(bar, rows * row_bytes);
+        tc::mbar_arrive_tx(bar, rows * row_bytes + (LOSE && m == p.lost ? 16 : 0));
         tc::bulk_g2s(at, static_cast<const T*>(p.dy) + m * p.lddy, row_bytes, bar);
         tc::bulk_g2s(at + row_bytes, static_cast<const T*>(p.s) + m * p.lds, row_bytes, bar);
         if (p.ds) tc::bulk_g2s(at + 2 * row_bytes, static_cast<const T*>(p.ds) + m * p.ldds, row_bytes, bar);
@@ -603,6 +607,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) rmsnorm_bwd_ring_kernel
     const int64_t first = (int64_t)blockIdx.x * slots + slot;
     if (l == 0) {
         never = 0;
+        lost_s[slot] = 0x7fffffff;
         for (int k = 0; k < p.stages; ++k) tc::mbar_init(full + k * 8, 1);
         tc::mbar_fence_init();
         for (int k = 0; k < p.stages; ++k)
@@ -619,11 +624,12 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) rmsnorm_bwd_ring_kernel
         for (int i = 0; i < 4; ++i) dw[c][i] = both(0.f);
     }
     __syncthreads();
-    int stage = 0, parity = 0;
+    volatile int* lost_at = lost_s + slot;
+    int stage = 0, parity = 0, step = 0;
     bool lost = false;
-    for (int64_t m = first; m < p.M; m += stride) {
-        if (!lost && !tc::mbar_wait(full + stage * 8, parity, &never)) {
-            lost = true;  // later waits are not begun: the rows run out without them
+    for (int64_t m = first; m < p.M; m += stride, ++step) {
+        if (!tc::mbar_wait(full + stage * 8, parity, &never)) {
+            *lost_at = step;
             atomicOr(p.err, kNormError);
         }
         const unsigned char* at = ring + (own - tc::smem_u32(ring)) + stage * rows * row_bytes;
@@ -649,6 +655,19 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) rmsnorm_bwd_ring_kernel
         }
         const float2 sums = reduce.sum(make_float2(square.x + square.y, dot.x + dot.y));
         if (tpr == 32) __syncwarp();
+        // one thread's wait may run out where another's did not: all have met since
+        if (*lost_at <= step) {
+            lost = true;
+            if (l == 0)  // none of the copies on their way may land behind this
+                for (int k = 0; k < p.stages && m + k * stride < p.M; ++k) {
+                    tc::mbar_wait_copies(full + stage * 8, parity);
+                    if (++stage == p.stages) {
+                        stage = 0;
+                        parity ^= 1;
+                    }
+                }
+            break;
+        }
         if (l == 0 && m + p.stages * stride < p.M) request(stage, m + p.stages * stride);  // read by all
         if (++stage == p.stages) {
             stage = 0;
@@ -671,6 +690,11 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) rmsnorm_bwd_ring_kernel
         }
     }
     if (!p.dw) return;
+    if (lost)
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dw[c][i] = both(NAN);
     __syncthreads();  // the ring becomes the place of the sums
     float2* dw2 = reinterpret_cast<float2*>(ring);
     for (int k = 0; k < slots; ++k) {
@@ -808,9 +832,9 @@ cudaError_t launch_bwd_ch(NormBwdParams p, cudaStream_t s) {
 }
 
 // CTAS CTAs per SM; the ring takes their share of its 227 KB.
-template <typename T, int CH, int THREADS, int CTAS>
+template <typename T, int CH, int THREADS, int CTAS, bool LOSE = false>
 cudaError_t launch_bwd_ring(NormBwdParams p, cudaStream_t s) {
-    auto kernel = rmsnorm_bwd_ring_kernel<T, CH, THREADS, CTAS>;
+    auto kernel = rmsnorm_bwd_ring_kernel<T, CH, THREADS, CTAS, LOSE>;
     constexpr int kShare = 227 * 1024 / CTAS - 2048;
     const int slots = THREADS / p.tpr, stage = slots * 3 * p.D * (int)sizeof(T);
     p.stages = kShare / stage < kMaxStages ? kShare / stage : kMaxStages;
@@ -983,6 +1007,29 @@ int gdr_rmsnorm_bwd(const void* dy, int64_t dy_stride, const void* s, int64_t s_
                       (!d_residual_out || wide_rows(d_residual_out, d_residual_out_stride, esize));
     return launch_result(dtype == GDR_BF16 ? launch_bwd<__nv_bfloat16>(p, wide, st) : launch_bwd<float>(p, wide, st),
                     "gdr_rmsnorm_bwd launch");
+}
+
+int gdr_selftest_rmsnorm_lost_copy(const void* dy, const void* s, const float* weight, int64_t M, int D,
+                                   int64_t lost_row, void* dx, float* dweight, void* workspace, size_t ws_bytes,
+                                   gdr_stream_t stream) {
+    if (int rc = check_sizes(M, D, 1e-6f, GDR_BF16)) return rc;
+    if (D % 8 || D < 512 || D > 4096) return set_last_error(GDR_ERR_UNSUPPORTED, "D %d", D);
+    if (M == 0) return set_ok();
+    const void* all[] = {dy, s, weight, dx, dweight};
+    for (const void* p : all)
+        if (int rc = check_floats("tensor", p)) return rc;
+    size_t need = 0;
+    if (int rc = gdr_rmsnorm_bwd_workspace_size(M, D, &need)) return rc;
+    if (!workspace || ws_bytes < need) return set_last_error(GDR_ERR_WORKSPACE, "workspace too small");
+    if (int rc = check_device()) return rc;
+    NormBwdParams p{};
+    p.dy = dy; p.s = s; p.w = weight; p.dx = dx; p.dw = dweight;
+    p.partial = static_cast<float*>(workspace);
+    p.lddy = p.lds = p.lddx = D;
+    p.M = M; p.D = D; p.eps = 1e-6f; p.lost = lost_row;
+    p.tpr = row_threads(D / 8, 2, 32);
+    return launch_result(launch_bwd_ring<__nv_bfloat16, 2, 256, 2, true>(p, (cudaStream_t)stream),
+                         "gdr_selftest_rmsnorm_lost_copy launch");
 }
 
 }  // extern "C"

@@ -425,7 +425,10 @@ GDR_API int gdr_rmsnorm_bwd_workspace_size(int64_t M, int D, size_t* bytes);
  *   workspace              gdr_rmsnorm_bwd_workspace_size bytes, 256-byte
  *                          aligned; needs no initialisation; may be NULL with
  *                          dweight NULL
- * The rows are summed in a fixed order: equal inputs give equal bits.
+ * The rows are summed in a fixed order: equal inputs give equal bits.  Rows
+ * come by copies whose waits are bounded (one second): one that gives up is
+ * reported by gdr_get_device_status; dx rows that the call has not written by
+ * then stay unwritten, and dweight is then NaN.
  */
 GDR_API int gdr_rmsnorm_bwd(const void* dy, int64_t dy_stride, const void* s, int64_t s_stride,
                             const float* weight, const void* d_residual_out,
@@ -466,6 +469,16 @@ GDR_API int gdr_selftest_linrec_lost_copy(const float* x, const float* g, const 
                                           int N, int64_t T_total, int D, int lost_row, float* y,
                                           float* final_state, void* workspace, size_t ws_bytes,
                                           gdr_stream_t stream);
+
+/*
+ * gdr_selftest_rmsnorm_lost_copy -- the same for gdr_rmsnorm_bwd's way out, on
+ * dense bf16 rows of 512 to 4096 elements with eps 1e-6: row `lost_row` waits
+ * for bytes that nothing copies.  Bit 0x400 of the device error word is set; dx
+ * holds the gradients or is unwritten, and dweight is NaN.
+ */
+GDR_API int gdr_selftest_rmsnorm_lost_copy(const void* dy, const void* s, const float* weight, int64_t M,
+                                           int D, int64_t lost_row, void* dx, float* dweight,
+                                           void* workspace, size_t ws_bytes, gdr_stream_t stream);
 
 /*
  * Kernel timing for diagnostics (no counterpart on the pages; measurement

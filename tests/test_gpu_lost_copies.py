@@ -57,3 +57,26 @@ def test_scan(T, D, lost):
     assert status() == 0
     assert all(bits_equal(a, b) for a, b in zip(gdr.linrec_fwd(x, g, cu), (want, last)))   # the context is intact
     assert status() == 0
+
+
+# one to eight rows at a time in a CTA; the first row of a CTA and later ones, the last of all
+@pytest.mark.parametrize("M,D,lost", [(1, 4096, 0), (5, 512, 3), (3000, 4096, 0), (3000, 4096, 2999), (6000, 512, 2500),
+                                      (4000, 1024, 1300), (2000, 2048, 700)])
+def test_norm_backward(M, D, lost):
+    r = torch.Generator().manual_seed(M + D)
+    dy, s = (torch.randn(M, D, generator=r).to(BF).to(DEV) for _ in range(2))
+    w = torch.randn(D, generator=r).to(DEV)
+    want, dw = gdr.rmsnorm_bwd(dy, s, w)
+    dx = Guarded((M, D), BF, DEV, fill_bytes=sentinel_like((M, D), BF))
+    got_dw = torch.zeros(D, device=DEV)
+    n = gdr.rmsnorm_bwd_workspace_size(M, D)
+    ws = torch.zeros(n, dtype=torch.uint8, device=DEV)
+    assert gdr.load().gdr_selftest_rmsnorm_lost_copy(ptr(dy), ptr(s), ptr(w), M, D, lost, ptr(dx.view), ptr(got_dw),
+                                                     ptr(ws), n, None) == 0
+    assert status() == 0x400 and dx.guards_intact()
+    blank = (dx.view.view(torch.int16) == sentinel_like((1,), BF).view(torch.int16).to(DEV)).all(1)
+    right = (dx.view.view(torch.int16) == want.view(torch.int16)).all(1)
+    assert blank[lost] and (blank | right).all(), "neither the call's rows nor untouched"
+    assert torch.isnan(got_dw).all()
+    assert all(bits_equal(a, b) for a, b in zip(gdr.rmsnorm_bwd(dy, s, w), (want, dw)))
+    assert status() == 0
