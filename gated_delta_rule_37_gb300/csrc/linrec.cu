@@ -1278,9 +1278,19 @@ __global__ void linrec_validate_kernel(const int32_t* cu, int N, int64_t T, cons
         }
     }
     if (tid == 0 && (cu[0] != 0 || cu[N] < 0 || cu[N] > T)) bad |= L_CU;
-    const int64_t rows = min(max((int64_t)cu[N], (int64_t)0), T);
-    for (int64_t i = tid; i < rows * D; i += nth)
-        if (!(to_f(g[i / D * ldg + i % D]) <= 0.f)) bad |= L_GATE;
+    auto gates = [&](int64_t row, int64_t rows, int64_t i, int64_t step) {
+        const TG* from = g + row * ldg;
+        for (; i < rows * D; i += step)
+            if (!(to_f(from[i / D * ldg + i % D]) <= 0.f)) bad |= L_GATE;
+    };
+    if (!idx) {
+        gates(0, min(max((int64_t)cu[N], (int64_t)0), T), tid, nth);
+    } else {  // a sequence per CTA: the rows of padding are not read
+        for (int64_t b = blockIdx.x; b < N; b += gridDim.x) {
+            const int64_t lo = max((int64_t)cu[b], (int64_t)0), hi = min((int64_t)cu[b + 1], T);
+            if (idx[b] >= 0 && idx[b] < num_slots) gates(lo, hi - lo, threadIdx.x, blockDim.x);
+        }
+    }
     if (bad) atomicOr(&g_linrec_findings, bad);
 }
 

@@ -348,9 +348,9 @@ GDR_API int gdr_linrec_bwd(const void* dy, int64_t dy_stride, const void* g, int
  *   state_pool     [num_slots, D] pool_dtype (GDR_F32 or GDR_BF16), dense; read,
  *                  and written in place only with GDR_COMMIT
  *   state_indices  [N] int32 device: the slot of each sequence; a value < 0 is
- *                  padding (nothing of that sequence is read or written; nor is
- *                  it for a value >= num_slots, an error that GDR_VALIDATE
- *                  reports).  With GDR_COMMIT valid slots must be unique.
+ *                  padding (nothing of that sequence is read or written, its
+ *                  gates are not checked; nor for a value >= num_slots, an
+ *                  error that GDR_VALIDATE reports).  With GDR_COMMIT valid slots must be unique.
  *   intermediate_states  [rows >= N, steps, D] pool dtype, dense, or NULL: row
  *                  b, step t receives the state after token t of sequence b;
  *                  steps >= L_b and padding rows are untouched.  L_b <= steps

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import gated_delta_rule_37_gb300 as gdr
-from tests.test_gpu_linrec import DEV, TYPES, check_bwd, check_fwd, make
+from tests.test_gpu_linrec import DEV, F, TYPES, check_bwd, check_fwd, make
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +38,25 @@ def test_unaligned_rows_through_a_stage_used_again(types):
     check_fwd(c, out.cpu(), hT.cpu())
     check_bwd(c, *(t.cpu() for t in gdr.linrec_bwd(x, g, y, cu, initial_state=h0, d_final_state=df)))
     assert gdr.device_status() == 0
+
+
+def test_validation_of_a_step_reads_no_padding():
+    """Gates of padding sequences are not looked at, whatever they hold; those
+    of the others are, in the first row and the last."""
+    lens = [2, 3, 0, 5, 1]
+    c = make(62, lens, 40, F, F, pad=2)
+    at = [int(v) for v in c["cu"]]
+    dev = {k: c[k].to(DEV) for k in ("x", "g", "cu")}
+    idx = torch.tensor([3, -1, 0, -7, 5], dtype=torch.int32, device=DEV)
+    call = lambda g: gdr.linrec_step(dev["x"], g, torch.zeros(6, 40, device=DEV), idx, dev["cu"],  # noqa: E731
+                                     flags=gdr.GDR_COMMIT | gdr.GDR_VALIDATE)
+    g = dev["g"].clone()
+    for a, b in ((at[1], at[2]), (at[3], at[4]), (at[5], c["T"])):
+        g[a:b] = float("nan")
+    call(g)
+    for row in (at[0], at[1] - 1, at[4]):
+        for value in (float("nan"), 0.5):
+            bad = g.clone()
+            bad[row, 39] = value
+            with pytest.raises(gdr.GdrError, match="gate"):
+                call(bad)
