@@ -1299,16 +1299,19 @@ int validate(const int32_t* cu, int N, int64_t T, const void* g, int64_t ldg, in
     void* word = nullptr;
     if (cudaGetSymbolAddress(&word, g_linrec_findings) != cudaSuccess)
         return set_last_error(GDR_ERR_LAUNCH, "validation word unavailable");
-    cudaMemsetAsync(word, 0, sizeof(unsigned), s);
+    cudaError_t e = cudaMemsetAsync(word, 0, sizeof(unsigned), s);
+    if (e != cudaSuccess) return set_last_error(GDR_ERR_LAUNCH, "validation: %s", cudaGetErrorString(e));
     if (gate_dtype == GDR_BF16)
         linrec_validate_kernel<<<304, 256, 0, s>>>(cu, N, T, static_cast<const __nv_bfloat16*>(g), ldg, D, idx,
                                                    num_slots, commit, steps);
     else
         linrec_validate_kernel<<<304, 256, 0, s>>>(cu, N, T, static_cast<const float*>(g), ldg, D, idx, num_slots,
                                                    commit, steps);
+    e = cudaGetLastError();
     unsigned found = 0;
-    cudaMemcpyAsync(&found, word, sizeof(unsigned), cudaMemcpyDeviceToHost, s);
-    const cudaError_t e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(&found, word, sizeof(unsigned), cudaMemcpyDeviceToHost, s);
+    const cudaError_t ended = cudaStreamSynchronize(s);  // also behind a copy that was refused: `found` is on this stack
+    if (e == cudaSuccess) e = ended;
     if (e != cudaSuccess) return set_last_error(GDR_ERR_LAUNCH, "validation: %s", cudaGetErrorString(e));
     if (found)
         return set_last_error(GDR_ERR_VALIDATION, "input validation failed (0x%x):%s%s%s%s%s", found,
