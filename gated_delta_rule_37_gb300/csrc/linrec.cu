@@ -58,6 +58,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <mutex>
 #include <type_traits>
 
 #include "common.cuh"
@@ -1296,6 +1297,9 @@ __global__ void linrec_validate_kernel(const int32_t* cu, int N, int64_t T, cons
 
 int validate(const int32_t* cu, int N, int64_t T, const void* g, int64_t ldg, int D, int gate_dtype,
              const int32_t* idx, int num_slots, int commit, int steps, cudaStream_t s) {
+    // one word for all: from its clearing to its reading it belongs to one call
+    static std::mutex turn;
+    const std::lock_guard<std::mutex> own(turn);
     void* word = nullptr;
     if (cudaGetSymbolAddress(&word, g_linrec_findings) != cudaSuccess)
         return set_last_error(GDR_ERR_LAUNCH, "validation word unavailable");

@@ -81,7 +81,8 @@ typedef enum gdr_gate_kind {
                               * The findings land in one library-wide device word:
                               * validated calls from different host threads must be
                               * serialised by the caller, or one call's reset of the
-                              * word can hide the other's findings.                  */
+                              * word can hide the other's findings.  (The gdr_linrec_*
+                              * calls have a word of their own and take turns.)      */
 #define GDR_CHANNEL_GATE 0x10 /* gdr_recurrent_fwd: g is per key channel, [T_total, Hv, K]  */
 #define GDR_CHUNK_SCAN 0x20   /* gdr_chunk_fwd: chunk-parallel state scan (long sequences)     */
 

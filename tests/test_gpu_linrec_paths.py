@@ -1,6 +1,8 @@
 """Paths of the gated linear recurrence that depend on the call's size: stages
 used again by later tiles; against the fp64 oracle, with the bounds of
 tests/test_gpu_linrec.py."""
+import threading
+
 import pytest
 import torch
 
@@ -60,3 +62,31 @@ def test_validation_of_a_step_reads_no_padding():
             bad[row, 39] = value
             with pytest.raises(gdr.GdrError, match="gate"):
                 call(bad)
+
+
+def test_validated_calls_from_two_threads():
+    """One thread's input is good and the other's bad, over and over: neither
+    takes the other's findings, or loses its own."""
+    c = make(63, [60], 64, F, F)
+    x, g, cu = (c[k].to(DEV) for k in ("x", "g", "cu"))
+    bad = g.clone()
+    bad[7, 9] = 1.0
+    torch.cuda.synchronize()
+    found = {}
+
+    def many(name, gates):
+        torch.cuda.set_device(0)
+        stream = torch.cuda.Stream()
+        found[name] = 0
+        for _ in range(1000):
+            try:
+                gdr.linrec_fwd(x, gates, cu, flags=gdr.GDR_VALIDATE, stream=stream)
+            except gdr.GdrError:
+                found[name] += 1
+
+    threads = [threading.Thread(target=many, args=a) for a in (("good", g), ("bad", bad), ("good too", g))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert found == {"good": 0, "bad": 1000, "good too": 0}
