@@ -1354,9 +1354,12 @@ int check_ints(const char* name, const void* p) {
 }
 
 // A sequence's last state may be written while another tile has yet to read its first.
-int check_apart(const char* name, const float* written, const float* read) {
-    if (written && written == read)
-        return set_last_error(GDR_ERR_INVALID_ARG, "%s must not be a state that the call reads", name);
+// Both are [N, D], dense.
+int check_apart(const char* name, const float* written, const float* read, int N, int D) {
+    const uintptr_t w = reinterpret_cast<uintptr_t>(written), r = reinterpret_cast<uintptr_t>(read);
+    const uintptr_t bytes = (uintptr_t)N * D * sizeof(float);
+    if (written && read && (w < r ? r - w : w - r) < bytes)
+        return set_last_error(GDR_ERR_INVALID_ARG, "%s must not overlap a state that the call reads", name);
     return GDR_OK;
 }
 
@@ -1408,7 +1411,7 @@ int gdr_linrec_fwd(const void* x, int64_t x_stride, const void* g, int64_t g_str
         return set_last_error(GDR_ERR_INVALID_ARG, "unsupported flags 0x%x for gdr_linrec_fwd", flags);
     if (int rc = check_aligned16("initial_state", initial_state)) return rc;
     if (int rc = check_aligned16("final_state", final_state)) return rc;
-    if (int rc = check_apart("final_state", final_state, initial_state)) return rc;
+    if (int rc = check_apart("final_state", final_state, initial_state, N, D)) return rc;
     cudaStream_t s = (cudaStream_t)stream;
     if (T_total == 0) return pass_states(initial_state, final_state, N, D, s);
     if (int rc = check_rows("x", x, x_stride, 0, element(dtype))) return rc;
@@ -1454,8 +1457,8 @@ int gdr_linrec_bwd(const void* dy, int64_t dy_stride, const void* g, int64_t g_s
     if (int rc = check_aligned16("initial_state", initial_state)) return rc;
     if (int rc = check_aligned16("d_final_state", d_final_state)) return rc;
     if (int rc = check_aligned16("d_initial_state", d_initial_state)) return rc;
-    if (int rc = check_apart("d_initial_state", d_initial_state, initial_state)) return rc;
-    if (int rc = check_apart("d_initial_state", d_initial_state, d_final_state)) return rc;
+    if (int rc = check_apart("d_initial_state", d_initial_state, initial_state, N, D)) return rc;
+    if (int rc = check_apart("d_initial_state", d_initial_state, d_final_state, N, D)) return rc;
     cudaStream_t s = (cudaStream_t)stream;
     if (T_total == 0) return pass_states(d_final_state, d_initial_state, N, D, s);
     if (int rc = check_rows("dy", dy, dy_stride, 0, element(dtype))) return rc;

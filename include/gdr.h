@@ -281,7 +281,7 @@ GDR_API int gdr_gating_fwd(const void* a, const float* dt_bias, const float* A_l
  *     multiples of 8 take the fast path.
  *   - dtype (GDR_BF16 or GDR_F32) is that of x, y and their gradients,
  *     gate_dtype (GDR_BF16 or GDR_F32) that of g and dg.  Prefill states are
- *     fp32 [N, D], dense; the one that is written is not one that is read.
+ *     fp32 [N, D], dense; the one that is written overlaps none that is read.
  *   - cu_seqlens [N+1] int32 device, cu[0] = 0, non-decreasing; sequences may
  *     be empty.  cu[N] may be less than T_total (a padded batch): rows from
  *     cu[N] on are neither read nor written.  A cu_seqlens that breaks these
