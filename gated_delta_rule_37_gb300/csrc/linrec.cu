@@ -1339,6 +1339,11 @@ int check_sizes(int N, int64_t T, int D, int dtype, int gate_dtype) {
         return set_last_error(GDR_ERR_UNSUPPORTED, "T_total (%lld) above 2^31 - 512", (long long)T);
     if (N > 0x7fffffff / 2) return set_last_error(GDR_ERR_UNSUPPORTED, "N too large");
     if (D > 1 << 24) return set_last_error(GDR_ERR_UNSUPPORTED, "D (%d) above 2^24", D);
+    return GDR_OK;
+}
+
+// The scans, as gdr_chunk_fwd: rows without a sequence.
+int check_sequences(int N, int64_t T) {
     if (T > 0 && N == 0) return set_last_error(GDR_ERR_INVALID_ARG, "T_total > 0 with N == 0");
     return GDR_OK;
 }
@@ -1393,6 +1398,7 @@ extern "C" {
 int gdr_linrec_workspace_size(int N, int64_t T_total, int D, int dtype, int gate_dtype, size_t* bytes) {
     if (!bytes) return set_last_error(GDR_ERR_INVALID_ARG, "bytes is NULL");
     if (int rc = check_sizes(N, T_total, D, dtype, gate_dtype)) return rc;
+    if (int rc = check_sequences(N, T_total)) return rc;
     if (dtype == GDR_BF16)
         *bytes = gate_dtype == GDR_BF16 ? scan_bytes<__nv_bfloat16, __nv_bfloat16>(T_total, D)
                                         : scan_bytes<__nv_bfloat16, float>(T_total, D);
@@ -1407,6 +1413,7 @@ int gdr_linrec_fwd(const void* x, int64_t x_stride, const void* g, int64_t g_str
                    void* y, int64_t y_stride, float* final_state, void* workspace, size_t ws_bytes,
                    gdr_stream_t stream) {
     if (int rc = check_sizes(N, T_total, D, dtype, gate_dtype)) return rc;
+    if (int rc = check_sequences(N, T_total)) return rc;
     if (flags & ~GDR_VALIDATE)
         return set_last_error(GDR_ERR_INVALID_ARG, "unsupported flags 0x%x for gdr_linrec_fwd", flags);
     if (int rc = check_aligned16("initial_state", initial_state)) return rc;
@@ -1432,6 +1439,7 @@ int gdr_selftest_linrec_lost_copy(const float* x, const float* g, const int32_t*
                                   int D, int lost_row, float* y, float* final_state, void* workspace, size_t ws_bytes,
                                   gdr_stream_t stream) {
     if (int rc = check_sizes(N, T_total, D, GDR_F32, GDR_F32)) return rc;
+    if (int rc = check_sequences(N, T_total)) return rc;
     if (T_total == 0) return set_ok();
     if (int rc = check_rows("x", x, D, 0, 4)) return rc;
     if (int rc = check_rows("g", g, D, 0, 4)) return rc;
@@ -1452,6 +1460,7 @@ int gdr_linrec_bwd(const void* dy, int64_t dy_stride, const void* g, int64_t g_s
                    void* dx, int64_t dx_stride, void* dg, int64_t dg_stride, float* d_initial_state,
                    void* workspace, size_t ws_bytes, gdr_stream_t stream) {
     if (int rc = check_sizes(N, T_total, D, dtype, gate_dtype)) return rc;
+    if (int rc = check_sequences(N, T_total)) return rc;
     if (flags & ~GDR_VALIDATE)
         return set_last_error(GDR_ERR_INVALID_ARG, "unsupported flags 0x%x for gdr_linrec_bwd", flags);
     if (int rc = check_aligned16("initial_state", initial_state)) return rc;

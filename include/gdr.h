@@ -31,7 +31,9 @@
  *   - Return value: GDR_OK or a gdr_status error code; on error nothing was
  *     launched and gdr_last_error() describes the problem (thread-local).
  *     Argument and shape checks happen on the host before any launch.
- *   - Empty work (T_total == 0 or N == 0) returns GDR_OK without a launch.
+ *   - Empty work (T_total == 0 or N == 0) returns GDR_OK without a launch (but
+ *     for final states, which are then the initial ones).  A prefill or its
+ *     backward with T_total > 0 and N == 0 is refused.
  */
 #ifndef GDR_H_
 #define GDR_H_
