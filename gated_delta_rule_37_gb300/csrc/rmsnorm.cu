@@ -866,8 +866,10 @@ cudaError_t launch_bwd(NormBwdParams p, bool wide, cudaStream_t s) {
             p.tpr = 512;
             return launch_bwd_ring<T, 2, 512, 1>(p, s);
         }
-        p.tpr = 512;
-        return launch_bwd_ring<T, 4, 512, 1>(p, s);
+        if constexpr (sizeof(T) == 2) {  // 32768 bytes of fp32 are 1024 pieces already
+            p.tpr = 512;
+            return launch_bwd_ring<T, 4, 512, 1>(p, s);
+        }
     }
     if (!wide) {
         const int ch = p.D <= 4 * kMaxThreads ? 4 : p.D <= 16 * kMaxThreads ? 16 : 64;
