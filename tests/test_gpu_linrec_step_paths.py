@@ -11,6 +11,7 @@ import pytest
 import torch
 
 import gated_delta_rule_37_gb300 as gdr
+from tests.gpu_util import sentinel_like
 from tests.test_gpu_linrec import BF, DEV, F, TYPES, check_step, f64, pool_case, run_step
 
 pytestmark = pytest.mark.gpu
@@ -102,3 +103,38 @@ def test_exponential(D):
     want = np.exp(f64(g))
     for got in (y, one, scan, last):
         assert (np.abs(f64(got) - want) <= 3 * U * want).all()
+
+
+@pytest.mark.parametrize("D", [4096, 4095])
+def test_offsets_beyond_32_bits(D):
+    """Slots, rows and kept states whose elements' numbers pass 2^31: the last ones against 64 bits."""
+    N, n, steps = (1 << 31) // (3 * D) + 40, 30, 3
+    c = pool_case(68, [1 + i % 3 for i in range(n)], D, BF, BF, BF, skip={4: -1})
+    T, slots = N - n + c["T"], (1 << 31) // D + 50
+    assert (N - n) * steps * D > 1 << 31 and (slots - 40) * D > 1 << 31
+    # sequences before: padding of one token each
+    big = {k: torch.zeros(T, D, dtype=BF, device=DEV) for k in ("x", "g")}
+    for k, v in big.items():
+        v[T - c["T"]:] = c[k].to(DEV)
+    pool = torch.zeros(slots, D, dtype=BF, device=DEV)
+    first = slots - c["pool"].shape[0]
+    pool[first:] = c["pool"].to(DEV)
+    idx = torch.full((N,), -1, dtype=torch.int32)
+    idx[N - n:] = torch.where(c["idx"] >= 0, c["idx"] + first, c["idx"])
+    cu = torch.cat([torch.arange(N - n, dtype=torch.int32), c["cu"] + (N - n)])
+    states = torch.zeros(N, steps, D, dtype=BF, device=DEV)
+    y = torch.zeros(T, D, dtype=BF, device=DEV)
+    gdr.linrec_step(big["x"], big["g"], pool, idx.to(DEV), cu.to(DEV), y=y, intermediate_states=states)
+    assert not y[:N - n].any() and not states[:N - n].any() and not pool[:first].any()
+    tail = sentinel_like((c["T"], D), BF)
+    kept = sentinel_like((n, steps, D), BF)
+    got_y, got_s = y[N - n:].cpu(), states[N - n:].cpu()
+    at = [int(v) for v in c["cu"]]
+    for k, i in enumerate(c["idx"].tolist()):
+        if i >= 0:
+            tail[at[k]:at[k + 1]] = got_y[at[k]:at[k + 1]]
+            kept[k, :at[k + 1] - at[k]] = got_s[k, :at[k + 1] - at[k]]
+        else:
+            assert not got_y[at[k]:at[k + 1]].any()
+        assert not got_s[k, at[k + 1] - at[k] if i >= 0 else 0:].any()
+    check_step(c, pool[first:].cpu(), tail, kept, commit=True)

@@ -84,3 +84,26 @@ def test_a_bad_value_in_a_group(D, group, dtype, aligned):
             assert (s[:, -1] == float("inf")).all() and torch.isnan(own[:, span - 3]).all()
             own[:, span - 3] = 0
             assert (own == 0).all()
+
+
+@pytest.mark.parametrize("aligned", [True, False], ids=["aligned", "unaligned"])
+@pytest.mark.parametrize("dtype,ints", [(BF, torch.int16), (F, torch.int32)], ids=["bf16", "f32"])
+def test_residual_addition_of_any_bits(dtype, ints, aligned):
+    """The stored sum is the rounded sum for all exponents: subnormal numbers,
+    sums that overflow or cancel, infinities, NaN."""
+    r = torch.Generator().manual_seed(5)
+    M, D = 1500, 1000
+    a, b = (torch.randint(-(1 << 8 * dtype.itemsize - 1), 1 << 8 * dtype.itemsize - 1, (M, D), generator=r).to(ints).view(dtype)
+            for _ in range(2))
+    b[: M // 3] = (a[: M // 3].view(ints) ^ torch.randint(0, 4, (M // 3, D), generator=r).to(ints)).view(dtype).neg()
+    near = torch.randint(-300, 300, (M // 3, D), generator=r).to(ints)
+    b[M // 3: 2 * (M // 3)] = (a[M // 3: 2 * (M // 3)].view(ints) + near * (1 << 8 * dtype.itemsize - 12)).view(dtype)
+    wide = torch.zeros(2, M, D + 8, dtype=dtype, device=DEV)
+    at = 0 if aligned else 1
+    x, res = wide[0, :, at:at + D], wide[1, :, at:at + D]
+    x.copy_(a)
+    res.copy_(b)
+    got = gdr.rmsnorm_fwd(x, torch.ones(D, device=DEV), residual=res)[1].cpu()
+    want = (a.double() + b.double()).to(dtype) if dtype == F else (a.float() + b.float()).to(dtype)
+    nan = torch.isnan(want)
+    assert torch.equal(torch.isnan(got), nan) and torch.equal(got.view(ints)[~nan], want.view(ints)[~nan])
