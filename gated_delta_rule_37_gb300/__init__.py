@@ -4,6 +4,8 @@ Every step of the computation runs in the library's CUDA kernels; this module
 only marshals torch tensors (device memory, streams) into the C ABI declared in
 ``include/gdr.h`` and raises on a non-zero status.  There is no CPU fallback:
 if ``libgdr.so`` is missing or no CUDA device is present, calls fail loudly.
+Nothing is recorded for automatic differentiation: outputs carry no gradient
+function, whatever the inputs require; gradients come from the ``*_bwd`` calls.
 
 Entry points (same names as the C ABI, without the ``gdr_`` prefix):
   chunk_fwd           chunked prefill          -> o, final_state

@@ -32,7 +32,9 @@
 // Taylor polynomial, ending in a fused multiply-add with 1, has a mean error
 // below 0.001 * 2^-24 there.  A run's decay is the exponential of its gates' sum:
 // the product of its tokens' rounded decays left 1.0e-6 at that memory, the sum
-// 3.5e-7 (fp32 states against 64 bits).
+// 3.5e-7 (fp32 states against 64 bits, channels of up to that memory; where all have
+// it, 5e-7, and 8e-7 for the gradient of fp32 initial states, whose runs are shorter:
+// the random walk of one rounding per run).
 //
 // What bounds it.  Less than two flops per byte: memory.  The floor of a call is
 // its rows' bytes at the copy rate (6.69 TB/s measured); one GB300, device times:
@@ -40,7 +42,7 @@
 //                          fp32, 16384 rows   123 us   98 %)
 //   backward 32768 x 4096  bf16, bf16 gates   214 us   94 %    (fp32 gates 275 us, 102 %;
 //                          fp32, 16384 rows   200 us  100 %)
-//   backward 7001 x 1001   fp32, odd rows      42 us   49 %    (50000 rows 193 us, 78 %)
+//   backward 7001 x 1001   fp32, odd rows      42 us   50 %    (50000 rows 193 us, 78 %)
 //   forward  6113 x 2048   bf16, 4 sequences   30 us   50 %
 // Long calls of narrow types are held by the chain of one tile's steps (composition,
 // fold, look-back, evaluation: about 10,500 cycles at two CTAs per SM, of which the
@@ -1233,9 +1235,12 @@ cudaError_t launch_step_t(const StepParams& p, cudaStream_t s) {
     if (p.D % 8 || !wide_rows<TX>(p.x, p.ldx, p.D) || !wide_rows<TG>(p.g, p.ldg, p.D) ||
         !wide_rows<TX>(p.y, p.ldy, p.D))
         return launch_step_v<TX, TG, TP, 1>(p, s);
-    // 8 channels per thread where that still gives every SM's schedulers work (the
-    // decode batch of 256: 3.8 us, with 4 channels 4.9, with 2 6.6), fewer otherwise
-    // (the verify batch of 64: with 2 channels 6.4 us, with 4 7.5, with 8 11.4)
+    // 8 channels per thread where that still gives every SM's schedulers work (decode of
+    // 256 x 4096: 3.6 us, with 4 channels 4.8, with 2 5.7), fewer otherwise (verify of 64
+    // x 1..12 x 4096 with states kept: with 2 channels 6.4 us, with 4 7.4, with 8 9.0).
+    // The number of tokens need not enter: verify of 128, 256 and 512 sequences takes
+    // 9.5, 13.4 and 24.3 us by this rule (4, 8, 8 channels), the best of the others 9.0,
+    // 13.8 and 24.6.
     const int64_t channels = (int64_t)p.N * p.D, full = (int64_t)sm_count() * 768;
     return channels >= full * 8 ? launch_step_v<TX, TG, TP, 8>(p, s)
          : channels >= full * 4 ? launch_step_v<TX, TG, TP, 4>(p, s) : launch_step_v<TX, TG, TP, 2>(p, s);

@@ -8,11 +8,25 @@
 // that alone).  One GB300, device times, of the copy rate (6.69 TB/s measured):
 //   forward  32768 x 4096  bf16 + residual, e4m3 by 128   153 us   92 %
 //            16384 x 4096  bf16 + residual, bf16           84 us   95 %
-//             8192 x 8192  bf16 + residual, e4m3 by row    90 us   78 %
+//            16384 x 4096  fp32 + residual                172 us   93 %
+//             8192 x 8192  bf16 + residual, e4m3 by row    88 us   80 %
+//            98000 x 128   bf16                            18 us   42 %
 //             3001 x 1001  fp32, e4m3 by row, odd rows     11 us   20 % (in L2)
 //                8 x 4096  bf16 + residual                2.5 us   (latency)
-//   backward 16384 x 4096  bf16 + residual gradient        90 us   90 %
-//             9000 x 1001  fp32, odd rows                  43 us   51 %
+//   backward 16384 x 4096  bf16 + residual gradient        90 us   89 %
+//            16384 x 4096  fp32 + residual gradient       167 us   96 %
+//             8192 x 7168  bf16 + residual gradient        82 us   86 %
+//             4096 x 16384 bf16 + residual gradient       160 us   50 %
+//             4096 x 16384 fp32 + residual gradient       583 us   28 %
+//            65536 x 256   bf16 + residual gradient        36 us   55 %
+//             9000 x 1001  fp32, odd rows                  41 us   52 %
+// A row of 128 is one load of each of its sixteen threads, which meet before the next
+// row's is asked for.  Registers do not hold the widest rows: the compiler spills 24
+// bytes of the forward at 8 bf16 pieces per thread and a scale per row, 80 to 128 at 8
+// fp32 pieces, 220 to 240 and 1260 to 1860 at 32 and 64 single elements; backward 310 in
+// the ring of 4 bf16 pieces (8200 to 16384 columns), 120 and 260 at 2 pieces from memory
+// (136 to 504 columns, bf16 and fp32), 1410 and 2650 at 8 (wider than the ring), 50 and
+// 1400 to 1700 at 16 and 64 single elements.
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -174,7 +188,7 @@ struct RowReduce {
 
 // Forward on aligned rows.  A row belongs to tpr threads, CH pieces of 8 elements
 // each, and is held as stored from its one read to its output.  CH = 8 where there
-// are rows enough (4: 84 -> 89 us, 2: 93 us at 16384 x 4096; 16 spills).  MODE: kSame for
+// are rows enough (bf16 at 16384 x 4096: 4: 84 -> 89 us, 2: 93 us).  MODE: kSame for
 // the input's type, kRow for codes with one scale per row, else the group's
 // length: its 8-element pieces lie in neighbouring threads.
 constexpr int kSame = -1, kRow = 0;
@@ -428,7 +442,7 @@ cudaError_t launch_fwd_any(const NormParams& p, bool fp8, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_fwd(NormParams p, bool fp8, bool wide, cudaStream_t s) {
-    // As many pieces per thread as registers hold, and fewer where there are too
+    // About as many pieces per thread as registers hold, and fewer where there are too
     // few rows to fill the GPU.
     const int64_t full = (int64_t)sm_count() * 1024;
     if (!wide) {

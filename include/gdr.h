@@ -397,7 +397,12 @@ GDR_API int gdr_linrec_step(const void* x, int64_t x_stride, const void* g, int6
  * D up to GDR_RMSNORM_MAX_D.  Rows need their element's alignment only; rows
  * of 8 aligned elements, with D and the strides multiples of 8, take the fast
  * path.  Sums are fp32: a row whose sum of squares passes fp32's range
- * (elements above about 1e19) gives 0 for its finite elements.
+ * (elements above about 1e19) gives 0 for its finite elements; with eps = 0 one
+ * whose squares fall below it (elements under about 1e-19) loses precision, and
+ * one whose squares vanish gives infinities and NaN.
+ * The codes are for a caller's own products: no entry point of the library reads
+ * them, and the scales are plain fp32 in row order, not a layout of block-scaled
+ * matrix instructions.
  */
 #define GDR_RMSNORM_MAX_D 32768
 GDR_API int gdr_rmsnorm_fwd(const void* x, int64_t x_stride, const void* residual,
