@@ -19,6 +19,12 @@ Entry points (same names as the C ABI, without the ``gdr_`` prefix):
                       e4m3 with scales                    -> y, residual_out, scales
   rmsnorm_bwd         its gradients                       -> dx, dweight
   linrec_workspace_size, rmsnorm_bwd_workspace_size
+  kv_append           new keys and values into a paged cache, rotary positions
+                      applied on the way                  -> q_out, k_out
+  attn_fwd            causal softmax attention over packed prompts -> o
+  attn_step           attention of a few tokens per sequence over the paged cache,
+                      a shared prefix read once for the batch      -> o
+  attn_step_workspace_size
 """
 from __future__ import annotations
 
@@ -34,7 +40,7 @@ LIB_PATH = os.path.join(_PKG, "libgdr.so")
 GDR_BF16, GDR_F32, GDR_E4M3 = 0, 1, 2
 GDR_GATE_SCALAR, GDR_GATE_CHANNEL = 0, 1
 GDR_QK_L2NORM, GDR_NEG_EIGVAL, GDR_COMMIT, GDR_VALIDATE, GDR_CHANNEL_GATE = 0x1, 0x2, 0x4, 0x8, 0x10
-GDR_CHUNK_SCAN = 0x20
+GDR_CHUNK_SCAN, GDR_ROPE_PAIRS = 0x20, 0x40
 CHUNK = 64
 
 STATUS = {0: "GDR_OK", 1: "GDR_ERR_INVALID_ARG", 2: "GDR_ERR_UNSUPPORTED", 3: "GDR_ERR_WORKSPACE",
@@ -45,6 +51,7 @@ EXPORTED = ("gdr_chunk_workspace_size", "gdr_chunk_fwd", "gdr_chunk_fwd_noalloc"
             "gdr_recurrent_fwd_gated", "gdr_recurrent_fwd_norm", "gdr_gating_fwd",
             "gdr_linrec_workspace_size", "gdr_linrec_fwd", "gdr_linrec_bwd", "gdr_linrec_step",
             "gdr_rmsnorm_fwd", "gdr_rmsnorm_bwd_workspace_size", "gdr_rmsnorm_bwd",
+            "gdr_kv_append", "gdr_attn_fwd", "gdr_attn_step_workspace_size", "gdr_attn_step",
             "gdr_last_error", "gdr_get_device_status", "gdr_selftest_bounded_wait", "gdr_selftest_linrec_lost_copy",
             "gdr_selftest_rmsnorm_lost_copy", "gdr_profile_enable", "gdr_profile_read", "gdr_version")
 
@@ -96,6 +103,15 @@ def load(path: str | None = None):
     lib.gdr_rmsnorm_bwd_workspace_size.restype = I
     lib.gdr_rmsnorm_bwd.argtypes = [P, I64, P, I64, P, P, I64, I64, I, F, I, P, I64, P, P, SZ, P]
     lib.gdr_rmsnorm_bwd.restype = I
+    lib.gdr_kv_append.argtypes = [P, I64, P, I64, P, I64, P, I, P, P, I64, I, P, I, I64, I, I, I, I, I, P, I64, P, I64,
+                                  P, P, I, I, P]
+    lib.gdr_kv_append.restype = I
+    lib.gdr_attn_fwd.argtypes = [P, I64, P, I64, P, I64, P, I, I64, I, I, I, F, I, I, P, I64, P]
+    lib.gdr_attn_fwd.restype = I
+    lib.gdr_attn_step_workspace_size.argtypes = [I, I64, I, I, I, I, I, ctypes.POINTER(SZ)]
+    lib.gdr_attn_step_workspace_size.restype = I
+    lib.gdr_attn_step.argtypes = [P, I64, P, P, I, I, P, I64, I, P, P, I, P, I, I64, I, I, I, F, I, I, P, I64, P, SZ, P]
+    lib.gdr_attn_step.restype = I
     lib.gdr_last_error.argtypes = []
     lib.gdr_last_error.restype = ctypes.c_char_p
     lib.gdr_get_device_status.argtypes = [P, ctypes.POINTER(I)]
@@ -621,6 +637,185 @@ def rmsnorm_bwd(dy, s, weight, *, eps: float = 1e-6, d_residual_out=None, dx=Non
     if code:
         _check(code)
     return dx, dweight
+
+
+# ---- softmax attention and its paged cache -----------------------------------
+#
+# Token tensors are [T, heads, D] with dense heads and a token stride of their
+# own (a column block of one projection's output); the rest as above.
+
+
+def _tokens(t, shape, dtype, device, what):
+    """(address, token stride) of a [T, heads, D] tensor with dense heads."""
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _refuse(t, shape, dtype, device, what)
+    token, head, col = t.stride()
+    T, H, D = shape
+    if col != 1 or (head != D and H > 1):
+        raise ValueError(f"{what} must have dense heads")
+    return t.data_ptr(), token if T > 1 else H * D
+
+
+def _attention_elsewhere(t, what, stream):
+    """As _elsewhere, for [T, heads, D] tensors."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{what} must be [T, heads, D]")
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _caches(k_cache, v_cache, block_table, cache_lens, N, Hkv, D, dtype, device):
+    """The paged cache's arguments: addresses and sizes."""
+    if k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("caches must be [pages, Hkv, page_size, D], block_table [N, max_pages]")
+    pages, _, page_size, _ = shape = k_cache.shape
+    if shape != (pages, Hkv, page_size, D):
+        raise ValueError(f"caches must be [pages, {Hkv}, page_size, {D}], not {tuple(shape)}")
+    kp = _dense(k_cache, shape, dtype, device, "k_cache")
+    vp = _dense(v_cache, shape, dtype, device, "v_cache")
+    columns = block_table.shape[1]
+    tp, ts = _rows(block_table, (N, columns), _I32, device, "block_table")
+    return kp, vp, pages, page_size, tp, ts, columns, _dense(cache_lens, (N,), _I32, device, "cache_lens")
+
+
+def kv_append(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens, *, q=None, freqs=None, flags: int = 0,
+              q_out=None, k_out=None, output_k: bool = False, stream=None):
+    """Appends k and v [T, Hkv, D] to the caches [pages, Hkv, page_size, D]:
+    token i of sequence n goes to position cache_lens[n] + i, in the page
+    block_table[n, position // page_size].  freqs [R / 2] fp32 (radians per
+    position; None: no rotation) turns the first R channels of k and of q
+    [T, Hq, D] (GDR_ROPE_PAIRS: neighbouring pairs).  cache_lens[n] < 0: the
+    sequence is skipped.  Returns (q_out or None, k_out or None): q turned, and
+    with output_k or k_out the turned k as dense rows; both may be in place."""
+    if stream is not None or not k.is_cuda or k.get_device() != _current_device() or k.dim() != 3:
+        with _attention_elsewhere(k, "k", stream):
+            return kv_append(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens, q=q, freqs=freqs,
+                             flags=flags, q_out=q_out, k_out=k_out, output_k=output_k)
+    dev, shape, kt = k.device, k.shape, k.dtype
+    T, Hkv, D = shape
+    code = _CODES.get(kt)
+    if code is None:
+        _not_a_code(kt)
+    N = cu_seqlens.numel() - 1
+    kp, ks = _tokens(k, shape, kt, dev, "k")
+    vp, vs = _tokens(v, shape, kt, dev, "v")
+    cp = _dense(cu_seqlens, (N + 1,), _I32, dev, "cu_seqlens")
+    ckp, cvp, pages, page_size, tp, ts, columns, lp = _caches(k_cache, v_cache, block_table, cache_lens, N, Hkv, D, kt,
+                                                              dev)
+    Hq, qp, qs, qop, qos = 0, None, 0, None, 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [T, Hq, D]")
+        Hq = q.shape[1]
+        wide = (T, Hq, D)
+        qp, qs = _tokens(q, wide, kt, dev, "q")
+        if q_out is None:
+            q_out = torch.empty(wide, dtype=kt, device=dev)
+        qop, qos = _tokens(q_out, wide, kt, dev, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    kop, kos = None, 0
+    if k_out is None and output_k:
+        k_out = torch.empty(shape, dtype=kt, device=dev)
+    if k_out is not None:
+        kop, kos = _tokens(k_out, shape, kt, dev, "k_out")
+    R, fp = 0, None
+    if freqs is not None:
+        R = 2 * freqs.numel()
+        fp = _dense(freqs, (R // 2,), _F32, dev, "freqs")
+    rc = (_lib or load()).gdr_kv_append(qp, qs, kp, ks, vp, vs, fp, R, lp, tp, ts, columns, cp, N, T, Hq, Hkv, D, code,
+                                        flags, qop, qos, kop, kos, ckp, cvp, pages, page_size,
+                                        _current_handle(dev.index))
+    if rc:
+        _check(rc)
+    return q_out, k_out
+
+
+def attn_fwd(q, k, v, cu_seqlens, *, scale=None, flags: int = 0, o=None, stream=None):
+    """Causal softmax attention over packed prompts: q [T, Hq, D], k and v
+    [T, Hkv, D] bf16 or fp32, D 64 or 128; query head h reads key head h /
+    (Hq / Hkv); scale defaults to D ** -0.5.  Rows from cu_seqlens[N] on are not
+    written.  Returns o [T, Hq, D]."""
+    if stream is not None or not q.is_cuda or q.get_device() != _current_device() or q.dim() != 3:
+        with _attention_elsewhere(q, "q", stream):
+            return attn_fwd(q, k, v, cu_seqlens, scale=scale, flags=flags, o=o)
+    dev, shape, qt = q.device, q.shape, q.dtype
+    T, Hq, D = shape
+    code = _CODES.get(qt)
+    if code is None:
+        _not_a_code(qt)
+    if k.dim() != 3:
+        raise ValueError("k must be [T, Hkv, D]")
+    Hkv = k.shape[1]
+    N = cu_seqlens.numel() - 1
+    narrow = (T, Hkv, D)
+    qp, qs = _tokens(q, shape, qt, dev, "q")
+    kp, ks = _tokens(k, narrow, qt, dev, "k")
+    vp, vs = _tokens(v, narrow, qt, dev, "v")
+    cp = _dense(cu_seqlens, (N + 1,), _I32, dev, "cu_seqlens")
+    if o is None:
+        o = torch.empty(shape, dtype=qt, device=dev)
+    op, os_ = _tokens(o, shape, qt, dev, "o")
+    rc = (_lib or load()).gdr_attn_fwd(qp, qs, kp, ks, vp, vs, cp, N, T, Hq, Hkv, D,
+                                       D ** -0.5 if scale is None else scale, code, flags, op, os_,
+                                       _current_handle(dev.index))
+    if rc:
+        _check(rc)
+    return o
+
+
+@functools.lru_cache(maxsize=4096)
+def _attn_step_bytes(N, T, Hq, Hkv, D, prefix_len, dtype):
+    out = ctypes.c_size_t(0)
+    _check(load().gdr_attn_step_workspace_size(N, T, Hq, Hkv, D, prefix_len, dtype, ctypes.byref(out)))
+    return out.value
+
+
+def attn_step_workspace_size(N: int, T: int, Hq: int, Hkv: int, D: int, *, prefix_len: int = 0, dtype: int) -> int:
+    return _attn_step_bytes(N, T, Hq, Hkv, D, prefix_len, dtype)
+
+
+def attn_step(q, k_cache, v_cache, block_table, cache_lens, cu_seqlens, *, prefix_pages=None, prefix_len: int = 0,
+              scale=None, flags: int = 0, o=None, workspace=None, stream=None):
+    """Attention of a few tokens per sequence over the paged cache, after
+    kv_append of the same tokens: token i of sequence n sees the keys 0 ..
+    cache_lens[n] + i (cache_lens as kv_append took it; < 0: skipped).  The first
+    prefix_len keys are the same for every sequence, in the pages prefix_pages
+    [ceil(prefix_len / page_size)] int32, and are read once for the batch.
+    Returns o [T, Hq, D]."""
+    if stream is not None or not q.is_cuda or q.get_device() != _current_device() or q.dim() != 3:
+        with _attention_elsewhere(q, "q", stream):
+            return attn_step(q, k_cache, v_cache, block_table, cache_lens, cu_seqlens, prefix_pages=prefix_pages,
+                             prefix_len=prefix_len, scale=scale, flags=flags, o=o, workspace=workspace)
+    dev, shape, qt = q.device, q.shape, q.dtype
+    T, Hq, D = shape
+    code = _CODES.get(qt)
+    if code is None:
+        _not_a_code(qt)
+    N = cu_seqlens.numel() - 1
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages, Hkv, page_size, D]")
+    Hkv = k_cache.shape[1]
+    qp, qs = _tokens(q, shape, qt, dev, "q")
+    cp = _dense(cu_seqlens, (N + 1,), _I32, dev, "cu_seqlens")
+    ckp, cvp, pages, page_size, tp, ts, columns, lp = _caches(k_cache, v_cache, block_table, cache_lens, N, Hkv, D, qt,
+                                                              dev)
+    pp = _dense(prefix_pages, (-(-prefix_len // max(page_size, 1)),), _I32, dev, "prefix_pages")
+    if o is None:
+        o = torch.empty(shape, dtype=qt, device=dev)
+    op, os_ = _tokens(o, shape, qt, dev, "o")
+    ws, wp, wn = _scratch(workspace, _attn_step_bytes(N, T, Hq, Hkv, D, prefix_len, code), dev)
+    rc = (_lib or load()).gdr_attn_step(qp, qs, ckp, cvp, pages, page_size, tp, ts, columns, lp, pp, prefix_len, cp, N,
+                                        T, Hq, Hkv, D, D ** -0.5 if scale is None else scale, code, flags, op, os_, wp,
+                                        wn, _current_handle(dev.index))
+    if rc:
+        _check(rc)
+    return o
 
 
 def device_status(stream=None) -> int:

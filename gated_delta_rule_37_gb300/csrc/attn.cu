@@ -1,0 +1,579 @@
+// Attention in fp32 on the CUDA cores (packed prompts, the step over the paged
+// cache), the merge of the step's partial results, and the layer's entry points
+// (contract in include/gdr.h).
+//
+// One pass over the keys with the running maximum m and sum l of a row's softmax, in
+// log2 units: with s_j = scale log2(e) q . k_j and m' = max(m, max_j s_j),
+//   l <- l 2^(m - m') + sum_j 2^(s_j - m'),   acc <- acc 2^(m - m') + sum_j 2^(s_j - m') v_j,
+// o = acc / l.  Two partial results join by the same rule.
+#include <math.h>
+
+#include "attn.h"
+#include "attn_step.cuh"
+#include "common.cuh"
+#include "gdr.h"
+#include "launch.h"
+
+namespace gdr {
+namespace {
+
+constexpr float kNone = -INFINITY;
+
+// ---- rows by keys on the CUDA cores ------------------------------------------------
+
+// RT rows by 64 keys, 256 threads as TR x TK: thread (tr, tk) has the rows tr + TR i, the
+// keys tk + TK j of the scores and D / TK channels of the sums.  TK threads of one warp
+// share a row, so that its maximum and sum are shuffles.
+template <typename T, int D, int RT> struct Simt {
+    static constexpr int TK = RT == 64 ? 16 : 32, TR = 256 / TK, RR = RT / TR, KK = kKeyTile / TK;
+    static constexpr int CV = D / TK < 4 ? D / TK : 4, CG = D / TK / CV;
+    static constexpr int LDQ = D + 4, LDP = kKeyTile + 4;  // rows of the products on different banks
+    struct Smem {
+        float q[RT][LDQ], k[kKeyTile][LDQ], v[kKeyTile][D], p[RT][LDP];
+        int64_t limit[RT];
+        int there[kKeyTile];
+    };
+
+    float m[RR], l[RR], acc[RR][CG * CV];
+
+    // rows(r): the address of row r's query, nullptr where there is none; limit(r): the
+    // end of the keys that it sees
+    template <typename R, typename L>
+    __device__ void start(Smem& s, R rows, L limit, float scale) {
+        __syncthreads();
+        constexpr int C = D / 4;
+        for (int i = threadIdx.x; i < RT * C; i += 256) {
+            const T* from = rows(i / C);
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
+            if (from) Vec<T, 4>::load(from + i % C * 4, x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s.q[i / C][i % C * 4 + e] = x[e] * scale;
+        }
+        for (int r = threadIdx.x; r < RT; r += 256) s.limit[r] = limit(r);
+#pragma unroll
+        for (int i = 0; i < RR; ++i) {
+            m[i] = kNone;
+            l[i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < CG * CV; ++c) acc[i][c] = 0.f;
+        }
+    }
+
+    // One tile of keys from position j0 on, those below `least` left out.  keys(j, kp, vp)
+    // gives a key's rows, false where there is none.
+    template <typename K>
+    __device__ void tile(Smem& s, int64_t j0, int64_t least, int64_t most, K keys) {
+        const int tk = threadIdx.x % TK, tr = threadIdx.x / TK;
+        __syncthreads();
+        constexpr int C = D / 4;
+        for (int i = threadIdx.x; i < kKeyTile * C; i += 256) {
+            const int64_t j = j0 + i / C;
+            const T *kp, *vp;
+            float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+            const bool there = j >= least && j < most && keys(j, kp, vp);
+            if (there) {
+                Vec<T, 4>::load(kp + i % C * 4, x);
+                Vec<T, 4>::load(vp + i % C * 4, y);
+            }
+            if (i % C == 0) s.there[i / C] = there;
+            Vec<float, 4>::store(&s.k[i / C][i % C * 4], x);
+            Vec<float, 4>::store(&s.v[i / C][i % C * 4], y);
+        }
+        __syncthreads();
+        float sc[RR][KK];
+#pragma unroll
+        for (int i = 0; i < RR; ++i)
+#pragma unroll
+            for (int j = 0; j < KK; ++j) sc[i][j] = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+            float4 qf[RR], kf[KK];
+#pragma unroll
+            for (int i = 0; i < RR; ++i) qf[i] = *reinterpret_cast<const float4*>(&s.q[tr + TR * i][d]);
+#pragma unroll
+            for (int j = 0; j < KK; ++j) kf[j] = *reinterpret_cast<const float4*>(&s.k[tk + TK * j][d]);
+#pragma unroll
+            for (int i = 0; i < RR; ++i)
+#pragma unroll
+                for (int j = 0; j < KK; ++j)
+                    sc[i][j] = fmaf(qf[i].x, kf[j].x, fmaf(qf[i].y, kf[j].y,
+                               fmaf(qf[i].z, kf[j].z, fmaf(qf[i].w, kf[j].w, sc[i][j]))));
+        }
+        bool masked = false;
+#pragma unroll
+        for (int i = 0; i < RR; ++i) {
+            const int64_t end = s.limit[tr + TR * i];
+            float top = m[i];
+#pragma unroll
+            for (int j = 0; j < KK; ++j) {
+                const int k = tk + TK * j;
+                if (!s.there[k] || j0 + k >= end) {
+                    sc[i][j] = kNone;
+                    masked = true;
+                }
+                top = fmaxf(top, sc[i][j]);
+            }
+#pragma unroll
+            for (int off = TK / 2; off; off /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float base = top == kNone ? 0.f : top, back = exp2f(m[i] - base);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < KK; ++j) {
+                const float e = exp2f(sc[i][j] - base);
+                s.p[tr + TR * i][tk + TK * j] = e;
+                sum += e;
+            }
+#pragma unroll
+            for (int off = TK / 2; off; off /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            m[i] = top;
+            l[i] = l[i] * back + sum;
+#pragma unroll
+            for (int c = 0; c < CG * CV; ++c) acc[i][c] *= back;
+        }
+        // a key that a row does not see may be an infinity, which a weight of 0 does not
+        // keep out: where the tile has such pairs each is asked for
+        masked = __syncthreads_or(masked);
+        if (!masked) {
+            product<false>(s, j0, tr, tk);
+        } else {
+            product<true>(s, j0, tr, tk);
+        }
+    }
+
+    template <bool MASKED>
+    __device__ void product(Smem& s, int64_t j0, int tr, int tk) {
+        int64_t end[RR];
+#pragma unroll
+        for (int i = 0; i < RR; ++i) end[i] = MASKED ? s.limit[tr + TR * i] - j0 : 0;
+#pragma unroll 2
+        for (int k = 0; k < kKeyTile; k += 4) {
+            float4 pf[RR];
+#pragma unroll
+            for (int i = 0; i < RR; ++i) pf[i] = *reinterpret_cast<const float4*>(&s.p[tr + TR * i][k]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float v[CG * CV];
+#pragma unroll
+                for (int g = 0; g < CG; ++g) Vec<float, CV>::load(&s.v[k + e][(tk + TK * g) * CV], v + g * CV);
+#pragma unroll
+                for (int i = 0; i < RR; ++i) {
+                    const float p = e == 0 ? pf[i].x : e == 1 ? pf[i].y : e == 2 ? pf[i].z : pf[i].w;
+                    if (MASKED && k + e >= end[i]) continue;
+#pragma unroll
+                    for (int c = 0; c < CG * CV; ++c) acc[i][c] = fmaf(p, v[c], acc[i][c]);
+                }
+            }
+        }
+    }
+
+    // out(r): where row r's result goes, nullptr where it is not wanted; o = acc / l
+    template <typename O>
+    __device__ void finish(O out) {
+        const int tk = threadIdx.x % TK, tr = threadIdx.x / TK;
+#pragma unroll
+        for (int i = 0; i < RR; ++i) {
+            T* to = out(tr + TR * i);
+            if (!to) continue;
+            const float inv = l[i] > 0.f ? 1.f / l[i] : l[i] == 0.f ? 0.f : l[i];  // a NaN stays one
+#pragma unroll
+            for (int c = 0; c < CG * CV; ++c) acc[i][c] *= inv;
+#pragma unroll
+            for (int g = 0; g < CG; ++g) Vec<T, CV>::store(to + (tk + TK * g) * CV, acc[i] + g * CV);
+        }
+    }
+
+    // sum(r) and stat(r): where row r's partial result goes
+    template <typename S, typename P>
+    __device__ void leave(S sum, P stat) {
+        const int tk = threadIdx.x % TK, tr = threadIdx.x / TK;
+#pragma unroll
+        for (int i = 0; i < RR; ++i) {
+            float* to = sum(tr + TR * i);
+            if (!to) continue;
+#pragma unroll
+            for (int g = 0; g < CG; ++g) Vec<float, CV>::store(to + (tk + TK * g) * CV, acc[i] + g * CV);
+            if (tk == 0) *stat(tr + TR * i) = make_float2(m[i], l[i]);
+        }
+    }
+};
+
+// Key j's rows in the caches, of key head h.
+template <typename T, int D>
+__device__ __forceinline__ bool cached(const Paged& c, const int32_t* pages, int Hkv, int h, int64_t j, const T*& kp,
+                                       const T*& vp) {
+    const int page = pages[j >> c.page_bits];
+    if (page < 0 || page >= c.num_pages) return false;
+    const int64_t row = (((int64_t)page * Hkv + h) << c.page_bits) + (j & (c.page_size - 1));
+    kp = static_cast<const T*>(c.k) + row * D;
+    vp = static_cast<const T*>(c.v) + row * D;
+    return true;
+}
+
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(256) prompt_simt_kernel(const AttnArgs a) {
+    extern __shared__ float4 raw[];
+    using E = Simt<T, D, RT>;
+    typename E::Smem& s = *reinterpret_cast<typename E::Smem*>(raw);
+    // blockIdx.x numbers the row tiles of all sequences, the last first: their rows see most keys
+    __shared__ int at_n, at_tile;
+    if (threadIdx.x == 0) at_n = -1;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int64_t left = gridDim.x - 1 - blockIdx.x;
+        for (int base = 0; base < a.N && left >= 0; base += 32) {
+            const int n = base + threadIdx.x;
+            int64_t tiles = 0;
+            if (n < a.N) {
+                const int64_t rows = (min((int64_t)a.cu[n + 1], a.T) - max(a.cu[n], 0)) * a.group;
+                tiles = rows > 0 ? (rows + RT - 1) / RT : 0;
+            }
+            int64_t upto = tiles;
+#pragma unroll
+            for (int off = 1; off < 32; off *= 2) {
+                const int64_t l = __shfl_up_sync(0xffffffffu, upto, off);
+                if ((int)threadIdx.x >= off) upto += l;
+            }
+            if (left < upto && left >= upto - tiles) {
+                at_n = n;
+                at_tile = (int)(left - (upto - tiles));
+            }
+            const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
+            left = left < all ? -1 : left - all;
+        }
+    }
+    __syncthreads();
+    if (at_n < 0) return;
+    const int n = at_n, h = blockIdx.y;
+    const int64_t t0 = max(a.cu[n], 0), L = min((int64_t)a.cu[n + 1], a.T) - t0;
+    const int64_t r0 = (int64_t)at_tile * RT, rows = min((int64_t)RT, L * a.group - r0);
+    auto element = [&](int64_t r, int64_t ld) { return (t0 + r / a.group) * ld + ((int64_t)h * a.group + r % a.group) * D; };
+    E e;
+    e.start(s, [&](int r) { return r < rows ? static_cast<const T*>(a.q) + element(r0 + r, a.ldq) : nullptr; },
+            [&](int r) { return r < rows ? (r0 + r) / a.group + 1 : 0; }, a.scale_log2);
+    const int64_t most = (r0 + rows - 1) / a.group + 1;
+    for (int64_t j = 0; j < most; j += kKeyTile)
+        e.tile(s, j, 0, most, [&](int64_t i, const T*& kp, const T*& vp) {
+            kp = static_cast<const T*>(a.k) + (t0 + i) * a.ldk + (int64_t)h * D;
+            vp = static_cast<const T*>(a.v) + (t0 + i) * a.ldv + (int64_t)h * D;
+            return true;
+        });
+    e.finish([&](int r) { return r < rows ? static_cast<T*>(a.o) + element(r0 + r, a.ldo) : nullptr; });
+}
+
+// The sequences' own keys.
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(256) step_simt_kernel(const AttnArgs a, const StepWork w) {
+    extern __shared__ float4 raw[];
+    using E = Simt<T, D, RT>;
+    typename E::Smem& s = *reinterpret_cast<typename E::Smem*>(raw);
+    const Plan plan = make_plan(a, w, blockIdx.x);
+    walk(a, w, plan, [&](int n, const Span& sp, int h, int row_tile, int from, int to, int slot) {
+        const int64_t t0 = max(a.cu[n], 0), len = a.cache.lens[n];
+        const int r0 = row_tile * RT, rows = min(RT, sp.rows - r0);
+        const int64_t most = min(len + (r0 + rows - 1) / a.group + 1, (int64_t)a.cache.max_pages << a.cache.page_bits);
+        const int32_t* pages = a.cache.table + n * a.cache.table_ld;
+        auto row = [&](int r) { return (t0 + (r0 + r) / a.group) * a.Hq + h * a.group + (r0 + r) % a.group; };
+        auto element = [&](int r, int64_t ld) {
+            return (t0 + (r0 + r) / a.group) * ld + (int64_t)(h * a.group + (r0 + r) % a.group) * D;
+        };
+        E e;
+        e.start(s, [&](int r) { return r < rows ? static_cast<const T*>(a.q) + element(r, a.ldq) : nullptr; },
+                [&](int r) { return r < rows ? len + (r0 + r) / a.group + 1 : 0; }, a.scale_log2);
+        for (int k = from; k < to; ++k)
+            e.tile(s, (int64_t)k * kKeyTile, a.cache.prefix_len, most, [&](int64_t j, const T*& kp, const T*& vp) {
+                return cached<T, D>(a.cache, pages, a.Hkv, h, j, kp, vp);
+            });
+        if (slot >= 0) {
+            const int64_t base = ((int64_t)blockIdx.x * 2 + slot) * w.rows;
+            e.leave([&](int r) { return r < rows ? w.slot_sum + (base + r) * D : nullptr; },
+                    [&](int r) { return w.slot_stat + base + r; });
+        } else if (a.cache.prefix_len > 0) {
+            e.leave([&](int r) { return r < rows ? w.row_sum + row(r) * D : nullptr; },
+                    [&](int r) { return w.row_stat + row(r); });
+        } else {
+            e.finish([&](int r) { return r < rows ? static_cast<T*>(a.o) + element(r, a.ldo) : nullptr; });
+        }
+    });
+}
+
+// The prefix: blockIdx = (row tile of all tokens' rows, key head, split).
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(256) prefix_simt_kernel(const AttnArgs a, const StepWork w) {
+    extern __shared__ float4 raw[];
+    using E = Simt<T, D, RT>;
+    typename E::Smem& s = *reinterpret_cast<typename E::Smem*>(raw);
+    const int h = blockIdx.y, tiles = (a.cache.prefix_len + kKeyTile - 1) / kKeyTile;
+    const int64_t r0 = (int64_t)blockIdx.x * RT, rows = min((int64_t)RT, a.T * a.group - r0);
+    const int from = (int)((int64_t)tiles * blockIdx.z / w.splits), to = (int)((int64_t)tiles * (blockIdx.z + 1) / w.splits);
+    auto row = [&](int r) {
+        return ((int64_t)blockIdx.z * a.T + (r0 + r) / a.group) * a.Hq + h * a.group + (int)((r0 + r) % a.group);
+    };
+    E e;
+    e.start(s, [&](int r) {
+                return r < rows ? static_cast<const T*>(a.q) + (r0 + r) / a.group * a.ldq +
+                                      (h * a.group + (r0 + r) % a.group) * D : nullptr;
+            },
+            [&](int r) -> int64_t {
+                if (r >= rows) return 0;
+                // the last sequence that starts at or before the token
+                const int64_t t = (r0 + r) / a.group;
+                int lo = 0, hi = a.N;
+                while (hi > lo) {
+                    const int mid = (lo + hi + 1) / 2;
+                    if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
+                }
+                if (lo >= a.N || a.cu[lo] > t || t >= a.cu[lo + 1] || a.cache.lens[lo] < 0) return 0;
+                return min((int64_t)a.cache.prefix_len, a.cache.lens[lo] + (t - a.cu[lo]) + 1);
+            }, a.scale_log2);
+    for (int k = from; k < to; ++k)
+        e.tile(s, (int64_t)k * kKeyTile, 0, a.cache.prefix_len, [&](int64_t j, const T*& kp, const T*& vp) {
+            return cached<T, D>(a.cache, a.cache.prefix, a.Hkv, h, j, kp, vp);
+        });
+    e.leave([&](int r) { return r < rows ? w.far_sum + row(r) * D : nullptr; },
+            [&](int r) { return w.far_stat + row(r); });
+}
+
+// ---- the merge ----------------------------------------------------------------------
+
+constexpr int kMergeThreads = 128;
+
+// blockIdx = (sequence, key head, share of its rows); a warp per row.
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeThreads) step_merge_kernel(const AttnArgs a, const StepWork w) {
+    constexpr int C = D / 32;
+    const int n = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31;
+    const Span s = span_of(a, w.rows, n);
+    const int64_t all = w.offsets[a.N], ctas = taking_part(all, w.ctas);
+    const int64_t t0 = max(a.cu[n], 0);
+    for (int r = blockIdx.z * (kMergeThreads / 32) + (threadIdx.x >> 5); r < s.rows; r += gridDim.z * (kMergeThreads / 32)) {
+        const int64_t row = (t0 + r / a.group) * a.Hq + h * a.group + r % a.group;
+        int64_t first = 0;
+        int near = 0;  // partial results of the own keys
+        if (s.key_tiles > 0) {
+            const int64_t u = w.offsets[n] + ((int64_t)h * s.row_tiles + r / w.rows) * s.key_tiles;
+            first = cta_of(u, all, ctas);
+            near = (int)(cta_of(u + s.key_tiles - 1, all, ctas) - first) + 1;
+        }
+        if (near == 1 && w.splits == 0) continue;  // written where it was computed
+        const int count = w.splits + near;
+        auto stat_at = [&](int i) -> const float2* {
+            if (i < w.splits) return w.far_stat + i * a.T * a.Hq + row;
+            if (near == 1) return w.row_stat + row;
+            const int c = i - w.splits;
+            return w.slot_stat + ((first + c) * 2 + (c == 0)) * w.rows + r % w.rows;
+        };
+        auto sum_at = [&](int i) -> const float* {
+            if (i < w.splits) return w.far_sum + (i * a.T * a.Hq + row) * D;
+            if (near == 1) return w.row_sum + row * D;
+            const int c = i - w.splits;
+            return w.slot_sum + (((first + c) * 2 + (c == 0)) * w.rows + r % w.rows) * D;
+        };
+        float top = kNone;
+        for (int i = lane; i < count; i += 32) top = fmaxf(top, stat_at(i)->x);
+#pragma unroll
+        for (int off = 16; off; off /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float base = top == kNone ? 0.f : top;
+        float l = 0.f, acc[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < count; ++i) {
+            const float2 st = *stat_at(i);
+            float x[C];
+            Vec<float, C>::load(sum_at(i) + lane * C, x);
+            if (st.x == kNone && st.y == 0.f) continue;  // saw no key: its sums are 0
+            const float f = exp2f(st.x - base);
+            l = fmaf(st.y, f, l);
+#pragma unroll
+            for (int c = 0; c < C; ++c) acc[c] = fmaf(x[c], f, acc[c]);
+        }
+        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] *= inv;
+        Vec<T, C>::store(static_cast<T*>(a.o) + (t0 + r / a.group) * a.ldo +
+                             (int64_t)(h * a.group + r % a.group) * D + lane * C, acc);
+    }
+}
+
+// ---- launches -----------------------------------------------------------------------
+
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename T, int D>
+cudaError_t launch_prompt_simt(const AttnArgs& a, cudaStream_t s) {
+    constexpr int RT = 64;
+    const size_t bytes = sizeof(typename Simt<T, D, RT>::Smem);
+    const cudaError_t e = allow_smem(prompt_simt_kernel<T, D, RT>, bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (a.T * a.group + RT - 1) / RT + a.N;
+    KernelTimer kt("attn_prompt_simt", s);
+    prompt_simt_kernel<T, D, RT><<<dim3((unsigned)tiles, a.Hkv), 256, bytes, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int D, int RT>
+cudaError_t launch_step_simt(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
+    const size_t bytes = sizeof(typename Simt<T, D, RT>::Smem);
+    cudaError_t e = allow_smem(step_simt_kernel<T, D, RT>, bytes);
+    if (e == cudaSuccess) e = allow_smem(prefix_simt_kernel<T, D, RT>, bytes);
+    if (e != cudaSuccess) return e;
+    if (w.splits > 0) {
+        KernelTimer kt("attn_prefix_simt", s);
+        const int64_t tiles = (a.T * a.group + RT - 1) / RT;
+        prefix_simt_kernel<T, D, RT><<<dim3((unsigned)tiles, a.Hkv, w.splits), 256, bytes, s>>>(a, w);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    KernelTimer kt("attn_step_simt", s);
+    step_simt_kernel<T, D, RT><<<w.ctas, 256, bytes, s>>>(a, w);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_merge(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
+    const int64_t rows = (a.T + a.N - 1) / a.N * a.group;  // of a sequence and key head, on average
+    const int64_t shares = (rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
+    KernelTimer kt("attn_step_merge", s);
+    step_merge_kernel<T, D><<<dim3(a.N, a.Hkv, (unsigned)(shares < 64 ? shares : 64)), kMergeThreads, 0, s>>>(a, w);
+    return cudaGetLastError();
+}
+
+// Rows per tile of the own keys' part: a tile's cost grows with it, and rows beyond the
+// first tile read the keys again.
+int rows_per_tile(int N, int64_t T, int group) { return (T + N - 1) / (N > 0 ? N : 1) * group <= 16 ? 16 : 64; }
+
+int prefix_splits(int64_t T, int Hkv, int group, int rows, int prefix_len) {
+    if (prefix_len == 0) return 0;
+    const int64_t tiles = (prefix_len + kKeyTile - 1) / kKeyTile;
+    const int64_t blocks = (T * group + rows - 1) / rows * Hkv;
+    int64_t splits = (2 * kSms + blocks - 1) / blocks;
+    if (splits > tiles) splits = tiles;
+    return (int)(splits < kMaxSplits ? splits : kMaxSplits);
+}
+
+// The workspace's parts (from `base`; a null one for the size alone).
+size_t step_layout(StepWork* w, char* base, int N, int64_t T, int Hq, int Hkv, int D, int prefix_len) {
+    size_t at = 0;
+    auto part = [&](size_t bytes) {
+        char* p = base + at;
+        at += (bytes + 255) / 256 * 256;
+        return p;
+    };
+    w->ctas = 2 * kSms;
+    w->rows = rows_per_tile(N, T, Hq / Hkv);
+    w->splits = prefix_splits(T, Hkv, Hq / Hkv, w->rows, prefix_len);
+    const size_t slots = (size_t)w->ctas * 2 * w->rows, rows = w->splits ? (size_t)T * Hq : 0;
+    w->offsets = reinterpret_cast<int64_t*>(part(sizeof(int64_t) * ((size_t)N + 1)));
+    w->slot_stat = reinterpret_cast<float2*>(part(sizeof(float2) * slots));
+    w->slot_sum = reinterpret_cast<float*>(part(sizeof(float) * slots * D));
+    w->row_stat = reinterpret_cast<float2*>(part(sizeof(float2) * rows));
+    w->row_sum = reinterpret_cast<float*>(part(sizeof(float) * rows * D));
+    w->far_stat = reinterpret_cast<float2*>(part(sizeof(float2) * rows * w->splits));
+    w->far_sum = reinterpret_cast<float*>(part(sizeof(float) * rows * w->splits * D));
+    return at;
+}
+
+template <typename T, int D>
+cudaError_t launch_step(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
+    const cudaError_t e = w.rows == 16 ? launch_step_simt<T, D, 16>(a, w, s) : launch_step_simt<T, D, 64>(a, w, s);
+    return e == cudaSuccess ? launch_merge<T, D>(a, w, s) : e;
+}
+
+int check_attention(int N, int64_t T, int Hq, int Hkv, int D, int dtype) {
+    if (int rc = check_heads(N, T, Hq, Hkv, D, dtype)) return rc;
+    if (Hq == 0) return set_last_error(GDR_ERR_INVALID_ARG, "Hq must be positive");
+    if (T * (Hq / Hkv) > 0x7fffffffLL - 512)
+        return set_last_error(GDR_ERR_UNSUPPORTED, "T_total (%lld) * Hq / Hkv too large", (long long)T);
+    return GDR_OK;
+}
+
+}  // namespace
+}  // namespace gdr
+
+using namespace gdr;
+
+extern "C" {
+
+int gdr_attn_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                 const int32_t* cu_seqlens, int N, int64_t T_total, int Hq, int Hkv, int D, float scale, int dtype,
+                 int flags, void* o, int64_t o_stride, gdr_stream_t stream) {
+    if (int rc = check_attention(N, T_total, Hq, Hkv, D, dtype)) return rc;
+    if (flags & ~GDR_VALIDATE) return set_last_error(GDR_ERR_INVALID_ARG, "unsupported flags 0x%x for gdr_attn_fwd", flags);
+    if (N == 0 || T_total == 0) return set_ok();
+    if (int rc = check_token_rows("q", q, q_stride, 0, dtype)) return rc;
+    if (int rc = check_token_rows("k", k, k_stride, 0, dtype)) return rc;
+    if (int rc = check_token_rows("v", v, v_stride, 0, dtype)) return rc;
+    if (int rc = check_token_rows("o", o, o_stride, (int64_t)Hq * D, dtype)) return rc;
+    if (int rc = check_int32s("cu_seqlens", cu_seqlens)) return rc;
+    if (o == q || o == k || o == v) return set_last_error(GDR_ERR_INVALID_ARG, "o must not be an input");
+    if (int rc = check_device()) return rc;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (flags & GDR_VALIDATE)
+        if (int rc = validate_attention(cu_seqlens, N, T_total, nullptr, s)) return rc;
+    AttnArgs a{};
+    a.q = q; a.k = k; a.v = v; a.o = o;
+    a.ldq = q_stride; a.ldk = k_stride; a.ldv = v_stride; a.ldo = o_stride;
+    a.cu = cu_seqlens; a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.group = Hq / Hkv; a.T = T_total;
+    a.scale_log2 = scale * 1.44269504088896341f;
+    a.dtype = dtype;
+    const cudaError_t e = dtype == GDR_BF16 ? (D == 128 ? launch_prompt_simt<__nv_bfloat16, 128>(a, s)
+                                                        : launch_prompt_simt<__nv_bfloat16, 64>(a, s))
+                                            : (D == 128 ? launch_prompt_simt<float, 128>(a, s)
+                                                        : launch_prompt_simt<float, 64>(a, s));
+    return launch_result(e, "gdr_attn_fwd launch");
+}
+
+int gdr_attn_step_workspace_size(int N, int64_t T_total, int Hq, int Hkv, int D, int prefix_len, int dtype,
+                                 size_t* bytes) {
+    if (!bytes) return set_last_error(GDR_ERR_INVALID_ARG, "bytes is NULL");
+    if (int rc = check_attention(N, T_total, Hq, Hkv, D, dtype)) return rc;
+    if (prefix_len < 0) return set_last_error(GDR_ERR_INVALID_ARG, "prefix_len (%d) negative", prefix_len);
+    StepWork w{};
+    *bytes = N == 0 || T_total == 0 ? 0 : step_layout(&w, nullptr, N, T_total, Hq, Hkv, D, prefix_len);
+    return set_ok();
+}
+
+int gdr_attn_step(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache, int num_pages,
+                  int page_size, const int32_t* block_table, int64_t table_stride, int max_pages,
+                  const int32_t* cache_lens, const int32_t* prefix_pages, int prefix_len, const int32_t* cu_seqlens,
+                  int N, int64_t T_total, int Hq, int Hkv, int D, float scale, int dtype, int flags, void* o,
+                  int64_t o_stride, void* workspace, size_t ws_bytes, gdr_stream_t stream) {
+    if (int rc = check_attention(N, T_total, Hq, Hkv, D, dtype)) return rc;
+    if (flags & ~GDR_VALIDATE) return set_last_error(GDR_ERR_INVALID_ARG, "unsupported flags 0x%x for gdr_attn_step", flags);
+    if (prefix_len < 0 || (prefix_len > 0) != (prefix_pages != nullptr))
+        return set_last_error(GDR_ERR_INVALID_ARG, "prefix_pages goes with prefix_len (%d) > 0", prefix_len);
+    if (N == 0 || T_total == 0) return set_ok();
+    AttnArgs a{};
+    a.cache = Paged{const_cast<void*>(k_cache), const_cast<void*>(v_cache), block_table, table_stride, cache_lens,
+                    prefix_pages, prefix_len, max_pages, num_pages, page_size, 0};
+    if (int rc = check_paged(a.cache, N, Hkv, D, dtype)) return rc;
+    while ((1 << a.cache.page_bits) < page_size) ++a.cache.page_bits;
+    if (prefix_pages)
+        if (int rc = check_int32s("prefix_pages", prefix_pages)) return rc;
+    if (int rc = check_token_rows("q", q, q_stride, 0, dtype)) return rc;
+    if (int rc = check_token_rows("o", o, o_stride, (int64_t)Hq * D, dtype)) return rc;
+    if (int rc = check_int32s("cu_seqlens", cu_seqlens)) return rc;
+    if (o == q || o == k_cache || o == v_cache) return set_last_error(GDR_ERR_INVALID_ARG, "o must not be an input");
+    StepWork w{};
+    const size_t need = step_layout(&w, static_cast<char*>(workspace), N, T_total, Hq, Hkv, D, prefix_len);
+    if (!workspace || ws_bytes < need)
+        return set_last_error(GDR_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace ? ws_bytes : (size_t)0, need);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return set_last_error(GDR_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+    if (int rc = check_device()) return rc;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (flags & GDR_VALIDATE)
+        if (int rc = validate_attention(cu_seqlens, N, T_total, &a.cache, s)) return rc;
+    a.q = q; a.o = o; a.ldq = q_stride; a.ldo = o_stride;
+    a.cu = cu_seqlens; a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.group = Hq / Hkv; a.T = T_total;
+    a.scale_log2 = scale * 1.44269504088896341f;
+    a.dtype = dtype;
+    const cudaError_t e = dtype == GDR_BF16 ? (D == 128 ? launch_step<__nv_bfloat16, 128>(a, w, s)
+                                                        : launch_step<__nv_bfloat16, 64>(a, w, s))
+                                            : (D == 128 ? launch_step<float, 128>(a, w, s) : launch_step<float, 64>(a, w, s));
+    return launch_result(e, "gdr_attn_step launch");
+}
+
+}  // extern "C"

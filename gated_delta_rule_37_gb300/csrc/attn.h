@@ -1,0 +1,46 @@
+// Internal interface of the attention layer's translation units: the paged
+// cache (kv.cu), the argument checks and entry points (attn.cu), the kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gdr {
+
+// A pair of paged caches and the sequences' pages.
+struct Paged {
+    void* k;  // [num_pages, Hkv, page_size, D]
+    void* v;
+    const int32_t* table;  // [N, max_pages], row stride table_ld
+    int64_t table_ld;
+    const int32_t* lens;    // [N] tokens in the cache before the call's; < 0: padding
+    const int32_t* prefix;  // pages of the first prefix_len keys (nullptr: none)
+    int prefix_len;
+    int max_pages, num_pages, page_size, page_bits;  // page_size = 1 << page_bits
+};
+
+struct AttnArgs {
+    const void* q;
+    const void* k;  // packed keys and values (gdr_attn_fwd)
+    const void* v;
+    void* o;
+    int64_t ldq, ldk, ldv, ldo;  // elements from one token to the next
+    const int32_t* cu;
+    int N, Hq, Hkv, D, group;  // group = Hq / Hkv
+    int64_t T;
+    float scale_log2;  // scale * log2(e): scores are kept in log2 units
+    int dtype;
+    Paged cache;  // gdr_attn_step
+};
+
+// The checks that every call of the layer makes; GDR_OK or a status with its message set.
+int check_heads(int N, int64_t T, int Hq, int Hkv, int D, int dtype);
+int check_token_rows(const char* name, const void* p, int64_t stride, int64_t least, int dtype);
+int check_int32s(const char* name, const void* p);
+int check_paged(const Paged& c, int N, int Hkv, int D, int dtype);
+
+// GDR_VALIDATE of the layer: cu_seqlens, and where `c` is given that every page
+// that the call reaches is there.  Synchronises the stream.
+int validate_attention(const int32_t* cu, int N, int64_t T, const Paged* c, cudaStream_t s);
+
+}  // namespace gdr

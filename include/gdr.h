@@ -87,6 +87,7 @@ typedef enum gdr_gate_kind {
                               * calls have a word of their own and take turns.)      */
 #define GDR_CHANNEL_GATE 0x10 /* gdr_recurrent_fwd: g is per key channel, [T_total, Hv, K]  */
 #define GDR_CHUNK_SCAN 0x20   /* gdr_chunk_fwd: chunk-parallel state scan (long sequences)     */
+#define GDR_ROPE_PAIRS 0x40   /* gdr_kv_append: channels 2j and 2j + 1 turn together           */
 
 /* Chunk length of the chunked prefill (tokens).  The pages' kernels use 64. */
 #define GDR_CHUNK 64
@@ -443,6 +444,112 @@ GDR_API int gdr_rmsnorm_bwd(const void* dy, int64_t dy_stride, const void* s, in
                             int64_t d_residual_out_stride, int64_t M, int D, float eps, int dtype,
                             void* dx, int64_t dx_stride, float* dweight, void* workspace,
                             size_t ws_bytes, gdr_stream_t stream);
+
+/*
+ * The softmax-attention layer that stands between delta-rule layers: a paged
+ * cache of keys and values, the prompt's attention (beside gdr_chunk_fwd) and
+ * the step over the cache (beside gdr_recurrent_fwd).  Query head h reads
+ * key / value head h / (Hq / Hkv), as value heads read key heads above.
+ *
+ * Conventions of gdr_kv_append, gdr_attn_fwd and gdr_attn_step, where they go
+ * beyond the library's:
+ *   - Token tensors are [T_total, heads, D] with dense heads and a token stride
+ *     in elements of their own (so they can be column blocks of one projection's
+ *     output): 16-byte aligned, the stride a multiple of 16 bytes, at least
+ *     heads * D for tensors that are written, any such stride >= 0 for the others.
+ *   - dtype (GDR_BF16 or GDR_F32) is that of every tensor and of the caches.
+ *     Scores, softmax statistics and sums are fp32; with GDR_BF16 the weights
+ *     exp(score - maximum) enter the product with v as bf16 numbers (and their
+ *     sum as they are).
+ *   - D 64 or 128; Hq a multiple of Hkv, up to GDR_ATTN_MAX_GROUP times it;
+ *     N up to 65535.
+ *   - cu_seqlens [N+1] int32 device, cu[0] = 0, non-decreasing; sequences may be
+ *     empty.  cu[N] may be less than T_total (a padded batch): rows from cu[N]
+ *     on are neither read as queries nor written.  A cu_seqlens that breaks
+ *     these rules never causes an access outside the tensors, but what is
+ *     written is then unspecified; GDR_VALIDATE turns it, and pages that are
+ *     missing, into GDR_ERR_VALIDATION.
+ *   - The caches are [num_pages, Hkv, page_size, D], dense, page_size 16, 32,
+ *     64, 128 or 256.  Position p of sequence n is row p % page_size of page
+ *     block_table[n][p / page_size]; block_table [N, max_pages] int32 device, row
+ *     stride table_stride.  A position beyond the table, or whose page number is
+ *     not in [0, num_pages), has no row: its key is not written, and not seen.
+ *   - cache_lens [N] int32 device: the tokens that sequence n had in the cache
+ *     before this call's; both calls of a step take the same numbers.  A value
+ *     < 0 is padding: nothing of that sequence is read or written.
+ *   - A NaN or infinity reaches only the rows that see its token; where rows of
+ *     the same tile do not, they are computed once more (slowly) without it.
+ *   - Results do not depend on scheduling: equal inputs give equal bits.
+ *
+ * gdr_kv_append -- appends keys and values to the caches, rotary positions
+ * applied on the way.  Token i of sequence n has position p = cache_lens[n] + i;
+ * channels j and j + rotary_dim / 2 of a head of q and k (with GDR_ROPE_PAIRS 2j
+ * and 2j + 1), j < rotary_dim / 2, become
+ *
+ *   a cos(p freqs[j]) - b sin(p freqs[j]),   b cos(p freqs[j]) + a sin(p freqs[j])
+ *
+ * and the others stay.  The angle is reduced exactly: far positions lose nothing.
+ *   q, k, v        [T_total, Hq | Hkv | Hkv, D] dtype; q NULL with Hq = 0
+ *   freqs          [rotary_dim / 2] fp32, finite, radians per position; NULL with
+ *                  rotary_dim 0
+ *   rotary_dim     0 .. D, a multiple of 16 (of 2 with GDR_ROPE_PAIRS)
+ *   q_out          [T_total, Hq, D] dtype: q, turned (written); may be q itself
+ *   k_out          [T_total, Hkv, D] dtype: k, turned, dense rows for
+ *                  gdr_attn_fwd (written), or NULL; may be k itself
+ *   k_cache, v_cache  the tokens' rows are written, nothing else.  Two tokens of
+ *                  one call must not share a row.
+ * Flags: GDR_ROPE_PAIRS, GDR_VALIDATE (the new tokens' pages only).
+ */
+#define GDR_ATTN_MAX_GROUP 128
+GDR_API int gdr_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, const float* freqs, int rotary_dim, const int32_t* cache_lens,
+                          const int32_t* block_table, int64_t table_stride, int max_pages,
+                          const int32_t* cu_seqlens, int N, int64_t T_total, int Hq, int Hkv, int D, int dtype,
+                          int flags, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                          void* k_cache, void* v_cache, int num_pages, int page_size, gdr_stream_t stream);
+
+/*
+ * gdr_attn_fwd -- causal attention over whole prompts, packed:
+ *
+ *   o_t = sum_j softmax_j(scale q_t . k_j) v_j,   j the tokens up to t of t's sequence
+ *
+ *   q, o  [T_total, Hq, D] dtype;  k, v  [T_total, Hkv, D] dtype
+ *   o     (written) must not overlap an input
+ * Flags: GDR_VALIDATE.
+ */
+GDR_API int gdr_attn_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                         int64_t v_stride, const int32_t* cu_seqlens, int N, int64_t T_total, int Hq, int Hkv,
+                         int D, float scale, int dtype, int flags, void* o, int64_t o_stride,
+                         gdr_stream_t stream);
+
+/* gdr_attn_step_workspace_size -- bytes of device workspace gdr_attn_step needs.
+ * Host only; depends on sizes alone. */
+GDR_API int gdr_attn_step_workspace_size(int N, int64_t T_total, int Hq, int Hkv, int D, int prefix_len, int dtype,
+                                         size_t* bytes);
+
+/*
+ * gdr_attn_step -- attention of a few new tokens of each sequence over the
+ * caches (decode, multi-step verify, the next piece of a prompt), after
+ * gdr_kv_append has put their keys there: token i of sequence n sees the keys
+ * 0 .. cache_lens[n] + i.
+ *   prefix_len     keys 0 .. prefix_len - 1 are the same rows for all sequences
+ *                  (0: none): row p % page_size of page prefix_pages[p /
+ *                  page_size], [ceil(prefix_len / page_size)] int32 device.  They
+ *                  are read once for the batch.  cache_lens counts them; block_table
+ *                  entries of pages that end within the prefix are not read.
+ *   q, o           [T_total, Hq, D] dtype; o (written) must not overlap an input.
+ *                  A row that sees no key is 0.
+ *   workspace      device scratch of gdr_attn_step_workspace_size bytes, 256-byte
+ *                  aligned; needs no initialisation.  Calls whose work may overlap
+ *                  on the GPU need one each.
+ * Flags: GDR_VALIDATE.
+ */
+GDR_API int gdr_attn_step(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache, int num_pages,
+                          int page_size, const int32_t* block_table, int64_t table_stride, int max_pages,
+                          const int32_t* cache_lens, const int32_t* prefix_pages, int prefix_len,
+                          const int32_t* cu_seqlens, int N, int64_t T_total, int Hq, int Hkv, int D, float scale,
+                          int dtype, int flags, void* o, int64_t o_stride, void* workspace, size_t ws_bytes,
+                          gdr_stream_t stream);
 
 /* Description of the last error on the calling thread ("" if none). */
 GDR_API const char* gdr_last_error(void);

@@ -18,6 +18,9 @@ Contents
   * ``linrec``, ``linrec_bwd`` -- the gated linear recurrence of packed
                        sequences and its gradients (numpy, fp64).
   * ``rmsnorm``, ``rmsnorm_bwd`` -- the row norm and its gradients (numpy, fp64).
+  * ``kv_append``, ``attn_fwd``, ``attn_step`` -- the paged cache with rotary
+                       positions, causal attention over packed prompts and over
+                       the cache (numpy, fp64).
 
 Recurrence per value-head (state S in R^{V x K}, V-major):
   S~ = exp(g_t) S_{t-1};  n_t = beta_t (v_t - S~ k_t);  S_t = S~ + n_t k_t^T;
@@ -286,3 +289,96 @@ def rmsnorm_bwd(dy, s, weight, eps: float):
     r = 1 / np.sqrt((s * s).mean(-1, keepdims=True) + eps)
     z = w * dy
     return r * z - r ** 3 * s * (s * z).mean(-1, keepdims=True), (r * dy * s).sum(0)
+
+
+def rotate(x, position, freqs, pairs: bool = False):
+    """Rotary positions: x [T, H, D] at position [T], freqs [R / 2] of the first R channels."""
+    x, freqs = _f64(x).copy(), _f64(freqs)
+    half = len(freqs)
+    # the product of a 31-bit and a 24-bit number: off by less than 2^-53 of itself
+    angle = np.outer(np.asarray(position, dtype=np.float64), freqs)
+    c, s = np.cos(angle)[:, None], np.sin(angle)[:, None]
+    a, b = (slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if pairs else (slice(0, half), slice(half, 2 * half))
+    xa, xb = x[..., a].copy(), x[..., b].copy()
+    x[..., a] = xa * c - xb * s
+    x[..., b] = xb * c + xa * s
+    return x
+
+
+def cache_row(page_size: int, pages, position: int, num_pages: int):
+    """(page, row) of a position, None where there is none."""
+    slot = position // page_size
+    if slot >= len(pages) or not 0 <= pages[slot] < num_pages:
+        return None
+    return int(pages[slot]), position % page_size
+
+
+def kv_append(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens, *, q=None, freqs=(), pairs: bool = False):
+    """Returns (q, k, k_cache, v_cache) after the append; rows of padding and outside every sequence are NaN
+    in q and k."""
+    k, v, kc, vc, cu = _f64(k), _f64(v), _f64(k_cache).copy(), _f64(v_cache).copy(), _cu64(cu_seqlens)
+    table, lens = np.asarray(block_table), np.asarray(cache_lens)
+    qo = None if q is None else np.full(q.shape, np.nan)
+    ko = np.full(k.shape, np.nan)
+    for n in range(len(cu) - 1):
+        if lens[n] < 0 or cu[n] == cu[n + 1]:
+            continue
+        part = slice(cu[n], cu[n + 1])
+        at = int(lens[n]) + np.arange(cu[n + 1] - cu[n])
+        ko[part] = rotate(k[part], at, freqs, pairs)
+        if q is not None:
+            qo[part] = rotate(_f64(q)[part], at, freqs, pairs)
+        for t, p in zip(range(cu[n], cu[n + 1]), at):
+            row = cache_row(kc.shape[2], table[n], int(p), kc.shape[0])
+            if row:
+                kc[row[0], :, row[1]] = ko[t]
+                vc[row[0], :, row[1]] = v[t]
+    return qo, ko, kc, vc
+
+
+def attend(q, k, v, scale: float):
+    """One row over the keys that it sees: q [D], k, v [n, D].  Returns (o, sum_j p_j |v_j|, max_j scale sum_d
+    |q_d k_jd|): the last two are what rounding errors of weights and of scores are in proportion to."""
+    if len(k) == 0:
+        return np.zeros(v.shape[1]), np.zeros(v.shape[1]), 0.0
+    s = scale * (k @ q)
+    p = np.exp(s - s.max())
+    p /= p.sum()
+    return p @ v, p @ np.abs(v), scale * (np.abs(k) @ np.abs(q)).max()
+
+
+def attn_fwd(q, k, v, cu_seqlens, scale: float):
+    """Causal attention over packed sequences.  Returns (o, weight, score) [T, Hq, D], [T, Hq, D], [T, Hq], NaN
+    outside every sequence."""
+    q, k, v, cu = _f64(q), _f64(k), _f64(v), _cu64(cu_seqlens)
+    group = q.shape[1] // k.shape[1]
+    o, w, b = np.full(q.shape, np.nan), np.full(q.shape, np.nan), np.full(q.shape[:2], np.nan)
+    for n in range(len(cu) - 1):
+        for t in range(cu[n], cu[n + 1]):
+            for h in range(q.shape[1]):
+                seen = slice(cu[n], t + 1), h // group
+                o[t, h], w[t, h], b[t, h] = attend(q[t, h], k[seen], v[seen], scale)
+    return o, w, b
+
+
+def attn_step(q, k_cache, v_cache, block_table, cache_lens, cu_seqlens, scale: float, prefix_pages=(),
+              prefix_len: int = 0):
+    """Attention over the paged cache; the same three results, NaN for padding and outside every sequence."""
+    q, kc, vc, cu = _f64(q), _f64(k_cache), _f64(v_cache), _cu64(cu_seqlens)
+    table, lens, prefix = np.asarray(block_table), np.asarray(cache_lens), np.asarray(prefix_pages)
+    group, page = q.shape[1] // kc.shape[1], kc.shape[2]
+    o, w, b = np.full(q.shape, np.nan), np.full(q.shape, np.nan), np.full(q.shape[:2], np.nan)
+    for n in range(len(cu) - 1):
+        if lens[n] < 0:
+            continue
+        for t in range(cu[n], cu[n + 1]):
+            rows = []
+            for p in range(int(lens[n]) + t - cu[n] + 1):
+                row = cache_row(page, prefix if p < prefix_len else table[n], p, kc.shape[0])
+                if row:
+                    rows.append(row)
+            at = tuple(np.array(rows, dtype=np.int64).reshape(-1, 2).T)
+            for h in range(q.shape[1]):
+                o[t, h], w[t, h], b[t, h] = attend(q[t, h], kc[at[0], h // group, at[1]], vc[at[0], h // group, at[1]],
+                                                   scale)
+    return o, w, b
