@@ -397,6 +397,9 @@ __global__ void __launch_bounds__(kMergeThreads) step_merge_kernel(const AttnArg
 
 // ---- launches -----------------------------------------------------------------------
 
+// Tokens that a tensor map takes: none overlaps its neighbour.
+bool tiled(int64_t ld, int heads, int D) { return ld >= (int64_t)heads * D; }
+
 template <typename K>
 cudaError_t allow_smem(K kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
@@ -420,7 +423,9 @@ cudaError_t launch_step_simt(const AttnArgs& a, const StepWork& w, cudaStream_t 
     cudaError_t e = allow_smem(step_simt_kernel<T, D, RT>, bytes);
     if (e == cudaSuccess) e = allow_smem(prefix_simt_kernel<T, D, RT>, bytes);
     if (e != cudaSuccess) return e;
-    if (w.splits > 0) {
+    if (w.splits > 0 && a.dtype == GDR_BF16 && tiled(a.ldq, a.Hq, D)) {
+        if ((e = launch_prefix_tc(a, w, s)) != cudaSuccess) return e;
+    } else if (w.splits > 0) {
         KernelTimer kt("attn_prefix_simt", s);
         const int64_t tiles = (a.T * a.group + RT - 1) / RT;
         prefix_simt_kernel<T, D, RT><<<dim3((unsigned)tiles, a.Hkv, w.splits), 256, bytes, s>>>(a, w);
@@ -444,17 +449,22 @@ cudaError_t launch_merge(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
 // first tile read the keys again.
 int rows_per_tile(int N, int64_t T, int group) { return (T + N - 1) / (N > 0 ? N : 1) * group <= 16 ? 16 : 64; }
 
-int prefix_splits(int64_t T, int Hkv, int group, int rows, int prefix_len) {
+// Cuts of the prefix along its keys: about as many CTAs as the GPU holds at once.
+int prefix_splits(int64_t T, int Hkv, int group, int rows, int prefix_len, int dtype) {
     if (prefix_len == 0) return 0;
-    const int64_t tiles = (prefix_len + kKeyTile - 1) / kKeyTile;
-    const int64_t blocks = (T * group + rows - 1) / rows * Hkv;
-    int64_t splits = (2 * kSms + blocks - 1) / blocks;
+    const bool tc = dtype == GDR_BF16;
+    const int64_t tokens = tc ? 2 * (128 / group) : 0;  // of a CTA
+    const int64_t tiles = (prefix_len + 127) / 128;
+    const int64_t blocks = (tc ? (T + tokens - 1) / tokens : (T * group + rows - 1) / rows) * Hkv;
+    int64_t splits = (tc ? kSms : 2 * kSms) / blocks;
     if (splits > tiles) splits = tiles;
+    if (splits < 1) splits = 1;
     return (int)(splits < kMaxSplits ? splits : kMaxSplits);
 }
 
 // The workspace's parts (from `base`; a null one for the size alone).
-size_t step_layout(StepWork* w, char* base, int N, int64_t T, int Hq, int Hkv, int D, int prefix_len) {
+size_t step_layout(StepWork* w, char* base, int N, int64_t T, int Hq, int Hkv, int D, int prefix_len,
+                   int dtype) {
     size_t at = 0;
     auto part = [&](size_t bytes) {
         char* p = base + at;
@@ -463,7 +473,7 @@ size_t step_layout(StepWork* w, char* base, int N, int64_t T, int Hq, int Hkv, i
     };
     w->ctas = 2 * kSms;
     w->rows = rows_per_tile(N, T, Hq / Hkv);
-    w->splits = prefix_splits(T, Hkv, Hq / Hkv, w->rows, prefix_len);
+    w->splits = prefix_splits(T, Hkv, Hq / Hkv, w->rows, prefix_len, dtype);
     const size_t slots = (size_t)w->ctas * 2 * w->rows, rows = w->splits ? (size_t)T * Hq : 0;
     w->offsets = reinterpret_cast<int64_t*>(part(sizeof(int64_t) * ((size_t)N + 1)));
     w->slot_stat = reinterpret_cast<float2*>(part(sizeof(float2) * slots));
@@ -481,11 +491,18 @@ cudaError_t launch_step(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
     return e == cudaSuccess ? launch_merge<T, D>(a, w, s) : e;
 }
 
+// scale: the maximum of the scores is that of the products only for one above 0
+int check_scale(float scale) {
+    if (!(scale > 0.f) || scale > 1e30f)
+        return set_last_error(GDR_ERR_INVALID_ARG, "scale must be positive and finite");
+    return GDR_OK;
+}
+
 int check_attention(int N, int64_t T, int Hq, int Hkv, int D, int dtype) {
     if (int rc = check_heads(N, T, Hq, Hkv, D, dtype)) return rc;
     if (Hq == 0) return set_last_error(GDR_ERR_INVALID_ARG, "Hq must be positive");
-    if (T * (Hq / Hkv) > 0x7fffffffLL - 512)
-        return set_last_error(GDR_ERR_UNSUPPORTED, "T_total (%lld) * Hq / Hkv too large", (long long)T);
+    if (T * Hq > 0x7fffffffLL - 512)
+        return set_last_error(GDR_ERR_UNSUPPORTED, "T_total (%lld) * Hq too large", (long long)T);
     return GDR_OK;
 }
 
@@ -501,6 +518,7 @@ int gdr_attn_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_strid
                  int flags, void* o, int64_t o_stride, gdr_stream_t stream) {
     if (int rc = check_attention(N, T_total, Hq, Hkv, D, dtype)) return rc;
     if (flags & ~GDR_VALIDATE) return set_last_error(GDR_ERR_INVALID_ARG, "unsupported flags 0x%x for gdr_attn_fwd", flags);
+    if (int rc = check_scale(scale)) return rc;
     if (N == 0 || T_total == 0) return set_ok();
     if (int rc = check_token_rows("q", q, q_stride, 0, dtype)) return rc;
     if (int rc = check_token_rows("k", k, k_stride, 0, dtype)) return rc;
@@ -518,8 +536,10 @@ int gdr_attn_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_strid
     a.cu = cu_seqlens; a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.group = Hq / Hkv; a.T = T_total;
     a.scale_log2 = scale * 1.44269504088896341f;
     a.dtype = dtype;
-    const cudaError_t e = dtype == GDR_BF16 ? (D == 128 ? launch_prompt_simt<__nv_bfloat16, 128>(a, s)
-                                                        : launch_prompt_simt<__nv_bfloat16, 64>(a, s))
+    const cudaError_t e = dtype == GDR_BF16 && tiled(q_stride, Hq, D) && tiled(k_stride, Hkv, D) && tiled(v_stride, Hkv, D)
+                              ? launch_prompt_tc(a, s)
+                          : dtype == GDR_BF16 ? (D == 128 ? launch_prompt_simt<__nv_bfloat16, 128>(a, s)
+                                                          : launch_prompt_simt<__nv_bfloat16, 64>(a, s))
                                             : (D == 128 ? launch_prompt_simt<float, 128>(a, s)
                                                         : launch_prompt_simt<float, 64>(a, s));
     return launch_result(e, "gdr_attn_fwd launch");
@@ -531,7 +551,7 @@ int gdr_attn_step_workspace_size(int N, int64_t T_total, int Hq, int Hkv, int D,
     if (int rc = check_attention(N, T_total, Hq, Hkv, D, dtype)) return rc;
     if (prefix_len < 0) return set_last_error(GDR_ERR_INVALID_ARG, "prefix_len (%d) negative", prefix_len);
     StepWork w{};
-    *bytes = N == 0 || T_total == 0 ? 0 : step_layout(&w, nullptr, N, T_total, Hq, Hkv, D, prefix_len);
+    *bytes = N == 0 || T_total == 0 ? 0 : step_layout(&w, nullptr, N, T_total, Hq, Hkv, D, prefix_len, dtype);
     return set_ok();
 }
 
@@ -544,6 +564,7 @@ int gdr_attn_step(const void* q, int64_t q_stride, const void* k_cache, const vo
     if (flags & ~GDR_VALIDATE) return set_last_error(GDR_ERR_INVALID_ARG, "unsupported flags 0x%x for gdr_attn_step", flags);
     if (prefix_len < 0 || (prefix_len > 0) != (prefix_pages != nullptr))
         return set_last_error(GDR_ERR_INVALID_ARG, "prefix_pages goes with prefix_len (%d) > 0", prefix_len);
+    if (int rc = check_scale(scale)) return rc;
     if (N == 0 || T_total == 0) return set_ok();
     AttnArgs a{};
     a.cache = Paged{const_cast<void*>(k_cache), const_cast<void*>(v_cache), block_table, table_stride, cache_lens,
@@ -557,7 +578,8 @@ int gdr_attn_step(const void* q, int64_t q_stride, const void* k_cache, const vo
     if (int rc = check_int32s("cu_seqlens", cu_seqlens)) return rc;
     if (o == q || o == k_cache || o == v_cache) return set_last_error(GDR_ERR_INVALID_ARG, "o must not be an input");
     StepWork w{};
-    const size_t need = step_layout(&w, static_cast<char*>(workspace), N, T_total, Hq, Hkv, D, prefix_len);
+    const size_t need = step_layout(&w, static_cast<char*>(workspace), N, T_total, Hq, Hkv, D, prefix_len,
+                                    dtype);
     if (!workspace || ws_bytes < need)
         return set_last_error(GDR_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace ? ws_bytes : (size_t)0, need);
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)

@@ -43,4 +43,10 @@ int check_paged(const Paged& c, int N, int Hkv, int D, int dtype);
 // that the call reaches is there.  Synchronises the stream.
 int validate_attention(const int32_t* cu, int N, int64_t T, const Paged* c, cudaStream_t s);
 
+struct StepWork;
+
+// Tensor-core paths (bf16).
+cudaError_t launch_prompt_tc(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_prefix_tc(const AttnArgs& a, const StepWork& w, cudaStream_t s);
+
 }  // namespace gdr

@@ -252,7 +252,7 @@ int check_heads(int N, int64_t T, int Hq, int Hkv, int D, int dtype) {
     if (N < 0 || T < 0) return set_last_error(GDR_ERR_INVALID_ARG, "negative N (%d) or T_total (%lld)", N, (long long)T);
     if (Hkv <= 0 || Hq < 0 || Hq % Hkv != 0)
         return set_last_error(GDR_ERR_INVALID_ARG, "Hq (%d) must be a multiple of Hkv (%d > 0)", Hq, Hkv);
-    if (Hq > 65535 || Hkv > 65535) return set_last_error(GDR_ERR_UNSUPPORTED, "more than 65535 heads");
+    if (Hq > 4096 || Hkv > 4096) return set_last_error(GDR_ERR_UNSUPPORTED, "more than 4096 heads");
     if (Hq / Hkv > GDR_ATTN_MAX_GROUP)
         return set_last_error(GDR_ERR_UNSUPPORTED, "Hq / Hkv (%d) above %d", Hq / Hkv, GDR_ATTN_MAX_GROUP);
     if (dtype != GDR_BF16 && dtype != GDR_F32) return set_last_error(GDR_ERR_UNSUPPORTED, "dtype %d", dtype);

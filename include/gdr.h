@@ -461,8 +461,8 @@ GDR_API int gdr_rmsnorm_bwd(const void* dy, int64_t dy_stride, const void* s, in
  *     Scores, softmax statistics and sums are fp32; with GDR_BF16 the weights
  *     exp(score - maximum) enter the product with v as bf16 numbers (and their
  *     sum as they are).
- *   - D 64 or 128; Hq a multiple of Hkv, up to GDR_ATTN_MAX_GROUP times it;
- *     N up to 65535.
+ *   - D 64 or 128; Hq a multiple of Hkv, up to GDR_ATTN_MAX_GROUP times it and
+ *     up to 4096; N up to 65535; T_total * Hq below 2^31 - 512; scale > 0.
  *   - cu_seqlens [N+1] int32 device, cu[0] = 0, non-decreasing; sequences may be
  *     empty.  cu[N] may be less than T_total (a padded batch): rows from cu[N]
  *     on are neither read as queries nor written.  A cu_seqlens that breaks

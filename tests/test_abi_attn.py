@@ -70,7 +70,8 @@ def _fwd(lib, **kw):
     (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(o=None), INVALID), (dict(o=P(130)), INVALID),
     (dict(ldo=504), INVALID), (dict(ldo=516), INVALID), (dict(o=P(16)), INVALID), (dict(o=P(48)), INVALID),
     (dict(Hq=0), INVALID), (dict(flags=gdr.GDR_ROPE_PAIRS), INVALID), (dict(ldk=1 << 32), INVALID),
-    (dict(T=(1 << 31) - 512, Hq=8), UNSUPPORTED),
+    (dict(T=(1 << 28), Hq=8), UNSUPPORTED), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(scale=float("inf")), INVALID), (dict(scale=float("nan")), INVALID),
 ])
 def test_fwd_rejects_before_launch(lib, kw, code):
     assert _fwd(lib, **kw) == code
@@ -91,6 +92,7 @@ def _step(lib, **kw):
     (dict(o=None), INVALID), (dict(o=P(16)), INVALID), (dict(ldo=504), INVALID), (dict(pl=-1), INVALID),
     (dict(pl=0), INVALID), (dict(pp=None), INVALID), (dict(pp=P(193)), INVALID), (dict(ws=None), WORKSPACE),
     (dict(wn=16), WORKSPACE), (dict(ws=P(128)), INVALID), (dict(Hq=0), INVALID), (dict(flags=gdr.GDR_COMMIT), INVALID),
+    (dict(scale=0.0), INVALID),
 ])
 def test_step_rejects_before_launch(lib, kw, code):
     assert _step(lib, **kw) == code
