@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(256) step_simt_kernel(const AttnArgs a, const 
         } else {
             e.finish([&](int r) { return r < rows ? static_cast<T*>(a.o) + element(r, a.ldo) : nullptr; });
         }
+        return true;
     });
 }
 
@@ -418,21 +419,23 @@ cudaError_t launch_prompt_simt(const AttnArgs& a, cudaStream_t s) {
 }
 
 template <typename T, int D, int RT>
-cudaError_t launch_step_simt(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
+cudaError_t launch_prefix_simt(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
     const size_t bytes = sizeof(typename Simt<T, D, RT>::Smem);
-    cudaError_t e = allow_smem(step_simt_kernel<T, D, RT>, bytes);
-    if (e == cudaSuccess) e = allow_smem(prefix_simt_kernel<T, D, RT>, bytes);
+    const cudaError_t e = allow_smem(prefix_simt_kernel<T, D, RT>, bytes);
     if (e != cudaSuccess) return e;
-    if (w.splits > 0 && a.dtype == GDR_BF16 && tiled(a.ldq, a.Hq, D)) {
-        if ((e = launch_prefix_tc(a, w, s)) != cudaSuccess) return e;
-    } else if (w.splits > 0) {
-        KernelTimer kt("attn_prefix_simt", s);
-        const int64_t tiles = (a.T * a.group + RT - 1) / RT;
-        prefix_simt_kernel<T, D, RT><<<dim3((unsigned)tiles, a.Hkv, w.splits), 256, bytes, s>>>(a, w);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
+    const int64_t tiles = (a.T * a.group + RT - 1) / RT;
+    KernelTimer kt("attn_prefix_simt", s);
+    prefix_simt_kernel<T, D, RT><<<dim3((unsigned)tiles, a.Hkv, w.splits), 256, bytes, s>>>(a, w);
+    return cudaGetLastError();
+}
+
+template <int D, int RT>
+cudaError_t launch_step_simt(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
+    const size_t bytes = sizeof(typename Simt<float, D, RT>::Smem);
+    const cudaError_t e = allow_smem(step_simt_kernel<float, D, RT>, bytes);
+    if (e != cudaSuccess) return e;
     KernelTimer kt("attn_step_simt", s);
-    step_simt_kernel<T, D, RT><<<w.ctas, 256, bytes, s>>>(a, w);
+    step_simt_kernel<float, D, RT><<<w.ctas, 256, bytes, s>>>(a, w);
     return cudaGetLastError();
 }
 
@@ -445,9 +448,12 @@ cudaError_t launch_merge(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// Rows per tile of the own keys' part: a tile's cost grows with it, and rows beyond the
-// first tile read the keys again.
-int rows_per_tile(int N, int64_t T, int group) { return (T + N - 1) / (N > 0 ? N : 1) * group <= 16 ? 16 : 64; }
+// Rows per tile of the own keys' part, by the rows that a sequence has on average: a
+// tile's cost grows with it, and rows beyond the first tile read the keys again.
+int rows_per_tile(int N, int64_t T, int group, int dtype) {
+    const int64_t rows = (T + N - 1) / (N > 0 ? N : 1) * group;
+    return rows <= 16 ? 16 : rows <= 32 && dtype == GDR_BF16 ? 32 : 64;
+}
 
 // Cuts of the prefix along its keys: about as many CTAs as the GPU holds at once.
 int prefix_splits(int64_t T, int Hkv, int group, int rows, int prefix_len, int dtype) {
@@ -471,8 +477,8 @@ size_t step_layout(StepWork* w, char* base, int N, int64_t T, int Hq, int Hkv, i
         at += (bytes + 255) / 256 * 256;
         return p;
     };
-    w->ctas = 2 * kSms;
-    w->rows = rows_per_tile(N, T, Hq / Hkv);
+    w->ctas = dtype == GDR_BF16 ? kSms : 2 * kSms;
+    w->rows = rows_per_tile(N, T, Hq / Hkv, dtype);
     w->splits = prefix_splits(T, Hkv, Hq / Hkv, w->rows, prefix_len, dtype);
     const size_t slots = (size_t)w->ctas * 2 * w->rows, rows = w->splits ? (size_t)T * Hq : 0;
     w->offsets = reinterpret_cast<int64_t*>(part(sizeof(int64_t) * ((size_t)N + 1)));
@@ -485,10 +491,18 @@ size_t step_layout(StepWork* w, char* base, int N, int64_t T, int Hq, int Hkv, i
     return at;
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_step(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
-    const cudaError_t e = w.rows == 16 ? launch_step_simt<T, D, 16>(a, w, s) : launch_step_simt<T, D, 64>(a, w, s);
-    return e == cudaSuccess ? launch_merge<T, D>(a, w, s) : e;
+    cudaError_t e = cudaSuccess;
+    if (a.dtype == GDR_BF16) {
+        if (w.splits > 0) e = tiled(a.ldq, a.Hq, D) ? launch_prefix_tc(a, w, s)
+                                                    : launch_prefix_simt<__nv_bfloat16, D, 64>(a, w, s);
+        if (e == cudaSuccess) e = launch_step_own(a, w, s);
+        return e == cudaSuccess ? launch_merge<__nv_bfloat16, D>(a, w, s) : e;
+    }
+    if (w.splits > 0) e = w.rows == 16 ? launch_prefix_simt<float, D, 16>(a, w, s) : launch_prefix_simt<float, D, 64>(a, w, s);
+    if (e == cudaSuccess) e = w.rows == 16 ? launch_step_simt<D, 16>(a, w, s) : launch_step_simt<D, 64>(a, w, s);
+    return e == cudaSuccess ? launch_merge<float, D>(a, w, s) : e;
 }
 
 // scale: the maximum of the scores is that of the products only for one above 0
@@ -592,9 +606,7 @@ int gdr_attn_step(const void* q, int64_t q_stride, const void* k_cache, const vo
     a.cu = cu_seqlens; a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.group = Hq / Hkv; a.T = T_total;
     a.scale_log2 = scale * 1.44269504088896341f;
     a.dtype = dtype;
-    const cudaError_t e = dtype == GDR_BF16 ? (D == 128 ? launch_step<__nv_bfloat16, 128>(a, w, s)
-                                                        : launch_step<__nv_bfloat16, 64>(a, w, s))
-                                            : (D == 128 ? launch_step<float, 128>(a, w, s) : launch_step<float, 64>(a, w, s));
+    const cudaError_t e = D == 128 ? launch_step<128>(a, w, s) : launch_step<64>(a, w, s);
     return launch_result(e, "gdr_attn_step launch");
 }
 

@@ -20,7 +20,7 @@
 namespace gdr {
 
 constexpr int kKeyTile = 64;       // keys per tile of the own parts
-constexpr int kStepThreads = 256;  // threads that form the plan
+constexpr int kStepThreads = 256;  // threads that form the plan (a block may have a warp or two more)
 constexpr int kSms = 152;
 constexpr int kMaxSplits = 64;
 
@@ -72,9 +72,9 @@ struct Plan {
 };
 
 // Formed by kStepThreads threads: thread i sums the tiles of a run of sequences.
-// CTA 0 leaves the sequences' numbers for the merge.
+// CTA 0 leaves the sequences' numbers for the merge.  Every thread of the block calls it.
 __device__ __forceinline__ Plan make_plan(const AttnArgs& a, const StepWork& w, int cta) {
-    __shared__ int64_t warp_units[kStepThreads / 32];
+    __shared__ int64_t warp_units[kStepThreads / 32 + 2];
     __shared__ Plan plan;
     const int tid = threadIdx.x, per = (a.N + kStepThreads - 1) / kStepThreads;
     const int lo = min(tid * per, a.N), hi = min(lo + per, a.N);
@@ -118,7 +118,7 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, const StepWork& w, 
 __device__ __forceinline__ int64_t cta_of(int64_t u, int64_t all, int64_t ctas) { return ((u + 1) * ctas - 1) / all; }
 
 // Calls job(n, span, key head, row tile, first key tile, last key tile + 1, slot) for every
-// run of key tiles of one row tile in the plan: slot -1 where it is whole.
+// run of key tiles of one row tile in the plan, until it says false: slot -1 where it is whole.
 template <typename F>
 __device__ __forceinline__ void walk(const AttnArgs& a, const StepWork& w, const Plan& plan, F job) {
     int64_t u = plan.from, offset = plan.offset;
@@ -130,7 +130,8 @@ __device__ __forceinline__ void walk(const AttnArgs& a, const StepWork& w, const
             const int begin = (int)(local - tile * s.key_tiles);
             const int end = (int)min((int64_t)s.key_tiles, begin + (plan.to - u));
             const int slot = begin == 0 && end == s.key_tiles ? -1 : begin > 0 ? 0 : 1;
-            job(n, s, (int)(tile / s.row_tiles), (int)(tile % s.row_tiles), s.first + begin, s.first + end, slot);
+            if (!job(n, s, (int)(tile / s.row_tiles), (int)(tile % s.row_tiles), s.first + begin, s.first + end, slot))
+                return;
             u += end - begin;
         }
         offset += s.units;

@@ -20,12 +20,12 @@
 // in shared memory (0 * NaN is a NaN), in the last tile alone.  Within a sequence a later
 // token's infinity or NaN could still reach an earlier row as 0 * inf; a row whose result
 // is not finite is computed once more, on the CUDA cores, from the keys that it sees.
-#include <cuda.h>
 #include <math.h>
 
 #include <atomic>
 
 #include "attn.h"
+#include "attn_copies.cuh"
 #include "attn_step.cuh"
 #include "common.cuh"
 #include "gdr.h"
@@ -44,7 +44,6 @@ constexpr int kWarps = 12;                // 2 x 4 of softmax; the copies', the 
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "more registers than the block has");
 constexpr float kLag = 8.f;               // how far P's reference may lag behind the maximum, log2 units
-constexpr unsigned kAttnError = 0x800;    // device error word: a wait gave up
 
 template <int D> struct Shape {
     static constexpr int BLOCKS = D / 64;                  // 128-byte column blocks of a row
@@ -66,17 +65,6 @@ struct TcParams {
     int box;     // rows of one copy of keys: 128, or a page's
     unsigned* err;
 };
-
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t mbar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(mbar) : "memory");
-}
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t mbar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(mbar) : "memory");
-}
 
 // D += A B with A in tensor memory.
 __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -109,12 +97,6 @@ __device__ __forceinline__ void tmem_put32(uint32_t addr, const uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // What a CTA works on.
 struct Job {
     int64_t t0;       // first token of its rows' sequence (prompt), or 0
@@ -124,37 +106,6 @@ struct Job {
     int keys;         // end of the keys, counted from the sequence's first
     int n;
 };
-
-// One row once more, a warp together: the keys [from, end) that it sees, read by
-// rows(j, k, v).  Lane l has channels (D / 32) l ..  Leaves the sums, not divided.
-template <int D, typename R>
-__device__ __noinline__ void row_again(const __nv_bfloat16* q, int64_t from, int64_t end, float scale, R rows,
-                                       float (&acc)[D / 32], float& m, float& l) {
-    constexpr int C = D / 32;
-    const int lane = threadIdx.x & 31;
-    float x[C];
-    Vec<__nv_bfloat16, C>::load(q + lane * C, x);
-    m = -INFINITY;
-    l = 0.f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = 0.f;
-    for (int64_t j = from; j < end; ++j) {
-        const __nv_bfloat16 *kp, *vp;
-        if (!rows(j, kp, vp)) continue;
-        float k[C], v[C], dot = 0.f;
-        Vec<__nv_bfloat16, C>::load(kp + lane * C, k);
-        Vec<__nv_bfloat16, C>::load(vp + lane * C, v);
-#pragma unroll
-        for (int c = 0; c < C; ++c) dot = fmaf(x[c], k[c], dot);
-        const float s = warp_sum(dot) * scale, top = fmaxf(m, s);
-        const float base = top == -INFINITY ? 0.f : top, back = exp2f(m - base), p = exp2f(s - base);
-        m = top;
-        l = fmaf(l, back, p);
-        // a weight of 0 (a score of -inf) takes nothing from the value
-#pragma unroll
-        for (int c = 0; c < C; ++c) acc[c] = p == 0.f ? acc[c] * back : fmaf(acc[c], back, p * v[c]);
-    }
-}
 
 template <int D, bool PREFIX>
 __global__ void __launch_bounds__(kWarps * 32, 1)
@@ -540,20 +491,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 const int64_t place_w = __shfl_sync(0xffffffffu, place, who);
                 const int limit_w = __shfl_sync(0xffffffffu, limit, who);
                 float acc[D / 32], mw, lw;
+                // by value: what the call takes by reference would live in local memory
+                const Paged cache = a.cache;
+                const int Hkv = a.Hkv;
+                const int64_t ldk = a.ldk, ldv = a.ldv;
+                const __nv_bfloat16* keys = static_cast<const __nv_bfloat16*>(a.k) + job.t0 * ldk + (int64_t)h * D;
+                const __nv_bfloat16* vals = static_cast<const __nv_bfloat16*>(a.v) + job.t0 * ldv + (int64_t)h * D;
                 row_again<D>(static_cast<const __nv_bfloat16*>(a.q) + at_w * a.ldq + head_w * D, (int64_t)from * kTile,
                              min(limit_w, end * kTile), c,
-                             [&](int64_t key, const __nv_bfloat16*& kp, const __nv_bfloat16*& vp) {
-                                 if (PREFIX) {
-                                     const int page = a.cache.prefix[key >> a.cache.page_bits];
-                                     if (page < 0 || page >= a.cache.num_pages) return false;
-                                     const int64_t r = (((int64_t)page * a.Hkv + h) << a.cache.page_bits) +
-                                                       (key & (a.cache.page_size - 1));
-                                     kp = static_cast<const __nv_bfloat16*>(a.cache.k) + r * D;
-                                     vp = static_cast<const __nv_bfloat16*>(a.cache.v) + r * D;
-                                 } else {
-                                     kp = static_cast<const __nv_bfloat16*>(a.k) + (job.t0 + key) * a.ldk + (int64_t)h * D;
-                                     vp = static_cast<const __nv_bfloat16*>(a.v) + (job.t0 + key) * a.ldv + (int64_t)h * D;
-                                 }
+                             [=](int64_t key, const __nv_bfloat16*& kp, const __nv_bfloat16*& vp) {
+                                 if (PREFIX) return cached_row<D>(cache, cache.prefix, Hkv, h, key, kp, vp);
+                                 kp = keys + key * ldk;
+                                 vp = vals + key * ldv;
                                  return true;
                              }, acc, mw, lw);
                 if (PREFIX) {
@@ -570,6 +519,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
     }
     fence_before();
+    __syncwarp();
     __syncthreads();
     if (tid == 0 && abort_flag) atomicOr(p.err, kAttnError);
     if (warp == 9) {
@@ -579,49 +529,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 }
 
 // ---- launches -----------------------------------------------------------------------
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static std::atomic<EncodeTiled> known{nullptr};
-    EncodeTiled f = known.load(std::memory_order_acquire);
-    if (f) return f;
-    void* entry = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &entry, 12000, cudaEnableDefault, &found) !=
-            cudaSuccess || found != cudaDriverEntryPointSuccess)
-        return nullptr;
-    f = reinterpret_cast<EncodeTiled>(entry);
-    known.store(f, std::memory_order_release);
-    return f;
-}
-
-bool encode(CUtensorMap* map, const void* p, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box) {
-    const EncodeTiled f = encode_tiled();
-    const cuuint32_t steps[3] = {1, 1, 1};
-    return f && f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(p), dims, strides, box, steps,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// [T, heads, D] rows in boxes of 64 channels, `hb` heads and `tb` tokens.
-bool encode_tokens(CUtensorMap* map, const void* p, int64_t ld, int64_t T, int heads, int D, int hb, int tb) {
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T};
-    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)hb, (cuuint32_t)tb};
-    return encode(map, p, 3, dims, strides, box);
-}
-
-// The cache's rows in boxes of 64 channels and `rows` rows.
-bool encode_cache(CUtensorMap* map, const void* p, int64_t all, int D, int rows) {
-    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)all};
-    const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)rows};
-    return encode(map, p, 2, dims, strides, box);
-}
 
 template <int D, bool PREFIX>
 cudaError_t launch_tc(TcParams p, dim3 grid, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,

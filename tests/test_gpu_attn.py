@@ -151,6 +151,28 @@ def test_step_cut_into_many_runs(dtype):
         check_attention(pool.step(q, lens, cu), pool.reference(q, lens, cu), 20001)
 
 
+@pytest.mark.parametrize("group,D", [(4, 128), (4, 64), (20, 128), (40, 128), (40, 64)])
+def test_step_long_runs(group, D):
+    """Runs of many tiles per CTA, many times over: the copies' ring laps often, and every call gives the same bits."""
+    Hkv, lens = 4, [60000, 25000]
+    cu = starts([1, 1])
+    pool = Pool(5, [a + 1 for a in lens], Hkv, D, 64, BF16)
+    q = normal(3, 2, Hkv * group, D, dtype=BF16, std=2.0)
+    o = pool.step(q, lens, cu)
+    for n, a in enumerate(lens):
+        k, v = (c[pool.table[n, :-(-(a + 1) // 64)].long()].transpose(1, 2).flatten(0, 1)[:a + 1].double()
+                for c in (pool.k, pool.v))
+        s = torch.einsum("hgd,jhd->hgj", q[n].double().view(Hkv, group, D), k) * D ** -0.5
+        p = torch.softmax(s, -1)
+        ref = torch.einsum("hgj,jhd->hgd", p, v).view(1, -1, D)
+        weight = torch.einsum("hgj,jhd->hgd", p, v.abs()).view(1, -1, D)
+        score = torch.einsum("hgd,jhd->hgj", q[n].double().view(Hkv, group, D).abs(), k.abs()).amax(-1) * D ** -0.5
+        check_attention(o[n:n + 1], [x.cpu().numpy() for x in (ref, weight, score.view(1, -1))], a + 1)
+    for _ in range(40):
+        assert bits_equal(o, pool.step(q, lens, cu))
+    assert gdr.device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("prefix", [0, 70])
 def test_step_leaves_unwritten_cache_rows_alone(dtype, prefix):
