@@ -267,11 +267,12 @@ __global__ void __launch_bounds__(256) step_simt_kernel(const AttnArgs a, const 
     using E = Simt<T, D, RT>;
     typename E::Smem& s = *reinterpret_cast<typename E::Smem*>(raw);
     const Plan plan = make_plan(a, w, blockIdx.x);
-    walk(a, w, plan, [&](int n, const Span& sp, int h, int row_tile, int from, int to, int slot) {
-        const int64_t t0 = max(a.cu[n], 0), len = a.cache.lens[n];
-        const int r0 = row_tile * RT, rows = min(RT, sp.rows - r0);
-        const int64_t most = min(len + (r0 + rows - 1) / a.group + 1, (int64_t)a.cache.max_pages << a.cache.page_bits);
-        const int32_t* pages = a.cache.table + n * a.cache.table_ld;
+    Runs runs(a, w, plan);
+    for (Run run; runs.next(run);) {
+        const int64_t t0 = run.s.t0, len = run.s.len;
+        const int r0 = run.row_tile * RT, rows = min(RT, run.s.rows - r0), h = run.h;
+        const int64_t most = min(len + (r0 + rows - 1) / a.group + 1, (int64_t)run.s.end);
+        const int32_t* pages = a.cache.table + run.n * a.cache.table_ld;
         auto row = [&](int r) { return (t0 + (r0 + r) / a.group) * a.Hq + h * a.group + (r0 + r) % a.group; };
         auto element = [&](int r, int64_t ld) {
             return (t0 + (r0 + r) / a.group) * ld + (int64_t)(h * a.group + (r0 + r) % a.group) * D;
@@ -279,12 +280,12 @@ __global__ void __launch_bounds__(256) step_simt_kernel(const AttnArgs a, const 
         E e;
         e.start(s, [&](int r) { return r < rows ? static_cast<const T*>(a.q) + element(r, a.ldq) : nullptr; },
                 [&](int r) { return r < rows ? len + (r0 + r) / a.group + 1 : 0; }, a.scale_log2);
-        for (int k = from; k < to; ++k)
+        for (int k = run.from; k < run.to; ++k)
             e.tile(s, (int64_t)k * kKeyTile, a.cache.prefix_len, most, [&](int64_t j, const T*& kp, const T*& vp) {
                 return cached<T, D>(a.cache, pages, a.Hkv, h, j, kp, vp);
             });
-        if (slot >= 0) {
-            const int64_t base = ((int64_t)blockIdx.x * 2 + slot) * w.rows;
+        if (run.slot >= 0) {
+            const int64_t base = ((int64_t)blockIdx.x * 2 + run.slot) * w.rows;
             e.leave([&](int r) { return r < rows ? w.slot_sum + (base + r) * D : nullptr; },
                     [&](int r) { return w.slot_stat + base + r; });
         } else if (a.cache.prefix_len > 0) {
@@ -293,8 +294,7 @@ __global__ void __launch_bounds__(256) step_simt_kernel(const AttnArgs a, const 
         } else {
             e.finish([&](int r) { return r < rows ? static_cast<T*>(a.o) + element(r, a.ldo) : nullptr; });
         }
-        return true;
-    });
+    }
 }
 
 // The prefix: blockIdx = (row tile of all tokens' rows, key head, split).
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kMergeThreads) step_merge_kernel(const AttnArg
     const int n = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31;
     const Span s = span_of(a, w.rows, n);
     const int64_t all = w.offsets[a.N], ctas = taking_part(all, w.ctas);
-    const int64_t t0 = max(a.cu[n], 0);
+    const int64_t t0 = s.t0;
     for (int r = blockIdx.z * (kMergeThreads / 32) + (threadIdx.x >> 5); r < s.rows; r += gridDim.z * (kMergeThreads / 32)) {
         const int64_t row = (t0 + r / a.group) * a.Hq + h * a.group + r % a.group;
         int64_t first = 0;

@@ -9,10 +9,10 @@
 // (m16n8k16, bf16 in, fp32 out), whose 16 rows fit the few there are.  (tcgen05's tiles
 // have 128 rows at least: with 4 to 64 of them filled it would read shared memory for
 // empty ones.)
-//   Each warp has 16 of a tile's 64 keys and a running maximum and sum of its own, so that
-// no tile needs a barrier; the warps' results are joined at the end of a run.  With up to
-// 32 rows two sets of four warps take the tiles in turn; with 64 both work on every tile,
-// 32 rows each.
+//   A warp has 16 rows and 16 or 32 of a tile's 64 keys, and a running maximum and sum of its
+// own, so that no tile needs a barrier; the warps' results are joined at the end of a run.
+// With up to 16 rows two sets of four warps take the tiles in turn; with more, rows are what
+// the warps share out first: fewer results to join.
 #include <math.h>
 
 #include <atomic>
@@ -31,25 +31,27 @@ namespace {
 constexpr int kReaders = 8;  // warps that compute
 constexpr int kStepBlock = (kReaders + 1) * 32;
 
-// MT row tiles of 16 per warp; SETS of four warps on the same keys with other rows.
-template <int D, int MT, int SETS> struct StepShape {
-    static constexpr int ROWS = 16 * MT * SETS;
+// ROWS rows a run: GROUPS of 16, each with the warps that have its keys.
+template <int D, int ROWS> struct StepShape {
+    static constexpr int GROUPS = ROWS / 16, SHARE = kReaders / GROUPS;  // SHARE warps have the same rows
+    static constexpr int KEYS = ROWS == 64 ? 32 : 16;                    // of a tile, per warp
+    static constexpr bool TURNS = SHARE * KEYS > kKeyTile;               // two sets of warps take the tiles in turn
     static constexpr int BLOCKS = D / 64, BLOCK_BYTES = kKeyTile * 128, TILE_BYTES = BLOCKS * BLOCK_BYTES;
     static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
     // Where two sets take the tiles in turn a stage belongs to one of them, for good: a wait
     // by parity knows only its barrier's last phase, and a set that skips a stage's tile
     // could take the phase before the skipped one for its own.
-    static constexpr int STAGES = D == 64 ? 10 : MT == 1 ? 6 : 4;
-    static_assert(SETS == 2 || STAGES % 2 == 0, "a stage per set");
-    static constexpr int Q_STRIDE = D * 2 + 16;      // a row of queries: 8 rows of a matrix on different banks
-    static constexpr int PARTS = 4, PART = D / PARTS;  // columns joined at a time
-    static constexpr int PART_LD = PART + 4;
-    static constexpr int JOIN_BYTES = kReaders * 16 * MT * PART_LD * 4;
+    static constexpr int STAGES = D == 64 ? 10 : ROWS == 16 ? 6 : 5;
+    static_assert(!TURNS || STAGES % 2 == 0, "a stage per set");
+    static constexpr int Q_STRIDE = D * 2 + 16;   // a row of queries: 8 rows of a matrix on different banks
+    // joined at a time: 8 rows of each group, half of the columns
+    static constexpr int PART = D / 2, PART_LD = PART + 4;
+    static constexpr int JOIN_BYTES = kReaders * 8 * PART_LD * 4;
     static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 2 * ROWS * Q_STRIDE + JOIN_BYTES;
 };
 
 struct StepJob {
-    int64_t t0, len, least, most;  // first token; keys before the call's; the keys that some row sees: least .. most - 1
+    int t0, len, least, most;  // first token; keys before the call's; the keys that some row sees: least .. most - 1
     int n, h, r0, rows, from, to, slot;
 };
 
@@ -87,15 +89,15 @@ __device__ __forceinline__ bool any_reader(bool x) {
     return r != 0;
 }
 
-template <int D, int MT, int SETS>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kStepBlock, 1)
     step_kernel(const StepParams p, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-    using C = StepShape<D, MT, SETS>;
+    using C = StepShape<D, ROWS>;
     extern __shared__ unsigned char raw[];
     __shared__ StepBarriers bars;
     __shared__ StepJob jobs[2];
     __shared__ uint32_t missing[C::STAGES];     // a bit per 16 keys without a page
-    __shared__ float2 stats[kReaders][16 * MT];
+    __shared__ float2 stats[kReaders][16];
     __shared__ uint32_t bad_rows[2];
     __shared__ int abort_flag;
     const AttnArgs& a = p.a;
@@ -104,12 +106,12 @@ __global__ void __launch_bounds__(kStepBlock, 1)
     const uint32_t ring = (smem_u32(raw) + 1023) & ~1023u;
     const uint32_t queries = ring + C::STAGES * C::STAGE_BYTES;
     unsigned char* const base = raw + (ring - smem_u32(raw));
-    float* const join = reinterpret_cast<float*>(base + C::STAGES * C::STAGE_BYTES + 2 * C::ROWS * C::Q_STRIDE);
+    float* const join = reinterpret_cast<float*>(base + C::STAGES * C::STAGE_BYTES + 2 * ROWS * C::Q_STRIDE);
 
     if (tid == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(smem_u32(&bars.full[i]), 1);
-            mbar_init(smem_u32(&bars.empty[i]), SETS == 2 ? 8 : 4);
+            mbar_init(smem_u32(&bars.empty[i]), C::TURNS ? kReaders / 2 : kReaders);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bars.q_full[i]), 1);
@@ -125,49 +127,58 @@ __global__ void __launch_bounds__(kStepBlock, 1)
         // ---- copies ----
         int it = 0, count = 0;  // tiles and runs so far
         bool ok = true;
-        walk(a, p.w, plan, [&](int n, const Span& sp, int h, int row_tile, int from, int to, int slot) {
+        const int pieces = kKeyTile / p.box;  // copies of a tile
+        // lane l: the page of piece `at` + l of a sequence
+        auto pages_from = [&](int n, int at) {
+            const int slot = (int)((int64_t)(at + lane) * p.box >> a.cache.page_bits);
+            return slot < a.cache.max_pages ? a.cache.table[n * a.cache.table_ld + slot] : -1;
+        };
+        Runs runs(a, p.w, plan);
+        Run run;
+        bool more = runs.next(run);
+        int held = more ? pages_from(run.n, run.from * pieces) : 0;
+        while (more && ok) {
+            const Run r = run;
+            int pages = held, at = r.from * pieces;
+            // the next run is looked up, and its first pages, before this one's copies are waited for
+            more = runs.next(run);
+            if (more) held = pages_from(run.n, run.from * pieces);
             const int q = count & 1;
             if (count >= 2) ok = mbar_wait(smem_u32(&bars.q_empty[q]), (count / 2 - 1) & 1, abort);
-            if (!(ok = __all_sync(0xffffffffu, ok))) return false;
-            const int64_t t0 = max(a.cu[n], 0), len = a.cache.lens[n];
-            const int r0 = row_tile * C::ROWS, rows = min(C::ROWS, sp.rows - r0);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            const int r0 = r.row_tile * ROWS, rows = min(ROWS, r.s.rows - r0);
             if (lane == 0) {
                 StepJob& j = jobs[q];
-                j.t0 = t0; j.len = len; j.n = n; j.h = h; j.r0 = r0; j.rows = rows; j.from = from; j.to = to;
-                j.slot = slot;
+                j.t0 = r.s.t0; j.len = r.s.len; j.n = r.n; j.h = r.h; j.r0 = r0; j.rows = rows;
+                j.from = r.from; j.to = r.to; j.slot = r.slot;
                 j.least = a.cache.prefix_len;
-                j.most = min(len + (r0 + rows - 1) / a.group + 1, (int64_t)a.cache.max_pages << a.cache.page_bits);
+                j.most = (int)min((int64_t)r.s.len + (r0 + rows - 1) / a.group + 1, (int64_t)r.s.end);
                 mbar_arrive_tx(smem_u32(&bars.q_full[q]), rows * D * 2);
             }
             __syncwarp();
-            for (int r = lane; r < rows; r += 32) {
-                const __nv_bfloat16* from_row = static_cast<const __nv_bfloat16*>(a.q) +
-                    (t0 + (r0 + r) / a.group) * a.ldq + (int64_t)(h * a.group + (r0 + r) % a.group) * D;
-                bulk_g2s(queries + (q * C::ROWS + r) * C::Q_STRIDE, from_row, D * 2, smem_u32(&bars.q_full[q]));
+            for (int i = lane; i < rows; i += 32) {
+                const int token = (r0 + i) / a.group, head = r.h * a.group + (r0 + i) - token * a.group;
+                bulk_g2s(queries + (q * ROWS + i) * C::Q_STRIDE,
+                         static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(r.s.t0 + token) * a.ldq + (int64_t)head * D,
+                         D * 2, smem_u32(&bars.q_full[q]));
             }
             ++count;
-            const int32_t* pages = a.cache.table + n * a.cache.table_ld;
-            const int pieces = kKeyTile / p.box;  // copies of a tile
-            int held = 0;                         // lane l: the page of piece `at` + l
-            int64_t at = -64;
-            for (int k = from; k < to; ++k, ++it) {
-                const int stage = it % C::STAGES;
-                const int64_t first = (int64_t)k * pieces;  // the tile's first piece
+            for (int k = r.from; k < r.to; ++k, ++it) {
+                const int stage = it % C::STAGES, first = k * pieces;  // the tile's first piece
                 if (first + pieces > at + 32) {
                     at = first;
-                    const int64_t slot_of = (at + lane) * p.box >> a.cache.page_bits;
-                    held = slot_of < a.cache.max_pages ? pages[slot_of] : -1;
+                    pages = pages_from(r.n, at);
                 }
-                int page = __shfl_sync(0xffffffffu, held, (int)(first - at) + (lane & (pieces - 1)));
-                const int64_t key = (int64_t)k * kKeyTile + (lane & (pieces - 1)) * p.box;
+                const int page = __shfl_sync(0xffffffffu, pages, first - at + (lane & (pieces - 1)));
+                const int key = k * kKeyTile + (lane & (pieces - 1)) * p.box;
                 const bool gone = page < 0 || page >= a.cache.num_pages;
                 // a piece without a page is read from the cache's first rows and left out
-                const int row = gone ? 0 : (int)((((int64_t)page * a.Hkv + h) << a.cache.page_bits) +
+                const int row = gone ? 0 : (int)((((int64_t)page * a.Hkv + r.h) << a.cache.page_bits) +
                                                  (key & (a.cache.page_size - 1)));
                 const bool part = __shfl_sync(0xffffffffu, gone, (lane & 3) * 16 / p.box);
                 const uint32_t out = __ballot_sync(0xffffffffu, part && lane < 4);
                 if (it >= C::STAGES) ok = mbar_wait(smem_u32(&bars.empty[stage]), (it / C::STAGES - 1) & 1, abort);
-                if (!(ok = __all_sync(0xffffffffu, ok))) return false;
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const uint32_t mbar = smem_u32(&bars.full[stage]), dst = ring + stage * C::STAGE_BYTES;
                 if (lane == 0) {
                     missing[stage] = out;
@@ -182,16 +193,14 @@ __global__ void __launch_bounds__(kStepBlock, 1)
                                value ? &mv : &mk, b * 64, row, mbar);
                 }
             }
-            return true;
-        });
-        // nothing may still be arriving when the CTA leaves; the last runs' queries first, as their
-        // barriers' phases are the last now
+        }
+        // nothing may still be arriving when the CTA leaves; the queries' barriers are waited for
+        // before the end is announced through them
         bool landed = true;
         for (int i = max(0, it - C::STAGES); i < it; ++i)
             landed &= mbar_wait_copies(smem_u32(&bars.full[i % C::STAGES]), (i / C::STAGES) & 1);
         for (int i = max(0, count - 2); i < count; ++i)
             landed &= mbar_wait_copies(smem_u32(&bars.q_full[i & 1]), (i / 2) & 1);
-        // no more runs
         if (ok && count >= 2) ok = mbar_wait(smem_u32(&bars.q_empty[count & 1]), (count / 2 - 1) & 1, abort);
         ok = __all_sync(0xffffffffu, ok && landed);
         if (ok && lane == 0) {
@@ -201,9 +210,11 @@ __global__ void __launch_bounds__(kStepBlock, 1)
         if (!ok) *abort = 1;
     } else {
         // ---- arithmetic ----
-        const int set = warp >> 2, part = warp & 3;       // the warp's 16 keys of a tile
-        const int quad = lane >> 2, pair = lane & 3;      // rows quad and quad + 8, keys or columns 2 pair, 2 pair + 1
+        const int group = warp % C::GROUPS, share = warp / C::GROUPS;
+        const int set = C::TURNS ? share >> 2 : 0, part = C::TURNS ? share & 3 : share;  // the warp's keys of a tile
+        const int quad = lane >> 2, pair = lane & 3;  // rows quad and quad + 8, keys or columns 2 pair, 2 pair + 1
         const float c = a.scale_log2;
+        constexpr int NT = C::KEYS / 8;               // 8 keys each
         int it = 0;
         for (int count = 0;; ++count) {
             const int q = count & 1;
@@ -214,133 +225,116 @@ __global__ void __launch_bounds__(kStepBlock, 1)
             }
             const StepJob j = jobs[q];
             if (j.n < 0) break;
-            const uint32_t my_q = queries + (q * C::ROWS + (SETS == 2 ? set * 16 * MT : 0)) * C::Q_STRIDE +
-                                  (lane & 15) * C::Q_STRIDE + (lane >> 4) * 16;
-            const int row_base = j.r0 + (SETS == 2 ? set * 16 * MT : 0);  // the warp's first row
-            uint32_t aq[MT == 1 ? D / 16 : 1][4];
-            if (MT == 1) {
+            uint32_t aq[D / 16][4];
+            {
+                const uint32_t at = queries + (q * ROWS + group * 16 + (lane & 15)) * C::Q_STRIDE + (lane >> 4) * 16;
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) ldmatrix4(aq[MT == 1 ? ks : 0], my_q + ks * 32);
+                for (int ks = 0; ks < D / 16; ++ks) ldmatrix4(aq[ks], at + ks * 32);
             }
-            float m[MT][2], l[MT][2], acc[MT][D / 8][4];
-            int64_t limit[MT][2];
+            float m[2], l[2], acc[D / 8][4];
+            int limit[2];
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
+            for (int i = 0; i < 2; ++i) {
+                m[i] = -INFINITY;
+                l[i] = 0.f;
+                limit[i] = min(j.len + (j.r0 + group * 16 + i * 8 + quad) / a.group + 1, j.most);
+            }
+            const int all_see = min(j.len + j.r0 / a.group + 1, j.most);  // end of the keys that every row sees
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    m[t][i] = -INFINITY;
-                    l[t][i] = 0.f;
-                    limit[t][i] = j.len + (row_base + t * 16 + i * 8 + quad) / a.group + 1;
-                }
+            for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[t][n][e] = 0.f;
+                for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
 
             for (int k = j.from; k < j.to; ++k, ++it) {
-                if (SETS == 1 && (it & 1) != set) continue;
+                if (C::TURNS && (it & 1) != set) continue;
                 const int stage = it % C::STAGES;
                 if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.full[stage]), (it / C::STAGES) & 1, abort));
                 if (!ok) continue;
                 const uint32_t ks_ = ring + stage * C::STAGE_BYTES, vs = ks_ + C::TILE_BYTES;
-                const int64_t key0 = (int64_t)k * kKeyTile + part * 16;
-                // scores of 16 rows by 16 keys: two tiles of 8 keys
-                float s[MT][2][4];
+                const int key0 = k * kKeyTile + part * C::KEYS;
+                float s[NT][4];
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[t][n][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
                 {
                     // matrices of a load: keys 0-7 and 8-15 (lane / 16), channels 0-7 and 8-15 (lane / 8 % 2)
-                    const int r = part * 16 + (lane >> 4) * 8 + (lane & 7), ch = (lane >> 3) & 1;
+                    const int r = part * C::KEYS + (lane >> 4) * 8 + (lane & 7), ch = (lane >> 3) & 1;
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        uint32_t b[4];
-                        ldmatrix4(b, ks_ + chunk_k128(r, ks * 2 + ch, kKeyTile));
+                    for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-                        for (int t = 0; t < MT; ++t) {
-                            uint32_t aq2[4];
-                            if (MT > 1) ldmatrix4(aq2, my_q + t * 16 * C::Q_STRIDE + ks * 32);
-                            mma16816(s[t][0], MT == 1 ? aq[MT == 1 ? ks : 0] : aq2, b[0], b[1]);
-                            mma16816(s[t][1], MT == 1 ? aq[MT == 1 ? ks : 0] : aq2, b[2], b[3]);
+                        for (int n = 0; n < NT; n += 2) {
+                            uint32_t b[4];
+                            ldmatrix4(b, ks_ + chunk_k128(r + n * 8, ks * 2 + ch, kKeyTile));
+                            mma16816(s[n], aq[ks], b[0], b[1]);
+                            mma16816(s[n + 1], aq[ks], b[2], b[3]);
                         }
-                    }
                 }
-                const bool gone = missing[stage] >> part & 1;
-                const bool edge = gone || key0 < j.least || key0 + 16 > j.len + 1 + j.r0 / a.group || key0 + 16 > j.most;
+                const uint32_t gone = missing[stage] >> (part * C::KEYS / 16) & ((1u << C::KEYS / 16) - 1);
+                const bool edge = gone || key0 < j.least || key0 + C::KEYS > all_see;
+                float now[2];
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    float now[2];
+                for (int i = 0; i < 2; ++i) {
+                    if (edge) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (edge) {
-#pragma unroll
-                            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const int64_t key = key0 + n * 8 + pair * 2 + e;
-                                    if (gone || key < j.least || key >= limit[t][i]) s[t][n][i * 2 + e] = -INFINITY;
-                                }
-                        }
-                        float top = fmaxf(fmaxf(s[t][0][i * 2], s[t][0][i * 2 + 1]),
-                                          fmaxf(s[t][1][i * 2], s[t][1][i * 2 + 1]));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                        now[i] = fmaxf(m[t][i], top * c);
-                    }
-                    if (__any_sync(0xffffffffu, now[0] > m[t][0] || now[1] > m[t][1])) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float back = now[i] == -INFINITY ? 1.f : ex2(m[t][i] - now[i]);
-                            m[t][i] = now[i];
-                            l[t][i] *= back;
-#pragma unroll
-                            for (int n = 0; n < D / 8; ++n) {
-                                acc[t][n][i * 2] *= back;
-                                acc[t][n][i * 2 + 1] *= back;
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float off = m[t][i] == -INFINITY ? 0.f : -m[t][i];
-#pragma unroll
-                        for (int n = 0; n < 2; ++n)
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const float x = ex2(fmaf(s[t][n][i * 2 + e], c, off));
-                                s[t][n][i * 2 + e] = x;
-                                l[t][i] += x;
+                                const int key = key0 + n * 8 + pair * 2 + e;
+                                if ((gone >> (n / 2) & 1) || key < j.least || key >= limit[i]) s[n][i * 2 + e] = -INFINITY;
                             }
                     }
-                }
-                // the weights as they lie are the next product's left operand
-                uint32_t pk[MT][4];
+                    float top = fmaxf(s[0][i * 2], s[0][i * 2 + 1]);
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    pk[t][0] = pack_bf16(s[t][0][0], s[t][0][1]);
-                    pk[t][1] = pack_bf16(s[t][0][2], s[t][0][3]);
-                    pk[t][2] = pack_bf16(s[t][1][0], s[t][1][1]);
-                    pk[t][3] = pack_bf16(s[t][1][2], s[t][1][3]);
+                    for (int n = 1; n < NT; ++n) top = fmaxf(top, fmaxf(s[n][i * 2], s[n][i * 2 + 1]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    now[i] = fmaxf(m[i], top * c);
                 }
-                // what no row sees may hold anything: a weight of 0 does not keep a NaN out
-                uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-                if (edge) {
+                if (__any_sync(0xffffffffu, now[0] > m[0] || now[1] > m[1])) {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const int64_t key = key0 + n * 8 + pair * 2;
-                        const bool first = !gone && key >= j.least && key < j.most;
-                        const bool second = !gone && key + 1 >= j.least && key + 1 < j.most;
-                        keep[n] = (first ? 0xffffu : 0u) | (second ? 0xffff0000u : 0u);
+                    for (int i = 0; i < 2; ++i) {
+                        const float back = now[i] == -INFINITY ? 1.f : ex2(m[i] - now[i]);
+                        m[i] = now[i];
+                        l[i] *= back;
+#pragma unroll
+                        for (int n = 0; n < D / 8; ++n) {
+                            acc[n][i * 2] *= back;
+                            acc[n][i * 2 + 1] *= back;
+                        }
                     }
                 }
-                {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float off = m[i] == -INFINITY ? 0.f : -m[i];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = ex2(fmaf(s[n][i * 2 + e], c, off));
+                            s[n][i * 2 + e] = x;
+                            l[i] += x;
+                        }
+                }
+#pragma unroll
+                for (int half = 0; half < NT / 2; ++half) {
+                    // the weights as they lie are the next product's left operand
+                    const uint32_t pk[4] = {pack_bf16(s[2 * half][0], s[2 * half][1]), pack_bf16(s[2 * half][2], s[2 * half][3]),
+                                            pack_bf16(s[2 * half + 1][0], s[2 * half + 1][1]),
+                                            pack_bf16(s[2 * half + 1][2], s[2 * half + 1][3])};
+                    // what no row sees may hold anything: a weight of 0 does not keep a NaN out
+                    uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+                    if (edge) {
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const int key = key0 + half * 16 + n * 8 + pair * 2;
+                            const bool there = !(gone >> half & 1);
+                            keep[n] = (there && key >= j.least && key < j.most ? 0xffffu : 0u) |
+                                      (there && key + 1 >= j.least && key + 1 < j.most ? 0xffff0000u : 0u);
+                        }
+                    }
                     // matrices of a load: keys 0-7 and 8-15 (lane / 8 % 2), channels 0-7 and 8-15 (lane / 16)
-                    const int r = part * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), ch = lane >> 4;
+                    const int r = part * C::KEYS + half * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), ch = lane >> 4;
 #pragma unroll
                     for (int n = 0; n < D / 16; ++n) {
                         uint32_t b[4];
@@ -351,11 +345,8 @@ __global__ void __launch_bounds__(kStepBlock, 1)
                             b[2] &= keep[0];
                             b[3] &= keep[1];
                         }
-#pragma unroll
-                        for (int t = 0; t < MT; ++t) {
-                            mma16816(acc[t][2 * n], pk[t], b[0], b[1]);
-                            mma16816(acc[t][2 * n + 1], pk[t], b[2], b[3]);
-                        }
+                        mma16816(acc[2 * n], pk, b[0], b[1]);
+                        mma16816(acc[2 * n + 1], pk, b[2], b[3]);
                     }
                 }
                 __syncwarp();
@@ -363,84 +354,81 @@ __global__ void __launch_bounds__(kStepBlock, 1)
             }
 
             // ---- the warps' results joined ----
+            if (lane == 0) mbar_arrive(smem_u32(&bars.q_empty[q]));
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float x = l[t][i];
-                    x += __shfl_xor_sync(0xffffffffu, x, 1);
-                    x += __shfl_xor_sync(0xffffffffu, x, 2);
-                    if (pair == 0) stats[warp][t * 16 + i * 8 + quad] = make_float2(m[t][i], x);
-                }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars.q_empty[q]));  // MT > 1 reads the queries up to here
-            constexpr int SHARE = SETS == 2 ? 4 : 8;  // warps with the same rows
-            constexpr int C4 = C::PART / 4;           // threads of a row in the join
-            constexpr int OUT = C::ROWS * C4 / (kReaders * 32) > 0 ? C::ROWS * C4 / (kReaders * 32) : 1;
+            for (int i = 0; i < 2; ++i) {
+                float x = l[i];
+                x += __shfl_xor_sync(0xffffffffu, x, 1);
+                x += __shfl_xor_sync(0xffffffffu, x, 2);
+                if (pair == 0) stats[warp][i * 8 + quad] = make_float2(m[i], x);
+            }
+            constexpr int C4 = C::PART / 4;                    // threads of a row
+            constexpr int ITEMS = C::GROUPS * 8 * C4;          // of a part
             bool stop = false;
 #pragma unroll
-            for (int b = 0; b < C::PARTS; ++b) {
-                constexpr int N8 = C::PART / 8;
+            for (int half = 0; half < 2; ++half) {             // rows 0-7 and 8-15 of each group
+                if (stop || (half && j.rows <= 8)) break;
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
+                for (int b = 0; b < 2; ++b) {                  // halves of the columns
+                    constexpr int N8 = C::PART / 8;
 #pragma unroll
-                    for (int n = 0; n < N8; ++n) {
-                        float* to = join + (warp * 16 * MT + t * 16 + quad) * C::PART_LD + n * 8 + pair * 2;
-                        *reinterpret_cast<float2*>(to) = make_float2(acc[t][b * N8 + n][0], acc[t][b * N8 + n][1]);
-                        *reinterpret_cast<float2*>(to + 8 * C::PART_LD) =
-                            make_float2(acc[t][b * N8 + n][2], acc[t][b * N8 + n][3]);
+                    for (int n = 0; n < N8; ++n)
+                        *reinterpret_cast<float2*>(join + (warp * 8 + quad) * C::PART_LD + n * 8 + pair * 2) =
+                            make_float2(acc[b * N8 + n][half * 2], acc[b * N8 + n][half * 2 + 1]);
+                    stop = any_reader(!ok);
+                    if (stop) break;
+#pragma unroll
+                    for (int i = tid; i < ITEMS; i += kReaders * 32) {
+                        const int g = i / C4 / 8, r8 = i / C4 % 8, col = i % C4 * 4, r = g * 16 + half * 8 + r8;
+                        if (r >= j.rows) continue;
+                        float2 st[C::SHARE];
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int w = 0; w < C::SHARE; ++w) {
+                            st[w] = stats[w * C::GROUPS + g][half * 8 + r8];
+                            top = fmaxf(top, st[w].x);
+                        }
+                        const float off = top == -INFINITY ? 0.f : top;
+                        float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int w = 0; w < C::SHARE; ++w) {
+                            const float f = ex2(st[w].x - off);
+                            const float4 y = *reinterpret_cast<const float4*>(
+                                join + ((w * C::GROUPS + g) * 8 + r8) * C::PART_LD + col);
+                            sum = fmaf(st[w].y, f, sum);
+                            x[0] = fmaf(y.x, f, x[0]);
+                            x[1] = fmaf(y.y, f, x[1]);
+                            x[2] = fmaf(y.z, f, x[2]);
+                            x[3] = fmaf(y.w, f, x[3]);
+                        }
+                        if (!(fabsf(x[0]) + fabsf(x[1]) + fabsf(x[2]) + fabsf(x[3]) + sum < INFINITY)) {
+                            atomicOr(&bad_rows[r >> 5], 1u << (r & 31));  // the same word whatever the order
+                            continue;
+                        }
+                        const int local = (j.r0 + r) / a.group, head = j.h * a.group + j.r0 + r - local * a.group;
+                        const int64_t token = j.t0 + local;
+                        if (j.slot < 0 && p.w.splits == 0) {
+                            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[e] *= inv;
+                            Vec<__nv_bfloat16, 4>::store(static_cast<__nv_bfloat16*>(a.o) + token * a.ldo +
+                                                             (int64_t)head * D + b * C::PART + col, x);
+                        } else {
+                            const int64_t at = j.slot < 0 ? token * a.Hq + head
+                                                          : ((int64_t)blockIdx.x * 2 + j.slot) * ROWS + r;
+                            Vec<float, 4>::store((j.slot < 0 ? p.w.row_sum : p.w.slot_sum) + at * D + b * C::PART + col, x);
+                            if (b == 0 && col == 0) (j.slot < 0 ? p.w.row_stat : p.w.slot_stat)[at] = make_float2(top, sum);
+                        }
                     }
-                stop = any_reader(!ok);
-                if (stop) break;
-#pragma unroll
-                for (int o = 0; o < OUT; ++o) {
-                    const int i = tid + o * kReaders * 32, r = i / C4, col = i % C4 * 4;
-                    if (r >= j.rows) continue;
-                    const int w0 = SETS == 2 ? r / (16 * MT) * 4 : 0, rw = SETS == 2 ? r % (16 * MT) : r;
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < SHARE; ++w) top = fmaxf(top, stats[w0 + w][rw].x);
-                    const float off = top == -INFINITY ? 0.f : top;
-                    float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int w = 0; w < SHARE; ++w) {
-                        const float2 st = stats[w0 + w][rw];
-                        const float f = ex2(st.x - off);
-                        const float4 y = *reinterpret_cast<const float4*>(
-                            join + ((w0 + w) * 16 * MT + rw) * C::PART_LD + col);
-                        sum = fmaf(st.y, f, sum);
-                        x[0] = fmaf(y.x, f, x[0]);
-                        x[1] = fmaf(y.y, f, x[1]);
-                        x[2] = fmaf(y.z, f, x[2]);
-                        x[3] = fmaf(y.w, f, x[3]);
-                    }
-                    if (!(fabsf(x[0]) + fabsf(x[1]) + fabsf(x[2]) + fabsf(x[3]) + sum < INFINITY)) {
-                        atomicOr(&bad_rows[r >> 5], 1u << (r & 31));  // the same word whatever the order
-                        continue;
-                    }
-                    const int64_t token = j.t0 + (j.r0 + r) / a.group;
-                    const int head = j.h * a.group + (j.r0 + r) % a.group;
-                    if (j.slot < 0 && p.w.splits == 0) {
-                        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] *= inv;
-                        Vec<__nv_bfloat16, 4>::store(static_cast<__nv_bfloat16*>(a.o) + token * a.ldo +
-                                                         (int64_t)head * D + b * C::PART + col, x);
-                    } else {
-                        const int64_t at = j.slot < 0 ? token * a.Hq + head
-                                                      : ((int64_t)blockIdx.x * 2 + j.slot) * p.w.rows + r;
-                        Vec<float, 4>::store((j.slot < 0 ? p.w.row_sum : p.w.slot_sum) + at * D + b * C::PART + col, x);
-                        if (b == 0 && col == 0) (j.slot < 0 ? p.w.row_stat : p.w.slot_stat)[at] = make_float2(top, sum);
-                    }
+                    any_reader(false);  // before the next part, or the next run's stats
                 }
-                any_reader(false);  // before the next columns, or the next run's stats
             }
             if (stop) {
                 *abort = 1;
                 break;
             }
             // rows that an infinity or a NaN has reached
-            const uint32_t bad[2] = {bad_rows[0], C::ROWS > 32 ? bad_rows[1] : 0};
+            const uint32_t bad[2] = {bad_rows[0], ROWS > 32 ? bad_rows[1] : 0};
             if (bad[0] | bad[1]) {
                 any_reader(false);  // all have read the words
                 if (tid == 0) bad_rows[0] = bad_rows[1] = 0;
@@ -450,11 +438,11 @@ __global__ void __launch_bounds__(kStepBlock, 1)
                     const int head = j.h * a.group + (j.r0 + r) % a.group;
                     const int32_t* pages = a.cache.table + j.n * a.cache.table_ld;
                     float x[D / 32], top, sum;
-                    const int64_t see = min(j.len + (j.r0 + r) / a.group + 1, j.most);
+                    const int see = min(j.len + (j.r0 + r) / a.group + 1, j.most);
                     const Paged cache = a.cache;
                     const int h = j.h, Hkv = a.Hkv;
                     row_again<D>(static_cast<const __nv_bfloat16*>(a.q) + token * a.ldq + (int64_t)head * D,
-                                 max((int64_t)j.from * kKeyTile, j.least), min((int64_t)j.to * kKeyTile, see), c,
+                                 max(j.from * kKeyTile, j.least), min(j.to * kKeyTile, see), c,
                                  [=](int64_t key, const __nv_bfloat16*& kp, const __nv_bfloat16*& vp) {
                                      return cached_row<D>(cache, pages, Hkv, h, key, kp, vp);
                                  }, x, top, sum);
@@ -466,7 +454,7 @@ __global__ void __launch_bounds__(kStepBlock, 1)
                                                               (int64_t)head * D + lane * (D / 32), x);
                     } else {
                         const int64_t at = j.slot < 0 ? token * a.Hq + head
-                                                      : ((int64_t)blockIdx.x * 2 + j.slot) * p.w.rows + r;
+                                                      : ((int64_t)blockIdx.x * 2 + j.slot) * ROWS + r;
                         Vec<float, D / 32>::store((j.slot < 0 ? p.w.row_sum : p.w.slot_sum) + at * D + lane * (D / 32), x);
                         if (lane == 0) (j.slot < 0 ? p.w.row_stat : p.w.slot_stat)[at] = make_float2(top, sum);
                     }
@@ -480,28 +468,27 @@ __global__ void __launch_bounds__(kStepBlock, 1)
     if (tid == 0 && abort_flag) atomicOr(p.err, kAttnError);
 }
 
-template <int D, int MT, int SETS>
+template <int D, int ROWS>
 cudaError_t launch_rows(StepParams p, cudaStream_t s) {
-    using C = StepShape<D, MT, SETS>;
-    static_assert(C::ROWS * (C::PART / 4) % (kReaders * 32) == 0 || C::ROWS * (C::PART / 4) < kReaders * 32, "join");
+    using C = StepShape<D, ROWS>;
     CUtensorMap mk, mv;
     const int64_t rows = (int64_t)p.a.cache.num_pages * p.a.Hkv << p.a.cache.page_bits;
     if (!encode_cache(&mk, p.a.cache.k, rows, D, p.box) || !encode_cache(&mv, p.a.cache.v, rows, D, p.box))
         return cudaErrorInvalidValue;
     // at every call: the attribute belongs to the context
     const cudaError_t set =
-        cudaFuncSetAttribute(step_kernel<D, MT, SETS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        cudaFuncSetAttribute(step_kernel<D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (set != cudaSuccess) return set;
     KernelTimer kt("attn_step", s);
-    step_kernel<D, MT, SETS><<<p.w.ctas, kStepBlock, C::SMEM, s>>>(p, mk, mv);
+    step_kernel<D, ROWS><<<p.w.ctas, kStepBlock, C::SMEM, s>>>(p, mk, mv);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_head(const StepParams& p, cudaStream_t s) {
-    return p.w.rows == 16   ? launch_rows<D, 1, 1>(p, s)
-           : p.w.rows == 32 ? launch_rows<D, 2, 1>(p, s)
-                            : launch_rows<D, 2, 2>(p, s);
+    return p.w.rows == 16   ? launch_rows<D, 16>(p, s)
+           : p.w.rows == 32 ? launch_rows<D, 32>(p, s)
+                            : launch_rows<D, 64>(p, s);
 }
 
 }  // namespace

@@ -40,22 +40,30 @@ struct Span {
     int row_tiles;
     int key_tiles;  // tiles of own keys
     int first;      // first of them, counted from position 0
+    int t0;         // first token
+    int len;        // tokens in the cache before the call's
+    int end;        // end of the positions that have a place in the table
     int64_t units;
 };
 
-__device__ __forceinline__ Span span_of(const AttnArgs& a, int rows_per_tile, int n) {
-    const int64_t fresh = min((int64_t)a.cu[n + 1], a.T) - max(a.cu[n], 0);
-    const int len = a.cache.lens[n];
-    Span s{0, 0, 0, 0, 0};
+// Of cu[n], cu[n + 1] and lens[n].
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int rows_per_tile, int begin, int stop, int len) {
+    Span s{0, 0, 0, 0, 0, 0, 0, 0};
+    s.t0 = max(begin, 0);
+    const int fresh = (int)min((int64_t)stop, a.T) - s.t0;
     if (fresh <= 0 || len < 0) return s;
+    s.len = len;
     // what lies behind the table's last page has no row
-    const int64_t end = min(len + fresh, (int64_t)a.cache.max_pages << a.cache.page_bits);
-    s.rows = (int)min(fresh * a.group, (int64_t)0x7fffffff);
+    s.end = (int)min((int64_t)len + fresh, (int64_t)a.cache.max_pages << a.cache.page_bits);
+    s.rows = fresh * a.group;
     s.row_tiles = (s.rows + rows_per_tile - 1) / rows_per_tile;
     s.first = a.cache.prefix_len / kKeyTile;
-    if (end > a.cache.prefix_len) s.key_tiles = (int)((end + kKeyTile - 1) / kKeyTile) - s.first;
+    if (s.end > a.cache.prefix_len) s.key_tiles = (s.end + kKeyTile - 1) / kKeyTile - s.first;
     s.units = (int64_t)s.row_tiles * s.key_tiles * a.Hkv;
     return s;
+}
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int rows_per_tile, int n) {
+    return span_of(a, rows_per_tile, a.cu[n], a.cu[n + 1], a.cache.lens[n]);
 }
 
 // The CTAs that take part: each at least `kLeast` tiles, as long as there are fewer than
@@ -117,26 +125,66 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, const StepWork& w, 
 // cta_of: the CTA whose run holds tile u.
 __device__ __forceinline__ int64_t cta_of(int64_t u, int64_t all, int64_t ctas) { return ((u + 1) * ctas - 1) / all; }
 
-// Calls job(n, span, key head, row tile, first key tile, last key tile + 1, slot) for every
-// run of key tiles of one row tile in the plan, until it says false: slot -1 where it is whole.
-template <typename F>
-__device__ __forceinline__ void walk(const AttnArgs& a, const StepWork& w, const Plan& plan, F job) {
-    int64_t u = plan.from, offset = plan.offset;
-    int n = plan.n;
-    while (u < plan.to && n < a.N) {
-        const Span s = span_of(a, w.rows, n);
-        while (u < plan.to && u < offset + s.units) {
-            const int64_t local = u - offset, tile = local / s.key_tiles;
-            const int begin = (int)(local - tile * s.key_tiles);
-            const int end = (int)min((int64_t)s.key_tiles, begin + (plan.to - u));
-            const int slot = begin == 0 && end == s.key_tiles ? -1 : begin > 0 ? 0 : 1;
-            if (!job(n, s, (int)(tile / s.row_tiles), (int)(tile % s.row_tiles), s.first + begin, s.first + end, slot))
-                return;
-            u += end - begin;
-        }
-        offset += s.units;
-        ++n;
+// One run of key tiles of one row tile.
+struct Run {
+    Span s;
+    int n, h, row_tile;
+    int from, to;  // key tiles, counted from position 0
+    int slot;      // -1: the row tile is whole; else where its partial result goes
+};
+
+// The runs of a plan one after the other.  The next sequence's numbers are asked for before
+// they are needed.
+class Runs {
+  public:
+    __device__ __forceinline__ Runs(const AttnArgs& args, const StepWork& w, const Plan& plan)
+        : a(args), rows(w.rows), u(plan.from), stop(plan.to), n(plan.n), h(0), row_tile(0), begin(0) {
+        if (u >= stop) return;
+        s = span_of(a, rows, n);
+        ask();
+        const int64_t local = u - plan.offset, tile = local / s.key_tiles;
+        begin = (int)(local - tile * s.key_tiles);
+        h = (int)(tile / s.row_tiles);
+        row_tile = (int)(tile - (int64_t)h * s.row_tiles);
     }
-}
+    __device__ __forceinline__ bool next(Run& r) {
+        if (u >= stop) return false;
+        while (h == a.Hkv || s.units == 0) {
+            if (++n >= a.N) return false;
+            s = span_of(a, rows, c0, c1, len);
+            ask();
+            h = 0;
+        }
+        r.s = s;
+        r.n = n;
+        r.h = h;
+        r.row_tile = row_tile;
+        const int end = (int)min((int64_t)s.key_tiles, begin + (stop - u));
+        r.from = s.first + begin;
+        r.to = s.first + end;
+        r.slot = begin == 0 && end == s.key_tiles ? -1 : begin > 0 ? 0 : 1;
+        u += end - begin;
+        begin = 0;
+        if (++row_tile == s.row_tiles) {
+            row_tile = 0;
+            ++h;
+        }
+        return true;
+    }
+
+  private:
+    __device__ __forceinline__ void ask() {
+        if (n + 1 >= a.N) return;
+        c0 = a.cu[n + 1];
+        c1 = a.cu[n + 2];
+        len = a.cache.lens[n + 1];
+    }
+    const AttnArgs& a;
+    int rows;
+    int64_t u, stop;
+    Span s;
+    int n, h, row_tile, begin;
+    int c0, c1, len;  // of sequence n + 1
+};
 
 }  // namespace gdr

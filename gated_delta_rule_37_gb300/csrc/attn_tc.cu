@@ -229,6 +229,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 }
             }
             const int pieces = kTile / p.box;
+            auto page_of = [&](int piece) {
+                const int64_t key = (int64_t)piece * p.box;
+                return key < a.cache.prefix_len ? a.cache.prefix[key >> a.cache.page_bits] : -1;
+            };
+            int held = 0, asked = PREFIX ? page_of(from * pieces + lane) : 0, at = -64;
             for (int it = 0; it < 2 * count && ok; ++it) {
                 const int stage = it % C::STAGES, j = from + (it >> 1);
                 if (it >= C::STAGES) ok = mbar_wait(smem_u32(&bars.empty[stage]), (it / C::STAGES - 1) & 1, abort);
@@ -239,16 +244,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 const uint32_t mbar = smem_u32(&bars.full[stage]), dst = ring + stage * C::TILE_BYTES;
                 const CUtensorMap* map = it & 1 ? &mv : &mk;
                 if (PREFIX) {
-                    // piece `lane` of the tile; one without a page is read from the cache's first rows and masked
-                    const int64_t key = (int64_t)j * kTile + lane * p.box;
-                    int row = 0;
-                    bool gone = true;
-                    if (lane < pieces && key < a.cache.prefix_len) {
-                        const int page = a.cache.prefix[key >> a.cache.page_bits];
-                        gone = page < 0 || page >= a.cache.num_pages;
-                        if (!gone)
-                            row = (int)((((int64_t)page * a.Hkv + h) << a.cache.page_bits) + (key & (a.cache.page_size - 1)));
+                    // piece `lane` of the tile; one without a page is read from the cache's first rows and
+                    // masked.  The pages are those of 32 pieces, asked for 32 pieces ahead
+                    const int first = j * pieces;
+                    if (first + pieces > at + 32) {
+                        at = first;
+                        held = asked;
+                        asked = page_of(at + 32 + lane);
                     }
+                    const int page = __shfl_sync(0xffffffffu, held, (first - at + lane) & 31);
+                    const int64_t key = (int64_t)j * kTile + lane * p.box;
+                    bool gone = page < 0 || page >= a.cache.num_pages;
+                    const int row = gone ? 0 : (int)((((int64_t)page * a.Hkv + h) << a.cache.page_bits) +
+                                                     (key & (a.cache.page_size - 1)));
                     gone = gone && key < a.cache.prefix_len;
                     const bool part = __shfl_sync(0xffffffffu, gone, lane * 16 / p.box & 31);
                     const uint32_t out = __ballot_sync(0xffffffffu, part && lane < kTile / 16);

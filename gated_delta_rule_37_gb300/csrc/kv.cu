@@ -288,6 +288,8 @@ int check_paged(const Paged& c, int N, int Hkv, int D, int dtype) {
                               c.max_pages);
     if ((int64_t)c.num_pages * Hkv * c.page_size > 0x7fffffffLL)
         return set_last_error(GDR_ERR_UNSUPPORTED, "caches of more than 2^31 - 1 rows");
+    if ((int64_t)c.max_pages * c.page_size > 0x7fffffffLL - 256)
+        return set_last_error(GDR_ERR_UNSUPPORTED, "block_table of more than 2^31 - 257 positions");
     if (!c.k || !c.v) return set_last_error(GDR_ERR_INVALID_ARG, "null pointer argument (cache)");
     if (int rc = check_aligned16("k_cache", c.k)) return rc;
     if (int rc = check_aligned16("v_cache", c.v)) return rc;

@@ -472,7 +472,8 @@ GDR_API int gdr_rmsnorm_bwd(const void* dy, int64_t dy_stride, const void* s, in
  *   - The caches are [num_pages, Hkv, page_size, D], dense, page_size 16, 32,
  *     64, 128 or 256.  Position p of sequence n is row p % page_size of page
  *     block_table[n][p / page_size]; block_table [N, max_pages] int32 device, row
- *     stride table_stride.  A position beyond the table, or whose page number is
+ *     stride table_stride, max_pages * page_size below 2^31 - 256 and the caches
+ *     below 2^31 rows (num_pages * Hkv * page_size).  A position beyond the table, or whose page number is
  *     not in [0, num_pages), has no row: its key is not written, and not seen.
  *   - cache_lens [N] int32 device: the tokens that sequence n had in the cache
  *     before this call's; both calls of a step take the same numbers.  A value

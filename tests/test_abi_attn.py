@@ -43,6 +43,7 @@ PAGED = [
     (dict(table=None), INVALID), (dict(table=P(98)), INVALID), (dict(ldt=3), INVALID), (dict(mp=0), INVALID),
     (dict(lens=None), INVALID), (dict(lens=P(81)), INVALID), (dict(pages=0), INVALID), (dict(ps=8), UNSUPPORTED),
     (dict(ps=48), UNSUPPORTED), (dict(ps=512), UNSUPPORTED), (dict(pages=1 << 30), UNSUPPORTED),
+    (dict(mp=1 << 27, ldt=1 << 27), UNSUPPORTED),
 ]
 
 
