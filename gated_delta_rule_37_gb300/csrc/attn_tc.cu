@@ -16,6 +16,9 @@
 //   The maximum m that P refers to follows the row's maximum lazily: O and the sum are
 // rescaled only when the maximum has risen by more than 2^8, so P stays within 2^8 and
 // O's rescaling, a trip through registers, is rare.  m cancels in O / sum.
+//   A CTA of a prompt takes row tiles of any sequence one after the other, those with most
+// keys first; its copies run ahead into the next one's keys while the last rows of this one
+// are rescaled and written.
 //   Keys behind a sequence's last one are not another's to see: their V rows are cleared
 // in shared memory (0 * NaN is a NaN), in the last tile alone.  Within a sequence a later
 // token's infinity or NaN could still reach an earlier row as 0 * inf; a row whose result
@@ -49,13 +52,18 @@ template <int D> struct Shape {
     static constexpr int BLOCKS = D / 64;                  // 128-byte column blocks of a row
     static constexpr int BLOCK_BYTES = kTile * 128;
     static constexpr int TILE_BYTES = BLOCKS * BLOCK_BYTES;
-    static constexpr int STAGES = D == 128 ? 5 : 8;
-    static constexpr int SMEM = 1024 + (2 + STAGES) * TILE_BYTES;
+    static constexpr int STAGES = D == 128 ? 4 : 8;
+    static constexpr int OUT_BYTES = 32 * 128;             // 128 bytes of a warp's rows on their way out
+    static constexpr int SMEM = 1024 + (2 + STAGES) * TILE_BYTES + 8 * OUT_BYTES;
     static constexpr uint32_t S = 0, O = 256;              // tensor memory columns: S of both row tiles, O of both
 };
 
+// Of each row tile: q, queries there; q_free, read for the last time; s, S there; p, P there;
+// o, O there; o_free, O read.  Of the ring: full, empty, and fixed: values behind the end are
+// cleared.  Of the jobs: job, job_free.  The copies may be two jobs ahead of the MMAs, so what
+// they tell of a job's last tile belongs to its stage, which waits to be read.
 struct Barriers {
-    uint64_t q[2], full[8], empty[8], s[2], p[2], o[2], fixed, drain;
+    uint64_t q[2], q_free[2], full[8], empty[8], s[2], p[2], o[2], o_free[2], job[2], job_free[2], fixed[8], drain;
 };
 
 struct TcParams {
@@ -63,6 +71,7 @@ struct TcParams {
     StepWork w;
     int tokens;  // of a row tile: 128 / group
     int box;     // rows of one copy of keys: 128, or a page's
+    int places;  // prompt: row tile pairs of a key head, empty ones among them
     unsigned* err;
 };
 
@@ -97,15 +106,44 @@ __device__ __forceinline__ void tmem_put32(uint32_t addr, const uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// What a CTA works on.
+// Two row tiles' work; n < 0: there is no more.
 struct Job {
-    int64_t t0;       // first token of its rows' sequence (prompt), or 0
-    int64_t i0;       // its first token, counted from t0
+    int64_t t0;       // first token of their sequence (prompt), or 0
+    int64_t i0;       // their first token, counted from t0
     int64_t end;      // tokens of the sequence, or of the batch
     int from, to[2];  // key tiles of the two row tiles: from .. to - 1
     int keys;         // end of the keys, counted from the sequence's first
-    int n;
+    int n, h;
 };
+
+// The pair of row tiles at a place of a prompt's call, by a warp.  Sequence n's places begin at
+// cu[n] / (tokens of a pair) + n, which leaves room for its last, partly filled one and is found
+// by search; false where the place is empty.
+__device__ __forceinline__ bool find_job(const AttnArgs& a, int pair_tokens, int64_t place, int h, Job& job) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = a.N - 1;
+    while (hi > lo) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = lo + (lane + 1) * step;
+        const bool below = at <= hi && max(a.cu[at], 0) / pair_tokens + (int64_t)at <= place;
+        lo += __popc(__ballot_sync(0xffffffffu, below)) * step;
+        hi = min(lo + step - 1, hi);
+    }
+    const int t0 = max(a.cu[lo], 0);
+    const int64_t L = min((int64_t)a.cu[lo + 1], a.T) - t0;
+    job.i0 = (place - lo - t0 / pair_tokens) * pair_tokens;
+    if (job.i0 < 0 || job.i0 >= L) return false;
+    const int64_t i1 = job.i0 + pair_tokens / 2;
+    job.t0 = t0;
+    job.end = L;
+    job.from = 0;
+    job.to[0] = (int)((min(i1, L) + kTile - 1) / kTile);
+    job.to[1] = i1 < L ? (int)((min(job.i0 + pair_tokens, L) + kTile - 1) / kTile) : 0;
+    job.keys = (int)min(job.i0 + pair_tokens, L);
+    job.n = lo;
+    job.h = h;
+    return true;
+}
 
 template <int D, bool PREFIX>
 __global__ void __launch_bounds__(kWarps * 32, 1)
@@ -114,32 +152,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     using C = Shape<D>;
     extern __shared__ unsigned char raw[];
     __shared__ Barriers bars;
-    __shared__ Job job;
+    __shared__ Job jobs[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ int limits[PREFIX ? 2 * kTile : 1];            // per token of the CTA: end of the keys that it sees
     __shared__ uint32_t missing[PREFIX ? 16 : 1];             // per key tile: a bit per 16 keys without a page
     const AttnArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = a.group;
-    const int h = PREFIX ? blockIdx.y : blockIdx.x % a.Hkv;
     volatile int* abort = &abort_flag;
 
-    // ---- what to do ----
     if (PREFIX) {
+        // every sequence marks its tokens that the CTA has; a prefix's CTA has one job
         const int64_t first = (int64_t)blockIdx.x * 2 * p.tokens;
-        const int tiles = (a.cache.prefix_len + kTile - 1) / kTile;
-        if (tid == 0) {
-            job.t0 = 0;
-            job.i0 = first;
-            job.end = a.T;
-            job.from = (int)((int64_t)tiles * blockIdx.z / p.w.splits);
-            job.to[0] = (int)((int64_t)tiles * (blockIdx.z + 1) / p.w.splits);
-            job.to[1] = first + p.tokens < a.T ? job.to[0] : job.from;
-            job.keys = a.cache.prefix_len;
-        }
         for (int i = tid; i < 2 * kTile; i += kWarps * 32) limits[i] = 0;
         __syncthreads();
-        // every sequence marks its tokens that the CTA has
         for (int n = tid; n < a.N; n += kWarps * 32) {
             const int len = a.cache.lens[n];
             const int64_t lo = a.cu[n], hi = min((int64_t)a.cu[n + 1], a.T);
@@ -147,59 +173,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             for (int64_t t = max(lo, first); t < min(hi, first + 2 * p.tokens); ++t)
                 limits[t - first] = (int)min((int64_t)a.cache.prefix_len, len + (t - lo) + 1);
         }
-    } else {
-        if (tid == 0) job.n = -1;
-        __syncthreads();
-        if (warp == 0) {
-            // the CTAs of all sequences in a row, the last first: their rows see most keys
-            int64_t left = gridDim.x / a.Hkv - 1 - blockIdx.x / a.Hkv;
-            for (int base = 0; base < a.N && left >= 0; base += 32) {
-                const int n = base + lane;
-                int64_t t0 = 0, L = 0, count = 0;
-                if (n < a.N) {
-                    t0 = max(a.cu[n], 0);
-                    L = min((int64_t)a.cu[n + 1], a.T) - t0;
-                    count = L > 0 ? (L + 2 * p.tokens - 1) / (2 * p.tokens) : 0;
-                }
-                int64_t upto = count;
-#pragma unroll
-                for (int off = 1; off < 32; off *= 2) {
-                    const int64_t u = __shfl_up_sync(0xffffffffu, upto, off);
-                    if (lane >= off) upto += u;
-                }
-                if (left < upto && left >= upto - count) {
-                    job.t0 = t0;
-                    job.i0 = (left - (upto - count)) * 2 * p.tokens;
-                    job.end = L;
-                    job.from = 0;
-                    const int64_t i1 = job.i0 + p.tokens;
-                    job.to[0] = (int)((min(i1, L) + kTile - 1) / kTile);
-                    job.to[1] = i1 < L ? (int)((min(i1 + p.tokens, L) + kTile - 1) / kTile) : 0;
-                    job.keys = (int)min(job.i0 + 2 * p.tokens, L);
-                    job.n = n;
-                }
-                const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
-                left = left < all ? -1 : left - all;
-            }
-        }
-        __syncthreads();
-        if (job.n < 0) return;
     }
-
-    // ---- barriers, tensor memory ----
     const uint32_t q_smem = (smem_u32(raw) + 1023) & ~1023u, ring = q_smem + 2 * C::TILE_BYTES;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bars.q[i]), 1);
+            mbar_init(smem_u32(&bars.q_free[i]), 1);
             mbar_init(smem_u32(&bars.s[i]), 1);
             mbar_init(smem_u32(&bars.p[i]), 4);
             mbar_init(smem_u32(&bars.o[i]), 1);
+            mbar_init(smem_u32(&bars.o_free[i]), 4);
+            mbar_init(smem_u32(&bars.job[i]), 1);
+            mbar_init(smem_u32(&bars.job_free[i]), 9);  // the MMAs' thread and eight warps
         }
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(smem_u32(&bars.full[i]), 1);
             mbar_init(smem_u32(&bars.empty[i]), 1);
+            mbar_init(smem_u32(&bars.fixed[i]), 1);
         }
-        mbar_init(smem_u32(&bars.fixed), 1);
         mbar_init(smem_u32(&bars.drain), 1);
         mbar_fence_init();
         abort_flag = 0;
@@ -209,107 +200,147 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_slot;
-    const int from = job.from, to0 = job.to[0], to1 = job.to[1], to = max(to0, to1), count = to - from;
-    const bool tail = job.keys < to * kTile;  // the last tile has rows that are not the sequence's
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
         if (warp == 8) {
             // ---- copies ----
-            int issued = 0;
+            int it = 0, count = 0, q_uses[2] = {0, 0};  // tiles of the ring and jobs so far
             bool ok = true;
-            if (lane == 0) {
-                for (int t = 0; t < 2; ++t) {
-                    if ((t ? to1 : to0) <= from) continue;
-                    const uint32_t mbar = smem_u32(&bars.q[t]);
-                    mbar_arrive_tx(mbar, C::BLOCKS * p.tokens * group * 128);
-                    for (int b = 0; b < C::BLOCKS; ++b)
-                        tma_3d(q_smem + t * C::TILE_BYTES + b * C::BLOCK_BYTES, &mq, b * 64, h * group,
-                               (int)(job.t0 + job.i0 + t * p.tokens), mbar);
-                }
-            }
             const int pieces = kTile / p.box;
             auto page_of = [&](int piece) {
                 const int64_t key = (int64_t)piece * p.box;
                 return key < a.cache.prefix_len ? a.cache.prefix[key >> a.cache.page_bits] : -1;
             };
-            int held = 0, asked = PREFIX ? page_of(from * pieces + lane) : 0, at = -64;
-            for (int it = 0; it < 2 * count && ok; ++it) {
-                const int stage = it % C::STAGES, j = from + (it >> 1);
-                if (it >= C::STAGES) ok = mbar_wait(smem_u32(&bars.empty[stage]), (it / C::STAGES - 1) & 1, abort);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t mbar = smem_u32(&bars.full[stage]), dst = ring + stage * C::TILE_BYTES;
-                const CUtensorMap* map = it & 1 ? &mv : &mk;
+            const int64_t all = PREFIX ? 1 : (int64_t)p.places * a.Hkv;
+            for (int64_t round = 0; ok; ++round) {
+                // CTAs in turn from the first to the last and back, heavy places first
+                const int64_t place = PREFIX ? round
+                    : round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                if (round * gridDim.x >= all && !(PREFIX && round == 0)) break;
+                Job job;
                 if (PREFIX) {
-                    // piece `lane` of the tile; one without a page is read from the cache's first rows and
-                    // masked.  The pages are those of 32 pieces, asked for 32 pieces ahead
-                    const int first = j * pieces;
-                    if (first + pieces > at + 32) {
-                        at = first;
-                        held = asked;
-                        asked = page_of(at + 32 + lane);
-                    }
-                    const int page = __shfl_sync(0xffffffffu, held, (first - at + lane) & 31);
-                    const int64_t key = (int64_t)j * kTile + lane * p.box;
-                    bool gone = page < 0 || page >= a.cache.num_pages;
-                    const int row = gone ? 0 : (int)((((int64_t)page * a.Hkv + h) << a.cache.page_bits) +
-                                                     (key & (a.cache.page_size - 1)));
-                    gone = gone && key < a.cache.prefix_len;
-                    const bool part = __shfl_sync(0xffffffffu, gone, lane * 16 / p.box & 31);
-                    const uint32_t out = __ballot_sync(0xffffffffu, part && lane < kTile / 16);
-                    if (lane == 0) {
-                        // the ring holds 4 key tiles at most, and the MMAs are one ahead of the softmax
-                        if (!(it & 1)) missing[(it >> 1) & 15] = out;
-                        mbar_arrive_tx(mbar, C::TILE_BYTES);
-                    }
-                    __syncwarp();
-                    if (lane < pieces)
-                        for (int b = 0; b < C::BLOCKS; ++b)
-                            tma_2d(dst + b * C::BLOCK_BYTES + lane * p.box * 128, map, b * 64, row, mbar);
-                } else if (lane == 0) {
-                    mbar_arrive_tx(mbar, C::TILE_BYTES);
-                    for (int b = 0; b < C::BLOCKS; ++b)
-                        tma_3d(dst + b * C::BLOCK_BYTES, map, b * 64, h, (int)(job.t0 + (int64_t)j * kTile), mbar);
+                    if (round > 0) break;
+                    const int64_t first = (int64_t)blockIdx.x * 2 * p.tokens;
+                    const int tiles = (a.cache.prefix_len + kTile - 1) / kTile;
+                    job.t0 = 0;
+                    job.i0 = first;
+                    job.end = a.T;
+                    job.from = (int)((int64_t)tiles * blockIdx.z / p.w.splits);
+                    job.to[0] = (int)((int64_t)tiles * (blockIdx.z + 1) / p.w.splits);
+                    job.to[1] = first + p.tokens < a.T ? job.to[0] : job.from;
+                    job.keys = a.cache.prefix_len;
+                    job.n = 0;
+                    job.h = blockIdx.y;
+                } else if (place >= all || !find_job(a, 2 * p.tokens, p.places - 1 - place / a.Hkv, (int)(place % a.Hkv), job)) {
+                    continue;
                 }
-                issued = it + 1;
-            }
-            if (ok && tail) {
-                // the last tile's values behind the end
-                const int it = 2 * count - 1, stage = it % C::STAGES, first = job.keys - (to - 1) * kTile;
-                ok = mbar_wait_copies(smem_u32(&bars.full[stage]), (it / C::STAGES) & 1);
-                if (ok) {
+                const int b = count & 1;
+                if (count >= 2) ok = mbar_wait(smem_u32(&bars.job_free[b]), (count / 2 - 1) & 1, abort);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                if (lane == 0) {
+                    jobs[b] = job;
+                    mbar_arrive(smem_u32(&bars.job[b]));
+                }
+                ++count;
+                const int from = job.from, to = max(job.to[0], job.to[1]), tiles = to - from, begin = it;
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (job.to[t] <= from) continue;
+                    if (q_uses[t]) ok = mbar_wait(smem_u32(&bars.q_free[t]), (q_uses[t] - 1) & 1, abort);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    ++q_uses[t];
+                    if (lane == 0) {
+                        const uint32_t mbar = smem_u32(&bars.q[t]);
+                        mbar_arrive_tx(mbar, C::BLOCKS * p.tokens * group * 128);
+                        for (int c = 0; c < C::BLOCKS; ++c)
+                            tma_3d(q_smem + t * C::TILE_BYTES + c * C::BLOCK_BYTES, &mq, c * 64, job.h * group,
+                                   (int)(job.t0 + job.i0 + t * p.tokens), mbar);
+                    }
+                }
+                int held = 0, asked = PREFIX ? page_of(from * pieces + lane) : 0, at = -64;
+                for (; it < begin + 2 * tiles && ok; ++it) {
+                    const int stage = it % C::STAGES, j = from + ((it - begin) >> 1);
+                    const bool value = (it - begin) & 1;
+                    if (it >= C::STAGES) ok = mbar_wait(smem_u32(&bars.empty[stage]), (it / C::STAGES - 1) & 1, abort);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    const uint32_t mbar = smem_u32(&bars.full[stage]), dst = ring + stage * C::TILE_BYTES;
+                    const CUtensorMap* map = value ? &mv : &mk;
+                    if (PREFIX) {
+                        // piece `lane` of the tile; one without a page is read from the cache's first rows and
+                        // masked.  The pages are those of 32 pieces, asked for 32 pieces ahead
+                        const int first = j * pieces;
+                        if (first + pieces > at + 32) {
+                            at = first;
+                            held = asked;
+                            asked = page_of(at + 32 + lane);
+                        }
+                        const int page = __shfl_sync(0xffffffffu, held, (first - at + lane) & 31);
+                        const int64_t key = (int64_t)j * kTile + lane * p.box;
+                        bool gone = page < 0 || page >= a.cache.num_pages;
+                        const int row = gone ? 0 : (int)((((int64_t)page * a.Hkv + job.h) << a.cache.page_bits) +
+                                                         (key & (a.cache.page_size - 1)));
+                        gone = gone && key < a.cache.prefix_len;
+                        const bool part = __shfl_sync(0xffffffffu, gone, lane * 16 / p.box & 31);
+                        const uint32_t out = __ballot_sync(0xffffffffu, part && lane < kTile / 16);
+                        if (lane == 0) {
+                            // the ring holds 4 key tiles at most, and the MMAs are one ahead of the softmax
+                            if (!value) missing[(j - from) & 15] = out;
+                            mbar_arrive_tx(mbar, C::TILE_BYTES);
+                        }
+                        __syncwarp();
+                        if (lane < pieces)
+                            for (int c = 0; c < C::BLOCKS; ++c)
+                                tma_2d(dst + c * C::BLOCK_BYTES + lane * p.box * 128, map, c * 64, row, mbar);
+                    } else if (lane == 0) {
+                        mbar_arrive_tx(mbar, C::TILE_BYTES);
+                        for (int c = 0; c < C::BLOCKS; ++c)
+                            tma_3d(dst + c * C::BLOCK_BYTES, map, c * 64, job.h, (int)(job.t0 + (int64_t)j * kTile), mbar);
+                    }
+                }
+                if (ok && job.keys < to * kTile) {
+                    // the last tile's values behind the end
+                    const int last = it - 1, stage = last % C::STAGES, first = job.keys - (to - 1) * kTile;
+                    ok = mbar_wait_copies(smem_u32(&bars.full[stage]), (last / C::STAGES) & 1);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     unsigned char* v = raw + (ring + stage * C::TILE_BYTES - smem_u32(raw));
                     for (int i = first * 8 + lane; i < kTile * 8; i += 32)
-                        for (int b = 0; b < C::BLOCKS; ++b)
-                            *reinterpret_cast<uint4*>(v + b * C::BLOCK_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
+                        for (int c = 0; c < C::BLOCKS; ++c)
+                            *reinterpret_cast<uint4*>(v + c * C::BLOCK_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&bars.fixed));
+                    if (lane == 0) mbar_arrive(smem_u32(&bars.fixed[stage]));
                 }
+            }
+            // no more jobs
+            if (ok && count >= 2) ok = mbar_wait(smem_u32(&bars.job_free[count & 1]), (count / 2 - 1) & 1, abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && lane == 0) {
+                jobs[count & 1].n = -1;
+                mbar_arrive(smem_u32(&bars.job[count & 1]));
             }
             if (!ok) *abort = 1;
             // nothing may still be arriving when the CTA leaves
-            for (int it = max(0, issued - C::STAGES); it < issued; ++it)
-                if (!mbar_wait_copies(smem_u32(&bars.full[it % C::STAGES]), (it / C::STAGES) & 1)) *abort = 1;
+            for (int i = max(0, it - C::STAGES); i < it; ++i)
+                if (!mbar_wait_copies(smem_u32(&bars.full[i % C::STAGES]), (i / C::STAGES) & 1)) *abort = 1;
             for (int t = 0; t < 2; ++t)
-                if ((t ? to1 : to0) > from && !mbar_wait_copies(smem_u32(&bars.q[t]), 0)) *abort = 1;
+                if (q_uses[t] && !mbar_wait_copies(smem_u32(&bars.q[t]), (q_uses[t] - 1) & 1)) *abort = 1;
         } else if (warp == 9) {
             // ---- MMAs ----
             if (lane == 0) {
                 constexpr uint32_t idesc_s = idesc_bf16(kTile, kTile, false, false);
                 constexpr uint32_t idesc_o = idesc_bf16(kTile, D, false, true);
-                auto wait = [&](uint64_t* bar, int parity) {
-                    const bool ok = mbar_spin(smem_u32(bar), parity & 1, abort);
-                    if (!ok) *abort = 1;
+                bool ok = true;
+                auto wait = [&](uint64_t* bar, int phase) {
+                    if (ok && !mbar_spin(smem_u32(bar), phase & 1, abort)) {
+                        ok = false;
+                        *abort = 1;
+                    }
                     return ok;
                 };
                 auto scores = [&](int t, int stage) {
                     const uint64_t q = smem_desc(q_smem + t * C::TILE_BYTES, 16, 1024, kSwizzle128);
                     const uint64_t k = smem_desc(ring + stage * C::TILE_BYTES, 16, 1024, kSwizzle128);
-    #pragma unroll
+#pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
                         const uint32_t off = (ks >> 2) * (C::BLOCK_BYTES / 16) + (ks & 3) * 2;
                         mma_bf16(tmem + C::S + t * kTile, q + off, k + off, idesc_s, ks > 0);
@@ -318,47 +349,61 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 };
                 auto values = [&](int t, int stage, bool first) {
                     const uint64_t v = smem_desc(ring + stage * C::TILE_BYTES, C::BLOCK_BYTES, 1024, kSwizzle128);
-    #pragma unroll
+#pragma unroll
                     for (int ks = 0; ks < kTile / 16; ++ks)
                         mma_bf16_ta(tmem + C::O + t * D, tmem + C::S + t * kTile + ks * 8, v + ks * 128, idesc_o,
                                     !(first && ks == 0));
                 };
-                bool ok = count == 0 || wait(&bars.full[0], 0);
-                for (int t = 0; t < 2 && ok; ++t)
-                    if ((t ? to1 : to0) > from) {
-                        ok = wait(&bars.q[t], 0);
-                        if (ok) {
+                int begin = 0, q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+                uint32_t fixes = 0;  // a bit per stage: the phase of its `fixed`
+                for (int count = 0; ok; ++count) {
+                    if (!wait(&bars.job[count & 1], count / 2)) break;
+                    const int n = jobs[count & 1].n, from = jobs[count & 1].from, keys = jobs[count & 1].keys;
+                    const int ends[2] = {jobs[count & 1].to[0], jobs[count & 1].to[1]};
+                    mbar_arrive(smem_u32(&bars.job_free[count & 1]));
+                    if (n < 0) break;
+                    const int to = max(ends[0], ends[1]), tiles = to - from;
+                    const bool tail = keys < to * kTile;
+                    if (!wait(&bars.full[begin % C::STAGES], begin / C::STAGES)) break;
+                    for (int t = 0; t < 2; ++t)
+                        if (ends[t] > from && wait(&bars.q[t], q_uses[t])) {
                             fence_after();
-                            scores(t, 0);
+                            scores(t, begin % C::STAGES);
+                            if (ends[t] == from + 1) mma_commit(smem_u32(&bars.q_free[t]));
                         }
-                    }
-                if (ok && count) mma_commit(smem_u32(&bars.empty[0]));
-                for (int i = 0; i < count && ok; ++i) {
-                    const int iv = 2 * i + 1, ik = 2 * i + 2, j = from + i;
-                    ok = wait(&bars.full[iv % C::STAGES], iv / C::STAGES);
-                    if (ok && i == count - 1 && tail) ok = wait(&bars.fixed, 0);
-                    bool have_k = false;
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        const int end = t ? to1 : to0;
-                        if (j >= end) continue;
-                        ok = wait(&bars.p[t], i);
+                    mma_commit(smem_u32(&bars.empty[begin % C::STAGES]));
+                    for (int i = 0; i < tiles && ok; ++i) {
+                        const int iv = begin + 2 * i + 1, ik = iv + 1, j = from + i;
+                        if (!wait(&bars.full[iv % C::STAGES], iv / C::STAGES)) break;
+                        if (i == tiles - 1 && tail) {
+                            const int stage = iv % C::STAGES;
+                            if (!wait(&bars.fixed[stage], fixes >> stage)) break;
+                            fixes ^= 1u << stage;
+                        }
+                        bool have_k = false;
+                        for (int t = 0; t < 2; ++t) {
+                            if (j >= ends[t]) continue;
+                            // O of the job before is read before it is written again
+                            if (i == 0 && q_uses[t] > 0 && !wait(&bars.o_free[t], q_uses[t] - 1)) break;
+                            if (!wait(&bars.p[t], p_uses[t]++)) break;
+                            fence_after();
+                            values(t, iv % C::STAGES, i == 0);
+                            if (j + 1 < ends[t]) {
+                                if (!have_k && !wait(&bars.full[ik % C::STAGES], ik / C::STAGES)) break;
+                                have_k = true;
+                                fence_after();
+                                scores(t, ik % C::STAGES);
+                                if (j + 2 == ends[t]) mma_commit(smem_u32(&bars.q_free[t]));
+                            } else {
+                                mma_commit(smem_u32(&bars.o[t]));
+                            }
+                        }
                         if (!ok) break;
-                        fence_after();
-                        values(t, iv % C::STAGES, i == 0);
-                        if (j + 1 < end) {
-                            if (!have_k) ok = wait(&bars.full[ik % C::STAGES], ik / C::STAGES);
-                            if (!ok) break;
-                            have_k = true;
-                            fence_after();
-                            scores(t, ik % C::STAGES);
-                        } else {
-                            mma_commit(smem_u32(&bars.o[t]));
-                        }
-                    }
-                    if (ok) {
                         mma_commit(smem_u32(&bars.empty[iv % C::STAGES]));
                         if (have_k) mma_commit(smem_u32(&bars.empty[ik % C::STAGES]));
                     }
+                    begin += 2 * tiles;
+                    for (int t = 0; t < 2; ++t) q_uses[t] += ends[t] > from;
                 }
                 // no MMA may still be running when tensor memory is given back
                 mma_commit(smem_u32(&bars.drain));
@@ -369,133 +414,158 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
         // ---- softmax: a row per thread ----
-        const int t = warp >> 2, row = tid & 127, end = t ? to1 : to0;
+        const int t = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane 32 (warp % 4) in the upper half
         const uint32_t ts = tmem + C::S + t * kTile + lanes, to_ = tmem + C::O + t * D + lanes;
-        const int local = row / group + t * p.tokens;                // token within the CTA
-        const int64_t token = job.i0 + local;                        // within the sequence
-        const bool there = row < p.tokens * group && token < job.end;
-        const int limit = !there ? 0x7fffffff : PREFIX ? limits[local] : (int)token + 1;
+        const int local = row / group + t * p.tokens;       // token within the CTA
         const float c = a.scale_log2;
-        float m = -INFINITY;
-        float2 sum = make_float2(0.f, 0.f);
-        bool ok = true;
-        for (int j = from, i = 0; j < end; ++j, ++i) {
-            ok = mbar_wait(smem_u32(&bars.s[t]), i & 1, abort);
-            ok = __all_sync(0xffffffffu, ok);
+        unsigned char* const out = raw + (ring + C::STAGES * C::TILE_BYTES - smem_u32(raw)) + warp * C::OUT_BYTES;
+        int s_uses = 0, o_uses = 0;
+        for (int count = 0;; ++count) {
+            bool ok = mbar_wait(smem_u32(&bars.job[count & 1]), (count / 2) & 1, abort);
+            if (!(ok = __all_sync(0xffffffffu, ok))) {
+                *abort = 1;
+                break;
+            }
+            const Job& job = jobs[count & 1];
+            const int n = job.n, from = job.from, end = job.to[t], h = job.h;
+            const int64_t token = job.i0 + local, t0 = job.t0;  // within the sequence
+            bool there = row < p.tokens * group && token < job.end;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.job_free[count & 1]));
+            if (n < 0) break;
+            if (end <= from) continue;
+            if (PREFIX) there = there && limits[local] > 0;     // padding has no row to leave
+            const int limit = !there ? 0x7fffffff : PREFIX ? limits[local] : (int)token + 1;
+            float m = -INFINITY;
+            float2 sum = make_float2(0.f, 0.f);
+            for (int j = from, i = 0; j < end; ++j, ++i) {
+                ok = mbar_wait(smem_u32(&bars.s[t]), s_uses++ & 1, abort);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                fence_after();
+                float s[kTile];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) tmem_fetch32(ts + b * 32, s + b * 32);
+                tmem_wait_ld();
+#pragma unroll
+                for (int b = 0; b < 4; ++b) arrived32(s + b * 32);
+                const int seen = limit - j * kTile;
+                if (__any_sync(0xffffffffu, seen < kTile)) {
+#pragma unroll
+                    for (int k = 0; k < kTile; ++k)
+                        if (k >= seen) s[k] = -INFINITY;
+                }
+                if (PREFIX) {
+                    const uint32_t gone = missing[i & 15];
+                    if (gone) {
+#pragma unroll
+                        for (int k = 0; k < kTile; ++k)
+                            if (gone >> (k / 16) & 1) s[k] = -INFINITY;
+                    }
+                }
+                float top = s[0];
+#pragma unroll
+                for (int k = 1; k < kTile; ++k) top = fmaxf(top, s[k]);
+                top *= c;
+                if (__any_sync(0xffffffffu, top > m + kLag)) {
+                    // to the new maximum where it has risen, by 1 where it has not
+                    const float now = fmaxf(top, m), back = now == -INFINITY ? 1.f : ex2(m - now);
+                    m = now;
+                    sum.x *= back;
+                    sum.y *= back;
+                    if (i > 0) {
+#pragma unroll
+                        for (int b = 0; b < D; b += 32) {
+                            float o[32];
+                            tmem_fetch32(to_ + b, o);
+                            tmem_wait_ld();
+                            arrived32(o);
+                            uint32_t u[32];
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(o[k] * back);
+                            tmem_put32(to_ + b, u);
+                        }
+                    }
+                }
+                const float base = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float2 x = __ffma2_rn(make_float2(s[b * 64 + 2 * k], s[b * 64 + 2 * k + 1]),
+                                                    make_float2(c, c), make_float2(base, base));
+                        const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                        sum = __fadd2_rn(sum, e);
+                        pk[k] = pack_bf16(e.x, e.y);
+                    }
+                    tmem_put32(ts + b * 32, pk);
+                }
+                tmem_wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars.p[t]));
+            }
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.o[t]), o_uses++ & 1, abort));
             if (!ok) {
                 *abort = 1;
                 break;
             }
             fence_after();
-            float s[kTile];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) tmem_fetch32(ts + b * 32, s + b * 32);
-            tmem_wait_ld();
-#pragma unroll
-            for (int b = 0; b < 4; ++b) arrived32(s + b * 32);
-            const int seen = limit - j * kTile;
-            if (__any_sync(0xffffffffu, seen < kTile)) {
-#pragma unroll
-                for (int k = 0; k < kTile; ++k)
-                    if (k >= seen) s[k] = -INFINITY;
-            }
-            if (PREFIX) {
-                const uint32_t gone = missing[i & 15];
-                if (gone) {
-#pragma unroll
-                    for (int k = 0; k < kTile; ++k)
-                        if (gone >> (k / 16) & 1) s[k] = -INFINITY;
-                }
-            }
-            float top = s[0];
-#pragma unroll
-            for (int k = 1; k < kTile; ++k) top = fmaxf(top, s[k]);
-            top *= c;
-            if (__any_sync(0xffffffffu, top > m + kLag)) {
-                // to the new maximum where it has risen, by 1 where it has not
-                const float now = fmaxf(top, m), back = now == -INFINITY ? 1.f : ex2(m - now);
-                m = now;
-                sum.x *= back;
-                sum.y *= back;
-                if (i > 0) {
-#pragma unroll
-                    for (int b = 0; b < D; b += 32) {
-                        float o[32];
-                        tmem_fetch32(to_ + b, o);
-                        tmem_wait_ld();
-                        arrived32(o);
-                        uint32_t u[32];
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(o[k] * back);
-                        tmem_put32(to_ + b, u);
-                    }
-                }
-            }
-            const float base = m == -INFINITY ? 0.f : -m;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const float2 x = __ffma2_rn(make_float2(s[b * 64 + 2 * k], s[b * 64 + 2 * k + 1]),
-                                                make_float2(c, c), make_float2(base, base));
-                    const float2 e = make_float2(ex2(x.x), ex2(x.y));
-                    sum = __fadd2_rn(sum, e);
-                    pk[k] = pack_bf16(e.x, e.y);
-                }
-                tmem_put32(ts + b * 32, pk);
-            }
-            tmem_wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars.p[t]));
-        }
-        if (end > from && ok) {
-            ok = mbar_wait(smem_u32(&bars.o[t]), 0, abort);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) *abort = 1;
-        }
-        if (end > from && ok) {
-            fence_after();
-            float l = sum.x + sum.y;
-            float o[D];
-#pragma unroll
-            for (int b = 0; b < D; b += 32) tmem_fetch32(to_ + b, o + b);
-            tmem_wait_ld();
-#pragma unroll
-            for (int b = 0; b < D; b += 32) arrived32(o + b);
-            const int64_t at = job.t0 + token;
+            const float l = sum.x + sum.y, inv = 1.f / l;
             const int64_t head = (int64_t)h * group + row % group;
-            float any = 0.f;
+            const int64_t place = ((int64_t)blockIdx.z * a.T + t0 + token) * a.Hq + head;  // PREFIX
+            char* to_row = PREFIX ? reinterpret_cast<char*>(p.w.far_sum + place * D)
+                                  : reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(a.o) + (t0 + token) * a.ldo + head * D);
+            float any = 0.f;  // stays 0 but for an infinity or a NaN
+            // a warp's rows through shared memory, 128 bytes of each at a time: what leaves are whole lines
+            constexpr int COLS = PREFIX ? 32 : 64;
 #pragma unroll
-            for (int k = 0; k < D; ++k) any = fmaf(o[k], 0.f, any);  // 0 but for an infinity or a NaN
-            const bool finite = any == 0.f && l < INFINITY && (PREFIX || l > 0.f);
-            const int64_t place = ((int64_t)blockIdx.z * a.T + at) * a.Hq + head;  // PREFIX
-            if (there && finite) {
-                if (PREFIX) {
-                    float* to_sum = p.w.far_sum + place * D;
+            for (int b = 0; b < D; b += COLS) {
+                uint32_t w[32];
 #pragma unroll
-                    for (int k = 0; k < D; k += 4) Vec<float, 4>::store(to_sum + k, o + k);
-                    p.w.far_stat[place] = make_float2(m, l);
-                } else {
-                    const float inv = 1.f / l;
-                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + at * a.ldo + head * D;
+                for (int e = 0; e < COLS; e += 32) {
+                    float o[32];
+                    tmem_fetch32(to_ + b + e, o);
+                    tmem_wait_ld();
+                    arrived32(o);
 #pragma unroll
-                    for (int k = 0; k < D; k += 8) {
-                        uint4 u;
-                        u.x = pack_bf16(o[k] * inv, o[k + 1] * inv);
-                        u.y = pack_bf16(o[k + 2] * inv, o[k + 3] * inv);
-                        u.z = pack_bf16(o[k + 4] * inv, o[k + 5] * inv);
-                        u.w = pack_bf16(o[k + 6] * inv, o[k + 7] * inv);
-                        *reinterpret_cast<uint4*>(out + k) = u;
+                    for (int k = 0; k < 32; ++k) any = fmaf(o[k], 0.f, any);
+                    if (PREFIX) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(o[k]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) w[(e / 2 + k) & 31] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
                     }
                 }
+                if (b + COLS == D) {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars.o_free[t]));
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<uint4*>(out + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                        make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int r = k * 4 + (lane >> 3), ch = lane & 7;
+                    char* to_it = reinterpret_cast<char*>(
+                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(there ? to_row : nullptr), r));
+                    if (to_it)
+                        *reinterpret_cast<uint4*>(to_it + b * (PREFIX ? 4 : 2) + ch * 16) =
+                            *reinterpret_cast<const uint4*>(out + r * 128 + ((ch ^ (r & 7)) << 4));
+                }
+                __syncwarp();
             }
+            if (PREFIX && there) p.w.far_stat[place] = make_float2(m, l);
+            const bool finite = any == 0.f && l < INFINITY && (PREFIX || l > 0.f);
             // rows that an infinity or a NaN has reached, one after the other
             for (uint32_t bad = __ballot_sync(0xffffffffu, there && !finite); bad; bad &= bad - 1) {
                 const int who = __ffs(bad) - 1;
-                const int64_t at_w = __shfl_sync(0xffffffffu, at, who), head_w = __shfl_sync(0xffffffffu, head, who);
+                const int64_t at_w = __shfl_sync(0xffffffffu, t0 + token, who), head_w = __shfl_sync(0xffffffffu, head, who);
                 const int64_t place_w = __shfl_sync(0xffffffffu, place, who);
                 const int limit_w = __shfl_sync(0xffffffffu, limit, who);
                 float acc[D / 32], mw, lw;
@@ -503,8 +573,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 const Paged cache = a.cache;
                 const int Hkv = a.Hkv;
                 const int64_t ldk = a.ldk, ldv = a.ldv;
-                const __nv_bfloat16* keys = static_cast<const __nv_bfloat16*>(a.k) + job.t0 * ldk + (int64_t)h * D;
-                const __nv_bfloat16* vals = static_cast<const __nv_bfloat16*>(a.v) + job.t0 * ldv + (int64_t)h * D;
+                const __nv_bfloat16* keys = static_cast<const __nv_bfloat16*>(a.k) + t0 * ldk + (int64_t)h * D;
+                const __nv_bfloat16* vals = static_cast<const __nv_bfloat16*>(a.v) + t0 * ldv + (int64_t)h * D;
                 row_again<D>(static_cast<const __nv_bfloat16*>(a.q) + at_w * a.ldq + head_w * D, (int64_t)from * kTile,
                              min(limit_w, end * kTile), c,
                              [=](int64_t key, const __nv_bfloat16*& kp, const __nv_bfloat16*& vp) {
@@ -517,9 +587,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     Vec<float, D / 32>::store(p.w.far_sum + place_w * D + lane * (D / 32), acc);
                     if (lane == 0) p.w.far_stat[place_w] = make_float2(mw, lw);
                 } else {
-                    const float inv = lw > 0.f ? 1.f / lw : lw == 0.f ? 0.f : lw;
+                    const float by = lw > 0.f ? 1.f / lw : lw == 0.f ? 0.f : lw;
 #pragma unroll
-                    for (int k = 0; k < D / 32; ++k) acc[k] *= inv;
+                    for (int k = 0; k < D / 32; ++k) acc[k] *= by;
                     Vec<__nv_bfloat16, D / 32>::store(static_cast<__nv_bfloat16*>(a.o) + at_w * a.ldo + head_w * D +
                                                           lane * (D / 32), acc);
                 }
@@ -574,9 +644,9 @@ cudaError_t launch_prompt_tc(const AttnArgs& a, cudaStream_t s) {
         !encode_tokens(&mk, a.k, a.ldk, a.T, a.Hkv, a.D, 1, kTile) ||
         !encode_tokens(&mv, a.v, a.ldv, a.T, a.Hkv, a.D, 1, kTile))
         return cudaErrorInvalidValue;
-    // a sequence's last CTA may be in part empty: one more for each
-    const int64_t tiles = a.T / (2 * p.tokens) + (a.N < a.T ? a.N : a.T);
-    const dim3 grid((unsigned)(tiles * a.Hkv));
+    p.places = (int)(a.T / (2 * p.tokens) + a.N);
+    const int64_t all = (int64_t)p.places * a.Hkv;
+    const dim3 grid((unsigned)(all < kSms ? all : kSms));
     return a.D == 128 ? launch_tc<128, false>(p, grid, mq, mk, mv, s) : launch_tc<64, false>(p, grid, mq, mk, mv, s);
 }
 

@@ -37,6 +37,24 @@ def test_prompt_matches_oracle(lengths, Hq, Hkv, D, dtype):
     assert bits_equal(o, gdr.attn_fwd(q, k, v, cu))
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(14, 2), (8, 8), (64, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_many_short_sequences(Hq, Hkv, D):
+    """Many times more row tiles than the GPU has CTAs, of one to five key tiles: whole problems fit into the copies'
+    ring, which is then ahead by more than one."""
+    lengths = [(37 * i) % 150 + 1 if i % 9 else 600 - i for i in range(400)]
+    T, cu = sum(lengths), starts(lengths)
+    q, k, v = normal(1, T, Hq, D, dtype=BF16, std=2.0), normal(2, T, Hkv, D, dtype=BF16), normal(3, T, Hkv, D, dtype=BF16)
+    o = gdr.attn_fwd(q, k, v, cu)
+    assert gdr.device_status() == 0
+    for n in range(0, 400, 13):
+        part = slice(sum(lengths[:n]), sum(lengths[:n + 1]))
+        check_attention(o[part], _reference(q[part], k[part], v[part], starts(lengths[n:n + 1])), lengths[n], str(n))
+    for _ in range(5):
+        assert bits_equal(o, gdr.attn_fwd(q, k, v, cu))
+    assert gdr.device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_prompt_rows_behind_and_strides(dtype):
     """Column blocks of one projection, rows behind the last sequence (of NaN), redzones, a scale of its own."""
