@@ -16,9 +16,12 @@
 //   The maximum m that P refers to follows the row's maximum lazily: O and the sum are
 // rescaled only when the maximum has risen by more than 2^8, so P stays within 2^8 and
 // O's rescaling, a trip through registers, is rare.  m cancels in O / sum.
-//   A CTA of a prompt takes row tiles of any sequence one after the other, those with most
-// keys first; its copies run ahead into the next one's keys while the last rows of this one
-// are rescaled and written.
+//   A CTA of a prompt takes row tiles of any sequence one after the other; its copies run
+// ahead into the next one's keys while the last rows of this one are rescaled and written.
+// The grid has a place for every pair of row tiles: a CTA that is done asks the hardware for
+// a CTA that has not started yet and takes its place, so whoever is free goes on, without a
+// counter in memory.  Places are in the order of their keys, most first, for up to 64
+// sequences; with more there are enough of them for any order.
 //   Keys behind a sequence's last one are not another's to see: their V rows are cleared
 // in shared memory (0 * NaN is a NaN), in the last tile alone.  Within a sequence a later
 // token's infinity or NaN could still reach an earlier row as 0 * inf; a row whose result
@@ -41,7 +44,7 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = 128;                // rows of a query tile, keys of a key tile
-constexpr int kWarps = 12;                // 2 x 4 of softmax; the copies', the MMAs' and two that only leave
+constexpr int kWarps = 12;                // 2 x 4 of softmax; copies, MMAs, values behind the end, places
 // Registers: a softmax thread keeps a row of S.  The block is launched with 168 a thread,
 // 3 x 168 for a thread of each warpgroup; the third one's go to the others.
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -60,10 +63,13 @@ template <int D> struct Shape {
 
 // Of each row tile: q, queries there; q_free, read for the last time; s, S there; p, P there;
 // o, O there; o_free, O read.  Of the ring: full, empty, and fixed: values behind the end are
-// cleared.  Of the jobs: job, job_free.  The copies may be two jobs ahead of the MMAs, so what
-// they tell of a job's last tile belongs to its stage, which waits to be read.
+// cleared (of a stage: the copies may be jobs ahead of the MMAs, but a stage waits to be
+// read).  Of the jobs: job, job_free; asked, its last copies are on their way (before, a wait
+// for a stage could take the phase before for that one); ahead, the copies are at its last
+// tiles; place, the answer where to go on is there.
 struct Barriers {
-    uint64_t q[2], q_free[2], full[8], empty[8], s[2], p[2], o[2], o_free[2], job[2], job_free[2], fixed[8], drain;
+    uint64_t q[2], q_free[2], full[8], empty[8], s[2], p[2], o[2], o_free[2], job[2], job_free[2], fixed[8], asked[2], ahead,
+        place, drain;
 };
 
 struct TcParams {
@@ -71,7 +77,6 @@ struct TcParams {
     StepWork w;
     int tokens;  // of a row tile: 128 / group
     int box;     // rows of one copy of keys: 128, or a page's
-    int places;  // prompt: row tile pairs of a key head, empty ones among them
     unsigned* err;
 };
 
@@ -114,35 +119,90 @@ struct Job {
     int from, to[2];  // key tiles of the two row tiles: from .. to - 1
     int keys;         // end of the keys, counted from the sequence's first
     int n, h;
+    bool clear;       // values behind the end are in the last tile
 };
 
-// The pair of row tiles at a place of a prompt's call, by a warp.  Sequence n's places begin at
-// cu[n] / (tokens of a pair) + n, which leaves room for its last, partly filled one and is found
-// by search; false where the place is empty.
-__device__ __forceinline__ bool find_job(const AttnArgs& a, int pair_tokens, int64_t place, int h, Job& job) {
+// Pairs of row tiles of sequence n.
+__device__ __forceinline__ int pairs_of(const AttnArgs& a, int pair_tokens, int n) {
+    if (n >= a.N) return 0;
+    const int64_t L = min((int64_t)a.cu[n + 1], a.T) - max(a.cu[n], 0);
+    return L > 0 ? (int)((L + pair_tokens - 1) / pair_tokens) : 0;
+}
+
+constexpr int kSorted = 64;  // sequences, two of a lane
+
+// The pair of row tiles at a place of a prompt's call, by a warp; false where the place is
+// empty.  Up to kSorted sequences (pairs: those of sequences lane and lane + 32): first all
+// pairs number p, of sequences that have so many, then all number p - 1.  More sequences: the
+// last one first; sequence n's places begin at cu[n] / (tokens of a pair) + n, which leaves
+// room for its last, partly filled one and is found by search.
+__device__ __forceinline__ bool find_job(const AttnArgs& a, int pair_tokens, const int (&pairs)[2], int64_t place,
+                                         int64_t places, int h, Job& job) {
     const int lane = threadIdx.x & 31;
-    int lo = 0, hi = a.N - 1;
-    while (hi > lo) {
-        const int step = (hi - lo + 31) / 32;
-        const int at = lo + (lane + 1) * step;
-        const bool below = at <= hi && max(a.cu[at], 0) / pair_tokens + (int64_t)at <= place;
-        lo += __popc(__ballot_sync(0xffffffffu, below)) * step;
-        hi = min(lo + step - 1, hi);
+    int n, pair;
+    if (a.N <= kSorted) {
+        // pairs numbered p and above
+        auto above = [&](int p) {
+            return __reduce_add_sync(0xffffffffu, (unsigned)(max(0, pairs[0] - p) + max(0, pairs[1] - p)));
+        };
+        if (place >= above(0)) return false;
+        int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, (unsigned)max(pairs[0], pairs[1]));
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (above(mid) > place) lo = mid; else hi = mid;
+        }
+        pair = lo;
+        const int rank = (int)(place - above(lo + 1));
+        const uint32_t has[2] = {__ballot_sync(0xffffffffu, pairs[0] > lo), __ballot_sync(0xffffffffu, pairs[1] > lo)};
+        const int in_first = __popc(has[0]);
+        n = rank < in_first ? (int)__fns(has[0], 0, rank + 1) : 32 + (int)__fns(has[1], 0, rank - in_first + 1);
+    } else {
+        place = places - 1 - place;
+        int lo = 0, hi = a.N - 1;
+        while (hi > lo) {
+            const int step = (hi - lo + 31) / 32;
+            const int at = lo + (lane + 1) * step;
+            const bool below = at <= hi && max(a.cu[at], 0) / pair_tokens + (int64_t)at <= place;
+            lo += __popc(__ballot_sync(0xffffffffu, below)) * step;
+            hi = min(lo + step - 1, hi);
+        }
+        n = lo;
+        const int64_t at = place - n - max(a.cu[n], 0) / pair_tokens;
+        if (at < 0 || at >= pairs_of(a, pair_tokens, n)) return false;
+        pair = (int)at;
     }
-    const int t0 = max(a.cu[lo], 0);
-    const int64_t L = min((int64_t)a.cu[lo + 1], a.T) - t0;
-    job.i0 = (place - lo - t0 / pair_tokens) * pair_tokens;
-    if (job.i0 < 0 || job.i0 >= L) return false;
+    job.t0 = max(a.cu[n], 0);
+    const int64_t L = min((int64_t)a.cu[n + 1], a.T) - job.t0;
+    job.i0 = (int64_t)pair * pair_tokens;
     const int64_t i1 = job.i0 + pair_tokens / 2;
-    job.t0 = t0;
     job.end = L;
     job.from = 0;
     job.to[0] = (int)((min(i1, L) + kTile - 1) / kTile);
     job.to[1] = i1 < L ? (int)((min(job.i0 + pair_tokens, L) + kTile - 1) / kTile) : 0;
     job.keys = (int)min(job.i0 + pair_tokens, L);
-    job.n = lo;
+    job.n = n;
     job.h = h;
+    // what lies behind within the sequence is left to the rows that it spoils
+    job.clear = job.keys == L && job.keys % kTile != 0;
     return true;
+}
+
+// Asks for a CTA of this grid that has not started, to take its place; the answer, 16 bytes,
+// arrives on the barrier.
+__device__ __forceinline__ void ask_place(uint32_t answer, uint32_t mbar) {
+    mbar_arrive_tx(mbar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 :: "r"(answer), "r"(mbar) : "memory");
+}
+// Its number, -1 where there was none.
+__device__ __forceinline__ int read_place(uint32_t answer) {
+    int x;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\tld.shared.b128 r, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tmov.b32 %0, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}\n"
+        : "=r"(x) : "r"(answer) : "memory");
+    return x;
 }
 
 template <int D, bool PREFIX>
@@ -153,6 +213,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     extern __shared__ unsigned char raw[];
     __shared__ Barriers bars;
     __shared__ Job jobs[2];
+    __shared__ __align__(16) unsigned char answer[16];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ int limits[PREFIX ? 2 * kTile : 1];            // per token of the CTA: end of the keys that it sees
@@ -184,13 +245,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             mbar_init(smem_u32(&bars.o[i]), 1);
             mbar_init(smem_u32(&bars.o_free[i]), 4);
             mbar_init(smem_u32(&bars.job[i]), 1);
-            mbar_init(smem_u32(&bars.job_free[i]), 9);  // the MMAs' thread and eight warps
+            mbar_init(smem_u32(&bars.asked[i]), 1);
+            mbar_init(smem_u32(&bars.job_free[i]), 11);  // the MMAs' thread and ten warps
         }
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(smem_u32(&bars.full[i]), 1);
             mbar_init(smem_u32(&bars.empty[i]), 1);
             mbar_init(smem_u32(&bars.fixed[i]), 1);
         }
+        mbar_init(smem_u32(&bars.ahead), 1);
+        mbar_init(smem_u32(&bars.place), 1);
         mbar_init(smem_u32(&bars.drain), 1);
         mbar_fence_init();
         abort_flag = 0;
@@ -212,37 +276,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 const int64_t key = (int64_t)piece * p.box;
                 return key < a.cache.prefix_len ? a.cache.prefix[key >> a.cache.page_bits] : -1;
             };
-            const int64_t all = PREFIX ? 1 : (int64_t)p.places * a.Hkv;
-            for (int64_t round = 0; ok; ++round) {
-                // CTAs in turn from the first to the last and back, heavy places first
-                const int64_t place = PREFIX ? round
-                    : round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-                if (round * gridDim.x >= all && !(PREFIX && round == 0)) break;
-                Job job;
-                if (PREFIX) {
-                    if (round > 0) break;
-                    const int64_t first = (int64_t)blockIdx.x * 2 * p.tokens;
-                    const int tiles = (a.cache.prefix_len + kTile - 1) / kTile;
-                    job.t0 = 0;
-                    job.i0 = first;
-                    job.end = a.T;
-                    job.from = (int)((int64_t)tiles * blockIdx.z / p.w.splits);
-                    job.to[0] = (int)((int64_t)tiles * (blockIdx.z + 1) / p.w.splits);
-                    job.to[1] = first + p.tokens < a.T ? job.to[0] : job.from;
-                    job.keys = a.cache.prefix_len;
-                    job.n = 0;
-                    job.h = blockIdx.y;
-                } else if (place >= all || !find_job(a, 2 * p.tokens, p.places - 1 - place / a.Hkv, (int)(place % a.Hkv), job)) {
-                    continue;
-                }
-                const int b = count & 1;
-                if (count >= 2) ok = mbar_wait(smem_u32(&bars.job_free[b]), (count / 2 - 1) & 1, abort);
+            for (;; ++count) {
+                ok = mbar_wait(smem_u32(&bars.job[count & 1]), (count / 2) & 1, abort);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                if (lane == 0) {
-                    jobs[b] = job;
-                    mbar_arrive(smem_u32(&bars.job[b]));
-                }
-                ++count;
+                const Job job = jobs[count & 1];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars.job_free[count & 1]));
+                if (job.n < 0) break;
                 const int from = job.from, to = max(job.to[0], job.to[1]), tiles = to - from, begin = it;
                 for (int t = 0; t < 2 && ok; ++t) {
                     if (job.to[t] <= from) continue;
@@ -259,6 +299,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 }
                 int held = 0, asked = PREFIX ? page_of(from * pieces + lane) : 0, at = -64;
                 for (; it < begin + 2 * tiles && ok; ++it) {
+                    // with a ring of tiles left to load the next place is looked for
+                    if (lane == 0 && it == max(begin, begin + 2 * tiles - C::STAGES)) mbar_arrive(smem_u32(&bars.ahead));
                     const int stage = it % C::STAGES, j = from + ((it - begin) >> 1);
                     const bool value = (it - begin) & 1;
                     if (it >= C::STAGES) ok = mbar_wait(smem_u32(&bars.empty[stage]), (it / C::STAGES - 1) & 1, abort);
@@ -297,26 +339,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                             tma_3d(dst + c * C::BLOCK_BYTES, map, c * 64, job.h, (int)(job.t0 + (int64_t)j * kTile), mbar);
                     }
                 }
-                if (ok && job.keys < to * kTile) {
-                    // the last tile's values behind the end
-                    const int last = it - 1, stage = last % C::STAGES, first = job.keys - (to - 1) * kTile;
-                    ok = mbar_wait_copies(smem_u32(&bars.full[stage]), (last / C::STAGES) & 1);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    unsigned char* v = raw + (ring + stage * C::TILE_BYTES - smem_u32(raw));
-                    for (int i = first * 8 + lane; i < kTile * 8; i += 32)
-                        for (int c = 0; c < C::BLOCKS; ++c)
-                            *reinterpret_cast<uint4*>(v + c * C::BLOCK_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&bars.fixed[stage]));
-                }
-            }
-            // no more jobs
-            if (ok && count >= 2) ok = mbar_wait(smem_u32(&bars.job_free[count & 1]), (count / 2 - 1) & 1, abort);
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok && lane == 0) {
-                jobs[count & 1].n = -1;
-                mbar_arrive(smem_u32(&bars.job[count & 1]));
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(smem_u32(&bars.asked[count & 1]));
             }
             if (!ok) *abort = 1;
             // nothing may still be arriving when the CTA leaves
@@ -358,12 +382,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 uint32_t fixes = 0;  // a bit per stage: the phase of its `fixed`
                 for (int count = 0; ok; ++count) {
                     if (!wait(&bars.job[count & 1], count / 2)) break;
-                    const int n = jobs[count & 1].n, from = jobs[count & 1].from, keys = jobs[count & 1].keys;
+                    const int n = jobs[count & 1].n, from = jobs[count & 1].from;
+                    const bool tail = jobs[count & 1].clear;
                     const int ends[2] = {jobs[count & 1].to[0], jobs[count & 1].to[1]};
                     mbar_arrive(smem_u32(&bars.job_free[count & 1]));
                     if (n < 0) break;
                     const int to = max(ends[0], ends[1]), tiles = to - from;
-                    const bool tail = keys < to * kTile;
                     if (!wait(&bars.full[begin % C::STAGES], begin / C::STAGES)) break;
                     for (int t = 0; t < 2; ++t)
                         if (ends[t] > from && wait(&bars.q[t], q_uses[t])) {
@@ -410,6 +434,102 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 if (!mbar_wait_copies(smem_u32(&bars.drain), 0)) *abort = 1;
             }
             __syncwarp();
+        } else if (warp == 10) {
+            // ---- values behind the end ----
+            int begin = 0;
+            for (int count = 0;; ++count) {
+                const int b = count & 1;
+                auto wait = [&](uint64_t* bar, int phase) {
+                    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1, abort));
+                };
+                bool ok = wait(&bars.job[b], count / 2);
+                if (ok) {
+                    const Job& job = jobs[b];
+                    if (job.n < 0) break;
+                    const int to = max(job.to[0], job.to[1]);
+                    begin += 2 * (to - job.from);
+                    ok = wait(&bars.asked[b], count / 2);
+                    if (ok && job.clear) {
+                        const int last = begin - 1, stage = last % C::STAGES;
+                        ok = wait(&bars.full[stage], last / C::STAGES);
+                        if (ok) {
+                            unsigned char* v = raw + (ring + stage * C::TILE_BYTES - smem_u32(raw));
+                            for (int i = (job.keys - (to - 1) * kTile) * 8 + lane; i < kTile * 8; i += 32)
+                                for (int c = 0; c < C::BLOCKS; ++c)
+                                    *reinterpret_cast<uint4*>(v + c * C::BLOCK_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(&bars.fixed[stage]));
+                        }
+                    }
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive(smem_u32(&bars.job_free[b]));
+                }
+                if (!ok) {
+                    *abort = 1;
+                    break;
+                }
+            }
+        } else {
+            // ---- places ----
+            const uint32_t at_answer = smem_u32(answer);
+            const int pair_tokens = 2 * p.tokens;
+            const int64_t places = PREFIX ? 1 : gridDim.x / a.Hkv;
+            int pairs[2] = {0, 0};
+            if (!PREFIX && a.N <= kSorted) {
+                pairs[0] = pairs_of(a, pair_tokens, lane);
+                pairs[1] = pairs_of(a, pair_tokens, lane + 32);
+            }
+            bool ok = true;
+            int count = 0;
+            for (int place = blockIdx.x, asked = 0; place >= 0; ++asked) {
+                Job job;
+                bool found;
+                if (PREFIX) {
+                    const int64_t first = (int64_t)blockIdx.x * pair_tokens;
+                    const int tiles = (a.cache.prefix_len + kTile - 1) / kTile;
+                    job.t0 = 0;
+                    job.i0 = first;
+                    job.end = a.T;
+                    job.from = (int)((int64_t)tiles * blockIdx.z / p.w.splits);
+                    job.to[0] = (int)((int64_t)tiles * (blockIdx.z + 1) / p.w.splits);
+                    job.to[1] = first + p.tokens < a.T ? job.to[0] : job.from;
+                    job.keys = a.cache.prefix_len;
+                    job.n = 0;
+                    job.h = blockIdx.y;
+                    job.clear = job.keys < job.to[0] * kTile;
+                    found = true;
+                } else {
+                    found = find_job(a, pair_tokens, pairs, place / a.Hkv, places, place % a.Hkv, job);
+                }
+                if (found) {
+                    if (count >= 2) ok = mbar_wait(smem_u32(&bars.job_free[count & 1]), (count / 2 - 1) & 1, abort);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (lane == 0) {
+                        jobs[count & 1] = job;
+                        mbar_arrive(smem_u32(&bars.job[count & 1]));
+                    }
+                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.ahead), count & 1, abort));
+                    ++count;
+                    if (!ok) break;
+                }
+                if (PREFIX) break;
+                if (lane == 0) ask_place(at_answer, smem_u32(&bars.place));
+                // it arrives whatever happens to the others, and none may be on its way when the CTA leaves
+                ok = __all_sync(0xffffffffu, mbar_wait_copies(smem_u32(&bars.place), asked & 1));
+                if (!ok) break;
+                place = read_place(at_answer);
+                fence_proxy_async();  // read before the next answer is written
+                __syncwarp();
+            }
+            // no more jobs
+            if (ok && count >= 2) ok = mbar_wait(smem_u32(&bars.job_free[count & 1]), (count / 2 - 1) & 1, abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) *abort = 1;
+            if (ok && lane == 0) {
+                jobs[count & 1].n = -1;
+                mbar_arrive(smem_u32(&bars.job[count & 1]));
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
@@ -467,7 +587,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
                 for (int k = 1; k < kTile; ++k) top = fmaxf(top, s[k]);
                 top *= c;
-                if (__any_sync(0xffffffffu, top > m + kLag)) {
+                // (a lane without a row has what was left in shared memory: it does not decide)
+                if (__any_sync(0xffffffffu, there && top > m + kLag)) {
                     // to the new maximum where it has risen, by 1 where it has not
                     const float now = fmaxf(top, m), back = now == -INFINITY ? 1.f : ex2(m - now);
                     m = now;
@@ -644,9 +765,7 @@ cudaError_t launch_prompt_tc(const AttnArgs& a, cudaStream_t s) {
         !encode_tokens(&mk, a.k, a.ldk, a.T, a.Hkv, a.D, 1, kTile) ||
         !encode_tokens(&mv, a.v, a.ldv, a.T, a.Hkv, a.D, 1, kTile))
         return cudaErrorInvalidValue;
-    p.places = (int)(a.T / (2 * p.tokens) + a.N);
-    const int64_t all = (int64_t)p.places * a.Hkv;
-    const dim3 grid((unsigned)(all < kSms ? all : kSms));
+    const dim3 grid((unsigned)((a.T / (2 * p.tokens) + a.N) * a.Hkv));
     return a.D == 128 ? launch_tc<128, false>(p, grid, mq, mk, mv, s) : launch_tc<64, false>(p, grid, mq, mk, mv, s);
 }
 
