@@ -13,9 +13,12 @@
 #include "common.cuh"
 #include "gdr.h"
 #include "launch.h"
+#include "tc.cuh"
 
 namespace gdr {
 namespace {
+
+using tc::grid_dep_wait;
 
 constexpr float kNone = -INFINITY;
 
@@ -269,6 +272,7 @@ __global__ void __launch_bounds__(256) step_simt_kernel(const AttnArgs a, const 
     const Plan plan = make_plan(a, w, blockIdx.x);
     Runs runs(a, w, plan);
     for (Run run; runs.next(run);) {
+        if (threadIdx.x == 0) leave_cut(w, plan, blockIdx.x, run);
         const int64_t t0 = run.s.t0, len = run.s.len;
         const int r0 = run.row_tile * RT, rows = min(RT, run.s.rows - r0), h = run.h;
         const int64_t most = min(len + (r0 + rows - 1) / a.group + 1, (int64_t)run.s.end);
@@ -336,58 +340,112 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(const AttnArgs a, cons
 
 // ---- the merge ----------------------------------------------------------------------
 
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 128, kMergeWarps = kMergeThreads / 32;
+constexpr int kBatch = 8;  // partial results that a warp has under way
 
-// blockIdx = (sequence, key head, share of its rows); a warp per row.
+// The partial results first, first + step, ... below count of one row, by a warp: adds them up
+// relative to the maximum of all `count`.  stat_at(i), sum_at(i): where they are.
+template <int C, typename S, typename P>
+__device__ __forceinline__ void join_parts(int count, int first, int step, S stat_at, P sum_at, float (&acc)[C], float& l) {
+    const int lane = threadIdx.x & 31;
+    float top = kNone;
+    for (int i = lane; i < count; i += 32) top = fmaxf(top, stat_at(i)->x);
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = 0.f;
+    l = 0.f;
+    float base = 0.f;
+    for (int i0 = first; i0 < count; i0 += step * kBatch) {
+        float2 st[kBatch];
+        float x[kBatch][C];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = i0 + k * step;
+            st[k] = make_float2(kNone, 0.f);
+            if (i >= count) continue;
+            st[k] = *stat_at(i);
+            Vec<float, C>::load(sum_at(i) + lane * C, x[k]);
+        }
+        if (i0 == first) {  // with the first loads under way
+#pragma unroll
+            for (int off = 16; off; off /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            base = top == kNone ? 0.f : top;
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (st[k].x == kNone && st[k].y == 0.f) continue;  // saw no key: its sums are 0
+            const float f = exp2f(st[k].x - base);
+            l = fmaf(st[k].y, f, l);
+#pragma unroll
+            for (int c = 0; c < C; ++c) acc[c] = fmaf(x[k][c], f, acc[c]);
+        }
+    }
+}
+
+// Without a prefix: the row tiles that are cut, blockIdx = (CTA that has the first part, row);
+// the block's warps share the parts, of which one long sequence has many.
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads) step_merge_kernel(const AttnArgs a, const StepWork w) {
     constexpr int C = D / 32;
+    __shared__ float sums[kMergeWarps][D], ls[kMergeWarps];
+    grid_dep_wait();
+    const Cut cut = w.cuts[blockIdx.x];
+    const int r = blockIdx.y, cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (r >= cut.rows) return;
+    auto place = [&](int i) { return ((int64_t)(cta + i) * 2 + (i == 0)) * w.rows + r; };
+    float acc[C], l;
+    join_parts(cut.parts, warp, kMergeWarps, [&](int i) { return w.slot_stat + place(i); },
+               [&](int i) { return w.slot_sum + place(i) * D; }, acc, l);
+    Vec<float, C>::store(&sums[warp][lane * C], acc);
+    if (lane == 0) ls[warp] = l;
+    __syncthreads();
+    const int d = threadIdx.x * 2;
+    if (d >= D) return;
+    float x[2] = {0.f, 0.f}, y = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMergeWarps; ++i) {
+        x[0] += sums[i][d];
+        x[1] += sums[i][d + 1];
+        y += ls[i];
+    }
+    const float inv = y > 0.f ? 1.f / y : y == 0.f ? 0.f : y;
+    x[0] *= inv;
+    x[1] *= inv;
+    const int row = cut.r0 + r, local = row / a.group, head = cut.h * a.group + row - local * a.group;
+    Vec<T, 2>::store(static_cast<T*>(a.o) + (int64_t)(cut.t0 + local) * a.ldo + (int64_t)head * D + d, x);
+}
+
+// With a prefix, which every row has partial results of: blockIdx = (sequence, key head, share
+// of its rows); a warp per row.
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeThreads) step_merge_prefix_kernel(const AttnArgs a, const StepWork w) {
+    constexpr int C = D / 32;
     const int n = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31;
     const Span s = span_of(a, w.rows, n);
+    grid_dep_wait();
     const int64_t all = w.offsets[a.N], ctas = taking_part(all, w.ctas);
     const int64_t t0 = s.t0;
-    for (int r = blockIdx.z * (kMergeThreads / 32) + (threadIdx.x >> 5); r < s.rows; r += gridDim.z * (kMergeThreads / 32)) {
+    for (int r = blockIdx.z * kMergeWarps + (threadIdx.x >> 5); r < s.rows; r += gridDim.z * kMergeWarps) {
         const int64_t row = (t0 + r / a.group) * a.Hq + h * a.group + r % a.group;
         int64_t first = 0;
         int near = 0;  // partial results of the own keys
         if (s.key_tiles > 0) {
-            const int64_t u = w.offsets[n] + ((int64_t)h * s.row_tiles + r / w.rows) * s.key_tiles;
+            const int64_t u = w.offsets[n] + ((int64_t)h * s.row_tiles + r / w.rows) * (s.key_tiles + kStart) + kStart;
             first = cta_of(u, all, ctas);
             near = (int)(cta_of(u + s.key_tiles - 1, all, ctas) - first) + 1;
         }
-        if (near == 1 && w.splits == 0) continue;  // written where it was computed
-        const int count = w.splits + near;
-        auto stat_at = [&](int i) -> const float2* {
-            if (i < w.splits) return w.far_stat + i * a.T * a.Hq + row;
-            if (near == 1) return w.row_stat + row;
-            const int c = i - w.splits;
-            return w.slot_stat + ((first + c) * 2 + (c == 0)) * w.rows + r % w.rows;
-        };
-        auto sum_at = [&](int i) -> const float* {
-            if (i < w.splits) return w.far_sum + (i * a.T * a.Hq + row) * D;
-            if (near == 1) return w.row_sum + row * D;
-            const int c = i - w.splits;
-            return w.slot_sum + (((first + c) * 2 + (c == 0)) * w.rows + r % w.rows) * D;
-        };
-        float top = kNone;
-        for (int i = lane; i < count; i += 32) top = fmaxf(top, stat_at(i)->x);
-#pragma unroll
-        for (int off = 16; off; off /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const float base = top == kNone ? 0.f : top;
-        float l = 0.f, acc[C];
-#pragma unroll
-        for (int c = 0; c < C; ++c) acc[c] = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < count; ++i) {
-            const float2 st = *stat_at(i);
-            float x[C];
-            Vec<float, C>::load(sum_at(i) + lane * C, x);
-            if (st.x == kNone && st.y == 0.f) continue;  // saw no key: its sums are 0
-            const float f = exp2f(st.x - base);
-            l = fmaf(st.y, f, l);
-#pragma unroll
-            for (int c = 0; c < C; ++c) acc[c] = fmaf(x[c], f, acc[c]);
-        }
+        auto slot = [&](int c) { return ((first + c) * 2 + (c == 0)) * w.rows + r % w.rows; };
+        float acc[C], l;
+        join_parts(w.splits + near, 0, 1,
+                   [&](int i) -> const float2* {
+                       return i < w.splits ? w.far_stat + i * a.T * a.Hq + row
+                              : near == 1  ? w.row_stat + row
+                                           : w.slot_stat + slot(i - w.splits);
+                   },
+                   [&](int i) -> const float* {
+                       return i < w.splits ? w.far_sum + (i * a.T * a.Hq + row) * D
+                              : near == 1  ? w.row_sum + row * D
+                                           : w.slot_sum + slot(i - w.splits) * D;
+                   }, acc, l);
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
 #pragma unroll
         for (int c = 0; c < C; ++c) acc[c] *= inv;
@@ -441,11 +499,13 @@ cudaError_t launch_step_simt(const AttnArgs& a, const StepWork& w, cudaStream_t 
 
 template <typename T, int D>
 cudaError_t launch_merge(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
-    const int64_t rows = (a.T + a.N - 1) / a.N * a.group;  // of a sequence and key head, on average
-    const int64_t shares = (rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
     KernelTimer kt("attn_step_merge", s);
-    step_merge_kernel<T, D><<<dim3(a.N, a.Hkv, (unsigned)(shares < 64 ? shares : 64)), kMergeThreads, 0, s>>>(a, w);
-    return cudaGetLastError();
+    if (w.splits == 0)
+        return launch_dependent(step_merge_kernel<T, D>, dim3(w.ctas, w.rows), dim3(kMergeThreads), 0, s, a, w);
+    const int64_t rows = (a.T + a.N - 1) / a.N * a.group;  // of a sequence and key head, on average
+    const int64_t shares = (rows + kMergeWarps - 1) / kMergeWarps;
+    return launch_dependent(step_merge_prefix_kernel<T, D>, dim3(a.N, a.Hkv, (unsigned)(shares < 64 ? shares : 64)),
+                            dim3(kMergeThreads), 0, s, a, w);
 }
 
 // Rows per tile of the own keys' part, by the rows that a sequence has on average: a
@@ -482,6 +542,7 @@ size_t step_layout(StepWork* w, char* base, int N, int64_t T, int Hq, int Hkv, i
     w->splits = prefix_splits(T, Hkv, Hq / Hkv, w->rows, prefix_len, dtype);
     const size_t slots = (size_t)w->ctas * 2 * w->rows, rows = w->splits ? (size_t)T * Hq : 0;
     w->offsets = reinterpret_cast<int64_t*>(part(sizeof(int64_t) * ((size_t)N + 1)));
+    w->cuts = reinterpret_cast<Cut*>(part(sizeof(Cut) * w->ctas));
     w->slot_stat = reinterpret_cast<float2*>(part(sizeof(float2) * slots));
     w->slot_sum = reinterpret_cast<float*>(part(sizeof(float) * slots * D));
     w->row_stat = reinterpret_cast<float2*>(part(sizeof(float2) * rows));

@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(kStepBlock, 1)
         abort_flag = 0;
         bad_rows[0] = bad_rows[1] = 0;
     }
+    grid_dep_launch();
     const Plan plan = make_plan(a, p.w, blockIdx.x);  // ends with a barrier of the block
 
     if (warp == kReaders) {
@@ -162,6 +163,7 @@ __global__ void __launch_bounds__(kStepBlock, 1)
                          static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(r.s.t0 + token) * a.ldq + (int64_t)head * D,
                          D * 2, smem_u32(&bars.q_full[q]));
             }
+            if (lane == 0) leave_cut(p.w, plan, blockIdx.x, r);
             ++count;
             for (int k = r.from; k < r.to; ++k, ++it) {
                 const int stage = it % C::STAGES, first = k * pieces;  // the tile's first piece
@@ -208,6 +210,8 @@ __global__ void __launch_bounds__(kStepBlock, 1)
             mbar_arrive(smem_u32(&bars.q_full[count & 1]));
         }
         if (!ok) *abort = 1;
+        // the merge waits for this grid alone, so this one ends behind the prefix's
+        grid_dep_wait();
     } else {
         // ---- arithmetic ----
         const int group = warp % C::GROUPS, share = warp / C::GROUPS;
@@ -480,6 +484,9 @@ cudaError_t launch_rows(StepParams p, cudaStream_t s) {
         cudaFuncSetAttribute(step_kernel<D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (set != cudaSuccess) return set;
     KernelTimer kt("attn_step", s);
+    // behind the prefix's kernel, which reads the same inputs and writes nothing that this one reads
+    if (p.w.splits > 0)
+        return launch_dependent(step_kernel<D, ROWS>, dim3(p.w.ctas), dim3(kStepBlock), C::SMEM, s, p, mk, mv);
     step_kernel<D, ROWS><<<p.w.ctas, kStepBlock, C::SMEM, s>>>(p, mk, mv);
     return cudaGetLastError();
 }

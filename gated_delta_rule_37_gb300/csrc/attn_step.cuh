@@ -7,10 +7,11 @@
 // that only the device knows: their key tiles are numbered (sequence, key head, row
 // tile, key tile) and every CTA takes an equal run of the numbers, so that ragged
 // batches are as balanced as even ones and one long sequence fills the GPU as well as
-// many short ones.  A row tile that lies within one CTA's run is finished there; one
-// that is cut leaves a partial result (unnormalised sums, running maximum and sum) in
-// each CTA's slots, of which a CTA needs two, for its first and its last row tile.  The
-// merge joins the partial results of a row in the order of its keys: no atomics, and
+// many short ones.  A row tile's first tile follows kStart numbers without one: what its
+// beginning and end cost, in tiles.  A row tile that lies within one CTA's run is finished
+// there; one that is cut leaves a partial result (unnormalised sums, running maximum and
+// sum) in each CTA's slots, of which a CTA needs two, for its first and its last row tile.
+// The merge joins the partial results of a row in the order of its keys: no atomics, and
 // the bits do not depend on which CTA ran first.
 #pragma once
 
@@ -24,8 +25,16 @@ constexpr int kStepThreads = 256;  // threads that form the plan (a block may ha
 constexpr int kSms = 152;
 constexpr int kMaxSplits = 64;
 
+// A row tile that begins in a CTA's run and ends in another's: rows rows from r0 on of the
+// sequence that begins at token t0, in the last slot of this CTA and the first of the
+// parts - 1 next ones.  rows 0: there is none.
+struct Cut {
+    int t0, h, r0, rows, parts;
+};
+
 struct StepWork {
-    int64_t* offsets;   // [N + 1]: number of the first tile of each sequence, and of all
+    int64_t* offsets;   // [N + 1]: first number of each sequence, and of all (with a prefix)
+    Cut* cuts;          // [ctas] (without)
     float2* slot_stat;  // [ctas][2][rows]: running maximum (log2 units) and sum
     float* slot_sum;    // [ctas][2][rows][D]
     float2* row_stat;   // [T][Hq]: rows that are whole but for the prefix
@@ -34,6 +43,11 @@ struct StepWork {
     float* far_sum;     // [splits][T][Hq][D]
     int ctas, rows, splits;
 };
+
+// (Measured, decode of 230 ragged sequences of up to 1024 own keys behind a prefix of 16000,
+// all three kernels: 0: 175 us, 1: 166, 2: 158, 4: 152, 6: 154; longer or fewer sequences and
+// 64 rows do not tell them apart.)
+constexpr int kStart = 4;
 
 struct Span {
     int rows;       // rows of one key head: tokens * group
@@ -59,7 +73,7 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int rows_per_tile, in
     s.row_tiles = (s.rows + rows_per_tile - 1) / rows_per_tile;
     s.first = a.cache.prefix_len / kKeyTile;
     if (s.end > a.cache.prefix_len) s.key_tiles = (s.end + kKeyTile - 1) / kKeyTile - s.first;
-    s.units = (int64_t)s.row_tiles * s.key_tiles * a.Hkv;
+    if (s.key_tiles > 0) s.units = (int64_t)s.row_tiles * (s.key_tiles + kStart) * a.Hkv;
     return s;
 }
 __device__ __forceinline__ Span span_of(const AttnArgs& a, int rows_per_tile, int n) {
@@ -74,13 +88,15 @@ __device__ __forceinline__ int64_t taking_part(int64_t units, int ctas) {
 }
 
 struct Plan {
-    int64_t from, to;  // this CTA's tiles
-    int64_t offset;    // number of the first tile of sequence n
-    int n;             // the sequence of its first tile
+    int64_t from, to;  // this CTA's numbers
+    int64_t offset;    // first number of sequence n
+    int64_t all, ctas; // numbers, and CTAs that share them
+    int n;             // the sequence of its first number
 };
 
-// Formed by kStepThreads threads: thread i sums the tiles of a run of sequences.
-// CTA 0 leaves the sequences' numbers for the merge.  Every thread of the block calls it.
+// Formed by kStepThreads threads: thread i sums the numbers of a run of sequences.
+// CTA 0 leaves the sequences' first ones for a merge with a prefix, which goes over all
+// rows; without, the CTAs leave the row tiles that are cut.  Every thread of the block calls it.
 __device__ __forceinline__ Plan make_plan(const AttnArgs& a, const StepWork& w, int cta) {
     __shared__ int64_t warp_units[kStepThreads / 32 + 2];
     __shared__ Plan plan;
@@ -104,25 +120,29 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, const StepWork& w, 
     }
     const int64_t ctas = taking_part(all, w.ctas);
     const int64_t from = cta < ctas ? all * cta / ctas : all, to = cta < ctas ? all * (cta + 1) / ctas : all;
-    if (tid == 0) plan = Plan{from, to, 0, 0};
+    if (tid == 0) {
+        plan = Plan{from, to, 0, all, ctas, 0};
+        w.cuts[cta].rows = 0;
+    }
     __syncthreads();
     int64_t at = before;
-    if (cta == 0 || (from >= before && from < before + mine))
+    const bool leave = cta == 0 && w.splits > 0;
+    if (leave || (from >= before && from < before + mine))
         for (int n = lo; n < hi; ++n) {
             const int64_t units = span_of(a, w.rows, n).units;
             if (from >= at && from < at + units) {
                 plan.offset = at;
                 plan.n = n;
             }
-            if (cta == 0) w.offsets[n] = at;
+            if (leave) w.offsets[n] = at;
             at += units;
         }
-    if (cta == 0 && tid == 0) w.offsets[a.N] = all;
+    if (leave && tid == 0) w.offsets[a.N] = all;
     __syncthreads();
     return plan;
 }
 
-// cta_of: the CTA whose run holds tile u.
+// The CTA whose run holds number u.
 __device__ __forceinline__ int64_t cta_of(int64_t u, int64_t all, int64_t ctas) { return ((u + 1) * ctas - 1) / all; }
 
 // One run of key tiles of one row tile.
@@ -131,7 +151,15 @@ struct Run {
     int n, h, row_tile;
     int from, to;  // key tiles, counted from position 0
     int slot;      // -1: the row tile is whole; else where its partial result goes
+    int64_t last;  // number of the row tile's last key tile
 };
+
+// A run that goes on in other CTAs, for the merge; by one thread.
+__device__ __forceinline__ void leave_cut(const StepWork& w, const Plan& plan, int cta, const Run& r) {
+    if (r.slot != 1) return;
+    const int r0 = r.row_tile * w.rows;
+    w.cuts[cta] = Cut{r.s.t0, r.h, r0, min(w.rows, r.s.rows - r0), (int)(cta_of(r.last, plan.all, plan.ctas) - cta) + 1};
+}
 
 // The runs of a plan one after the other.  The next sequence's numbers are asked for before
 // they are needed.
@@ -142,34 +170,38 @@ class Runs {
         if (u >= stop) return;
         s = span_of(a, rows, n);
         ask();
-        const int64_t local = u - plan.offset, tile = local / s.key_tiles;
-        begin = (int)(local - tile * s.key_tiles);
+        const int64_t local = u - plan.offset, tile = local / (s.key_tiles + kStart);
+        begin = (int)(local - tile * (s.key_tiles + kStart));
         h = (int)(tile / s.row_tiles);
         row_tile = (int)(tile - (int64_t)h * s.row_tiles);
     }
     __device__ __forceinline__ bool next(Run& r) {
-        if (u >= stop) return false;
-        while (h == a.Hkv || s.units == 0) {
-            if (++n >= a.N) return false;
-            s = span_of(a, rows, c0, c1, len);
-            ask();
-            h = 0;
+        while (u < stop) {
+            while (h == a.Hkv || s.units == 0) {
+                if (++n >= a.N) return false;
+                s = span_of(a, rows, c0, c1, len);
+                ask();
+                h = 0;
+            }
+            const int end = (int)min((int64_t)s.key_tiles + kStart, begin + (stop - u));
+            const int from = max(begin - kStart, 0), to = max(end - kStart, 0);
+            r.s = s;
+            r.n = n;
+            r.h = h;
+            r.row_tile = row_tile;
+            r.from = s.first + from;
+            r.to = s.first + to;
+            r.slot = from == 0 && to == s.key_tiles ? -1 : from > 0 ? 0 : 1;
+            r.last = u - begin + s.key_tiles + kStart - 1;
+            u += end - begin;
+            begin = 0;
+            if (++row_tile == s.row_tiles) {
+                row_tile = 0;
+                ++h;
+            }
+            if (to > from) return true;
         }
-        r.s = s;
-        r.n = n;
-        r.h = h;
-        r.row_tile = row_tile;
-        const int end = (int)min((int64_t)s.key_tiles, begin + (stop - u));
-        r.from = s.first + begin;
-        r.to = s.first + end;
-        r.slot = begin == 0 && end == s.key_tiles ? -1 : begin > 0 ? 0 : 1;
-        u += end - begin;
-        begin = 0;
-        if (++row_tile == s.row_tiles) {
-            row_tile = 0;
-            ++h;
-        }
-        return true;
+        return false;
     }
 
   private:

@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     __shared__ uint32_t missing[PREFIX ? 16 : 1];             // per key tile: a bit per 16 keys without a page
     const AttnArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = a.group;
+    if (PREFIX) grid_dep_launch();  // the own keys' CTAs start where this grid's have left
     volatile int* abort = &abort_flag;
 
     if (PREFIX) {
