@@ -435,16 +435,17 @@ __global__ void __launch_bounds__(kMergeThreads) step_merge_prefix_kernel(const 
         }
         auto slot = [&](int c) { return ((first + c) * 2 + (c == 0)) * w.rows + r % w.rows; };
         float acc[C], l;
-        join_parts(w.splits + near, 0, 1,
+        const int far = far_parts(a, w, t0 + r / a.group, h);
+        join_parts(far + near, 0, 1,
                    [&](int i) -> const float2* {
-                       return i < w.splits ? w.far_stat + i * a.T * a.Hq + row
+                       return i < far ? w.far_stat + i * a.T * a.Hq + row
                               : near == 1  ? w.row_stat + row
-                                           : w.slot_stat + slot(i - w.splits);
+                                           : w.slot_stat + slot(i - far);
                    },
                    [&](int i) -> const float* {
-                       return i < w.splits ? w.far_sum + (i * a.T * a.Hq + row) * D
+                       return i < far ? w.far_sum + (i * a.T * a.Hq + row) * D
                               : near == 1  ? w.row_sum + row * D
-                                           : w.slot_sum + slot(i - w.splits) * D;
+                                           : w.slot_sum + slot(i - far) * D;
                    }, acc, l);
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
 #pragma unroll
@@ -516,16 +517,26 @@ int rows_per_tile(int N, int64_t T, int group, int dtype) {
 }
 
 // Cuts of the prefix along its keys: about as many CTAs as the GPU holds at once.
-int prefix_splits(int64_t T, int Hkv, int group, int rows, int prefix_len, int dtype) {
-    if (prefix_len == 0) return 0;
-    const bool tc = dtype == GDR_BF16;
-    const int64_t tokens = tc ? 2 * (128 / group) : 0;  // of a CTA
-    const int64_t tiles = (prefix_len + 127) / 128;
-    const int64_t blocks = (tc ? (T + tokens - 1) / tokens : (T * group + rows - 1) / rows) * Hkv;
-    int64_t splits = (tc ? kSms : 2 * kSms) / blocks;
+void prefix_cuts(StepWork* w, int64_t T, int Hkv, int group, int prefix_len, int dtype) {
+    w->splits = w->far_ctas = w->far_tokens = 0;
+    if (prefix_len == 0) return;
+    const int64_t tiles = (prefix_len + kFarTile - 1) / kFarTile;
+    if (dtype == GDR_BF16) {
+        w->far_tokens = prefix_block_tokens(group);
+        const int64_t blocks = (T + w->far_tokens - 1) / w->far_tokens * Hkv, all = blocks * tiles;
+        int64_t ctas = all < kSms ? all : kSms;
+        if (ctas > blocks * kMaxSplits) ctas = blocks * kMaxSplits;
+        const int64_t least = all / ctas;  // tiles of a CTA
+        const int64_t parts = (tiles + least - 1) / least + 1;
+        w->far_ctas = (int)ctas;
+        w->splits = (int)(parts < tiles ? parts : tiles);
+        return;
+    }
+    const int64_t blocks = (T * group + w->rows - 1) / w->rows * Hkv;
+    int64_t splits = 2 * kSms / blocks;
     if (splits > tiles) splits = tiles;
     if (splits < 1) splits = 1;
-    return (int)(splits < kMaxSplits ? splits : kMaxSplits);
+    w->splits = (int)(splits < kMaxSplits ? splits : kMaxSplits);
 }
 
 // The workspace's parts (from `base`; a null one for the size alone).
@@ -539,7 +550,7 @@ size_t step_layout(StepWork* w, char* base, int N, int64_t T, int Hq, int Hkv, i
     };
     w->ctas = dtype == GDR_BF16 ? kSms : 2 * kSms;
     w->rows = rows_per_tile(N, T, Hq / Hkv, dtype);
-    w->splits = prefix_splits(T, Hkv, Hq / Hkv, w->rows, prefix_len, dtype);
+    prefix_cuts(w, T, Hkv, Hq / Hkv, prefix_len, dtype);
     const size_t slots = (size_t)w->ctas * 2 * w->rows, rows = w->splits ? (size_t)T * Hq : 0;
     w->offsets = reinterpret_cast<int64_t*>(part(sizeof(int64_t) * ((size_t)N + 1)));
     w->cuts = reinterpret_cast<Cut*>(part(sizeof(Cut) * w->ctas));
@@ -553,11 +564,11 @@ size_t step_layout(StepWork* w, char* base, int N, int64_t T, int Hq, int Hkv, i
 }
 
 template <int D>
-cudaError_t launch_step(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
+cudaError_t launch_step(const AttnArgs& a, StepWork w, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     if (a.dtype == GDR_BF16) {
-        if (w.splits > 0) e = tiled(a.ldq, a.Hq, D) ? launch_prefix_tc(a, w, s)
-                                                    : launch_prefix_simt<__nv_bfloat16, D, 64>(a, w, s);
+        if (!tiled(a.ldq, a.Hq, D)) w.far_ctas = 0;
+        if (w.splits > 0) e = w.far_ctas ? launch_prefix_tc(a, w, s) : launch_prefix_simt<__nv_bfloat16, D, 64>(a, w, s);
         if (e == cudaSuccess) e = launch_step_own(a, w, s);
         return e == cudaSuccess ? launch_merge<__nv_bfloat16, D>(a, w, s) : e;
     }

@@ -47,6 +47,7 @@ struct StepWork;
 
 // Tensor-core paths (bf16).
 cudaError_t launch_prompt_tc(const AttnArgs& a, cudaStream_t s);
+int prefix_block_tokens(int group);  // tokens of a block of rows of the prefix's kernel
 cudaError_t launch_prefix_tc(const AttnArgs& a, const StepWork& w, cudaStream_t s);
 cudaError_t launch_step_own(const AttnArgs& a, const StepWork& w, cudaStream_t s);
 

@@ -2,7 +2,9 @@
 //
 // The keys of a step are the prefix's, which every row of the batch sees, and each
 // sequence's own.  The prefix is one tall problem (all tokens' rows of a key head
-// against the same keys), cut along the keys into `splits` so that it fills the GPU.
+// against the same keys), cut along the keys so that it fills the GPU: on the tensor
+// cores its (block of rows, key head, key tile) are numbered and shared out like the own
+// parts' tiles below, elsewhere every block is cut into `splits`.
 // The own parts are as many problems as there are sequences and key heads, of lengths
 // that only the device knows: their key tiles are numbered (sequence, key head, row
 // tile, key tile) and every CTA takes an equal run of the numbers, so that ragged
@@ -21,6 +23,7 @@
 namespace gdr {
 
 constexpr int kKeyTile = 64;       // keys per tile of the own parts
+constexpr int kFarTile = 128;      // keys per tile of the prefix, on the tensor cores
 constexpr int kStepThreads = 256;  // threads that form the plan (a block may have a warp or two more)
 constexpr int kSms = 152;
 constexpr int kMaxSplits = 64;
@@ -41,7 +44,9 @@ struct StepWork {
     float* row_sum;     // [T][Hq][D]
     float2* far_stat;   // [splits][T][Hq]: the prefix
     float* far_sum;     // [splits][T][Hq][D]
-    int ctas, rows, splits;
+    int ctas, rows;
+    int splits;               // partial results of a row of the prefix, at most
+    int far_ctas, far_tokens; // of the tensor cores' kernel, and tokens of a block (far_ctas 0: another kernel)
 };
 
 // (Measured, decode of 230 ragged sequences of up to 1024 own keys behind a prefix of 16000,
@@ -153,6 +158,14 @@ struct Run {
     int slot;      // -1: the row tile is whole; else where its partial result goes
     int64_t last;  // number of the row tile's last key tile
 };
+
+// The partial results that a row of `token` has of the prefix.
+__device__ __forceinline__ int far_parts(const AttnArgs& a, const StepWork& w, int64_t token, int h) {
+    if (w.far_ctas == 0) return w.splits;
+    const int64_t tiles = (a.cache.prefix_len + kFarTile - 1) / kFarTile, blocks = (a.T + w.far_tokens - 1) / w.far_tokens;
+    const int64_t all = blocks * a.Hkv * tiles, u = (token / w.far_tokens * a.Hkv + h) * tiles;
+    return (int)(cta_of(u + tiles - 1, all, w.far_ctas) - cta_of(u, all, w.far_ctas)) + 1;
+}
 
 // A run that goes on in other CTAs, for the merge; by one thread.
 __device__ __forceinline__ void leave_cut(const StepWork& w, const Plan& plan, int cta, const Run& r) {

@@ -43,12 +43,14 @@ namespace {
 
 using namespace tc;
 
+static_assert(kFarTile == 128, "the prefix's key tile");
 constexpr int kTile = 128;                // rows of a query tile, keys of a key tile
 constexpr int kWarps = 12;                // 2 x 4 of softmax; copies, MMAs, values behind the end, places
 // Registers: a softmax thread keeps a row of S.  The block is launched with 168 a thread,
 // 3 x 168 for a thread of each warpgroup; the third one's go to the others.
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "more registers than the block has");
+constexpr int kNoRow = 0x7fffffff;        // the limit of a lane without a row: it masks nothing
 constexpr float kLag = 8.f;               // how far P's reference may lag behind the maximum, log2 units
 
 template <int D> struct Shape {
@@ -66,10 +68,10 @@ template <int D> struct Shape {
 // cleared (of a stage: the copies may be jobs ahead of the MMAs, but a stage waits to be
 // read).  Of the jobs: job, job_free; asked, its last copies are on their way (before, a wait
 // for a stage could take the phase before for that one); ahead, the copies are at its last
-// tiles; place, the answer where to go on is there.
+// tiles; limits_free, the prefix's limits are read; place, the answer where to go on is there.
 struct Barriers {
     uint64_t q[2], q_free[2], full[8], empty[8], s[2], p[2], o[2], o_free[2], job[2], job_free[2], fixed[8], asked[2], ahead,
-        place, drain;
+        limits_free, place, drain;
 };
 
 struct TcParams {
@@ -79,6 +81,13 @@ struct TcParams {
     int box;     // rows of one copy of keys: 128, or a page's
     unsigned* err;
 };
+
+// One lane of a warp that is together, always the same.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t x;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}\n" : "=r"(x));
+    return x != 0;
+}
 
 // D += A B with A in tensor memory.
 __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -119,6 +128,7 @@ struct Job {
     int from, to[2];  // key tiles of the two row tiles: from .. to - 1
     int keys;         // end of the keys, counted from the sequence's first
     int n, h;
+    int part;         // of the prefix's partial results
     bool clear;       // values behind the end are in the last tile
 };
 
@@ -127,6 +137,35 @@ __device__ __forceinline__ int pairs_of(const AttnArgs& a, int pair_tokens, int 
     if (n >= a.N) return 0;
     const int64_t L = min((int64_t)a.cu[n + 1], a.T) - max(a.cu[n], 0);
     return L > 0 ? (int)((L + pair_tokens - 1) / pair_tokens) : 0;
+}
+
+// Of the tokens first .. first + tokens - 1 of a batch the end of the prefix's keys that each
+// sees, 0 for padding; by a warp.
+__device__ __forceinline__ void mark_limits(const AttnArgs& a, int64_t first, int tokens, int* limits) {
+    const int lane = threadIdx.x & 31;
+    for (int i = lane; i < tokens; i += 32) limits[i] = 0;
+    __syncwarp();
+    // the last sequence that begins at or before the first token
+    int lo = 0, hi = a.N - 1;
+    while (hi > lo) {
+        const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+        lo += __popc(__ballot_sync(0xffffffffu, at <= hi && a.cu[at] <= first)) * step;
+        hi = min(lo + step - 1, hi);
+    }
+    for (int base = lo; base < a.N; base += 32) {
+        const int n = base + lane;
+        bool behind = true;
+        if (n < a.N) {
+            const int len = a.cache.lens[n];
+            const int64_t begin = a.cu[n], end = min((int64_t)a.cu[n + 1], a.T);
+            behind = begin >= first + tokens;
+            if (len >= 0)
+                for (int64_t t = max(begin, first); t < min(end, first + tokens); ++t)
+                    limits[t - first] = (int)min((int64_t)a.cache.prefix_len, len + (t - begin) + 1);
+        }
+        if (__any_sync(0xffffffffu, behind)) break;
+    }
+    __syncwarp();
 }
 
 constexpr int kSorted = 64;  // sequences, two of a lane
@@ -216,26 +255,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     __shared__ __align__(16) unsigned char answer[16];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
-    __shared__ int limits[PREFIX ? 2 * kTile : 1];            // per token of the CTA: end of the keys that it sees
+    __shared__ int limits[PREFIX ? 2 * kTile : 1];            // per token of the job: end of the keys that it sees
     __shared__ uint32_t missing[PREFIX ? 16 : 1];             // per key tile: a bit per 16 keys without a page
     const AttnArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = a.group;
     if (PREFIX) grid_dep_launch();  // the own keys' CTAs start where this grid's have left
     volatile int* abort = &abort_flag;
 
-    if (PREFIX) {
-        // every sequence marks its tokens that the CTA has; a prefix's CTA has one job
-        const int64_t first = (int64_t)blockIdx.x * 2 * p.tokens;
-        for (int i = tid; i < 2 * kTile; i += kWarps * 32) limits[i] = 0;
-        __syncthreads();
-        for (int n = tid; n < a.N; n += kWarps * 32) {
-            const int len = a.cache.lens[n];
-            const int64_t lo = a.cu[n], hi = min((int64_t)a.cu[n + 1], a.T);
-            if (len < 0) continue;
-            for (int64_t t = max(lo, first); t < min(hi, first + 2 * p.tokens); ++t)
-                limits[t - first] = (int)min((int64_t)a.cache.prefix_len, len + (t - lo) + 1);
-        }
-    }
     const uint32_t q_smem = (smem_u32(raw) + 1023) & ~1023u, ring = q_smem + 2 * C::TILE_BYTES;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -255,6 +281,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             mbar_init(smem_u32(&bars.fixed[i]), 1);
         }
         mbar_init(smem_u32(&bars.ahead), 1);
+        mbar_init(smem_u32(&bars.limits_free), 8);
         mbar_init(smem_u32(&bars.place), 1);
         mbar_init(smem_u32(&bars.drain), 1);
         mbar_fence_init();
@@ -270,7 +297,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
         if (warp == 8) {
             // ---- copies ----
-            int it = 0, count = 0, q_uses[2] = {0, 0};  // tiles of the ring and jobs so far
+            int it = 0, count = 0, q_uses[2] = {0, 0};  // tiles of the ring (keys and values in turn) and jobs so far
             bool ok = true;
             const int pieces = kTile / p.box;
             auto page_of = [&](int piece) {
@@ -327,7 +354,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                         const uint32_t out = __ballot_sync(0xffffffffu, part && lane < kTile / 16);
                         if (lane == 0) {
                             // the ring holds 4 key tiles at most, and the MMAs are one ahead of the softmax
-                            if (!value) missing[(j - from) & 15] = out;
+                            if (!value) missing[(it >> 1) & 15] = out;
                             mbar_arrive_tx(mbar, C::TILE_BYTES);
                         }
                         __syncwarp();
@@ -351,89 +378,93 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 if (q_uses[t] && !mbar_wait_copies(smem_u32(&bars.q[t]), (q_uses[t] - 1) & 1)) *abort = 1;
         } else if (warp == 9) {
             // ---- MMAs ----
-            if (lane == 0) {
-                constexpr uint32_t idesc_s = idesc_bf16(kTile, kTile, false, false);
-                constexpr uint32_t idesc_o = idesc_bf16(kTile, D, false, true);
-                bool ok = true;
-                auto wait = [&](uint64_t* bar, int phase) {
-                    if (ok && !mbar_spin(smem_u32(bar), phase & 1, abort)) {
-                        ok = false;
-                        *abort = 1;
+            // An MMA takes its operands from uniform registers, and one that a single lane has computed
+            // costs a trip there each time, more than the MMA itself: so the whole warp walks
+            // through the jobs, with values that are the same in all lanes, and one issues.
+            constexpr uint32_t idesc_s = idesc_bf16(kTile, kTile, false, false);
+            constexpr uint32_t idesc_o = idesc_bf16(kTile, D, false, true);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint64_t q0 = smem_desc(q_smem, 16, 1024, kSwizzle128);
+            const uint64_t k0 = smem_desc(ring, 16, 1024, kSwizzle128);
+            const uint64_t v0 = smem_desc(ring, C::BLOCK_BYTES, 1024, kSwizzle128);
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, int phase) {
+                ok = __all_sync(0xffffffffu, mbar_spin(smem_u32(bar), phase & 1, abort));
+                if (!ok) *abort = 1;
+                return ok;
+            };
+            auto there = [&](int it) { return wait(&bars.full[it % C::STAGES], it / C::STAGES); };
+            auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+            auto commit = [&](uint64_t* bar) {
+                if (elect_one()) mma_commit(smem_u32(bar));
+            };
+            // of the ring's tiles so far; of each row tile: the jobs that had it, its key tiles
+            int begin = 0, uses[2] = {0, 0}, p_uses[2] = {0, 0};
+            uint32_t fixes = 0;  // a bit per stage: the phase of its `fixed`
+            for (int count = 0; ok; ++count) {
+                if (!wait(&bars.job[count & 1], count / 2)) break;
+                const Job& job = jobs[count & 1];
+                const int n = same(job.n), from = same(job.from), clear = same(job.clear);
+                const int mine[2] = {same(job.to[0]) - from, same(job.to[1]) - from};
+                if (lane == 0) mbar_arrive(smem_u32(&bars.job_free[count & 1]));
+                if (n < 0) break;
+                const int tiles = max(mine[0], mine[1]);
+                // S of key tile i follows the O += P V of the tile before
+                for (int i = 0; i <= tiles && ok; ++i) {
+                    const int ik = begin + 2 * i, iv = ik - 1;
+                    if (i > 0 && !there(iv)) break;
+                    if (i == tiles && clear) {
+                        const int stage = iv % C::STAGES;
+                        if (!wait(&bars.fixed[stage], fixes >> stage)) break;
+                        fixes ^= 1u << stage;
                     }
-                    return ok;
-                };
-                auto scores = [&](int t, int stage) {
-                    const uint64_t q = smem_desc(q_smem + t * C::TILE_BYTES, 16, 1024, kSwizzle128);
-                    const uint64_t k = smem_desc(ring + stage * C::TILE_BYTES, 16, 1024, kSwizzle128);
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t off = (ks >> 2) * (C::BLOCK_BYTES / 16) + (ks & 3) * 2;
-                        mma_bf16(tmem + C::S + t * kTile, q + off, k + off, idesc_s, ks > 0);
-                    }
-                    mma_commit(smem_u32(&bars.s[t]));
-                };
-                auto values = [&](int t, int stage, bool first) {
-                    const uint64_t v = smem_desc(ring + stage * C::TILE_BYTES, C::BLOCK_BYTES, 1024, kSwizzle128);
-#pragma unroll
-                    for (int ks = 0; ks < kTile / 16; ++ks)
-                        mma_bf16_ta(tmem + C::O + t * D, tmem + C::S + t * kTile + ks * 8, v + ks * 128, idesc_o,
-                                    !(first && ks == 0));
-                };
-                int begin = 0, q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
-                uint32_t fixes = 0;  // a bit per stage: the phase of its `fixed`
-                for (int count = 0; ok; ++count) {
-                    if (!wait(&bars.job[count & 1], count / 2)) break;
-                    const int n = jobs[count & 1].n, from = jobs[count & 1].from;
-                    const bool tail = jobs[count & 1].clear;
-                    const int ends[2] = {jobs[count & 1].to[0], jobs[count & 1].to[1]};
-                    mbar_arrive(smem_u32(&bars.job_free[count & 1]));
-                    if (n < 0) break;
-                    const int to = max(ends[0], ends[1]), tiles = to - from;
-                    if (!wait(&bars.full[begin % C::STAGES], begin / C::STAGES)) break;
-                    for (int t = 0; t < 2; ++t)
-                        if (ends[t] > from && wait(&bars.q[t], q_uses[t])) {
-                            fence_after();
-                            scores(t, begin % C::STAGES);
-                            if (ends[t] == from + 1) mma_commit(smem_u32(&bars.q_free[t]));
-                        }
-                    mma_commit(smem_u32(&bars.empty[begin % C::STAGES]));
-                    for (int i = 0; i < tiles && ok; ++i) {
-                        const int iv = begin + 2 * i + 1, ik = iv + 1, j = from + i;
-                        if (!wait(&bars.full[iv % C::STAGES], iv / C::STAGES)) break;
-                        if (i == tiles - 1 && tail) {
-                            const int stage = iv % C::STAGES;
-                            if (!wait(&bars.fixed[stage], fixes >> stage)) break;
-                            fixes ^= 1u << stage;
-                        }
-                        bool have_k = false;
-                        for (int t = 0; t < 2; ++t) {
-                            if (j >= ends[t]) continue;
-                            // O of the job before is read before it is written again
-                            if (i == 0 && q_uses[t] > 0 && !wait(&bars.o_free[t], q_uses[t] - 1)) break;
-                            if (!wait(&bars.p[t], p_uses[t]++)) break;
-                            fence_after();
-                            values(t, iv % C::STAGES, i == 0);
-                            if (j + 1 < ends[t]) {
-                                if (!have_k && !wait(&bars.full[ik % C::STAGES], ik / C::STAGES)) break;
-                                have_k = true;
-                                fence_after();
-                                scores(t, ik % C::STAGES);
-                                if (j + 2 == ends[t]) mma_commit(smem_u32(&bars.q_free[t]));
-                            } else {
-                                mma_commit(smem_u32(&bars.o[t]));
-                            }
-                        }
+                    for (int t = 0; t < 2; ++t) {
                         if (!ok) break;
-                        mma_commit(smem_u32(&bars.empty[iv % C::STAGES]));
-                        if (have_k) mma_commit(smem_u32(&bars.empty[ik % C::STAGES]));
+                        if (i > 0 && i <= mine[t]) {
+                            // O of the job before is read before it is written again
+                            if (i == 1 && uses[t] > 0 && !wait(&bars.o_free[t], uses[t] - 1)) break;
+                            if (!wait(&bars.p[t], p_uses[t] + i - 1)) break;
+                            fence_after();
+                            const uint64_t v = v0 + iv % C::STAGES * (C::TILE_BYTES / 16);
+                            if (elect_one()) {
+#pragma unroll
+                                for (int ks = 0; ks < kTile / 16; ++ks)
+                                    mma_bf16_ta(tm + C::O + t * D, tm + C::S + t * kTile + ks * 8, v + ks * 128, idesc_o,
+                                                i > 1 || ks > 0);
+                            }
+                            if (i == mine[t]) commit(&bars.o[t]);
+                        }
+                        if (i < mine[t]) {
+                            if (!there(ik)) break;
+                            if (i == 0 && !wait(&bars.q[t], uses[t])) break;
+                            fence_after();
+                            const uint64_t q = q0 + t * (C::TILE_BYTES / 16), k = k0 + ik % C::STAGES * (C::TILE_BYTES / 16);
+                            if (elect_one()) {
+#pragma unroll
+                                for (int ks = 0; ks < D / 16; ++ks) {
+                                    const uint32_t off = (ks >> 2) * (C::BLOCK_BYTES / 16) + (ks & 3) * 2;
+                                    mma_bf16(tm + C::S + t * kTile, q + off, k + off, idesc_s, ks > 0);
+                                }
+                                mma_commit(smem_u32(&bars.s[t]));
+                            }
+                            if (i + 1 == mine[t]) commit(&bars.q_free[t]);
+                        }
                     }
-                    begin += 2 * tiles;
-                    for (int t = 0; t < 2; ++t) q_uses[t] += ends[t] > from;
+                    if (!ok) break;
+                    if (i > 0) commit(&bars.empty[iv % C::STAGES]);
+                    if (i < tiles) commit(&bars.empty[ik % C::STAGES]);
                 }
-                // no MMA may still be running when tensor memory is given back
-                mma_commit(smem_u32(&bars.drain));
-                if (!mbar_wait_copies(smem_u32(&bars.drain), 0)) *abort = 1;
+                begin += 2 * tiles;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    uses[t] += mine[t] > 0;
+                    p_uses[t] += max(mine[t], 0);
+                }
             }
+            // no MMA may still be running when tensor memory is given back
+            commit(&bars.drain);
+            if (!mbar_wait_copies(smem_u32(&bars.drain), 0)) *abort = 1;
             __syncwarp();
         } else if (warp == 10) {
             // ---- values behind the end ----
@@ -481,31 +512,43 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 pairs[0] = pairs_of(a, pair_tokens, lane);
                 pairs[1] = pairs_of(a, pair_tokens, lane + 32);
             }
+            const int far_tiles = PREFIX ? (a.cache.prefix_len + kTile - 1) / kTile : 1;
+            const int64_t units = PREFIX ? (a.T + pair_tokens - 1) / pair_tokens * a.Hkv * far_tiles : 1;
+            int64_t unit = units * blockIdx.x / gridDim.x;
+            const int64_t unit_end = units * (blockIdx.x + 1) / gridDim.x;
             bool ok = true;
             int count = 0;
             for (int place = blockIdx.x, asked = 0; place >= 0; ++asked) {
                 Job job;
                 bool found;
                 if (PREFIX) {
-                    const int64_t first = (int64_t)blockIdx.x * pair_tokens;
-                    const int tiles = (a.cache.prefix_len + kTile - 1) / kTile;
+                    // the next tiles of this CTA's share, up to the end of a block of rows
+                    const int64_t block = unit / far_tiles;
+                    const int from = (int)(unit - block * far_tiles);
+                    const int to = (int)min((int64_t)far_tiles, from + unit_end - unit);
+                    const int64_t first = block / a.Hkv * pair_tokens;
                     job.t0 = 0;
                     job.i0 = first;
                     job.end = a.T;
-                    job.from = (int)((int64_t)tiles * blockIdx.z / p.w.splits);
-                    job.to[0] = (int)((int64_t)tiles * (blockIdx.z + 1) / p.w.splits);
-                    job.to[1] = first + p.tokens < a.T ? job.to[0] : job.from;
+                    job.from = from;
+                    job.to[0] = to;
+                    job.to[1] = first + p.tokens < a.T ? to : from;
                     job.keys = a.cache.prefix_len;
                     job.n = 0;
-                    job.h = blockIdx.y;
-                    job.clear = job.keys < job.to[0] * kTile;
+                    job.h = (int)(block % a.Hkv);
+                    job.part = (int)(blockIdx.x - cta_of(block * far_tiles, units, gridDim.x));
+                    job.clear = job.keys < to * kTile;
+                    unit += to - from;
                     found = true;
                 } else {
                     found = find_job(a, pair_tokens, pairs, place / a.Hkv, places, place % a.Hkv, job);
                 }
                 if (found) {
                     if (count >= 2) ok = mbar_wait(smem_u32(&bars.job_free[count & 1]), (count / 2 - 1) & 1, abort);
+                    // the limits have one place, which those of the job before have to leave
+                    if (PREFIX && ok && count >= 1) ok = mbar_wait(smem_u32(&bars.limits_free), (count - 1) & 1, abort);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (PREFIX) mark_limits(a, job.i0, pair_tokens, limits);
                     if (lane == 0) {
                         jobs[count & 1] = job;
                         mbar_arrive(smem_u32(&bars.job[count & 1]));
@@ -514,7 +557,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     ++count;
                     if (!ok) break;
                 }
-                if (PREFIX) break;
+                if (PREFIX && unit == unit_end) break;
+                if (PREFIX) continue;
                 if (lane == 0) ask_place(at_answer, smem_u32(&bars.place));
                 // it arrives whatever happens to the others, and none may be on its way when the CTA leaves
                 ok = __all_sync(0xffffffffu, mbar_wait_copies(smem_u32(&bars.place), asked & 1));
@@ -538,10 +582,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         const int t = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane 32 (warp % 4) in the upper half
         const uint32_t ts = tmem + C::S + t * kTile + lanes, to_ = tmem + C::O + t * D + lanes;
-        const int local = row / group + t * p.tokens;       // token within the CTA
         const float c = a.scale_log2;
         unsigned char* const out = raw + (ring + C::STAGES * C::TILE_BYTES - smem_u32(raw)) + warp * C::OUT_BYTES;
         int s_uses = 0, o_uses = 0;
+        int tiles_before = 0;  // key tiles of the jobs so far
         for (int count = 0;; ++count) {
             bool ok = mbar_wait(smem_u32(&bars.job[count & 1]), (count / 2) & 1, abort);
             if (!(ok = __all_sync(0xffffffffu, ok))) {
@@ -549,15 +593,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 break;
             }
             const Job& job = jobs[count & 1];
-            const int n = job.n, from = job.from, end = job.to[t], h = job.h;
-            const int64_t token = job.i0 + local, t0 = job.t0;  // within the sequence
-            bool there = row < p.tokens * group && token < job.end;
+            if (job.n < 0) break;
+            const int from = job.from, end = job.to[t], first_tile = tiles_before;
+            tiles_before += max(job.to[0], job.to[1]) - from;
+            // what the loop does not need is read once more behind it: S takes the registers
+            int limit = kNoRow;
+            if (end > from) {
+                const int local = row / group + t * p.tokens;  // token within the job
+                if (row < p.tokens * group && job.i0 + local < job.end) {
+                    limit = PREFIX ? limits[local] : (int)job.i0 + local + 1;
+                    if (PREFIX && limit == 0) limit = kNoRow;  // padding has no row to leave
+                }
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars.job_free[count & 1]));
-            if (n < 0) break;
-            if (end <= from) continue;
-            if (PREFIX) there = there && limits[local] > 0;     // padding has no row to leave
-            const int limit = !there ? 0x7fffffff : PREFIX ? limits[local] : (int)token + 1;
+            if (PREFIX && lane == 0) mbar_arrive(smem_u32(&bars.limits_free));
+            if (end <= from) {
+                if (lane == 0) mbar_arrive(smem_u32(&bars.job_free[count & 1]));
+                continue;
+            }
             float m = -INFINITY;
             float2 sum = make_float2(0.f, 0.f);
             for (int j = from, i = 0; j < end; ++j, ++i) {
@@ -567,29 +620,22 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 float s[kTile];
 #pragma unroll
                 for (int b = 0; b < 4; ++b) tmem_fetch32(ts + b * 32, s + b * 32);
+                const uint32_t gone = PREFIX ? missing[(first_tile + i) & 15] : 0;
                 tmem_wait_ld();
 #pragma unroll
                 for (int b = 0; b < 4; ++b) arrived32(s + b * 32);
                 const int seen = limit - j * kTile;
-                if (__any_sync(0xffffffffu, seen < kTile)) {
+                if (__any_sync(0xffffffffu, seen < kTile || (PREFIX && gone))) {
 #pragma unroll
                     for (int k = 0; k < kTile; ++k)
-                        if (k >= seen) s[k] = -INFINITY;
-                }
-                if (PREFIX) {
-                    const uint32_t gone = missing[i & 15];
-                    if (gone) {
-#pragma unroll
-                        for (int k = 0; k < kTile; ++k)
-                            if (gone >> (k / 16) & 1) s[k] = -INFINITY;
-                    }
+                        if (k >= seen || (PREFIX && (gone >> (k / 16) & 1))) s[k] = -INFINITY;
                 }
                 float top = s[0];
 #pragma unroll
                 for (int k = 1; k < kTile; ++k) top = fmaxf(top, s[k]);
                 top *= c;
                 // (a lane without a row has what was left in shared memory: it does not decide)
-                if (__any_sync(0xffffffffu, there && top > m + kLag)) {
+                if (__any_sync(0xffffffffu, limit != kNoRow && top > m + kLag)) {
                     // to the new maximum where it has risen, by 1 where it has not
                     const float now = fmaxf(top, m), back = now == -INFINITY ? 1.f : ex2(m - now);
                     m = now;
@@ -635,8 +681,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             }
             fence_after();
             const float l = sum.x + sum.y, inv = 1.f / l;
-            const int64_t head = (int64_t)h * group + row % group;
-            const int64_t place = ((int64_t)blockIdx.z * a.T + t0 + token) * a.Hq + head;  // PREFIX
+            const bool there = limit != kNoRow;
+            const int h = job.h, part = PREFIX ? job.part : 0, local = row / group;
+            const int64_t head = (int64_t)h * group + row - local * group;
+            const int64_t token = job.i0 + local + t * p.tokens, t0 = job.t0;  // within the sequence
+            const int64_t place = ((int64_t)part * a.T + t0 + token) * a.Hq + head;  // PREFIX
             char* to_row = PREFIX ? reinterpret_cast<char*>(p.w.far_sum + place * D)
                                   : reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(a.o) + (t0 + token) * a.ldo + head * D);
             float any = 0.f;  // stays 0 but for an infinity or a NaN
@@ -716,6 +765,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                                                           lane * (D / 32), acc);
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.job_free[count & 1]));
         }
     }
     fence_before();
@@ -754,7 +805,7 @@ cudaError_t launch_tc(TcParams p, dim3 grid, const CUtensorMap& mq, const CUtens
 
 }  // namespace
 
-int prefix_tile_tokens(int group) { return kTile / group; }
+int prefix_block_tokens(int group) { return 2 * (kTile / group); }
 
 cudaError_t launch_prompt_tc(const AttnArgs& a, cudaStream_t s) {
     TcParams p{};
@@ -781,8 +832,7 @@ cudaError_t launch_prefix_tc(const AttnArgs& a, const StepWork& w, cudaStream_t 
     if (!encode_tokens(&mq, a.q, a.ldq, a.T, a.Hq, a.D, a.group, p.tokens) ||
         !encode_cache(&mk, a.cache.k, rows, a.D, p.box) || !encode_cache(&mv, a.cache.v, rows, a.D, p.box))
         return cudaErrorInvalidValue;
-    const int64_t tiles = (a.T + 2 * p.tokens - 1) / (2 * p.tokens);
-    const dim3 grid((unsigned)tiles, a.Hkv, w.splits);
+    const dim3 grid((unsigned)w.far_ctas);
     return a.D == 128 ? launch_tc<128, true>(p, grid, mq, mk, mv, s) : launch_tc<64, true>(p, grid, mq, mk, mv, s);
 }
 
