@@ -61,9 +61,19 @@ template <> struct Pack16<__nv_bfloat16> {
     static constexpr int VEC = 8;
 };
 
-template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&f)[Pack16<T>::VEC]) {
-    Vec<T, Pack16<T>::VEC>::load(p, f);
+__device__ __forceinline__ void spread(const uint4& u, float (&f)[4]) {
+    f[0] = __uint_as_float(u.x);
+    f[1] = __uint_as_float(u.y);
+    f[2] = __uint_as_float(u.z);
+    f[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ void spread(const uint4& u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
 }
 __device__ __forceinline__ void store16(float* p, const float (&f)[4]) { Vec<float, 4>::store(p, f); }
 __device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&f)[8]) {
@@ -80,19 +90,36 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&f)[8]) {
 
 // One block per (token, share of the heads).  A thread owns two 16-byte pieces of a
 // head's row, the pieces x and x + R / 2 where those turn with one another, and walks
-// over the heads.
+// over the heads.  What it reads of its first head does not depend on the token's place,
+// which takes four trips to memory in turn: it is asked for before them, and each next
+// head's before this one is turned and written.
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
     constexpr int VEC = Pack16<T>::VEC, PIECES = D / (2 * VEC), LANES = kAppendThreads / PIECES;
     __shared__ float2 turn[D / 2];
     const int64_t t = blockIdx.x;
+    const int half = p.R / 2;
+    const int piece = threadIdx.x % PIECES, lane = threadIdx.x / PIECES + LANES * blockIdx.y;
+    const int heads = p.Hq + 2 * p.Hkv;
+    // the pieces' channels, and whether they turn with one another element by element
+    const bool across = !p.pairs && piece * VEC < half;
+    const int c0 = across ? piece * VEC : p.pairs ? piece * 2 * VEC : 2 * half + (piece - half / VEC) * 2 * VEC;
+    const int c1 = across ? c0 + half : c0 + VEC;
+    uint4 next[2];
+    auto ask = [&](int h) {
+        const T* from = h < p.Hq           ? static_cast<const T*>(p.q) + t * p.ldq + (int64_t)h * D
+                        : h < p.Hq + p.Hkv ? static_cast<const T*>(p.k) + t * p.ldk + (int64_t)(h - p.Hq) * D
+                                           : static_cast<const T*>(p.v) + t * p.ldv + (int64_t)(h - p.Hq - p.Hkv) * D;
+        next[0] = *reinterpret_cast<const uint4*>(from + c0);
+        next[1] = *reinterpret_cast<const uint4*>(from + c1);
+    };
+    if (lane < heads) ask(lane);
     if (p.cu[0] > t) return;
     const int n = find_sequence(p.cu, p.N, t);
     if (n >= p.N || t >= p.cu[n + 1]) return;  // behind the last sequence
     const int len = p.c.lens[n];
     if (len < 0) return;
     const int64_t pos = (int64_t)len + (t - p.cu[n]);
-    const int half = p.R / 2;
     for (int j = threadIdx.x; j < half; j += kAppendThreads) {
         const double turns = (double)p.freqs[j] * 0.15915494309189533577;
         const long long unit = (long long)((turns - rint(turns)) * 18446744073709551616.0);
@@ -110,31 +137,23 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
         if (page >= 0 && page < p.c.num_pages)
             row = ((int64_t)page * p.Hkv << p.c.page_bits) + (pos & (p.c.page_size - 1));
     }
-    const int piece = threadIdx.x % PIECES, lane = threadIdx.x / PIECES + LANES * blockIdx.y;
-    const int heads = p.Hq + 2 * p.Hkv;
-    // the pieces' channels, and whether they turn with one another element by element
-    const bool across = !p.pairs && piece * VEC < half;
-    const int c0 = across ? piece * VEC : p.pairs ? piece * 2 * VEC : 2 * half + (piece - half / VEC) * 2 * VEC;
-    const int c1 = across ? c0 + half : c0 + VEC;
-    for (int h = lane; h < heads; h += LANES * gridDim.y) {
-        const T* from;
+    const int step = LANES * gridDim.y;
+    for (int h = lane; h < heads; h += step) {
         T* dense = nullptr;
         T* cached = nullptr;
         if (h < p.Hq) {
-            from = static_cast<const T*>(p.q) + t * p.ldq + (int64_t)h * D;
             dense = static_cast<T*>(p.q_out) + t * p.ldqo + (int64_t)h * D;
         } else {
             const int kv = h < p.Hq + p.Hkv ? h - p.Hq : h - p.Hq - p.Hkv;
             const bool key = h < p.Hq + p.Hkv;
-            from = key ? static_cast<const T*>(p.k) + t * p.ldk + (int64_t)kv * D
-                       : static_cast<const T*>(p.v) + t * p.ldv + (int64_t)kv * D;
             if (key && p.k_out) dense = static_cast<T*>(p.k_out) + t * p.ldko + (int64_t)kv * D;
             if (row >= 0)
                 cached = static_cast<T*>(key ? p.c.k : p.c.v) + (row + ((int64_t)kv << p.c.page_bits)) * D;
         }
         float x[VEC], y[VEC];
-        load16<T>(from + c0, x);
-        load16<T>(from + c1, y);
+        spread(next[0], x);
+        spread(next[1], y);
+        if (h + step < heads) ask(h + step);
         if (h < p.Hq + p.Hkv && half > 0) {
             if (across) {
 #pragma unroll
