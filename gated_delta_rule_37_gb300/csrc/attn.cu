@@ -595,6 +595,9 @@ int check_scale(float scale) {
 int check_attention(int N, int64_t T, int Hq, int Hkv, int D, int dtype) {
     if (int rc = check_heads(N, T, Hq, Hkv, D, dtype)) return rc;
     if (Hq == 0) return set_last_error(GDR_ERR_INVALID_ARG, "Hq must be positive");
+    // (the bf16 prompt looks at N * Hkv places at least)
+    if ((int64_t)N * Hkv > 1 << 24)
+        return set_last_error(GDR_ERR_UNSUPPORTED, "N (%d) * Hkv (%d) above 2^24", N, Hkv);
     if (T * Hq > 0x7fffffffLL - 512)
         return set_last_error(GDR_ERR_UNSUPPORTED, "T_total (%lld) * Hq too large", (long long)T);
     return GDR_OK;
@@ -619,7 +622,11 @@ int gdr_attn_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_strid
     if (int rc = check_token_rows("v", v, v_stride, 0, dtype)) return rc;
     if (int rc = check_token_rows("o", o, o_stride, (int64_t)Hq * D, dtype)) return rc;
     if (int rc = check_int32s("cu_seqlens", cu_seqlens)) return rc;
-    if (o == q || o == k || o == v) return set_last_error(GDR_ERR_INVALID_ARG, "o must not be an input");
+    const int64_t e = dtype == GDR_BF16 ? 2 : 4;
+    const MemRows out{"o", o, (int64_t)Hq * D * e, o_stride * e, T_total};
+    if (int rc = check_apart(out, {"q", q, (int64_t)Hq * D * e, q_stride * e, T_total})) return rc;
+    if (int rc = check_apart(out, {"k", k, (int64_t)Hkv * D * e, k_stride * e, T_total})) return rc;
+    if (int rc = check_apart(out, {"v", v, (int64_t)Hkv * D * e, v_stride * e, T_total})) return rc;
     if (int rc = check_device()) return rc;
     cudaStream_t s = (cudaStream_t)stream;
     if (flags & GDR_VALIDATE)
@@ -630,13 +637,13 @@ int gdr_attn_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_strid
     a.cu = cu_seqlens; a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.group = Hq / Hkv; a.T = T_total;
     a.scale_log2 = scale * 1.44269504088896341f;
     a.dtype = dtype;
-    const cudaError_t e = dtype == GDR_BF16 && tiled(q_stride, Hq, D) && tiled(k_stride, Hkv, D) && tiled(v_stride, Hkv, D)
+    const cudaError_t launched = dtype == GDR_BF16 && tiled(q_stride, Hq, D) && tiled(k_stride, Hkv, D) && tiled(v_stride, Hkv, D)
                               ? launch_prompt_tc(a, s)
                           : dtype == GDR_BF16 ? (D == 128 ? launch_prompt_simt<__nv_bfloat16, 128>(a, s)
                                                           : launch_prompt_simt<__nv_bfloat16, 64>(a, s))
                                             : (D == 128 ? launch_prompt_simt<float, 128>(a, s)
                                                         : launch_prompt_simt<float, 64>(a, s));
-    return launch_result(e, "gdr_attn_fwd launch");
+    return launch_result(launched, "gdr_attn_fwd launch");
 }
 
 int gdr_attn_step_workspace_size(int N, int64_t T_total, int Hq, int Hkv, int D, int prefix_len, int dtype,
@@ -670,7 +677,6 @@ int gdr_attn_step(const void* q, int64_t q_stride, const void* k_cache, const vo
     if (int rc = check_token_rows("q", q, q_stride, 0, dtype)) return rc;
     if (int rc = check_token_rows("o", o, o_stride, (int64_t)Hq * D, dtype)) return rc;
     if (int rc = check_int32s("cu_seqlens", cu_seqlens)) return rc;
-    if (o == q || o == k_cache || o == v_cache) return set_last_error(GDR_ERR_INVALID_ARG, "o must not be an input");
     StepWork w{};
     const size_t need = step_layout(&w, static_cast<char*>(workspace), N, T_total, Hq, Hkv, D, prefix_len,
                                     dtype);
@@ -678,6 +684,16 @@ int gdr_attn_step(const void* q, int64_t q_stride, const void* k_cache, const vo
         return set_last_error(GDR_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace ? ws_bytes : (size_t)0, need);
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
         return set_last_error(GDR_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+    const int64_t e = dtype == GDR_BF16 ? 2 : 4, cache = (int64_t)num_pages * Hkv * page_size * D * e;
+    const MemRows out{"o", o, (int64_t)Hq * D * e, o_stride * e, T_total};
+    const MemRows in[3] = {{"q", q, (int64_t)Hq * D * e, q_stride * e, T_total}, {"k_cache", k_cache, cache, cache, 1},
+                           {"v_cache", v_cache, cache, cache, 1}};
+    for (const MemRows& x : in)
+        if (int rc = check_apart(out, x)) return rc;
+    const MemRows scratch{"workspace", workspace, (int64_t)need, (int64_t)need, 1};
+    if (int rc = check_apart(scratch, out)) return rc;
+    for (const MemRows& x : in)
+        if (int rc = check_apart(scratch, x)) return rc;
     if (int rc = check_device()) return rc;
     cudaStream_t s = (cudaStream_t)stream;
     if (flags & GDR_VALIDATE)
@@ -686,8 +702,8 @@ int gdr_attn_step(const void* q, int64_t q_stride, const void* k_cache, const vo
     a.cu = cu_seqlens; a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.group = Hq / Hkv; a.T = T_total;
     a.scale_log2 = scale * 1.44269504088896341f;
     a.dtype = dtype;
-    const cudaError_t e = D == 128 ? launch_step<128>(a, w, s) : launch_step<64>(a, w, s);
-    return launch_result(e, "gdr_attn_step launch");
+    const cudaError_t launched = D == 128 ? launch_step<128>(a, w, s) : launch_step<64>(a, w, s);
+    return launch_result(launched, "gdr_attn_step launch");
 }
 
 }  // extern "C"

@@ -39,6 +39,16 @@ int check_token_rows(const char* name, const void* p, int64_t stride, int64_t le
 int check_int32s(const char* name, const void* p);
 int check_paged(const Paged& c, int N, int Hkv, int D, int dtype);
 
+// Rows in memory: `rows` of them, `row` bytes each, `ld` bytes from one to the next.
+struct MemRows {
+    const char* name;
+    const void* p;
+    int64_t row, ld, rows;
+};
+// GDR_OK if what is written shares no byte with the other (column blocks of the same rows do
+// not), else a status with its message set.  A null pointer shares nothing.
+int check_apart(const MemRows& written, const MemRows& other);
+
 // GDR_VALIDATE of the layer: cu_seqlens, and where `c` is given that every page
 // that the call reaches is there.  Synchronises the stream.
 int validate_attention(const int32_t* cu, int N, int64_t T, const Paged* c, cudaStream_t s);

@@ -28,6 +28,14 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
         :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(mbar) : "memory");
 }
 
+// mbar_wait for those that may wait for a warp with rows to compute once more, which counts
+// itself in `busy` and can take longer than the limit.
+__device__ __forceinline__ bool mbar_wait_busy(uint32_t mbar, uint32_t parity, volatile int* abort, volatile int* busy) {
+    while (!mbar_wait(mbar, parity, abort))
+        if (*abort || *busy == 0) return false;
+    return true;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -254,13 +254,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     __shared__ Job jobs[2];
     __shared__ __align__(16) unsigned char answer[16];
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, busy_warps;
     __shared__ int limits[PREFIX ? 2 * kTile : 1];            // per token of the job: end of the keys that it sees
     __shared__ uint32_t missing[PREFIX ? 16 : 1];             // per key tile: a bit per 16 keys without a page
     const AttnArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = a.group;
     if (PREFIX) grid_dep_launch();  // the own keys' CTAs start where this grid's have left
     volatile int* abort = &abort_flag;
+    volatile int* busy = &busy_warps;
 
     const uint32_t q_smem = (smem_u32(raw) + 1023) & ~1023u, ring = q_smem + 2 * C::TILE_BYTES;
     if (tid == 0) {
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         mbar_init(smem_u32(&bars.place), 1);
         mbar_init(smem_u32(&bars.drain), 1);
         mbar_fence_init();
-        abort_flag = 0;
+        abort_flag = busy_warps = 0;
     }
     if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), 512);
     fence_before();
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 return key < a.cache.prefix_len ? a.cache.prefix[key >> a.cache.page_bits] : -1;
             };
             for (;; ++count) {
-                ok = mbar_wait(smem_u32(&bars.job[count & 1]), (count / 2) & 1, abort);
+                ok = mbar_wait_busy(smem_u32(&bars.job[count & 1]), (count / 2) & 1, abort, busy);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const Job job = jobs[count & 1];
                 __syncwarp();
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 const int from = job.from, to = max(job.to[0], job.to[1]), tiles = to - from, begin = it;
                 for (int t = 0; t < 2 && ok; ++t) {
                     if (job.to[t] <= from) continue;
-                    if (q_uses[t]) ok = mbar_wait(smem_u32(&bars.q_free[t]), (q_uses[t] - 1) & 1, abort);
+                    if (q_uses[t]) ok = mbar_wait_busy(smem_u32(&bars.q_free[t]), (q_uses[t] - 1) & 1, abort, busy);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     ++q_uses[t];
                     if (lane == 0) {
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     if (lane == 0 && it == max(begin, begin + 2 * tiles - C::STAGES)) mbar_arrive(smem_u32(&bars.ahead));
                     const int stage = it % C::STAGES, j = from + ((it - begin) >> 1);
                     const bool value = (it - begin) & 1;
-                    if (it >= C::STAGES) ok = mbar_wait(smem_u32(&bars.empty[stage]), (it / C::STAGES - 1) & 1, abort);
+                    if (it >= C::STAGES) ok = mbar_wait_busy(smem_u32(&bars.empty[stage]), (it / C::STAGES - 1) & 1, abort, busy);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     const uint32_t mbar = smem_u32(&bars.full[stage]), dst = ring + stage * C::TILE_BYTES;
                     const CUtensorMap* map = value ? &mv : &mk;
@@ -389,7 +390,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             const uint64_t v0 = smem_desc(ring, C::BLOCK_BYTES, 1024, kSwizzle128);
             bool ok = true;
             auto wait = [&](uint64_t* bar, int phase) {
-                ok = __all_sync(0xffffffffu, mbar_spin(smem_u32(bar), phase & 1, abort));
+                bool there = mbar_spin(smem_u32(bar), phase & 1, abort);
+                while (!there && !*abort && *busy) there = mbar_spin(smem_u32(bar), phase & 1, abort);
+                ok = __all_sync(0xffffffffu, there);
                 if (!ok) *abort = 1;
                 return ok;
             };
@@ -472,7 +475,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             for (int count = 0;; ++count) {
                 const int b = count & 1;
                 auto wait = [&](uint64_t* bar, int phase) {
-                    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1, abort));
+                    return __all_sync(0xffffffffu, mbar_wait_busy(smem_u32(bar), phase & 1, abort, busy));
                 };
                 bool ok = wait(&bars.job[b], count / 2);
                 if (ok) {
@@ -544,16 +547,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     found = find_job(a, pair_tokens, pairs, place / a.Hkv, places, place % a.Hkv, job);
                 }
                 if (found) {
-                    if (count >= 2) ok = mbar_wait(smem_u32(&bars.job_free[count & 1]), (count / 2 - 1) & 1, abort);
+                    if (count >= 2) ok = mbar_wait_busy(smem_u32(&bars.job_free[count & 1]), (count / 2 - 1) & 1, abort, busy);
                     // the limits have one place, which those of the job before have to leave
-                    if (PREFIX && ok && count >= 1) ok = mbar_wait(smem_u32(&bars.limits_free), (count - 1) & 1, abort);
+                    if (PREFIX && ok && count >= 1) ok = mbar_wait_busy(smem_u32(&bars.limits_free), (count - 1) & 1, abort, busy);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     if (PREFIX) mark_limits(a, job.i0, pair_tokens, limits);
                     if (lane == 0) {
                         jobs[count & 1] = job;
                         mbar_arrive(smem_u32(&bars.job[count & 1]));
                     }
-                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.ahead), count & 1, abort));
+                    ok = __all_sync(0xffffffffu, mbar_wait_busy(smem_u32(&bars.ahead), count & 1, abort, busy));
                     ++count;
                     if (!ok) break;
                 }
@@ -568,7 +571,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 __syncwarp();
             }
             // no more jobs
-            if (ok && count >= 2) ok = mbar_wait(smem_u32(&bars.job_free[count & 1]), (count / 2 - 1) & 1, abort);
+            if (ok && count >= 2) ok = mbar_wait_busy(smem_u32(&bars.job_free[count & 1]), (count / 2 - 1) & 1, abort, busy);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) *abort = 1;
             if (ok && lane == 0) {
@@ -587,7 +590,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         int s_uses = 0, o_uses = 0;
         int tiles_before = 0;  // key tiles of the jobs so far
         for (int count = 0;; ++count) {
-            bool ok = mbar_wait(smem_u32(&bars.job[count & 1]), (count / 2) & 1, abort);
+            bool ok = mbar_wait_busy(smem_u32(&bars.job[count & 1]), (count / 2) & 1, abort, busy);
             if (!(ok = __all_sync(0xffffffffu, ok))) {
                 *abort = 1;
                 break;
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             float m = -INFINITY;
             float2 sum = make_float2(0.f, 0.f);
             for (int j = from, i = 0; j < end; ++j, ++i) {
-                ok = mbar_wait(smem_u32(&bars.s[t]), s_uses++ & 1, abort);
+                ok = mbar_wait_busy(smem_u32(&bars.s[t]), s_uses++ & 1, abort, busy);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 fence_after();
                 float s[kTile];
@@ -674,7 +677,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars.p[t]));
             }
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.o[t]), o_uses++ & 1, abort));
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_busy(smem_u32(&bars.o[t]), o_uses++ & 1, abort, busy));
             if (!ok) {
                 *abort = 1;
                 break;
@@ -734,7 +737,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             if (PREFIX && there) p.w.far_stat[place] = make_float2(m, l);
             const bool finite = any == 0.f && l < INFINITY && (PREFIX || l > 0.f);
             // rows that an infinity or a NaN has reached, one after the other
-            for (uint32_t bad = __ballot_sync(0xffffffffu, there && !finite); bad; bad &= bad - 1) {
+            uint32_t bad = __ballot_sync(0xffffffffu, there && !finite);
+            if (bad && lane == 0) atomicAdd(&busy_warps, 1);
+            const bool again = bad;
+            for (; bad; bad &= bad - 1) {
                 const int who = __ffs(bad) - 1;
                 const int64_t at_w = __shfl_sync(0xffffffffu, t0 + token, who), head_w = __shfl_sync(0xffffffffu, head, who);
                 const int64_t place_w = __shfl_sync(0xffffffffu, place, who);
@@ -766,6 +772,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 }
             }
             __syncwarp();
+            if (again && lane == 0) atomicSub(&busy_warps, 1);
             if (lane == 0) mbar_arrive(smem_u32(&bars.job_free[count & 1]));
         }
     }

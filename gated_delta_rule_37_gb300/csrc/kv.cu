@@ -292,6 +292,17 @@ int check_token_rows(const char* name, const void* p, int64_t stride, int64_t le
     return GDR_OK;
 }
 
+int check_apart(const MemRows& a, const MemRows& b) {
+    if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return GDR_OK;
+    const int64_t pa = (int64_t)reinterpret_cast<uintptr_t>(a.p), pb = (int64_t)reinterpret_cast<uintptr_t>(b.p);
+    if (pa + (a.rows - 1) * a.ld + a.row <= pb || pb + (b.rows - 1) * b.ld + b.row <= pa) return GDR_OK;
+    if (a.ld == b.ld && a.ld > 0) {
+        const int64_t d = ((pb - pa) % a.ld + a.ld) % a.ld;  // where b's rows begin within a's
+        if (d >= a.row && d + b.row <= a.ld) return GDR_OK;
+    }
+    return set_last_error(GDR_ERR_INVALID_ARG, "%s is written and overlaps %s", a.name, b.name);
+}
+
 int check_int32s(const char* name, const void* p) {
     if (!p) return set_last_error(GDR_ERR_INVALID_ARG, "null pointer argument (%s)", name);
     if (reinterpret_cast<uintptr_t>(p) & 3u)
@@ -358,6 +369,21 @@ int gdr_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stri
     if (rotary_dim > 0 && (!freqs || (reinterpret_cast<uintptr_t>(freqs) & 3u)))
         return set_last_error(GDR_ERR_INVALID_ARG, "freqs missing or not 4-byte aligned");
     if (int rc = check_int32s("cu_seqlens", cu_seqlens)) return rc;
+    {
+        const int64_t e = dtype == GDR_BF16 ? 2 : 4, cache = (int64_t)num_pages * Hkv * page_size * D * e;
+        const MemRows in[3] = {{"q", q, wide * e, q_stride * e, T_total}, {"k", k, narrow * e, k_stride * e, T_total},
+                               {"v", v, narrow * e, v_stride * e, T_total}};
+        const MemRows out[4] = {{"q_out", q_out, wide * e, q_out_stride * e, T_total},
+                                {"k_out", k_out, narrow * e, k_out_stride * e, T_total},
+                                {"k_cache", k_cache, cache, cache, 1}, {"v_cache", v_cache, cache, cache, 1}};
+        for (int i = 0; i < 4; ++i) {
+            for (int j = 0; j < 3; ++j)
+                if (!(i < 2 && i == j && out[i].p == in[j].p))  // in place
+                    if (int rc = check_apart(out[i], in[j])) return rc;
+            for (int j = i + 1; j < 4; ++j)
+                if (int rc = check_apart(out[i], out[j])) return rc;
+        }
+    }
     if (int rc = check_device()) return rc;
     cudaStream_t s = (cudaStream_t)stream;
     if (flags & GDR_VALIDATE) {

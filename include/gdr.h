@@ -462,7 +462,8 @@ GDR_API int gdr_rmsnorm_bwd(const void* dy, int64_t dy_stride, const void* s, in
  *     exp(score - maximum) enter the product with v as bf16 numbers (and their
  *     sum as they are).
  *   - D 64 or 128; Hq a multiple of Hkv, up to GDR_ATTN_MAX_GROUP times it and
- *     up to 4096; N up to 65535; T_total * Hq below 2^31 - 512; scale > 0.
+ *     up to 4096; N up to 65535, N * Hkv up to 2^24; T_total * Hq below 2^31 - 512;
+ *     scale > 0.
  *   - cu_seqlens [N+1] int32 device, cu[0] = 0, non-decreasing; sequences may be
  *     empty.  cu[N] may be less than T_total (a padded batch): rows from cu[N]
  *     on are neither read as queries nor written.  A cu_seqlens that breaks
@@ -479,7 +480,11 @@ GDR_API int gdr_rmsnorm_bwd(const void* dy, int64_t dy_stride, const void* s, in
  *     before this call's; both calls of a step take the same numbers.  A value
  *     < 0 is padding: nothing of that sequence is read or written.
  *   - A NaN or infinity reaches only the rows that see its token; where rows of
- *     the same tile do not, they are computed once more (slowly) without it.
+ *     the same tile do not, they are computed once more (slowly) without it.  A
+ *     row that sees no key, or whose scores are all -inf, is 0.
+ *   - What is written shares no memory with an input, the workspace or what else
+ *     is written, but where a tensor is said to be in place; column blocks of the
+ *     same rows share none.
  *   - Results do not depend on scheduling: equal inputs give equal bits.
  *
  * gdr_kv_append -- appends keys and values to the caches, rotary positions
@@ -515,7 +520,7 @@ GDR_API int gdr_kv_append(const void* q, int64_t q_stride, const void* k, int64_
  *   o_t = sum_j softmax_j(scale q_t . k_j) v_j,   j the tokens up to t of t's sequence
  *
  *   q, o  [T_total, Hq, D] dtype;  k, v  [T_total, Hkv, D] dtype
- *   o     (written) must not overlap an input
+ *   o     (written)
  * Flags: GDR_VALIDATE.
  */
 GDR_API int gdr_attn_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
@@ -538,8 +543,7 @@ GDR_API int gdr_attn_step_workspace_size(int N, int64_t T_total, int Hq, int Hkv
  *                  page_size], [ceil(prefix_len / page_size)] int32 device.  They
  *                  are read once for the batch.  cache_lens counts them; block_table
  *                  entries of pages that end within the prefix are not read.
- *   q, o           [T_total, Hq, D] dtype; o (written) must not overlap an input.
- *                  A row that sees no key is 0.
+ *   q, o           [T_total, Hq, D] dtype; o is written
  *   workspace      device scratch of gdr_attn_step_workspace_size bytes, 256-byte
  *                  aligned; needs no initialisation.  Calls whose work may overlap
  *                  on the GPU need one each.
