@@ -28,13 +28,13 @@ constexpr float kNone = -INFINITY;
 // keys tk + TK j of the scores and D / TK channels of the sums.  TK threads of one warp
 // share a row, so that its maximum and sum are shuffles.
 template <typename T, int D, int RT> struct Simt {
-    static constexpr int TK = RT == 64 ? 16 : 32, TR = 256 / TK, RR = RT / TR, KK = kKeyTile / TK;
+    static constexpr int TK = RT >= 64 ? 16 : 32, TR = 256 / TK, RR = RT / TR, KK = kKeyTile / TK;
     static constexpr int CV = D / TK < 4 ? D / TK : 4, CG = D / TK / CV;
     static constexpr int LDQ = D + 4, LDP = kKeyTile + 4;  // rows of the products on different banks
     struct Smem {
         float q[RT][LDQ], k[kKeyTile][LDQ], v[kKeyTile][D], p[RT][LDP];
         int64_t limit[RT];
-        int there[kKeyTile];
+        int there[2][kKeyTile];  // of this tile and the next
     };
 
     float m[RR], l[RR], acc[RR][CG * CV];
@@ -62,32 +62,70 @@ template <typename T, int D, int RT> struct Simt {
         }
     }
 
-    // One tile of keys from position j0 on, those below `least` left out.  keys(j, kp, vp)
-    // gives a key's rows, false where there is none.
-    template <typename K>
-    __device__ void tile(Smem& s, int64_t j0, int64_t least, int64_t most, K keys) {
-        const int tk = threadIdx.x % TK, tr = threadIdx.x / TK;
-        __syncthreads();
+    // Rows of keys or values from position j0 on to shared memory, zeros where there are none;
+    // fp32 by asynchronous copies.  keys(j, kp, vp) gives a key's rows, false where it has none.
+    template <bool VALUES, int LD, typename K>
+    __device__ void load(float (&to)[kKeyTile][LD], int* there, int64_t j0, int64_t least, int64_t most, K keys) {
         constexpr int C = D / 4;
+#pragma unroll 4
         for (int i = threadIdx.x; i < kKeyTile * C; i += 256) {
             const int64_t j = j0 + i / C;
-            const T *kp, *vp;
-            float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-            const bool there = j >= least && j < most && keys(j, kp, vp);
-            if (there) {
-                Vec<T, 4>::load(kp + i % C * 4, x);
-                Vec<T, 4>::load(vp + i % C * 4, y);
+            const T *kp = nullptr, *vp = nullptr;
+            const bool has = j >= least && j < most && keys(j, kp, vp);
+            if (!VALUES && i % C == 0) there[i / C] = has;
+            float* row = &to[i / C][i % C * 4];
+            const T* from = (VALUES ? vp : kp) + i % C * 4;
+            if (sizeof(T) == 4) {
+                const uint32_t dst = (uint32_t)__cvta_generic_to_shared(row), bytes = has ? 16 : 0;
+                const void* src = has ? static_cast<const void*>(from) : a_row;  // read only if there are bytes
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+            } else {
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                if (has) Vec<T, 4>::load(from, x);
+                Vec<float, 4>::store(row, x);
             }
-            if (i % C == 0) s.there[i / C] = there;
-            Vec<float, 4>::store(&s.k[i / C][i % C * 4], x);
-            Vec<float, 4>::store(&s.v[i / C][i % C * 4], y);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // All of this thread's copies but the last set.
+    __device__ static void landed() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+    const void* a_row;  // an address that may be given where nothing is read
+
+    // The tiles of keys from position j0 to j1, those below `least` and from `most` on left out.
+    // A tile's values arrive while its scores are formed, the next one's keys during the
+    // product with the values.
+    template <typename K>
+    __device__ void tiles(Smem& s, int64_t j0, int64_t j1, int64_t least, int64_t most, K keys) {
+        if (j0 >= j1) return;
         __syncthreads();
-        float sc[RR][KK];
+        load<false>(s.k, s.there[0], j0, least, most, keys);
+        for (int b = 0; j0 < j1; j0 += kKeyTile, b ^= 1) {
+            load<true>(s.v, nullptr, j0, least, most, keys);
+            landed();
+            __syncthreads();
+            const int tk = threadIdx.x % TK, tr = threadIdx.x / TK;
+            // a key that a row does not see may be an infinity, which a weight of 0 does not
+            // keep out: where the tile has such pairs each is asked for
+            const bool masked = __syncthreads_or(scores(s, s.there[b], j0, tr, tk));
+            if (j0 + kKeyTile < j1) load<false>(s.k, s.there[b ^ 1], j0 + kKeyTile, least, most, keys);
+            else asm volatile("cp.async.commit_group;" ::: "memory");
+            landed();
+            __syncthreads();
+            if (!masked) product<false>(s, j0, tr, tk);
+            else product<true>(s, j0, tr, tk);
+            __syncthreads();
+        }
+    }
+
+    // One tile's scores and weights; whether a row does not see one of its keys.
+    __device__ bool scores(Smem& s, const int* there, int64_t j0, int tr, int tk) {
+        // even and odd channels apart: two fused multiply-adds an instruction
+        float2 part[RR][KK];
 #pragma unroll
         for (int i = 0; i < RR; ++i)
 #pragma unroll
-            for (int j = 0; j < KK; ++j) sc[i][j] = 0.f;
+            for (int j = 0; j < KK; ++j) part[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
         for (int d = 0; d < D; d += 4) {
             float4 qf[RR], kf[KK];
@@ -99,9 +137,15 @@ template <typename T, int D, int RT> struct Simt {
             for (int i = 0; i < RR; ++i)
 #pragma unroll
                 for (int j = 0; j < KK; ++j)
-                    sc[i][j] = fmaf(qf[i].x, kf[j].x, fmaf(qf[i].y, kf[j].y,
-                               fmaf(qf[i].z, kf[j].z, fmaf(qf[i].w, kf[j].w, sc[i][j]))));
+                    part[i][j] = __ffma2_rn(make_float2(qf[i].x, qf[i].y), make_float2(kf[j].x, kf[j].y),
+                                            __ffma2_rn(make_float2(qf[i].z, qf[i].w), make_float2(kf[j].z, kf[j].w),
+                                                       part[i][j]));
         }
+        float sc[RR][KK];
+#pragma unroll
+        for (int i = 0; i < RR; ++i)
+#pragma unroll
+            for (int j = 0; j < KK; ++j) sc[i][j] = part[i][j].x + part[i][j].y;
         bool masked = false;
 #pragma unroll
         for (int i = 0; i < RR; ++i) {
@@ -110,7 +154,7 @@ template <typename T, int D, int RT> struct Simt {
 #pragma unroll
             for (int j = 0; j < KK; ++j) {
                 const int k = tk + TK * j;
-                if (!s.there[k] || j0 + k >= end) {
+                if (!there[k] || j0 + k >= end) {
                     sc[i][j] = kNone;
                     masked = true;
                 }
@@ -133,14 +177,7 @@ template <typename T, int D, int RT> struct Simt {
 #pragma unroll
             for (int c = 0; c < CG * CV; ++c) acc[i][c] *= back;
         }
-        // a key that a row does not see may be an infinity, which a weight of 0 does not
-        // keep out: where the tile has such pairs each is asked for
-        masked = __syncthreads_or(masked);
-        if (!masked) {
-            product<false>(s, j0, tr, tk);
-        } else {
-            product<true>(s, j0, tr, tk);
-        }
+        return masked;
     }
 
     template <bool MASKED>
@@ -163,7 +200,12 @@ template <typename T, int D, int RT> struct Simt {
                     const float p = e == 0 ? pf[i].x : e == 1 ? pf[i].y : e == 2 ? pf[i].z : pf[i].w;
                     if (MASKED && k + e >= end[i]) continue;
 #pragma unroll
-                    for (int c = 0; c < CG * CV; ++c) acc[i][c] = fmaf(p, v[c], acc[i][c]);
+                    for (int c = 0; c < CG * CV; c += 2) {
+                        const float2 a = __ffma2_rn(make_float2(p, p), make_float2(v[c], v[c + 1]),
+                                                    make_float2(acc[i][c], acc[i][c + 1]));
+                        acc[i][c] = a.x;
+                        acc[i][c + 1] = a.y;
+                    }
                 }
             }
         }
@@ -254,12 +296,12 @@ __global__ void __launch_bounds__(256) prompt_simt_kernel(const AttnArgs a) {
     e.start(s, [&](int r) { return r < rows ? static_cast<const T*>(a.q) + element(r0 + r, a.ldq) : nullptr; },
             [&](int r) { return r < rows ? (r0 + r) / a.group + 1 : 0; }, a.scale_log2);
     const int64_t most = (r0 + rows - 1) / a.group + 1;
-    for (int64_t j = 0; j < most; j += kKeyTile)
-        e.tile(s, j, 0, most, [&](int64_t i, const T*& kp, const T*& vp) {
-            kp = static_cast<const T*>(a.k) + (t0 + i) * a.ldk + (int64_t)h * D;
-            vp = static_cast<const T*>(a.v) + (t0 + i) * a.ldv + (int64_t)h * D;
-            return true;
-        });
+    e.a_row = a.q;
+    e.tiles(s, 0, most, 0, most, [&](int64_t i, const T*& kp, const T*& vp) {
+        kp = static_cast<const T*>(a.k) + (t0 + i) * a.ldk + (int64_t)h * D;
+        vp = static_cast<const T*>(a.v) + (t0 + i) * a.ldv + (int64_t)h * D;
+        return true;
+    });
     e.finish([&](int r) { return r < rows ? static_cast<T*>(a.o) + element(r0 + r, a.ldo) : nullptr; });
 }
 
@@ -284,10 +326,9 @@ __global__ void __launch_bounds__(256) step_simt_kernel(const AttnArgs a, const 
         E e;
         e.start(s, [&](int r) { return r < rows ? static_cast<const T*>(a.q) + element(r, a.ldq) : nullptr; },
                 [&](int r) { return r < rows ? len + (r0 + r) / a.group + 1 : 0; }, a.scale_log2);
-        for (int k = run.from; k < run.to; ++k)
-            e.tile(s, (int64_t)k * kKeyTile, a.cache.prefix_len, most, [&](int64_t j, const T*& kp, const T*& vp) {
-                return cached<T, D>(a.cache, pages, a.Hkv, h, j, kp, vp);
-            });
+        e.a_row = a.q;
+        e.tiles(s, (int64_t)run.from * kKeyTile, (int64_t)run.to * kKeyTile, a.cache.prefix_len, most,
+                [&](int64_t j, const T*& kp, const T*& vp) { return cached<T, D>(a.cache, pages, a.Hkv, h, j, kp, vp); });
         if (run.slot >= 0) {
             const int64_t base = ((int64_t)blockIdx.x * 2 + run.slot) * w.rows;
             e.leave([&](int r) { return r < rows ? w.slot_sum + (base + r) * D : nullptr; },
@@ -330,10 +371,11 @@ __global__ void __launch_bounds__(256) prefix_simt_kernel(const AttnArgs a, cons
                 if (lo >= a.N || a.cu[lo] > t || t >= a.cu[lo + 1] || a.cache.lens[lo] < 0) return 0;
                 return min((int64_t)a.cache.prefix_len, a.cache.lens[lo] + (t - a.cu[lo]) + 1);
             }, a.scale_log2);
-    for (int k = from; k < to; ++k)
-        e.tile(s, (int64_t)k * kKeyTile, 0, a.cache.prefix_len, [&](int64_t j, const T*& kp, const T*& vp) {
-            return cached<T, D>(a.cache, a.cache.prefix, a.Hkv, h, j, kp, vp);
-        });
+    e.a_row = a.q;
+    e.tiles(s, (int64_t)from * kKeyTile, (int64_t)to * kKeyTile, 0, a.cache.prefix_len,
+            [&](int64_t j, const T*& kp, const T*& vp) {
+                return cached<T, D>(a.cache, a.cache.prefix, a.Hkv, h, j, kp, vp);
+            });
     e.leave([&](int r) { return r < rows ? w.far_sum + row(r) * D : nullptr; },
             [&](int r) { return w.far_stat + row(r); });
 }
@@ -476,13 +518,17 @@ cudaError_t launch_prompt_rows(const AttnArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// 16 rows a tile where tiles of 64 would leave SMs without one.  (Measured with fp32, 16 rows
-// against 64: 2 heads of 64, 128 tokens 9.9 / 16.2 us, 512 tokens 29 / 49; 8 heads of 128 on one
-// key head, 1000 tokens 115 / 158; 16 of 128, 512 tokens, nearly a tile for each SM, 95 / 83;
+// The largest tiles that leave no SM without one: 128 rows by heads of 128, 64, else 16.
+// (Measured with fp32.  128 rows against 64: 32 heads of 128 on 8, 4000 tokens 3.5 / 4.5 ms, 16 on
+// 2, 2000 tokens 461 / 519 us; heads of 64, of which 64 rows leave room for two CTAs, 2.0 / 1.9 ms.
+// 16 rows against 64: 2 heads of 64, 128 tokens 9.9 / 16.2 us, 512 tokens 28 / 49; 8 heads of 128 on
+// one key head, 1000 tokens 114 / 158; 16 of 128, 512 tokens, nearly a tile for each SM, 93 / 83;
 // 32 of 128 on 8, 4000 tokens 6.8 / 4.8 ms.)
 template <typename T, int D>
 cudaError_t launch_prompt_simt(const AttnArgs& a, cudaStream_t s) {
-    return (a.T * a.group + 63) / 64 * a.Hkv < kSms ? launch_prompt_rows<T, D, 16>(a, s) : launch_prompt_rows<T, D, 64>(a, s);
+    const auto tiles = [&](int rows) { return (a.T * a.group + rows - 1) / rows * a.Hkv; };
+    if (D == 128 && tiles(128) >= kSms) return launch_prompt_rows<T, D, D == 128 ? 128 : 64>(a, s);
+    return tiles(64) >= kSms ? launch_prompt_rows<T, D, 64>(a, s) : launch_prompt_rows<T, D, 16>(a, s);
 }
 
 template <typename T, int D, int RT>
