@@ -428,7 +428,8 @@ __device__ __forceinline__ void join_parts(int count, int first, int step, S sta
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads) step_merge_kernel(const AttnArgs a, const StepWork w) {
     constexpr int C = D / 32;
-    __shared__ float sums[kMergeWarps][D], ls[kMergeWarps];
+    __shared__ __align__(16) float sums[kMergeWarps][D];
+    __shared__ float ls[kMergeWarps];
     grid_dep_wait();
     const Cut cut = w.cuts[blockIdx.x];
     const int r = blockIdx.y, cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -567,8 +568,12 @@ cudaError_t launch_merge(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
 // tile's cost grows with it, and rows beyond the first tile read the keys again.
 int rows_per_tile(int N, int64_t T, int group, int dtype) {
     const int64_t rows = (T + N - 1) / (N > 0 ? N : 1) * group;
+    if (dtype == GDR_F32 && rows <= 8) return rows <= 4 ? 4 : 8;
     return rows <= 16 ? 16 : rows <= 32 && dtype == GDR_BF16 ? 32 : 64;
 }
+
+// Rows per tile of the prefix on the CUDA cores.
+int far_rows(const StepWork& w) { return w.rows <= 16 ? 16 : 64; }
 
 // Cuts of the prefix along its keys: about as many CTAs as the GPU holds at once.
 void prefix_cuts(StepWork* w, int64_t T, int Hkv, int group, int prefix_len, int dtype) {
@@ -586,7 +591,7 @@ void prefix_cuts(StepWork* w, int64_t T, int Hkv, int group, int prefix_len, int
         w->splits = (int)(parts < tiles ? parts : tiles);
         return;
     }
-    const int64_t blocks = (T * group + w->rows - 1) / w->rows * Hkv;
+    const int64_t blocks = (T * group + far_rows(*w) - 1) / far_rows(*w) * Hkv;
     int64_t splits = 2 * kSms / blocks;
     if (splits > tiles) splits = tiles;
     if (splits < 1) splits = 1;
@@ -602,8 +607,8 @@ size_t step_layout(StepWork* w, char* base, int N, int64_t T, int Hq, int Hkv, i
         at += (bytes + 255) / 256 * 256;
         return p;
     };
-    w->ctas = dtype == GDR_BF16 ? kSms : 2 * kSms;
     w->rows = rows_per_tile(N, T, Hq / Hkv, dtype);
+    w->ctas = dtype == GDR_BF16 || w->rows == 8 ? kSms : 2 * kSms;  // what the GPU holds at once
     prefix_cuts(w, T, Hkv, Hq / Hkv, prefix_len, dtype);
     const size_t slots = (size_t)w->ctas * 2 * w->rows, rows = w->splits ? (size_t)T * Hq : 0;
     w->offsets = reinterpret_cast<int64_t*>(part(sizeof(int64_t) * ((size_t)N + 1)));
@@ -626,8 +631,12 @@ cudaError_t launch_step(const AttnArgs& a, StepWork w, cudaStream_t s) {
         if (e == cudaSuccess) e = launch_step_own(a, w, s);
         return e == cudaSuccess ? launch_merge<__nv_bfloat16, D>(a, w, s) : e;
     }
-    if (w.splits > 0) e = w.rows == 16 ? launch_prefix_simt<float, D, 16>(a, w, s) : launch_prefix_simt<float, D, 64>(a, w, s);
-    if (e == cudaSuccess) e = w.rows == 16 ? launch_step_simt<D, 16>(a, w, s) : launch_step_simt<D, 64>(a, w, s);
+    if (w.splits > 0)
+        e = far_rows(w) == 16 ? launch_prefix_simt<float, D, 16>(a, w, s) : launch_prefix_simt<float, D, 64>(a, w, s);
+    if (e == cudaSuccess)
+        e = w.rows <= 8    ? launch_step_few(a, w, s)
+            : w.rows == 16 ? launch_step_simt<D, 16>(a, w, s)
+                           : launch_step_simt<D, 64>(a, w, s);
     return e == cudaSuccess ? launch_merge<float, D>(a, w, s) : e;
 }
 

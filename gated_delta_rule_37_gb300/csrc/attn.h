@@ -61,4 +61,7 @@ int prefix_block_tokens(int group);  // tokens of a block of rows of the prefix'
 cudaError_t launch_prefix_tc(const AttnArgs& a, const StepWork& w, cudaStream_t s);
 cudaError_t launch_step_own(const AttnArgs& a, const StepWork& w, cudaStream_t s);
 
+// The own keys' part in fp32 for w.rows 4 or 8.
+cudaError_t launch_step_few(const AttnArgs& a, const StepWork& w, cudaStream_t s);
+
 }  // namespace gdr
