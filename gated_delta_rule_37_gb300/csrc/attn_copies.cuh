@@ -28,12 +28,19 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
         :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(mbar) : "memory");
 }
 
-// mbar_wait for those that may wait for a warp with rows to compute once more, which counts
-// itself in `busy` and can take longer than the limit.
-__device__ __forceinline__ bool mbar_wait_busy(uint32_t mbar, uint32_t parity, volatile int* abort, volatile int* busy) {
-    while (!mbar_wait(mbar, parity, abort))
-        if (*abort || *busy == 0) return false;
-    return true;
+// mbar_wait for those that may wait for a warp with rows to compute once more, which can take
+// longer than the limit: it counts itself in abort[1].
+__device__ __forceinline__ bool mbar_wait_busy(uint32_t mbar, uint32_t parity, volatile int* abort) {
+    if (mbar_test(mbar, parity)) return true;
+    uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try(mbar, parity)) return true;
+        if ((i & 255) == 0) {
+            if (abort[0]) return false;
+            if (abort[1]) t0 = globaltimer_ns();
+            if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+        }
+    }
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -99,11 +99,10 @@ __global__ void __launch_bounds__(kStepBlock, 1)
     __shared__ uint32_t missing[C::STAGES];     // a bit per 16 keys without a page
     __shared__ float2 stats[kReaders][16];
     __shared__ uint32_t bad_rows[2];
-    __shared__ int abort_flag, busy_warps;
+    __shared__ int abort_busy[2];
     const AttnArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    volatile int* abort = &abort_flag;
-    volatile int* busy = &busy_warps;
+    volatile int* abort = abort_busy;  // a wait gave up; warps with rows to compute once more
     const uint32_t ring = (smem_u32(raw) + 1023) & ~1023u;
     const uint32_t queries = ring + C::STAGES * C::STAGE_BYTES;
     unsigned char* const base = raw + (ring - smem_u32(raw));
@@ -119,7 +118,7 @@ __global__ void __launch_bounds__(kStepBlock, 1)
             mbar_init(smem_u32(&bars.q_empty[i]), kReaders);
         }
         mbar_fence_init();
-        abort_flag = busy_warps = 0;
+        abort_busy[0] = abort_busy[1] = 0;
         bad_rows[0] = bad_rows[1] = 0;
     }
     grid_dep_launch();
@@ -146,7 +145,7 @@ __global__ void __launch_bounds__(kStepBlock, 1)
             more = runs.next(run);
             if (more) held = pages_from(run.n, run.from * pieces);
             const int q = count & 1;
-            if (count >= 2) ok = mbar_wait_busy(smem_u32(&bars.q_empty[q]), (count / 2 - 1) & 1, abort, busy);
+            if (count >= 2) ok = mbar_wait_busy(smem_u32(&bars.q_empty[q]), (count / 2 - 1) & 1, abort);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             const int r0 = r.row_tile * ROWS, rows = min(ROWS, r.s.rows - r0);
             if (lane == 0) {
@@ -180,7 +179,7 @@ __global__ void __launch_bounds__(kStepBlock, 1)
                                                  (key & (a.cache.page_size - 1)));
                 const bool part = __shfl_sync(0xffffffffu, gone, (lane & 3) * 16 / p.box);
                 const uint32_t out = __ballot_sync(0xffffffffu, part && lane < 4);
-                if (it >= C::STAGES) ok = mbar_wait_busy(smem_u32(&bars.empty[stage]), (it / C::STAGES - 1) & 1, abort, busy);
+                if (it >= C::STAGES) ok = mbar_wait_busy(smem_u32(&bars.empty[stage]), (it / C::STAGES - 1) & 1, abort);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const uint32_t mbar = smem_u32(&bars.full[stage]), dst = ring + stage * C::STAGE_BYTES;
                 if (lane == 0) {
@@ -204,7 +203,7 @@ __global__ void __launch_bounds__(kStepBlock, 1)
             landed &= mbar_wait_copies(smem_u32(&bars.full[i % C::STAGES]), (i / C::STAGES) & 1);
         for (int i = max(0, count - 2); i < count; ++i)
             landed &= mbar_wait_copies(smem_u32(&bars.q_full[i & 1]), (i / 2) & 1);
-        if (ok && count >= 2) ok = mbar_wait_busy(smem_u32(&bars.q_empty[count & 1]), (count / 2 - 1) & 1, abort, busy);
+        if (ok && count >= 2) ok = mbar_wait_busy(smem_u32(&bars.q_empty[count & 1]), (count / 2 - 1) & 1, abort);
         ok = __all_sync(0xffffffffu, ok && landed);
         if (ok && lane == 0) {
             jobs[count & 1].n = -1;
@@ -223,7 +222,7 @@ __global__ void __launch_bounds__(kStepBlock, 1)
         int it = 0;
         for (int count = 0;; ++count) {
             const int q = count & 1;
-            bool ok = mbar_wait_busy(smem_u32(&bars.q_full[q]), (count / 2) & 1, abort, busy);
+            bool ok = mbar_wait_busy(smem_u32(&bars.q_full[q]), (count / 2) & 1, abort);
             if (any_reader(!ok)) {
                 *abort = 1;
                 break;
@@ -253,7 +252,7 @@ __global__ void __launch_bounds__(kStepBlock, 1)
             for (int k = j.from; k < j.to; ++k, ++it) {
                 if (C::TURNS && (it & 1) != set) continue;
                 const int stage = it % C::STAGES;
-                if (ok) ok = __all_sync(0xffffffffu, mbar_wait_busy(smem_u32(&bars.full[stage]), (it / C::STAGES) & 1, abort, busy));
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait_busy(smem_u32(&bars.full[stage]), (it / C::STAGES) & 1, abort));
                 if (!ok) continue;
                 const uint32_t ks_ = ring + stage * C::STAGE_BYTES, vs = ks_ + C::TILE_BYTES;
                 const int key0 = k * kKeyTile + part * C::KEYS;
@@ -437,7 +436,7 @@ __global__ void __launch_bounds__(kStepBlock, 1)
             if (bad[0] | bad[1]) {
                 any_reader(false);  // all have read the words
                 if (tid == 0) bad_rows[0] = bad_rows[1] = 0;
-                if (lane == 0) atomicAdd(&busy_warps, 1);
+                if (lane == 0) atomicAdd(&abort_busy[1], 1);
                 for (int r = warp; r < j.rows; r += kReaders) {
                     if (!(bad[r >> 5] >> (r & 31) & 1)) continue;
                     const int64_t token = j.t0 + (j.r0 + r) / a.group;
@@ -465,14 +464,14 @@ __global__ void __launch_bounds__(kStepBlock, 1)
                         if (lane == 0) (j.slot < 0 ? p.w.row_stat : p.w.slot_stat)[at] = make_float2(top, sum);
                     }
                 }
-                if (lane == 0) atomicSub(&busy_warps, 1);
+                if (lane == 0) atomicSub(&abort_busy[1], 1);
                 any_reader(false);  // the words are clear before the next run's join
             }
         }
     }
     __syncwarp();
     __syncthreads();
-    if (tid == 0 && abort_flag) atomicOr(p.err, kAttnError);
+    if (tid == 0 && abort_busy[0]) atomicOr(p.err, kAttnError);
 }
 
 template <int D, int ROWS>

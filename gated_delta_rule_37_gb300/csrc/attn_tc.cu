@@ -254,14 +254,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     __shared__ Job jobs[2];
     __shared__ __align__(16) unsigned char answer[16];
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag, busy_warps;
+    __shared__ int abort_busy[2];
     __shared__ int limits[PREFIX ? 2 * kTile : 1];            // per token of the job: end of the keys that it sees
     __shared__ uint32_t missing[PREFIX ? 16 : 1];             // per key tile: a bit per 16 keys without a page
     const AttnArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = a.group;
     if (PREFIX) grid_dep_launch();  // the own keys' CTAs start where this grid's have left
-    volatile int* abort = &abort_flag;
-    volatile int* busy = &busy_warps;
+    volatile int* abort = abort_busy;  // a wait gave up; warps with rows to compute once more
 
     const uint32_t q_smem = (smem_u32(raw) + 1023) & ~1023u, ring = q_smem + 2 * C::TILE_BYTES;
     if (tid == 0) {
@@ -286,7 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         mbar_init(smem_u32(&bars.place), 1);
         mbar_init(smem_u32(&bars.drain), 1);
         mbar_fence_init();
-        abort_flag = busy_warps = 0;
+        abort_busy[0] = abort_busy[1] = 0;
     }
     if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), 512);
     fence_before();
@@ -306,7 +305,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 return key < a.cache.prefix_len ? a.cache.prefix[key >> a.cache.page_bits] : -1;
             };
             for (;; ++count) {
-                ok = mbar_wait_busy(smem_u32(&bars.job[count & 1]), (count / 2) & 1, abort, busy);
+                ok = mbar_wait_busy(smem_u32(&bars.job[count & 1]), (count / 2) & 1, abort);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const Job job = jobs[count & 1];
                 __syncwarp();
@@ -315,7 +314,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 const int from = job.from, to = max(job.to[0], job.to[1]), tiles = to - from, begin = it;
                 for (int t = 0; t < 2 && ok; ++t) {
                     if (job.to[t] <= from) continue;
-                    if (q_uses[t]) ok = mbar_wait_busy(smem_u32(&bars.q_free[t]), (q_uses[t] - 1) & 1, abort, busy);
+                    if (q_uses[t]) ok = mbar_wait_busy(smem_u32(&bars.q_free[t]), (q_uses[t] - 1) & 1, abort);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     ++q_uses[t];
                     if (lane == 0) {
@@ -332,7 +331,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     if (lane == 0 && it == max(begin, begin + 2 * tiles - C::STAGES)) mbar_arrive(smem_u32(&bars.ahead));
                     const int stage = it % C::STAGES, j = from + ((it - begin) >> 1);
                     const bool value = (it - begin) & 1;
-                    if (it >= C::STAGES) ok = mbar_wait_busy(smem_u32(&bars.empty[stage]), (it / C::STAGES - 1) & 1, abort, busy);
+                    if (it >= C::STAGES) ok = mbar_wait_busy(smem_u32(&bars.empty[stage]), (it / C::STAGES - 1) & 1, abort);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     const uint32_t mbar = smem_u32(&bars.full[stage]), dst = ring + stage * C::TILE_BYTES;
                     const CUtensorMap* map = value ? &mv : &mk;
@@ -390,9 +389,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             const uint64_t v0 = smem_desc(ring, C::BLOCK_BYTES, 1024, kSwizzle128);
             bool ok = true;
             auto wait = [&](uint64_t* bar, int phase) {
-                bool there = mbar_spin(smem_u32(bar), phase & 1, abort);
-                while (!there && !*abort && *busy) there = mbar_spin(smem_u32(bar), phase & 1, abort);
-                ok = __all_sync(0xffffffffu, there);
+                ok = __all_sync(0xffffffffu, mbar_wait_busy(smem_u32(bar), phase & 1, abort));
                 if (!ok) *abort = 1;
                 return ok;
             };
@@ -475,7 +472,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             for (int count = 0;; ++count) {
                 const int b = count & 1;
                 auto wait = [&](uint64_t* bar, int phase) {
-                    return __all_sync(0xffffffffu, mbar_wait_busy(smem_u32(bar), phase & 1, abort, busy));
+                    return __all_sync(0xffffffffu, mbar_wait_busy(smem_u32(bar), phase & 1, abort));
                 };
                 bool ok = wait(&bars.job[b], count / 2);
                 if (ok) {
@@ -547,16 +544,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     found = find_job(a, pair_tokens, pairs, place / a.Hkv, places, place % a.Hkv, job);
                 }
                 if (found) {
-                    if (count >= 2) ok = mbar_wait_busy(smem_u32(&bars.job_free[count & 1]), (count / 2 - 1) & 1, abort, busy);
+                    if (count >= 2) ok = mbar_wait_busy(smem_u32(&bars.job_free[count & 1]), (count / 2 - 1) & 1, abort);
                     // the limits have one place, which those of the job before have to leave
-                    if (PREFIX && ok && count >= 1) ok = mbar_wait_busy(smem_u32(&bars.limits_free), (count - 1) & 1, abort, busy);
+                    if (PREFIX && ok && count >= 1) ok = mbar_wait_busy(smem_u32(&bars.limits_free), (count - 1) & 1, abort);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     if (PREFIX) mark_limits(a, job.i0, pair_tokens, limits);
                     if (lane == 0) {
                         jobs[count & 1] = job;
                         mbar_arrive(smem_u32(&bars.job[count & 1]));
                     }
-                    ok = __all_sync(0xffffffffu, mbar_wait_busy(smem_u32(&bars.ahead), count & 1, abort, busy));
+                    ok = __all_sync(0xffffffffu, mbar_wait_busy(smem_u32(&bars.ahead), count & 1, abort));
                     ++count;
                     if (!ok) break;
                 }
@@ -571,7 +568,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 __syncwarp();
             }
             // no more jobs
-            if (ok && count >= 2) ok = mbar_wait_busy(smem_u32(&bars.job_free[count & 1]), (count / 2 - 1) & 1, abort, busy);
+            if (ok && count >= 2) ok = mbar_wait_busy(smem_u32(&bars.job_free[count & 1]), (count / 2 - 1) & 1, abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) *abort = 1;
             if (ok && lane == 0) {
@@ -590,7 +587,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         int s_uses = 0, o_uses = 0;
         int tiles_before = 0;  // key tiles of the jobs so far
         for (int count = 0;; ++count) {
-            bool ok = mbar_wait_busy(smem_u32(&bars.job[count & 1]), (count / 2) & 1, abort, busy);
+            bool ok = mbar_wait_busy(smem_u32(&bars.job[count & 1]), (count / 2) & 1, abort);
             if (!(ok = __all_sync(0xffffffffu, ok))) {
                 *abort = 1;
                 break;
@@ -617,7 +614,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             float m = -INFINITY;
             float2 sum = make_float2(0.f, 0.f);
             for (int j = from, i = 0; j < end; ++j, ++i) {
-                ok = mbar_wait_busy(smem_u32(&bars.s[t]), s_uses++ & 1, abort, busy);
+                ok = mbar_wait_busy(smem_u32(&bars.s[t]), s_uses++ & 1, abort);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 fence_after();
                 float s[kTile];
@@ -677,7 +674,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars.p[t]));
             }
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_busy(smem_u32(&bars.o[t]), o_uses++ & 1, abort, busy));
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_busy(smem_u32(&bars.o[t]), o_uses++ & 1, abort));
             if (!ok) {
                 *abort = 1;
                 break;
@@ -738,7 +735,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             const bool finite = any == 0.f && l < INFINITY && (PREFIX || l > 0.f);
             // rows that an infinity or a NaN has reached, one after the other
             uint32_t bad = __ballot_sync(0xffffffffu, there && !finite);
-            if (bad && lane == 0) atomicAdd(&busy_warps, 1);
+            if (bad && lane == 0) atomicAdd(&abort_busy[1], 1);
             const bool again = bad;
             for (; bad; bad &= bad - 1) {
                 const int who = __ffs(bad) - 1;
@@ -772,14 +769,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 }
             }
             __syncwarp();
-            if (again && lane == 0) atomicSub(&busy_warps, 1);
+            if (again && lane == 0) atomicSub(&abort_busy[1], 1);
             if (lane == 0) mbar_arrive(smem_u32(&bars.job_free[count & 1]));
         }
     }
     fence_before();
     __syncwarp();
     __syncthreads();
-    if (tid == 0 && abort_flag) atomicOr(p.err, kAttnError);
+    if (tid == 0 && abort_busy[0]) atomicOr(p.err, kAttnError);
     if (warp == 9) {
         fence_after();
         tmem_dealloc(tmem, 512);
