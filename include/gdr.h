@@ -478,7 +478,7 @@ GDR_API int gdr_rmsnorm_bwd(const void* dy, int64_t dy_stride, const void* s, in
  *     not in [0, num_pages), has no row: its key is not written, and not seen.
  *   - cache_lens [N] int32 device: the tokens that sequence n had in the cache
  *     before this call's; both calls of a step take the same numbers.  A value
- *     < 0 is padding: nothing of that sequence is read or written.
+ *     < 0 is padding: nothing of that sequence is used or written.
  *   - A NaN or infinity reaches only the rows that see its token; where rows of
  *     the same tile do not, they are computed once more (slowly) without it.  A
  *     row that sees no key, or whose scores are all -inf, is 0.
@@ -486,6 +486,8 @@ GDR_API int gdr_rmsnorm_bwd(const void* dy, int64_t dy_stride, const void* s, in
  *     is written, but where a tensor is said to be in place; column blocks of the
  *     same rows share none.
  *   - Results do not depend on scheduling: equal inputs give equal bits.
+ *   - A wait inside a kernel that gives up sets bit 0x800 of the device error word;
+ *     o is then written in part.
  *
  * gdr_kv_append -- appends keys and values to the caches, rotary positions
  * applied on the way.  Token i of sequence n has position p = cache_lens[n] + i;
