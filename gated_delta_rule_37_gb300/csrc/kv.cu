@@ -6,9 +6,10 @@
 //   a' = a cos(p f) - b sin(p f),  b' = b cos(p f) + a sin(p f).
 // The angle counts only up to whole turns, and in 32 bits a far position has no
 // fraction of a turn left.  So f / 2 pi is kept as a fixed-point fraction of a turn
-// in 64 bits (formed in fp64, off by less than 2^-53 turns for f <= 1), and p times
-// it wraps modulo one turn by itself: the upper 32 bits are the angle, off by at most
-// p 2^-53 + 2^-33 turns, and a sine of half a turn or less remains.
+// in 64 bits, off by less than 2^-63 turns for f <= 1, and p times it wraps modulo one
+// turn by itself: the upper 32 bits are the angle, off by at most p 2^-63 + 2^-32
+// turns, and a sine of half a turn or less remains.  (All in integers: fp64 is two
+// operations a clock on an SM, which bound prompts of few heads.)
 #include <math.h>
 
 #include <mutex>
@@ -32,6 +33,7 @@ struct AppendParams {
     const int32_t* cu;
     int64_t T;
     int N, Hq, Hkv, R, pairs;
+    int tokens;  // of a block
     Paged c;
 };
 
@@ -88,57 +90,114 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&f)[8]) {
     *reinterpret_cast<uint4*>(p) = u;
 }
 
-// One block per (token, share of the heads).  A thread owns two 16-byte pieces of a
-// head's row, the pieces x and x + R / 2 where those turn with one another, and walks
-// over the heads.  What it reads of its first head does not depend on the token's place,
-// which takes four trips to memory in turn: it is asked for before them, and each next
-// head's before this one is turned and written.
-template <typename T, int D>
+// f / 2 pi modulo 1 in 64 bits.  With f = m 2^e, m of 24 bits, and K = 2^64 / 2 pi rounded, it is
+// m K 2^e: a product of 86 bits, shifted.
+__device__ __forceinline__ uint64_t turn_of(float f) {
+    constexpr uint64_t K = 0x28be60db9391054aull;
+    const uint32_t bits = __float_as_uint(f), field = bits >> 23 & 255;
+    const uint64_t m = (bits & 0x7fffffu) | (field ? 0x800000u : 0u);
+    const int right = 150 - (int)max(field, 1u);  // -e
+    const uint64_t lo = m * K, hi = __umul64hi(m, K);
+    uint64_t unit = 0;
+    if (right > 0 && right < 64) unit = lo >> right | hi << (64 - right);
+    else if (right >= 64 && right < 128) unit = hi >> (right - 64);
+    else if (right <= 0 && right > -64) unit = lo << -right;
+    return bits >> 31 ? 0 - unit : unit;
+}
+
+// The row of position pos of sequence n in the caches, of head 0; -1 where it has none.
+__device__ __forceinline__ int64_t cache_row(const AppendParams& p, int n, int64_t pos) {
+    const int64_t slot = pos >> p.c.page_bits;
+    if (slot >= p.c.max_pages) return -1;
+    const int page = p.c.table[n * p.c.table_ld + slot];
+    if (page < 0 || page >= p.c.num_pages) return -1;
+    return ((int64_t)page * p.Hkv << p.c.page_bits) + (pos & (p.c.page_size - 1));
+}
+
+constexpr int kMostTokens = 8;  // of a block
+
+// One block per (token, share of the heads), or with MANY per p.tokens tokens.  A thread owns
+// two 16-byte pieces of a head's row, the pieces x and x + R / 2 where those turn with one
+// another, and walks over the heads.  What it reads of its first head does not depend on
+// the token's place, which takes four trips to memory in turn: it is asked for before them,
+// and each next head's before this one is turned and written.
+template <typename T, int D, bool MANY>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
     constexpr int VEC = Pack16<T>::VEC, PIECES = D / (2 * VEC), LANES = kAppendThreads / PIECES;
-    __shared__ float2 turn[D / 2];
-    const int64_t t = blockIdx.x;
+    constexpr int TOKENS = MANY ? kMostTokens : 1;
+    __shared__ float2 turn[TOKENS][D / 2];
+    __shared__ int64_t places[TOKENS], rows[TOKENS];  // MANY: position, -1 for none, and row in the caches
+    const int64_t t0 = MANY ? (int64_t)blockIdx.x * p.tokens : blockIdx.x;
+    const int count = MANY ? (int)min((int64_t)p.tokens, p.T - t0) : 1;
     const int half = p.R / 2;
     const int piece = threadIdx.x % PIECES, lane = threadIdx.x / PIECES + LANES * blockIdx.y;
-    const int heads = p.Hq + 2 * p.Hkv;
+    const int heads = p.Hq + 2 * p.Hkv, items = heads * count;  // of one token after the other
     // the pieces' channels, and whether they turn with one another element by element
     const bool across = !p.pairs && piece * VEC < half;
     const int c0 = across ? piece * VEC : p.pairs ? piece * 2 * VEC : 2 * half + (piece - half / VEC) * 2 * VEC;
     const int c1 = across ? c0 + half : c0 + VEC;
     uint4 next[2];
-    auto ask = [&](int h) {
+    auto ask = [&](int item) {
+        const int tok = MANY ? item / heads : 0, h = item - tok * heads;
+        const int64_t t = t0 + tok;
         const T* from = h < p.Hq           ? static_cast<const T*>(p.q) + t * p.ldq + (int64_t)h * D
                         : h < p.Hq + p.Hkv ? static_cast<const T*>(p.k) + t * p.ldk + (int64_t)(h - p.Hq) * D
                                            : static_cast<const T*>(p.v) + t * p.ldv + (int64_t)(h - p.Hq - p.Hkv) * D;
         next[0] = *reinterpret_cast<const uint4*>(from + c0);
         next[1] = *reinterpret_cast<const uint4*>(from + c1);
     };
-    if (lane < heads) ask(lane);
-    if (p.cu[0] > t) return;
-    const int n = find_sequence(p.cu, p.N, t);
-    if (n >= p.N || t >= p.cu[n + 1]) return;  // behind the last sequence
-    const int len = p.c.lens[n];
-    if (len < 0) return;
-    const int64_t pos = (int64_t)len + (t - p.cu[n]);
-    for (int j = threadIdx.x; j < half; j += kAppendThreads) {
-        const double turns = (double)p.freqs[j] * 0.15915494309189533577;
-        const long long unit = (long long)((turns - rint(turns)) * 18446744073709551616.0);
-        const long long angle = (long long)((unsigned long long)unit * (unsigned long long)pos);
+    if (lane < items) ask(lane);
+    int n = 0;
+    int64_t pos = 0, row = -1;
+    if (MANY) {
+        if (threadIdx.x < count) {
+            // the last sequence that begins at or before the token
+            const int64_t t = t0 + threadIdx.x;
+            int hi = p.N;
+            while (hi > n) {
+                const int mid = (n + hi + 1) / 2;
+                if (p.cu[mid] <= t) n = mid; else hi = mid - 1;
+            }
+            pos = -1;
+            if (n < p.N && p.cu[n] <= t && t < p.cu[n + 1]) {
+                const int len = p.c.lens[n];
+                if (len >= 0) {
+                    pos = (int64_t)len + (t - p.cu[n]);
+                    row = cache_row(p, n, pos);
+                }
+            }
+            places[threadIdx.x] = pos;
+            rows[threadIdx.x] = row;
+        }
+        __syncthreads();
+    } else {
+        if (p.cu[0] > t0) return;
+        n = find_sequence(p.cu, p.N, t0);
+        if (n >= p.N || t0 >= p.cu[n + 1]) return;  // behind the last sequence
+        const int len = p.c.lens[n];
+        if (len < 0) return;
+        pos = (int64_t)len + (t0 - p.cu[n]);
+    }
+    for (int i = threadIdx.x; i < half * count; i += kAppendThreads) {
+        const int tok = MANY ? i / half : 0, j = i - tok * half;
+        const uint64_t angle = turn_of(p.freqs[j]) * (uint64_t)(MANY ? places[tok] : pos);
         float s, c;
         sincospif((float)(int)(angle >> 32) * 0x1p-31f, &s, &c);
-        turn[j] = make_float2(c, s);
+        turn[tok][j] = make_float2(c, s);
     }
     __syncthreads();
 
-    int64_t row = -1;  // the token's row in the caches, of head 0
-    const int64_t slot = pos >> p.c.page_bits;
-    if (slot < p.c.max_pages) {
-        const int page = p.c.table[n * p.c.table_ld + slot];
-        if (page >= 0 && page < p.c.num_pages)
-            row = ((int64_t)page * p.Hkv << p.c.page_bits) + (pos & (p.c.page_size - 1));
-    }
+    if (!MANY) row = cache_row(p, n, pos);
     const int step = LANES * gridDim.y;
-    for (int h = lane; h < heads; h += step) {
+    for (int item = lane; item < items; item += step) {
+        const int tok = MANY ? item / heads : 0, h = item - tok * heads;
+        const int64_t t = t0 + tok;
+        if (MANY) row = rows[tok];
+        float x[VEC], y[VEC];
+        spread(next[0], x);
+        spread(next[1], y);
+        if (item + step < items) ask(item + step);
+        if (MANY && places[tok] < 0) continue;
         T* dense = nullptr;
         T* cached = nullptr;
         if (h < p.Hq) {
@@ -150,15 +209,12 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
             if (row >= 0)
                 cached = static_cast<T*>(key ? p.c.k : p.c.v) + (row + ((int64_t)kv << p.c.page_bits)) * D;
         }
-        float x[VEC], y[VEC];
-        spread(next[0], x);
-        spread(next[1], y);
-        if (h + step < heads) ask(h + step);
         if (h < p.Hq + p.Hkv && half > 0) {
+            const float2* const w_of = turn[tok];
             if (across) {
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    const float2 w = turn[c0 + i];
+                    const float2 w = w_of[c0 + i];
                     const float a = x[i], b = y[i];
                     x[i] = a * w.x - b * w.y;
                     y[i] = b * w.x + a * w.y;
@@ -167,13 +223,13 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
 #pragma unroll
                 for (int i = 0; i < VEC; i += 2) {
                     if (c0 + i < p.R) {
-                        const float2 w = turn[(c0 + i) / 2];
+                        const float2 w = w_of[(c0 + i) / 2];
                         const float a = x[i], b = x[i + 1];
                         x[i] = a * w.x - b * w.y;
                         x[i + 1] = b * w.x + a * w.y;
                     }
                     if (c1 + i < p.R) {
-                        const float2 w = turn[(c1 + i) / 2];
+                        const float2 w = w_of[(c1 + i) / 2];
                         const float a = y[i], b = y[i + 1];
                         y[i] = a * w.x - b * w.y;
                         y[i + 1] = b * w.x + a * w.y;
@@ -193,15 +249,23 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
 }
 
 template <typename T, int D>
-cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
+cudaError_t launch_append(AppendParams p, cudaStream_t s) {
     constexpr int LANES = kAppendThreads / (D / (2 * Pack16<T>::VEC));
-    // few tokens: their heads over several blocks
+    // few tokens: their heads over several blocks; many of few heads: several to a block, as long
+    // as that leaves eight blocks to an SM and gives a thread no more than four pairs of pieces
+    // (measured, several / one: 14998 tokens of 2 + 2 heads of 128 17 / 30 us, 16000 of 8 + 1 of 64
+    // 15 / 28, 7001 of 12 + 4 of 64 in fp32 19 / 20; a prompt of 32768 tokens of 32 + 8 heads, which has
+    // one to a block, 143 us: 6.1 TB/s)
     const int heads = p.Hq + 2 * p.Hkv, most = (heads + LANES - 1) / LANES;
     const int64_t full = (int64_t)sm_count() * 8;
     const int64_t share = p.T < full ? full / (p.T > 0 ? p.T : 1) : 1;
-    const dim3 grid((unsigned)p.T, (unsigned)(share < most ? share : most));
+    p.tokens = 1;
+    while (p.tokens < kMostTokens && p.T / (2 * p.tokens) >= full && 2 * p.tokens * heads <= 4 * LANES) p.tokens *= 2;
     KernelTimer kt("kv_append", s);
-    kv_append_kernel<T, D><<<grid, kAppendThreads, 0, s>>>(p);
+    if (p.tokens > 1)
+        kv_append_kernel<T, D, true><<<(unsigned)((p.T + p.tokens - 1) / p.tokens), kAppendThreads, 0, s>>>(p);
+    else
+        kv_append_kernel<T, D, false><<<dim3((unsigned)p.T, (unsigned)(share < most ? share : most)), kAppendThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -261,3 +261,40 @@ def test_layer_in_place_in_one_projection():
     assert bits_equal(q.contiguous(), qa) and bits_equal(k.contiguous(), ka)
     assert bits_equal(rows[:, (Hq + Hkv) * D:].contiguous(), kept[:, (Hq + Hkv) * D:].contiguous())
     assert bits_equal(gdr.attn_fwd(q, k, v, cu), gdr.attn_fwd(qa, ka, v.contiguous(), cu))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("Hq,Hkv,D,R,pairs", [(2, 2, 128, 128, False), (8, 1, 64, 32, True), (0, 1, 64, 64, False),
+                                              (16, 2, 128, 64, False)])
+def test_append_of_many_tokens_is_that_of_few(Hq, Hkv, D, R, pairs, dtype):
+    """Blocks that have several tokens give the bits of blocks that have one: rows behind the last sequence, empty
+    sequences, padding, missing pages and places beyond the table among them."""
+    page, N = 32, 61
+    lengths = [(0, 1, 400, 7, 233, 64, 331)[i % 7] for i in range(N)]
+    lens = [-1 if i % 10 == 4 else (i * 37) % 90 for i in range(N)]
+    T, first = sum(lengths), np.cumsum([0, *lengths])
+    assert T // 2 >= 152 * 8 and max(lengths) < 2 * 152 * 8
+    width = max(-(-(a + n) // page) for a, n in zip(lens, lengths)) - 1  # the longest lacks its last page
+    order = np.random.default_rng(1).permutation(N * width)
+    table = torch.from_numpy(order.reshape(N, width).astype(np.int32)).to(DEV)
+    table[3, 1], table[5, 0] = -1, N * width
+    q, k, v = (normal(i, T + 5, H, D, dtype=dtype) if H else None for i, H in ((1, Hq), (2, Hkv), (3, Hkv)))
+    f = normal(4, R // 2, std=0.3)
+    flags = gdr.GDR_ROPE_PAIRS if pairs else 0
+
+    def call(kc, vc, a, b, q_out, k_out):
+        part = slice(first[a], first[b] if b < N else T + 5)
+        cut = lambda t: None if t is None else t[part]
+        gdr.kv_append(k[part], v[part], kc, vc, table[a:b], ints(lens[a:b]), starts(lengths[a:b]), q=cut(q), freqs=f,
+                      flags=flags, q_out=cut(q_out), k_out=k_out[part])
+
+    out = []
+    for cuts in ([0, N], [*range(0, N, 4), N]):
+        kc = torch.full((N * width, Hkv, page, D), 9.0, dtype=dtype, device=DEV)
+        vc = kc.clone()
+        q_out, k_out = (torch.full_like(t, 5.0) if t is not None else None for t in (q, k))
+        for a, b in zip(cuts[:-1], cuts[1:]):
+            call(kc, vc, a, b, q_out, k_out)
+        out.append([t for t in (kc, vc, q_out, k_out) if t is not None])
+    assert all(bits_equal(x, y) for x, y in zip(*out))
+    assert (out[0][-1][T:] == 5.0).all() and (out[0][0] == 9.0).any()
