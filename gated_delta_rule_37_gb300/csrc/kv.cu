@@ -253,9 +253,9 @@ cudaError_t launch_append(AppendParams p, cudaStream_t s) {
     constexpr int LANES = kAppendThreads / (D / (2 * Pack16<T>::VEC));
     // few tokens: their heads over several blocks; many of few heads: several to a block, as long
     // as that leaves eight blocks to an SM and gives a thread no more than four pairs of pieces
-    // (measured, several / one: 14998 tokens of 2 + 2 heads of 128 17 / 30 us, 16000 of 8 + 1 of 64
-    // 15 / 28, 7001 of 12 + 4 of 64 in fp32 19 / 20; a prompt of 32768 tokens of 32 + 8 heads, which has
-    // one to a block, 143 us: 6.1 TB/s)
+    // (measured, several / one, when the angles still took fp64: 14998 tokens of 2 + 2 heads of 128
+    // 22 / 35 us, 16000 of 8 + 1 of 64 18 / 33, 7001 of 12 + 4 of 64 in fp32 19.5 / 20.8; with integers
+    // 17, 15 and 19.  A prompt of 32768 tokens of 32 + 8 heads has one to a block: 143 us, 6.1 TB/s.)
     const int heads = p.Hq + 2 * p.Hkv, most = (heads + LANES - 1) / LANES;
     const int64_t full = (int64_t)sm_count() * 8;
     const int64_t share = p.T < full ? full / (p.T > 0 ? p.T : 1) : 1;
