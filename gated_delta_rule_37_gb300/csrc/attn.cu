@@ -503,15 +503,11 @@ __global__ void __launch_bounds__(kMergeThreads) step_merge_prefix_kernel(const 
 // Tokens that a tensor map takes: none overlaps its neighbour.
 bool tiled(int64_t ld, int heads, int D) { return ld >= (int64_t)heads * D; }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 template <typename T, int D, int RT>
 cudaError_t launch_prompt_rows(const AttnArgs& a, cudaStream_t s) {
     const size_t bytes = sizeof(typename Simt<T, D, RT>::Smem);
-    const cudaError_t e = allow_smem(prompt_simt_kernel<T, D, RT>, bytes);
+    static std::atomic<uint64_t> known{0};
+    const cudaError_t e = allow_smem(prompt_simt_kernel<T, D, RT>, (int)bytes, known);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (a.T * a.group + RT - 1) / RT + a.N;
     KernelTimer kt("attn_prompt_simt", s);
@@ -535,7 +531,8 @@ cudaError_t launch_prompt_simt(const AttnArgs& a, cudaStream_t s) {
 template <typename T, int D, int RT>
 cudaError_t launch_prefix_simt(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
     const size_t bytes = sizeof(typename Simt<T, D, RT>::Smem);
-    const cudaError_t e = allow_smem(prefix_simt_kernel<T, D, RT>, bytes);
+    static std::atomic<uint64_t> known{0};
+    const cudaError_t e = allow_smem(prefix_simt_kernel<T, D, RT>, (int)bytes, known);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (a.T * a.group + RT - 1) / RT;
     KernelTimer kt("attn_prefix_simt", s);
@@ -546,7 +543,8 @@ cudaError_t launch_prefix_simt(const AttnArgs& a, const StepWork& w, cudaStream_
 template <int D, int RT>
 cudaError_t launch_step_simt(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
     const size_t bytes = sizeof(typename Simt<float, D, RT>::Smem);
-    const cudaError_t e = allow_smem(step_simt_kernel<float, D, RT>, bytes);
+    static std::atomic<uint64_t> known{0};
+    const cudaError_t e = allow_smem(step_simt_kernel<float, D, RT>, (int)bytes, known);
     if (e != cudaSuccess) return e;
     KernelTimer kt("attn_step_simt", s);
     step_simt_kernel<float, D, RT><<<w.ctas, 256, bytes, s>>>(a, w);

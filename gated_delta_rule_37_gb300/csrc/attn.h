@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace gdr {
 
 // A pair of paged caches and the sequences' pages.
@@ -54,6 +56,20 @@ int check_apart(const MemRows& written, const MemRows& other);
 int validate_attention(const int32_t* cu, int N, int64_t T, const Paged* c, cudaStream_t s);
 
 struct StepWork;
+
+// A number of the current context that no other one of this process has; 0 if there is none.
+uint64_t context_number();
+
+// Allows `kernel` its dynamic shared memory.  The attribute belongs to the context, and setting
+// it costs a fifth of a launch: `known` (one per kernel) keeps the context that has it.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& known) {
+    const uint64_t now = context_number();
+    if (now != 0 && known.load(std::memory_order_relaxed) == now) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) known.store(now, std::memory_order_relaxed);
+    return e;
+}
 
 // Tensor-core paths (bf16).
 cudaError_t launch_prompt_tc(const AttnArgs& a, cudaStream_t s);

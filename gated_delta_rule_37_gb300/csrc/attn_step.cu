@@ -481,9 +481,8 @@ cudaError_t launch_rows(StepParams p, cudaStream_t s) {
     const int64_t rows = (int64_t)p.a.cache.num_pages * p.a.Hkv << p.a.cache.page_bits;
     if (!encode_cache(&mk, p.a.cache.k, rows, D, p.box) || !encode_cache(&mv, p.a.cache.v, rows, D, p.box))
         return cudaErrorInvalidValue;
-    // at every call: the attribute belongs to the context
-    const cudaError_t set =
-        cudaFuncSetAttribute(step_kernel<D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static std::atomic<uint64_t> known{0};
+    const cudaError_t set = allow_smem(step_kernel<D, ROWS>, C::SMEM, known);
     if (set != cudaSuccess) return set;
     KernelTimer kt("attn_step", s);
     // behind the prefix's kernel, which reads the same inputs and writes nothing that this one reads

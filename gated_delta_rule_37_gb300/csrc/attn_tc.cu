@@ -788,9 +788,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 template <int D, bool PREFIX>
 cudaError_t launch_tc(TcParams p, dim3 grid, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                       cudaStream_t s) {
-    // at every call: the attribute belongs to the context
-    const cudaError_t set = cudaFuncSetAttribute(attn_tc_kernel<D, PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 Shape<D>::SMEM);
+    static std::atomic<uint64_t> known{0};
+    const cudaError_t set = allow_smem(attn_tc_kernel<D, PREFIX>, Shape<D>::SMEM, known);
     if (set != cudaSuccess) return set;
     // a warpgroup that asks for more registers than the block was launched with waits forever
     static std::atomic<bool> enough{false};
@@ -808,6 +807,23 @@ cudaError_t launch_tc(TcParams p, dim3 grid, const CUtensorMap& mq, const CUtens
 }
 
 }  // namespace
+
+uint64_t context_number() {
+    using GetId = CUresult (*)(CUcontext, unsigned long long*);
+    static std::atomic<GetId> known{nullptr};
+    GetId get = known.load(std::memory_order_acquire);
+    if (!get) {
+        void* entry = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuCtxGetId", &entry, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            return 0;
+        get = reinterpret_cast<GetId>(entry);
+        known.store(get, std::memory_order_release);
+    }
+    unsigned long long id = 0;
+    return get(nullptr, &id) == CUDA_SUCCESS ? id + 1 : 0;
+}
 
 int prefix_block_tokens(int group) { return 2 * (kTile / group); }
 
