@@ -423,8 +423,8 @@ __device__ __forceinline__ void join_parts(int count, int first, int step, S sta
     }
 }
 
-// Without a prefix: the row tiles that are cut, blockIdx = (CTA that has the first part, row);
-// the block's warps share the parts, of which one long sequence has many.
+// Without a prefix: the row tiles that are cut, blockIdx = (CTA that has the first part, share
+// of its rows); the block's warps share the parts of a row, of which one long sequence has many.
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads) step_merge_kernel(const AttnArgs a, const StepWork w) {
     constexpr int C = D / 32;
@@ -432,29 +432,31 @@ __global__ void __launch_bounds__(kMergeThreads) step_merge_kernel(const AttnArg
     __shared__ float ls[kMergeWarps];
     grid_dep_wait();
     const Cut cut = w.cuts[blockIdx.x];
-    const int r = blockIdx.y, cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (r >= cut.rows) return;
-    auto place = [&](int i) { return ((int64_t)(cta + i) * 2 + (i == 0)) * w.rows + r; };
-    float acc[C], l;
-    join_parts(cut.parts, warp, kMergeWarps, [&](int i) { return w.slot_stat + place(i); },
-               [&](int i) { return w.slot_sum + place(i) * D; }, acc, l);
-    Vec<float, C>::store(&sums[warp][lane * C], acc);
-    if (lane == 0) ls[warp] = l;
-    __syncthreads();
-    const int d = threadIdx.x * 2;
-    if (d >= D) return;
-    float x[2] = {0.f, 0.f}, y = 0.f;
+    const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = threadIdx.x * 2;
+    for (int r = blockIdx.y; r < cut.rows; r += gridDim.y) {
+        auto place = [&](int i) { return ((int64_t)(cta + i) * 2 + (i == 0)) * w.rows + r; };
+        float acc[C], l;
+        join_parts(cut.parts, warp, kMergeWarps, [&](int i) { return w.slot_stat + place(i); },
+                   [&](int i) { return w.slot_sum + place(i) * D; }, acc, l);
+        Vec<float, C>::store(&sums[warp][lane * C], acc);
+        if (lane == 0) ls[warp] = l;
+        __syncthreads();
+        if (d < D) {
+            float x[2] = {0.f, 0.f}, y = 0.f;
 #pragma unroll
-    for (int i = 0; i < kMergeWarps; ++i) {
-        x[0] += sums[i][d];
-        x[1] += sums[i][d + 1];
-        y += ls[i];
+            for (int i = 0; i < kMergeWarps; ++i) {
+                x[0] += sums[i][d];
+                x[1] += sums[i][d + 1];
+                y += ls[i];
+            }
+            const float inv = y > 0.f ? 1.f / y : y == 0.f ? 0.f : y;
+            x[0] *= inv;
+            x[1] *= inv;
+            const int row = cut.r0 + r, local = row / a.group, head = cut.h * a.group + row - local * a.group;
+            Vec<T, 2>::store(static_cast<T*>(a.o) + (int64_t)(cut.t0 + local) * a.ldo + (int64_t)head * D + d, x);
+        }
+        __syncthreads();
     }
-    const float inv = y > 0.f ? 1.f / y : y == 0.f ? 0.f : y;
-    x[0] *= inv;
-    x[1] *= inv;
-    const int row = cut.r0 + r, local = row / a.group, head = cut.h * a.group + row - local * a.group;
-    Vec<T, 2>::store(static_cast<T*>(a.o) + (int64_t)(cut.t0 + local) * a.ldo + (int64_t)head * D + d, x);
 }
 
 // With a prefix, which every row has partial results of: blockIdx = (sequence, key head, share
@@ -555,7 +557,8 @@ template <typename T, int D>
 cudaError_t launch_merge(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
     KernelTimer kt("attn_step_merge", s);
     if (w.splits == 0)
-        return launch_dependent(step_merge_kernel<T, D>, dim3(w.ctas, w.rows), dim3(kMergeThreads), 0, s, a, w);
+        return launch_dependent(step_merge_kernel<T, D>, dim3(w.ctas, w.rows < 16 ? w.rows : 16), dim3(kMergeThreads), 0,
+                                s, a, w);
     const int64_t rows = (a.T + a.N - 1) / a.N * a.group;  // of a sequence and key head, on average
     const int64_t shares = (rows + kMergeWarps - 1) / kMergeWarps;
     return launch_dependent(step_merge_prefix_kernel<T, D>, dim3(a.N, a.Hkv, (unsigned)(shares < 64 ? shares : 64)),
