@@ -566,18 +566,26 @@ cudaError_t launch_merge(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
 }
 
 // Rows per tile of the own keys' part, by the rows that a sequence has on average: a
-// tile's cost grows with it, and rows beyond the first tile read the keys again.
+// tile's cost grows with it, and rows beyond the first tile read the keys again.  (fp32, 32 rows
+// against 64, which leave room for one CTA on an SM: 20 sequences of up to 12 tokens and 4000
+// keys, 16 heads of 128 on 2, 117 / 156 us; 28 of few keys 20 / 23; 100 of up to 1000, 32 heads of 64
+// on 8, 242 / 248.)
 int rows_per_tile(int N, int64_t T, int group, int dtype) {
     const int64_t rows = (T + N - 1) / (N > 0 ? N : 1) * group;
     if (dtype == GDR_F32 && rows <= 8) return rows <= 4 ? 4 : 8;
-    return rows <= 16 ? 16 : rows <= 32 && dtype == GDR_BF16 ? 32 : 64;
+    return rows <= 16 ? 16 : rows <= 32 || dtype == GDR_F32 ? 32 : 64;
 }
 
-// Rows per tile of the prefix on the CUDA cores.
-int far_rows(const StepWork& w) { return w.rows <= 16 ? 16 : 64; }
+// Rows per tile of the prefix in fp32, by the rows that the batch has on a key head.  (All
+// kernels, 128 against 64: 32 sequences of up to 12 tokens behind 4000, 16 heads of 128 on 2, 270 / 304 us;
+// 64 against 16: 200 of one token behind 3000, 8 heads of 64 on one, 68 / 100 us.)
+int far_rows(int64_t T, int group, int D) {
+    const int64_t rows = T * group;
+    return rows >= 128 && D == 128 ? 128 : rows > 16 ? 64 : 16;
+}
 
 // Cuts of the prefix along its keys: about as many CTAs as the GPU holds at once.
-void prefix_cuts(StepWork* w, int64_t T, int Hkv, int group, int prefix_len, int dtype) {
+void prefix_cuts(StepWork* w, int64_t T, int Hkv, int group, int D, int prefix_len, int dtype) {
     w->splits = w->far_ctas = w->far_tokens = 0;
     if (prefix_len == 0) return;
     const int64_t tiles = (prefix_len + kFarTile - 1) / kFarTile;
@@ -592,8 +600,9 @@ void prefix_cuts(StepWork* w, int64_t T, int Hkv, int group, int prefix_len, int
         w->splits = (int)(parts < tiles ? parts : tiles);
         return;
     }
-    const int64_t blocks = (T * group + far_rows(*w) - 1) / far_rows(*w) * Hkv;
-    int64_t splits = 2 * kSms / blocks;
+    const int rows = far_rows(T, group, D);
+    const int64_t blocks = (T * group + rows - 1) / rows * Hkv;
+    int64_t splits = (rows >= 64 && D == 128 ? 1 : 2) * kSms / blocks;  // CTAs that the GPU holds at once
     if (splits > tiles) splits = tiles;
     if (splits < 1) splits = 1;
     w->splits = (int)(splits < kMaxSplits ? splits : kMaxSplits);
@@ -610,7 +619,7 @@ size_t step_layout(StepWork* w, char* base, int N, int64_t T, int Hq, int Hkv, i
     };
     w->rows = rows_per_tile(N, T, Hq / Hkv, dtype);
     w->ctas = dtype == GDR_BF16 || w->rows == 8 ? kSms : 2 * kSms;  // what the GPU holds at once
-    prefix_cuts(w, T, Hkv, Hq / Hkv, prefix_len, dtype);
+    prefix_cuts(w, T, Hkv, Hq / Hkv, D, prefix_len, dtype);
     const size_t slots = (size_t)w->ctas * 2 * w->rows, rows = w->splits ? (size_t)T * Hq : 0;
     w->offsets = reinterpret_cast<int64_t*>(part(sizeof(int64_t) * ((size_t)N + 1)));
     w->cuts = reinterpret_cast<Cut*>(part(sizeof(Cut) * w->ctas));
@@ -632,12 +641,16 @@ cudaError_t launch_step(const AttnArgs& a, StepWork w, cudaStream_t s) {
         if (e == cudaSuccess) e = launch_step_own(a, w, s);
         return e == cudaSuccess ? launch_merge<__nv_bfloat16, D>(a, w, s) : e;
     }
-    if (w.splits > 0)
-        e = far_rows(w) == 16 ? launch_prefix_simt<float, D, 16>(a, w, s) : launch_prefix_simt<float, D, 64>(a, w, s);
+    if (w.splits > 0) {
+        const int rows = far_rows(a.T, a.group, D);
+        e = rows == 16   ? launch_prefix_simt<float, D, 16>(a, w, s)
+            : rows == 64 ? launch_prefix_simt<float, D, 64>(a, w, s)
+                         : launch_prefix_simt<float, D, D == 128 ? 128 : 64>(a, w, s);
+    }
     if (e == cudaSuccess)
         e = w.rows <= 8    ? launch_step_few(a, w, s)
             : w.rows == 16 ? launch_step_simt<D, 16>(a, w, s)
-                           : launch_step_simt<D, 64>(a, w, s);
+                           : launch_step_simt<D, 32>(a, w, s);
     return e == cudaSuccess ? launch_merge<float, D>(a, w, s) : e;
 }
 
