@@ -85,11 +85,9 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int rows_per_tile, in
     return span_of(a, rows_per_tile, a.cu[n], a.cu[n + 1], a.cache.lens[n]);
 }
 
-// The CTAs that take part: each at least `kLeast` tiles, as long as there are fewer than
-// would give all of them that.
-constexpr int kLeast = 1;
+// The CTAs that take part, if there is less work than CTAs.
 __device__ __forceinline__ int64_t taking_part(int64_t units, int ctas) {
-    return max((int64_t)1, min((int64_t)ctas, (units + kLeast - 1) / kLeast));
+    return max((int64_t)1, min((int64_t)ctas, units));
 }
 
 struct Plan {
