@@ -566,7 +566,10 @@ cudaError_t launch_merge(const AttnArgs& a, const StepWork& w, cudaStream_t s) {
 }
 
 // Rows per tile of the own keys' part, by the rows that a sequence has on average: a
-// tile's cost grows with it, and rows beyond the first tile read the keys again.  (fp32, 32 rows
+// tile's cost grows with it, and rows beyond the first tile read the keys again.  (bf16, own
+// keys of up to 2000: 16 rows against 32, 64 sequences with 18 rows 26 / 27 us, with 26, 32 heads of 64
+// on 8, 71 / 65; 32 against 64, 64 with 51 rows 44 / 47, the same behind a prefix 70 / 68, 4 with 1037
+// rows 217 / 176.  fp32, 32 rows
 // against 64, which leave room for one CTA on an SM: 20 sequences of up to 12 tokens and 4000
 // keys, 16 heads of 128 on 2, 117 / 156 us; 28 of few keys 20 / 23; 100 of up to 1000, 32 heads of 64
 // on 8, 242 / 248.)

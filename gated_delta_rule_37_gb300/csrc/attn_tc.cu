@@ -51,7 +51,8 @@ constexpr int kWarps = 12;                // 2 x 4 of softmax; copies, MMAs, val
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "more registers than the block has");
 constexpr int kNoRow = 0x7fffffff;        // the limit of a lane without a row: it masks nothing
-constexpr float kLag = 8.f;               // how far P's reference may lag behind the maximum, log2 units
+// How far P's reference may lag behind the maximum, log2 units (8 / 0: 32768 tokens 5.5 / 5.8 ms).
+constexpr float kLag = 8.f;
 
 template <int D> struct Shape {
     static constexpr int BLOCKS = D / 64;                  // 128-byte column blocks of a row
@@ -168,7 +169,9 @@ __device__ __forceinline__ void mark_limits(const AttnArgs& a, int64_t first, in
     __syncwarp();
 }
 
-constexpr int kSorted = 64;  // sequences, two of a lane
+// Sequences, two of a lane.  (Sorted / in their own order: 4 prompts of 65 to 3000 tokens 60 / 63 us, 64
+// of 16001 in all 50 / 53.)
+constexpr int kSorted = 64;
 
 // The pair of row tiles at a place of a prompt's call, by a warp; false where the place is
 // empty.  Up to kSorted sequences (pairs: those of sequences lane and lane + 32): first all
