@@ -14,7 +14,7 @@
 // With up to 16 rows two sets of four warps take the tiles in turn; with more, rows are what
 // the warps share out first: fewer results to join.
 //   Measured: 256 sequences of up to 4096 keys, 32 heads of 128 on 8, 300 us, 6.5 TB/s; one of 65536
-// 50 us, of which 5 pass before the first tile is there and 4 in the merge; 230 of up to 1024 behind
+// 50 us, of which 5 pass before the first tile is there, the last ones in the merge; 230 of up to 1024 behind
 // a prefix 80 us, 6.1 TB/s, where a run's beginning and end (1.9 us) count.
 #include <math.h>
 
