@@ -9,8 +9,8 @@
 // of a tile, which lie in one page, and a running maximum and sum of its own; the eight
 // warps' results are joined at the end of a run.
 //   Measured (against the tiles of 16 rows through shared memory): 64 sequences of up to 4096
-// keys, 8 heads of 128 with 4 rows each, 212 us (409; 0.92 GB: 4.3 TB/s), 16 heads of 64 with
-// one row 244 us (487); 256 of up to 300, 2 heads with 7 rows, 46 us (61).  What bounds it is the
+// keys, 8 heads of 128 with 4 rows each, 174 us (409; 0.92 GB: 5.3 TB/s), 16 heads of 64 with
+// one row 176 us (487); 256 of up to 300, 2 heads with 7 rows, 46 us (61).  What bounds it is the
 // rows under way: a warp waits for its 4 or 8 keys before it asks for the next.
 #include <math.h>
 
@@ -26,6 +26,10 @@ namespace {
 
 constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
 constexpr int kWarpKeys = kKeyTile / kFewWarps;  // of a tile
+
+__device__ __forceinline__ void prefetch_line(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" :: "l"(p));
+}
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kFewThreads, ROWS == 4 ? 2 : 1) step_few_kernel(const AttnArgs a, const StepWork w) {
@@ -65,12 +69,30 @@ __global__ void __launch_bounds__(kFewThreads, ROWS == 4 ? 2 : 1) step_few_kerne
             const int64_t j = (int64_t)k * kKeyTile + warp * kWarpKeys;
             return k < run.to && j < most ? pages[j >> a.cache.page_bits] : -1;
         };
-        int next = page_of(run.from);
+        auto row_of = [&](int page, int j) {
+            return (((int64_t)page * a.Hkv + h) << a.cache.page_bits) + (j & (a.cache.page_size - 1));
+        };
+        // With 4 rows the next tile's rows go to L2 while this one's are worked on (64 sequences of up
+        // to 4096 keys, 8 heads of 128: 174 / 212 us); with 8 registers are short (256 of up to 300: 62 / 46).
+        constexpr bool FETCH = ROWS == 4;
+        int ahead = page_of(run.from), next = FETCH ? page_of(run.from + 1) : 0;
         for (int k = run.from; k < run.to; ++k) {
-            const int page = next, j0 = k * kKeyTile + warp * kWarpKeys;
-            next = page_of(k + 1);
+            const int page = ahead, j0 = k * kKeyTile + warp * kWarpKeys;
+            if (FETCH) {
+                ahead = next;
+                next = page_of(k + 2);
+                if (ahead >= 0 && ahead < a.cache.num_pages) {
+                    constexpr int LINES = kWarpKeys * D / 32;  // of 128 bytes: a warp's keys are dense
+                    const int64_t at = row_of(ahead, j0 + kKeyTile) * D;
+#pragma unroll
+                    for (int i = lane; i < 2 * LINES; i += 32)
+                        prefetch_line(static_cast<const float*>(i < LINES ? a.cache.k : a.cache.v) + at + i % LINES * 32);
+                }
+            } else {
+                ahead = page_of(k + 1);
+            }
             if (page < 0 || page >= a.cache.num_pages || j0 >= most || j0 + kWarpKeys <= least) continue;
-            const int64_t row = (((int64_t)page * a.Hkv + h) << a.cache.page_bits) + (j0 & (a.cache.page_size - 1));
+            const int64_t row = row_of(page, j0);
             const float* kp = static_cast<const float*>(a.cache.k) + (row + second) * D + sub * 4;
             const float* vp = static_cast<const float*>(a.cache.v) + (row + second) * D + sub * 4;
             const bool edge = j0 < least || j0 + kWarpKeys > all_see;
