@@ -677,6 +677,14 @@ int check_attention(int N, int64_t T, int Hq, int Hkv, int D, int dtype) {
     return GDR_OK;
 }
 
+// The prefix's positions, as the table's: its tiles' ends are counted in 32 bits.
+int check_prefix(int prefix_len) {
+    if (prefix_len < 0) return set_last_error(GDR_ERR_INVALID_ARG, "prefix_len (%d) negative", prefix_len);
+    if (prefix_len > 0x7fffffff - 256)
+        return set_last_error(GDR_ERR_UNSUPPORTED, "prefix_len (%d) above 2^31 - 257", prefix_len);
+    return GDR_OK;
+}
+
 }  // namespace
 }  // namespace gdr
 
@@ -724,7 +732,7 @@ int gdr_attn_step_workspace_size(int N, int64_t T_total, int Hq, int Hkv, int D,
                                  size_t* bytes) {
     if (!bytes) return set_last_error(GDR_ERR_INVALID_ARG, "bytes is NULL");
     if (int rc = check_attention(N, T_total, Hq, Hkv, D, dtype)) return rc;
-    if (prefix_len < 0) return set_last_error(GDR_ERR_INVALID_ARG, "prefix_len (%d) negative", prefix_len);
+    if (int rc = check_prefix(prefix_len)) return rc;
     StepWork w{};
     *bytes = N == 0 || T_total == 0 ? 0 : step_layout(&w, nullptr, N, T_total, Hq, Hkv, D, prefix_len, dtype);
     return set_ok();
@@ -737,7 +745,8 @@ int gdr_attn_step(const void* q, int64_t q_stride, const void* k_cache, const vo
                   int64_t o_stride, void* workspace, size_t ws_bytes, gdr_stream_t stream) {
     if (int rc = check_attention(N, T_total, Hq, Hkv, D, dtype)) return rc;
     if (flags & ~GDR_VALIDATE) return set_last_error(GDR_ERR_INVALID_ARG, "unsupported flags 0x%x for gdr_attn_step", flags);
-    if (prefix_len < 0 || (prefix_len > 0) != (prefix_pages != nullptr))
+    if (int rc = check_prefix(prefix_len)) return rc;
+    if ((prefix_len > 0) != (prefix_pages != nullptr))
         return set_last_error(GDR_ERR_INVALID_ARG, "prefix_pages goes with prefix_len (%d) > 0", prefix_len);
     if (int rc = check_scale(scale)) return rc;
     if (N == 0 || T_total == 0) return set_ok();

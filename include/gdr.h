@@ -541,7 +541,7 @@ GDR_API int gdr_attn_step_workspace_size(int N, int64_t T_total, int Hq, int Hkv
  * gdr_kv_append has put their keys there: token i of sequence n sees the keys
  * 0 .. cache_lens[n] + i.
  *   prefix_len     keys 0 .. prefix_len - 1 are the same rows for all sequences
- *                  (0: none): row p % page_size of page prefix_pages[p /
+ *                  (0: none; below 2^31 - 256): row p % page_size of page prefix_pages[p /
  *                  page_size], [ceil(prefix_len / page_size)] int32 device.  They
  *                  are read once for the batch.  cache_lens counts them; block_table
  *                  entries of pages that end within the prefix are not read.
