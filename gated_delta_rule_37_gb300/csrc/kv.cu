@@ -289,8 +289,9 @@ __global__ void attention_validate_kernel(const int32_t* cu, int N, int64_t T, i
             const int64_t fresh = (int64_t)cu[b + 1] - cu[b];
             if (c.lens[b] < 0 || fresh <= 0) continue;
             const int64_t end = c.lens[b] + fresh;  // positions 0 .. end - 1, the prefix's in its own pages
+            if (end <= c.prefix_len) continue;          // no page of its own
             const int64_t pages = (end + c.page_size - 1) >> c.page_bits;
-            if (end > c.prefix_len && pages > c.max_pages) bad |= A_LONG;
+            if (pages > c.max_pages) bad |= A_LONG;
             // a call without a prefix that only writes reaches the new tokens' pages alone
             const int64_t from = c.prefix_len < 0 ? c.lens[b] : c.prefix_len;
             for (int64_t j = (from >> c.page_bits) + threadIdx.x; j < min(pages, (int64_t)c.max_pages); j += blockDim.x) {
