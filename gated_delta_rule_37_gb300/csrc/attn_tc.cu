@@ -228,8 +228,10 @@ __device__ __forceinline__ bool find_job(const AttnArgs& a, int pair_tokens, con
     job.keys = (int)min(job.i0 + pair_tokens, L);
     job.n = n;
     job.h = h;
-    // what lies behind within the sequence is left to the rows that it spoils
-    job.clear = job.keys == L && job.keys % kTile != 0;
+    // The sequence ends inside the last key tile: what follows there is another's.  (With several heads
+    // to a key head a pair has fewer tokens than a key tile has keys: not the last pair alone.)  What lies
+    // behind within the sequence is left to the rows that it spoils.
+    job.clear = (int64_t)max(job.to[0], job.to[1]) * kTile > L;
     return true;
 }
 
