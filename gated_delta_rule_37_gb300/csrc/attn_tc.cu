@@ -345,7 +345,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     const uint32_t mbar = smem_u32(&bars.full[stage]), dst = ring + stage * C::TILE_BYTES;
                     const CUtensorMap* map = value ? &mv : &mk;
                     if (PREFIX) {
-                        // piece `lane` of the tile; one without a page is read from the cache's first rows and
+                        // piece `lane` of the tile; one without a page lies before the cache's first row, where a
+                        // copy reads zeros (a weight of 0 would not keep another page's NaN out), and is
                         // masked.  The pages are those of 32 pieces, asked for 32 pieces ahead
                         const int first = j * pieces;
                         if (first + pieces > at + 32) {
@@ -356,8 +357,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                         const int page = __shfl_sync(0xffffffffu, held, (first - at + lane) & 31);
                         const int64_t key = (int64_t)j * kTile + lane * p.box;
                         bool gone = page < 0 || page >= a.cache.num_pages;
-                        const int row = gone ? 0 : (int)((((int64_t)page * a.Hkv + job.h) << a.cache.page_bits) +
-                                                         (key & (a.cache.page_size - 1)));
+                        const int row = gone ? -p.box : (int)((((int64_t)page * a.Hkv + job.h) << a.cache.page_bits) +
+                                                              (key & (a.cache.page_size - 1)));
                         gone = gone && key < a.cache.prefix_len;
                         const bool part = __shfl_sync(0xffffffffu, gone, lane * 16 / p.box & 31);
                         const uint32_t out = __ballot_sync(0xffffffffu, part && lane < kTile / 16);
