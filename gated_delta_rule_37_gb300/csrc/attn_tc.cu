@@ -14,8 +14,9 @@
 // other's O += P V and next S.  S of one tile is free again when its O += P V has read P,
 // and MMAs run in the order of their issue, so that needs no wait.
 //   The maximum m that P refers to follows the row's maximum lazily: O and the sum are
-// rescaled only when the maximum has risen by more than 2^8, so P stays within 2^8 and
-// O's rescaling, a trip through registers, is rare.  m cancels in O / sum.
+// rescaled only when the maximum has risen by more than 2^8, so O's rescaling, a trip through
+// registers, is rare.  P is taken 2^8 smaller for it and never above 1: values whose weighted
+// sum fits in fp32 do not overflow on the way.  m cancels in O / sum.
 //   A CTA of a prompt takes row tiles of any sequence one after the other; its copies run
 // ahead into the next one's keys while the last rows of this one are rescaled and written.
 // The grid has a place for every pair of row tiles: a CTA that is done asks the hardware for
@@ -24,8 +25,11 @@
 // sequences; with more there are enough of them for any order.
 //   Keys behind a sequence's last one are not another's to see: their V rows are cleared
 // in shared memory (0 * NaN is a NaN), in the last tile alone.  Within a sequence a later
-// token's infinity or NaN could still reach an earlier row as 0 * inf; a row whose result
-// is not finite is computed once more, on the CUDA cores, from the keys that it sees.
+// token's infinity or NaN could still reach an earlier row as 0 * inf.  A row whose result is not
+// finite is right if only keys that it sees have such values, which the values between its
+// own token and the end of its last key tile tell; else those before tell whether it is a NaN or
+// an infinity by its own keys too, and only if not it is computed once more, on the CUDA cores, from the
+// keys that it sees: the rows within a key tile before a bad token.
 //   Measured, heads of 128: 2900 cycles for a key tile of both row tiles, of which the four
 // products are 2048 and most of the rest is the issuing warp's between them; 32768 tokens, 32 heads
 // on 8, 5.5 ms, 1600 TFLOP/s.  Heads of 64 take 2700 for half of the products: there the softmax
@@ -665,7 +669,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                         }
                     }
                 }
-                const float base = m == -INFINITY ? 0.f : -m;
+                const float base = m == -INFINITY ? 0.f : -kLag - m;
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     uint32_t pk[32];
@@ -741,45 +745,35 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 }
                 __syncwarp();
             }
-            if (PREFIX && there) p.w.far_stat[place] = make_float2(m, l);
-            const bool finite = any == 0.f && l < INFINITY && (PREFIX || l > 0.f);
-            // rows that an infinity or a NaN has reached, one after the other
-            uint32_t bad = __ballot_sync(0xffffffffu, there && !finite);
-            if (bad && lane == 0) atomicAdd(&abort_busy[1], 1);
-            const bool again = bad;
-            for (; bad; bad &= bad - 1) {
-                const int who = __ffs(bad) - 1;
-                const int64_t at_w = __shfl_sync(0xffffffffu, t0 + token, who), head_w = __shfl_sync(0xffffffffu, head, who);
-                const int64_t place_w = __shfl_sync(0xffffffffu, place, who);
-                const int limit_w = __shfl_sync(0xffffffffu, limit, who);
-                float acc[D / 32], mw, lw;
-                // by value: what the call takes by reference would live in local memory
-                const Paged cache = a.cache;
-                const int Hkv = a.Hkv;
-                const int64_t ldk = a.ldk, ldv = a.ldv;
-                const __nv_bfloat16* keys = static_cast<const __nv_bfloat16*>(a.k) + t0 * ldk + (int64_t)h * D;
-                const __nv_bfloat16* vals = static_cast<const __nv_bfloat16*>(a.v) + t0 * ldv + (int64_t)h * D;
-                row_again<D>(static_cast<const __nv_bfloat16*>(a.q) + at_w * a.ldq + head_w * D, (int64_t)from * kTile,
-                             min(limit_w, end * kTile), c,
-                             [=](int64_t key, const __nv_bfloat16*& kp, const __nv_bfloat16*& vp) {
-                                 if (PREFIX) return cached_row<D>(cache, cache.prefix, Hkv, h, key, kp, vp);
-                                 kp = keys + key * ldk;
-                                 vp = vals + key * ldv;
-                                 return true;
-                             }, acc, mw, lw);
-                if (PREFIX) {
-                    Vec<float, D / 32>::store(p.w.far_sum + place_w * D + lane * (D / 32), acc);
-                    if (lane == 0) p.w.far_stat[place_w] = make_float2(mw, lw);
-                } else {
-                    const float by = lw > 0.f ? 1.f / lw : lw == 0.f ? 0.f : lw;
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) acc[k] *= by;
-                    Vec<__nv_bfloat16, D / 32>::store(static_cast<__nv_bfloat16*>(a.o) + at_w * a.ldo + head_w * D +
-                                                          lane * (D / 32), acc);
+            if (PREFIX && there) p.w.far_stat[place] = make_float2(m + kLag, l);
+            // A sum of weights that is a NaN comes from a score that the row sees, and the row is right as
+            // it is; one of 0 from scores of -inf alone (the prefix's merge leaves such a part out).
+            const uint32_t zero = PREFIX ? 0 : __ballot_sync(0xffffffffu, there && l == 0.f);
+            const uint32_t bad = __ballot_sync(0xffffffffu, there && any != 0.f && l > 0.f);
+            if (zero | bad) {
+                if (lane == 0) atomicAdd(&abort_busy[1], 1);
+                if (zero >> lane & 1)
+                    for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(to_row + d * 2) = make_uint4(0, 0, 0, 0);
+                if (bad) {
+                    // by value: what the call takes by reference would live in local memory
+                    const Paged cache = a.cache;
+                    const int Hkv = a.Hkv;
+                    const int64_t ldk = a.ldk, ldv = a.ldv;
+                    const __nv_bfloat16* keys = static_cast<const __nv_bfloat16*>(a.k) + t0 * ldk + (int64_t)h * D;
+                    const __nv_bfloat16* vals = static_cast<const __nv_bfloat16*>(a.v) + t0 * ldv + (int64_t)h * D;
+                    const int loaded = job.clear ? min(job.keys, end * kTile) : end * kTile;
+                    rows_again<D>(bad, PREFIX, static_cast<const __nv_bfloat16*>(a.q) + (t0 + token) * a.ldq + head * D,
+                                  to_row, PREFIX ? p.w.far_stat + place : nullptr, limit, from * kTile, loaded, c,
+                                  [=](int64_t key, const __nv_bfloat16*& kp, const __nv_bfloat16*& vp) {
+                                      if (PREFIX) return cached_row<D>(cache, cache.prefix, Hkv, h, key, kp, vp);
+                                      kp = keys + key * ldk;
+                                      vp = vals + key * ldv;
+                                      return true;
+                                  });
                 }
+                __syncwarp();
+                if (lane == 0) atomicSub(&abort_busy[1], 1);
             }
-            __syncwarp();
-            if (again && lane == 0) atomicSub(&abort_busy[1], 1);
             if (lane == 0) mbar_arrive(smem_u32(&bars.job_free[count & 1]));
         }
     }
