@@ -58,6 +58,12 @@ struct StepJob {
     int n, h, r0, rows, from, to, slot;
 };
 
+// A run with rows whose sums hold an infinity or a NaN, a bit each.
+struct BadRun {
+    StepJob job;
+    uint32_t rows[2];
+};
+
 struct StepBarriers {
     uint64_t full[10], empty[10], q_full[2], q_empty[2];
 };
@@ -92,9 +98,44 @@ __device__ __forceinline__ bool any_reader(bool x) {
     return r != 0;
 }
 
+// These rows, by the eight warps: lane i of a warp has row 8 i + warp.  Of a row whose weights' sum is a
+// NaN, from a score that it sees, all is one already.
+template <int D, int ROWS>
+__device__ __noinline__ void run_again(const StepParams& p, const BadRun& run, const float2 (*stats)[16]) {
+    const AttnArgs& a = p.a;
+    const StepJob& j = run.job;
+    const int lane = threadIdx.x & 31, r = min(lane * kReaders + (int)(threadIdx.x >> 5), ROWS - 1);
+    const bool mine = lane < ROWS / kReaders && (run.rows[r >> 5] >> (r & 31) & 1);
+    using C = StepShape<D, ROWS>;
+    float weights = 0.f;
+    for (int w = 0; w < C::SHARE; ++w) weights += stats[w * C::GROUPS + r / 16][r % 16].y;
+    const int64_t token = j.t0 + (j.r0 + r) / a.group;
+    const int head = j.h * a.group + (j.r0 + r) % a.group;
+    const bool whole = j.slot < 0 && p.w.splits == 0;
+    const int64_t at = j.slot < 0 ? token * a.Hq + head : ((int64_t)blockIdx.x * 2 + j.slot) * ROWS + r;
+    auto* const o = static_cast<__nv_bfloat16*>(a.o) + token * a.ldo + (int64_t)head * D;
+    // scores of -inf alone weigh nothing, whatever the values (the merge leaves such a part out)
+    if (whole && mine && weights == 0.f)
+        for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(o + d) = make_uint4(0, 0, 0, 0);
+    const uint32_t rows = __ballot_sync(0xffffffffu, mine && weights > 0.f);
+    if (!rows) return;
+    // the end of the run's keys, and of those that the row sees: a row that sees all has met its own alone
+    const int last = min(j.to * kKeyTile, j.most);
+    const int end = (int)min((int64_t)j.len + (j.r0 + r) / a.group + 1, (int64_t)last);
+    void* const to = whole ? static_cast<void*>(o) : (j.slot < 0 ? p.w.row_sum : p.w.slot_sum) + at * D;
+    const Paged cache = a.cache;
+    const int32_t* pages = a.cache.table + j.n * a.cache.table_ld;
+    const int h = j.h, Hkv = a.Hkv;
+    rows_again<D>(rows, !whole, static_cast<const __nv_bfloat16*>(a.q) + token * a.ldq + (int64_t)head * D, to,
+                  (j.slot < 0 ? p.w.row_stat : p.w.slot_stat) + at, end, max(j.from * kKeyTile, j.least), last,
+                  a.scale_log2, [=](int64_t key, const __nv_bfloat16*& kp, const __nv_bfloat16*& vp) {
+                      return cached_row<D>(cache, pages, Hkv, h, key, kp, vp);
+                  });
+}
+
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kStepBlock, 1)
-    step_kernel(const StepParams p, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    step_kernel(const __grid_constant__ StepParams p, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
     using C = StepShape<D, ROWS>;
     extern __shared__ unsigned char raw[];
     __shared__ StepBarriers bars;
@@ -102,6 +143,7 @@ __global__ void __launch_bounds__(kStepBlock, 1)
     __shared__ uint32_t missing[C::STAGES];     // a bit per 16 keys without a page
     __shared__ float2 stats[kReaders][16];
     __shared__ uint32_t bad_rows[2];
+    __shared__ BadRun bad_run;
     __shared__ int abort_busy[2];
     const AttnArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -408,10 +450,8 @@ __global__ void __launch_bounds__(kStepBlock, 1)
                             x[2] = fmaf(y.z, f, x[2]);
                             x[3] = fmaf(y.w, f, x[3]);
                         }
-                        if (!(fabsf(x[0]) + fabsf(x[1]) + fabsf(x[2]) + fabsf(x[3]) + sum < INFINITY)) {
+                        if (!(fabsf(x[0]) + fabsf(x[1]) + fabsf(x[2]) + fabsf(x[3]) + sum < INFINITY))
                             atomicOr(&bad_rows[r >> 5], 1u << (r & 31));  // the same word whatever the order
-                            continue;
-                        }
                         const int local = (j.r0 + r) / a.group, head = j.h * a.group + j.r0 + r - local * a.group;
                         const int64_t token = j.t0 + local;
                         if (j.slot < 0 && p.w.splits == 0) {
@@ -435,38 +475,16 @@ __global__ void __launch_bounds__(kStepBlock, 1)
                 break;
             }
             // rows that an infinity or a NaN has reached
-            const uint32_t bad[2] = {bad_rows[0], ROWS > 32 ? bad_rows[1] : 0};
-            if (bad[0] | bad[1]) {
+            if (bad_rows[0] | bad_rows[1]) {
                 any_reader(false);  // all have read the words
-                if (tid == 0) bad_rows[0] = bad_rows[1] = 0;
-                if (lane == 0) atomicAdd(&abort_busy[1], 1);
-                for (int r = warp; r < j.rows; r += kReaders) {
-                    if (!(bad[r >> 5] >> (r & 31) & 1)) continue;
-                    const int64_t token = j.t0 + (j.r0 + r) / a.group;
-                    const int head = j.h * a.group + (j.r0 + r) % a.group;
-                    const int32_t* pages = a.cache.table + j.n * a.cache.table_ld;
-                    float x[D / 32], top, sum;
-                    const int see = (int)min((int64_t)j.len + (j.r0 + r) / a.group + 1, (int64_t)j.most);
-                    const Paged cache = a.cache;
-                    const int h = j.h, Hkv = a.Hkv;
-                    row_again<D>(static_cast<const __nv_bfloat16*>(a.q) + token * a.ldq + (int64_t)head * D,
-                                 max(j.from * kKeyTile, j.least), min(j.to * kKeyTile, see), c,
-                                 [=](int64_t key, const __nv_bfloat16*& kp, const __nv_bfloat16*& vp) {
-                                     return cached_row<D>(cache, pages, Hkv, h, key, kp, vp);
-                                 }, x, top, sum);
-                    if (j.slot < 0 && p.w.splits == 0) {
-                        const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
-#pragma unroll
-                        for (int e = 0; e < D / 32; ++e) x[e] *= inv;
-                        Vec<__nv_bfloat16, D / 32>::store(static_cast<__nv_bfloat16*>(a.o) + token * a.ldo +
-                                                              (int64_t)head * D + lane * (D / 32), x);
-                    } else {
-                        const int64_t at = j.slot < 0 ? token * a.Hq + head
-                                                      : ((int64_t)blockIdx.x * 2 + j.slot) * ROWS + r;
-                        Vec<float, D / 32>::store((j.slot < 0 ? p.w.row_sum : p.w.slot_sum) + at * D + lane * (D / 32), x);
-                        if (lane == 0) (j.slot < 0 ? p.w.row_stat : p.w.slot_stat)[at] = make_float2(top, sum);
-                    }
+                if (tid == 0) {
+                    bad_run = BadRun{j, {bad_rows[0], bad_rows[1]}};
+                    bad_rows[0] = bad_rows[1] = 0;
                 }
+                if (lane == 0) atomicAdd(&abort_busy[1], 1);
+                any_reader(false);
+                run_again<D, ROWS>(p, bad_run, stats);
+                __syncwarp();
                 if (lane == 0) atomicSub(&abort_busy[1], 1);
                 any_reader(false);  // the words are clear before the next run's join
             }

@@ -130,6 +130,53 @@ def test_prompt_of_rows_that_see_a_bad_value(what, D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("prefix", [0, 4096])
+@pytest.mark.parametrize("what", BAD)
+def test_step_of_rows_that_see_a_bad_value(what, prefix, D):
+    """The same of decode, the bad token in the prefix or at the beginning of every sequence."""
+    N, Hq, Hkv, own = 64, 32, 8, 4096
+    lens, cu = [prefix + own - 1] * N, starts([1] * N)
+    pool = Pool(1, [prefix + own] * N, Hkv, D, 64, BF16, prefix)
+    q = normal(2, N, Hq, D, dtype=BF16)
+    clean = pool.step(q, lens, cu)
+    good = _time(lambda: pool.step(q, lens, cu))
+    pages = pool.prefix_list[:1] if prefix else [t[0] for t in pool.table_list]
+    if what == "key":
+        pool.k[pages, 0, 0, 5] = NAN
+    elif what.endswith("channel"):
+        pool.v[:, 0, :, 5] = NAN if what == "channel" else -INF
+    else:
+        pool.v[pages, 0, 0, 5] = NAN if what == "value" else INF
+    o = pool.step(q, lens, cu)
+    hit = torch.zeros(o.shape, dtype=torch.bool, device=DEV)
+    hit[:, :Hq // Hkv, slice(None) if what == "key" else 5] = True
+    assert not torch.isfinite(o[hit]).any()
+    assert bits_equal(torch.where(hit, 0, o), torch.where(hit, 0, clean))
+    bad = _time(lambda: pool.step(q, lens, cu))
+    assert bad < 4 * good, f"{bad:.3f} ms against {good:.3f}"
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_verify_of_rows_that_see_a_bad_value(D):
+    """Several tokens of a sequence: those that see the last one's NaN, those that see the first one's, and a channel
+    that is NaN throughout."""
+    N, m, Hq, Hkv, own = 32, 12, 32, 8, 4096
+    lens, cu = [own - m] * N, starts([m] * N)
+    pool = Pool(1, [own] * N, Hkv, D, 64, BF16)
+    q = normal(2, N * m, Hq, D, dtype=BF16)
+    clean = pool.step(q, lens, cu)
+    good = _time(lambda: pool.step(q, lens, cu))
+    pool.v[:, 0, :, 5] = NAN
+    o = pool.step(q, lens, cu)
+    hit = torch.zeros(o.shape, dtype=torch.bool, device=DEV)
+    hit[:, :4, 5] = True
+    assert torch.isnan(o[hit]).all()
+    assert bits_equal(torch.where(hit, 0, o), torch.where(hit, 0, clean))
+    bad = _time(lambda: pool.step(q, lens, cu))
+    assert bad < 4 * good, f"{bad:.3f} ms against {good:.3f}"
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_prompt_of_scores_of_minus_infinity(D):
     """Many rows that see scores of -inf alone: 0, whatever the values, and as fast as others."""
     T, Hq, Hkv = 8192, 8, 2
