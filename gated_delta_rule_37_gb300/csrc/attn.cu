@@ -222,9 +222,10 @@ template <typename T, int D, int RT> struct Simt {
         for (int i = 0; i < RR; ++i) {
             T* to = out(tr + TR * i);
             if (!to) continue;
-            const float inv = l[i] > 0.f ? 1.f / l[i] : l[i] == 0.f ? 0.f : l[i];  // a NaN stays one
+            const float inv = l[i] > 0.f ? 1.f / l[i] : l[i];  // a NaN stays one
+            // (scores of -inf alone weigh nothing, whatever the values)
 #pragma unroll
-            for (int c = 0; c < CG * CV; ++c) acc[i][c] *= inv;
+            for (int c = 0; c < CG * CV; ++c) acc[i][c] = l[i] == 0.f ? 0.f : acc[i][c] * inv;
 #pragma unroll
             for (int g = 0; g < CG; ++g) Vec<T, CV>::store(to + (tk + TK * g) * CV, acc[i] + g * CV);
         }
@@ -417,7 +418,7 @@ __device__ __forceinline__ void join_parts(int count, int first, int step, S sta
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            if (st[k].x == kNone && st[k].y == 0.f) continue;  // saw no key: its sums are 0
+            if (st[k].x == kNone && st[k].y == 0.f) continue;  // no key, or scores of -inf alone: no weight
             const float f = exp2f(st[k].x - base);
             l = fmaf(st[k].y, f, l);
 #pragma unroll

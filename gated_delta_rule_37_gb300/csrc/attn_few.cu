@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kFewThreads, ROWS == 4 ? 2 : 1) step_few_kerne
 #pragma unroll
             for (int n = 0; n < kFewWarps; ++n) {
                 const float2 st = stats[n][r];
-                if (st.x == -INFINITY && st.y == 0.f) continue;  // saw no key: its sums are 0
+                if (st.x == -INFINITY && st.y == 0.f) continue;  // no key, or scores of -inf alone: no weight
                 const float f = exp2f(st.x - base);
                 const float4 y = *reinterpret_cast<const float4*>(&join[n][r][col]);
                 sum = fmaf(st.y, f, sum);

@@ -192,6 +192,30 @@ def test_prompt_of_scores_of_minus_infinity(D):
     assert bad < 4 * good, f"{bad:.3f} ms against {good:.3f}"
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,m", [(2, 1), (2, 3), (16, 1), (16, 5)])
+def test_scores_of_minus_infinity_of_bad_values(m, Hq, D, dtype):
+    """A row all of whose scores are -inf is 0 also where the values are not finite: prompts, the step in each of its
+    tiles, in one run and cut into several, with a prefix and without."""
+    T = 900
+    q, k, v = torch.ones(T, Hq, D, dtype=dtype, device=DEV), normal(1, T, 1, D, dtype=dtype), normal(2, T, 1, D, dtype=dtype)
+    k[:, :, 0] = -INF
+    v[0, 0, 3], v[500, 0, 4], v[T - 1, 0, 5] = NAN, INF, NAN
+    assert (gdr.attn_fwd(q, k, v, starts([T])) == 0).all()
+    for prefix in (0, 200):
+        pool = Pool(1, [T, T], 1, D, 64, dtype, prefix)
+        for n in range(2):
+            for p in range(-(-T // 64)):
+                pages = pool.prefix_list if (p + 1) * 64 <= prefix or pool.table_list[n][p] < 0 else pool.table_list[n]
+                rows = slice(p * 64, min((p + 1) * 64, T))
+                pool.k[pages[p], 0, :rows.stop - rows.start], pool.v[pages[p], 0, :rows.stop - rows.start] = k[rows, 0], v[rows, 0]
+        if prefix:  # the page that it ends in is the prefix's and each sequence's
+            pool.k[pool.prefix_list[3], 0], pool.v[pool.prefix_list[3], 0] = k[192:256, 0], v[192:256, 0]
+        o = pool.step(q[:2 * m], [T - m, T - m], starts([m, m]))
+        assert (o == 0).all(), prefix
+
+
 # ---- values near the type's largest -----------------------------------------------------------
 
 
