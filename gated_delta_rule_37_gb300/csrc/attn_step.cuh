@@ -25,7 +25,7 @@ namespace gdr {
 constexpr int kKeyTile = 64;       // keys per tile of the own parts
 constexpr int kFarTile = 128;      // keys per tile of the prefix, on the tensor cores
 constexpr int kStepThreads = 256;  // threads that form the plan (a block may have a warp or two more)
-constexpr int kSms = 152;
+constexpr int kSms = 152;          // GB300's: the workspace's size, which the host alone tells, follows it
 constexpr int kMaxSplits = 64;
 
 // A row tile that begins in a CTA's run and ends in another's: rows rows from r0 on of the

@@ -479,9 +479,10 @@ GDR_API int gdr_rmsnorm_bwd(const void* dy, int64_t dy_stride, const void* s, in
  *   - cache_lens [N] int32 device: the tokens that sequence n had in the cache
  *     before this call's; both calls of a step take the same numbers.  A value
  *     < 0 is padding: nothing of that sequence is used or written.
- *   - A NaN or infinity reaches only the rows that see its token; where rows of
- *     the same tile do not, they are computed once more (slowly) without it.  A
- *     row that sees no key, or whose scores are all -inf, is 0.
+ *   - A NaN or infinity reaches only the rows that see its token.  With GDR_BF16,
+ *     rows that share a tile of keys with a value of which they do not see the
+ *     token are computed once more without it, slowly; rows that see it are not.
+ *     A row that sees no key, or whose scores are all -inf, is 0.
  *   - What is written shares no memory with an input, the workspace or what else
  *     is written, but where a tensor is said to be in place; column blocks of the
  *     same rows share none.
@@ -544,7 +545,7 @@ GDR_API int gdr_attn_step_workspace_size(int N, int64_t T_total, int Hq, int Hkv
  *                  (0: none; below 2^31 - 256): row p % page_size of page prefix_pages[p /
  *                  page_size], [ceil(prefix_len / page_size)] int32 device.  They
  *                  are read once for the batch.  cache_lens counts them; block_table
- *                  entries of pages that end within the prefix are not read.
+ *                  entries of pages that end within the prefix may hold anything.
  *   q, o           [T_total, Hq, D] dtype; o is written
  *   workspace      device scratch of gdr_attn_step_workspace_size bytes, 256-byte
  *                  aligned; needs no initialisation.  Calls whose work may overlap

@@ -46,3 +46,18 @@ def test_a_sequence_beyond_the_prefix_does():
     with pytest.raises(gdr.GdrError, match="page number outside"):  # an append writes to its own pages, shared or not
         k = normal(3, 2, 1, 64, dtype=torch.bfloat16)
         gdr.kv_append(k, k, pool.k, pool.v, pool.table, ints([128, 99]), cu, flags=gdr.GDR_VALIDATE)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("page,prefix,m", [(16, 105, 1), (16, 48, 3), (32, 100, 20), (64, 200, 1)])
+def test_entries_within_the_prefix_hold_anything(page, prefix, m, dtype):
+    """Of pages that end within the prefix: no page, one that is not there, one of NaN, another sequence's."""
+    lens, cu = [prefix + 40, prefix, prefix + 700], starts([m] * 3)
+    pool = Pool(1, [a + m for a in lens], 2, 64, page, dtype, prefix)
+    q = normal(2, 3 * m, 8, 64, dtype=dtype)
+    want = pool.step(q, lens, cu, flags=gdr.GDR_VALIDATE)
+    for spare in pool.spare:
+        pool.k[spare], pool.v[spare] = float("nan"), float("inf")
+    for entry in (pool.k.shape[0], -7, pool.spare[0], pool.table_list[2][prefix // page + 1]):
+        pool.table[:, :prefix // page] = entry
+        assert bits_equal(pool.step(q, lens, cu, flags=gdr.GDR_VALIDATE), want)
