@@ -13,6 +13,8 @@
 // own, so that no tile needs a barrier; the warps' results are joined at the end of a run.
 // With up to 16 rows two sets of four warps take the tiles in turn; with more, rows are what
 // the warps share out first: fewer results to join.
+//   A row whose sums are not finite is written as it is.  Where the run has a key that the row does not
+// see, whose value may have reached it as 0 * inf, the warps look at the values again: never in decode.
 //   Measured: 256 sequences of up to 4096 keys, 32 heads of 128 on 8, 300 us, 6.5 TB/s; one of 65536
 // 50 us, of which 5 pass before the first tile is there, the last ones in the merge; 230 of up to 1024 behind
 // a prefix 80 us, 6.1 TB/s, where a run's beginning and end (1.9 us) count.

@@ -7,7 +7,7 @@
 // 128.  Per row tile and key tile, with S and O in tensor memory:
 //   S = Q K^T     one thread issues it: Q and K from shared memory, 128 x 128 x D
 //   P = 2^(S c - m)   a warpgroup, a row per thread, c = scale log2(e): P goes back into
-//                 S's columns as bf16, its sum stays in fp32
+//                 S's columns as bf16 (a product's operands have one type, V's), its sum stays fp32
 //   O += P V      P from tensor memory, V from shared memory as it was loaded (rows of
 //                 keys: the contraction runs down the tile)
 // The two row tiles alternate: while one's P is formed the tensor cores work on the
@@ -29,10 +29,12 @@
 // finite is right if only keys that it sees have such values, which the values between its
 // own token and the end of its last key tile tell; else those before tell whether it is a NaN or
 // an infinity by its own keys too, and only if not it is computed once more, on the CUDA cores, from the
-// keys that it sees: the rows within a key tile before a bad token.
+// keys that it sees: the rows within a key tile before a bad token.  (8192 tokens of 8 heads of 128, 0.103 ms:
+// one early NaN in a key / a value 0.103 / 0.133, one in the middle 0.118, a channel of NaN / of infinities
+// 0.153 / 0.360.)
 //   Measured, heads of 128: 2900 cycles for a key tile of both row tiles, of which the four
 // products are 2048 and most of the rest is the issuing warp's between them; 32768 tokens, 32 heads
-// on 8, 5.5 ms, 1600 TFLOP/s.  Heads of 64 take 2700 for half of the products: there the softmax
+// on 8, 5.55 ms, 1585 TFLOP/s.  Heads of 64 take 2700 for half of the products: there the softmax
 // warps' chain of 1250 and the trips between them and the issuing warp bound it.
 #include <math.h>
 
