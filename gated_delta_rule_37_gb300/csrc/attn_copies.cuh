@@ -129,14 +129,14 @@ __device__ __forceinline__ void largest_bits(int64_t from, int64_t end, R rows, 
         as_signed[w] = 0x80008000u;
         as_unsigned[w] = 0;
     }
-    for (int64_t j0 = from; j0 < end; j0 += KEYS) {
+    auto look = [&](auto key_of) {
         uint32_t v[KEYS][W];
 #pragma unroll
         for (int i = 0; i < KEYS; ++i) {
             const __nv_bfloat16 *kp, *vp;
 #pragma unroll
             for (int w = 0; w < W; ++w) v[i][w] = 0;
-            if (rows(min(j0 + i, end - 1), kp, vp) && mine) {
+            if (rows(key_of(i), kp, vp) && mine) {
                 const uint32_t* at = reinterpret_cast<const uint32_t*>(vp) + lane * W;
                 if constexpr (W == 2) {
                     const uint2 x = *reinterpret_cast<const uint2*>(at);
@@ -158,8 +158,13 @@ __device__ __forceinline__ void largest_bits(int64_t from, int64_t end, R rows, 
             const uint32_t nan = __vcmpgts2(as_signed[w], 0x7f807f80u) | __vcmpgtu2(as_unsigned[w], 0xff80ff80u);
             more |= (want[w] & ~nan) != 0;
         }
-        if (!__any_sync(0xffffffffu, more)) break;
-    }
+        return __any_sync(0xffffffffu, more) != 0;
+    };
+    int64_t j0 = from;
+    for (; j0 + KEYS <= end; j0 += KEYS)
+        if (!look([&](int i) { return j0 + i; })) return;
+    // (the last key several times, not one behind it)
+    if (j0 < end) look([&](int i) { return min(j0 + i, end - 1); });
 }
 
 // A warp's rows (bad: a bit for each lane that has one; its query, result, statistics and the end

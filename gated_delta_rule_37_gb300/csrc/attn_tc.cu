@@ -31,7 +31,7 @@
 // an infinity by its own keys too, and only if not it is computed once more, on the CUDA cores, from the
 // keys that it sees: the rows within a key tile before a bad token.  (8192 tokens of 8 heads of 128, 0.103 ms:
 // one early NaN in a key / a value 0.103 / 0.133, one in the middle 0.118, a channel of NaN / of infinities
-// 0.153 / 0.360.)
+// 0.147 / 0.276.)
 //   Measured, heads of 128: 2900 cycles for a key tile of both row tiles, of which the four
 // products are 2048 and most of the rest is the issuing warp's between them; 32768 tokens, 32 heads
 // on 8, 5.55 ms, 1585 TFLOP/s.  Heads of 64 take 2700 for half of the products: there the softmax
