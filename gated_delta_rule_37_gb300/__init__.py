@@ -772,7 +772,8 @@ def attn_fwd(q, k, v, cu_seqlens, *, scale=None, flags: int = 0, o=None, stream=
 @functools.lru_cache(maxsize=4096)
 def _attn_step_bytes(N, T, Hq, Hkv, D, prefix_len, dtype):
     out = ctypes.c_size_t(0)
-    _check(load().gdr_attn_step_workspace_size(N, T, Hq, Hkv, D, prefix_len, dtype, ctypes.byref(out)))
+    # (ctypes would wrap a length of more than 32 bits; the largest int is refused)
+    _check(load().gdr_attn_step_workspace_size(N, T, Hq, Hkv, D, min(prefix_len, 2 ** 31 - 1), dtype, ctypes.byref(out)))
     return out.value
 
 

@@ -137,7 +137,8 @@ __device__ __noinline__ void run_again(const StepParams& p, const BadRun& run, c
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kStepBlock, 1)
-    step_kernel(const __grid_constant__ StepParams p, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    step_kernel(const __grid_constant__ StepParams p, const __grid_constant__ CUtensorMap mk,
+                const __grid_constant__ CUtensorMap mv) {
     using C = StepShape<D, ROWS>;
     extern __shared__ unsigned char raw[];
     __shared__ StepBarriers bars;

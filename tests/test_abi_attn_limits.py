@@ -27,3 +27,10 @@ def test_the_longest_prefix_has_a_workspace(lib, dtype):
     """One that grows with the rows, not with the keys: as many partial results of a row as one a hundredth as long."""
     size = [gdr.attn_step_workspace_size(2, 4, 8, 2, 64, prefix_len=n, dtype=dtype) for n in (LONGEST // 100, LONGEST)]
     assert 0 < size[1] < 2 * size[0] < 1 << 24
+
+
+@pytest.mark.parametrize("prefix_len", [2 ** 31, 2 ** 32, 2 ** 32 + 100])
+def test_the_binding_passes_no_other_prefix(lib, prefix_len):
+    """Lengths that 32 bits would wrap to a shorter one."""
+    with pytest.raises(gdr.GdrError, match="prefix_len"):
+        gdr.attn_step_workspace_size(2, 4, 8, 2, 64, prefix_len=prefix_len, dtype=BF16)
